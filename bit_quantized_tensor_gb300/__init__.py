@@ -15,6 +15,19 @@ Functions (same names as the C ABI):
                             (alpha=...: the column-wise affine form,
                             Y = alpha (.) (...) + b, through w4a4_gemm_affine)
 B / W operands are K-major (N x K row-major), the layout every call takes.
+
+Microscaled 4-bit floating point (fmt "nv": blocks of 16 with e4m3 scales and a
+tensor scale; "mx": blocks of 32 with power-of-two scales) and layer norm:
+  fp4_tensor_scale(X)             the "nv" tensor scale of X
+  fp4_quantize(X, fmt)            X -> packed operand (codes, scales)
+  fp4_quantize_both(X, fmt)       packed operands of X and of its transpose
+  fp4_dequantize(Xq, Xs, K, fmt)  the values of a packed operand
+  fp4_gemm(Aq, As, Bq, Bs, K)     A . B^T (+ bias) of packed operands
+  fp4_linear(X, Wq, Ws)           Q(X) . W^T (+ bias), X quantized in the call
+  fp4_linear_backward(dY, X, ...) dX, dW and the bias gradient
+  layer_norm(X, gamma, beta)      y, mean, rstd
+  layer_norm_fp4(X, gamma, beta)  the same, y quantized to a packed operand
+  layer_norm_backward(...)        dX, dgamma, dbeta
 """
 from __future__ import annotations
 
@@ -35,7 +48,12 @@ STATUS_NAMES = {0: "QG_OK", 1: "QG_ERR_INVALID_ARG", 2: "QG_ERR_UNSUPPORTED",
                 6: "QG_ERR_TIMEOUT"}
 QG_ROW_MAJOR, QG_COL_MAJOR = 0, 1
 (QG_OP_S8, QG_OP_S4, QG_OP_F16, QG_OP_W4A16, QG_OP_W4A4, QG_OP_S8_HOST, QG_OP_W4A4_PREPACKED,
- QG_OP_W4A4_WEIGHTS) = range(8)
+ QG_OP_W4A4_WEIGHTS, QG_OP_FP4_LINEAR, QG_OP_FP4_LINEAR_BACKWARD, QG_OP_LAYER_NORM_BACKWARD,
+ QG_OP_FP4_TENSOR_SCALE) = range(12)
+QG_FP4_NV, QG_FP4_MX = 0, 1
+QG_F16, QG_BF16, QG_F32 = 0, 1, 2
+FP4_FORMATS = {"nv": QG_FP4_NV, "mx": QG_FP4_MX}
+FP4_BLOCK = {"nv": 16, "mx": 32}
 
 
 class QgError(RuntimeError):
@@ -54,6 +72,7 @@ _i64 = ctypes.c_int64
 _p = ctypes.c_void_p
 _sz = ctypes.c_size_t
 _int = ctypes.c_int
+_f32 = ctypes.c_float
 
 # C signatures (restype, argtypes) of every exported function.
 SIGNATURES = {
@@ -91,6 +110,26 @@ SIGNATURES = {
     "w4a4_prepack_weights": (_int, [_i64, _i64, _p, _p, _i64, _p, _p, _sz, _p]),
     "w4a4_gemm_prepacked": (_int, [_i64, _i64, _i64, _p, _p, _p, _sz, _i64, _p, _p, _i64, _p, _p, _i64,
                                    _p, _sz, _p]),
+    "qg_block_kernel_budget_count": (_int, []),
+    "qg_block_kernel_budget_get": (_int, [_int, ctypes.POINTER(KernelBudgetC)]),
+    "qg_block_kernel_budget_measure": (_int, [_int, ctypes.POINTER(_int), ctypes.POINTER(_int),
+                                              ctypes.POINTER(_int)]),
+    "qg_fp4_codes_ld": (_i64, [_i64]),
+    "qg_fp4_scale_bytes": (_sz, [_int, _i64, _i64]),
+    "fp4_tensor_scale": (_int, [_int, _i64, _i64, _p, _i64, _p, _p, _sz, _p]),
+    "fp4_quantize": (_int, [_int, _int, _i64, _i64, _p, _i64, _p, _p, _p, _p]),
+    "fp4_quantize_both": (_int, [_int, _int, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p]),
+    "fp4_dequantize": (_int, [_int, _int, _i64, _i64, _p, _p, _p, _p, _i64, _p]),
+    "fp4_gemm": (_int, [_int, _int, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _p, _p, _i64, _p]),
+    "fp4_linear": (_int, [_int, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _sz,
+                          _p]),
+    "fp4_linear_backward": (_int, [_int, _int, _i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _p, _p, _p,
+                                   _p, _i64, _p, _i64, _p, _p, _sz, _p]),
+    "layer_norm": (_int, [_int, _i64, _i64, _p, _i64, _p, _p, _int, _f32, _p, _i64, _p, _p, _p]),
+    "layer_norm_fp4": (_int, [_int, _int, _i64, _i64, _p, _i64, _p, _p, _int, _f32, _p, _p, _p, _p, _p,
+                              _p]),
+    "layer_norm_backward": (_int, [_int, _i64, _i64, _p, _i64, _p, _i64, _p, _int, _p, _p, _p, _i64, _p,
+                                   _p, _p, _sz, _p]),
 }
 
 _lib = None
@@ -181,22 +220,27 @@ def device_status_detail(stream=None) -> dict:
     return dict(zip(STATUS_WORDS, (int(w) for w in words)))
 
 
-def kernel_budgets(measure: bool = False) -> list:
-    """The library's kernel budget table, one dict per kernel instance.  With
-    measure=True (needs a device) each entry also gets the compiled kernel's
-    registers per thread, static shared memory and the CTAs per SM the
-    device's occupancy calculator gives at the entry's launch shape."""
+def kernel_budgets(measure: bool = False, table: str = "gemm") -> list:
+    """One of the library's kernel budget tables, one dict per kernel instance:
+    table "gemm" (the GEMMs and their quantizers) or "block" (microscaled 4-bit
+    operators and layer norm).  With measure=True (needs a device) each entry
+    also gets the compiled kernel's registers per thread, static shared memory
+    and the CTAs per SM the device's occupancy calculator gives at the entry's
+    launch shape."""
+    if table not in ("gemm", "block"):
+        raise ValueError("table must be 'gemm' or 'block'")
+    stem = "qg_kernel_budget" if table == "gemm" else "qg_block_kernel_budget"
     L = lib()
     out = []
-    for i in range(int(L.qg_kernel_budget_count())):
+    for i in range(int(getattr(L, f"{stem}_count")())):
         b = KernelBudgetC()
-        _check("qg_kernel_budget_get", L.qg_kernel_budget_get(i, ctypes.byref(b)))
+        _check(f"{stem}_get", getattr(L, f"{stem}_get")(i, ctypes.byref(b)))
         e = {name: getattr(b, name) for name, _ in KernelBudgetC._fields_}
         e["kernel"] = b.kernel.decode()
         if measure:
             regs, ssm, ctas = _int(), _int(), _int()
-            _check("qg_kernel_budget_measure",
-                   L.qg_kernel_budget_measure(i, ctypes.byref(regs), ctypes.byref(ssm), ctypes.byref(ctas)))
+            _check(f"{stem}_measure", getattr(L, f"{stem}_measure")(
+                i, ctypes.byref(regs), ctypes.byref(ssm), ctypes.byref(ctas)))
             e.update(regs_per_thread=regs.value, static_smem_bytes=ssm.value, ctas_per_sm=ctas.value)
         out.append(e)
     return out
@@ -433,3 +477,324 @@ def w4a4_gemm_prepacked(Xq, Xscale, packed, N: int, K: int, XU=None, Vt=None, bi
         bias.data_ptr() if bias is not None else None, Y.data_ptr(), Y.stride(0),
         ws.data_ptr(), wsb, _stream(stream)))
     return Y
+
+
+# ---------------------------------------------------------------- microscaled 4-bit, layer norm
+
+def _dtype_id(dtype, name):
+    torch = _torch()
+    if dtype is torch.bfloat16:
+        return QG_BF16
+    if dtype is torch.float16:
+        return QG_F16
+    if dtype is torch.float32:
+        return QG_F32
+    raise TypeError(f"{name} must be float16, bfloat16 or float32, got {dtype}")
+
+
+def _fmt_id(fmt):
+    try:
+        return FP4_FORMATS[fmt]
+    except (KeyError, TypeError):
+        raise ValueError(f"fmt must be 'nv' or 'mx', got {fmt!r}") from None
+
+
+def _on(t, name, device):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, other operands on {device}")
+
+
+def _matrix(t, name, device=None, dtype=None, shape=None):
+    """Checks a 2-D floating matrix with unit column stride; returns its leading dimension."""
+    _on(t, name, device)
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, got {rows} x {cols}")
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1 and rows > 0:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    if rows > 1 and ld < cols:
+        raise ValueError(f"the rows of {name} overlap")
+    return ld if rows > 1 else cols
+
+
+def _packed(codes, scales, name, fmt, K, device=None):
+    """Checks a packed operand; returns its number of rows."""
+    torch = _torch()
+    for t, part in ((codes, "codes"), (scales, "scales")):
+        _on(t, f"{name} {part}", device)
+        if t.dtype is not torch.uint8 or not t.is_contiguous():
+            raise TypeError(f"{name} {part} must be contiguous uint8")
+        device = t.device
+    if codes.dim() != 2 or codes.shape[1] != (K + 31) // 32 * 16:
+        raise ValueError(f"{name} codes must be rows x {(K + 31) // 32 * 16} bytes for K = {K}")
+    rows = codes.shape[0]
+    blk = FP4_BLOCK[fmt]
+    if scales.numel() != (rows + 127) // 128 * (((K + blk - 1) // blk + 3) // 4) * 512:
+        raise ValueError(f"{name} scales do not match {rows} rows of {K} values in format {fmt!r}")
+    return rows
+
+
+def _new_packed(rows, K, fmt, device):
+    torch = _torch()
+    blk = FP4_BLOCK[fmt]
+    return (torch.empty((rows, (K + 31) // 32 * 16), dtype=torch.uint8, device=device),
+            torch.empty(((rows + 127) // 128, ((K + blk - 1) // blk + 3) // 4, 512), dtype=torch.uint8,
+                        device=device))
+
+
+def _one_f32(t, name, fmt, device):
+    """Address of a tensor scale (one fp32 on the device), or None."""
+    if t is None:
+        return None
+    if fmt == "mx":
+        raise ValueError(f"{name}: format 'mx' has no tensor scale")
+    torch = _torch()
+    _on(t, name, device)
+    if t.dtype is not torch.float32 or t.numel() != 1:
+        raise TypeError(f"{name} must be one float32")
+    return t.data_ptr()
+
+
+def _vector(t, name, n, dtypes, device):
+    """Address of a contiguous vector of n values, or None."""
+    if t is None:
+        return None
+    _on(t, name, device)
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous values")
+    return t.data_ptr()
+
+
+def _scratch(ws, need, device, stream):
+    """The caller's workspace, or a new one that stays alive for `stream`."""
+    torch = _torch()
+    if ws is None:
+        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        if stream is not None:
+            ws.record_stream(stream)
+    else:
+        _on(ws, "ws", device)
+    return ws, ws.numel() * ws.element_size()
+
+
+def _weights(gamma, beta, D, xdtype, device):
+    """Addresses of gamma and beta and the id of their common type."""
+    torch = _torch()
+    either = (xdtype, torch.float32)
+    g = _vector(gamma, "gamma", D, either, device)
+    b = _vector(beta, "beta", D, either, device)
+    if gamma is not None and beta is not None and gamma.dtype is not beta.dtype:
+        raise TypeError("gamma and beta must have the same type")
+    w = gamma if gamma is not None else beta
+    return g, b, _dtype_id(xdtype if w is None else w.dtype, "gamma")
+
+
+def fp4_tensor_scale(X, out=None, ws=None, stream=None):
+    """The "nv" tensor scale of X: max(|x|) / 2688 over its finite values, one fp32 on the device."""
+    torch = _torch()
+    ld = _matrix(X, "X")
+    dt = _dtype_id(X.dtype, "X")
+    if out is None:
+        out = torch.empty(1, dtype=torch.float32, device=X.device)
+    ptr = _one_f32(out, "out", "nv", X.device)
+    ws, wsb = _scratch(ws, 4096, X.device, stream)
+    _check("fp4_tensor_scale", lib().fp4_tensor_scale(dt, X.shape[0], X.shape[1], X.data_ptr(), ld, ptr,
+                                                      ws.data_ptr(), wsb, _stream(stream)))
+    return out
+
+
+def fp4_quantize(X, fmt: str = "nv", scale=None, out=None, stream=None):
+    """X (M x K) -> (codes, scales), blocks along its rows; scale: the "nv" tensor scale (None = 1)."""
+    f = _fmt_id(fmt)
+    ld = _matrix(X, "X")
+    M, K = X.shape
+    if out is None:
+        out = _new_packed(M, K, fmt, X.device)
+    Xq, Xs = out
+    if _packed(Xq, Xs, "out", fmt, K, X.device) != M:
+        raise ValueError(f"out must have {M} rows")
+    _check("fp4_quantize", lib().fp4_quantize(
+        f, _dtype_id(X.dtype, "X"), M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, X.device),
+        Xq.data_ptr(), Xs.data_ptr(), _stream(stream)))
+    return Xq, Xs
+
+
+def fp4_quantize_both(X, fmt: str = "nv", scale=None, out=None, stream=None):
+    """X (M x K) -> (codes, scales) of X and (codes, scales) of its transpose, reading X once."""
+    f = _fmt_id(fmt)
+    ld = _matrix(X, "X")
+    M, K = X.shape
+    if out is None:
+        out = _new_packed(M, K, fmt, X.device) + _new_packed(K, M, fmt, X.device)
+    Xq, Xs, Tq, Ts = out
+    if (_packed(Xq, Xs, "out", fmt, K, X.device) != M or _packed(Tq, Ts, "transposed out", fmt, M, X.device) != K):
+        raise ValueError(f"out must have {M} rows, and {K} transposed")
+    _check("fp4_quantize_both", lib().fp4_quantize_both(
+        f, _dtype_id(X.dtype, "X"), M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, X.device),
+        Xq.data_ptr(), Xs.data_ptr(), Tq.data_ptr(), Ts.data_ptr(), _stream(stream)))
+    return Xq, Xs, Tq, Ts
+
+
+def fp4_dequantize(Xq, Xs, K: int, fmt: str = "nv", scale=None, dtype=None, Y=None, stream=None):
+    """The values (M x K) of a packed operand, in `dtype` (default: that of Y, or float32)."""
+    torch = _torch()
+    f = _fmt_id(fmt)
+    M = _packed(Xq, Xs, "X", fmt, K)
+    if Y is None:
+        Y = torch.empty((M, K), dtype=dtype or torch.float32, device=Xq.device)
+    ld = _matrix(Y, "Y", Xq.device, dtype, (M, K))
+    _check("fp4_dequantize", lib().fp4_dequantize(
+        f, _dtype_id(Y.dtype, "Y"), M, K, Xq.data_ptr(), Xs.data_ptr(), _one_f32(scale, "scale", fmt, Xq.device),
+        Y.data_ptr(), ld, _stream(stream)))
+    return Y
+
+
+def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None, bias=None, dtype=None,
+             Y=None, stream=None):
+    """Y = A . B^T + bias of packed A (M x K) and B (N x K), in `dtype` (default: that of Y, or bfloat16)."""
+    torch = _torch()
+    f = _fmt_id(fmt)
+    M = _packed(Aq, As, "A", fmt, K)
+    N = _packed(Bq, Bs, "B", fmt, K, Aq.device)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=Aq.device)
+    ld = _matrix(Y, "Y", Aq.device, dtype, (M, N))
+    _check("fp4_gemm", lib().fp4_gemm(
+        f, _dtype_id(Y.dtype, "Y"), M, N, K, Aq.data_ptr(), As.data_ptr(),
+        _one_f32(a_scale, "a_scale", fmt, Aq.device), Bq.data_ptr(), Bs.data_ptr(),
+        _one_f32(b_scale, "b_scale", fmt, Aq.device), _vector(bias, "bias", N, (Y.dtype,), Aq.device),
+        Y.data_ptr(), ld, _stream(stream)))
+    return Y
+
+
+def fp4_linear(X, Wq, Ws, fmt: str = "nv", x_scale=None, w_scale=None, bias=None, Y=None, ws=None, stream=None):
+    """Y = Q(X) . W^T + bias with packed weights W (N x K); X (M x K) is quantized in the call, Y has its type."""
+    torch = _torch()
+    f = _fmt_id(fmt)
+    ldx = _matrix(X, "X")
+    dev = X.device
+    dt = _dtype_id(X.dtype, "X")
+    M, K = X.shape
+    N = _packed(Wq, Ws, "W", fmt, K, dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=X.dtype, device=dev)
+    ldy = _matrix(Y, "Y", dev, X.dtype, (M, N))
+    ws, wsb = _scratch(ws, workspace_size(QG_OP_FP4_LINEAR, M, N, K), dev, stream)
+    _check("fp4_linear", lib().fp4_linear(
+        f, dt, M, N, K, X.data_ptr(), ldx, _one_f32(x_scale, "x_scale", fmt, dev), Wq.data_ptr(), Ws.data_ptr(),
+        _one_f32(w_scale, "w_scale", fmt, dev), _vector(bias, "bias", N, (X.dtype,), dev), Y.data_ptr(), ldy,
+        ws.data_ptr(), wsb, _stream(stream)))
+    return Y
+
+
+def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale=None, w_scale=None,
+                        need_dx: bool = True, need_dw: bool = True, need_db: bool = True, out=None, ws=None,
+                        stream=None):
+    """Gradients (dX, dW, db) of Y = X . W^T + bias from quantized products.
+
+    Wtq, Wts: the packed transpose of W (K rows, blocks along N; the last two
+    results of fp4_quantize_both(W)).  dX and dW have the type of dY, db (the
+    column sums of dY) is fp32.  A gradient that is not needed is None.
+    """
+    torch = _torch()
+    f = _fmt_id(fmt)
+    lddy = _matrix(dY, "dY")
+    dev, dtype = dY.device, dY.dtype
+    dt = _dtype_id(dtype, "dY")
+    M, N = dY.shape
+    _on(X, "X", dev)
+    K = X.shape[-1]
+    ldx = _matrix(X, "X", dev, dtype, (M, K))
+    if _packed(Wtq, Wts, "W^T", fmt, N, dev) != K:
+        raise ValueError(f"W^T must have {K} rows")
+    if out is None:
+        out = (torch.empty((M, K), dtype=dtype, device=dev) if need_dx else None,
+               torch.empty((N, K), dtype=dtype, device=dev) if need_dw else None,
+               torch.empty(N, dtype=torch.float32, device=dev) if need_db else None)
+    dX, dW, db = out
+    lddx = 0 if dX is None else _matrix(dX, "dX", dev, dtype, (M, K))
+    lddw = 0 if dW is None else _matrix(dW, "dW", dev, dtype, (N, K))
+    if dX is None and dW is None and db is None:
+        return out
+    ws, wsb = _scratch(ws, workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K), dev, stream)
+    _check("fp4_linear_backward", lib().fp4_linear_backward(
+        f, dt, M, N, K, dY.data_ptr(), lddy, _one_f32(dy_scale, "dy_scale", fmt, dev), X.data_ptr(), ldx,
+        _one_f32(x_scale, "x_scale", fmt, dev), Wtq.data_ptr(), Wts.data_ptr(),
+        _one_f32(w_scale, "w_scale", fmt, dev), None if dX is None else dX.data_ptr(), lddx,
+        None if dW is None else dW.data_ptr(), lddw, _vector(db, "db", N, (torch.float32,), dev),
+        ws.data_ptr(), wsb, _stream(stream)))
+    return out
+
+
+def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, Y=None, stats=None, stream=None):
+    """(Y, mean, rstd) of the rows of X (M x D); gamma and beta in X's type or fp32 (None = 1, 0)."""
+    torch = _torch()
+    ldx = _matrix(X, "X")
+    dev = X.device
+    M, D = X.shape
+    g, b, wd = _weights(gamma, beta, D, X.dtype, dev)
+    if Y is None:
+        Y = torch.empty((M, D), dtype=X.dtype, device=dev)
+    ldy = _matrix(Y, "Y", dev, X.dtype, (M, D))
+    mean, rstd = stats if stats is not None else torch.empty((2, M), dtype=torch.float32, device=dev).unbind(0)
+    f32 = (torch.float32,)
+    _check("layer_norm", lib().layer_norm(
+        _dtype_id(X.dtype, "X"), M, D, X.data_ptr(), ldx, g, b, wd, eps, Y.data_ptr(), ldy,
+        _vector(mean, "mean", M, f32, dev), _vector(rstd, "rstd", M, f32, dev), _stream(stream)))
+    return Y, mean, rstd
+
+
+def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv", scale=None, out=None, stats=None,
+                   stream=None):
+    """(codes, scales, mean, rstd): layer_norm of X with y quantized instead of stored."""
+    torch = _torch()
+    f = _fmt_id(fmt)
+    ldx = _matrix(X, "X")
+    dev = X.device
+    M, D = X.shape
+    g, b, wd = _weights(gamma, beta, D, X.dtype, dev)
+    if out is None:
+        out = _new_packed(M, D, fmt, dev)
+    Xq, Xs = out
+    if _packed(Xq, Xs, "out", fmt, D, dev) != M:
+        raise ValueError(f"out must have {M} rows")
+    mean, rstd = stats if stats is not None else torch.empty((2, M), dtype=torch.float32, device=dev).unbind(0)
+    f32 = (torch.float32,)
+    _check("layer_norm_fp4", lib().layer_norm_fp4(
+        f, _dtype_id(X.dtype, "X"), M, D, X.data_ptr(), ldx, g, b, wd, eps, _one_f32(scale, "scale", fmt, dev),
+        Xq.data_ptr(), Xs.data_ptr(), _vector(mean, "mean", M, f32, dev), _vector(rstd, "rstd", M, f32, dev),
+        _stream(stream)))
+    return Xq, Xs, mean, rstd
+
+
+def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None):
+    """(dX, dgamma, dbeta) of layer_norm, with the mean and rstd it returned; dgamma and dbeta are fp32."""
+    torch = _torch()
+    ldx = _matrix(X, "X")
+    dev = X.device
+    M, D = X.shape
+    lddy = _matrix(dY, "dY", dev, X.dtype, (M, D))
+    g, _, wd = _weights(gamma, None, D, X.dtype, dev)
+    if out is None:
+        dgb = torch.empty((2, D), dtype=torch.float32, device=dev)
+        out = (torch.empty((M, D), dtype=X.dtype, device=dev), dgb[0], dgb[1])
+    dX, dgamma, dbeta = out
+    lddx = _matrix(dX, "dX", dev, X.dtype, (M, D))
+    f32 = (torch.float32,)
+    ws, wsb = _scratch(ws, workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D), dev, stream)
+    _check("layer_norm_backward", lib().layer_norm_backward(
+        _dtype_id(X.dtype, "X"), M, D, dY.data_ptr(), lddy, X.data_ptr(), ldx, g, wd,
+        _vector(mean, "mean", M, f32, dev), _vector(rstd, "rstd", M, f32, dev), dX.data_ptr(), lddx,
+        _vector(dgamma, "dgamma", D, f32, dev), _vector(dbeta, "dbeta", D, f32, dev), ws.data_ptr(), wsb,
+        _stream(stream)))
+    return out

@@ -1,0 +1,306 @@
+// Microscaled 4-bit floating point: formats, packed layout and conversions
+// shared by the quantizers, the products and the norm that feeds them.
+//
+// A value is e2m1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives) times the scale
+// of its block along the reduction axis, times a scale of the whole tensor:
+//   nv: blocks of 16, e4m3 block scale  s = e4m3(fl(amax / fl(6 ts))), at most
+//       448, tensor scale ts (fp32);
+//   mx: blocks of 32, e8m0 block scale  s = 2^(floor(log2 amax) - 2), no
+//       tensor scale (1).
+// With d = fl(s ts) and r = fl(1 / d), the code of x is fl(x r) rounded to
+// e2m1, ties to even, saturated at +-6; a block whose scale is 0 gets codes 0.
+// A block that holds an infinity or a NaN gets the format's NaN scale.
+//
+// Packed layout of a rows x K operand:
+//   codes  : rows of codes_ld(K) bytes, the even position in the low nibble,
+//            zero behind K;
+//   scales : 512-byte tiles of 128 rows x 4 blocks, row-block major; row r,
+//            block c of a tile at byte 16 (r % 32) + 4 (r / 32) + c.  This is
+//            the order in which tcgen05.cp 32x128b puts scales into tensor
+//            memory (lane r % 32, column r / 32, byte c), so a tile moves from
+//            global memory to the tensor core untouched.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "qg_internal.h"
+
+namespace qg {
+
+constexpr int kNv = QG_FP4_NV, kMx = QG_FP4_MX;
+
+__host__ __device__ constexpr int fp4_block(int fmt) { return fmt == kNv ? 16 : 32; }
+__host__ __device__ inline int64_t fp4_codes_ld(int64_t K) { return (K + 31) / 32 * 16; }
+__host__ __device__ inline int64_t fp4_col_tiles(int fmt, int64_t K) {
+    const int64_t b = fp4_block(fmt);
+    return ((K + b - 1) / b + 3) / 4;
+}
+__host__ __device__ inline int64_t fp4_scale_bytes(int fmt, int64_t rows, int64_t K) {
+    return (rows + 127) / 128 * fp4_col_tiles(fmt, K) * 512;
+}
+// Byte of the scale of (row, block) among `col_tiles` tiles a row-block.
+__host__ __device__ inline int64_t fp4_scale_offset(int64_t row, int64_t blk, int64_t col_tiles) {
+    return ((row >> 7) * col_tiles + (blk >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
+}
+
+// ------------------------------------------------------- element types
+
+template <class T>
+__device__ __forceinline__ float to_f32(T v);
+template <>
+__device__ __forceinline__ float to_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float v) { return __float2half_rn(v); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+// Two values from / to one 32-bit word of a 16-bit type.
+template <class T>
+__device__ __forceinline__ float2 unpack2(uint32_t w);
+template <>
+__device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+template <>
+__device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// N consecutive values; p is 16-byte aligned and all N exist.
+template <class T, int N>
+__device__ __forceinline__ void load_vec(const T* p, float (&x)[N]) {
+    if constexpr (sizeof(T) == 4) {
+        static_assert(N % 4 == 0, "16-byte pieces");
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(p + i);
+            x[i] = v.x; x[i + 1] = v.y; x[i + 2] = v.z; x[i + 3] = v.w;
+        }
+    } else {
+        static_assert(N % 8 == 0, "16-byte pieces");
+#pragma unroll
+        for (int i = 0; i < N; i += 8) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack2<T>(w[j]);
+                x[i + 2 * j] = f.x;
+                x[i + 2 * j + 1] = f.y;
+            }
+        }
+    }
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_vec(T* p, const float (&x)[N]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4)
+            *reinterpret_cast<float4*>(p + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 8)
+            *reinterpret_cast<uint4*>(p + i) =
+                make_uint4(pack2<T>(x[i], x[i + 1]), pack2<T>(x[i + 2], x[i + 3]),
+                           pack2<T>(x[i + 4], x[i + 5]), pack2<T>(x[i + 6], x[i + 7]));
+    }
+}
+
+// N consecutive values of which the first `n` exist (the rest read as 0).
+template <class T, int N>
+__device__ __forceinline__ void load_some(const T* p, int n, bool aligned, float (&x)[N]) {
+    if (aligned && n >= N) {
+        load_vec<T, N>(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = i < n ? to_f32<T>(p[i]) : 0.f;
+    }
+}
+
+template <class T, int N>
+__device__ __forceinline__ void store_some(T* p, int n, bool aligned, const float (&x)[N]) {
+    if (aligned && n >= N) {
+        store_vec<T, N>(p, x);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < n) p[i] = from_f32<T>(x[i]);
+    }
+}
+
+// ------------------------------------------------------- scales and codes
+
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+    const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte), __NV_E4M3);
+    return __half2float(__half(h));
+}
+
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255 ? 0x7fc00000u : byte << 23);
+}
+
+template <int FMT>
+__device__ __forceinline__ float scale_value(uint32_t byte) {
+    return FMT == kNv ? e4m3_value(byte) : e8m0_value(byte);
+}
+
+// Scale byte of a block and the factor r its values are multiplied by.
+// `amax_bits` is the largest |x| of the block as bits: as unsigned numbers
+// they order like the magnitudes, with infinity and NaN above all others.
+struct BlockScale {
+    uint32_t byte;
+    float r;
+};
+
+template <int FMT>
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float ts, float six_ts) {
+    BlockScale b;
+    if constexpr (FMT == kNv) {
+        const float q = __fdiv_rn(__uint_as_float(amax_bits), six_ts);
+        b.byte = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+        const float d = __fmul_rn(e4m3_value(b.byte), ts);
+        b.r = b.byte ? __frcp_rn(d) : 0.f;
+        if (amax_bits >= 0x7f800000u) b = {0x7fu, 0.f};
+    } else {
+        const uint32_t e = amax_bits >> 23;  // floor(log2) + 127; 0 below 2^-126
+        b.byte = e > 2 ? e - 2 : 0;
+        // 2^(127 - byte): bits (254 - byte) << 23; byte <= 252, so it is normal
+        b.r = __uint_as_float((254u - b.byte) << 23);
+        if (amax_bits >= 0x7f800000u) b = {0xffu, 0.f};
+    }
+    return b;
+}
+
+// Eight values to eight e2m1 codes (round to nearest, ties to even, saturated
+// at 6), value i in nibble i.
+__device__ __forceinline__ uint32_t e2m1x8(const float* x) {
+    uint32_t r;
+    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        "mov.b32 %0, {b0, b1, b2, b3};\n}"
+        : "=r"(r)
+        : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+
+// Eight codes to eight values, exact.
+__device__ __forceinline__ void e2m1x8_values(uint32_t w, float (&x)[8]) {
+    uint32_t h[4];
+    asm("{\n.reg .b8 b0, b1, b2, b3;\n"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = unpack2<__half>(h[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+template <int N>
+__device__ __forceinline__ uint32_t absmax_bits(const float (&x)[N]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+}
+
+// One block of a row: its codes (BLOCK / 8 words) and its scale byte.
+template <int FMT>
+__device__ __forceinline__ uint32_t quantize_block(const float (&x)[fp4_block(FMT)], float ts, float six_ts,
+                                                   uint32_t (&codes)[fp4_block(FMT) / 8]) {
+    constexpr int B = fp4_block(FMT);
+    const BlockScale s = block_scale<FMT>(absmax_bits<B>(x), ts, six_ts);
+#pragma unroll
+    for (int i = 0; i < B; i += 8) {
+        float y[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(x[i + j], s.r);
+        codes[i / 8] = e2m1x8(y);
+    }
+    return s.byte;
+}
+
+// ------------------------------------------------------- host
+
+inline size_t dtype_bytes(int dtype) { return dtype == QG_F32 ? 4 : 2; }
+inline bool dtype_ok(int dtype) { return dtype == QG_F16 || dtype == QG_BF16 || dtype == QG_F32; }
+inline bool fmt_ok(int fmt) { return fmt == kNv || fmt == kMx; }
+
+// Launches with programmatic stream serialization: the kernel may be set up
+// while the one before it on the stream drains.  Every kernel launched this
+// way begins with pdl_wait_prior_grid() before it reads or writes memory that
+// an earlier call may use, and lets its own successor start only after that.
+template <class F, class... Args>
+int launch_serialized(F* kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
+                      Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cluster > 1) {
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+    }
+    return map_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+// Calls f with a value of the C++ type of `dtype`.
+template <class F>
+int by_dtype(int dtype, F&& f) {
+    if (dtype == QG_F16) return f(__half{});
+    if (dtype == QG_BF16) return f(__nv_bfloat16{});
+    return f(float{});
+}
+
+// Quantizers (qg_fp4_quant.cu); arguments already checked.
+int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
+                     uint8_t* Xq, uint8_t* Xs, bool zero_pad, cudaStream_t s);
+int fp4_quantize_both_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
+                          uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* colsum, float* partial,
+                          cudaStream_t s);
+
+// Adds `parts` rows of n partial sums, in order, into out (qg_norm.cu).
+int sum_partials_run(const float* partial, int64_t parts, int64_t n, float* out, cudaStream_t s);
+
+}  // namespace qg

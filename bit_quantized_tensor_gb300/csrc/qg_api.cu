@@ -34,6 +34,11 @@ std::vector<qg::KernelBudget>& budgets() {
     return v;
 }
 
+std::vector<qg::KernelBudget>& block_budgets() {
+    static std::vector<qg::KernelBudget> v;
+    return v;
+}
+
 std::mutex& budgets_mutex() {
     static std::mutex m;
     return m;
@@ -47,6 +52,12 @@ int register_kernel_budget(const KernelBudget& b) {
     std::lock_guard<std::mutex> g(budgets_mutex());
     budgets().push_back(b);
     return static_cast<int>(budgets().size()) - 1;
+}
+
+int register_block_kernel_budget(const KernelBudget& b) {
+    std::lock_guard<std::mutex> g(budgets_mutex());
+    block_budgets().push_back(b);
+    return static_cast<int>(block_budgets().size()) - 1;
 }
 
 int record_cuda_error(int code) {
@@ -94,6 +105,51 @@ int num_sms(int device) {
 
 }  // namespace qg
 
+static int budget_count(const std::vector<qg::KernelBudget>& table) {
+    std::lock_guard<std::mutex> g(budgets_mutex());
+    return static_cast<int>(table.size());
+}
+
+static int budget_get(const std::vector<qg::KernelBudget>& table, int index, qg_kernel_budget* out) {
+    if (!out) return QG_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> g(budgets_mutex());
+    if (index < 0 || index >= static_cast<int>(table.size())) return QG_ERR_INVALID_ARG;
+    const qg::KernelBudget& b = table[static_cast<size_t>(index)];
+    out->kernel = b.name;
+    out->threads = b.threads;
+    out->smem_bytes = b.smem_bytes;
+    out->tmem_cols = b.tmem_cols;
+    out->cluster = b.cluster;
+    out->min_ctas_per_sm = b.min_ctas_per_sm;
+    return QG_OK;
+}
+
+static int budget_measure(const std::vector<qg::KernelBudget>& table, int index, int* regs_per_thread,
+                          int* static_smem_bytes, int* ctas_per_sm) {
+    if (!regs_per_thread || !static_smem_bytes || !ctas_per_sm) return QG_ERR_INVALID_ARG;
+    qg::KernelBudget b;
+    {
+        std::lock_guard<std::mutex> g(budgets_mutex());
+        if (index < 0 || index >= static_cast<int>(table.size())) return QG_ERR_INVALID_ARG;
+        b = table[static_cast<size_t>(index)];
+    }
+    cudaFuncAttributes fa;
+    cudaError_t e = cudaFuncGetAttributes(&fa, b.func);
+    if (e != cudaSuccess) return qg::map_cuda(e);
+    *regs_per_thread = fa.numRegs;
+    *static_smem_bytes = static_cast<int>(fa.sharedSizeBytes);
+    if (b.smem_bytes > 0) {
+        e = cudaFuncSetAttribute(b.func, cudaFuncAttributeMaxDynamicSharedMemorySize, b.smem_bytes);
+        if (e != cudaSuccess) return qg::map_cuda(e);
+    }
+    int n = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, b.func, b.threads,
+                                                      static_cast<size_t>(b.smem_bytes));
+    if (e != cudaSuccess) return qg::map_cuda(e);
+    *ctas_per_sm = n;
+    return QG_OK;
+}
+
 static size_t round_up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
 extern "C" {
@@ -139,6 +195,10 @@ size_t qg_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
             const size_t np = (n + 3) & ~static_cast<size_t>(3);
             return round_up256(n * k) + round_up256(4 * nblk * np);
         }
+        case QG_OP_FP4_LINEAR: return qg::fp4_linear_workspace(M, K);
+        case QG_OP_FP4_LINEAR_BACKWARD: return qg::fp4_linear_backward_workspace(M, N, K);
+        case QG_OP_LAYER_NORM_BACKWARD: return qg::norm_backward_workspace(K);
+        case QG_OP_FP4_TENSOR_SCALE: return 4096;  // one maximum per CTA, at most 1024
         default:
             return 0;
     }
@@ -173,49 +233,22 @@ int qg_device_status_detail(int* words, void* stream) {
 
 int qg_device_status(void* stream) { return qg_device_status_detail(nullptr, stream); }
 
-int qg_kernel_budget_count(void) {
-    std::lock_guard<std::mutex> g(budgets_mutex());
-    return static_cast<int>(budgets().size());
+int qg_kernel_budget_count(void) { return budget_count(budgets()); }
+
+int qg_kernel_budget_get(int index, qg_kernel_budget* out) { return budget_get(budgets(), index, out); }
+
+int qg_kernel_budget_measure(int index, int* regs_per_thread, int* static_smem_bytes, int* ctas_per_sm) {
+    return budget_measure(budgets(), index, regs_per_thread, static_smem_bytes, ctas_per_sm);
 }
 
-int qg_kernel_budget_get(int index, qg_kernel_budget* out) {
-    if (!out) return QG_ERR_INVALID_ARG;
-    std::lock_guard<std::mutex> g(budgets_mutex());
-    if (index < 0 || index >= static_cast<int>(budgets().size())) return QG_ERR_INVALID_ARG;
-    const qg::KernelBudget& b = budgets()[static_cast<size_t>(index)];
-    out->kernel = b.name;
-    out->threads = b.threads;
-    out->smem_bytes = b.smem_bytes;
-    out->tmem_cols = b.tmem_cols;
-    out->cluster = b.cluster;
-    out->min_ctas_per_sm = b.min_ctas_per_sm;
-    return QG_OK;
+int qg_block_kernel_budget_count(void) { return budget_count(block_budgets()); }
+
+int qg_block_kernel_budget_get(int index, qg_kernel_budget* out) {
+    return budget_get(block_budgets(), index, out);
 }
 
-int qg_kernel_budget_measure(int index, int* regs_per_thread, int* static_smem_bytes,
-                             int* ctas_per_sm) {
-    if (!regs_per_thread || !static_smem_bytes || !ctas_per_sm) return QG_ERR_INVALID_ARG;
-    qg::KernelBudget b;
-    {
-        std::lock_guard<std::mutex> g(budgets_mutex());
-        if (index < 0 || index >= static_cast<int>(budgets().size())) return QG_ERR_INVALID_ARG;
-        b = budgets()[static_cast<size_t>(index)];
-    }
-    cudaFuncAttributes fa;
-    cudaError_t e = cudaFuncGetAttributes(&fa, b.func);
-    if (e != cudaSuccess) return qg::map_cuda(e);
-    *regs_per_thread = fa.numRegs;
-    *static_smem_bytes = static_cast<int>(fa.sharedSizeBytes);
-    if (b.smem_bytes > 0) {
-        e = cudaFuncSetAttribute(b.func, cudaFuncAttributeMaxDynamicSharedMemorySize, b.smem_bytes);
-        if (e != cudaSuccess) return qg::map_cuda(e);
-    }
-    int n = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, b.func, b.threads,
-                                                      static_cast<size_t>(b.smem_bytes));
-    if (e != cudaSuccess) return qg::map_cuda(e);
-    *ctas_per_sm = n;
-    return QG_OK;
+int qg_block_kernel_budget_measure(int index, int* regs_per_thread, int* static_smem_bytes, int* ctas_per_sm) {
+    return budget_measure(block_budgets(), index, regs_per_thread, static_smem_bytes, ctas_per_sm);
 }
 
 }  // extern "C"

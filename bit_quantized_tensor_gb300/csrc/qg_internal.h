@@ -66,11 +66,24 @@ struct KernelBudget {
 };
 int register_kernel_budget(const KernelBudget& b);
 
+// The kernels around the GEMMs (microscaled 4-bit operators, norms) register in
+// a table of their own.
+int register_block_kernel_budget(const KernelBudget& b);
+
 #define QG_BUDGET_CAT2(a, b) a##b
 #define QG_BUDGET_CAT(a, b) QG_BUDGET_CAT2(a, b)
 #define QG_KERNEL_BUDGET(...)                                       \
     static const int QG_BUDGET_CAT(qg_kernel_budget_, __COUNTER__) = \
         ::qg::register_kernel_budget(::qg::KernelBudget{__VA_ARGS__})
+
+#define QG_BLOCK_KERNEL_BUDGET(...)                                       \
+    static const int QG_BUDGET_CAT(qg_block_kernel_budget_, __COUNTER__) = \
+        ::qg::register_block_kernel_budget(::qg::KernelBudget{__VA_ARGS__})
+
+// Workspace bytes of the microscaled 4-bit products and of the norm's backward.
+size_t fp4_linear_workspace(int64_t M, int64_t K);
+size_t fp4_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
+size_t norm_backward_workspace(int64_t D);
 
 // Workspace bytes of qgemm_s8_host (qg_hostio.cu).
 size_t s8_host_workspace(int64_t M, int64_t N, int64_t K);

@@ -66,7 +66,11 @@ typedef enum { QG_ROW_MAJOR = 0, QG_COL_MAJOR = 1 } qg_layout;
 typedef enum {
     QG_OP_S8 = 0, QG_OP_S4 = 1, QG_OP_F16 = 2, QG_OP_W4A16 = 3, QG_OP_W4A4 = 4, QG_OP_S8_HOST = 5,
     QG_OP_W4A4_PREPACKED = 6,  /* workspace of w4a4_gemm_prepacked */
-    QG_OP_W4A4_WEIGHTS = 7     /* size of the buffer w4a4_prepack_weights fills (M unused: pass 1) */
+    QG_OP_W4A4_WEIGHTS = 7,    /* size of the buffer w4a4_prepack_weights fills (M unused: pass 1) */
+    QG_OP_FP4_LINEAR = 8,           /* workspace of fp4_linear (either format) */
+    QG_OP_FP4_LINEAR_BACKWARD = 9,  /* workspace of fp4_linear_backward (either format) */
+    QG_OP_LAYER_NORM_BACKWARD = 10, /* workspace of layer_norm_backward (K = row length; M, N unused: pass 1) */
+    QG_OP_FP4_TENSOR_SCALE = 11     /* workspace of fp4_tensor_scale (sizes unused: pass 1) */
 } qg_op;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -131,6 +135,13 @@ int qg_kernel_budget_get(int index, qg_kernel_budget *out);
  * entry's size first, as the launcher does).  QG_ERR_CUDA without a device. */
 int qg_kernel_budget_measure(int index, int *regs_per_thread, int *static_smem_bytes,
                              int *ctas_per_sm);
+
+/* The same three for the table of the kernels around the GEMMs: microscaled
+ * 4-bit floating point and layer norm. */
+int qg_block_kernel_budget_count(void);
+int qg_block_kernel_budget_get(int index, qg_kernel_budget *out);
+int qg_block_kernel_budget_measure(int index, int *regs_per_thread, int *static_smem_bytes,
+                                   int *ctas_per_sm);
 
 /* Self-test of the failure path (no counterpart on the pages): enqueues one
  * CTA that waits on an mbarrier nothing arrives on, with a limit of limit_ns
@@ -417,6 +428,120 @@ int w4a4_gemm_prepacked(int64_t M, int64_t N, int64_t K,
                         const uint16_t *XU, const uint16_t *V, int64_t rank,
                         const uint16_t *bias, uint16_t *Y, int64_t ldy,
                         void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * Microscaled 4-bit floating point, and the layer norm in front of it.
+ *
+ * A value is an e2m1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and negatives) times the
+ * scale of its block of consecutive values along the reduction axis (the row
+ * of the packed operand), times a scale of the whole tensor:
+ *   QG_FP4_NV  blocks of 16; block scale s = e4m3(fl(amax / fl(6 ts))), ties
+ *              to even, at most 448; ts the tensor scale, a positive fp32 in
+ *              device memory (NULL = 1).
+ *   QG_FP4_MX  blocks of 32; block scale s = 2^(floor(log2 amax) - 2), as an
+ *              e8m0 byte (exponent + 127, at least 0); no tensor scale.
+ * With d = fl(s ts) and r = fl(1 / d) (fl: rounded to fp32), the code of x is
+ * fl(x r) rounded to e2m1, ties to even, saturated at +-6.  A block whose
+ * scale rounds to 0 has codes 0.  A block with an infinity or a NaN gets the
+ * NaN scale (0x7f, 0xff): its values, and sums over them, are NaN.
+ *
+ * Packed operand of a rows x K matrix, K >= 1:
+ *   codes   rows x qg_fp4_codes_ld(K) bytes (K up to whole 16 bytes), the even
+ *           position in the low nibble, 0 behind K;
+ *   scales  qg_fp4_scale_bytes(fmt, rows, K) bytes: tiles of 128 rows x 4
+ *           blocks, 512 bytes each, ceil(blocks / 4) tiles for every 128 rows;
+ *           row r, block c of a tile at byte 16 (r % 32) + 4 (r / 32) + c;
+ *           0 behind the last row and the last block.
+ * Codes and scales are 16-byte aligned.  Matrices of floating type (qg_dtype)
+ * are row-major with any leading dimension >= their row length and any address
+ * their element size allows; 16-byte aligned rows are read and written faster.
+ * Sizes may be 0 unless stated otherwise: nothing is enqueued for an empty
+ * result, and a product over nothing is its bias (or 0).
+ * Calls are asynchronous on `stream`, may be captured in a CUDA graph, and give
+ * the same bits on every run.  Outputs must not overlap inputs. */
+typedef enum { QG_FP4_NV = 0, QG_FP4_MX = 1 } qg_fp4_format;
+typedef enum { QG_F16 = 0, QG_BF16 = 1, QG_F32 = 2 } qg_dtype;
+
+/* Bytes of a packed row of K codes; 0 for K <= 0. */
+int64_t qg_fp4_codes_ld(int64_t K);
+
+/* Bytes of the scales of a packed rows x K operand; 0 for an empty one or an
+ * unknown format. */
+size_t qg_fp4_scale_bytes(int fmt, int64_t rows, int64_t K);
+
+/* *scale = max(fl(amax fl(1 / 2688)), 2^-100) over the finite values of X
+ * (M x K), 1 if they are all 0: the tensor scale with which the largest value of X is the
+ * largest code (6) times the largest block scale (448).
+ *  ws: qg_workspace_size(QG_OP_FP4_TENSOR_SCALE, 1, 1, 1) bytes. */
+int fp4_tensor_scale(int dtype, int64_t M, int64_t K, const void *X, int64_t ldx, float *scale,
+                     void *ws, size_t ws_bytes, void *stream);
+
+/* X (M x K) to the packed operand (Xq, Xs), blocks along its rows. */
+int fp4_quantize(int fmt, int dtype, int64_t M, int64_t K, const void *X, int64_t ldx,
+                 const float *tscale, uint8_t *Xq, uint8_t *Xs, void *stream);
+
+/* X (M x K) to the packed operand of X (Xq, Xs; both may be NULL) and of its
+ * transpose (Tq, Ts: K rows, blocks along M), reading X once. */
+int fp4_quantize_both(int fmt, int dtype, int64_t M, int64_t K, const void *X, int64_t ldx,
+                      const float *tscale, uint8_t *Xq, uint8_t *Xs, uint8_t *Tq, uint8_t *Ts,
+                      void *stream);
+
+/* The values a packed operand stands for, fl(code d) rounded to `dtype`. */
+int fp4_dequantize(int fmt, int dtype, int64_t M, int64_t K, const uint8_t *Xq, const uint8_t *Xs,
+                   const float *tscale, void *Y, int64_t ldy, void *stream);
+
+/* Y (M x N, `dtype`) = A . B^T + bias with A (M x K) and B (N x K) packed and
+ * bias N values of `dtype` or NULL: fp32 accumulation, one rounding. */
+int fp4_gemm(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const uint8_t *Aq,
+             const uint8_t *As, const float *a_tscale, const uint8_t *Bq, const uint8_t *Bs,
+             const float *b_tscale, const void *bias, void *Y, int64_t ldy, void *stream);
+
+/* Y = Q(X) . W^T + bias: fp4_quantize of X (M x K, `dtype`) and fp4_gemm with
+ * the packed weights W (N x K) in one call.
+ *  ws: qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K) bytes, 256-byte aligned. */
+int fp4_linear(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
+               const float *x_tscale, const uint8_t *Wq, const uint8_t *Ws, const float *w_tscale,
+               const void *bias, void *Y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of Y = X . W^T + bias from dY (M x N), all of `dtype` but db:
+ *   dX (M x K) = Q(dY) . Q(W^T)^T,  W^T packed by the caller (Wtq, Wts: K rows,
+ *                blocks along N; fp4_quantize_both of W gives it)
+ *   dW (N x K) = Q(dY^T) . Q(X^T)^T
+ *   db (N, fp32) = column sums of dY, not quantized
+ * Any of dX, dW and db may be NULL and is then left out.
+ *  ws: qg_workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K) bytes, 256-byte
+ *      aligned. */
+int fp4_linear_backward(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const void *dY,
+                        int64_t lddy, const float *dy_tscale, const void *X, int64_t ldx,
+                        const float *x_tscale, const uint8_t *Wtq, const uint8_t *Wts,
+                        const float *w_tscale, void *dX, int64_t lddx, void *dW, int64_t lddw,
+                        float *db, void *ws, size_t ws_bytes, void *stream);
+
+/* Layer norm of every row of X (M x D, D >= 1):
+ *   mean = sum(x) / D, rstd = 1 / sqrt(sum((x - mean)^2) / D + eps),
+ *   y = (x - mean) rstd gamma + beta.
+ * gamma and beta: D values of type wdtype (that of X, or QG_F32), NULL = 1, 0.
+ * mean and rstd (M fp32 each) may be NULL.  Statistics are fp32. */
+int layer_norm(int dtype, int64_t M, int64_t D, const void *X, int64_t ldx, const void *gamma,
+               const void *beta, int wdtype, float eps, void *Y, int64_t ldy, float *mean,
+               float *rstd, void *stream);
+
+/* The same, with y (fp32, not rounded in between) quantized into the packed
+ * operand (Xq, Xs) instead of stored. */
+int layer_norm_fp4(int fmt, int dtype, int64_t M, int64_t D, const void *X, int64_t ldx,
+                   const void *gamma, const void *beta, int wdtype, float eps,
+                   const float *tscale, uint8_t *Xq, uint8_t *Xs, float *mean, float *rstd,
+                   void *stream);
+
+/* Gradients of layer_norm, with mean and rstd as it wrote them:
+ *   xh = (x - mean) rstd, d = dy gamma,
+ *   dX = rstd (d - sum(d) / D - xh sum(d xh) / D)      (type of X)
+ *   dgamma = sum over rows of dy xh, dbeta = sum over rows of dy   (D fp32 each)
+ *  ws: qg_workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D) bytes. */
+int layer_norm_backward(int dtype, int64_t M, int64_t D, const void *dY, int64_t lddy,
+                        const void *X, int64_t ldx, const void *gamma, int wdtype,
+                        const float *mean, const float *rstd, void *dX, int64_t lddx,
+                        float *dgamma, float *dbeta, void *ws, size_t ws_bytes, void *stream);
 
 #ifdef __cplusplus
 }
