@@ -52,8 +52,6 @@ QG_ROW_MAJOR, QG_COL_MAJOR = 0, 1
  QG_OP_FP4_TENSOR_SCALE) = range(12)
 QG_FP4_NV, QG_FP4_MX = 0, 1
 QG_F16, QG_BF16, QG_F32 = 0, 1, 2
-FP4_FORMATS = {"nv": QG_FP4_NV, "mx": QG_FP4_MX}
-FP4_BLOCK = {"nv": 16, "mx": 32}
 
 
 class QgError(RuntimeError):
@@ -159,9 +157,15 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:  # an import statement on every call costs more than the call
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream(stream=None) -> int:
@@ -480,74 +484,94 @@ def w4a4_gemm_prepacked(Xq, Xscale, packed, N: int, K: int, XU=None, Vt=None, bi
 
 
 # ---------------------------------------------------------------- microscaled 4-bit, layer norm
+#
+# A small call takes a few microseconds on the device, so the host side counts:
+# each operand is looked at once, and the current stream comes as a raw handle
+# (the stream object that torch.cuda.current_stream() builds costs 3 us).
+
+_dtype_ids = None
+
 
 def _dtype_id(dtype, name):
-    torch = _torch()
-    if dtype is torch.bfloat16:
-        return QG_BF16
-    if dtype is torch.float16:
-        return QG_F16
-    if dtype is torch.float32:
-        return QG_F32
-    raise TypeError(f"{name} must be float16, bfloat16 or float32, got {dtype}")
+    global _dtype_ids
+    if _dtype_ids is None:
+        torch = _torch()
+        _dtype_ids = {torch.float16: QG_F16, torch.bfloat16: QG_BF16, torch.float32: QG_F32}
+    i = _dtype_ids.get(dtype)
+    if i is None:
+        raise TypeError(f"{name} must be float16, bfloat16 or float32, got {dtype}")
+    return i
 
 
 def _fmt_id(fmt):
-    try:
-        return FP4_FORMATS[fmt]
-    except (KeyError, TypeError):
-        raise ValueError(f"fmt must be 'nv' or 'mx', got {fmt!r}") from None
+    if fmt == "nv":
+        return QG_FP4_NV
+    if fmt == "mx":
+        return QG_FP4_MX
+    raise ValueError(f"fmt must be 'nv' or 'mx', got {fmt!r}")
+
+
+def _raw_stream(stream, device):
+    if stream is None:
+        return _torch_module._C._cuda_getCurrentRawStream(device.index)
+    return stream.cuda_stream
 
 
 def _on(t, name, device):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, _torch_module.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, other operands on {device}")
 
 
-def _matrix(t, name, device=None, dtype=None, shape=None):
-    """Checks a 2-D floating matrix with unit column stride; returns its leading dimension."""
+def _matrix(t, name, device=None, dtype=None, rows=None, cols=None):
+    """Checks a 2-D matrix with unit column stride; returns its leading dimension."""
     _on(t, name, device)
     if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 2:
+    shape = t.shape
+    if len(shape) != 2:
         raise ValueError(f"{name} must be 2-D")
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError(f"{name} must be {shape[0]} x {shape[1]}, got {rows} x {cols}")
+    m, k = shape
+    if rows is not None and (m != rows or k != cols):
+        raise ValueError(f"{name} must be {rows} x {cols}, got {m} x {k}")
     ld, unit = t.stride()
-    if unit != 1 and cols > 1 and rows > 0:
+    if unit != 1 and k > 1 and m > 0:
         raise ValueError(f"{name} must have a contiguous last dimension")
-    if rows > 1 and ld < cols:
+    if m <= 1:
+        return k
+    if ld < k:
         raise ValueError(f"the rows of {name} overlap")
-    return ld if rows > 1 else cols
+    return ld
+
+
+def _packed_shapes(rows, K, fmt):
+    per_tile = 64 if fmt == "nv" else 128  # values along K that a scale tile covers
+    return (rows, (K + 31) // 32 * 16), ((rows + 127) // 128, (K + per_tile - 1) // per_tile, 512)
 
 
 def _packed(codes, scales, name, fmt, K, device=None):
     """Checks a packed operand; returns its number of rows."""
-    torch = _torch()
-    for t, part in ((codes, "codes"), (scales, "scales")):
-        _on(t, f"{name} {part}", device)
-        if t.dtype is not torch.uint8 or not t.is_contiguous():
-            raise TypeError(f"{name} {part} must be contiguous uint8")
-        device = t.device
-    if codes.dim() != 2 or codes.shape[1] != (K + 31) // 32 * 16:
-        raise ValueError(f"{name} codes must be rows x {(K + 31) // 32 * 16} bytes for K = {K}")
-    rows = codes.shape[0]
-    blk = FP4_BLOCK[fmt]
-    if scales.numel() != (rows + 127) // 128 * (((K + blk - 1) // blk + 3) // 4) * 512:
-        raise ValueError(f"{name} scales do not match {rows} rows of {K} values in format {fmt!r}")
+    u8 = _torch_module.uint8
+    _on(codes, name, device)
+    _on(scales, name, codes.device)
+    if (codes.dtype is not u8 or scales.dtype is not u8 or not codes.is_contiguous()
+            or not scales.is_contiguous()):
+        raise TypeError(f"{name}: codes and scales must be contiguous uint8")
+    shape = codes.shape
+    rows = shape[0] if len(shape) == 2 else 0
+    want, (tr, tc, _) = _packed_shapes(rows, K, fmt)
+    if shape != want:
+        raise ValueError(f"{name}: codes must be rows x {want[1]} bytes for K = {K}")
+    if scales.numel() != tr * tc * 512:
+        raise ValueError(f"{name}: scales do not match {rows} rows of {K} values in format {fmt!r}")
     return rows
 
 
 def _new_packed(rows, K, fmt, device):
-    torch = _torch()
-    blk = FP4_BLOCK[fmt]
-    return (torch.empty((rows, (K + 31) // 32 * 16), dtype=torch.uint8, device=device),
-            torch.empty(((rows + 127) // 128, ((K + blk - 1) // blk + 3) // 4, 512), dtype=torch.uint8,
-                        device=device))
+    torch = _torch_module
+    c, s = _packed_shapes(rows, K, fmt)
+    return torch.empty(c, dtype=torch.uint8, device=device), torch.empty(s, dtype=torch.uint8, device=device)
 
 
 def _one_f32(t, name, fmt, device):
@@ -556,20 +580,19 @@ def _one_f32(t, name, fmt, device):
         return None
     if fmt == "mx":
         raise ValueError(f"{name}: format 'mx' has no tensor scale")
-    torch = _torch()
     _on(t, name, device)
-    if t.dtype is not torch.float32 or t.numel() != 1:
+    if t.dtype is not _torch_module.float32 or t.numel() != 1:
         raise TypeError(f"{name} must be one float32")
     return t.data_ptr()
 
 
-def _vector(t, name, n, dtypes, device):
+def _vector(t, name, n, dtype, device):
     """Address of a contiguous vector of n values, or None."""
     if t is None:
         return None
     _on(t, name, device)
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must hold {n} contiguous values")
     return t.data_ptr()
@@ -577,71 +600,84 @@ def _vector(t, name, n, dtypes, device):
 
 def _scratch(ws, need, device, stream):
     """The caller's workspace, or a new one that stays alive for `stream`."""
-    torch = _torch()
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+        ws = _torch_module.empty(need if need > 256 else 256, dtype=_torch_module.uint8, device=device)
         if stream is not None:
             ws.record_stream(stream)
     else:
         _on(ws, "ws", device)
-    return ws, ws.numel() * ws.element_size()
+        need = ws.numel() * ws.element_size()
+    return ws, need
 
 
 def _weights(gamma, beta, D, xdtype, device):
-    """Addresses of gamma and beta and the id of their common type."""
-    torch = _torch()
-    either = (xdtype, torch.float32)
-    g = _vector(gamma, "gamma", D, either, device)
-    b = _vector(beta, "beta", D, either, device)
-    if gamma is not None and beta is not None and gamma.dtype is not beta.dtype:
-        raise TypeError("gamma and beta must have the same type")
+    """Addresses of gamma and beta and the id of their common type (that of X, or fp32)."""
     w = gamma if gamma is not None else beta
-    return g, b, _dtype_id(xdtype if w is None else w.dtype, "gamma")
+    if w is None:
+        return None, None, _dtype_id(xdtype, "X")
+    _on(w, "gamma", device)
+    wdtype = w.dtype
+    if wdtype is not xdtype and wdtype is not _torch_module.float32:
+        raise TypeError(f"gamma and beta must be {xdtype} or float32, got {wdtype}")
+    if gamma is not None and beta is not None and beta.dtype is not wdtype:
+        raise TypeError("gamma and beta must have the same type")
+    return (_vector(gamma, "gamma", D, wdtype, device), _vector(beta, "beta", D, wdtype, device),
+            _dtype_id(wdtype, "gamma"))
 
 
 def fp4_tensor_scale(X, out=None, ws=None, stream=None):
     """The "nv" tensor scale of X: max(|x|) / 2688 over its finite values, one fp32 on the device."""
     torch = _torch()
     ld = _matrix(X, "X")
+    dev = X.device
     dt = _dtype_id(X.dtype, "X")
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=X.device)
-    ptr = _one_f32(out, "out", "nv", X.device)
-    ws, wsb = _scratch(ws, 4096, X.device, stream)
-    _check("fp4_tensor_scale", lib().fp4_tensor_scale(dt, X.shape[0], X.shape[1], X.data_ptr(), ld, ptr,
-                                                      ws.data_ptr(), wsb, _stream(stream)))
+        out = torch.empty(1, dtype=torch.float32, device=dev)
+    ptr = _one_f32(out, "out", "nv", dev)
+    ws, wsb = _scratch(ws, 4096, dev, stream)
+    M, K = X.shape
+    _check("fp4_tensor_scale", lib().fp4_tensor_scale(dt, M, K, X.data_ptr(), ld, ptr, ws.data_ptr(), wsb,
+                                                      _raw_stream(stream, dev)))
     return out
 
 
 def fp4_quantize(X, fmt: str = "nv", scale=None, out=None, stream=None):
     """X (M x K) -> (codes, scales), blocks along its rows; scale: the "nv" tensor scale (None = 1)."""
+    _torch()
     f = _fmt_id(fmt)
     ld = _matrix(X, "X")
+    dev = X.device
+    dt = _dtype_id(X.dtype, "X")
     M, K = X.shape
     if out is None:
-        out = _new_packed(M, K, fmt, X.device)
-    Xq, Xs = out
-    if _packed(Xq, Xs, "out", fmt, K, X.device) != M:
-        raise ValueError(f"out must have {M} rows")
+        Xq, Xs = _new_packed(M, K, fmt, dev)
+    else:
+        Xq, Xs = out
+        if _packed(Xq, Xs, "out", fmt, K, dev) != M:
+            raise ValueError(f"out must have {M} rows")
     _check("fp4_quantize", lib().fp4_quantize(
-        f, _dtype_id(X.dtype, "X"), M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, X.device),
-        Xq.data_ptr(), Xs.data_ptr(), _stream(stream)))
+        f, dt, M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, dev), Xq.data_ptr(), Xs.data_ptr(),
+        _raw_stream(stream, dev)))
     return Xq, Xs
 
 
 def fp4_quantize_both(X, fmt: str = "nv", scale=None, out=None, stream=None):
     """X (M x K) -> (codes, scales) of X and (codes, scales) of its transpose, reading X once."""
+    _torch()
     f = _fmt_id(fmt)
     ld = _matrix(X, "X")
+    dev = X.device
+    dt = _dtype_id(X.dtype, "X")
     M, K = X.shape
     if out is None:
-        out = _new_packed(M, K, fmt, X.device) + _new_packed(K, M, fmt, X.device)
-    Xq, Xs, Tq, Ts = out
-    if (_packed(Xq, Xs, "out", fmt, K, X.device) != M or _packed(Tq, Ts, "transposed out", fmt, M, X.device) != K):
+        out = _new_packed(M, K, fmt, dev) + _new_packed(K, M, fmt, dev)
+    elif (_packed(out[0], out[1], "out", fmt, K, dev) != M
+          or _packed(out[2], out[3], "transposed out", fmt, M, dev) != K):
         raise ValueError(f"out must have {M} rows, and {K} transposed")
+    Xq, Xs, Tq, Ts = out
     _check("fp4_quantize_both", lib().fp4_quantize_both(
-        f, _dtype_id(X.dtype, "X"), M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, X.device),
-        Xq.data_ptr(), Xs.data_ptr(), Tq.data_ptr(), Ts.data_ptr(), _stream(stream)))
+        f, dt, M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, dev), Xq.data_ptr(), Xs.data_ptr(),
+        Tq.data_ptr(), Ts.data_ptr(), _raw_stream(stream, dev)))
     return Xq, Xs, Tq, Ts
 
 
@@ -650,12 +686,15 @@ def fp4_dequantize(Xq, Xs, K: int, fmt: str = "nv", scale=None, dtype=None, Y=No
     torch = _torch()
     f = _fmt_id(fmt)
     M = _packed(Xq, Xs, "X", fmt, K)
+    dev = Xq.device
     if Y is None:
-        Y = torch.empty((M, K), dtype=dtype or torch.float32, device=Xq.device)
-    ld = _matrix(Y, "Y", Xq.device, dtype, (M, K))
+        Y = torch.empty((M, K), dtype=dtype or torch.float32, device=dev)
+        ld = K
+    else:
+        ld = _matrix(Y, "Y", dev, dtype, M, K)
     _check("fp4_dequantize", lib().fp4_dequantize(
-        f, _dtype_id(Y.dtype, "Y"), M, K, Xq.data_ptr(), Xs.data_ptr(), _one_f32(scale, "scale", fmt, Xq.device),
-        Y.data_ptr(), ld, _stream(stream)))
+        f, _dtype_id(Y.dtype, "Y"), M, K, Xq.data_ptr(), Xs.data_ptr(), _one_f32(scale, "scale", fmt, dev),
+        Y.data_ptr(), ld, _raw_stream(stream, dev)))
     return Y
 
 
@@ -665,15 +704,21 @@ def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None
     torch = _torch()
     f = _fmt_id(fmt)
     M = _packed(Aq, As, "A", fmt, K)
-    N = _packed(Bq, Bs, "B", fmt, K, Aq.device)
+    dev = Aq.device
+    N = _packed(Bq, Bs, "B", fmt, K, dev)
     if Y is None:
-        Y = torch.empty((M, N), dtype=dtype or torch.bfloat16, device=Aq.device)
-    ld = _matrix(Y, "Y", Aq.device, dtype, (M, N))
+        dtype = dtype or torch.bfloat16
+        dt = _dtype_id(dtype, "Y")
+        Y = torch.empty((M, N), dtype=dtype, device=dev)
+        ld = N
+    else:
+        ld = _matrix(Y, "Y", dev, dtype, M, N)
+        dtype = Y.dtype
+        dt = _dtype_id(dtype, "Y")
     _check("fp4_gemm", lib().fp4_gemm(
-        f, _dtype_id(Y.dtype, "Y"), M, N, K, Aq.data_ptr(), As.data_ptr(),
-        _one_f32(a_scale, "a_scale", fmt, Aq.device), Bq.data_ptr(), Bs.data_ptr(),
-        _one_f32(b_scale, "b_scale", fmt, Aq.device), _vector(bias, "bias", N, (Y.dtype,), Aq.device),
-        Y.data_ptr(), ld, _stream(stream)))
+        f, dt, M, N, K, Aq.data_ptr(), As.data_ptr(), _one_f32(a_scale, "a_scale", fmt, dev), Bq.data_ptr(),
+        Bs.data_ptr(), _one_f32(b_scale, "b_scale", fmt, dev), _vector(bias, "bias", N, dtype, dev), Y.data_ptr(),
+        ld, _raw_stream(stream, dev)))
     return Y
 
 
@@ -683,17 +728,21 @@ def fp4_linear(X, Wq, Ws, fmt: str = "nv", x_scale=None, w_scale=None, bias=None
     f = _fmt_id(fmt)
     ldx = _matrix(X, "X")
     dev = X.device
-    dt = _dtype_id(X.dtype, "X")
+    dtype = X.dtype
+    dt = _dtype_id(dtype, "X")
     M, K = X.shape
     N = _packed(Wq, Ws, "W", fmt, K, dev)
     if Y is None:
-        Y = torch.empty((M, N), dtype=X.dtype, device=dev)
-    ldy = _matrix(Y, "Y", dev, X.dtype, (M, N))
-    ws, wsb = _scratch(ws, workspace_size(QG_OP_FP4_LINEAR, M, N, K), dev, stream)
-    _check("fp4_linear", lib().fp4_linear(
+        Y = torch.empty((M, N), dtype=dtype, device=dev)
+        ldy = N
+    else:
+        ldy = _matrix(Y, "Y", dev, dtype, M, N)
+    L = lib()
+    ws, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K), dev, stream)
+    _check("fp4_linear", L.fp4_linear(
         f, dt, M, N, K, X.data_ptr(), ldx, _one_f32(x_scale, "x_scale", fmt, dev), Wq.data_ptr(), Ws.data_ptr(),
-        _one_f32(w_scale, "w_scale", fmt, dev), _vector(bias, "bias", N, (X.dtype,), dev), Y.data_ptr(), ldy,
-        ws.data_ptr(), wsb, _stream(stream)))
+        _one_f32(w_scale, "w_scale", fmt, dev), _vector(bias, "bias", N, dtype, dev), Y.data_ptr(), ldy,
+        ws.data_ptr(), wsb, _raw_stream(stream, dev)))
     return Y
 
 
@@ -714,7 +763,7 @@ def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale
     M, N = dY.shape
     _on(X, "X", dev)
     K = X.shape[-1]
-    ldx = _matrix(X, "X", dev, dtype, (M, K))
+    ldx = _matrix(X, "X", dev, dtype, M, K)
     if _packed(Wtq, Wts, "W^T", fmt, N, dev) != K:
         raise ValueError(f"W^T must have {K} rows")
     if out is None:
@@ -722,58 +771,72 @@ def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale
                torch.empty((N, K), dtype=dtype, device=dev) if need_dw else None,
                torch.empty(N, dtype=torch.float32, device=dev) if need_db else None)
     dX, dW, db = out
-    lddx = 0 if dX is None else _matrix(dX, "dX", dev, dtype, (M, K))
-    lddw = 0 if dW is None else _matrix(dW, "dW", dev, dtype, (N, K))
+    lddx = 0 if dX is None else _matrix(dX, "dX", dev, dtype, M, K)
+    lddw = 0 if dW is None else _matrix(dW, "dW", dev, dtype, N, K)
     if dX is None and dW is None and db is None:
         return out
-    ws, wsb = _scratch(ws, workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K), dev, stream)
-    _check("fp4_linear_backward", lib().fp4_linear_backward(
+    L = lib()
+    ws, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K), dev, stream)
+    _check("fp4_linear_backward", L.fp4_linear_backward(
         f, dt, M, N, K, dY.data_ptr(), lddy, _one_f32(dy_scale, "dy_scale", fmt, dev), X.data_ptr(), ldx,
         _one_f32(x_scale, "x_scale", fmt, dev), Wtq.data_ptr(), Wts.data_ptr(),
         _one_f32(w_scale, "w_scale", fmt, dev), None if dX is None else dX.data_ptr(), lddx,
-        None if dW is None else dW.data_ptr(), lddw, _vector(db, "db", N, (torch.float32,), dev),
-        ws.data_ptr(), wsb, _stream(stream)))
+        None if dW is None else dW.data_ptr(), lddw, _vector(db, "db", N, torch.float32, dev),
+        ws.data_ptr(), wsb, _raw_stream(stream, dev)))
     return out
+
+
+def _stats(stats, M, device):
+    """mean and rstd: the caller's (checked) or new ones."""
+    torch = _torch_module
+    f32 = torch.float32
+    if stats is None:
+        return torch.empty(M, dtype=f32, device=device), torch.empty(M, dtype=f32, device=device)
+    mean, rstd = stats
+    _vector(mean, "mean", M, f32, device)
+    _vector(rstd, "rstd", M, f32, device)
+    return mean, rstd
 
 
 def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, Y=None, stats=None, stream=None):
     """(Y, mean, rstd) of the rows of X (M x D); gamma and beta in X's type or fp32 (None = 1, 0)."""
     torch = _torch()
     ldx = _matrix(X, "X")
-    dev = X.device
+    dev, dtype = X.device, X.dtype
+    dt = _dtype_id(dtype, "X")
     M, D = X.shape
-    g, b, wd = _weights(gamma, beta, D, X.dtype, dev)
+    g, b, wd = _weights(gamma, beta, D, dtype, dev)
     if Y is None:
-        Y = torch.empty((M, D), dtype=X.dtype, device=dev)
-    ldy = _matrix(Y, "Y", dev, X.dtype, (M, D))
-    mean, rstd = stats if stats is not None else torch.empty((2, M), dtype=torch.float32, device=dev).unbind(0)
-    f32 = (torch.float32,)
-    _check("layer_norm", lib().layer_norm(
-        _dtype_id(X.dtype, "X"), M, D, X.data_ptr(), ldx, g, b, wd, eps, Y.data_ptr(), ldy,
-        _vector(mean, "mean", M, f32, dev), _vector(rstd, "rstd", M, f32, dev), _stream(stream)))
+        Y = torch.empty((M, D), dtype=dtype, device=dev)
+        ldy = D
+    else:
+        ldy = _matrix(Y, "Y", dev, dtype, M, D)
+    mean, rstd = _stats(stats, M, dev)
+    _check("layer_norm", lib().layer_norm(dt, M, D, X.data_ptr(), ldx, g, b, wd, eps, Y.data_ptr(), ldy,
+                                          mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev)))
     return Y, mean, rstd
 
 
 def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv", scale=None, out=None, stats=None,
                    stream=None):
     """(codes, scales, mean, rstd): layer_norm of X with y quantized instead of stored."""
-    torch = _torch()
+    _torch()
     f = _fmt_id(fmt)
     ldx = _matrix(X, "X")
-    dev = X.device
+    dev, dtype = X.device, X.dtype
+    dt = _dtype_id(dtype, "X")
     M, D = X.shape
-    g, b, wd = _weights(gamma, beta, D, X.dtype, dev)
+    g, b, wd = _weights(gamma, beta, D, dtype, dev)
     if out is None:
-        out = _new_packed(M, D, fmt, dev)
-    Xq, Xs = out
-    if _packed(Xq, Xs, "out", fmt, D, dev) != M:
-        raise ValueError(f"out must have {M} rows")
-    mean, rstd = stats if stats is not None else torch.empty((2, M), dtype=torch.float32, device=dev).unbind(0)
-    f32 = (torch.float32,)
+        Xq, Xs = _new_packed(M, D, fmt, dev)
+    else:
+        Xq, Xs = out
+        if _packed(Xq, Xs, "out", fmt, D, dev) != M:
+            raise ValueError(f"out must have {M} rows")
+    mean, rstd = _stats(stats, M, dev)
     _check("layer_norm_fp4", lib().layer_norm_fp4(
-        f, _dtype_id(X.dtype, "X"), M, D, X.data_ptr(), ldx, g, b, wd, eps, _one_f32(scale, "scale", fmt, dev),
-        Xq.data_ptr(), Xs.data_ptr(), _vector(mean, "mean", M, f32, dev), _vector(rstd, "rstd", M, f32, dev),
-        _stream(stream)))
+        f, dt, M, D, X.data_ptr(), ldx, g, b, wd, eps, _one_f32(scale, "scale", fmt, dev), Xq.data_ptr(),
+        Xs.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev)))
     return Xq, Xs, mean, rstd
 
 
@@ -781,20 +844,22 @@ def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None
     """(dX, dgamma, dbeta) of layer_norm, with the mean and rstd it returned; dgamma and dbeta are fp32."""
     torch = _torch()
     ldx = _matrix(X, "X")
-    dev = X.device
+    dev, dtype, f32 = X.device, X.dtype, torch.float32
+    dt = _dtype_id(dtype, "X")
     M, D = X.shape
-    lddy = _matrix(dY, "dY", dev, X.dtype, (M, D))
-    g, _, wd = _weights(gamma, None, D, X.dtype, dev)
+    lddy = _matrix(dY, "dY", dev, dtype, M, D)
+    g, _, wd = _weights(gamma, None, D, dtype, dev)
     if out is None:
-        dgb = torch.empty((2, D), dtype=torch.float32, device=dev)
-        out = (torch.empty((M, D), dtype=X.dtype, device=dev), dgb[0], dgb[1])
-    dX, dgamma, dbeta = out
-    lddx = _matrix(dX, "dX", dev, X.dtype, (M, D))
-    f32 = (torch.float32,)
-    ws, wsb = _scratch(ws, workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D), dev, stream)
-    _check("layer_norm_backward", lib().layer_norm_backward(
-        _dtype_id(X.dtype, "X"), M, D, dY.data_ptr(), lddy, X.data_ptr(), ldx, g, wd,
-        _vector(mean, "mean", M, f32, dev), _vector(rstd, "rstd", M, f32, dev), dX.data_ptr(), lddx,
-        _vector(dgamma, "dgamma", D, f32, dev), _vector(dbeta, "dbeta", D, f32, dev), ws.data_ptr(), wsb,
-        _stream(stream)))
-    return out
+        dX = torch.empty((M, D), dtype=dtype, device=dev)
+        dgamma, dbeta = torch.empty(D, dtype=f32, device=dev), torch.empty(D, dtype=f32, device=dev)
+        lddx = D
+    else:
+        dX, dgamma, dbeta = out
+        lddx = _matrix(dX, "dX", dev, dtype, M, D)
+    L = lib()
+    ws, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D), dev, stream)
+    _check("layer_norm_backward", L.layer_norm_backward(
+        dt, M, D, dY.data_ptr(), lddy, X.data_ptr(), ldx, g, wd, _vector(mean, "mean", M, f32, dev),
+        _vector(rstd, "rstd", M, f32, dev), dX.data_ptr(), lddx, _vector(dgamma, "dgamma", D, f32, dev),
+        _vector(dbeta, "dbeta", D, f32, dev), ws.data_ptr(), wsb, _raw_stream(stream, dev)))
+    return dX, dgamma, dbeta

@@ -1,0 +1,309 @@
+// The same product on CTA pairs, for problems with many tokens: 256 x 256
+// tiles, persistent.  Two CTAs of a cluster share a tile; CTA r holds 128 rows
+// of the tokens and 128 rows of the weights, and the leader's cta_group::2 MMA
+// reads both halves, so each SM loads half as many weights per product as with
+// a tile of its own.  Each CTA also holds the scales of its own 128 token rows
+// and of all 256 weight rows, since its half of the accumulator needs them all.
+//
+// Tensor memory (512 columns) cannot hold two 256-column accumulators and the
+// scales.  The two accumulators therefore overlap by 48 columns:
+//   [0, 256) accumulator 0, [208, 464) accumulator 1, [464, 512) scales.
+// The epilogue drains the shared columns of a tile first and then lets the
+// MMAs of the next tile go, which write the other accumulator.  That costs the
+// tensor cores the time to drain 48 columns a tile instead of 256.
+#pragma once
+#include "fp4_gemm.cuh"
+#include "tc_gemm.cuh"
+
+namespace qg {
+
+template <int FMT>
+__device__ __forceinline__ void fp4_mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    if constexpr (FMT == kNv)
+        asm volatile(
+            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
+                d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+// In both CTAs of the pair, each from its own shared memory.
+__device__ __forceinline__ void fp4_copy_scales_pair(uint32_t tmem, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+}
+
+template <int FMT_>
+struct Fp4PairCfg {
+    static constexpr int FMT = FMT_;
+    static constexpr int ATOMS = FMT == kNv ? 4 : 2;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
+    static constexpr int S_BYTES = ATOMS * 512;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 3 * S_BYTES;
+    static constexpr int BARRIER_BYTES = 256;
+    static constexpr int STAGES = (232448 - BARRIER_BYTES - 1024) / STAGE_BYTES;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BARRIER_BYTES + 1024;
+    static constexpr int ACC_STEP = 208;              // first column of accumulator 1
+    static constexpr int SHARED_COLS = 256 - ACC_STEP;
+    static constexpr int SFA_COL = ACC_STEP + 256, SFB_COL = SFA_COL + 4 * ATOMS;
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int THREADS = 32 * (2 + EPI_WARPS);
+    static_assert(SFB_COL + 8 * ATOMS <= 512, "tensor memory");
+    static_assert(STAGES >= 4 && SMEM_BYTES <= 232448 && 2 * SMEM_BYTES > 233472, "shared memory, one CTA per SM");
+    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms of 1 KB");
+};
+
+constexpr int kSiteFp4PairEmpty = 311;
+constexpr int kSiteFp4PairAcc = 312;
+constexpr int kSiteFp4PairFull = 313;
+constexpr int kSiteFp4PairEpi = 314;
+constexpr int kSiteFp4PairDrainTma = 315;
+constexpr int kSiteFp4PairDrainMma = 316;
+
+// 16 values of a row to Y, whole 32-byte sectors where alignment allows.
+template <class T>
+__device__ __forceinline__ void fp4_store16(T* dst, int left, const float (&f)[16]) {
+    if (left >= 16 && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
+        if constexpr (sizeof(T) == 2) {
+            uint4 a = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
+            uint4 b = make_uint4(pack2<T>(f[8], f[9]), pack2<T>(f[10], f[11]), pack2<T>(f[12], f[13]),
+                                 pack2<T>(f[14], f[15]));
+            st_global_32(dst, a, b, false);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 16; h += 8)
+                st_global_32(dst + h,
+                             make_uint4(__float_as_uint(f[h]), __float_as_uint(f[h + 1]), __float_as_uint(f[h + 2]),
+                                        __float_as_uint(f[h + 3])),
+                             make_uint4(__float_as_uint(f[h + 4]), __float_as_uint(f[h + 5]),
+                                        __float_as_uint(f[h + 6]), __float_as_uint(f[h + 7])),
+                             false);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            if (i < left) dst[i] = from_f32<T>(f[i]);
+    }
+}
+
+template <class Cfg>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
+    fp4_gemm2_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+                     const __grid_constant__ CUtensorMap tmSX, const __grid_constant__ CUtensorMap tmSW,
+                     const Fp4Params p) {
+    constexpr int STAGES = Cfg::STAGES, FMT = Cfg::FMT, ATOMS = Cfg::ATOMS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    // per stage: token codes | weight codes | token scales | weight scales (two blocks of 128 rows)
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * Cfg::STAGE_BYTES);
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+    auto accf_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+    const uint32_t next_bar = bar0 + 8u * (2 * STAGES + 2);  // leader: the next tile's MMAs may start
+    const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 3);
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    auto stage_smem = [&](int s) { return smem_u32(smem + s * Cfg::STAGE_BYTES); };
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(accf_bar(0), 1);
+        mbar_init(accf_bar(1), 1);
+        mbar_init(next_bar, 2 * Cfg::EPI_WARPS);
+        mbar_init(drain_bar, 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmSX);
+        tma_prefetch_desc(&tmSW);
+    }
+    if (warp == 1) tmem_alloc_pair(smem_u32(tmem_holder), 512);
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+    const int num_m = (p.M + 255) / 256, num_n = (p.N + 255) / 256;
+    const int ntiles = num_m * num_n;
+    const int num_kb = (p.K + kFp4Bk - 1) / kFp4Bk;
+    const int col_tiles = static_cast<int>(fp4_col_tiles(FMT, p.K));
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer (both CTAs)
+            Ring<STAGES> ps;
+            uint32_t armed = 0, armed_phase = 0;
+            const uint64_t keep = l2_policy_evict_normal();
+            bool ok = true;
+            for (int t = pair; ok && t < ntiles; t += npairs) {
+                int mb, nb;
+                tile_coords(t, num_m, num_n, mb, nb, kGroupMPairs);
+                const int arow = mb * 256 + static_cast<int>(rank) * 128;
+                const int brow = nb * 256 + static_cast<int>(rank) * 128;
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!bounded_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl, kSiteFp4PairEmpty)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full = mapa_shared(full_bar(ps.slot()), 0);
+                    if (leader) {
+                        mbar_arrive_expect_tx(full_bar(ps.slot()), 2 * Cfg::STAGE_BYTES);
+                        armed |= 1u << ps.slot();
+                        armed_phase = (armed_phase & ~(1u << ps.slot())) | (ps.parity() << ps.slot());
+                    }
+                    const uint32_t a = stage_smem(ps.slot()), b = a + Cfg::A_BYTES;
+                    const uint32_t sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
+                    tma_load_2d_pair(a, &tmX, kb * (kFp4Bk / 2), arow, full, keep);
+                    tma_load_2d_pair(b, &tmW, kb * (kFp4Bk / 2), brow, full, keep);
+                    // rows of scale tiles past the operand read as 0
+                    tma_load_2d_pair(sa, &tmSX, 0, (arow >> 7) * col_tiles + kb * ATOMS, full, keep);
+                    tma_load_2d_pair(sb, &tmSW, 0, (nb * 2) * col_tiles + kb * ATOMS, full, keep);
+                    tma_load_2d_pair(sb + Cfg::S_BYTES, &tmSW, 0, (nb * 2 + 1) * col_tiles + kb * ATOMS, full, keep);
+                    ps.next();
+                }
+            }
+            if (!ok) {
+                if (leader) {
+                    for (int s = 0; s < STAGES; ++s)
+                        if (armed & (1u << s))
+                            bounded_wait(full_bar(s), (armed_phase >> s) & 1u, nullptr, p.ctl, kSiteFp4PairDrainTma);
+                } else {
+                    // the leader's barrier cannot be polled from here: a fixed time to land
+                    const uint64_t t0 = global_timer_ns();
+                    while (global_timer_ns() - t0 < 1000000) {
+                    }
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ------------------------------------------------ MMA issuer (leader)
+            Ring<STAGES> ps;
+            int n = 0;  // tiles begun
+            bool ok = true;
+            for (int t = pair; ok && t < ntiles; t += npairs, ++n) {
+                // tile n - 1 has handed over the shared columns, and with it all of tile n - 2
+                if (n > 0 && !bounded_wait(next_bar, (n - 1) & 1u, abort_flag, p.ctl, kSiteFp4PairAcc)) break;
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>((n & 1) * Cfg::ACC_STEP);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!bounded_wait(full_bar(ps.slot()), ps.parity(), abort_flag, p.ctl, kSiteFp4PairFull)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = stage_smem(ps.slot()), b = a + Cfg::A_BYTES;
+                    const uint32_t sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
+                    const int steps = min(4, (p.K - kb * kFp4Bk + 63) / 64);  // none behind K
+                    const int atoms = FMT == kNv ? steps : (steps + 1) / 2;
+#pragma unroll
+                    for (int j = 0; j < ATOMS; ++j) {
+                        if (j >= atoms) break;
+                        fp4_copy_scales_pair(tmem + Cfg::SFA_COL + 4 * j, fp4_scale_desc(sa + 512 * j));
+                        fp4_copy_scales_pair(tmem + Cfg::SFB_COL + 8 * j, fp4_scale_desc(sb + 512 * j));
+                        fp4_copy_scales_pair(tmem + Cfg::SFB_COL + 8 * j + 4,
+                                             fp4_scale_desc(sb + Cfg::S_BYTES + 512 * j));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (j >= steps) break;
+                        const uint32_t atom = FMT == kNv ? j : j >> 1;
+                        const uint32_t id = FMT == kNv ? 0u : 2u * (j & 1);
+                        fp4_mma_pair<FMT>(d, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
+                                          fp4_idesc<FMT>(256, 256, id), tmem + Cfg::SFA_COL + 4 * atom,
+                                          tmem + Cfg::SFB_COL + 8 * atom, (kb > 0 || j > 0) ? 1u : 0u);
+                    }
+                    tc_commit_pair(empty_bar(ps.slot()), 0x3);
+                    ps.next();
+                }
+                if (!ok) break;
+                tc_commit_pair(accf_bar(n & 1), 0x3);
+            }
+            tc_commit_pair(drain_bar, 0x1);
+            bounded_wait(drain_bar, 0u, nullptr, p.ctl, kSiteFp4PairDrainMma);
+        }
+    } else {
+        // ---------------------------------------------------- epilogue (both CTAs)
+        const int quad = warp & 3, half = (warp - 2) >> 2;
+        const float alpha = fp4_alpha(p);
+        const uint32_t next = mapa_shared(next_bar, 0);
+        int n = 0;
+        for (int t = pair; t < ntiles; t += npairs, ++n) {
+            int mb, nb;
+            tile_coords(t, num_m, num_n, mb, nb, kGroupMPairs);
+            const int row = mb * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+            const bool got = bounded_wait(accf_bar(n & 1), (n >> 1) & 1u, abort_flag, p.ctl, kSiteFp4PairEpi);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
+                                   static_cast<uint32_t>((n & 1) * Cfg::ACC_STEP);
+            // accumulator 0 shares its last 48 columns, accumulator 1 its first 48:
+            // the half that holds them starts there
+            const bool sharing = half == ((n & 1) ? 0 : 1);
+            auto release = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster_relaxed(next);
+            };
+            if (!sharing) release();
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+                // 16 columns a step; half 1 goes down from the top
+                const int c = half ? 240 - 16 * i : 16 * i;
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(taddr + c, r);
+                tmem_wait_ld();
+                if (sharing && i == Cfg::SHARED_COLS / 16 - 1) release();
+                const int col = nb * 256 + c;
+                if (row >= p.M || col >= p.N) continue;
+                float f[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha;
+                if (p.bias) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        if (col + j < p.N) f[j] += typed_at(p.bias, p.dtype, col + j);
+                }
+                const int64_t at = row * p.ldy + col;
+                if (p.dtype == QG_F16)
+                    fp4_store16(static_cast<__half*>(p.Y) + at, p.N - col, f);
+                else if (p.dtype == QG_BF16)
+                    fp4_store16(static_cast<__nv_bfloat16*>(p.Y) + at, p.N - col, f);
+                else
+                    fp4_store16(static_cast<float*>(p.Y) + at, p.N - col, f);
+            }
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves while its partner may still use it
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+}  // namespace qg

@@ -1,9 +1,10 @@
 // Products of microscaled 4-bit operands: fp4_gemm (both packed), fp4_linear
 // (activations quantized in the call) and fp4_linear_backward (gradients of
-// the activations, the weights and the bias).  Kernels: fp4_gemm.cuh.
+// the activations, the weights and the bias).  Kernels: fp4_gemm.cuh
+// (one CTA a tile) and fp4_gemm2.cuh (CTA pairs).
 #include <mutex>
 
-#include "fp4_gemm.cuh"
+#include "fp4_gemm2.cuh"
 
 namespace qg {
 
@@ -13,17 +14,17 @@ struct Fp4Operand {
     const float* ts;
 };
 
-// Lifts the kernel's dynamic shared-memory limit, once per device.
-template <class Cfg>
-static int raise_smem() {
+// Lifts the kernel's dynamic shared-memory limit, once per device.  Cfg keeps
+// the flags of different kernels apart.
+template <class Cfg, class F>
+static int raise_smem(F* kernel) {
     static std::mutex mu;
     static bool done[64] = {};
     const int dev = current_device();
     if (dev < 0 || dev >= 64) return QG_ERR_CUDA;
     std::lock_guard<std::mutex> g(mu);
     if (done[dev]) return QG_OK;
-    const cudaError_t e = cudaFuncSetAttribute(fp4_gemm_kernel<Cfg>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               Cfg::SMEM_BYTES);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
     if (e != cudaSuccess) return map_cuda(e);
     done[dev] = true;
     return QG_OK;
@@ -47,13 +48,29 @@ static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params&
     if (!rc) rc = codes_map(&tx, x, p.K, Cfg::NT);
     if (!rc) rc = scales_map(&tsw, w, Cfg::FMT, p.K, Cfg::ATOMS);
     if (!rc) rc = scales_map(&tsx, x, Cfg::FMT, p.K, Cfg::ATOMS);
-    if (!rc) rc = raise_smem<Cfg>();
+    if (!rc) rc = raise_smem<Cfg>(fp4_gemm_kernel<Cfg>);
     if (rc) return rc;
     const int64_t gy = (p.N + 127) / 128, gz = (p.M + Cfg::NT - 1) / Cfg::NT;
     if (gy > 65535 || gz > 65535) return QG_ERR_UNSUPPORTED;
     return launch_serialized(fp4_gemm_kernel<Cfg>,
                              dim3(static_cast<unsigned>(splits), static_cast<unsigned>(gy), static_cast<unsigned>(gz)),
                              kFp4Threads, Cfg::SMEM_BYTES, splits, s, tw, tx, tsw, tsx, p);
+}
+
+template <class Cfg>
+static int launch_fp4_pair(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, int dev, cudaStream_t s) {
+    CUtensorMap tw, tx, tsw, tsx;
+    int rc = codes_map(&tw, w, p.K, 128);
+    if (!rc) rc = codes_map(&tx, x, p.K, 128);
+    if (!rc) rc = scales_map(&tsw, w, Cfg::FMT, p.K, Cfg::ATOMS);
+    if (!rc) rc = scales_map(&tsx, x, Cfg::FMT, p.K, Cfg::ATOMS);
+    if (!rc) rc = raise_smem<Cfg>(fp4_gemm2_kernel<Cfg>);
+    if (rc) return rc;
+    const int64_t tiles = (int64_t(p.M) + 255) / 256 * ((int64_t(p.N) + 255) / 256);
+    if (tiles > INT32_MAX) return QG_ERR_UNSUPPORTED;
+    const int64_t pairs = num_sms(dev) / 2;
+    return launch_serialized(fp4_gemm2_kernel<Cfg>, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))),
+                             Cfg::THREADS, Cfg::SMEM_BYTES, 1, s, tx, tw, tsx, tsw, p);
 }
 
 // Splits of K over a cluster: doubled while the tiles alone leave half of the
@@ -66,6 +83,7 @@ static int choose_splits(int64_t tiles, int64_t num_kb, int sms) {
 
 template <int FMT>
 static int run_fmt(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, int dev, cudaStream_t s) {
+    if (p.M > 128 && p.N > 128 && (p.M > 256 || p.N > 2048)) return launch_fp4_pair<Fp4PairCfg<FMT>>(x, w, p, dev, s);
     const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
     const int64_t tiles = (int64_t(p.N) + 127) / 128 * ((int64_t(p.M) + nt - 1) / nt);
     const int splits = choose_splits(tiles, (p.K + kFp4Bk - 1) / kFp4Bk, num_sms(dev));
@@ -143,6 +161,10 @@ QG_FP4_GEMM_BUDGET(kNv, "nv", 16); QG_FP4_GEMM_BUDGET(kNv, "nv", 32);
 QG_FP4_GEMM_BUDGET(kNv, "nv", 64); QG_FP4_GEMM_BUDGET(kNv, "nv", 128);
 QG_FP4_GEMM_BUDGET(kMx, "mx", 16); QG_FP4_GEMM_BUDGET(kMx, "mx", 32);
 QG_FP4_GEMM_BUDGET(kMx, "mx", 64); QG_FP4_GEMM_BUDGET(kMx, "mx", 128);
+QG_BLOCK_KERNEL_BUDGET("fp4_gemm2_kernel<nv>", reinterpret_cast<const void*>(fp4_gemm2_kernel<Fp4PairCfg<kNv>>),
+                       Fp4PairCfg<kNv>::THREADS, Fp4PairCfg<kNv>::SMEM_BYTES, 512, 2, 1);
+QG_BLOCK_KERNEL_BUDGET("fp4_gemm2_kernel<mx>", reinterpret_cast<const void*>(fp4_gemm2_kernel<Fp4PairCfg<kMx>>),
+                       Fp4PairCfg<kMx>::THREADS, Fp4PairCfg<kMx>::SMEM_BYTES, 512, 2, 1);
 QG_BLOCK_KERNEL_BUDGET("k_fp4_only_bias", reinterpret_cast<const void*>(k_fp4_only_bias), 256, 0, 0, 1, 4);
 
 // Checks shared by the three calls.
