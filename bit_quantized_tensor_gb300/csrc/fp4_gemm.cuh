@@ -24,29 +24,75 @@ __host__ __device__ constexpr uint32_t fp4_idesc(uint32_t m, uint32_t n, uint32_
            ((FMT == kMx ? 1u : 0u) << 23) | ((m >> 4) << 24) | (scale_id << 29);
 }
 
-template <int FMT>
+// The asynchronous instructions below are issued by whole warps with one
+// elected lane's predicate, and never inside a branch on the lane: in
+// convergent code the descriptors and addresses stay in uniform registers.
+// Issued from inside `if (lane == 0)` every operand is moved there one by one,
+// which was measured at 200 cycles an MMA and 52 a scale copy, whatever their
+// size; like this an MMA of 256 x 256 x 64 takes its 128 cycles and the copies
+// disappear behind it (12 copies and 4 MMAs: 534 cycles).
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
+}
+
+#define QG_FP4_MMA(GROUP, KIND)                                                                              \
+    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"                       \
+                 "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"( \
+                     d_tmem),                                                                                \
+                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected)       \
+                 : "memory")
+
+// PAIR: M = 256 across the two CTAs of a cluster, issued by the leader.
+template <int FMT, bool PAIR>
 __device__ __forceinline__ void fp4_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    if constexpr (FMT == kNv)
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-                d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t elected) {
+    if constexpr (FMT == kNv && !PAIR)
+        QG_FP4_MMA("1", "mxf4nvf4.block_scale.block16");
+    else if constexpr (FMT == kNv)
+        QG_FP4_MMA("2", "mxf4nvf4.block_scale.block16");
+    else if constexpr (!PAIR)
+        QG_FP4_MMA("1", "mxf4.block_scale.block32");
     else
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-                d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
+        QG_FP4_MMA("2", "mxf4.block_scale.block32");
 }
 
 // One 512-byte scale tile from shared memory into four columns of tensor
-// memory, repeated in each quarter of the lanes.
-__device__ __forceinline__ void fp4_copy_scales(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+// memory, repeated in each quarter of the lanes (PAIR: in both CTAs, each from
+// its own shared memory).
+template <bool PAIR>
+__device__ __forceinline__ void fp4_copy_scales(uint32_t tmem, uint64_t desc, uint32_t elected) {
+    if constexpr (PAIR)
+        asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(
+                         tmem),
+                     "l"(desc), "r"(elected)
+                     : "memory");
+    else
+        asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(
+                         tmem),
+                     "l"(desc), "r"(elected)
+                     : "memory");
+}
+
+// tma_load_2d and tma_load_2d_pair of an elected lane.
+__device__ __forceinline__ void fp4_load(uint32_t dst, const void* tmap, int32_t c0, int32_t c1, uint32_t bar,
+                                         uint32_t elected) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(bar), "r"(elected)
+        : "memory");
+}
+__device__ __forceinline__ void fp4_load_pair(uint32_t dst, const void* tmap, int32_t c0, int32_t c1,
+                                              uint32_t cluster_bar, uint32_t elected) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %5, 0;\n"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+        "[%1, {%2, %3}], [%4];\n}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(cluster_bar), "r"(elected)
+        : "memory");
 }
 
 // Shared-memory descriptor of a scale tile: 32 rows of 16 bytes, no swizzle,
@@ -169,78 +215,85 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);  // known to be uniform
 
     // The bounded waits below start only when the previous kernel is done (they
     // must not count its time); the producer alone may run ahead of that.
     if (warp != 4) pdl_wait_prior_grid();
     bool ok = true;
     if (warp == 4) {
-        if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_normal();
-            auto load_w = [&](int kb, int s) {
-                tma_load_2d(a_smem(s), &tmW, kb * (kFp4Bk / 2), n0, full_bar(s), keep);
-                tma_load_2d(a_smem(s) + Cfg::A_BYTES + Cfg::B_ALLOC, &tmSW, 0,
-                            static_cast<int>(blockIdx.y * fp4_col_tiles(FMT, p.K)) + kb * Cfg::ATOMS, full_bar(s),
-                            keep);
-            };
-            auto load_x = [&](int kb, int s) {
-                tma_load_2d(a_smem(s) + Cfg::A_BYTES, &tmX, kb * (kFp4Bk / 2), m0, full_bar(s), keep);
-                tma_load_2d(a_smem(s) + Cfg::A_BYTES + Cfg::B_ALLOC + Cfg::S_BYTES, &tmSX, 0,
-                            static_cast<int>((m0 >> 7) * fp4_col_tiles(FMT, p.K)) + kb * Cfg::ATOMS, full_bar(s),
-                            keep);
-            };
-            // Weights that were complete before the previous kernel began may
-            // be fetched while that kernel (which makes the tokens' codes) runs.
-            const int ahead = min(kb1 - kb0, STAGES);
-            if (!p.weights_ready) pdl_wait_prior_grid();
-            for (int i = 0; i < ahead; ++i) {
-                mbar_arrive_expect_tx(full_bar(i), Cfg::TX_BYTES);
-                load_w(kb0 + i, i);
-            }
-            if (p.weights_ready) pdl_wait_prior_grid();
-            for (int i = 0; i < ahead; ++i) load_x(kb0 + i, i);
-            Ring<STAGES> ps;
-            for (int i = 0; i < ahead; ++i) ps.next();
-            for (int kb = kb0 + ahead; kb < kb1; ++kb) {
-                if (!bounded_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl, kSiteFp4Empty)) break;
-                mbar_arrive_expect_tx(full_bar(ps.slot()), Cfg::TX_BYTES);
-                load_w(kb, ps.slot());
-                load_x(kb, ps.slot());
-                ps.next();
-            }
+        const uint32_t elected = elect_lane();
+        const int tiles_k = static_cast<int>(fp4_col_tiles(FMT, p.K));
+        auto arm = [&](int s) {
+            if (elected) mbar_arrive_expect_tx(full_bar(s), Cfg::TX_BYTES);
+            __syncwarp();
+        };
+        auto load_w = [&](int kb, int s) {
+            fp4_load(a_smem(s), &tmW, kb * (kFp4Bk / 2), n0, full_bar(s), elected);
+            fp4_load(a_smem(s) + Cfg::A_BYTES + Cfg::B_ALLOC, &tmSW, 0, (n0 >> 7) * tiles_k + kb * Cfg::ATOMS,
+                     full_bar(s), elected);
+        };
+        auto load_x = [&](int kb, int s) {
+            fp4_load(a_smem(s) + Cfg::A_BYTES, &tmX, kb * (kFp4Bk / 2), m0, full_bar(s), elected);
+            fp4_load(a_smem(s) + Cfg::A_BYTES + Cfg::B_ALLOC + Cfg::S_BYTES, &tmSX, 0,
+                     (m0 >> 7) * tiles_k + kb * Cfg::ATOMS, full_bar(s), elected);
+        };
+        // Weights that were complete before the previous kernel began may
+        // be fetched while that kernel (which makes the tokens' codes) runs.
+        const int ahead = min(kb1 - kb0, STAGES);
+        if (!p.weights_ready) pdl_wait_prior_grid();
+        for (int i = 0; i < ahead; ++i) {
+            arm(i);
+            load_w(kb0 + i, i);
         }
-        __syncwarp();
+        if (p.weights_ready) pdl_wait_prior_grid();
+        for (int i = 0; i < ahead; ++i) load_x(kb0 + i, i);
+        Ring<STAGES> ps;
+        for (int i = 0; i < ahead; ++i) ps.next();
+        for (int kb = kb0 + ahead; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu, bounded_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl,
+                                                      kSiteFp4Empty)))
+                break;
+            arm(ps.slot());
+            load_w(kb, ps.slot());
+            load_x(kb, ps.slot());
+            ps.next();
+        }
     } else if (warp == 5) {
-        if (lane == 0) {
-            Ring<STAGES> ps;
-            const uint32_t sfb_shift = static_cast<uint32_t>((m0 & 127) >> 5);  // tile inside its 128 scale rows
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!bounded_wait(full_bar(ps.slot()), ps.parity(), abort_flag, p.ctl, kSiteFp4Full)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const int steps = min(4, (p.K - kb * kFp4Bk + 63) / 64);  // none behind K: its scales may be stale
-                const uint32_t a = a_smem(ps.slot()), b = a + Cfg::A_BYTES;
-                const uint32_t sa = b + Cfg::B_ALLOC, sb = sa + Cfg::S_BYTES;
-                const int atoms = FMT == kNv ? steps : (steps + 1) / 2;
-                for (int j = 0; j < atoms; ++j) {
-                    fp4_copy_scales(tmem + Cfg::SFA_COL + 4 * j, fp4_scale_desc(sa + 512 * j));
-                    fp4_copy_scales(tmem + Cfg::SFB_COL + 4 * j, fp4_scale_desc(sb + 512 * j));
-                }
-                for (int j = 0; j < steps; ++j) {
-                    const uint32_t col = FMT == kNv ? 4u * j : 4u * (j >> 1);
-                    const uint32_t id = FMT == kNv ? 0u : 2u * (j & 1);
-                    fp4_mma<FMT>(tmem, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
-                                 fp4_idesc<FMT>(128, NT, id), tmem + Cfg::SFA_COL + col,
-                                 tmem + Cfg::SFB_COL + col + sfb_shift, (kb > kb0 || j > 0) ? 1u : 0u);
-                }
-                tc_commit(empty_bar(ps.slot()));
-                ps.next();
+        const uint32_t elected = elect_lane();
+        Ring<STAGES> ps;
+        const uint32_t sfb_shift = static_cast<uint32_t>((m0 & 127) >> 5);  // tile inside its 128 scale rows
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!__all_sync(0xffffffffu,
+                            bounded_wait(full_bar(ps.slot()), ps.parity(), abort_flag, p.ctl, kSiteFp4Full))) {
+                ok = false;
+                break;
             }
-            tc_commit(acc_bar);
+            tc_fence_after();
+            const int steps = min(4, (p.K - kb * kFp4Bk + 63) / 64);  // none behind K: its scales may be stale
+            const uint32_t a = a_smem(ps.slot()), b = a + Cfg::A_BYTES;
+            const uint32_t sa = b + Cfg::B_ALLOC, sb = sa + Cfg::S_BYTES;
+            const int atoms = FMT == kNv ? steps : (steps + 1) / 2;
+#pragma unroll
+            for (int j = 0; j < Cfg::ATOMS; ++j) {
+                if (j >= atoms) break;
+                fp4_copy_scales<false>(tmem + Cfg::SFA_COL + 4 * j, fp4_scale_desc(sa + 512 * j), elected);
+                fp4_copy_scales<false>(tmem + Cfg::SFB_COL + 4 * j, fp4_scale_desc(sb + 512 * j), elected);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (j >= steps) break;
+                const uint32_t col = FMT == kNv ? 4u * j : 4u * (j >> 1);
+                const uint32_t id = FMT == kNv ? 0u : 2u * (j & 1);
+                fp4_mma<FMT, false>(tmem, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
+                                    fp4_idesc<FMT>(128, NT, id), tmem + Cfg::SFA_COL + col,
+                                    tmem + Cfg::SFB_COL + col + sfb_shift, (kb > kb0 || j > 0) ? 1u : 0u, elected);
+            }
+            if (elected) tc_commit(empty_bar(ps.slot()));
+            __syncwarp();
+            ps.next();
         }
+        if (elected) tc_commit(acc_bar);
         __syncwarp();
     }
     if (warp == 4) pdl_wait_prior_grid();

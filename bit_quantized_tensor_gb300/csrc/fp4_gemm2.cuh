@@ -17,30 +17,6 @@
 
 namespace qg {
 
-template <int FMT>
-__device__ __forceinline__ void fp4_mma_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    if constexpr (FMT == kNv)
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::2.kind::mxf4nvf4.block_scale.block16 [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-                d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n.reg .pred p;\nsetp.ne.b32 p, %6, 0;\n"
-            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"(
-                d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-            : "memory");
-}
-
-// In both CTAs of the pair, each from its own shared memory.
-__device__ __forceinline__ void fp4_copy_scales_pair(uint32_t tmem, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
-}
-
 template <int FMT_>
 struct Fp4PairCfg {
     static constexpr int FMT = FMT_;
@@ -139,7 +115,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     tc_fence_before();
     cluster_sync();
     tc_fence_after();
-    const uint32_t tmem = *tmem_holder;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);  // known to be uniform
     pdl_wait_prior_grid();
     pdl_launch_dependents();
 
@@ -150,65 +126,70 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     const int col_tiles = static_cast<int>(fp4_col_tiles(FMT, p.K));
 
     if (warp == 0) {
-        if (lane == 0) {
-            // ------------------------------------------------ TMA producer (both CTAs)
-            Ring<STAGES> ps;
-            uint32_t armed = 0, armed_phase = 0;
-            const uint64_t keep = l2_policy_evict_normal();
-            bool ok = true;
-            for (int t = pair; ok && t < ntiles; t += npairs) {
-                int mb, nb;
-                tile_coords(t, num_m, num_n, mb, nb, kGroupMPairs);
-                const int arow = mb * 256 + static_cast<int>(rank) * 128;
-                const int brow = nb * 256 + static_cast<int>(rank) * 128;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!bounded_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl, kSiteFp4PairEmpty)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t full = mapa_shared(full_bar(ps.slot()), 0);
-                    if (leader) {
-                        mbar_arrive_expect_tx(full_bar(ps.slot()), 2 * Cfg::STAGE_BYTES);
-                        armed |= 1u << ps.slot();
-                        armed_phase = (armed_phase & ~(1u << ps.slot())) | (ps.parity() << ps.slot());
-                    }
-                    const uint32_t a = stage_smem(ps.slot()), b = a + Cfg::A_BYTES;
-                    const uint32_t sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
-                    tma_load_2d_pair(a, &tmX, kb * (kFp4Bk / 2), arow, full, keep);
-                    tma_load_2d_pair(b, &tmW, kb * (kFp4Bk / 2), brow, full, keep);
-                    // rows of scale tiles past the operand read as 0
-                    tma_load_2d_pair(sa, &tmSX, 0, (arow >> 7) * col_tiles + kb * ATOMS, full, keep);
-                    tma_load_2d_pair(sb, &tmSW, 0, (nb * 2) * col_tiles + kb * ATOMS, full, keep);
-                    tma_load_2d_pair(sb + Cfg::S_BYTES, &tmSW, 0, (nb * 2 + 1) * col_tiles + kb * ATOMS, full, keep);
-                    ps.next();
+        // ------------------------------------------------ TMA producer (both CTAs)
+        const uint32_t elected = elect_lane();
+        Ring<STAGES> ps;
+        uint32_t armed = 0, armed_phase = 0;
+        bool ok = true;
+        for (int t = pair; ok && t < ntiles; t += npairs) {
+            int mb, nb;
+            tile_coords(t, num_m, num_n, mb, nb, kGroupMPairs);
+            const int arow = mb * 256 + static_cast<int>(rank) * 128;
+            const int brow = nb * 256 + static_cast<int>(rank) * 128;
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!__all_sync(0xffffffffu, bounded_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl,
+                                                          kSiteFp4PairEmpty))) {
+                    ok = false;
+                    break;
                 }
-            }
-            if (!ok) {
+                const uint32_t full = mapa_shared(full_bar(ps.slot()), 0);
                 if (leader) {
-                    for (int s = 0; s < STAGES; ++s)
-                        if (armed & (1u << s))
-                            bounded_wait(full_bar(s), (armed_phase >> s) & 1u, nullptr, p.ctl, kSiteFp4PairDrainTma);
-                } else {
-                    // the leader's barrier cannot be polled from here: a fixed time to land
-                    const uint64_t t0 = global_timer_ns();
-                    while (global_timer_ns() - t0 < 1000000) {
-                    }
+                    if (elected) mbar_arrive_expect_tx(full_bar(ps.slot()), 2 * Cfg::STAGE_BYTES);
+                    __syncwarp();
+                    armed |= 1u << ps.slot();
+                    armed_phase = (armed_phase & ~(1u << ps.slot())) | (ps.parity() << ps.slot());
+                }
+                const uint32_t a = stage_smem(ps.slot()), b = a + Cfg::A_BYTES;
+                const uint32_t sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
+                fp4_load_pair(a, &tmX, kb * (kFp4Bk / 2), arow, full, elected);
+                fp4_load_pair(b, &tmW, kb * (kFp4Bk / 2), brow, full, elected);
+                // rows of scale tiles past the operand read as 0
+                fp4_load_pair(sa, &tmSX, 0, (arow >> 7) * col_tiles + kb * ATOMS, full, elected);
+                fp4_load_pair(sb, &tmSW, 0, (nb * 2) * col_tiles + kb * ATOMS, full, elected);
+                fp4_load_pair(sb + Cfg::S_BYTES, &tmSW, 0, (nb * 2 + 1) * col_tiles + kb * ATOMS, full, elected);
+                ps.next();
+            }
+        }
+        if (!ok) {
+            if (leader) {
+                for (int s = 0; s < STAGES; ++s)
+                    if (armed & (1u << s))
+                        bounded_wait(full_bar(s), (armed_phase >> s) & 1u, nullptr, p.ctl, kSiteFp4PairDrainTma);
+            } else {
+                // the leader's barrier cannot be polled from here: a fixed time to land
+                const uint64_t t0 = global_timer_ns();
+                while (global_timer_ns() - t0 < 1000000) {
                 }
             }
         }
+        __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
             // ------------------------------------------------ MMA issuer (leader)
+            const uint32_t elected = elect_lane();
             Ring<STAGES> ps;
             int n = 0;  // tiles begun
             bool ok = true;
             for (int t = pair; ok && t < ntiles; t += npairs, ++n) {
                 // tile n - 1 has handed over the shared columns, and with it all of tile n - 2
-                if (n > 0 && !bounded_wait(next_bar, (n - 1) & 1u, abort_flag, p.ctl, kSiteFp4PairAcc)) break;
+                if (n > 0 && !__all_sync(0xffffffffu, bounded_wait(next_bar, (n - 1) & 1u, abort_flag, p.ctl,
+                                                                   kSiteFp4PairAcc)))
+                    break;
                 tc_fence_after();
                 const uint32_t d = tmem + static_cast<uint32_t>((n & 1) * Cfg::ACC_STEP);
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    if (!bounded_wait(full_bar(ps.slot()), ps.parity(), abort_flag, p.ctl, kSiteFp4PairFull)) {
+                    if (!__all_sync(0xffffffffu, bounded_wait(full_bar(ps.slot()), ps.parity(), abort_flag, p.ctl,
+                                                              kSiteFp4PairFull))) {
                         ok = false;
                         break;
                     }
@@ -220,29 +201,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < ATOMS; ++j) {
                         if (j >= atoms) break;
-                        fp4_copy_scales_pair(tmem + Cfg::SFA_COL + 4 * j, fp4_scale_desc(sa + 512 * j));
-                        fp4_copy_scales_pair(tmem + Cfg::SFB_COL + 8 * j, fp4_scale_desc(sb + 512 * j));
-                        fp4_copy_scales_pair(tmem + Cfg::SFB_COL + 8 * j + 4,
-                                             fp4_scale_desc(sb + Cfg::S_BYTES + 512 * j));
+                        fp4_copy_scales<true>(tmem + Cfg::SFA_COL + 4 * j, fp4_scale_desc(sa + 512 * j), elected);
+                        fp4_copy_scales<true>(tmem + Cfg::SFB_COL + 8 * j, fp4_scale_desc(sb + 512 * j), elected);
+                        fp4_copy_scales<true>(tmem + Cfg::SFB_COL + 8 * j + 4,
+                                              fp4_scale_desc(sb + Cfg::S_BYTES + 512 * j), elected);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (j >= steps) break;
                         const uint32_t atom = FMT == kNv ? j : j >> 1;
                         const uint32_t id = FMT == kNv ? 0u : 2u * (j & 1);
-                        fp4_mma_pair<FMT>(d, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
-                                          fp4_idesc<FMT>(256, 256, id), tmem + Cfg::SFA_COL + 4 * atom,
-                                          tmem + Cfg::SFB_COL + 8 * atom, (kb > 0 || j > 0) ? 1u : 0u);
+                        fp4_mma<FMT, true>(d, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
+                                           fp4_idesc<FMT>(256, 256, id), tmem + Cfg::SFA_COL + 4 * atom,
+                                           tmem + Cfg::SFB_COL + 8 * atom, (kb > 0 || j > 0) ? 1u : 0u, elected);
                     }
-                    tc_commit_pair(empty_bar(ps.slot()), 0x3);
+                    if (elected) tc_commit_pair(empty_bar(ps.slot()), 0x3);
+                    __syncwarp();
                     ps.next();
                 }
                 if (!ok) break;
-                tc_commit_pair(accf_bar(n & 1), 0x3);
+                if (elected) tc_commit_pair(accf_bar(n & 1), 0x3);
+                __syncwarp();
             }
-            tc_commit_pair(drain_bar, 0x1);
+            if (elected) tc_commit_pair(drain_bar, 0x1);
+            __syncwarp();
             bounded_wait(drain_bar, 0u, nullptr, p.ctl, kSiteFp4PairDrainMma);
         }
+        __syncwarp();
     } else {
         // ---------------------------------------------------- epilogue (both CTAs)
         const int quad = warp & 3, half = (warp - 2) >> 2;
