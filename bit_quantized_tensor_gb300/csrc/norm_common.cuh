@@ -50,8 +50,8 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 // With many rows the kernels walk over them with a ring of rows in shared
 // memory that cp.async.bulk fills some rows ahead, so the loads of the next
 // rows are in flight while a row goes through its reductions, at no cost in
-// registers.  A bulk copy wants whole 16-byte pieces: of a row that starts or
-// ends inside one, the few bytes of the edge pieces are copied by threads.
+// registers.  A bulk copy moves whole 16-byte pieces, so a row that starts or
+// ends inside one comes with a few bytes of its neighbours.
 //
 // A group of TPR threads (a warp, or the CTA) has a ring of its own.
 
@@ -70,68 +70,83 @@ struct RowRing {
     int64_t row_bytes;
 };
 
-// Bytes of a slot: a row at any offset inside its first 16-byte piece.
-__host__ __device__ inline int64_t row_slot_bytes(int64_t row_bytes) { return (row_bytes + 15 + 15) / 16 * 16; }
+// Bytes of a slot: a row at any offset inside its first 16-byte piece, readable
+// to the end of its last 32 bytes.
+__host__ __device__ inline int64_t row_slot_bytes(int64_t row_bytes) { return (row_bytes + 15 + 31) / 32 * 32; }
 
-// A row in memory cut at 16-byte boundaries.
+// The 16-byte pieces that a bulk copy fetches for a row: all that it touches,
+// but of the matrix's first row none that begins before it, and of its last
+// row none that ends behind it (memory there need not be the caller's).
 struct RowPieces {
-    uintptr_t start, end, base;  // the row; the 16-byte piece it starts in
-    uintptr_t a;                 // first whole piece
-    uint32_t whole;              // bytes of whole pieces
+    uintptr_t start, end, base;  // the row; the piece it starts in
+    uintptr_t a;                 // first piece fetched
+    uint32_t bytes;              // of pieces fetched
 };
-__device__ __forceinline__ RowPieces row_pieces(const void* row, int64_t bytes) {
+__device__ __forceinline__ RowPieces row_pieces(const void* row, int64_t row_bytes, bool first, bool last) {
     RowPieces q;
     q.start = reinterpret_cast<uintptr_t>(row);
-    q.end = q.start + bytes;
+    q.end = q.start + row_bytes;
     q.base = q.start & ~uintptr_t(15);
-    q.a = (q.start + 15) & ~uintptr_t(15);
-    const uintptr_t b = q.end & ~uintptr_t(15);
-    q.whole = b > q.a ? static_cast<uint32_t>(b - q.a) : 0u;
+    q.a = first ? (q.start + 15) & ~uintptr_t(15) : q.base;
+    const uintptr_t b = last ? q.end & ~uintptr_t(15) : (q.end + 15) & ~uintptr_t(15);
+    q.bytes = b > q.a ? static_cast<uint32_t>(b - q.a) : 0u;
     return q;
 }
-// The bytes outside the whole pieces, two a thread (elements are 2 or 4 bytes
-// at addresses that are multiples of 2).
+// The rest of a first or last row, two bytes a thread (elements are 2 or 4
+// bytes, at addresses that are multiples of 2).
 __device__ __forceinline__ void row_edges(const RowPieces& q, uint8_t* dst, int t) {
-    const uintptr_t head_end = q.whole ? q.a : q.end;
+    if (t >= 32) return;
+    const uintptr_t head_end = q.bytes ? q.a : q.end;
     const uintptr_t h = q.start + 2 * t;
-    if (t < 32 && h < head_end)
-        *reinterpret_cast<uint16_t*>(dst + (h - q.base)) = *reinterpret_cast<const uint16_t*>(h);
-    const uintptr_t e = q.a + q.whole + 2 * t;
-    if (q.whole && t < 8 && e < q.end)
-        *reinterpret_cast<uint16_t*>(dst + (e - q.base)) = *reinterpret_cast<const uint16_t*>(e);
+    if (h < head_end) *reinterpret_cast<uint16_t*>(dst + (h - q.base)) = *reinterpret_cast<const uint16_t*>(h);
+    const uintptr_t e = q.a + q.bytes + 2 * t;
+    if (q.bytes && e < q.end) *reinterpret_cast<uint16_t*>(dst + (e - q.base)) = *reinterpret_cast<const uint16_t*>(e);
 }
 
-// Starts the copy of a row into slot s.  All threads of the group call it, after
-// all of them have read the slot's previous row and synchronized; the edges are
-// visible after the group's next synchronization.
-template <int TPR>
-__device__ __forceinline__ void row_fetch(const RowRing& r, int s, const void* row) {
+__device__ __forceinline__ void row_copy(const RowPieces& q, uint8_t* dst, uint32_t bar) {
+    if (q.bytes) bulk_copy_g2s(smem_u32(dst + (q.a - q.base)), reinterpret_cast<const void*>(q.a), q.bytes, bar);
+}
+
+// Starts the copy of row i of M into slot s.  All threads of the group call it,
+// after all of them have read the slot's previous row and synchronized; what
+// row_edges copies is visible after the group's next synchronization.
+// EDGES: rows may start or end inside a piece.
+template <int TPR, bool EDGES>
+__device__ __forceinline__ void row_fetch(const RowRing& r, int s, const void* row, int64_t i, int64_t M) {
     const int t = threadIdx.x % TPR;
+    const bool first = i == 0, last = i == M - 1;
+    const bool alone = EDGES && (first || last);
+    if (t && !alone) return;
     uint8_t* dst = r.slots + static_cast<int64_t>(s) * r.slot_bytes;
-    const RowPieces q = row_pieces(row, r.row_bytes);
+    const RowPieces q = row_pieces(row, r.row_bytes, first, last);
     const uint32_t bar = r.bar0 + 8 * s;
     if (t == 0) {
-        mbar_arrive_expect_tx(bar, q.whole);
-        if (q.whole) bulk_copy_g2s(smem_u32(dst + (q.a - q.base)), reinterpret_cast<const void*>(q.a), q.whole, bar);
+        mbar_arrive_expect_tx(bar, q.bytes);
+        row_copy(q, dst, bar);
     }
-    if ((q.start | q.end) & 15) row_edges(q, dst, t);
+    if (alone) row_edges(q, dst, t);
 }
 
 // The same for two rows of one length that share a slot: x, then y half a slot on.
 template <int TPR>
-__device__ __forceinline__ void row_fetch2(const RowRing& r, int s, const void* x, const void* y) {
+__device__ __forceinline__ void row_fetch2(const RowRing& r, int s, const void* x, const void* y, int64_t i,
+                                           int64_t M) {
     const int t = threadIdx.x % TPR;
+    const bool first = i == 0, last = i == M - 1;
+    if (t && !first && !last) return;
     uint8_t* dx = r.slots + static_cast<int64_t>(s) * r.slot_bytes;
     uint8_t* dy = dx + r.slot_bytes / 2;
-    const RowPieces p = row_pieces(x, r.row_bytes), q = row_pieces(y, r.row_bytes);
+    const RowPieces p = row_pieces(x, r.row_bytes, first, last), q = row_pieces(y, r.row_bytes, first, last);
     const uint32_t bar = r.bar0 + 8 * s;
     if (t == 0) {
-        mbar_arrive_expect_tx(bar, p.whole + q.whole);
-        if (p.whole) bulk_copy_g2s(smem_u32(dx + (p.a - p.base)), reinterpret_cast<const void*>(p.a), p.whole, bar);
-        if (q.whole) bulk_copy_g2s(smem_u32(dy + (q.a - q.base)), reinterpret_cast<const void*>(q.a), q.whole, bar);
+        mbar_arrive_expect_tx(bar, p.bytes + q.bytes);
+        row_copy(p, dx, bar);
+        row_copy(q, dy, bar);
     }
-    if ((p.start | p.end) & 15) row_edges(p, dx, t);
-    if ((q.start | q.end) & 15) row_edges(q, dy, t);
+    if (first || last) {
+        row_edges(p, dx, t);
+        row_edges(q, dy, t);
+    }
 }
 
 template <class T>
@@ -186,17 +201,45 @@ __device__ __forceinline__ void store_pairs(T* p, const uint64_t (&v)[4]) {
     }
     store_vec<T, 8>(p, x);
 }
-// gamma or beta of 8 columns (w 16-byte aligned, k a multiple of 8); `none` without one.
-template <class T>
-__device__ __forceinline__ void weight_pairs(const void* w, bool f32, int k, float none, uint64_t (&g)[4]) {
-    if (!w) {
+// The rows of a group may start inside a 16-byte piece, but all at the same
+// place (`lead` values into it): its columns then come in aligned pieces of 8
+// that begin at column -lead.  Pieces that reach outside [0, D) are cut.
+__device__ __forceinline__ bool piece_cut(int k, int D) { return k < 0 || k + 8 > D; }
+__device__ __forceinline__ void cut_piece(uint64_t (&v)[4], int k, int D) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) g[j] = two(none, none);
-    } else if (f32) {
-        load_pairs<float>(static_cast<const float*>(w) + k, g);
-    } else {
-        load_pairs<T>(static_cast<const T*>(w) + k, g);
+    for (int j = 0; j < 4; ++j) {
+        const float2 f = both(v[j]);
+        const int a = k + 2 * j;
+        v[j] = two(a >= 0 && a < D ? f.x : 0.f, a + 1 >= 0 && a + 1 < D ? f.y : 0.f);
     }
+}
+template <class T>
+__device__ __forceinline__ void load_piece(const T* p, int k, int D, uint64_t (&v)[4]) {
+    load_pairs<T>(p, v);
+    if (piece_cut(k, D)) cut_piece(v, k, D);
+}
+// To memory: whole where p is the start of a 16-byte piece, else one by one.
+template <class T>
+__device__ __forceinline__ void store_piece(T* row, int k, int D, bool whole, const uint64_t (&v)[4]) {
+    if (whole && !piece_cut(k, D)) {
+        store_pairs<T>(row + k, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 f = both(v[j / 2]);
+            if (k + j >= 0 && k + j < D) row[k + j] = from_f32<T>(j & 1 ? f.y : f.x);
+        }
+    }
+}
+// gamma or beta of a piece, 0 outside [0, D), `none` without one.
+template <class T>
+__device__ __forceinline__ void weight_piece(const void* w, bool f32, int k, int D, float none, uint64_t (&g)[4]) {
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] = k + j < 0 || k + j >= D ? 0.f : w ? weight_at<T>(w, f32, k + j) : none;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) g[j] = two(f[2 * j], f[2 * j + 1]);
 }
 
 // gamma or beta as fp32 in shared memory, for rows that are not read in pieces.
@@ -213,13 +256,31 @@ constexpr int kSiteNormRow = 401;
 constexpr int64_t kRingSmem = 160 * 1024;
 
 // Slots of a ring: as many as an SM's share holds, `least` at least.
-inline int ring_slots(int64_t slot_bytes, int64_t rings_per_sm, int least) {
-    const int64_t n = kRingSmem / (slot_bytes * rings_per_sm);
+inline int ring_slots(int64_t slot_bytes, int64_t rings_per_sm, int least, int64_t smem = kRingSmem) {
+    const int64_t n = smem / (slot_bytes * rings_per_sm);
     return static_cast<int>(n < least ? least : n > kRingMax ? kRingMax : n);
 }
 
 inline bool vec_ok(const void* p, int64_t ld, size_t elem, int64_t rows) {
     return aligned16(p) && (rows <= 1 || (static_cast<size_t>(ld) * elem) % 16 == 0);
+}
+
+// Rows a step must be a multiple of for all rows of a group to start at the same
+// place inside a 16-byte piece.
+inline int64_t same_place_rows(int64_t ld, size_t elem) {
+    int64_t n = 1;
+    while ((static_cast<size_t>(ld) * elem * static_cast<size_t>(n)) % 16 != 0) n *= 2;
+    return n;  // at most 8: elements are 2 or 4 bytes
+}
+
+// CTAs to launch for M rows, at most `most`: with more rows than groups, rounded
+// down so that a group's rows lie a multiple of `same` apart (0: cannot be).
+inline int64_t norm_ctas(int64_t M, int64_t groups, int64_t most, int64_t same) {
+    const int64_t want = (M + groups - 1) / groups;
+    if (want <= most) return want;
+    int64_t n = most;
+    while (n > 0 && n * groups % same != 0) --n;
+    return n;
 }
 
 // Argument checks of the norm's calls (qg_norm.cu).

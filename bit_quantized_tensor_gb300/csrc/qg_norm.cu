@@ -139,23 +139,24 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
 }
 
 __host__ __device__ constexpr int norm_threads(int tpr) { return tpr == 32 ? 256 : tpr; }
-__host__ __device__ constexpr int norm_min_ctas(int tpr, bool vec) {
-    return tpr == 32 ? 2 : vec || tpr == 1024 ? 1024 / tpr : 512 / tpr;  // staged weights take room
-}
+__host__ __device__ constexpr int norm_min_ctas(int tpr) { return tpr == 32 ? 2 : 512 / tpr; }
 
-// VEC: rows, gamma and beta (and y) are read and written in whole 16-byte
-// pieces, 8 columns a step (D a multiple of 8).  Without VEC, gamma and beta
-// wait in shared memory as fp32 behind the ring, and the columns of a step are
-// neighbours in neighbouring threads (FMT >= 0: 8 consecutive ones of a thread
-// all the same, since a code word takes eight).  Arithmetic on pairs keeps the
-// VEC form at about 9 instructions a value (32 without, which bound it: 8192 x
-// 8192 bf16 took 77 us).
-template <class T, int TPR, int VPT, int FMT, bool VEC>
-__global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR, VEC))
+// A thread holds 8 consecutive columns a step, and gamma and beta of its
+// columns stay in registers from row to row.  EDGES: rows may start or end
+// inside a 16-byte piece; then all rows of a group start at the same place in
+// one (the launch sees to it) and the columns are cut from there, in aligned
+// pieces.  Codes cannot follow that (a code word takes eight columns from a
+// multiple of eight on), so FMT >= 0 with EDGES reads the ring value by value.
+//
+// What bounds it besides memory is the number of instructions a value: at 32
+// (scalar arithmetic, weights and guards for every row) 8192 x 8192 bf16 took
+// 77 us, at 26 67 us; pairs, 32 columns a thread and held weights leave fewer.
+template <class T, int TPR, int FMT, bool EDGES>
+__global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
     k_layer_norm_rows(const NormParams p, int slots, const Ctl ctl) {
     constexpr int GROUPS = norm_threads(TPR) / TPR;
-    constexpr int E = 8 * VPT;
-    constexpr bool RUNS = VEC || FMT >= 0;  // 8 consecutive values a step
+    constexpr int VPT = 4;
+    constexpr bool PIECES = FMT < 0 || !EDGES;
     extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ __align__(8) uint64_t bars[GROUPS][kRingMax];
     __shared__ float red[2][32];
@@ -180,53 +181,64 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR, VEC))
     const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
     int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group;
     for (int s = 0; s < slots; ++s)
-        if (row + s * step < p.M) row_fetch<TPR>(ring, s, X + (row + s * step) * p.ldx);
-    float* const sg = reinterpret_cast<float*>(ring_smem + static_cast<int64_t>(GROUPS) * slots * ring.slot_bytes);
-    float* const sb = sg + (D + 7) / 8 * 8;
-    if constexpr (!VEC) {
-        stage_weights<T>(sg, p.gamma, p.w_f32, D, 1.f);
-        stage_weights<T>(sb, p.beta, p.w_f32, D, 0.f);
-    }
+        if (row + s * step < p.M) row_fetch<TPR, EDGES>(ring, s, X + (row + s * step) * p.ldx, row + s * step, p.M);
     __syncthreads();
     const float ts = FMT == kNv && p.ts ? *p.ts : 1.f;
     const float six_ts = __fmul_rn(6.f, ts);
     const float inv_d = __frcp_rn(static_cast<float>(D));
-    auto index = [&](int e) { return RUNS ? ((e >> 3) * TPR + t) * 8 + (e & 7) : e * TPR + t; };
+    // values before column 0 in a row's first piece
+    const int lead = FMT < 0 && EDGES
+                         ? static_cast<int>((reinterpret_cast<uintptr_t>(X + row * p.ldx) & 15) / sizeof(T))
+                         : 0;
+    auto first = [&](int i) { return (i * TPR + t) * 8 - lead; };  // column of step i
+    uint64_t hg[4 * VPT], hb[4 * VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        uint64_t g[4], b[4];
+        weight_piece<T>(p.gamma, p.w_f32, first(i), D, 1.f, g);
+        weight_piece<T>(p.beta, p.w_f32, first(i), D, 0.f, b);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            hg[4 * i + j] = g[j];
+            hb[4 * i + j] = b[j];
+        }
+    }
 
     int s = 0;
     uint32_t phase = 0;
     for (; row < p.M; row += step) {
-        const void* at = X + row * p.ldx;
         // a wait that runs out is recorded, ends the fetching, and lets the
         // remaining rows through with whatever their slots hold
         bounded_wait(ring.bar0 + 8 * s, phase, &abort_flag, ctl, kSiteNormRow);
-        const T* x = row_in_slot<T>(ring, s, at);
-        uint64_t v[E / 2];
+        const T* x = row_in_slot<T>(ring, s, X + row * p.ldx);
+        uint64_t v[4 * VPT];
         uint64_t sum2 = 0;  // (0, 0)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if constexpr (VEC) {
-                const int k = (i * TPR + t) * 8;
-                uint64_t u[4] = {0, 0, 0, 0};
-                if (k < D) load_pairs<T>(x + k, u);
+            const int k = first(i);
+            uint64_t u[4] = {0, 0, 0, 0};
+            if (k < D) {
+                if constexpr (PIECES) {
+                    load_piece<T>(x + k, k, D, u);
+                } else {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[4 * i + j] = u[j];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int k = index(8 * i + 2 * j), l = index(8 * i + 2 * j + 1);
-                    v[4 * i + j] = two(k < D ? to_f32<T>(x[k]) : 0.f, l < D ? to_f32<T>(x[l]) : 0.f);
+                    for (int j = 0; j < 4; ++j)
+                        u[j] = two(k + 2 * j < D ? to_f32<T>(x[k + 2 * j]) : 0.f,
+                                   k + 2 * j + 1 < D ? to_f32<T>(x[k + 2 * j + 1]) : 0.f);
                 }
             }
-        }
 #pragma unroll
-        for (int e = 0; e < E / 2; ++e) sum2 = add_two(sum2, v[e]);
+            for (int j = 0; j < 4; ++j) {
+                v[4 * i + j] = u[j];
+                sum2 = add_two(sum2, u[j]);
+            }
+        }
         const float2 sum = both(sum2);
         const float mean = row_sum<TPR>(sum.x + sum.y, red[0]) * inv_d;
         // all threads have read the slot
         if constexpr (TPR == 32) __syncwarp();
         if (row + slots * step < p.M && !*static_cast<volatile int*>(&abort_flag))
-            row_fetch<TPR>(ring, s, X + (row + slots * step) * p.ldx);
+            row_fetch<TPR, EDGES>(ring, s, X + (row + slots * step) * p.ldx, row + slots * step, p.M);
         if (++s == slots) {
             s = 0;
             phase ^= 1u;
@@ -235,15 +247,14 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR, VEC))
         uint64_t var2 = 0;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
+            uint64_t c[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = add_two(v[4 * i + j], minus);
+            if (piece_cut(first(i), D)) cut_piece(c, first(i), D);  // nothing outside the row counts
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                uint64_t& c = v[4 * i + j];
-                c = add_two(c, minus);
-                if constexpr (!VEC) {  // nothing behind the row counts
-                    const float2 f = both(c);
-                    c = two(index(8 * i + 2 * j) < D ? f.x : 0.f, index(8 * i + 2 * j + 1) < D ? f.y : 0.f);
-                }
-                if (!VEC || (i * TPR + t) * 8 < D) var2 = fma_two(c, c, var2);
+                var2 = fma_two(c[j], c[j], var2);
+                v[4 * i + j] = c[j];
             }
         }
         const float2 var = both(var2);
@@ -255,43 +266,24 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR, VEC))
         const uint64_t r2 = two(rstd, rstd);
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
-            if constexpr (RUNS) {
-                const int k = (i * TPR + t) * 8;
-                if (i > 0 && (i * TPR + (t & ~31)) * 8 >= (D + 127) / 128 * 128) continue;  // the warp is past the row
-                uint64_t y[4] = {0, 0, 0, 0};
-                if (k < D) {
-                    uint64_t g[4], b[4];
-                    if constexpr (VEC) {
-                        weight_pairs<T>(p.gamma, p.w_f32, k, 1.f, g);
-                        weight_pairs<T>(p.beta, p.w_f32, k, 0.f, b);
-                    } else {
-                        load_pairs<float>(sg + k, g);  // past D: values that are dropped below
-                        load_pairs<float>(sb + k, b);
-                    }
+            const int k = first(i);
+            if (FMT < 0 && k >= D) continue;
+            if (FMT >= 0 && i > 0 && (i * TPR + (t & ~31)) * 8 >= (D + 127) / 128 * 128) continue;  // the whole warp
+            uint64_t y[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) y[j] = fma_two(mul_two(v[4 * i + j], r2), g[j], b[j]);
-                }
-                if constexpr (FMT >= 0) {
-                    float f[8];
+            for (int j = 0; j < 4; ++j) y[j] = fma_two(mul_two(v[4 * i + j], r2), hg[4 * i + j], hb[4 * i + j]);
+            if constexpr (FMT >= 0) {
+                // 0 behind the row: c, gamma and beta are 0 there
+                float f[8];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 h = both(y[j]);
-                        f[2 * j] = VEC || k + 2 * j < D ? h.x : 0.f;
-                        f[2 * j + 1] = VEC || k + 2 * j + 1 < D ? h.y : 0.f;
-                    }
-                    quantize_lane8<FMT>(f, k, p.D, row, ts, six_ts, p.Xq, p.Xs);
-                } else if (k < D) {
-                    store_pairs<T>(static_cast<T*>(p.Y) + row * p.ldy + k, y);
+                for (int j = 0; j < 4; ++j) {
+                    const float2 h = both(y[j]);
+                    f[2 * j] = h.x;
+                    f[2 * j + 1] = h.y;
                 }
+                quantize_lane8<FMT>(f, k, p.D, row, ts, six_ts, p.Xq, p.Xs);
             } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int k = (8 * i + j) * TPR + t;
-                    if (k >= D) continue;
-                    const float2 c = both(v[4 * i + j / 2]);
-                    static_cast<T*>(p.Y)[row * p.ldy + k] =
-                        from_f32<T>(fmaf((j & 1 ? c.y : c.x) * rstd, sg[k], sb[k]));
-                }
+                store_piece<T>(static_cast<T*>(p.Y) + row * p.ldy, k, D, !EDGES || p.y_vec, y);
             }
         }
     }
@@ -355,6 +347,7 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const NormPara
 // ------------------------------------------------------- host side
 
 constexpr int64_t kMaxHeldFwd = 1024 * 32;   // longest row that k_layer_norm holds
+constexpr int64_t kMaxRingFwd = 512 * 32 - 8;  // longest row that k_layer_norm_rows holds, at any place in a piece
 
 template <class T, int TPR, int VPT, int FMT, bool VEC>
 static int launch_norm(const NormParams& p, cudaStream_t s) {
@@ -367,34 +360,44 @@ static int launch_norm(const NormParams& p, cudaStream_t s) {
 // Threads a row: with enough rows to fill the SMs, as few as hold the row in 32
 // registers each (many rows in flight, few barriers); with fewer rows than SMs,
 // one step of 8 values a thread, since then the row's own latency is all there is.
-// gamma and beta as fp32 behind a ring.
-static int64_t staged_weights(int64_t D) { return 2 * ((D + 7) / 8 * 8) * 4; }
-
-// Largest dynamic shared memory of an instance (rows of 8 VPT TPR values).
-static int ring_bytes(int tpr, int vpt, size_t elem, bool vec) {
-    const int64_t slot = row_slot_bytes(static_cast<int64_t>(tpr) * vpt * 8 * static_cast<int64_t>(elem));
-    const int groups = norm_threads(tpr) / tpr;
-    return static_cast<int>(slot * ring_slots(slot, groups * norm_min_ctas(tpr, vec), 2) * groups +
-                            (vec ? 0 : staged_weights(int64_t(tpr) * vpt * 8)));
+// Slots of a ring, 2 at least: the edges of a row show one synchronization
+// after their copy.
+static int norm_slots(int64_t slot_bytes, int tpr) {
+    return ring_slots(slot_bytes, norm_threads(tpr) / tpr * norm_min_ctas(tpr), 2);
 }
 
-template <class T, int TPR, int VPT, int FMT, bool VEC>
-static int launch_norm_rows(const NormParams& p, int dev, cudaStream_t s) {
-    constexpr int THREADS = norm_threads(TPR), GROUPS = THREADS / TPR, CTAS = norm_min_ctas(TPR, VEC);
+// Largest dynamic shared memory of an instance (rows of 32 columns a thread).
+static int ring_bytes(int tpr, size_t elem) {
+    const int64_t slot = row_slot_bytes(static_cast<int64_t>(tpr) * 32 * static_cast<int64_t>(elem));
+    return static_cast<int>(slot * norm_slots(slot, tpr) * (norm_threads(tpr) / tpr));
+}
+
+template <class T, int TPR, int FMT, bool EDGES>
+static int launch_norm_rows(const NormParams& p, int64_t same, int dev, cudaStream_t s) {
+    constexpr int THREADS = norm_threads(TPR), GROUPS = THREADS / TPR, CTAS = norm_min_ctas(TPR);
     const Ctl ctl = host_ctl(dev);
     if (!ctl.status) return QG_ERR_CUDA;
     const int64_t slot = row_slot_bytes(p.D * static_cast<int64_t>(sizeof(T)));
-    const int slots = ring_slots(slot, GROUPS * CTAS, 2)  /* edges show one synchronization after their copy */;
-    const int64_t smem = slot * slots * GROUPS + (VEC ? 0 : staged_weights(p.D));
-    auto* f = k_layer_norm_rows<T, TPR, VPT, FMT, VEC>;
+    const int slots = norm_slots(slot, TPR);
+    const int64_t smem = slot * slots * GROUPS;
+    auto* f = k_layer_norm_rows<T, TPR, FMT, EDGES>;
     if (smem > 48 * 1024 - 1024) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return map_cuda(e);
     }
-    int64_t ctas = (p.M + GROUPS - 1) / GROUPS;
-    if (ctas > CTAS * num_sms(dev)) ctas = CTAS * num_sms(dev);
+    const int64_t ctas = norm_ctas(p.M, GROUPS, int64_t(CTAS) * num_sms(dev), same);
     return launch_serialized(f, dim3(static_cast<unsigned>(ctas)), THREADS, static_cast<size_t>(smem), 1, s, p, slots,
                              ctl);
+}
+
+// Threads a row: as few as hold it in 32 columns each.
+template <class T, int FMT, bool EDGES>
+static int norm_rows_by_size(const NormParams& p, int64_t same, int dev, cudaStream_t s) {
+    const int64_t D = p.D + (EDGES ? 8 : 0);  // its place in the first piece
+    if (D <= 1024) return launch_norm_rows<T, 32, FMT, EDGES>(p, same, dev, s);
+    if (D <= 4096) return launch_norm_rows<T, 128, FMT, EDGES>(p, same, dev, s);
+    if (D <= 8192) return launch_norm_rows<T, 256, FMT, EDGES>(p, same, dev, s);
+    return launch_norm_rows<T, 512, FMT, EDGES>(p, same, dev, s);
 }
 
 template <class T, int FMT, bool VEC>
@@ -404,17 +407,15 @@ static int norm_by_size(const NormParams& p, int dev, cudaStream_t s) {
     if (p.M <= num_sms(dev)) {
         if (D <= 2048) return launch_norm<T, 256, 1, FMT, VEC>(p, s);
         if (D <= 8192) return launch_norm<T, 1024, 1, FMT, VEC>(p, s);
-    } else if (p.x_vec && p.w_vec && p.D % 8 == 0 && (FMT >= 0 || VEC)) {
-        if (D <= 1024) return launch_norm_rows<T, 32, 4, FMT, true>(p, dev, s);
-        if (D <= 2048) return launch_norm_rows<T, 128, 2, FMT, true>(p, dev, s);
-        if (D <= 4096) return launch_norm_rows<T, 256, 2, FMT, true>(p, dev, s);
-        if (D <= 8192) return launch_norm_rows<T, 512, 2, FMT, true>(p, dev, s);
-        if (D <= 16384) return launch_norm_rows<T, 1024, 2, FMT, true>(p, dev, s);
-    } else {
-        if (D <= 1024) return launch_norm_rows<T, 32, 4, FMT, false>(p, dev, s);
-        if (D <= 2048) return launch_norm_rows<T, 128, 2, FMT, false>(p, dev, s);
-        if (D <= 4096) return launch_norm_rows<T, 256, 2, FMT, false>(p, dev, s);
-        if (D <= 8192) return launch_norm_rows<T, 512, 2, FMT, false>(p, dev, s);
+    } else if (D <= kMaxRingFwd) {
+        const int64_t same = same_place_rows(p.ldx, sizeof(T));
+        const bool edges = !p.x_vec || p.D * sizeof(T) % 16 != 0;
+        // y is stored in pieces where its rows start at the same places as those of x
+        NormParams q = p;
+        q.y_vec = FMT >= 0 || (reinterpret_cast<uintptr_t>(p.X) % 16 == reinterpret_cast<uintptr_t>(p.Y) % 16 &&
+                               (static_cast<size_t>(p.ldx) * sizeof(T)) % 16 == (static_cast<size_t>(p.ldy) * sizeof(T)) % 16);
+        if (!edges && q.y_vec) return norm_rows_by_size<T, FMT, false>(q, 1, dev, s);
+        return norm_rows_by_size<T, FMT, true>(q, FMT < 0 ? same : 1, dev, s);
     }
     if (D <= kMaxHeldFwd) return launch_norm<T, 1024, 4, FMT, VEC>(p, s);
     return launch_serialized(k_layer_norm_long<T, FMT>, dim3(static_cast<unsigned>(p.M)), kLongThreads, 0, 1, s, p);
@@ -477,16 +478,16 @@ static int norm_call(int fmt, int dtype, int64_t M, int64_t D, const void* X, in
     QG_NORM_FWD(T, NAME, 256, 1, FMT, FNAME, VEC);        \
     QG_NORM_FWD(T, NAME, 1024, 1, FMT, FNAME, VEC);       \
     QG_NORM_FWD(T, NAME, 1024, 4, FMT, FNAME, VEC)
-// shared memory of a full ring: the longest row the instance takes, unaligned
-#define QG_NORM_ROWS(T, NAME, TPR, VPT, FMT, FNAME, VEC)                                                   \
-    QG_BLOCK_KERNEL_BUDGET("k_layer_norm_rows<" NAME "," #TPR "," #VPT "," FNAME "," #VEC ">",             \
-                           (reinterpret_cast<const void*>(k_layer_norm_rows<T, TPR, VPT, FMT, VEC>)),      \
-                           norm_threads(TPR), ring_bytes(TPR, VPT, sizeof(T), VEC), 0, 1, norm_min_ctas(TPR, VEC))
-#define QG_NORM_ROWS_SIZES(T, NAME, FMT, FNAME, VEC)      \
-    QG_NORM_ROWS(T, NAME, 32, 4, FMT, FNAME, VEC);        \
-    QG_NORM_ROWS(T, NAME, 128, 2, FMT, FNAME, VEC);       \
-    QG_NORM_ROWS(T, NAME, 256, 2, FMT, FNAME, VEC);       \
-    QG_NORM_ROWS(T, NAME, 512, 2, FMT, FNAME, VEC)
+// shared memory of a full ring: the longest row the instance takes
+#define QG_NORM_ROWS(T, NAME, TPR, FMT, FNAME, EDGES)                                                  \
+    QG_BLOCK_KERNEL_BUDGET("k_layer_norm_rows<" NAME "," #TPR "," FNAME "," #EDGES ">",                \
+                           (reinterpret_cast<const void*>(k_layer_norm_rows<T, TPR, FMT, EDGES>)),     \
+                           norm_threads(TPR), ring_bytes(TPR, sizeof(T)), 0, 1, norm_min_ctas(TPR))
+#define QG_NORM_ROWS_SIZES(T, NAME, FMT, FNAME, EDGES) \
+    QG_NORM_ROWS(T, NAME, 32, FMT, FNAME, EDGES);      \
+    QG_NORM_ROWS(T, NAME, 128, FMT, FNAME, EDGES);     \
+    QG_NORM_ROWS(T, NAME, 256, FMT, FNAME, EDGES);     \
+    QG_NORM_ROWS(T, NAME, 512, FMT, FNAME, EDGES)
 #define QG_NORM_LONG(T, NAME)                                                                              \
     QG_BLOCK_KERNEL_BUDGET("k_layer_norm_long<" NAME ">", (reinterpret_cast<const void*>(k_layer_norm_long<T, kToValues>)), \
                            kLongThreads, 0, 0, 1, 1);                                                      \
@@ -499,15 +500,12 @@ static int norm_call(int fmt, int dtype, int64_t M, int64_t D, const void* X, in
     QG_NORM_FWD_SIZES(T, NAME, kToValues, "y", false);        \
     QG_NORM_FWD_SIZES(T, NAME, kNv, "nv", true);              \
     QG_NORM_FWD_SIZES(T, NAME, kMx, "mx", true);              \
-    QG_NORM_ROWS(T, NAME, 1024, 2, kToValues, "y", true); \
-    QG_NORM_ROWS_SIZES(T, NAME, kToValues, "y", true);        \
     QG_NORM_ROWS_SIZES(T, NAME, kToValues, "y", false);       \
-    QG_NORM_ROWS(T, NAME, 1024, 2, kNv, "nv", true); \
-    QG_NORM_ROWS_SIZES(T, NAME, kNv, "nv", true);             \
+    QG_NORM_ROWS_SIZES(T, NAME, kToValues, "y", true);        \
     QG_NORM_ROWS_SIZES(T, NAME, kNv, "nv", false);            \
-    QG_NORM_ROWS(T, NAME, 1024, 2, kMx, "mx", true); \
-    QG_NORM_ROWS_SIZES(T, NAME, kMx, "mx", true);             \
+    QG_NORM_ROWS_SIZES(T, NAME, kNv, "nv", true);             \
     QG_NORM_ROWS_SIZES(T, NAME, kMx, "mx", false);            \
+    QG_NORM_ROWS_SIZES(T, NAME, kMx, "mx", true);             \
     QG_NORM_LONG(T, NAME)
 QG_NORM_BUDGETS(__half, "f16");
 QG_NORM_BUDGETS(__nv_bfloat16, "bf16");

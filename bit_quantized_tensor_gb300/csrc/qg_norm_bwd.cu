@@ -50,12 +50,33 @@ int sum_partials_run(const float* partial, int64_t parts, int64_t n, float* out,
 //
 // A CTA of 512 threads walks over rows, TPR threads a row, each group with a
 // ring of (x, dy) row pairs in shared memory (norm_common.cuh).  A thread
-// meets the same columns in every row and keeps their sums for gamma and beta
-// in registers; x and dy are read from the ring twice, for the row's two sums
-// and for dx, rather than held in between.  A slot is refilled one row late,
-// behind the next row's only barrier.  At the end the groups add up in shared
-// memory, in order, and each CTA leaves one row of partial sums.
+// meets the same columns in every row and keeps gamma and their sums for
+// dgamma and dbeta in registers, which leaves an SM only 16 warps.  So that the
+// exchange of a row's two sums between its warps does not show, it is split:
+// the warps leave their part of row i + 1, arrive at a barrier, finish dx of
+// row i from the ring, and only then wait.  At the end each CTA adds up its
+// groups, in order, and leaves one row of partial sums.
 constexpr int kBwdThreads = 512;
+constexpr int kSiteNormSums = 402;
+
+// Sums of two values over a warp with one value's shuffles: the halves of the
+// warp take one each.  Lanes 0-15 end with the sum of a, the others with that of b.
+template <int LANES>
+__device__ __forceinline__ float half_sums(float v) {
+#pragma unroll
+    for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+__device__ __forceinline__ float warp_sums_by_half(float a, float b) {
+    const bool low = (threadIdx.x & 16) == 0;
+    const float other = __shfl_xor_sync(0xffffffffu, low ? b : a, 16);
+    return half_sums<16>((low ? a : b) + other);
+}
+// The halves' sums to every lane: (a, b).
+__device__ __forceinline__ float2 from_halves(float v) {
+    const float other = __shfl_xor_sync(0xffffffffu, v, 16);
+    return (threadIdx.x & 16) == 0 ? make_float2(v, other) : make_float2(other, v);
+}
 
 struct NormBwdParams {
     int64_t M, D;
@@ -70,25 +91,33 @@ struct NormBwdParams {
 };
 
 
-template <class T, int TPR, int VPT, bool VEC>
+// VEC: all rows of a group, of x, dy and dx alike, start at the same place
+// inside a 16-byte piece, and come in aligned pieces of 8 columns from there
+// (EDGES; else at its start and whole).  Without VEC (rows of different places)
+// the columns of a step are neighbours in neighbouring threads, and gamma waits
+// in shared memory behind the ring.
+template <class T, int TPR, int VPT, bool VEC, bool EDGES>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_layer_norm_backward(const NormBwdParams p, int slots, const Ctl ctl) {
-    constexpr int GROUPS = kBwdThreads / TPR;
+    constexpr int GROUPS = kBwdThreads / TPR, WARPS = TPR / 32;
     constexpr int E = 8 * VPT;
     constexpr int COLS = TPR * E;
     extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ __align__(8) uint64_t bars[GROUPS][kRingMax];
-    __shared__ float2 red[2][kBwdThreads / 32];
+    __shared__ __align__(8) uint64_t sum_bars[GROUPS];
+    __shared__ float red[2][GROUPS][2][16];  // a row's sums, per warp: d, d c
     __shared__ int abort_flag;
-    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+    const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, lane = threadIdx.x & 31;
     const int D = static_cast<int>(p.D);
     RowRing ring;
     ring.bar0 = smem_u32(&bars[group][0]);
     ring.row_bytes = p.D * static_cast<int64_t>(sizeof(T));
     ring.slot_bytes = static_cast<int>(2 * row_slot_bytes(ring.row_bytes));
     ring.slots = ring_smem + static_cast<int64_t>(group) * slots * ring.slot_bytes;
+    const uint32_t sum_bar = smem_u32(&sum_bars[group]);
     if (t == 0) {
         for (int s = 0; s < slots; ++s) mbar_init(ring.bar0 + 8 * s, 1);
+        mbar_init(sum_bar, WARPS);
         fence_mbar_init();
     }
     if (threadIdx.x == 0) abort_flag = 0;
@@ -101,22 +130,26 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group;
     for (int s = 0; s < slots; ++s) {
         const int64_t r = row + s * step;
-        if (r < p.M) row_fetch2<TPR>(ring, s, X + r * p.ldx, dY + r * p.lddy);
+        if (r < p.M) row_fetch2<TPR>(ring, s, X + r * p.ldx, dY + r * p.lddy, r, p.M);
     }
-    // without VEC gamma waits in shared memory as fp32, behind the ring
     float* const sg = reinterpret_cast<float*>(ring_smem + static_cast<int64_t>(GROUPS) * slots * ring.slot_bytes);
     if constexpr (!VEC) stage_weights<T>(sg, p.gamma, p.w_f32, D, 1.f);
     __syncthreads();
     const float inv_d = __frcp_rn(static_cast<float>(D));
-    uint64_t dg[E / 2], db[E / 2];
+    // values before column 0 in a row's first piece
+    const int lead =
+        VEC && EDGES ? static_cast<int>((reinterpret_cast<uintptr_t>(X + row * p.ldx) & 15) / sizeof(T)) : 0;
+    uint64_t dg[E / 2], db[E / 2], hg[VEC ? E / 2 : 1];
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dg[e] = db[e] = 0;
 
-    // column of value j of step i, and whether no lane of the warp has one left
-    auto column = [&](int i, int j) { return VEC ? (i * TPR + t) * 8 + j : (8 * i + j) * TPR + t; };
-    auto step_done = [&](int i) { return VEC ? (i * TPR + t) * 8 >= D : 8 * i * TPR >= D; };
+    // column of value j of step i, and whether the thread has none left
+    auto column = [&](int i, int j) { return VEC ? (i * TPR + t) * 8 - lead + j : (8 * i + j) * TPR + t; };
+    auto step_done = [&](int i) { return VEC ? column(i, 0) >= D : 8 * i * TPR >= D; };
     auto values = [&](const T* x, int i, uint64_t(&v)[4]) {
-        if constexpr (VEC) {
+        if constexpr (VEC && EDGES) {
+            load_piece<T>(x + column(i, 0), column(i, 0), D, v);
+        } else if constexpr (VEC) {
             load_pairs<T>(x + column(i, 0), v);
         } else {
 #pragma unroll
@@ -126,41 +159,42 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
     };
-    auto gammas = [&](int i, uint64_t(&g)[4]) {
-        if constexpr (VEC) {
-            weight_pairs<T>(p.gamma, p.w_f32, column(i, 0), 1.f, g);
-        } else {
+    if constexpr (VEC) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < VPT; ++i) {
+            uint64_t g[4];
+            weight_piece<T>(p.gamma, p.w_f32, column(i, 0), D, 1.f, g);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) hg[4 * i + j] = g[j];
+        }
+    }
+    auto gammas = [&](int i, uint64_t(&g)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if constexpr (VEC) {
+                g[j] = hg[4 * i + j];
+            } else {
                 const int k = column(i, 2 * j), l = column(i, 2 * j + 1);
                 g[j] = two(k < D ? sg[k] : 0.f, l < D ? sg[l] : 0.f);
             }
         }
     };
+    // where a row lies in its slot: x, and dy half a slot on
+    const bool moves = VEC ? false : true;  // its place in a piece changes from row to row
+    auto place = [&](const T* base, int64_t ld, int64_t r) {
+        return static_cast<int>(moves ? reinterpret_cast<uintptr_t>(base + r * ld) & 15 : lead * sizeof(T));
+    };
 
-    float mean = 0.f, rstd = 0.f;
-    if (row < p.M) {
-        mean = p.mean[row];
-        rstd = p.rstd[row];
-    }
-    int s = 0, before = slots - 1;
-    uint32_t phase = 0;
-    int flip = 0;
-    bool first = true;
-    for (; row < p.M; row += step, flip ^= 1) {
-        float mean_next = 0.f, rstd_next = 0.f;
-        if (row + step < p.M) {
-            mean_next = p.mean[row + step];
-            rstd_next = p.rstd[row + step];
-        }
+    // part 1 of row r in slot s: dgamma, dbeta and the warp's part of the row's sums,
+    // by halves of the warp (outside the row dy is 0, and with it every term);
+    // with c = x - mean: dgamma += (dy rstd) c
+    auto part1 = [&](int64_t r, int s, uint32_t phase, float mean, float rstd) {
         // a wait that runs out is recorded, ends the fetching, and lets the
         // remaining rows through with whatever their slots hold
         bounded_wait(ring.bar0 + 8 * s, phase, &abort_flag, ctl, kSiteNormRow);
-        const T* x = row_in_slot<T>(ring, s, X + row * p.ldx);
-        const T* dy = reinterpret_cast<const T*>(reinterpret_cast<const uint8_t*>(
-                          row_in_slot<T>(ring, s, dY + row * p.lddy)) + ring.slot_bytes / 2);
-        // with c = x - mean: dgamma += (dy rstd) c, and the row's sums of d and of d c
-        // (behind the row dy is 0, and with it every term)
+        const uint8_t* slot = ring.slots + static_cast<int64_t>(s) * ring.slot_bytes;
+        const T* x = reinterpret_cast<const T*>(slot + place(X, p.ldx, r));
+        const T* dy = reinterpret_cast<const T*>(slot + ring.slot_bytes / 2 + place(dY, p.lddy, r));
         const uint64_t minus = two(-mean, -mean), r2 = two(rstd, rstd);
         uint64_t a1 = 0, a2 = 0;
 #pragma unroll
@@ -179,28 +213,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 a2 = fma_two(d, c, a2);
             }
         }
-        float s1 = warp_sum(both(a1).x + both(a1).y);
-        float s2 = warp_sum(both(a2).x + both(a2).y);
-        if constexpr (TPR > 32) {
-            float2* r = red[flip] + group * (TPR / 32);
-            if ((threadIdx.x & 31) == 0) r[t >> 5] = make_float2(s1, s2);
-            // the TPR threads of this row only
-            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
-            const float2 w = (threadIdx.x & 31) < TPR / 32 ? r[threadIdx.x & 31] : make_float2(0.f, 0.f);
-            s1 = warp_sum(w.x);
-            s2 = warp_sum(w.y);
-        } else {
-            __syncwarp();
-        }
-        // everyone is done with the row before: its slot takes the row `slots - 1` ahead of this one
-        const int64_t ahead = row + (slots - 1) * step;
-        if (!first && ahead < p.M && !*static_cast<volatile int*>(&abort_flag))
-            row_fetch2<TPR>(ring, before, X + ahead * p.ldx, dY + ahead * p.lddy);
-        first = false;
-        // dx = d rstd - (sum(d) / D) rstd - c (sum(d c) / D) rstd^3
-        const float k0 = -(s1 * inv_d) * rstd, k1 = -((s2 * rstd) * inv_d) * rstd * rstd;
-        const uint64_t b0 = two(k0, k0), b1 = two(k1, k1);
-        T* o = static_cast<T*>(p.dX) + row * p.lddx;
+        const float2 f1 = both(a1), f2 = both(a2);
+        return warp_sums_by_half(f1.x + f1.y, f2.x + f2.y);
+    };
+    // part 2: dx = d rstd - (sum(d) / D) rstd - c (sum(d c) / D) rstd^3
+    auto part2 = [&](int64_t r, int s, float mean, float rstd, float2 sum) {
+        const uint8_t* slot = ring.slots + static_cast<int64_t>(s) * ring.slot_bytes;
+        const T* x = reinterpret_cast<const T*>(slot + place(X, p.ldx, r));
+        const T* dy = reinterpret_cast<const T*>(slot + ring.slot_bytes / 2 + place(dY, p.lddy, r));
+        const float k0 = -(sum.x * inv_d) * rstd, k1 = -((sum.y * rstd) * inv_d) * rstd * rstd;
+        const uint64_t b0 = two(k0, k0), b1 = two(k1, k1), r2 = two(rstd, rstd), minus = two(-mean, -mean);
+        T* o = static_cast<T*>(p.dX) + r * p.lddx;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             if (step_done(i)) continue;
@@ -211,7 +234,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 y[j] = fma_two(add_two(u[j], minus), b1, fma_two(mul_two(y[j], g[j]), r2, b0));
-            if constexpr (VEC) {
+            if constexpr (VEC && EDGES) {
+                store_piece<T>(o, column(i, 0), D, true, y);
+            } else if constexpr (VEC) {
                 store_pairs<T>(o + column(i, 0), y);
             } else {
 #pragma unroll
@@ -221,9 +246,63 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
             }
         }
-        mean = mean_next;
-        rstd = rstd_next;
-        before = s;
+    };
+
+    int s = 0, n = 0;  // slot and number of the row that part 1 takes next
+    uint32_t phase = 0;
+    float mean = 0.f, rstd = 0.f, mean1 = 0.f, rstd1 = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
+    if (row < p.M) {
+        mean1 = p.mean[row];
+        rstd1 = p.rstd[row];
+    }
+    // in each round: part 1 of row `row`, part 2 of the row before it
+    int s_before = 0;
+    for (; row < p.M + step; row += step, ++n) {
+        const bool here = row < p.M, next = row + step < p.M;
+        float v = 0.f, mean2 = 0.f, rstd2 = 0.f;
+        if (next) {
+            mean2 = p.mean[row + step];
+            rstd2 = p.rstd[row + step];
+        }
+        if (here) {
+            v = part1(row, s, phase, mean1, rstd1);
+            if constexpr (TPR > 32) {
+                if ((lane & 15) == 0) red[n & 1][group][lane >> 4][t >> 5] = v;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(sum_bar);
+            }
+        }
+        if (n > 0) part2(row - step, s_before, mean, rstd, sum);
+        if (here) {
+            if constexpr (TPR > 32) {
+                bounded_wait(sum_bar, n & 1, &abort_flag, ctl, kSiteNormSums);
+                v = (lane & 15) < WARPS ? red[n & 1][group][lane >> 4][lane & 15] : 0.f;
+                v = half_sums<WARPS>(v);
+                v = __shfl_sync(0xffffffffu, v, lane & 16);
+            } else {
+                __syncwarp();
+            }
+            sum = from_halves(v);
+        }
+        // every warp has arrived for this row, so it is done with part 2 of the one two
+        // rows back: that slot takes the row `slots - 2` ahead of this one
+        const int64_t ahead = row + (slots - 2) * step;
+        if (n > 1 && ahead < p.M && !*static_cast<volatile int*>(&abort_flag)) {
+            const int free_slot = s >= 2 ? s - 2 : s + slots - 2;
+            row_fetch2<TPR>(ring, free_slot, X + ahead * p.ldx, dY + ahead * p.lddy, ahead, p.M);
+        }
+        if (n > 1 && ahead == p.M - 1) {  // what threads copied of the last row, once
+            if constexpr (TPR > 32)
+                asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
+            else
+                __syncwarp();
+        }
+        mean = mean1;
+        rstd = rstd1;
+        mean1 = mean2;
+        rstd1 = rstd2;
+        s_before = s;
         if (++s == slots) {
             s = 0;
             phase ^= 1u;
@@ -235,25 +314,27 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         while (global_timer_ns() - t0 < 1000000) {
         }
     }
-    // the groups' sums, in order, over the idle ring; then one row of partials
-    float* sums = reinterpret_cast<float*>(ring_smem);
-    for (int g = 0; g < GROUPS; ++g) {
-        if (group == g) {
+    // every group's sums over the idle ring, then one row of partials
+    float* sums = reinterpret_cast<float*>(ring_smem);  // [GROUPS][2][COLS]
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float* a = sums + column(e / 8, e % 8);
-                const float2 fg = both(dg[e / 2]), fb = both(db[e / 2]);
-                const float vg = e & 1 ? fg.y : fg.x, vb = e & 1 ? fb.y : fb.x;
-                a[0] = g ? a[0] + vg : vg;
-                a[COLS] = g ? a[COLS] + vb : vb;
-            }
-        }
-        __syncthreads();
+    for (int e = 0; e < E; ++e) {
+        const int k = column(e / 8, e % 8);
+        if (k < 0 || k >= D) continue;
+        const float2 fg = both(dg[e / 2]), fb = both(db[e / 2]);
+        sums[2 * group * COLS + k] = e & 1 ? fg.y : fg.x;
+        sums[(2 * group + 1) * COLS + k] = e & 1 ? fb.y : fb.x;
     }
+    __syncthreads();
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
     for (int k = threadIdx.x; k < D; k += kBwdThreads) {
-        out[k] = sums[k];
-        out[p.D + k] = sums[COLS + k];
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            a += sums[2 * g * COLS + k];
+            b += sums[(2 * g + 1) * COLS + k];
+        }
+        out[k] = a;
+        out[p.D + k] = b;
     }
 }
 
@@ -327,24 +408,23 @@ constexpr int kMaxPartials = 512;      // rows of partial sums, at most
 static int64_t bwd_smem(int tpr, int vpt, int64_t D, size_t elem, bool vec, int* slots) {
     const int groups = kBwdThreads / tpr;
     const int64_t slot = 2 * row_slot_bytes(D * static_cast<int64_t>(elem));
-    // 3: the edges of a row are visible one barrier after their copy, which itself is one row late
-    *slots = ring_slots(slot, groups, 3);
-    const int64_t ring = slot * *slots * groups + (vec ? 0 : (D + 7) / 8 * 32), sums = int64_t(2) * tpr * vpt * 8 * 4;
+    *slots = ring_slots(slot, groups, 3, 200 * 1024);  // two rows are in use at a time
+    const int64_t ring = slot * *slots * groups + (vec ? 0 : (D + 7) / 8 * 32);
+    const int64_t sums = int64_t(groups) * 2 * tpr * vpt * 8 * 4;
     return ring > sums ? ring : sums;
 }
 
-template <class T, int TPR, int VPT, bool VEC>
-static int launch_norm_bwd(const NormBwdParams& p, int dev, int64_t* parts, cudaStream_t s) {
+template <class T, int TPR, int VPT, bool VEC, bool EDGES>
+static int launch_norm_bwd(const NormBwdParams& p, int64_t same, int dev, int64_t* parts, cudaStream_t s) {
     constexpr int GROUPS = kBwdThreads / TPR;
     const Ctl ctl = host_ctl(dev);
     if (!ctl.status) return QG_ERR_CUDA;
-    int64_t ctas = (p.M + GROUPS - 1) / GROUPS;
-    if (ctas > num_sms(dev)) ctas = num_sms(dev);
-    if (ctas > kMaxPartials) ctas = kMaxPartials;
+    const int most = num_sms(dev) < kMaxPartials ? num_sms(dev) : kMaxPartials;
+    const int64_t ctas = norm_ctas(p.M, GROUPS, most, same);
     *parts = ctas;
     int slots = 0;
     const int64_t smem = bwd_smem(TPR, VPT, p.D, sizeof(T), VEC, &slots);
-    auto* f = k_layer_norm_backward<T, TPR, VPT, VEC>;
+    auto* f = k_layer_norm_backward<T, TPR, VPT, VEC, EDGES>;
     if (smem > 44 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return map_cuda(e);
@@ -353,22 +433,20 @@ static int launch_norm_bwd(const NormBwdParams& p, int dev, int64_t* parts, cuda
                              slots, ctl);
 }
 
-// Threads a row: as few as hold the row's sums (16 or 32 columns a thread), so
-// that an SM has several rows in different phases; limited by three slots of
-// (x, dy) a group in shared memory, which halves the columns for fp32.
-template <class T, bool VEC>
-static int norm_bwd_by_size(const NormBwdParams& p, int dev, int64_t* parts, cudaStream_t s) {
-    constexpr bool WIDE = sizeof(T) == 4;
-    if (p.D <= 256) return launch_norm_bwd<T, 32, 1, VEC>(p, dev, parts, s);
-    if (p.D <= 512) return launch_norm_bwd<T, 32, 2, VEC>(p, dev, parts, s);
-    if constexpr (!WIDE)
-        if (p.D <= 1024) return launch_norm_bwd<T, 32, 4, VEC>(p, dev, parts, s);
-    if (p.D <= 2048) return launch_norm_bwd<T, 128, 2, VEC>(p, dev, parts, s);
-    if (p.D <= 4096) return launch_norm_bwd<T, 256, 2, VEC>(p, dev, parts, s);
-    if constexpr (WIDE)
-        return launch_norm_bwd<T, 512, 2, VEC>(p, dev, parts, s);
-    else
-        return launch_norm_bwd<T, 256, 4, VEC>(p, dev, parts, s);
+// Threads a row: a warp while its lanes can hold the row's sums (up to 24
+// columns each; fp32 rows 16, for their slots), above that as few as hold them
+// in 16 columns each.
+template <class T, bool VEC, bool EDGES>
+static int norm_bwd_by_size(const NormBwdParams& p, int64_t same, int dev, int64_t* parts, cudaStream_t s) {
+    const int64_t D = p.D + (VEC && EDGES ? 8 : 0);  // its place in the first piece
+    if (D <= 256) return launch_norm_bwd<T, 32, 1, VEC, EDGES>(p, same, dev, parts, s);
+    if (D <= 512) return launch_norm_bwd<T, 32, 2, VEC, EDGES>(p, same, dev, parts, s);
+    if constexpr (VEC && sizeof(T) == 2)
+        if (D <= 768) return launch_norm_bwd<T, 32, 3, VEC, EDGES>(p, same, dev, parts, s);
+    if (D <= 1024) return launch_norm_bwd<T, 128, 1, VEC, EDGES>(p, same, dev, parts, s);
+    if (D <= 2048) return launch_norm_bwd<T, 128, 2, VEC, EDGES>(p, same, dev, parts, s);
+    if (D <= 4096) return launch_norm_bwd<T, 256, 2, VEC, EDGES>(p, same, dev, parts, s);
+    return launch_norm_bwd<T, 512, 2, VEC, EDGES>(p, same, dev, parts, s);
 }
 
 template <class T>
@@ -377,9 +455,19 @@ static int norm_backward(const NormBwdParams& p, float* dgamma, float* dbeta, in
     int rc = QG_OK;
     if (p.M > 0) {
         if (p.D <= kMaxHeldBwd) {
-            rc = p.x_vec && p.dy_vec && p.dx_vec && p.w_vec && p.D % 8 == 0
-                     ? norm_bwd_by_size<T, true>(p, dev, &parts, s)
-                     : norm_bwd_by_size<T, false>(p, dev, &parts, s);
+            // do rows of x, dy and dx start at the same places?
+            const uintptr_t x = reinterpret_cast<uintptr_t>(p.X) % 16;
+            const size_t lx = static_cast<size_t>(p.ldx) * sizeof(T) % 16;
+            const bool alike = reinterpret_cast<uintptr_t>(p.dY) % 16 == x && reinterpret_cast<uintptr_t>(p.dX) % 16 == x &&
+                               (p.M == 1 || (static_cast<size_t>(p.lddy) * sizeof(T) % 16 == lx &&
+                                             static_cast<size_t>(p.lddx) * sizeof(T) % 16 == lx));
+            const bool edges = lx || x || p.D % 8;
+            if (alike && !edges)
+                rc = norm_bwd_by_size<T, true, false>(p, 1, dev, &parts, s);
+            else if (alike && p.D + 8 <= kMaxHeldBwd)
+                rc = norm_bwd_by_size<T, true, true>(p, same_place_rows(p.ldx, sizeof(T)), dev, &parts, s);
+            else
+                rc = norm_bwd_by_size<T, false, false>(p, 1, dev, &parts, s);
         } else {
             rc = launch_serialized(k_layer_norm_backward_long<T>, dim3(static_cast<unsigned>(p.M)), kLongThreads, 0,
                                    1, s, p);
@@ -407,17 +495,18 @@ static int bwd_smem_most(int tpr, int vpt, size_t elem, bool vec) {
     return static_cast<int>(bwd_smem(tpr, vpt, int64_t(tpr) * vpt * 8, elem, vec, &slots));
 }
 
-#define QG_NORM_BWD(T, NAME, TPR, VPT, VEC)                                                            \
-    QG_BLOCK_KERNEL_BUDGET("k_layer_norm_backward<" NAME "," #TPR "," #VPT "," #VEC ">",               \
-                           (reinterpret_cast<const void*>(k_layer_norm_backward<T, TPR, VPT, VEC>)),   \
+#define QG_NORM_BWD(T, NAME, TPR, VPT, VEC, EDGES)                                                     \
+    QG_BLOCK_KERNEL_BUDGET("k_layer_norm_backward<" NAME "," #TPR "," #VPT "," #VEC "," #EDGES ">",    \
+                           (reinterpret_cast<const void*>(k_layer_norm_backward<T, TPR, VPT, VEC, EDGES>)), \
                            kBwdThreads, bwd_smem_most(TPR, VPT, sizeof(T), VEC), 0, 1, 1)
-#define QG_NORM_BWD_SIZES(T, NAME, VEC)                                                                \
-    QG_NORM_BWD(T, NAME, 32, 1, VEC); QG_NORM_BWD(T, NAME, 32, 2, VEC);                                \
-    QG_NORM_BWD(T, NAME, 128, 2, VEC); QG_NORM_BWD(T, NAME, 256, 2, VEC)
-#define QG_NORM_BWD_16(T, NAME, VEC) QG_NORM_BWD(T, NAME, 32, 4, VEC); QG_NORM_BWD(T, NAME, 256, 4, VEC)
+#define QG_NORM_BWD_SIZES(T, NAME, VEC, EDGES)                                                         \
+    QG_NORM_BWD(T, NAME, 32, 1, VEC, EDGES); QG_NORM_BWD(T, NAME, 32, 2, VEC, EDGES);                  \
+    QG_NORM_BWD(T, NAME, 128, 1, VEC, EDGES); QG_NORM_BWD(T, NAME, 128, 2, VEC, EDGES);                \
+    QG_NORM_BWD(T, NAME, 256, 2, VEC, EDGES); QG_NORM_BWD(T, NAME, 512, 2, VEC, EDGES)
 #define QG_NORM_BWD_BUDGETS(T, NAME)                                                                       \
-    QG_NORM_BWD_SIZES(T, NAME, true);                                                                      \
-    QG_NORM_BWD_SIZES(T, NAME, false);                                                                     \
+    QG_NORM_BWD_SIZES(T, NAME, true, false);                                                               \
+    QG_NORM_BWD_SIZES(T, NAME, true, true);                                                                \
+    QG_NORM_BWD_SIZES(T, NAME, false, false);                                                              \
     QG_BLOCK_KERNEL_BUDGET("k_layer_norm_backward_long<" NAME ">",                                         \
                            reinterpret_cast<const void*>(k_layer_norm_backward_long<T>), kLongThreads, 0, 0, 1, 1); \
     QG_BLOCK_KERNEL_BUDGET("k_layer_norm_columns<" NAME ">",                                               \
@@ -425,12 +514,10 @@ static int bwd_smem_most(int tpr, int vpt, size_t elem, bool vec) {
 QG_NORM_BWD_BUDGETS(__half, "f16");
 QG_NORM_BWD_BUDGETS(__nv_bfloat16, "bf16");
 QG_NORM_BWD_BUDGETS(float, "f32");
-QG_NORM_BWD_16(__half, "f16", true);
-QG_NORM_BWD_16(__half, "f16", false);
-QG_NORM_BWD_16(__nv_bfloat16, "bf16", true);
-QG_NORM_BWD_16(__nv_bfloat16, "bf16", false);
-QG_NORM_BWD(float, "f32", 512, 2, true);
-QG_NORM_BWD(float, "f32", 512, 2, false);
+QG_NORM_BWD(__half, "f16", 32, 3, true, false);
+QG_NORM_BWD(__half, "f16", 32, 3, true, true);
+QG_NORM_BWD(__nv_bfloat16, "bf16", 32, 3, true, false);
+QG_NORM_BWD(__nv_bfloat16, "bf16", 32, 3, true, true);
 QG_BLOCK_KERNEL_BUDGET("k_sum_partials", reinterpret_cast<const void*>(k_sum_partials), kSumCols* kSumSlices, 0, 0,
                        1, 4);
 
