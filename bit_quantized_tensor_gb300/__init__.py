@@ -112,6 +112,7 @@ SIGNATURES = {
     "qg_block_kernel_budget_get": (_int, [_int, ctypes.POINTER(KernelBudgetC)]),
     "qg_block_kernel_budget_measure": (_int, [_int, ctypes.POINTER(_int), ctypes.POINTER(_int),
                                               ctypes.POINTER(_int)]),
+    "qg_set_fp4_path": (_int, [_int, _int]),
     "qg_fp4_codes_ld": (_i64, [_i64]),
     "qg_fp4_scale_bytes": (_sz, [_int, _i64, _i64]),
     "fp4_tensor_scale": (_int, [_int, _i64, _i64, _p, _i64, _p, _p, _sz, _p]),

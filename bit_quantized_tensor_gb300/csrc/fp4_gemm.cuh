@@ -6,6 +6,8 @@
 // needs the scales of its rows in tensor memory too, which tcgen05.cp brings
 // there from shared memory in the layout that the packed scales already have.
 #pragma once
+#include <type_traits>
+
 #include "fp4_common.cuh"
 #include "qg_gemm_host.h"
 #include "qg_ptx.cuh"
@@ -106,10 +108,18 @@ __device__ __forceinline__ uint64_t fp4_scale_desc(uint32_t smem_addr) {
 //
 // The weights' rows are the 128 rows of the MMA and the tokens its NT columns,
 // so that few tokens waste few columns and the weights, which are what a small
-// batch has to read, move in whole 16 KB boxes.  A cluster of S CTAs splits K
-// and joins the fp32 sums through distributed shared memory, in rank order.
+// batch has to read, move in whole 16 KB boxes.  Tiles of fewer than 128 tokens
+// hold all tokens (M <= NT): scales start at a multiple of four columns of
+// tensor memory, so a tile cannot begin inside 128 scale rows.  A cluster of S CTAs splits K:
+// each CTA sends its fp32 sums of a column to the CTA that owns the column,
+// which adds them up in rank order.
 //   warp 4  TMA producer      warp 5  MMA issuer, owner of the tensor memory
-//   warps 0-3  epilogue (their lane quarter of the accumulator)
+//   warps 0-3  epilogue (their lane quarter of the accumulator); with QUANT
+//              they first quantize the tokens' values of the CTA's K range into
+//              the ring themselves, which spares a small batch a kernel
+// With few tokens nothing but latency counts: the ring takes less than half an
+// SM's shared memory, so that a call's CTAs can set up and fetch their weights
+// while those of the call before it finish.
 constexpr int kFp4Threads = 192;
 constexpr int kFp4Bk = 256;  // K of a stage: one 128-byte swizzled row of codes
 
@@ -120,20 +130,21 @@ struct Fp4Cfg {
     static constexpr int A_BYTES = 128 * 128;
     static constexpr int B_BYTES = NT * 128;
     static constexpr int S_BYTES = ATOMS * 512;                 // scales of 128 rows
-    static constexpr int B_ALLOC = B_BYTES < 1024 ? 1024 : B_BYTES;  // swizzle atoms of 1 KB
-    static constexpr int STAGE_BYTES = A_BYTES + B_ALLOC + 2 * S_BYTES;
-    static constexpr int TX_BYTES = A_BYTES + B_BYTES + 2 * S_BYTES;
-    static constexpr int STAGES = NT >= 128 ? 5 : 8;
+    static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 2 * S_BYTES;
+    static constexpr int W_BYTES = A_BYTES + S_BYTES;           // of a stage, the weights' part
+    static constexpr int STAGES = 4;
     static constexpr int BARRIER_BYTES = 256;
+    static constexpr int JOIN_BYTES = NT * 128 * 4;             // sums from the cluster (S > 1)
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BARRIER_BYTES + 1024;
+    static constexpr int SMEM_JOIN_BYTES = SMEM_BYTES + JOIN_BYTES;
     static constexpr int SFA_COL = NT;                          // D at column 0
     static constexpr int SFB_COL = NT + 4 * ATOMS;
     static constexpr int COLS_USED = NT + 8 * ATOMS;
     static constexpr int TMEM_COLS = COLS_USED <= 64 ? 64 : COLS_USED <= 128 ? 128 : 256;
     static_assert(NT % 16 == 0 && NT <= 128, "MMA columns");
     static_assert(COLS_USED <= TMEM_COLS, "tensor memory");
-    static_assert(SMEM_BYTES <= 232448, "shared memory");
-    static_assert(128 * NT * 4 <= STAGES * STAGE_BYTES, "the joined sums reuse the ring");
+    static_assert(SMEM_JOIN_BYTES <= 232448, "shared memory");
+    static_assert(STAGE_BYTES % 1024 == 0, "swizzle atoms of 1 KB");
 };
 
 struct Fp4Params {
@@ -144,14 +155,17 @@ struct Fp4Params {
     int64_t ldy;
     int dtype;           // of Y and bias
     bool weights_ready;  // the weights were complete before the kernel ahead on the stream started
+    const void* X;       // QUANT: the tokens' values
+    int64_t ldx;
+    bool x_aligned;
     Ctl ctl;
 };
 
 constexpr int kSiteFp4Empty = 301;
 constexpr int kSiteFp4Full = 302;
 constexpr int kSiteFp4Acc = 303;
-constexpr int kSiteFp4DrainTma = 304;
-constexpr int kSiteFp4DrainMma = 305;
+constexpr int kSiteFp4Quant = 304;
+constexpr int kSiteFp4Join = 305;
 
 __device__ __forceinline__ float fp4_alpha(const Fp4Params& p) {
     return (p.ts_a ? *p.ts_a : 1.f) * (p.ts_b ? *p.ts_b : 1.f);
@@ -171,12 +185,26 @@ __device__ __forceinline__ void typed_store(void* v, int dtype, int64_t i, float
         static_cast<float*>(v)[i] = x;
 }
 
-template <class Cfg>
+// The two halves of cluster_sync.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Waits, bounded, until `bar` has completed phase `parity`, whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag, const Ctl& ctl,
+                                          int site) {
+    return __all_sync(0xffffffffu, bounded_wait(bar, parity, abort_flag, ctl, site));
+}
+
+// QUANT: the type of the tokens' values, or void with packed tokens.
+template <class Cfg, class QUANT>
 __global__ void __launch_bounds__(kFp4Threads, 1)
     fp4_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const __grid_constant__ CUtensorMap tmSW, const __grid_constant__ CUtensorMap tmSX,
                     const Fp4Params p) {
     constexpr int NT = Cfg::NT, STAGES = Cfg::STAGES, FMT = Cfg::FMT;
+    constexpr bool Q = !std::is_void<QUANT>::value;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
@@ -186,8 +214,10 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
     const uint32_t acc_bar = bar0 + 8u * (2 * STAGES);
-    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 1);
+    const uint32_t join_bar = acc_bar + 8u;  // the cluster's sums of this CTA's columns have arrived
+    uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    float* const join = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE_BYTES + Cfg::BARRIER_BYTES);
     auto a_smem = [&](int s) { return smem_u32(smem + s * Cfg::STAGE_BYTES); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -197,46 +227,58 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const int num_kb = (p.K + kFp4Bk - 1) / kFp4Bk;
     const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * split / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (split + 1) / splits);
+    const int cols = min(NT, p.M - m0);  // tokens of this tile
+    const int per = (cols + splits - 1) / splits;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(full_bar(s), 1);
+            mbar_init(full_bar(s), Q ? 1 + 4 : 1);  // the producer, and the quantizing warps
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(acc_bar, 1);
+        mbar_init(join_bar, 1);
         *abort_flag = 0;
         fence_mbar_init();
+        // column c belongs to CTA c / per, which gets its sums from every CTA
+        if (splits > 1) mbar_arrive_expect_tx(join_bar, splits * max(0, min(cols - split * per, per)) * 512);
+    }
+    if (threadIdx.x == 128) {
         tma_prefetch_desc(&tmW);
-        tma_prefetch_desc(&tmX);
         tma_prefetch_desc(&tmSW);
-        tma_prefetch_desc(&tmSX);
+        if constexpr (!Q) {
+            tma_prefetch_desc(&tmX);
+            tma_prefetch_desc(&tmSX);
+        }
     }
     if (warp == 5) tmem_alloc(smem_u32(tmem_holder), Cfg::TMEM_COLS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    if (splits > 1) cluster_arrive();  // this CTA runs: its shared memory may be written (awaited below)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);  // known to be uniform
 
+    bool ok = true;
     // The bounded waits below start only when the previous kernel is done (they
     // must not count its time); the producer alone may run ahead of that.
     if (warp != 4) pdl_wait_prior_grid();
-    bool ok = true;
     if (warp == 4) {
         const uint32_t elected = elect_lane();
         const int tiles_k = static_cast<int>(fp4_col_tiles(FMT, p.K));
         auto arm = [&](int s) {
-            if (elected) mbar_arrive_expect_tx(full_bar(s), Cfg::TX_BYTES);
+            if (elected) mbar_arrive_expect_tx(full_bar(s), Q ? Cfg::W_BYTES : Cfg::STAGE_BYTES);
             __syncwarp();
         };
         auto load_w = [&](int kb, int s) {
             fp4_load(a_smem(s), &tmW, kb * (kFp4Bk / 2), n0, full_bar(s), elected);
-            fp4_load(a_smem(s) + Cfg::A_BYTES + Cfg::B_ALLOC, &tmSW, 0, (n0 >> 7) * tiles_k + kb * Cfg::ATOMS,
+            fp4_load(a_smem(s) + Cfg::A_BYTES + Cfg::B_BYTES, &tmSW, 0, (n0 >> 7) * tiles_k + kb * Cfg::ATOMS,
                      full_bar(s), elected);
         };
         auto load_x = [&](int kb, int s) {
-            fp4_load(a_smem(s) + Cfg::A_BYTES, &tmX, kb * (kFp4Bk / 2), m0, full_bar(s), elected);
-            fp4_load(a_smem(s) + Cfg::A_BYTES + Cfg::B_ALLOC + Cfg::S_BYTES, &tmSX, 0,
-                     (m0 >> 7) * tiles_k + kb * Cfg::ATOMS, full_bar(s), elected);
+            if constexpr (!Q) {
+                fp4_load(a_smem(s) + Cfg::A_BYTES, &tmX, kb * (kFp4Bk / 2), m0, full_bar(s), elected);
+                fp4_load(a_smem(s) + Cfg::A_BYTES + Cfg::B_BYTES + Cfg::S_BYTES, &tmSX, 0,
+                         (m0 >> 7) * tiles_k + kb * Cfg::ATOMS, full_bar(s), elected);
+            }
         };
         // Weights that were complete before the previous kernel began may
         // be fetched while that kernel (which makes the tokens' codes) runs.
@@ -251,9 +293,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         Ring<STAGES> ps;
         for (int i = 0; i < ahead; ++i) ps.next();
         for (int kb = kb0 + ahead; kb < kb1; ++kb) {
-            if (!__all_sync(0xffffffffu, bounded_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl,
-                                                      kSiteFp4Empty)))
-                break;
+            if (!warp_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl, kSiteFp4Empty)) break;
             arm(ps.slot());
             load_w(kb, ps.slot());
             load_x(kb, ps.slot());
@@ -262,17 +302,15 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     } else if (warp == 5) {
         const uint32_t elected = elect_lane();
         Ring<STAGES> ps;
-        const uint32_t sfb_shift = static_cast<uint32_t>((m0 & 127) >> 5);  // tile inside its 128 scale rows
         for (int kb = kb0; kb < kb1; ++kb) {
-            if (!__all_sync(0xffffffffu,
-                            bounded_wait(full_bar(ps.slot()), ps.parity(), abort_flag, p.ctl, kSiteFp4Full))) {
+            if (!warp_wait(full_bar(ps.slot()), ps.parity(), abort_flag, p.ctl, kSiteFp4Full)) {
                 ok = false;
                 break;
             }
             tc_fence_after();
             const int steps = min(4, (p.K - kb * kFp4Bk + 63) / 64);  // none behind K: its scales may be stale
             const uint32_t a = a_smem(ps.slot()), b = a + Cfg::A_BYTES;
-            const uint32_t sa = b + Cfg::B_ALLOC, sb = sa + Cfg::S_BYTES;
+            const uint32_t sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
             const int atoms = FMT == kNv ? steps : (steps + 1) / 2;
 #pragma unroll
             for (int j = 0; j < Cfg::ATOMS; ++j) {
@@ -287,7 +325,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 const uint32_t id = FMT == kNv ? 0u : 2u * (j & 1);
                 fp4_mma<FMT, false>(tmem, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
                                     fp4_idesc<FMT>(128, NT, id), tmem + Cfg::SFA_COL + col,
-                                    tmem + Cfg::SFB_COL + col + sfb_shift, (kb > kb0 || j > 0) ? 1u : 0u, elected);
+                                    tmem + Cfg::SFB_COL + col, (kb > kb0 || j > 0) ? 1u : 0u, elected);
             }
             if (elected) tc_commit(empty_bar(ps.slot()));
             __syncwarp();
@@ -295,10 +333,43 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         }
         if (elected) tc_commit(acc_bar);
         __syncwarp();
+    } else if constexpr (Q) {
+        // the tokens' codes and scales of the CTA's K range, block by block, in
+        // the places where TMA would put them: 128-byte rows, 16-byte pieces
+        // exchanged by the row's low three bits; scales as in memory
+        constexpr int B = fp4_block(FMT), BLOCKS = kFp4Bk / B;
+        const float ts = FMT == kNv && p.ts_a ? *p.ts_a : 1.f;
+        const float six_ts = __fmul_rn(6.f, ts);
+        Ring<STAGES> ps;
+        for (int kb = kb0; kb < kb1; ++kb) {
+            if (!warp_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl, kSiteFp4Quant)) break;
+            uint8_t* const codes_at = smem + ps.slot() * Cfg::STAGE_BYTES + Cfg::A_BYTES;
+            uint8_t* const scales_at = codes_at + Cfg::B_BYTES + Cfg::S_BYTES;
+            for (int i = threadIdx.x; i < cols * BLOCKS; i += 128) {
+                const int m = i / BLOCKS, blk = i % BLOCKS;
+                const int k = kb * kFp4Bk + blk * B;
+                float x[B];
+                uint32_t codes[B / 8];
+                load_some<QUANT, B>(static_cast<const QUANT*>(p.X) + (m0 + m) * p.ldx + k, min(p.K - k, B), p.x_aligned, x);
+                const uint32_t byte = quantize_block<FMT>(x, ts, six_ts, codes);
+                uint8_t* const row = codes_at + m * 128;
+                if constexpr (B == 16)
+                    *reinterpret_cast<uint2*>(row + (((blk >> 1) ^ (m & 7)) << 4) + 8 * (blk & 1)) =
+                        make_uint2(codes[0], codes[1]);
+                else
+                    *reinterpret_cast<uint4*>(row + ((blk ^ (m & 7)) << 4)) =
+                        make_uint4(codes[0], codes[1], codes[2], codes[3]);
+                scales_at[(blk >> 2) * 512 + (m & 31) * 16 + (m >> 5) * 4 + (blk & 3)] = static_cast<uint8_t>(byte);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full_bar(ps.slot()));
+            ps.next();
+        }
     }
-    if (warp == 4) pdl_wait_prior_grid();
     // Everyone waits for the accumulator: warps 0-3 read it, the others must
     // not leave (or let the ring be reused) before the MMAs and copies end.
+    if (warp == 4) pdl_wait_prior_grid();
     if (!bounded_wait(acc_bar, 0u, nullptr, p.ctl, kSiteFp4Acc)) ok = false;
     if (warp == 4 && lane == 0 && *abort_flag) {
         // copies may still be in flight: give them a fixed time to land
@@ -311,65 +382,64 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     const bool good = __syncthreads_and(ok && !*abort_flag);
     const float alpha = fp4_alpha(p);
     const bool empty = kb1 == kb0;
+    const int n = n0 + warp * 32 + lane;
+    const float bias = warp < 4 && p.bias && n < p.N ? typed_at(p.bias, p.dtype, n) : 0.f;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
 
     if (splits == 1) {
         if (warp < 4 && good) {
-            const int n = n0 + warp * 32 + lane;
-            const float bias = p.bias && n < p.N ? typed_at(p.bias, p.dtype, n) : 0.f;
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = 0; c < cols; c += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(taddr + c, r);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const int m = m0 + c + i;
                     const float acc = empty ? 0.f : __uint_as_float(r[i]);
-                    if (n < p.N && m < p.M)
-                        typed_store(p.Y, p.dtype, m * p.ldy + n, fmaf(acc, alpha, bias));
+                    if (n < p.N && c + i < cols)
+                        typed_store(p.Y, p.dtype, (m0 + c + i) * p.ldy + n, fmaf(acc, alpha, bias));
                 }
             }
         }
         tc_fence_before();
         __syncthreads();
     } else {
-        // fp32 sums to shared memory (the ring is idle), column by column
-        float* red = reinterpret_cast<float*>(smem);
+        // fp32 sums, column by column, over the idle ring; then each owner's
+        // columns in one copy to join[rank][column][row] there
+        float* const sums = reinterpret_cast<float*>(smem);
         if (warp < 4) {
-            const uint32_t taddr = tmem + (static_cast<uint32_t>(warp * 32) << 16);
 #pragma unroll 1
-            for (int c = 0; c < NT; c += 16) {
+            for (int c = 0; c < cols; c += 16) {
                 uint32_t r[16];
                 tmem_ld_32x32b_x16(taddr + c, r);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) red[(c + i) * 128 + warp * 32 + lane] = __uint_as_float(r[i]);
+                for (int i = 0; i < 16; ++i)
+                    if (c + i < cols) sums[(c + i) * 128 + warp * 32 + lane] = __uint_as_float(r[i]);
             }
+            fence_proxy_async_smem();
         }
         tc_fence_before();
         __syncthreads();
-        cluster_sync();
-        const int per = (NT + splits - 1) / splits;
-        const int c1 = min(NT, (split + 1) * per);
-        const uint32_t red0 = smem_u32(red);
-        if (warp < 4) {
-            const int n = n0 + threadIdx.x;
-            const float bias = p.bias && n < p.N ? typed_at(p.bias, p.dtype, n) : 0.f;
-            for (int c = split * per; c < c1; ++c) {
-                if (m0 + c >= p.M) break;
-                float acc = 0.f;
-                for (int s = 0; s < splits; ++s) {
-                    float v;
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                 : "=f"(v)
-                                 : "r"(mapa_shared(red0 + 4u * (c * 128 + threadIdx.x), s)));
-                    acc += v;
-                }
-                if (good && n < p.N) typed_store(p.Y, p.dtype, (m0 + c) * p.ldy + n, fmaf(acc, alpha, bias));
-            }
+        cluster_wait();  // every CTA of the cluster runs and has armed its barrier
+        if (threadIdx.x < splits) {
+            const int owner = threadIdx.x, mine = min(cols - owner * per, per);
+            if (mine > 0)
+                bulk_copy_s2s_cluster(mapa_shared(smem_u32(join) + 512u * (split * per), owner),
+                                      smem_u32(sums) + 512u * (owner * per), 512u * mine, mapa_shared(join_bar, owner));
         }
-        cluster_sync();  // nobody leaves while its sums may still be read
+        __syncwarp();
+        const int c1 = min(cols, (split + 1) * per);
+        if (warp < 4 && split * per < cols) {
+            const bool joined = warp_wait(join_bar, 0u, nullptr, p.ctl, kSiteFp4Join);
+            if (good && joined && n < p.N)
+                for (int c = split * per; c < c1; ++c) {
+                    float acc = 0.f;
+                    for (int s = 0; s < splits; ++s) acc += join[(s * per + c - split * per) * 128 + threadIdx.x];
+                    typed_store(p.Y, p.dtype, (m0 + c) * p.ldy + n, fmaf(acc, alpha, bias));
+                }
+        }
+        cluster_sync();  // nobody leaves while its sums may still be on their way
     }
     if (warp == 5) {
         __syncwarp();

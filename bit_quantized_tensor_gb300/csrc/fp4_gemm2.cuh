@@ -25,12 +25,13 @@ struct Fp4PairCfg {
     static constexpr int S_BYTES = ATOMS * 512;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES + 3 * S_BYTES;
     static constexpr int BARRIER_BYTES = 256;
-    static constexpr int STAGES = (232448 - BARRIER_BYTES - 1024) / STAGE_BYTES;
-    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BARRIER_BYTES + 1024;
+    static constexpr int EPI_WARPS = 8;
+    static constexpr int OUT_BYTES = EPI_WARPS * 2048;  // 32 rows x 16 columns a warp, see fp4_store_rows
+    static constexpr int STAGES = (232448 - BARRIER_BYTES - OUT_BYTES - 1024) / STAGE_BYTES;
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + BARRIER_BYTES + OUT_BYTES + 1024;
     static constexpr int ACC_STEP = 208;              // first column of accumulator 1
     static constexpr int SHARED_COLS = 256 - ACC_STEP;
     static constexpr int SFA_COL = ACC_STEP + 256, SFB_COL = SFA_COL + 4 * ATOMS;
-    static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 32 * (2 + EPI_WARPS);
     static_assert(SFB_COL + 8 * ATOMS <= 512, "tensor memory");
     static_assert(STAGES >= 4 && SMEM_BYTES <= 232448 && 2 * SMEM_BYTES > 233472, "shared memory, one CTA per SM");
@@ -44,30 +45,65 @@ constexpr int kSiteFp4PairEpi = 314;
 constexpr int kSiteFp4PairDrainTma = 315;
 constexpr int kSiteFp4PairDrainMma = 316;
 
-// 16 values of a row to Y, whole 32-byte sectors where alignment allows.
+// 16 values of a row to Y in whole 32-byte sectors (dst 32-byte aligned).
 template <class T>
-__device__ __forceinline__ void fp4_store16(T* dst, int left, const float (&f)[16]) {
-    if (left >= 16 && (reinterpret_cast<uintptr_t>(dst) & 31u) == 0) {
-        if constexpr (sizeof(T) == 2) {
-            uint4 a = make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7]));
-            uint4 b = make_uint4(pack2<T>(f[8], f[9]), pack2<T>(f[10], f[11]), pack2<T>(f[12], f[13]),
-                                 pack2<T>(f[14], f[15]));
-            st_global_32(dst, a, b, false);
-        } else {
-#pragma unroll
-            for (int h = 0; h < 16; h += 8)
-                st_global_32(dst + h,
-                             make_uint4(__float_as_uint(f[h]), __float_as_uint(f[h + 1]), __float_as_uint(f[h + 2]),
-                                        __float_as_uint(f[h + 3])),
-                             make_uint4(__float_as_uint(f[h + 4]), __float_as_uint(f[h + 5]),
-                                        __float_as_uint(f[h + 6]), __float_as_uint(f[h + 7])),
-                             false);
-        }
+__device__ __forceinline__ void fp4_store16(T* dst, const float (&f)[16]) {
+    if constexpr (sizeof(T) == 2) {
+        st_global_32(dst,
+                     make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])),
+                     make_uint4(pack2<T>(f[8], f[9]), pack2<T>(f[10], f[11]), pack2<T>(f[12], f[13]),
+                                pack2<T>(f[14], f[15])),
+                     false);
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            if (i < left) dst[i] = from_f32<T>(f[i]);
+        for (int h = 0; h < 16; h += 8)
+            st_global_32(dst + h,
+                         make_uint4(__float_as_uint(f[h]), __float_as_uint(f[h + 1]), __float_as_uint(f[h + 2]),
+                                    __float_as_uint(f[h + 3])),
+                         make_uint4(__float_as_uint(f[h + 4]), __float_as_uint(f[h + 5]), __float_as_uint(f[h + 6]),
+                                    __float_as_uint(f[h + 7])),
+                         false);
     }
+}
+
+// 32 rows x 16 columns of a warp (lane = row) to Y where rows are not 32-byte
+// aligned or end inside the 16 columns: turned in shared memory, so that
+// neighbouring lanes store neighbouring words of a row.  One value a lane and
+// store instead (32 rows an instruction) took 36 us for 777 x 1001 x 2304.
+// `buf`: 512 words of the warp; 16-byte pieces are exchanged by the row, which
+// keeps both directions free of bank conflicts.
+template <class T>
+__device__ __forceinline__ void fp4_store_rows(uint8_t* buf, const float (&f)[16], T* Y, int64_t ldy, int row0, int M,
+                                               int col, int N) {
+    constexpr int RB = 16 * static_cast<int>(sizeof(T)), PIECES = RB / 16;
+    const int lane = threadIdx.x & 31;
+    auto turn = [](int r) { return PIECES == 4 ? (r >> 1) & 3 : (r >> 2) & 1; };
+    float g[16 / PIECES];
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) {
+#pragma unroll
+        for (int j = 0; j < 16 / PIECES; ++j) g[j] = f[q * (16 / PIECES) + j];
+        store_vec<T, 16 / PIECES>(reinterpret_cast<T*>(buf + lane * RB + ((q ^ turn(lane)) << 4)), g);
+    }
+    __syncwarp();
+    constexpr int WORDS = RB / 4, PER = 4 / static_cast<int>(sizeof(T));  // words a row, values a word
+    const int w = lane % WORDS, c = col + w * PER;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+        const int r = i * (32 / WORDS) + lane / WORDS;
+        const uint32_t v = *reinterpret_cast<const uint32_t*>(buf + r * RB + (((w >> 2) ^ turn(r)) << 4) + (w & 3) * 4);
+        if (row0 + r >= M || c >= N) continue;
+        T* dst = Y + (row0 + r) * ldy + c;
+        if constexpr (sizeof(T) == 4) {
+            *reinterpret_cast<uint32_t*>(dst) = v;
+        } else if (c + 1 < N && (reinterpret_cast<uintptr_t>(dst) & 3) == 0) {
+            *reinterpret_cast<uint32_t*>(dst) = v;
+        } else {
+            reinterpret_cast<uint16_t*>(dst)[0] = static_cast<uint16_t>(v);
+            if (c + 1 < N) reinterpret_cast<uint16_t*>(dst)[1] = static_cast<uint16_t>(v >> 16);
+        }
+    }
+    __syncwarp();
 }
 
 template <class Cfg>
@@ -89,6 +125,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 3);
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+    uint8_t* const out_smem = smem + STAGES * Cfg::STAGE_BYTES + Cfg::BARRIER_BYTES;
     auto stage_smem = [&](int s) { return smem_u32(smem + s * Cfg::STAGE_BYTES); };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -233,11 +270,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         const int quad = warp & 3, half = (warp - 2) >> 2;
         const float alpha = fp4_alpha(p);
         const uint32_t next = mapa_shared(next_bar, 0);
+        uint8_t* const buf = out_smem + (warp - 2) * 2048;
+        const bool sectors = (reinterpret_cast<uintptr_t>(p.Y) & 31) == 0 &&
+                             (p.ldy * (p.dtype == QG_F32 ? 4 : 2)) % 32 == 0;
+        auto put = [&](auto* Y, const float(&f)[16], int row0, int col) {
+            if (sectors && col + 16 <= p.N) {
+                if (row0 + lane < p.M) fp4_store16(Y + (row0 + lane) * p.ldy + col, f);
+            } else {
+                fp4_store_rows(buf, f, Y, p.ldy, row0, p.M, col, p.N);
+            }
+        };
         int n = 0;
         for (int t = pair; t < ntiles; t += npairs, ++n) {
             int mb, nb;
             tile_coords(t, num_m, num_n, mb, nb, kGroupMPairs);
-            const int row = mb * 256 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+            const int row0 = mb * 256 + static_cast<int>(rank) * 128 + quad * 32;
             const bool got = bounded_wait(accf_bar(n & 1), (n >> 1) & 1u, abort_flag, p.ctl, kSiteFp4PairEpi);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
@@ -261,7 +308,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 tmem_wait_ld();
                 if (sharing && i == Cfg::SHARED_COLS / 16 - 1) release();
                 const int col = nb * 256 + c;
-                if (row >= p.M || col >= p.N) continue;
+                if (row0 >= p.M || col >= p.N) continue;
                 float f[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha;
@@ -270,13 +317,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     for (int j = 0; j < 16; ++j)
                         if (col + j < p.N) f[j] += typed_at(p.bias, p.dtype, col + j);
                 }
-                const int64_t at = row * p.ldy + col;
                 if (p.dtype == QG_F16)
-                    fp4_store16(static_cast<__half*>(p.Y) + at, p.N - col, f);
+                    put(static_cast<__half*>(p.Y), f, row0, col);
                 else if (p.dtype == QG_BF16)
-                    fp4_store16(static_cast<__nv_bfloat16*>(p.Y) + at, p.N - col, f);
+                    put(static_cast<__nv_bfloat16*>(p.Y), f, row0, col);
                 else
-                    fp4_store16(static_cast<float*>(p.Y) + at, p.N - col, f);
+                    put(static_cast<float*>(p.Y), f, row0, col);
             }
         }
     }

@@ -2,6 +2,7 @@
 // (activations quantized in the call) and fp4_linear_backward (gradients of
 // the activations, the weights and the bias).  Kernels: fp4_gemm.cuh
 // (one CTA a tile) and fp4_gemm2.cuh (CTA pairs).
+#include <atomic>
 #include <mutex>
 
 #include "fp4_gemm2.cuh"
@@ -14,17 +15,17 @@ struct Fp4Operand {
     const float* ts;
 };
 
-// Lifts the kernel's dynamic shared-memory limit, once per device.  Cfg keeps
-// the flags of different kernels apart.
-template <class Cfg, class F>
-static int raise_smem(F* kernel) {
+// Lifts the kernel's dynamic shared-memory limit, once per device;
+// each kernel is called with a type of its own as TAG, which keeps its flags.
+template <class TAG, class F>
+static int raise_smem(F* kernel, int bytes) {
     static std::mutex mu;
     static bool done[64] = {};
     const int dev = current_device();
     if (dev < 0 || dev >= 64) return QG_ERR_CUDA;
     std::lock_guard<std::mutex> g(mu);
     if (done[dev]) return QG_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return map_cuda(e);
     done[dev] = true;
     return QG_OK;
@@ -41,20 +42,27 @@ static int scales_map(CUtensorMap* map, const Fp4Operand& o, int fmt, int64_t K,
                         512, 128, atoms, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-template <class Cfg>
+template <class Cfg, class QUANT>
 static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, int splits, cudaStream_t s) {
+    struct Flags {};  // the kernel's own shared-memory flag below
     CUtensorMap tw, tx, tsw, tsx;
     int rc = codes_map(&tw, w, p.K, 128);
-    if (!rc) rc = codes_map(&tx, x, p.K, Cfg::NT);
     if (!rc) rc = scales_map(&tsw, w, Cfg::FMT, p.K, Cfg::ATOMS);
-    if (!rc) rc = scales_map(&tsx, x, Cfg::FMT, p.K, Cfg::ATOMS);
-    if (!rc) rc = raise_smem<Cfg>(fp4_gemm_kernel<Cfg>);
+    if constexpr (std::is_void<QUANT>::value) {
+        if (!rc) rc = codes_map(&tx, x, p.K, Cfg::NT);
+        if (!rc) rc = scales_map(&tsx, x, Cfg::FMT, p.K, Cfg::ATOMS);
+    } else {  // not used
+        tx = tw;
+        tsx = tsw;
+    }
+    if (!rc) rc = raise_smem<Flags>(fp4_gemm_kernel<Cfg, QUANT>, Cfg::SMEM_JOIN_BYTES);
     if (rc) return rc;
     const int64_t gy = (p.N + 127) / 128, gz = (p.M + Cfg::NT - 1) / Cfg::NT;
     if (gy > 65535 || gz > 65535) return QG_ERR_UNSUPPORTED;
-    return launch_serialized(fp4_gemm_kernel<Cfg>,
+    return launch_serialized(fp4_gemm_kernel<Cfg, QUANT>,
                              dim3(static_cast<unsigned>(splits), static_cast<unsigned>(gy), static_cast<unsigned>(gz)),
-                             kFp4Threads, Cfg::SMEM_BYTES, splits, s, tw, tx, tsw, tsx, p);
+                             kFp4Threads, splits > 1 ? Cfg::SMEM_JOIN_BYTES : Cfg::SMEM_BYTES, splits, s, tw, tx, tsw,
+                             tsx, p);
 }
 
 template <class Cfg>
@@ -64,7 +72,7 @@ static int launch_fp4_pair(const Fp4Operand& x, const Fp4Operand& w, const Fp4Pa
     if (!rc) rc = codes_map(&tx, x, p.K, 128);
     if (!rc) rc = scales_map(&tsw, w, Cfg::FMT, p.K, Cfg::ATOMS);
     if (!rc) rc = scales_map(&tsx, x, Cfg::FMT, p.K, Cfg::ATOMS);
-    if (!rc) rc = raise_smem<Cfg>(fp4_gemm2_kernel<Cfg>);
+    if (!rc) rc = raise_smem<Cfg>(fp4_gemm2_kernel<Cfg>, Cfg::SMEM_BYTES);
     if (rc) return rc;
     const int64_t tiles = (int64_t(p.M) + 255) / 256 * ((int64_t(p.N) + 255) / 256);
     if (tiles > INT32_MAX) return QG_ERR_UNSUPPORTED;
@@ -73,39 +81,83 @@ static int launch_fp4_pair(const Fp4Operand& x, const Fp4Operand& w, const Fp4Pa
                              Cfg::THREADS, Cfg::SMEM_BYTES, 1, s, tx, tw, tsx, tsw, p);
 }
 
-// Splits of K over a cluster: doubled while the tiles alone leave half of the
-// SMs without work and each split keeps at least two K blocks.
-static int choose_splits(int64_t tiles, int64_t num_kb, int sms) {
+// How a product is cut (qg_set_fp4_path): 0 by the rule below, else the
+// tokens of a tile (256: CTA pairs) and the splits of K (0: by the rule).
+static std::atomic<int> g_fp4_nt{0}, g_fp4_splits{0};
+
+struct Fp4Plan {
+    int nt, splits;
+};
+
+// Splits of K over a cluster: doubled while the CTAs so far leave SMs with room
+// (two CTAs an SM with 16 tokens a tile) and each split keeps two K blocks.
+static int choose_splits(int64_t tiles, int64_t num_kb, int room) {
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= sms && num_kb >= 4 * s) s *= 2;
+    while (s < 8 && tiles * s * 2 <= room && num_kb >= 4 * s) s *= 2;
     return s;
 }
 
+static Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int sms) {
+    Fp4Plan f{g_fp4_nt.load(), g_fp4_splits.load()};
+    if (!f.nt) f.nt = M > 128 && N > 128 && (M > 256 || N > 2048) ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    if (f.nt < M && f.nt < 128) f.nt = 128;  // smaller tiles hold all tokens
+    if (f.nt == 256)
+        f.splits = 1;
+    else if (!f.splits)
+        f.splits = choose_splits((N + 127) / 128 * ((M + f.nt - 1) / f.nt), (K + kFp4Bk - 1) / kFp4Bk,
+                                 f.nt <= 16 ? 2 * sms : sms);
+    if (f.splits > (K + kFp4Bk - 1) / kFp4Bk) f.splits = 1;
+    return f;
+}
+
 template <int FMT>
-static int run_fmt(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, int dev, cudaStream_t s) {
-    if (p.M > 128 && p.N > 128 && (p.M > 256 || p.N > 2048)) return launch_fp4_pair<Fp4PairCfg<FMT>>(x, w, p, dev, s);
-    const int nt = p.M <= 16 ? 16 : p.M <= 32 ? 32 : p.M <= 64 ? 64 : 128;
-    const int64_t tiles = (int64_t(p.N) + 127) / 128 * ((int64_t(p.M) + nt - 1) / nt);
-    const int splits = choose_splits(tiles, (p.K + kFp4Bk - 1) / kFp4Bk, num_sms(dev));
-    switch (nt) {
-        case 16: return launch_fp4<Fp4Cfg<FMT, 16>>(x, w, p, splits, s);
-        case 32: return launch_fp4<Fp4Cfg<FMT, 32>>(x, w, p, splits, s);
-        case 64: return launch_fp4<Fp4Cfg<FMT, 64>>(x, w, p, splits, s);
-        default: return launch_fp4<Fp4Cfg<FMT, 128>>(x, w, p, splits, s);
+static int run_fmt(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, const Fp4Plan& f, int dev,
+                   cudaStream_t s) {
+    switch (f.nt) {
+        case 16: return launch_fp4<Fp4Cfg<FMT, 16>, void>(x, w, p, f.splits, s);
+        case 32: return launch_fp4<Fp4Cfg<FMT, 32>, void>(x, w, p, f.splits, s);
+        case 64: return launch_fp4<Fp4Cfg<FMT, 64>, void>(x, w, p, f.splits, s);
+        case 128: return launch_fp4<Fp4Cfg<FMT, 128>, void>(x, w, p, f.splits, s);
+        default: return launch_fp4_pair<Fp4PairCfg<FMT>>(x, w, p, dev, s);
     }
+}
+
+static Fp4Params fp4_params(int dtype, int64_t M, int64_t N, int64_t K, const Fp4Operand& x, const Fp4Operand& w,
+                            const void* bias, void* Y, int64_t ldy, bool weights_ready, int dev) {
+    Fp4Params p = {};
+    p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K);
+    p.ts_a = x.ts; p.ts_b = w.ts; p.bias = bias; p.Y = Y; p.ldy = ldy; p.dtype = dtype;
+    p.weights_ready = weights_ready;
+    p.ctl = host_ctl(dev);
+    return p;
 }
 
 // Y (M x N) = alpha X . W^T + bias, K >= 0.
 static int fp4_gemm_run(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const Fp4Operand& x,
                         const Fp4Operand& w, const void* bias, void* Y, int64_t ldy, bool weights_ready, int dev,
                         cudaStream_t s) {
-    Fp4Params p = {};
-    p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K);
-    p.ts_a = x.ts; p.ts_b = w.ts; p.bias = bias; p.Y = Y; p.ldy = ldy; p.dtype = dtype;
-    p.weights_ready = weights_ready;
-    p.ctl = host_ctl(dev);
+    const Fp4Params p = fp4_params(dtype, M, N, K, x, w, bias, Y, ldy, weights_ready, dev);
     if (!p.ctl.status) return QG_ERR_CUDA;
-    return fmt == kNv ? run_fmt<kNv>(x, w, p, dev, s) : run_fmt<kMx>(x, w, p, dev, s);
+    const Fp4Plan f = plan_fp4(M, N, K, num_sms(dev));
+    return fmt == kNv ? run_fmt<kNv>(x, w, p, f, dev, s) : run_fmt<kMx>(x, w, p, f, dev, s);
+}
+
+// The product of up to 16 tokens that are still values: one kernel.
+static int fp4_linear_few(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+                          const float* x_ts, const Fp4Operand& w, const void* bias, void* Y, int64_t ldy, int dev,
+                          cudaStream_t s) {
+    const Fp4Operand x{nullptr, nullptr, M, x_ts};
+    Fp4Params p = fp4_params(dtype, M, N, K, x, w, bias, Y, ldy, false, dev);
+    if (!p.ctl.status) return QG_ERR_CUDA;
+    p.X = X;
+    p.ldx = ldx;
+    p.x_aligned = aligned16(X) && (M <= 1 || static_cast<size_t>(ldx) * dtype_bytes(dtype) % 16 == 0);
+    const Fp4Plan f = plan_fp4(M, N, K, num_sms(dev));
+    return by_dtype(dtype, [&](auto t) {
+        using T = decltype(t);
+        return fmt == kNv ? launch_fp4<Fp4Cfg<kNv, 16>, T>(x, w, p, f.splits, s)
+                          : launch_fp4<Fp4Cfg<kMx, 16>, T>(x, w, p, f.splits, s);
+    });
 }
 
 // Products over nothing: every output is its bias (or 0).
@@ -153,14 +205,18 @@ struct Carver {
     }
 };
 
-#define QG_FP4_GEMM_BUDGET(FMT, FNAME, NT)                                                     \
-    QG_BLOCK_KERNEL_BUDGET("fp4_gemm_kernel<" FNAME "," #NT ">",                               \
-                           (reinterpret_cast<const void*>(fp4_gemm_kernel<Fp4Cfg<FMT, NT>>)),  \
-                           kFp4Threads, (Fp4Cfg<FMT, NT>::SMEM_BYTES), (Fp4Cfg<FMT, NT>::TMEM_COLS), 8, 1)
-QG_FP4_GEMM_BUDGET(kNv, "nv", 16); QG_FP4_GEMM_BUDGET(kNv, "nv", 32);
-QG_FP4_GEMM_BUDGET(kNv, "nv", 64); QG_FP4_GEMM_BUDGET(kNv, "nv", 128);
-QG_FP4_GEMM_BUDGET(kMx, "mx", 16); QG_FP4_GEMM_BUDGET(kMx, "mx", 32);
-QG_FP4_GEMM_BUDGET(kMx, "mx", 64); QG_FP4_GEMM_BUDGET(kMx, "mx", 128);
+#define QG_FP4_GEMM_BUDGET(FMT, FNAME, NT, QUANT, QNAME)                                              \
+    QG_BLOCK_KERNEL_BUDGET("fp4_gemm_kernel<" FNAME "," #NT "," QNAME ">",                            \
+                           (reinterpret_cast<const void*>(fp4_gemm_kernel<Fp4Cfg<FMT, NT>, QUANT>)),  \
+                           kFp4Threads, (Fp4Cfg<FMT, NT>::SMEM_JOIN_BYTES), (Fp4Cfg<FMT, NT>::TMEM_COLS), 8, \
+                           1)
+#define QG_FP4_GEMM_BUDGETS(FMT, FNAME)                                                               \
+    QG_FP4_GEMM_BUDGET(FMT, FNAME, 16, void, "packed"); QG_FP4_GEMM_BUDGET(FMT, FNAME, 32, void, "packed"); \
+    QG_FP4_GEMM_BUDGET(FMT, FNAME, 64, void, "packed"); QG_FP4_GEMM_BUDGET(FMT, FNAME, 128, void, "packed"); \
+    QG_FP4_GEMM_BUDGET(FMT, FNAME, 16, __half, "f16"); QG_FP4_GEMM_BUDGET(FMT, FNAME, 16, float, "f32"); \
+    QG_FP4_GEMM_BUDGET(FMT, FNAME, 16, __nv_bfloat16, "bf16")
+QG_FP4_GEMM_BUDGETS(kNv, "nv");
+QG_FP4_GEMM_BUDGETS(kMx, "mx");
 QG_BLOCK_KERNEL_BUDGET("fp4_gemm2_kernel<nv>", reinterpret_cast<const void*>(fp4_gemm2_kernel<Fp4PairCfg<kNv>>),
                        Fp4PairCfg<kNv>::THREADS, Fp4PairCfg<kNv>::SMEM_BYTES, 512, 2, 1);
 QG_BLOCK_KERNEL_BUDGET("fp4_gemm2_kernel<mx>", reinterpret_cast<const void*>(fp4_gemm2_kernel<Fp4PairCfg<kMx>>),
@@ -185,6 +241,15 @@ static int check_typed(const void* v, int dtype) {
 using namespace qg;
 
 extern "C" {
+
+int qg_set_fp4_path(int tokens, int splits) {
+    if (tokens != 0 && tokens != 16 && tokens != 32 && tokens != 64 && tokens != 128 && tokens != 256)
+        return QG_ERR_INVALID_ARG;
+    if (splits != 0 && splits != 1 && splits != 2 && splits != 4 && splits != 8) return QG_ERR_INVALID_ARG;
+    g_fp4_nt.store(tokens);
+    g_fp4_splits.store(splits);
+    return QG_OK;
+}
 
 int fp4_gemm(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const uint8_t* Aq, const uint8_t* As,
              const float* a_tscale, const uint8_t* Bq, const uint8_t* Bs, const float* b_tscale, const void* bias,
@@ -223,6 +288,8 @@ int fp4_linear(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const void* 
     if (dev < 0 || dev >= 64) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return only_bias(dtype, M, N, bias, Y, ldy, s);
+    if (plan_fp4(M, N, K, num_sms(dev)).nt == 16)
+        return fp4_linear_few(fmt, dtype, M, N, K, X, ldx, x_tscale, {Wq, Ws, N, w_tscale}, bias, Y, ldy, dev, s);
     Carver c{static_cast<uint8_t*>(ws)};
     uint8_t* xq = c.take(packed_codes(M, K));
     uint8_t* xs = c.take(packed_scales(M, K));

@@ -462,6 +462,14 @@ int w4a4_gemm_prepacked(int64_t M, int64_t N, int64_t K,
 typedef enum { QG_FP4_NV = 0, QG_FP4_MX = 1 } qg_fp4_format;
 typedef enum { QG_F16 = 0, QG_BF16 = 1, QG_F32 = 2 } qg_dtype;
 
+/* Testing hook: how the products below are cut.  tokens: rows of A (tokens) a
+ * tile covers, 16, 32, 64 or 128 (one CTA a tile; below 128 only where that is
+ * all rows, else 128), 256 (CTA pairs, 256 x 256 tiles) or 0 = by the problem's
+ * size (default); splits: CTAs of a cluster that
+ * share K, 1, 2, 4 or 8, or 0 = by the size (ignored by CTA pairs, and where K
+ * has fewer blocks of 256).  Results differ only by the order of fp32 sums. */
+int qg_set_fp4_path(int tokens, int splits);
+
 /* Bytes of a packed row of K codes; 0 for K <= 0. */
 int64_t qg_fp4_codes_ld(int64_t K);
 

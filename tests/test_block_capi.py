@@ -74,6 +74,12 @@ def test_product_refusals(L):
     assert _linear(L, M=0) == 0
 
 
+def test_cut_refusals(L):
+    for tokens, splits in ((8, 0), (-1, 0), (512, 0), (0, 3), (0, 16), (0, -1)):
+        assert L.qg_set_fp4_path(tokens, splits) == 1
+    assert L.qg_set_fp4_path(0, 0) == 0
+
+
 def _backward(L, fmt=0, dt=1, M=4, N=8, K=64, dY=P, lddy=8, X=P, ldx=64, w=P, sw=P, dX=P, lddx=64, dW=P, lddw=64,
               db=P, ws=P, wsb=BIG):
     return L.fp4_linear_backward(fmt, dt, M, N, K, dY, lddy, None, X, ldx, None, w, sw, None, dX, lddx, dW, lddw, db,

@@ -204,6 +204,29 @@ def test_gemm(torch, qg, M, N, K, fmt, dtype):
     assert bool((wide[:, :3] == 7).all()) and bool((wide[:, N + 3:] == 7).all())
 
 
+CUTS = [(16, 1), (16, 2), (16, 4), (16, 8), (32, 1), (32, 4), (64, 1), (64, 2), (128, 1), (128, 2), (128, 8), (256, 0)]
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+@pytest.mark.parametrize("tokens,splits", CUTS)
+def test_every_cut_of_a_product(torch, qg, tokens, splits, fmt):
+    """Each tile and split, with tokens that fill a tile, that leave some out and that need several."""
+    try:
+        assert qg.lib().qg_set_fp4_path(tokens, splits) == qg.QG_OK
+        for M, N, K in [(1, 130, 2100), (tokens, 257, 2048), (min(tokens, 128) - 3, 128, 1057), (261, 300, 2111)]:
+            a, b = activations(M, K, 70 + M), activations(N, K, 71 + N, 0.05)
+            bias = on_gpu(torch, activations(1, N, 22)[0], "float16")
+            pa, pb = packed(torch, a, fmt), packed(torch, b, fmt)
+            want = ref.quantized(a, fmt), ref.quantized(b, fmt)
+            y = qg.fp4_gemm(*pa, *pb, K, fmt, bias=bias, dtype=torch.float16)
+            check_product(y, *want, 1.0, as_np(bias), "float16")
+            assert torch.equal(y, qg.fp4_gemm(*pa, *pb, K, fmt, bias=bias, dtype=torch.float16))
+            X = on_gpu(torch, a)
+            check_product(qg.fp4_linear(X, *pb, fmt), *want, 1.0, None, "float32")
+    finally:
+        qg.lib().qg_set_fp4_path(0, 0)
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
 @pytest.mark.parametrize("fmt", ["nv", "mx"])
 def test_products_of_nothing(torch, qg, fmt, dtype):
@@ -233,6 +256,7 @@ def test_linear_is_quantize_then_gemm(torch, qg, M, N, K, fmt):
     xs = qg.fp4_tensor_scale(X) if fmt == "nv" else None
     q, s = qg.fp4_quantize(X, fmt, scale=xs)
     want = qg.fp4_gemm(q, s, *w, K, fmt, a_scale=xs, bias=bias)
+    # (the same cut of K: one token to sixteen are quantized inside the product's kernel)
     assert torch.equal(qg.fp4_linear(X, *w, fmt, x_scale=xs, bias=bias), want)
     # strided activations, another stream, a workspace full of NaN bytes
     wide = torch.empty((M, K + 9), dtype=X.dtype, device="cuda")
