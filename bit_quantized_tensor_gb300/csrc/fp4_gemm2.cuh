@@ -273,7 +273,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
         uint8_t* const buf = out_smem + (warp - 2) * 2048;
         const bool sectors = (reinterpret_cast<uintptr_t>(p.Y) & 31) == 0 &&
                              (p.ldy * (p.dtype == QG_F32 ? 4 : 2)) % 32 == 0;
-        auto put = [&](auto* Y, const float(&f)[16], int row0, int col) {
+        // 16 columns of the warp's rows, in the type of Y
+        auto put = [&](auto* Y, const uint32_t(&r)[16], int row0, int col) {
+            using T = typename std::remove_pointer<decltype(Y)>::type;
+            const T* bias = static_cast<const T*>(p.bias);
+            float f[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha;
+            if (bias) {
+                if (col + 16 <= p.N) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[j] += to_f32<T>(__ldg(bias + col + j));
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[j] += to_f32<T>(__ldg(bias + min(col + j, p.N - 1)));
+                }
+            }
             if (sectors && col + 16 <= p.N) {
                 if (row0 + lane < p.M) fp4_store16(Y + (row0 + lane) * p.ldy + col, f);
             } else {
@@ -290,39 +305,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             tc_fence_after();
             const uint32_t taddr = tmem + (static_cast<uint32_t>(quad * 32) << 16) +
                                    static_cast<uint32_t>((n & 1) * Cfg::ACC_STEP);
-            // accumulator 0 shares its last 48 columns, accumulator 1 its first 48:
-            // the half that holds them starts there
-            const bool sharing = half == ((n & 1) ? 0 : 1);
+            // Accumulator 0 shares its last 48 columns and accumulator 1 its first 48
+            // with the other one.  A warp's arrival says that it has read those of its
+            // half (whether they are shared or not) and all of the tile before.
             auto release = [&] {
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster_relaxed(next);
             };
-            if (!sharing) release();
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i) {
-                // 16 columns a step; half 1 goes down from the top
-                const int c = half ? 240 - 16 * i : 16 * i;
-                uint32_t r[16];
-                tmem_ld_32x32b_x16(taddr + c, r);
-                tmem_wait_ld();
-                if (sharing && i == Cfg::SHARED_COLS / 16 - 1) release();
+            auto put_any = [&](const uint32_t(&r)[16], int c) {
                 const int col = nb * 256 + c;
-                if (row0 >= p.M || col >= p.N) continue;
-                float f[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha;
-                if (p.bias) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        if (col + j < p.N) f[j] += typed_at(p.bias, p.dtype, col + j);
-                }
+                if (row0 >= p.M || col >= p.N) return;
                 if (p.dtype == QG_F16)
-                    put(static_cast<__half*>(p.Y), f, row0, col);
+                    put(static_cast<__half*>(p.Y), r, row0, col);
                 else if (p.dtype == QG_BF16)
-                    put(static_cast<__nv_bfloat16*>(p.Y), f, row0, col);
+                    put(static_cast<__nv_bfloat16*>(p.Y), r, row0, col);
                 else
-                    put(static_cast<float*>(p.Y), f, row0, col);
+                    put(static_cast<float*>(p.Y), r, row0, col);
+            };
+            // 16 columns a step, half 1 from the top down, so that the shared ones are
+            // the first of the half that has them: all of those are read before any is
+            // stored, since the next tile's MMAs wait for them
+            auto col_of = [&](int i) { return half ? 240 - 16 * i : 16 * i; };
+            uint32_t r[Cfg::SHARED_COLS / 16][16];
+#pragma unroll
+            for (int i = 0; i < Cfg::SHARED_COLS / 16; ++i) tmem_ld_32x32b_x16(taddr + col_of(i), r[i]);
+            tmem_wait_ld();
+            release();
+#pragma unroll
+            for (int i = 0; i < Cfg::SHARED_COLS / 16; ++i) put_any(r[i], col_of(i));
+#pragma unroll 1
+            for (int i = Cfg::SHARED_COLS / 16; i < 8; ++i) {
+                tmem_ld_32x32b_x16(taddr + col_of(i), r[0]);
+                tmem_wait_ld();
+                put_any(r[0], col_of(i));
             }
         }
     }

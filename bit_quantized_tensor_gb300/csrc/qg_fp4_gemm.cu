@@ -89,24 +89,51 @@ struct Fp4Plan {
     int nt, splits;
 };
 
-// Splits of K over a cluster: doubled while the CTAs so far leave SMs with room
-// (two CTAs an SM with 16 tokens a tile) and each split keeps two K blocks.
-static int choose_splits(int64_t tiles, int64_t num_kb, int room) {
+// Splits of K over a cluster: doubled while a CTA an SM takes them and each keeps
+// a K block, or, up to two CTAs an SM (16 tokens a tile: two fit), while each
+// keeps eight.  Measured (us, a call in a chain): 1 x 4096 x 4096 4.2 with 4
+// splits, 4.8 with 8; 16 x 8192 x 8192 7.7 with 4, 9.7 with 2; 8 x 1024 x 2048
+// 3.0 with 8, 3.4 with 4.
+static int choose_splits(int64_t tiles, int64_t num_kb, int nt, int sms) {
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= room && num_kb >= 4 * s) s *= 2;
+    while (s < 8 && 2 * s <= num_kb) {
+        const int64_t ctas = tiles * s * 2;
+        if (!(ctas <= (nt == 128 ? sms / 2 : sms) || (nt == 16 && ctas <= 2 * sms && num_kb >= 16 * s))) break;
+        s *= 2;
+    }
     return s;
 }
 
-static Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, int sms) {
+// Estimates in microseconds, fitted to products of 64 to 2048 tokens: a pair's
+// tile takes 0.30 a K block, a 128-token tile 0.37, and a cluster's join grows
+// with the number of CTAs that exchange sums at once.
+//   2048 x 2048 x 2048: pairs 8.2, single CTAs 18;  128 x 4096 x 4096: 10.5, 11.3;
+//   100 x 300 x 8192: pairs 14, single CTAs with 8 splits 8.3.  Rows of Y that are
+// not 32-byte aligned cost pairs 3 more: 777 x 1001 x 2304 11.8, single CTAs 10.2.
+static double pair_time(int64_t M, int64_t N, int64_t kb, bool sectors, int sms) {
+    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256), pairs = sms > 1 ? sms / 2 : 1;
+    return (sectors ? 3.6 : 6.6) +
+           static_cast<double>((tiles + pairs - 1) / pairs) * (0.30 * static_cast<double>(kb) + 0.6);
+}
+static double single_time(int64_t M, int64_t N, int64_t kb, int splits, int sms) {
+    const int64_t ctas = (M + 127) / 128 * ((N + 127) / 128) * splits;
+    return 5.0 + static_cast<double>((ctas + sms - 1) / sms) * 0.37 * static_cast<double>(kb) / splits +
+           (splits > 1 ? 2.0 + 0.06 * static_cast<double>(ctas) : 0.0);
+}
+
+static bool whole_sectors(const void* Y, int64_t ldy, int dtype) {
+    return (reinterpret_cast<uintptr_t>(Y) & 31u) == 0 && static_cast<size_t>(ldy) * dtype_bytes(dtype) % 32 == 0;
+}
+
+static Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, bool sectors, int sms) {
     Fp4Plan f{g_fp4_nt.load(), g_fp4_splits.load()};
-    if (!f.nt) f.nt = M > 128 && N > 128 && (M > 256 || N > 2048) ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
-    if (f.nt < M && f.nt < 128) f.nt = 128;  // smaller tiles hold all tokens
-    if (f.nt == 256)
-        f.splits = 1;
-    else if (!f.splits)
-        f.splits = choose_splits((N + 127) / 128 * ((M + f.nt - 1) / f.nt), (K + kFp4Bk - 1) / kFp4Bk,
-                                 f.nt <= 16 ? 2 * sms : sms);
-    if (f.splits > (K + kFp4Bk - 1) / kFp4Bk) f.splits = 1;
+    const int64_t kb = (K + kFp4Bk - 1) / kFp4Bk;
+    if (f.nt < M && f.nt && f.nt < 128) f.nt = 128;  // smaller tiles hold all tokens
+    const bool chosen = f.nt != 0;
+    if (!chosen) f.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+    if (!f.splits) f.splits = choose_splits((N + 127) / 128 * ((M + f.nt - 1) / f.nt), kb, f.nt, sms);
+    if (!chosen && f.nt == 128 && pair_time(M, N, kb, sectors, sms) < single_time(M, N, kb, f.splits, sms)) f.nt = 256;
+    if (f.nt == 256 || f.splits > kb) f.splits = 1;
     return f;
 }
 
@@ -138,7 +165,7 @@ static int fp4_gemm_run(int fmt, int dtype, int64_t M, int64_t N, int64_t K, con
                         cudaStream_t s) {
     const Fp4Params p = fp4_params(dtype, M, N, K, x, w, bias, Y, ldy, weights_ready, dev);
     if (!p.ctl.status) return QG_ERR_CUDA;
-    const Fp4Plan f = plan_fp4(M, N, K, num_sms(dev));
+    const Fp4Plan f = plan_fp4(M, N, K, whole_sectors(Y, ldy, dtype), num_sms(dev));
     return fmt == kNv ? run_fmt<kNv>(x, w, p, f, dev, s) : run_fmt<kMx>(x, w, p, f, dev, s);
 }
 
@@ -152,7 +179,7 @@ static int fp4_linear_few(int fmt, int dtype, int64_t M, int64_t N, int64_t K, c
     p.X = X;
     p.ldx = ldx;
     p.x_aligned = aligned16(X) && (M <= 1 || static_cast<size_t>(ldx) * dtype_bytes(dtype) % 16 == 0);
-    const Fp4Plan f = plan_fp4(M, N, K, num_sms(dev));
+    const Fp4Plan f = plan_fp4(M, N, K, whole_sectors(Y, ldy, dtype), num_sms(dev));
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         return fmt == kNv ? launch_fp4<Fp4Cfg<kNv, 16>, T>(x, w, p, f.splits, s)
@@ -288,7 +315,7 @@ int fp4_linear(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const void* 
     if (dev < 0 || dev >= 64) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return only_bias(dtype, M, N, bias, Y, ldy, s);
-    if (plan_fp4(M, N, K, num_sms(dev)).nt == 16)
+    if (plan_fp4(M, N, K, whole_sectors(Y, ldy, dtype), num_sms(dev)).nt == 16)
         return fp4_linear_few(fmt, dtype, M, N, K, X, ldx, x_tscale, {Wq, Ws, N, w_tscale}, bias, Y, ldy, dev, s);
     Carver c{static_cast<uint8_t*>(ws)};
     uint8_t* xq = c.take(packed_codes(M, K));
