@@ -24,6 +24,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "qg_internal.h"
 
 namespace qg {
@@ -236,6 +238,20 @@ __device__ __forceinline__ uint32_t absmax_bits(const float (&x)[N]) {
     return m;
 }
 
+// The codes of 8 values times r.
+__device__ __forceinline__ uint32_t scaled_codes8(const float* x, float r) {
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+        uint64_t p, f;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x[j]), "f"(x[j + 1]));
+        asm("mov.b64 %0, {%1, %1};" : "=l"(f) : "f"(r));
+        asm("mul.rn.f32x2 %0, %0, %1;" : "+l"(p) : "l"(f));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(y[j]), "=f"(y[j + 1]) : "l"(p));
+    }
+    return e2m1x8(y);
+}
+
 // One block of a row: its codes (BLOCK / 8 words) and its scale byte.
 template <int FMT>
 __device__ __forceinline__ uint32_t quantize_block(const float (&x)[fp4_block(FMT)], float ts, float six_ts,
@@ -243,13 +259,69 @@ __device__ __forceinline__ uint32_t quantize_block(const float (&x)[fp4_block(FM
     constexpr int B = fp4_block(FMT);
     const BlockScale s = block_scale<FMT>(absmax_bits<B>(x), ts, six_ts);
 #pragma unroll
-    for (int i = 0; i < B; i += 8) {
-        float y[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(x[i + j], s.r);
-        codes[i / 8] = e2m1x8(y);
-    }
+    for (int i = 0; i < B; i += 8) codes[i / 8] = scaled_codes8(x + i, s.r);
     return s.byte;
+}
+
+// The same for a block that is still packed in words of T (two 16-bit values
+// each): the maximum is found on the packed words.
+template <class T>
+__device__ __forceinline__ uint32_t packed_amax_bits(uint32_t m) {  // the larger half of m, as fp32 bits
+    const uint32_t h = max(m & 0xffffu, m >> 16);
+    if constexpr (std::is_same<T, __half>::value)
+        return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
+    else
+        return h << 16;
+}
+template <int FMT, class T, int WORDS>
+__device__ __forceinline__ uint32_t quantize_words(const uint32_t (&w)[WORDS], float ts, float six_ts,
+                                                   uint32_t (&codes)[fp4_block(FMT) / 8]) {
+    constexpr int B = fp4_block(FMT);
+    static_assert(WORDS * 4 == B * static_cast<int>(sizeof(T)), "one block");
+    if constexpr (sizeof(T) == 4) {
+        float x[B];
+#pragma unroll
+        for (int i = 0; i < B; ++i) x[i] = __uint_as_float(w[i]);
+        return quantize_block<FMT>(x, ts, six_ts, codes);
+    } else {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        const BlockScale s = block_scale<FMT>(packed_amax_bits<T>(m), ts, six_ts);
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4) {
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack2<T>(w[i + j]);
+                x[2 * j] = f.x;
+                x[2 * j + 1] = f.y;
+            }
+            codes[i / 4] = scaled_codes8(x, s.r);
+        }
+        return s.byte;
+    }
+}
+
+// N values as they lie in memory, the first n of them existing (the rest 0).
+template <class T, int N>
+__device__ __forceinline__ void load_words(const T* p, int n, bool aligned, uint32_t (&w)[N * sizeof(T) / 4]) {
+    constexpr int W = N * static_cast<int>(sizeof(T)) / 4;
+    if (aligned && n >= N) {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+            w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+        }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) w[i] = i < n ? reinterpret_cast<const uint32_t*>(p)[i] : 0u;
+    } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < W; ++i)
+            w[i] = (2 * i < n ? h[2 * i] : 0u) | (2 * i + 1 < n ? static_cast<uint32_t>(h[2 * i + 1]) << 16 : 0u);
+    }
 }
 
 // ------------------------------------------------------- host

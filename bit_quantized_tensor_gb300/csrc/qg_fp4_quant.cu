@@ -13,171 +13,191 @@ namespace qg {
 // the maximum and the codes stay in its registers, and the scale bytes of the
 // four blocks of a scale tile's row go out as one word through two shuffles.
 // Bound by memory: 2 or 4 bytes in and 0.56 (nv) or 0.53 (mx) out per value.
+// 2^log_tx threads lie along a row (at least 4), the others of the CTA on
+// further rows.
 constexpr int kQuantThreads = 256;
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kQuantThreads)
-    k_fp4_quantize(int64_t M, int64_t rows, int64_t K, const T* __restrict__ X, int64_t ldx, bool aligned,
+    k_fp4_quantize(int64_t M, int64_t rows, int64_t K, int log_tx, const T* __restrict__ X, int64_t ldx, bool aligned,
                    const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
     constexpr int B = fp4_block(FMT);
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const int64_t tiles = fp4_col_tiles(FMT, K);
+    const int tx = 1 << log_tx;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantThreads >> log_tx) + (threadIdx.x >> log_tx);
+    if (row >= rows) return;  // tx >= 4: groups of 4 lanes leave together
+    const int64_t tiles = fp4_col_tiles(FMT, K), ld = fp4_codes_ld(K);
     const int64_t per_row = 4 * tiles;  // blocks of a row, up to whole scale words
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kQuantThreads + threadIdx.x;
-    const int64_t row = item / per_row, blk = item - row * per_row;
-    if (row >= rows) return;  // per_row is a multiple of 4: groups of 4 lanes leave together
     const float ts = FMT == kNv && tscale ? *tscale : 1.f;
     const float six_ts = __fmul_rn(6.f, ts);
-    uint32_t byte = 0;
-    const int64_t k0 = blk * B, ld = fp4_codes_ld(K);
-    if (row < M && k0 < 2 * ld) {
-        uint32_t codes[B / 8];
-        if (k0 < K) {
-            float x[B];
-            load_some<T, B>(X + row * ldx + k0, static_cast<int>(min(K - k0, int64_t(B))), aligned, x);
-            byte = quantize_block<FMT>(x, ts, six_ts, codes);
-        } else {
-#pragma unroll
-            for (int i = 0; i < B / 8; ++i) codes[i] = 0;
-        }
-        uint8_t* q = Xq + row * ld + k0 / 2;
-        if constexpr (B == 16)
-            *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
-        else
-            *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-    }
     const uint32_t quad = 0xfu << (threadIdx.x & 28);
-    uint32_t word = byte << (8 * (threadIdx.x & 3));
-    word |= __shfl_xor_sync(quad, word, 1);
-    word |= __shfl_xor_sync(quad, word, 2);
-    if ((threadIdx.x & 3) == 0) *reinterpret_cast<uint32_t*>(Xs + fp4_scale_offset(row, blk, tiles)) = word;
+    for (int64_t blk = static_cast<int64_t>(blockIdx.y) * tx + (threadIdx.x & (tx - 1)); blk < per_row;
+         blk += static_cast<int64_t>(gridDim.y) * tx) {
+        uint32_t byte = 0;
+        const int64_t k0 = blk * B;
+        if (row < M && k0 < 2 * ld) {
+            uint32_t codes[B / 8];
+            if (k0 < K) {
+                uint32_t w[B * sizeof(T) / 4];
+                load_words<T, B>(X + row * ldx + k0, static_cast<int>(min(K - k0, int64_t(B))), aligned, w);
+                byte = quantize_words<FMT, T>(w, ts, six_ts, codes);
+            } else {
+#pragma unroll
+                for (int i = 0; i < B / 8; ++i) codes[i] = 0;
+            }
+            uint8_t* q = Xq + row * ld + k0 / 2;
+            if constexpr (B == 16)
+                *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
+            else
+                *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+        }
+        uint32_t word = byte << (8 * (threadIdx.x & 3));
+        word |= __shfl_xor_sync(quad, word, 1);
+        word |= __shfl_xor_sync(quad, word, 2);
+        if ((threadIdx.x & 3) == 0) *reinterpret_cast<uint32_t*>(Xs + fp4_scale_offset(row, blk, tiles)) = word;
+    }
 }
 
 // ------------------------------------------------------- rows and columns
 //
-// A CTA takes a tile of 128 x 128 values through shared memory once and
-// quantizes it along both axes: X (blocks along a row) and X^T (blocks along
-// a column), as a training step needs an operand once for each of its two
-// products.  The tile also gives the column sums (the bias gradient).
+// A CTA takes a tile of 128 x 128 values once and quantizes it along both axes:
+// X (blocks along a row) and X^T (blocks along a column), as a training step
+// needs an operand once for each of its two products.  Rows are quantized from
+// the registers of the load, columns from shared memory, two of a 16-bit type
+// at a time.  Codes of X^T and all scales are put together in shared memory
+// and leave in 16-byte pieces.  The tile also gives the column sums (the bias
+// gradient).  Bound by memory: 2 or 4 bytes in, 1.12 or 1.06 out per value.
 constexpr int kBothThreads = 256;
 constexpr int kTile = 128;
 
-template <class T>
+template <int FMT, class T>
 struct BothSmem {
-    // 4-byte words a row: odd, so that a warp walking down a column as well as
-    // along a row meets distinct banks
+    static constexpr int B = fp4_block(FMT), NB = kTile / B;   // blocks along an axis of the tile
+    // words a row of the tile: odd, so that a warp along a row and one down a
+    // column both meet distinct banks
     static constexpr int PITCH = kTile * static_cast<int>(sizeof(T)) / 4 + 1;
-    static constexpr int BYTES = kTile * PITCH * 4;
+    static constexpr int SCALES = NB / 4 * 512;                // of one direction
+    static constexpr int CODES_PITCH = kTile / 2 + 16;         // bytes a row of X^T's codes
+    static constexpr int TILE_BYTES = (kTile * PITCH * 4 + 15) / 16 * 16;
+    static constexpr int BYTES = TILE_BYTES + kTile * CODES_PITCH + 2 * SCALES + NB * kTile * 4;
 };
-
-template <class T>
-__device__ __forceinline__ float tile_at(const uint32_t* tile, int m, int k) {
-    return to_f32<T>(reinterpret_cast<const T*>(tile + m * BothSmem<T>::PITCH)[k]);
-}
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kBothThreads)
     k_fp4_quantize_both(int64_t M, int64_t K, const T* __restrict__ X, int64_t ldx, bool aligned,
                         const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs,
                         uint8_t* __restrict__ Tq, uint8_t* __restrict__ Ts, float* __restrict__ partial) {
-    constexpr int B = fp4_block(FMT);
-    constexpr int NB = kTile / B;  // blocks along an axis of the tile
-    constexpr int PITCH = BothSmem<T>::PITCH;
-    extern __shared__ uint32_t tile[];
-    __shared__ float colsum[kBothThreads / kTile][kTile];
+    using S = BothSmem<FMT, T>;
+    constexpr int B = S::B, NB = S::NB, PITCH = S::PITCH, W = B * static_cast<int>(sizeof(T)) / 4;
+    extern __shared__ __align__(16) uint8_t both_smem[];
+    uint32_t* const tile = reinterpret_cast<uint32_t*>(both_smem);
+    uint8_t* const tcodes = both_smem + S::TILE_BYTES;
+    uint8_t* const rscales = tcodes + kTile * S::CODES_PITCH;
+    uint8_t* const tscales = rscales + S::SCALES;
+    float* const sums = reinterpret_cast<float*>(tscales + S::SCALES);  // [NB][kTile]
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, k0 = static_cast<int64_t>(blockIdx.x) * kTile;
     const float ts = FMT == kNv && tscale ? *tscale : 1.f;
     const float six_ts = __fmul_rn(6.f, ts);
+    const int64_t ldq = fp4_codes_ld(K), ldt = fp4_codes_ld(M);
+    // place of (row, block) in this tile's scale tiles
+    auto scale_at = [](int r, int b) { return (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3); };
 
-    // the tile, zero outside X
-    constexpr int V = 16 / static_cast<int>(sizeof(T));
-    for (int i = threadIdx.x; i < kTile * (kTile / V); i += kBothThreads) {
-        const int m = i / (kTile / V), k = (i % (kTile / V)) * V;
-        uint32_t w[4] = {0, 0, 0, 0};
-        const int64_t left = K - (k0 + k);
-        if (m0 + m < M && left > 0) {
-            const T* p = X + (m0 + m) * ldx + k0 + k;
-            if (aligned && left >= V) {
-                const uint4 v = *reinterpret_cast<const uint4*>(p);
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-            } else {
-                T e[V];
+    // the tile, zero outside X, and the blocks along its rows
+#pragma unroll 2
+    for (int i = threadIdx.x; i < kTile * NB; i += kBothThreads) {
+        const int m = i / NB, b = i % NB;
+        const int64_t k = k0 + b * B;
+        const bool in = m0 + m < M;
+        uint32_t w[W];
+        if (in && k < K) {
+            load_words<T, B>(X + (m0 + m) * ldx + k, static_cast<int>(min(K - k, int64_t(B))), aligned, w);
+        } else {
 #pragma unroll
-                for (int j = 0; j < V; ++j) e[j] = j < left ? p[j] : from_f32<T>(0.f);
-                memcpy(w, e, 16);
-            }
+            for (int j = 0; j < W; ++j) w[j] = 0;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tile[m * PITCH + k * static_cast<int>(sizeof(T)) / 4 + j] = w[j];
+        for (int j = 0; j < W; ++j) tile[m * PITCH + b * W + j] = w[j];
+        if (Xq) {
+            uint32_t codes[B / 8];
+            rscales[scale_at(m, b)] = static_cast<uint8_t>(quantize_words<FMT, T>(w, ts, six_ts, codes));
+            if (in && k < 2 * ldq) {
+                uint8_t* q = Xq + (m0 + m) * ldq + k / 2;
+                if constexpr (B == 16)
+                    *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
+                else
+                    *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            }
+        }
     }
     __syncthreads();
 
-    if (Xq) {
-        const int64_t ld = fp4_codes_ld(K), tiles = fp4_col_tiles(FMT, K);
-        for (int i = threadIdx.x; i < kTile * NB; i += kBothThreads) {
-            // a warp's lanes on 32 rows of the same block
-            const int m = i % kTile, b = i / kTile;
-            const int64_t k = k0 + b * B;
-            if (k >= 2 * ld) continue;  // uniform over the CTA's threads of a block
-            float x[B];
-            uint32_t codes[B / 8];
+    // blocks along the columns: 32-bit words, that is one or two columns a thread
+    constexpr int PER = 4 / static_cast<int>(sizeof(T)), COLS = kTile / PER;
+    for (int i = threadIdx.x; i < COLS * NB; i += kBothThreads) {
+        const int c = i % COLS, b = i / COLS;  // a warp's lanes on neighbouring words
+        uint32_t v[B];
 #pragma unroll
-            for (int j = 0; j < B; ++j) x[j] = tile_at<T>(tile, m, b * B + j);
-            const uint32_t byte = quantize_block<FMT>(x, ts, six_ts, codes);
-            if (m0 + m < M) {
-                uint8_t* q = Xq + (m0 + m) * ld + k / 2;
+        for (int j = 0; j < B; ++j) v[j] = tile[(b * B + j) * PITCH + c];
+#pragma unroll
+        for (int h = 0; h < PER; ++h) {
+            uint32_t w[W], codes[B / 8];
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                if constexpr (PER == 1) {
+                    w[j] = v[j];
+                    sum += __uint_as_float(w[j]);
+                } else {
+                    w[j] = __byte_perm(v[2 * j], v[2 * j + 1], h ? 0x7632 : 0x5410);
+                    const float2 f = unpack2<typename std::conditional<PER == 1, __half, T>::type>(w[j]);
+                    sum += f.x + f.y;
+                }
+            }
+            const int k = PER * c + h;
+            if (Tq) {
+                tscales[scale_at(k, b)] = static_cast<uint8_t>(quantize_words<FMT, T>(w, ts, six_ts, codes));
+                uint8_t* q = tcodes + k * S::CODES_PITCH + b * (B / 2);
                 if constexpr (B == 16)
                     *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
                 else
                     *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
             }
-            Xs[fp4_scale_offset(m0 + m, k / B, tiles)] = static_cast<uint8_t>(m0 + m < M ? byte : 0);
-        }
-        // blocks between ld and the end of the last scale word
-        for (int i = threadIdx.x; i < kTile * NB; i += kBothThreads) {
-            const int m = i % kTile, b = i / kTile;
-            const int64_t k = k0 + b * B;
-            if (k >= 2 * ld && k / B < 4 * tiles) Xs[fp4_scale_offset(m0 + m, k / B, tiles)] = 0;
+            if (partial) sums[b * kTile + k] = sum;
         }
     }
+    __syncthreads();
+
     if (Tq) {
-        const int64_t ld = fp4_codes_ld(M), tiles = fp4_col_tiles(FMT, M);
-        for (int i = threadIdx.x; i < kTile * NB; i += kBothThreads) {
-            const int k = i % kTile, b = i / kTile;
-            const int64_t m = m0 + b * B;
-            if (m >= 2 * ld) continue;
-            float x[B];
-            uint32_t codes[B / 8];
+        // rows of 64 bytes, four threads each; ldt is a multiple of 16 bytes
 #pragma unroll
-            for (int j = 0; j < B; ++j) x[j] = tile_at<T>(tile, b * B + j, k);
-            const uint32_t byte = quantize_block<FMT>(x, ts, six_ts, codes);
-            if (k0 + k < K) {
-                uint8_t* q = Tq + (k0 + k) * ld + m / 2;
-                if constexpr (B == 16)
-                    *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
-                else
-                    *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-            }
-            Ts[fp4_scale_offset(k0 + k, m / B, tiles)] = static_cast<uint8_t>(k0 + k < K ? byte : 0);
-        }
-        for (int i = threadIdx.x; i < kTile * NB; i += kBothThreads) {
-            const int k = i % kTile, b = i / kTile;
-            const int64_t m = m0 + b * B;
-            if (m >= 2 * ld && m / B < 4 * tiles) Ts[fp4_scale_offset(k0 + k, m / B, tiles)] = 0;
+        for (int i = threadIdx.x; i < kTile * 4; i += kBothThreads) {
+            const int k = i / 4, piece = i % 4;
+            const int64_t at = m0 / 2 + 16 * piece;
+            if (k0 + k < K && at < ldt)
+                *reinterpret_cast<uint4*>(Tq + (k0 + k) * ldt + at) =
+                    *reinterpret_cast<const uint4*>(tcodes + k * S::CODES_PITCH + 16 * piece);
         }
     }
-    if (partial) {
-        const int k = threadIdx.x % kTile, part = threadIdx.x / kTile;
-        constexpr int ROWS = kTile / (kBothThreads / kTile);
-        float sum = 0.f;
-#pragma unroll 8
-        for (int m = 0; m < ROWS; ++m) sum += tile_at<T>(tile, part * ROWS + m, k);
-        colsum[part][k] = sum;
-        __syncthreads();
-        if (part == 0 && k0 + k < K) partial[blockIdx.y * K + k0 + k] = colsum[0][k] + colsum[1][k];
+    // whole scale tiles; values outside X were 0, so their scales are
+    constexpr int PIECES = S::SCALES / 16;
+    for (int i = threadIdx.x; i < 2 * PIECES; i += kBothThreads) {
+        const bool t = i >= PIECES;
+        const int j = t ? i - PIECES : i;
+        uint8_t* const out = t ? Ts : Xs;
+        const int64_t tiles = fp4_col_tiles(FMT, t ? M : K);
+        const int64_t col = (t ? m0 : k0) / (4 * B) + j / 32;
+        if (out && col < tiles)
+            *reinterpret_cast<uint4*>(out + ((t ? k0 : m0) / 128 * tiles + col) * 512 + j % 32 * 16) =
+                *reinterpret_cast<const uint4*>((t ? tscales : rscales) + 16 * j);
+    }
+    if (partial && threadIdx.x < kTile && k0 + threadIdx.x < K) {
+        float sum = sums[threadIdx.x];
+#pragma unroll
+        for (int b = 1; b < NB; ++b) sum += sums[b * kTile + threadIdx.x];
+        partial[blockIdx.y * K + k0 + threadIdx.x] = sum;
     }
 }
 
@@ -203,15 +223,32 @@ __global__ void __launch_bounds__(kAmaxThreads)
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const int64_t per_row = (K + V - 1) / V;
-    const int64_t items = M * per_row, step = static_cast<int64_t>(gridDim.x) * kAmaxThreads;
+    const int64_t per_row = (K + V - 1) / V, step = static_cast<int64_t>(gridDim.x) * kAmaxThreads;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kAmaxThreads + threadIdx.x;
     uint32_t m = 0;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kAmaxThreads + threadIdx.x; i < items; i += step) {
-        const int64_t row = i / per_row, k = (i - row * per_row) * V;
-        float x[V];
-        load_some<T, V>(X + row * ldx + k, static_cast<int>(min(K - k, int64_t(V))), aligned, x);
+    for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
+        const T* const x = X + row * ldx;
+        // four loads in flight a thread
+        for (int64_t i = first; i < per_row; i += 4 * step) {
+            uint32_t w[4][4];
 #pragma unroll
-        for (int j = 0; j < V; ++j) m = max(m, finite_abs_bits(x[j]));
+            for (int u = 0; u < 4; ++u) {
+                const int64_t k = (i + u * step) * V;
+                load_words<T, V>(x + k, static_cast<int>(max(int64_t(0), min(K - k, int64_t(V)))), aligned, w[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 4) {
+                        m = max(m, finite_abs_bits(__uint_as_float(w[u][j])));
+                    } else {
+                        const float2 f = unpack2<T>(w[u][j]);
+                        m = max(m, max(finite_abs_bits(f.x), finite_abs_bits(f.y)));
+                    }
+                }
+            }
+        }
     }
     m = __reduce_max_sync(0xffffffffu, m);
     __shared__ uint32_t wm[kAmaxThreads / 32];
@@ -220,7 +257,7 @@ __global__ void __launch_bounds__(kAmaxThreads)
     if (threadIdx.x < 32) {
         m = threadIdx.x < kAmaxThreads / 32 ? wm[threadIdx.x] : 0u;
         m = __reduce_max_sync(0xffffffffu, m);
-        if (threadIdx.x == 0) part[blockIdx.x] = m;
+        if (threadIdx.x == 0) part[blockIdx.y * gridDim.x + blockIdx.x] = m;
     }
 }
 
@@ -274,17 +311,35 @@ static bool rows_aligned(const void* p, int64_t ld, size_t elem, int64_t rows) {
 int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                      uint8_t* Xq, uint8_t* Xs, bool zero_pad, cudaStream_t s) {
     const int64_t rows = zero_pad ? (M + 127) / 128 * 128 : M;
-    const int64_t items = rows * 4 * fp4_col_tiles(fmt, K);
-    const int64_t ctas = (items + kQuantThreads - 1) / kQuantThreads;
-    if (ctas == 0) return QG_OK;
-    if (ctas > INT32_MAX) return QG_ERR_UNSUPPORTED;
+    const int64_t per_row = 4 * fp4_col_tiles(fmt, K);
+    if (rows == 0 || per_row == 0) return QG_OK;
+    int log_tx = 2;
+    while (log_tx < 8 && (int64_t(1) << log_tx) < per_row) ++log_tx;
+    const int64_t ty = kQuantThreads >> log_tx, gx = (rows + ty - 1) / ty;
+    int64_t gy = (per_row + (int64_t(1) << log_tx) - 1) >> log_tx;
+    if (gx > INT32_MAX) return QG_ERR_UNSUPPORTED;
+    if (gy > 65535) gy = 65535;
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const bool al = rows_aligned(X, ldx, sizeof(T), M);
         auto* f = fmt == kNv ? k_fp4_quantize<kNv, T> : k_fp4_quantize<kMx, T>;
-        return launch_serialized(f, dim3(static_cast<unsigned>(ctas)), kQuantThreads, 0, 1, s, M, rows, K,
-                                 static_cast<const T*>(X), ldx, al, ts, Xq, Xs);
+        return launch_serialized(f, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kQuantThreads, 0, 1, s,
+                                 M, rows, K, log_tx, static_cast<const T*>(X), ldx, al, ts, Xq, Xs);
     });
+}
+
+template <int FMT, class T>
+static int launch_both(int64_t gx, int64_t gy, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
+                       uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* partial, cudaStream_t s) {
+    constexpr int SMEM = BothSmem<FMT, T>::BYTES;
+    auto* f = k_fp4_quantize_both<FMT, T>;
+    if constexpr (SMEM > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return map_cuda(e);
+    }
+    return launch_serialized(f, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kBothThreads, SMEM, 1, s, M,
+                             K, static_cast<const T*>(X), ldx, rows_aligned(X, ldx, sizeof(T), M), ts, Xq, Xs, Tq, Ts,
+                             partial);
 }
 
 int fp4_quantize_both_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
@@ -296,24 +351,22 @@ int fp4_quantize_both_run(int fmt, int dtype, int64_t M, int64_t K, const void* 
     if (gx && gy)
         rc = by_dtype(dtype, [&](auto t) {
             using T = decltype(t);
-            const bool al = rows_aligned(X, ldx, sizeof(T), M);
-            auto* f = fmt == kNv ? k_fp4_quantize_both<kNv, T> : k_fp4_quantize_both<kMx, T>;
-            if constexpr (BothSmem<T>::BYTES > 48 * 1024) {
-                const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                           BothSmem<T>::BYTES);
-                if (e != cudaSuccess) return map_cuda(e);
-            }
-            return launch_serialized(f, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kBothThreads,
-                                     BothSmem<T>::BYTES, 1, s, M, K, static_cast<const T*>(X), ldx, al, ts, Xq,
-                                     Xs, Tq, Ts, colsum ? partial : nullptr);
+            float* const part = colsum ? partial : nullptr;
+            return fmt == kNv ? launch_both<kNv, T>(gx, gy, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s)
+                              : launch_both<kMx, T>(gx, gy, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s);
         });
     if (rc || !colsum) return rc;
     return sum_partials_run(partial, gy, K, colsum, s);
 }
 
-static int amax_ctas(int64_t M, int64_t K) {
-    const int64_t n = (M * ((K + 7) / 8) + kAmaxThreads - 1) / kAmaxThreads;
-    return static_cast<int>(n < 1 ? 1 : n > kAmaxMaxCtas ? kAmaxMaxCtas : n);
+// CTAs along a row and over the rows: about two an SM, each thread with 4 loads.
+static dim3 amax_grid(int64_t M, int64_t K, size_t elem) {
+    const int64_t pieces = (K * static_cast<int64_t>(elem) + 15) / 16;
+    int64_t x = (pieces + 4 * kAmaxThreads - 1) / (4 * kAmaxThreads);
+    x = x < 1 ? 1 : x > kAmaxMaxCtas / 2 ? kAmaxMaxCtas / 2 : x;
+    int64_t y = kAmaxMaxCtas / 2 / x;
+    y = M < 1 ? 1 : y > M ? M : y;
+    return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
 }
 
 #define QG_FP4_BUDGETS(T, NAME)                                                                              \
@@ -323,10 +376,10 @@ static int amax_ctas(int64_t M, int64_t K) {
                            kQuantThreads, 0, 0, 1, 4);                                                       \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize_both<nv," NAME ">",                                               \
                            reinterpret_cast<const void*>(k_fp4_quantize_both<kNv, T>), kBothThreads,         \
-                           BothSmem<T>::BYTES, 0, 1, 2);                                                     \
+                           (BothSmem<kNv, T>::BYTES), 0, 1, 2);                                              \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize_both<mx," NAME ">",                                               \
                            reinterpret_cast<const void*>(k_fp4_quantize_both<kMx, T>), kBothThreads,         \
-                           BothSmem<T>::BYTES, 0, 1, 2);                                                     \
+                           (BothSmem<kMx, T>::BYTES), 0, 1, 2);                                              \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_amax<" NAME ">", reinterpret_cast<const void*>(k_fp4_amax<T>), kAmaxThreads, \
                            0, 0, 1, 2);                                                                      \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_dequantize<nv," NAME ">",                                                  \
@@ -383,11 +436,12 @@ int fp4_tensor_scale(int dtype, int64_t M, int64_t K, const void* X, int64_t ldx
         k = M * K;
         m = k ? 1 : 0;
     }
-    const int ctas = amax_ctas(m, k);
+    const dim3 grid = amax_grid(m, k, dtype_bytes(dtype));
+    const int ctas = static_cast<int>(grid.x * grid.y);
     uint32_t* part = static_cast<uint32_t*>(ws);
     rc = by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
-        return launch_serialized(k_fp4_amax<T>, dim3(static_cast<unsigned>(ctas)), kAmaxThreads, 0, 1, s, m, k,
+        return launch_serialized(k_fp4_amax<T>, grid, kAmaxThreads, 0, 1, s, m, k,
                                  static_cast<const T*>(X), ldx, rows_aligned(X, ldx, sizeof(T), m), part);
     });
     if (rc) return rc;
