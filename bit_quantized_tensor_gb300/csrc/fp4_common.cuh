@@ -131,6 +131,26 @@ __device__ __forceinline__ void store_vec(T* p, const float (&x)[N]) {
     }
 }
 
+// 16 values in whole 32-byte sectors (p 32-byte aligned), one store a sector.
+template <class T>
+__device__ __forceinline__ void store_sectors(T* p, const float (&x)[16]) {
+    constexpr int PER = 32 / static_cast<int>(sizeof(T));
+#pragma unroll
+    for (int i = 0; i < 16; i += PER) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (sizeof(T) == 4)
+                w[j] = __float_as_uint(x[i + j]);
+            else
+                w[j] = pack2<T>(x[i + 2 * j], x[i + 2 * j + 1]);
+        }
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + i), "r"(w[0]), "r"(w[1]),
+                     "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    }
+}
+
 // N consecutive values of which the first `n` exist (the rest read as 0).
 template <class T, int N>
 __device__ __forceinline__ void load_some(const T* p, int n, bool aligned, float (&x)[N]) {
@@ -177,15 +197,40 @@ struct BlockScale {
     float r;
 };
 
+// e4m3(fl(amax / six_ts)).  The product with inv_six = fl(1 / six_ts) is within
+// 2^-22 of the quotient, so both round to the same e4m3 number unless it lies
+// within 4 units of the last place of the middle between two of them, or
+// below 2^-6, where they lie closer: then the division itself is done.
+__device__ __forceinline__ uint32_t nv_scale_byte(uint32_t amax_bits, float six_ts, float inv_six) {
+    float q = __fmul_rn(__uint_as_float(amax_bits), inv_six);
+    const uint32_t low = (__float_as_uint(q) & 0xfffffu) - 0x7fffcu;  // distance from the middle, + 4
+    if (low <= 8u || !(q >= 0x1p-6f)) q = __fdiv_rn(__uint_as_float(amax_bits), six_ts);
+    return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
+}
+
+// What a kernel needs of the tensor scale.
+struct TensorScale {
+    float ts, six, inv_six;
+};
+__device__ __forceinline__ TensorScale tensor_scale(const float* ts) {
+    TensorScale t;
+    t.ts = ts ? *ts : 1.f;
+    t.six = __fmul_rn(6.f, t.ts);
+    t.inv_six = __frcp_rn(t.six);
+    return t;
+}
+
+// r of every e4m3 byte (128 of them).
+__device__ __forceinline__ float nv_factor(uint32_t byte, float ts) {
+    return byte && byte < 127 ? __frcp_rn(__fmul_rn(e4m3_value(byte), ts)) : 0.f;
+}
+
 template <int FMT>
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float ts, float six_ts) {
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const TensorScale& t) {
     BlockScale b;
     if constexpr (FMT == kNv) {
-        const float q = __fdiv_rn(__uint_as_float(amax_bits), six_ts);
-        b.byte = __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
-        const float d = __fmul_rn(e4m3_value(b.byte), ts);
-        b.r = b.byte ? __frcp_rn(d) : 0.f;
-        if (amax_bits >= 0x7f800000u) b = {0x7fu, 0.f};
+        b.byte = amax_bits >= 0x7f800000u ? 0x7fu : nv_scale_byte(amax_bits, t.six, t.inv_six);
+        b.r = nv_factor(b.byte, t.ts);
     } else {
         const uint32_t e = amax_bits >> 23;  // floor(log2) + 127; 0 below 2^-126
         b.byte = e > 2 ? e - 2 : 0;
@@ -194,6 +239,20 @@ __device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, float ts, 
         if (amax_bits >= 0x7f800000u) b = {0xffu, 0.f};
     }
     return b;
+}
+
+// The same with the factors of all bytes in shared memory (128 floats, nv).
+__device__ __forceinline__ void fill_factors(float* table, float ts) {
+    for (int i = threadIdx.x; i < 128; i += blockDim.x) table[i] = nv_factor(i, ts);
+}
+template <int FMT>
+__device__ __forceinline__ BlockScale block_scale(uint32_t amax_bits, const TensorScale& t, const float* table) {
+    if constexpr (FMT == kNv) {
+        const uint32_t byte = amax_bits >= 0x7f800000u ? 0x7fu : nv_scale_byte(amax_bits, t.six, t.inv_six);
+        return {byte, table[byte]};
+    } else {
+        return block_scale<FMT>(amax_bits, t);
+    }
 }
 
 // Eight values to eight e2m1 codes (round to nearest, ties to even, saturated
@@ -254,10 +313,10 @@ __device__ __forceinline__ uint32_t scaled_codes8(const float* x, float r) {
 
 // One block of a row: its codes (BLOCK / 8 words) and its scale byte.
 template <int FMT>
-__device__ __forceinline__ uint32_t quantize_block(const float (&x)[fp4_block(FMT)], float ts, float six_ts,
+__device__ __forceinline__ uint32_t quantize_block(const float (&x)[fp4_block(FMT)], const TensorScale& t,
                                                    uint32_t (&codes)[fp4_block(FMT) / 8]) {
     constexpr int B = fp4_block(FMT);
-    const BlockScale s = block_scale<FMT>(absmax_bits<B>(x), ts, six_ts);
+    const BlockScale s = block_scale<FMT>(absmax_bits<B>(x), t);
 #pragma unroll
     for (int i = 0; i < B; i += 8) codes[i / 8] = scaled_codes8(x + i, s.r);
     return s.byte;
@@ -274,20 +333,23 @@ __device__ __forceinline__ uint32_t packed_amax_bits(uint32_t m) {  // the large
         return h << 16;
 }
 template <int FMT, class T, int WORDS>
-__device__ __forceinline__ uint32_t quantize_words(const uint32_t (&w)[WORDS], float ts, float six_ts,
-                                                   uint32_t (&codes)[fp4_block(FMT) / 8]) {
+__device__ __forceinline__ uint32_t quantize_words(const uint32_t (&w)[WORDS], const TensorScale& t,
+                                                   const float* table, uint32_t (&codes)[fp4_block(FMT) / 8]) {
     constexpr int B = fp4_block(FMT);
     static_assert(WORDS * 4 == B * static_cast<int>(sizeof(T)), "one block");
     if constexpr (sizeof(T) == 4) {
         float x[B];
 #pragma unroll
         for (int i = 0; i < B; ++i) x[i] = __uint_as_float(w[i]);
-        return quantize_block<FMT>(x, ts, six_ts, codes);
+        const BlockScale s = block_scale<FMT>(absmax_bits<B>(x), t, table);
+#pragma unroll
+        for (int i = 0; i < B; i += 8) codes[i / 8] = scaled_codes8(x + i, s.r);
+        return s.byte;
     } else {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
-        const BlockScale s = block_scale<FMT>(packed_amax_bits<T>(m), ts, six_ts);
+        const BlockScale s = block_scale<FMT>(packed_amax_bits<T>(m), t, table);
 #pragma unroll
         for (int i = 0; i < WORDS; i += 4) {
             float x[8];

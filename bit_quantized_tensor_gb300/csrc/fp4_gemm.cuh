@@ -338,8 +338,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         // the places where TMA would put them: 128-byte rows, 16-byte pieces
         // exchanged by the row's low three bits; scales as in memory
         constexpr int B = fp4_block(FMT), BLOCKS = kFp4Bk / B;
-        const float ts = FMT == kNv && p.ts_a ? *p.ts_a : 1.f;
-        const float six_ts = __fmul_rn(6.f, ts);
+        const TensorScale ts = tensor_scale(FMT == kNv ? p.ts_a : nullptr);
         Ring<STAGES> ps;
         for (int kb = kb0; kb < kb1; ++kb) {
             if (!warp_wait(empty_bar(ps.slot()), ps.parity() ^ 1u, abort_flag, p.ctl, kSiteFp4Quant)) break;
@@ -351,7 +350,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 float x[B];
                 uint32_t codes[B / 8];
                 load_some<QUANT, B>(static_cast<const QUANT*>(p.X) + (m0 + m) * p.ldx + k, min(p.K - k, B), p.x_aligned, x);
-                const uint32_t byte = quantize_block<FMT>(x, ts, six_ts, codes);
+                const uint32_t byte = quantize_block<FMT>(x, ts, codes);
                 uint8_t* const row = codes_at + m * 128;
                 if constexpr (B == 16)
                     *reinterpret_cast<uint2*>(row + (((blk >> 1) ^ (m & 7)) << 4) + 8 * (blk & 1)) =

@@ -45,27 +45,6 @@ constexpr int kSiteFp4PairEpi = 314;
 constexpr int kSiteFp4PairDrainTma = 315;
 constexpr int kSiteFp4PairDrainMma = 316;
 
-// 16 values of a row to Y in whole 32-byte sectors (dst 32-byte aligned).
-template <class T>
-__device__ __forceinline__ void fp4_store16(T* dst, const float (&f)[16]) {
-    if constexpr (sizeof(T) == 2) {
-        st_global_32(dst,
-                     make_uint4(pack2<T>(f[0], f[1]), pack2<T>(f[2], f[3]), pack2<T>(f[4], f[5]), pack2<T>(f[6], f[7])),
-                     make_uint4(pack2<T>(f[8], f[9]), pack2<T>(f[10], f[11]), pack2<T>(f[12], f[13]),
-                                pack2<T>(f[14], f[15])),
-                     false);
-    } else {
-#pragma unroll
-        for (int h = 0; h < 16; h += 8)
-            st_global_32(dst + h,
-                         make_uint4(__float_as_uint(f[h]), __float_as_uint(f[h + 1]), __float_as_uint(f[h + 2]),
-                                    __float_as_uint(f[h + 3])),
-                         make_uint4(__float_as_uint(f[h + 4]), __float_as_uint(f[h + 5]), __float_as_uint(f[h + 6]),
-                                    __float_as_uint(f[h + 7])),
-                         false);
-    }
-}
-
 // 32 rows x 16 columns of a warp (lane = row) to Y where rows are not 32-byte
 // aligned or end inside the 16 columns: turned in shared memory, so that
 // neighbouring lanes store neighbouring words of a row.  One value a lane and
@@ -290,7 +269,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 }
             }
             if (sectors && col + 16 <= p.N) {
-                if (row0 + lane < p.M) fp4_store16(Y + (row0 + lane) * p.ldy + col, f);
+                if (row0 + lane < p.M) store_sectors(Y + (row0 + lane) * p.ldy + col, f);
             } else {
                 fp4_store_rows(buf, f, Y, p.ldy, row0, p.M, col, p.N);
             }

@@ -253,7 +253,7 @@ QG_BLOCK_KERNEL_BUDGET("k_fp4_only_bias", reinterpret_cast<const void*>(k_fp4_on
 // Checks shared by the three calls.
 static int check_product(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const float* ta, const float* tb) {
     if (!fmt_ok(fmt) || !dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
-    if (M < 0 || N < 0 || K < 0 || M > (1 << 30) || N > (1 << 30) || K > (1 << 30)) return QG_ERR_INVALID_ARG;
+    if (M < 0 || N < 0 || K < 0 || M > (1 << 27) || N > (1 << 27) || K > (1 << 27)) return QG_ERR_INVALID_ARG;
     if (fmt == kMx && (ta || tb)) return QG_ERR_UNSUPPORTED;
     if (reinterpret_cast<uintptr_t>(ta) % 4 || reinterpret_cast<uintptr_t>(tb) % 4) return QG_ERR_MISALIGNED;
     return QG_OK;

@@ -9,12 +9,14 @@ namespace qg {
 
 // ------------------------------------------------------- along the rows
 //
-// One thread quantizes one block: its 16 or 32 values come in 16-byte loads,
-// the maximum and the codes stay in its registers, and the scale bytes of the
-// four blocks of a scale tile's row go out as one word through two shuffles.
-// Bound by memory: 2 or 4 bytes in and 0.56 (nv) or 0.53 (mx) out per value.
-// 2^log_tx threads lie along a row (at least 4), the others of the CTA on
-// further rows.
+// One thread quantizes a block at a time: its 16 or 32 values come in 16-byte
+// loads, the maximum and the codes stay in its registers, and the scale bytes
+// of the four blocks of a scale tile's row go out as one word through two
+// shuffles.  2^log_tx threads lie along a row (at least 4), the others of the
+// CTA on further rows; a thread walks down the rows with the same column, so
+// that addresses only advance.  Bound by memory (2 or 4 bytes in, 0.56 or 0.53
+// out per value) once the instructions are few: with one block a thread and the
+// divisions written out, 15 instructions a value took 21 us for 4096 x 8192 bf16.
 constexpr int kQuantThreads = 256;
 
 template <int FMT, class T>
@@ -22,40 +24,62 @@ __global__ void __launch_bounds__(kQuantThreads)
     k_fp4_quantize(int64_t M, int64_t rows, int64_t K, int log_tx, const T* __restrict__ X, int64_t ldx, bool aligned,
                    const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
     constexpr int B = fp4_block(FMT);
+    __shared__ float factors[128];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const int tx = 1 << log_tx;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kQuantThreads >> log_tx) + (threadIdx.x >> log_tx);
-    if (row >= rows) return;  // tx >= 4: groups of 4 lanes leave together
+    const TensorScale ts = tensor_scale(FMT == kNv ? tscale : nullptr);
+    if constexpr (FMT == kNv) {
+        fill_factors(factors, ts.ts);
+        __syncthreads();
+    }
+    const int tx = 1 << log_tx, ty = kQuantThreads >> log_tx;
     const int64_t tiles = fp4_col_tiles(FMT, K), ld = fp4_codes_ld(K);
-    const int64_t per_row = 4 * tiles;  // blocks of a row, up to whole scale words
-    const float ts = FMT == kNv && tscale ? *tscale : 1.f;
-    const float six_ts = __fmul_rn(6.f, ts);
+    const int64_t blk = static_cast<int64_t>(blockIdx.y) * tx + (threadIdx.x & (tx - 1));
+    if (blk >= 4 * tiles) return;  // tx >= 4: groups of 4 lanes leave together
+    const int64_t k0 = blk * B;
+    const bool some = k0 < K, codes_here = k0 < 2 * ld;
+    const int n = static_cast<int>(min(K - k0, int64_t(B)));
     const uint32_t quad = 0xfu << (threadIdx.x & 28);
-    for (int64_t blk = static_cast<int64_t>(blockIdx.y) * tx + (threadIdx.x & (tx - 1)); blk < per_row;
-         blk += static_cast<int64_t>(gridDim.y) * tx) {
-        uint32_t byte = 0;
-        const int64_t k0 = blk * B;
-        if (row < M && k0 < 2 * ld) {
-            uint32_t codes[B / 8];
-            if (k0 < K) {
-                uint32_t w[B * sizeof(T) / 4];
-                load_words<T, B>(X + row * ldx + k0, static_cast<int>(min(K - k0, int64_t(B))), aligned, w);
-                byte = quantize_words<FMT, T>(w, ts, six_ts, codes);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ty;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * ty + (threadIdx.x >> log_tx);
+    const T* x = X + row * ldx + k0;
+    uint8_t* q = Xq + row * ld + k0 / 2;
+    uint8_t* const s0 = Xs + (blk >> 2) * 512;
+    // U rows' blocks are on their way before the first is quantized
+    constexpr int W = B * static_cast<int>(sizeof(T)) / 4, U = 32 / W;
+    for (; row < rows; row += U * step) {
+        uint32_t w[U][W];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (some && row + u * step < M) {
+                load_words<T, B>(x, n, aligned, w[u]);
             } else {
 #pragma unroll
-                for (int i = 0; i < B / 8; ++i) codes[i] = 0;
+                for (int i = 0; i < W; ++i) w[u][i] = 0;  // also a block behind K
             }
-            uint8_t* q = Xq + row * ld + k0 / 2;
-            if constexpr (B == 16)
-                *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
-            else
-                *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            x += step * ldx;
         }
-        uint32_t word = byte << (8 * (threadIdx.x & 3));
-        word |= __shfl_xor_sync(quad, word, 1);
-        word |= __shfl_xor_sync(quad, word, 2);
-        if ((threadIdx.x & 3) == 0) *reinterpret_cast<uint32_t*>(Xs + fp4_scale_offset(row, blk, tiles)) = word;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t here = row + u * step;
+            if (U > 1 && here >= rows) break;  // groups of 4 lanes alike
+            uint32_t byte = 0;
+            if (here < M && codes_here) {
+                uint32_t codes[B / 8];
+                byte = quantize_words<FMT, T>(w[u], ts, factors, codes);
+                if constexpr (B == 16)
+                    *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
+                else
+                    *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+            }
+            q += step * ld;
+            uint32_t word = byte << (8 * (threadIdx.x & 3));
+            word |= __shfl_xor_sync(quad, word, 1);
+            word |= __shfl_xor_sync(quad, word, 2);
+            const uint32_t r = static_cast<uint32_t>(here) & 127u;
+            if ((threadIdx.x & 3) == 0)
+                *reinterpret_cast<uint32_t*>(s0 + (here >> 7) * tiles * 512 + (r & 31u) * 16 + (r >> 5) * 4) = word;
+        }
     }
 }
 
@@ -80,7 +104,7 @@ struct BothSmem {
     static constexpr int SCALES = NB / 4 * 512;                // of one direction
     static constexpr int CODES_PITCH = kTile / 2 + 16;         // bytes a row of X^T's codes
     static constexpr int TILE_BYTES = (kTile * PITCH * 4 + 15) / 16 * 16;
-    static constexpr int BYTES = TILE_BYTES + kTile * CODES_PITCH + 2 * SCALES + NB * kTile * 4;
+    static constexpr int BYTES = TILE_BYTES + kTile * CODES_PITCH + 2 * SCALES + NB * kTile * 4 + 512;
 };
 
 template <int FMT, class T>
@@ -96,39 +120,52 @@ __global__ void __launch_bounds__(kBothThreads)
     uint8_t* const rscales = tcodes + kTile * S::CODES_PITCH;
     uint8_t* const tscales = rscales + S::SCALES;
     float* const sums = reinterpret_cast<float*>(tscales + S::SCALES);  // [NB][kTile]
+    float* const factors = sums + NB * kTile;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, k0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    const float ts = FMT == kNv && tscale ? *tscale : 1.f;
-    const float six_ts = __fmul_rn(6.f, ts);
+    const TensorScale ts = tensor_scale(FMT == kNv ? tscale : nullptr);
+    if constexpr (FMT == kNv) {
+        fill_factors(factors, ts.ts);
+        __syncthreads();
+    }
     const int64_t ldq = fp4_codes_ld(K), ldt = fp4_codes_ld(M);
     // place of (row, block) in this tile's scale tiles
     auto scale_at = [](int r, int b) { return (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3); };
 
-    // the tile, zero outside X, and the blocks along its rows
-#pragma unroll 2
-    for (int i = threadIdx.x; i < kTile * NB; i += kBothThreads) {
-        const int m = i / NB, b = i % NB;
-        const int64_t k = k0 + b * B;
-        const bool in = m0 + m < M;
-        uint32_t w[W];
-        if (in && k < K) {
-            load_words<T, B>(X + (m0 + m) * ldx + k, static_cast<int>(min(K - k, int64_t(B))), aligned, w);
-        } else {
+    // the tile, zero outside X, and the blocks along its rows; a thread's blocks are
+    // loaded (U at a time) before the first is quantized
+    constexpr int ITERS = kTile * NB / kBothThreads, U = 32 / W < ITERS ? 32 / W : ITERS;
+#pragma unroll 1
+    for (int i0 = 0; i0 < ITERS; i0 += U) {
+        uint32_t w[U][W];
 #pragma unroll
-            for (int j = 0; j < W; ++j) w[j] = 0;
+        for (int u = 0; u < U; ++u) {
+            const int i = (i0 + u) * kBothThreads + threadIdx.x, m = i / NB, b = i % NB;
+            const int64_t k = k0 + b * B;
+            if (m0 + m < M && k < K) {
+                load_words<T, B>(X + (m0 + m) * ldx + k, static_cast<int>(min(K - k, int64_t(B))), aligned, w[u]);
+            } else {
+#pragma unroll
+                for (int j = 0; j < W; ++j) w[u][j] = 0;
+            }
         }
 #pragma unroll
-        for (int j = 0; j < W; ++j) tile[m * PITCH + b * W + j] = w[j];
-        if (Xq) {
-            uint32_t codes[B / 8];
-            rscales[scale_at(m, b)] = static_cast<uint8_t>(quantize_words<FMT, T>(w, ts, six_ts, codes));
-            if (in && k < 2 * ldq) {
-                uint8_t* q = Xq + (m0 + m) * ldq + k / 2;
-                if constexpr (B == 16)
-                    *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
-                else
-                    *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+        for (int u = 0; u < U; ++u) {
+            const int i = (i0 + u) * kBothThreads + threadIdx.x, m = i / NB, b = i % NB;
+            const int64_t k = k0 + b * B;
+#pragma unroll
+            for (int j = 0; j < W; ++j) tile[m * PITCH + b * W + j] = w[u][j];
+            if (Xq) {
+                uint32_t codes[B / 8];
+                rscales[scale_at(m, b)] = static_cast<uint8_t>(quantize_words<FMT, T>(w[u], ts, factors, codes));
+                if (m0 + m < M && k < 2 * ldq) {
+                    uint8_t* q = Xq + (m0 + m) * ldq + k / 2;
+                    if constexpr (B == 16)
+                        *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
+                    else
+                        *reinterpret_cast<uint4*>(q) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+                }
             }
         }
     }
@@ -158,7 +195,7 @@ __global__ void __launch_bounds__(kBothThreads)
             }
             const int k = PER * c + h;
             if (Tq) {
-                tscales[scale_at(k, b)] = static_cast<uint8_t>(quantize_words<FMT, T>(w, ts, six_ts, codes));
+                tscales[scale_at(k, b)] = static_cast<uint8_t>(quantize_words<FMT, T>(w, ts, factors, codes));
                 uint8_t* q = tcodes + k * S::CODES_PITCH + b * (B / 2);
                 if constexpr (B == 16)
                     *reinterpret_cast<uint2*>(q) = make_uint2(codes[0], codes[1]);
@@ -225,31 +262,41 @@ __global__ void __launch_bounds__(kAmaxThreads)
     pdl_launch_dependents();
     const int64_t per_row = (K + V - 1) / V, step = static_cast<int64_t>(gridDim.x) * kAmaxThreads;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kAmaxThreads + threadIdx.x;
-    uint32_t m = 0;
-    for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
-        const T* const x = X + row * ldx;
-        // four loads in flight a thread
-        for (int64_t i = first; i < per_row; i += 4 * step) {
-            uint32_t w[4][4];
+    // one pass over the thread's share, four loads in flight; without `finite`
+    // infinities and NaN count as what their bits are, above all else
+    auto share = [&](auto finite) {
+        uint32_t m = 0;
+        for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
+            const T* const x = X + row * ldx;
+            for (int64_t i = first; i < per_row; i += 4 * step) {
+                uint32_t w[4][4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t k = (i + u * step) * V;
-                load_words<T, V>(x + k, static_cast<int>(max(int64_t(0), min(K - k, int64_t(V)))), aligned, w[u]);
-            }
+                for (int u = 0; u < 4; ++u) {
+                    const int64_t k = (i + u * step) * V;
+                    load_words<T, V>(x + k, static_cast<int>(max(int64_t(0), min(K - k, int64_t(V)))), aligned, w[u]);
+                }
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
+                for (int u = 0; u < 4; ++u) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (sizeof(T) == 4) {
-                        m = max(m, finite_abs_bits(__uint_as_float(w[u][j])));
-                    } else {
-                        const float2 f = unpack2<T>(w[u][j]);
-                        m = max(m, max(finite_abs_bits(f.x), finite_abs_bits(f.y)));
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (sizeof(T) == 4) {
+                            const uint32_t v = w[u][j] & 0x7fffffffu;
+                            m = max(m, decltype(finite)::value ? finite_abs_bits(__uint_as_float(v)) : v);
+                        } else if constexpr (decltype(finite)::value) {
+                            const float2 f = unpack2<T>(w[u][j]);
+                            m = max(m, max(finite_abs_bits(f.x), finite_abs_bits(f.y)));
+                        } else {
+                            m = __vmaxu2(m, w[u][j] & 0x7fff7fffu);
+                        }
                     }
                 }
             }
         }
-    }
+        if constexpr (sizeof(T) == 2 && !decltype(finite)::value) m = packed_amax_bits<T>(m);
+        return m;
+    };
+    uint32_t m = share(std::false_type{});
+    if (m >= 0x7f800000u) m = share(std::true_type{});
     m = __reduce_max_sync(0xffffffffu, m);
     __shared__ uint32_t wm[kAmaxThreads / 32];
     if ((threadIdx.x & 31) == 0) wm[threadIdx.x >> 5] = m;
@@ -274,32 +321,48 @@ __global__ void __launch_bounds__(32) k_fp4_scale_join(const uint32_t* __restric
 
 // ------------------------------------------------------- back to values
 
+// One thread takes 16 values a step and walks down the rows, as above; its two
+// 16-byte stores are one of 32 bytes where rows are aligned to that.  Bound by
+// memory (0.56 or 0.53 bytes in, 2 or 4 out per value).
 constexpr int kDequantThreads = 256;
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kDequantThreads)
-    k_fp4_dequantize(int64_t M, int64_t K, const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
-                     const float* __restrict__ tscale, T* __restrict__ Y, int64_t ldy, bool aligned) {
+    k_fp4_dequantize(int64_t M, int64_t K, int log_tx, const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
+                     const float* __restrict__ tscale, T* __restrict__ Y, int64_t ldy, bool aligned, bool sectors) {
     constexpr int B = fp4_block(FMT);
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const int64_t per_row = (K + 15) / 16;  // one thread takes 16 values
-    const int64_t item = static_cast<int64_t>(blockIdx.x) * kDequantThreads + threadIdx.x;
-    const int64_t row = item / per_row, k = (item - row * per_row) * 16;
-    if (row >= M) return;
+    const int tx = 1 << log_tx, ty = kDequantThreads >> log_tx;
+    const int64_t k = (static_cast<int64_t>(blockIdx.y) * tx + (threadIdx.x & (tx - 1))) * 16;
+    if (k >= K) return;
     const float ts = FMT == kNv && tscale ? *tscale : 1.f;
-    const uint2 q = *reinterpret_cast<const uint2*>(Xq + row * fp4_codes_ld(K) + k / 2);
-    const uint32_t byte = Xs[fp4_scale_offset(row, k / B, fp4_col_tiles(FMT, K))];
-    const float d = __fmul_rn(scale_value<FMT>(byte), ts);
-    float lo[8], hi[8], x[16];
-    e2m1x8_values(q.x, lo);
-    e2m1x8_values(q.y, hi);
+    const int n = static_cast<int>(min(K - k, int64_t(16)));
+    const int64_t step = static_cast<int64_t>(gridDim.x) * ty, ld = fp4_codes_ld(K);
+    const int64_t tiles = fp4_col_tiles(FMT, K), blk = k / B;
+    int64_t row = static_cast<int64_t>(blockIdx.x) * ty + (threadIdx.x >> log_tx);
+    const uint8_t* q = Xq + row * ld + k / 2;
+    const uint8_t* const s0 = Xs + (blk >> 2) * 512 + (blk & 3);
+    T* y = Y + row * ldy + k;
+#pragma unroll 2
+    for (; row < M; row += step, q += step * ld, y += step * ldy) {
+        const uint2 c = *reinterpret_cast<const uint2*>(q);
+        const uint32_t r = static_cast<uint32_t>(row) & 127u;
+        const uint32_t byte = s0[(row >> 7) * tiles * 512 + (r & 31u) * 16 + (r >> 5) * 4];
+        const float d = __fmul_rn(scale_value<FMT>(byte), ts);
+        float lo[8], hi[8], x[16];
+        e2m1x8_values(c.x, lo);
+        e2m1x8_values(c.y, hi);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = __fmul_rn(lo[i], d);
-        x[8 + i] = __fmul_rn(hi[i], d);
+        for (int i = 0; i < 8; ++i) {
+            x[i] = __fmul_rn(lo[i], d);
+            x[8 + i] = __fmul_rn(hi[i], d);
+        }
+        if (sectors && n == 16)
+            store_sectors(y, x);
+        else
+            store_some<T, 16>(y, n, aligned, x);
     }
-    store_some<T, 16>(Y + row * ldy + k, static_cast<int>(min(K - k, int64_t(16))), aligned, x);
 }
 
 // ------------------------------------------------------- host side
@@ -308,23 +371,36 @@ static bool rows_aligned(const void* p, int64_t ld, size_t elem, int64_t rows) {
     return aligned16(p) && (rows <= 1 || (static_cast<size_t>(ld) * elem) % 16 == 0);
 }
 
+// Cut of a kernel whose threads walk down the rows: 2^log_tx threads along a
+// row, grid.y over the row, and in grid.x enough CTAs for eight an SM.
+struct Walk {
+    int log_tx;
+    dim3 grid;
+};
+static Walk walk(int64_t rows, int64_t per_row, int threads) {
+    Walk w;
+    w.log_tx = 2;
+    while (w.log_tx < 8 && (int64_t(1) << w.log_tx) < per_row) ++w.log_tx;
+    const int64_t ty = threads >> w.log_tx;
+    const int64_t gy = (per_row + (int64_t(1) << w.log_tx) - 1) >> w.log_tx;
+    const int64_t most = 8 * num_sms(current_device()) / gy + 1;
+    const int64_t gx = (rows + ty - 1) / ty;
+    w.grid = dim3(static_cast<unsigned>(gx < most ? gx : most), static_cast<unsigned>(gy));
+    return w;
+}
+
 int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                      uint8_t* Xq, uint8_t* Xs, bool zero_pad, cudaStream_t s) {
     const int64_t rows = zero_pad ? (M + 127) / 128 * 128 : M;
     const int64_t per_row = 4 * fp4_col_tiles(fmt, K);
     if (rows == 0 || per_row == 0) return QG_OK;
-    int log_tx = 2;
-    while (log_tx < 8 && (int64_t(1) << log_tx) < per_row) ++log_tx;
-    const int64_t ty = kQuantThreads >> log_tx, gx = (rows + ty - 1) / ty;
-    int64_t gy = (per_row + (int64_t(1) << log_tx) - 1) >> log_tx;
-    if (gx > INT32_MAX) return QG_ERR_UNSUPPORTED;
-    if (gy > 65535) gy = 65535;
+    const Walk w = walk(rows, per_row, kQuantThreads);
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const bool al = rows_aligned(X, ldx, sizeof(T), M);
         auto* f = fmt == kNv ? k_fp4_quantize<kNv, T> : k_fp4_quantize<kMx, T>;
-        return launch_serialized(f, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kQuantThreads, 0, 1, s,
-                                 M, rows, K, log_tx, static_cast<const T*>(X), ldx, al, ts, Xq, Xs);
+        return launch_serialized(f, w.grid, kQuantThreads, 0, 1, s, M, rows, K, w.log_tx, static_cast<const T*>(X), ldx,
+                                 al, ts, Xq, Xs);
     });
 }
 
@@ -395,10 +471,12 @@ QG_BLOCK_KERNEL_BUDGET("k_fp4_scale_join", reinterpret_cast<const void*>(k_fp4_s
 
 using namespace qg;
 
+constexpr int64_t kMaxCols = int64_t(1) << 27;  // grid.y covers a row
+
 // Checks shared by the calls that read a rows x K matrix of floating type.
 static int check_matrix(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx) {
     if (!fmt_ok(fmt) || !dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
-    if (M < 0 || K < 0 || M > INT32_MAX || K > INT32_MAX) return QG_ERR_INVALID_ARG;
+    if (M < 0 || K < 0 || M > INT32_MAX || K > kMaxCols) return QG_ERR_INVALID_ARG;
     if (M && K && !X) return QG_ERR_INVALID_ARG;
     if (M > 1 && ldx < K) return QG_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(X) % dtype_bytes(dtype)) return QG_ERR_MISALIGNED;
@@ -486,14 +564,14 @@ int fp4_dequantize(int fmt, int dtype, int64_t M, int64_t K, const uint8_t* Xq, 
     if (!Xq || !Xs) return QG_ERR_INVALID_ARG;
     if (!aligned16(Xq) || !aligned16(Xs)) return QG_ERR_MISALIGNED;
     if (current_device() < 0) return QG_ERR_CUDA;
-    const int64_t items = M * ((K + 15) / 16), ctas = (items + kDequantThreads - 1) / kDequantThreads;
-    if (ctas > INT32_MAX) return QG_ERR_UNSUPPORTED;
+    const Walk w = walk(M, (K + 15) / 16, kDequantThreads);
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         auto* f = fmt == kNv ? k_fp4_dequantize<kNv, T> : k_fp4_dequantize<kMx, T>;
-        return launch_serialized(f, dim3(static_cast<unsigned>(ctas)), kDequantThreads, 0, 1,
-                                 static_cast<cudaStream_t>(stream), M, K, Xq, Xs, tscale, static_cast<T*>(Y), ldy,
-                                 rows_aligned(Y, ldy, sizeof(T), M));
+        const bool sectors = (reinterpret_cast<uintptr_t>(Y) & 31u) == 0 &&
+                             (M <= 1 || static_cast<size_t>(ldy) * sizeof(T) % 32 == 0);
+        return launch_serialized(f, w.grid, kDequantThreads, 0, 1, static_cast<cudaStream_t>(stream), M, K, w.log_tx, Xq,
+                                 Xs, tscale, static_cast<T*>(Y), ldy, rows_aligned(Y, ldy, sizeof(T), M), sectors);
     });
 }
 

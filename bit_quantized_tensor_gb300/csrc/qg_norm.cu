@@ -12,18 +12,15 @@ namespace qg {
 // and the first lane of every four blocks their scale word.  All lanes of the
 // warp take part; positions behind D hold 0.
 template <int FMT>
-__device__ __forceinline__ void quantize_lane8(const float (&y)[8], int64_t k, int64_t D, int64_t row, float ts,
-                                               float six_ts, uint8_t* Xq, uint8_t* Xs) {
+__device__ __forceinline__ void quantize_lane8(const float (&y)[8], int64_t k, int64_t D, int64_t row,
+                                               const TensorScale& ts, uint8_t* Xq, uint8_t* Xs) {
     constexpr int LANES = fp4_block(FMT) / 8;
     uint32_t m = absmax_bits<8>(y);
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const BlockScale s = block_scale<FMT>(m, ts, six_ts);
-    float q[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q[j] = __fmul_rn(y[j], s.r);
+    const BlockScale s = block_scale<FMT>(m, ts);
     const int64_t ld = fp4_codes_ld(D), tiles = fp4_col_tiles(FMT, D);
-    if (k < 2 * ld) *reinterpret_cast<uint32_t*>(Xq + row * ld + k / 2) = e2m1x8(q);
+    if (k < 2 * ld) *reinterpret_cast<uint32_t*>(Xq + row * ld + k / 2) = scaled_codes8(y, s.r);
     const int blk = (threadIdx.x & 31) / LANES;
     uint32_t word = s.byte << (8 * (blk & 3));
     word |= __shfl_xor_sync(0xffffffffu, word, LANES);
@@ -108,8 +105,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    const float ts = FMT == kNv && p.ts ? *p.ts : 1.f;
-    const float six_ts = __fmul_rn(6.f, ts);
+    const TensorScale ts = tensor_scale(FMT == kNv ? p.ts : nullptr);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         if constexpr (VEC) {
@@ -122,7 +118,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
             for (int j = 0; j < 8; ++j)
                 y[j] = k + j < D ? fmaf((v[8 * i + j] - mean) * rstd, g[j], b[j]) : 0.f;
             if constexpr (FMT >= 0)
-                quantize_lane8<FMT>(y, k, p.D, row, ts, six_ts, p.Xq, p.Xs);
+                quantize_lane8<FMT>(y, k, p.D, row, ts, p.Xq, p.Xs);
             else if (k < D)
                 store_some<T, 8>(static_cast<T*>(p.Y) + row * p.ldy + k, D - k, p.y_vec, y);
         } else {
@@ -183,8 +179,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
     for (int s = 0; s < slots; ++s)
         if (row + s * step < p.M) row_fetch<TPR, EDGES>(ring, s, X + (row + s * step) * p.ldx, row + s * step, p.M);
     __syncthreads();
-    const float ts = FMT == kNv && p.ts ? *p.ts : 1.f;
-    const float six_ts = __fmul_rn(6.f, ts);
+    const TensorScale ts = tensor_scale(FMT == kNv ? p.ts : nullptr);
     const float inv_d = __frcp_rn(static_cast<float>(D));
     // values before column 0 in a row's first piece
     const int lead = FMT < 0 && EDGES
@@ -281,7 +276,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
                     f[2 * j] = h.x;
                     f[2 * j + 1] = h.y;
                 }
-                quantize_lane8<FMT>(f, k, p.D, row, ts, six_ts, p.Xq, p.Xs);
+                quantize_lane8<FMT>(f, k, p.D, row, ts, p.Xq, p.Xs);
             } else {
                 store_piece<T>(static_cast<T*>(p.Y) + row * p.ldy, k, D, !EDGES || p.y_vec, y);
             }
@@ -326,8 +321,7 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const NormPara
         if (p.mean) p.mean[row] = mean;
         if (p.rstd) p.rstd[row] = rstd;
     }
-    const float ts = FMT == kNv && p.ts ? *p.ts : 1.f;
-    const float six_ts = __fmul_rn(6.f, ts);
+    const TensorScale ts = tensor_scale(FMT == kNv ? p.ts : nullptr);
     for (int64_t k0 = 0; k0 < D; k0 += kLongThreads * 8) {  // whole warps, for the shuffles
         const int64_t k = k0 + threadIdx.x * 8;
         const int n = static_cast<int>(max(int64_t(0), min(D - k, int64_t(8))));
@@ -338,7 +332,7 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const NormPara
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = j < n ? fmaf((u[j] - mean) * rstd, g[j], b[j]) : 0.f;
         if constexpr (FMT >= 0)
-            quantize_lane8<FMT>(y, k, D, row, ts, six_ts, p.Xq, p.Xs);
+            quantize_lane8<FMT>(y, k, D, row, ts, p.Xq, p.Xs);
         else if (n > 0)
             store_some<T, 8>(static_cast<T*>(p.Y) + row * p.ldy + k, n, p.y_vec, y);
     }

@@ -455,7 +455,8 @@ int w4a4_gemm_prepacked(int64_t M, int64_t N, int64_t K,
  * Codes and scales are 16-byte aligned.  Matrices of floating type (qg_dtype)
  * are row-major with any leading dimension >= their row length and any address
  * their element size allows; 16-byte aligned rows are read and written faster.
- * Sizes may be 0 unless stated otherwise: nothing is enqueued for an empty
+ * Sizes are at most 2^27 (row counts of the quantizers and norms 2^31 - 1) and
+ * may be 0 unless stated otherwise: nothing is enqueued for an empty
  * result, and a product over nothing is its bias (or 0).
  * Calls are asynchronous on `stream`, may be captured in a CUDA graph, and give
  * the same bits on every run.  Outputs must not overlap inputs. */

@@ -62,7 +62,7 @@ def _linear(L, fmt=0, dt=1, M=4, N=8, K=64, X=P, ldx=64, w=P, sw=P, Y=P, ldy=8, 
 
 def test_product_refusals(L):
     assert _gemm(L, fmt=7) == 2 and _gemm(L, dt=-1) == 2 and _gemm(L, fmt=1, ta=P) == 2 and _gemm(L, fmt=1, tb=P) == 2
-    assert _gemm(L, M=-1) == 1 and _gemm(L, K=(1 << 30) + 1) == 1 and _gemm(L, ldy=7) == 1
+    assert _gemm(L, M=-1) == 1 and _gemm(L, K=(1 << 27) + 1) == 1 and _gemm(L, ldy=7) == 1
     for name in ("a", "sa", "b", "sb", "Y"):
         assert _gemm(L, **{name: None}) == 1, name
     for name in ("a", "sa", "b", "sb"):
