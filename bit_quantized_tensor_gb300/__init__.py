@@ -487,8 +487,31 @@ def w4a4_gemm_prepacked(Xq, Xscale, packed, N: int, K: int, XU=None, Vt=None, bi
 # ---------------------------------------------------------------- microscaled 4-bit, layer norm
 #
 # A small call takes a few microseconds on the device, so the host side counts:
-# each operand is looked at once, and the current stream comes as a raw handle
-# (the stream object that torch.cuda.current_stream() builds costs 3 us).
+# the ordinary call goes through _host(); for the others each operand is looked
+# at once, and the current stream comes as a raw handle (the stream object that
+# torch.cuda.current_stream() builds costs 3 us).
+
+_host_module = None
+_HOST_ENTRIES = ("qg_workspace_size", "fp4_tensor_scale", "fp4_quantize", "fp4_dequantize", "fp4_gemm", "fp4_linear",
+                 "fp4_linear_backward", "layer_norm", "layer_norm_fp4", "layer_norm_backward")
+
+
+def _host():
+    """csrc/qg_host.cpp: the ordinary call of each function below, in C++.  Its functions
+    return None for any other call, which then goes through ctypes."""
+    global _host_module
+    if _host_module is None:
+        _torch()
+        L = lib()
+        try:
+            from . import _qg_host
+        except ImportError as e:
+            raise RuntimeError("_qg_host.so is missing or does not load: build it with `python -c \"import "
+                               "__graft_entry__ as g; g.build()\"`") from e
+        _qg_host.bind([ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _HOST_ENTRIES])
+        _host_module = _qg_host
+    return _host_module
+
 
 _dtype_ids = None
 
@@ -600,15 +623,17 @@ def _vector(t, name, n, dtype, device):
 
 
 def _scratch(ws, need, device, stream):
-    """The caller's workspace, or a new one that stays alive for `stream`."""
+    """Address and size of the caller's workspace, or of a new one that stays alive for `stream`."""
     if ws is None:
-        ws = _torch_module.empty(need if need > 256 else 256, dtype=_torch_module.uint8, device=device)
+        if need == 0:
+            return None, None, 0
+        ws = _torch_module.empty(need, dtype=_torch_module.uint8, device=device)
         if stream is not None:
             ws.record_stream(stream)
     else:
         _on(ws, "ws", device)
         need = ws.numel() * ws.element_size()
-    return ws, need
+    return ws, ws.data_ptr(), need
 
 
 def _weights(gamma, beta, D, xdtype, device):
@@ -628,6 +653,10 @@ def _weights(gamma, beta, D, xdtype, device):
 
 def fp4_tensor_scale(X, out=None, ws=None, stream=None):
     """The "nv" tensor scale of X: max(|x|) / 2688 over its finite values, one fp32 on the device."""
+    if out is None and ws is None and stream is None:
+        scale = _host().fp4_tensor_scale(X)
+        if scale is not None:
+            return scale
     torch = _torch()
     ld = _matrix(X, "X")
     dev = X.device
@@ -635,15 +664,19 @@ def fp4_tensor_scale(X, out=None, ws=None, stream=None):
     if out is None:
         out = torch.empty(1, dtype=torch.float32, device=dev)
     ptr = _one_f32(out, "out", "nv", dev)
-    ws, wsb = _scratch(ws, 4096, dev, stream)
+    ws, wsp, wsb = _scratch(ws, 4096, dev, stream)
     M, K = X.shape
-    _check("fp4_tensor_scale", lib().fp4_tensor_scale(dt, M, K, X.data_ptr(), ld, ptr, ws.data_ptr(), wsb,
+    _check("fp4_tensor_scale", lib().fp4_tensor_scale(dt, M, K, X.data_ptr(), ld, ptr, wsp, wsb,
                                                       _raw_stream(stream, dev)))
     return out
 
 
 def fp4_quantize(X, fmt: str = "nv", scale=None, out=None, stream=None):
     """X (M x K) -> (codes, scales), blocks along its rows; scale: the "nv" tensor scale (None = 1)."""
+    if out is None and stream is None:
+        both = _host().fp4_quantize(X, fmt, scale)
+        if both is not None:
+            return both
     _torch()
     f = _fmt_id(fmt)
     ld = _matrix(X, "X")
@@ -684,6 +717,10 @@ def fp4_quantize_both(X, fmt: str = "nv", scale=None, out=None, stream=None):
 
 def fp4_dequantize(Xq, Xs, K: int, fmt: str = "nv", scale=None, dtype=None, Y=None, stream=None):
     """The values (M x K) of a packed operand, in `dtype` (default: that of Y, or float32)."""
+    if Y is None and stream is None:
+        values = _host().fp4_dequantize(Xq, Xs, K, fmt, scale, dtype)
+        if values is not None:
+            return values
     torch = _torch()
     f = _fmt_id(fmt)
     M = _packed(Xq, Xs, "X", fmt, K)
@@ -702,6 +739,10 @@ def fp4_dequantize(Xq, Xs, K: int, fmt: str = "nv", scale=None, dtype=None, Y=No
 def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None, bias=None, dtype=None,
              Y=None, stream=None):
     """Y = A . B^T + bias of packed A (M x K) and B (N x K), in `dtype` (default: that of Y, or bfloat16)."""
+    if Y is None and stream is None:
+        product = _host().fp4_gemm(Aq, As, Bq, Bs, K, fmt, a_scale, b_scale, bias, dtype)
+        if product is not None:
+            return product
     torch = _torch()
     f = _fmt_id(fmt)
     M = _packed(Aq, As, "A", fmt, K)
@@ -725,6 +766,10 @@ def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None
 
 def fp4_linear(X, Wq, Ws, fmt: str = "nv", x_scale=None, w_scale=None, bias=None, Y=None, ws=None, stream=None):
     """Y = Q(X) . W^T + bias with packed weights W (N x K); X (M x K) is quantized in the call, Y has its type."""
+    if Y is None and ws is None and stream is None:
+        product = _host().fp4_linear(X, Wq, Ws, fmt, x_scale, w_scale, bias)
+        if product is not None:
+            return product
     torch = _torch()
     f = _fmt_id(fmt)
     ldx = _matrix(X, "X")
@@ -739,11 +784,11 @@ def fp4_linear(X, Wq, Ws, fmt: str = "nv", x_scale=None, w_scale=None, bias=None
     else:
         ldy = _matrix(Y, "Y", dev, dtype, M, N)
     L = lib()
-    ws, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K), dev, stream)
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K), dev, stream)
     _check("fp4_linear", L.fp4_linear(
         f, dt, M, N, K, X.data_ptr(), ldx, _one_f32(x_scale, "x_scale", fmt, dev), Wq.data_ptr(), Ws.data_ptr(),
         _one_f32(w_scale, "w_scale", fmt, dev), _vector(bias, "bias", N, dtype, dev), Y.data_ptr(), ldy,
-        ws.data_ptr(), wsb, _raw_stream(stream, dev)))
+        wsp, wsb, _raw_stream(stream, dev)))
     return Y
 
 
@@ -756,6 +801,10 @@ def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale
     results of fp4_quantize_both(W)).  dX and dW have the type of dY, db (the
     column sums of dY) is fp32.  A gradient that is not needed is None.
     """
+    if need_dx and need_dw and need_db and out is None and ws is None and stream is None:
+        grads = _host().fp4_linear_backward(dY, X, Wtq, Wts, fmt, dy_scale, x_scale, w_scale)
+        if grads is not None:
+            return grads
     torch = _torch()
     f = _fmt_id(fmt)
     lddy = _matrix(dY, "dY")
@@ -777,13 +826,13 @@ def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale
     if dX is None and dW is None and db is None:
         return out
     L = lib()
-    ws, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K), dev, stream)
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K), dev, stream)
     _check("fp4_linear_backward", L.fp4_linear_backward(
         f, dt, M, N, K, dY.data_ptr(), lddy, _one_f32(dy_scale, "dy_scale", fmt, dev), X.data_ptr(), ldx,
         _one_f32(x_scale, "x_scale", fmt, dev), Wtq.data_ptr(), Wts.data_ptr(),
         _one_f32(w_scale, "w_scale", fmt, dev), None if dX is None else dX.data_ptr(), lddx,
         None if dW is None else dW.data_ptr(), lddw, _vector(db, "db", N, torch.float32, dev),
-        ws.data_ptr(), wsb, _raw_stream(stream, dev)))
+        wsp, wsb, _raw_stream(stream, dev)))
     return out
 
 
@@ -801,6 +850,10 @@ def _stats(stats, M, device):
 
 def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, Y=None, stats=None, stream=None):
     """(Y, mean, rstd) of the rows of X (M x D); gamma and beta in X's type or fp32 (None = 1, 0)."""
+    if Y is None and stats is None and stream is None:
+        result = _host().layer_norm(X, gamma, beta, eps)
+        if result is not None:
+            return result
     torch = _torch()
     ldx = _matrix(X, "X")
     dev, dtype = X.device, X.dtype
@@ -820,7 +873,14 @@ def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, Y=None, stats=None, 
 
 def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv", scale=None, out=None, stats=None,
                    stream=None):
-    """(codes, scales, mean, rstd): layer_norm of X with y quantized instead of stored."""
+    """(codes, scales, mean, rstd): layer_norm of X with y quantized instead of stored.
+
+    mean and rstd are None unless stats is True (new ones) or gives the two tensors.
+    """
+    if out is None and stream is None and (stats is None or stats is True):
+        result = _host().layer_norm_fp4(X, gamma, beta, eps, fmt, scale, stats is True)
+        if result is not None:
+            return result
     _torch()
     f = _fmt_id(fmt)
     ldx = _matrix(X, "X")
@@ -834,15 +894,20 @@ def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv",
         Xq, Xs = out
         if _packed(Xq, Xs, "out", fmt, D, dev) != M:
             raise ValueError(f"out must have {M} rows")
-    mean, rstd = _stats(stats, M, dev)
+    mean, rstd = (None, None) if stats is None else _stats(None if stats is True else stats, M, dev)
     _check("layer_norm_fp4", lib().layer_norm_fp4(
         f, dt, M, D, X.data_ptr(), ldx, g, b, wd, eps, _one_f32(scale, "scale", fmt, dev), Xq.data_ptr(),
-        Xs.data_ptr(), mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev)))
+        Xs.data_ptr(), None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
+        _raw_stream(stream, dev)))
     return Xq, Xs, mean, rstd
 
 
 def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None):
     """(dX, dgamma, dbeta) of layer_norm, with the mean and rstd it returned; dgamma and dbeta are fp32."""
+    if out is None and ws is None and stream is None:
+        grads = _host().layer_norm_backward(dY, X, gamma, mean, rstd)
+        if grads is not None:
+            return grads
     torch = _torch()
     ldx = _matrix(X, "X")
     dev, dtype, f32 = X.device, X.dtype, torch.float32
@@ -858,9 +923,9 @@ def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None
         dX, dgamma, dbeta = out
         lddx = _matrix(dX, "dX", dev, dtype, M, D)
     L = lib()
-    ws, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D), dev, stream)
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D), dev, stream)
     _check("layer_norm_backward", L.layer_norm_backward(
         dt, M, D, dY.data_ptr(), lddy, X.data_ptr(), ldx, g, wd, _vector(mean, "mean", M, f32, dev),
         _vector(rstd, "rstd", M, f32, dev), dX.data_ptr(), lddx, _vector(dgamma, "dgamma", D, f32, dev),
-        _vector(dbeta, "dbeta", D, f32, dev), ws.data_ptr(), wsb, _raw_stream(stream, dev)))
+        _vector(dbeta, "dbeta", D, f32, dev), wsp, wsb, _raw_stream(stream, dev)))
     return dX, dgamma, dbeta

@@ -5,8 +5,9 @@ repository root, then nvcc links them into
 ``bit_quantized_tensor_gb300/libqgemm.so`` with the CUDA runtime linked
 statically (the library has no run-time dependency on libcudart or
 libcuda; the driver's tensor-map encoder is fetched through the runtime's
-entry-point query).  A build is skipped when the library is newer than every
-source and header.
+entry-point query).  Beside it g++ builds ``_qg_host.so``, the torch-facing
+host side of the small calls.  A build is skipped when both are newer than
+every source and header.
 """
 from __future__ import annotations
 
@@ -22,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqgemm.so")
+HOST_SRC = os.path.join(CSRC, "qg_host.cpp")
+HOST = os.path.join(PKG, "_qg_host.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -43,16 +46,35 @@ def sources() -> list[str]:
 
 
 def _deps() -> list[str]:
-    return (sources() + glob.glob(os.path.join(CSRC, "*.cuh"))
+    return (sources() + [HOST_SRC] + glob.glob(os.path.join(CSRC, "*.cuh"))
             + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
             + [os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(HOST):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def build_host() -> None:
+    """The Python extension of csrc/qg_host.cpp, against the torch that is installed."""
+    import sysconfig
+
+    import torch
+    tdir = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = HOST + f".tmp{os.getpid()}"
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-o", tmp, HOST_SRC, "-I", INCLUDE,
+           "-I", os.path.join(tdir, "include"), "-I", os.path.join(tdir, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-L", os.path.join(tdir, "lib"), "-lc10", "-ltorch_cpu", "-lc10_cuda", "-ltorch_cuda", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, HOST)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -74,8 +96,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        host = ex.submit(build_host)
         objs = list(ex.map(compile_one, srcs))
+        host.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

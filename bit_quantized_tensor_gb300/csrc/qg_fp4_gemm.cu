@@ -214,7 +214,15 @@ static size_t packed_scales(int64_t rows, int64_t K) {
     return up256(static_cast<size_t>(fp4_scale_bytes(kNv, rows, K)));
 }
 
-size_t fp4_linear_workspace(int64_t M, int64_t K) { return packed_codes(M, K) + packed_scales(M, K); }
+// Are M tokens quantized inside the product's kernel?
+static bool quantized_inside(int64_t M) {
+    const int nt = g_fp4_nt.load();
+    return M <= 16 && (nt == 0 || nt == 16);
+}
+
+size_t fp4_linear_workspace(int64_t M, int64_t K) {
+    return quantized_inside(M) ? 0 : packed_codes(M, K) + packed_scales(M, K);
+}
 
 size_t fp4_linear_backward_workspace(int64_t M, int64_t N, int64_t K) {
     return packed_codes(M, N) + packed_scales(M, N) + packed_codes(N, M) + packed_scales(N, M) +
@@ -309,13 +317,14 @@ int fp4_linear(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const void* 
     if (M == 0 || N == 0) return QG_OK;
     if (!Y || (M > 1 && (ldy < N || ldx < K)) || (K > 0 && (!X || !Wq || !Ws))) return QG_ERR_INVALID_ARG;
     if (!aligned16(Wq) || !aligned16(Ws)) return QG_ERR_MISALIGNED;
-    if (K > 0 && (!ws || ws_bytes < fp4_linear_workspace(M, K))) return QG_ERR_WORKSPACE;
+    const bool inside = quantized_inside(M);
+    if (K > 0 && !inside && (!ws || ws_bytes < fp4_linear_workspace(M, K))) return QG_ERR_WORKSPACE;
     if (reinterpret_cast<uintptr_t>(ws) & 255u) return QG_ERR_MISALIGNED;
     const int dev = current_device();
     if (dev < 0 || dev >= 64) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return only_bias(dtype, M, N, bias, Y, ldy, s);
-    if (plan_fp4(M, N, K, whole_sectors(Y, ldy, dtype), num_sms(dev)).nt == 16)
+    if (inside)
         return fp4_linear_few(fmt, dtype, M, N, K, X, ldx, x_tscale, {Wq, Ws, N, w_tscale}, bias, Y, ldy, dev, s);
     Carver c{static_cast<uint8_t*>(ws)};
     uint8_t* xq = c.take(packed_codes(M, K));

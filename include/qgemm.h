@@ -507,7 +507,9 @@ int fp4_gemm(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const uint8_t 
 
 /* Y = Q(X) . W^T + bias: fp4_quantize of X (M x K, `dtype`) and fp4_gemm with
  * the packed weights W (N x K) in one call.
- *  ws: qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K) bytes, 256-byte aligned. */
+ *  ws: qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K) bytes, 256-byte aligned; 0
+ *      bytes (ws may be NULL) for up to 16 tokens, which the product's kernel
+ *      quantizes itself. */
 int fp4_linear(int fmt, int dtype, int64_t M, int64_t N, int64_t K, const void *X, int64_t ldx,
                const float *x_tscale, const uint8_t *Wq, const uint8_t *Ws, const float *w_tscale,
                const void *bias, void *Y, int64_t ldy, void *ws, size_t ws_bytes, void *stream);

@@ -26,7 +26,8 @@ def test_packed_sizes(L):
 
 def test_workspace_sizes(L):
     ws = L.qg_workspace_size
-    assert ws(qg.QG_OP_FP4_LINEAR, 1, 4096, 4096) == 2048 + 64 * 512
+    assert ws(qg.QG_OP_FP4_LINEAR, 17, 4096, 4096) == 17 * 2048 + 64 * 512
+    assert ws(qg.QG_OP_FP4_LINEAR, 16, 4096, 4096) == 0  # quantized inside the product
     assert ws(qg.QG_OP_LAYER_NORM_BACKWARD, 1, 1, 100) >= 2 * 100 * 4
     assert ws(qg.QG_OP_FP4_TENSOR_SCALE, 1, 1, 1) > 0
     assert ws(qg.QG_OP_FP4_LINEAR_BACKWARD, 64, 64, 64) > 0
@@ -56,7 +57,7 @@ def _gemm(L, fmt=0, dt=1, M=4, N=8, K=64, a=P, sa=P, ta=None, b=P, sb=P, tb=None
     return L.fp4_gemm(fmt, dt, M, N, K, a, sa, ta, b, sb, tb, bias, Y, ldy, None)
 
 
-def _linear(L, fmt=0, dt=1, M=4, N=8, K=64, X=P, ldx=64, w=P, sw=P, Y=P, ldy=8, ws=P, wsb=BIG):
+def _linear(L, fmt=0, dt=1, M=40, N=8, K=64, X=P, ldx=64, w=P, sw=P, Y=P, ldy=8, ws=P, wsb=BIG):
     return L.fp4_linear(fmt, dt, M, N, K, X, ldx, None, w, sw, None, None, Y, ldy, ws, wsb, None)
 
 

@@ -261,7 +261,7 @@ def test_linear_is_quantize_then_gemm(torch, qg, M, N, K, fmt):
     # strided activations, another stream, a workspace full of NaN bytes
     wide = torch.empty((M, K + 9), dtype=X.dtype, device="cuda")
     wide[:, 1:K + 1] = X
-    ws = torch.full((qg.workspace_size(qg.QG_OP_FP4_LINEAR, M, N, K),), 255, dtype=torch.uint8, device="cuda")
+    ws = torch.full((max(256, qg.workspace_size(qg.QG_OP_FP4_LINEAR, M, N, K)),), 255, dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     y = qg.fp4_linear(wide[:, 1:K + 1], *w, fmt, x_scale=xs, bias=bias, ws=ws, stream=side)
@@ -396,7 +396,7 @@ def test_refusals(torch, qg):
     with pytest.raises(ValueError, match="Y must be"):
         qg.fp4_linear(X, q, s, "nv", Y=torch.empty((4, 5), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(qg.QgError, match="QG_ERR_WORKSPACE"):
-        qg.fp4_linear(X, q, s, "nv", ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
+        qg.fp4_linear(X.repeat(10, 1), q, s, "nv", ws=torch.empty(8, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError, match="W\\^T"):
         qg.fp4_linear_backward(torch.ones((4, 64), dtype=torch.bfloat16, device="cuda"), X, q, s, "nv")
     assert qg.fp4_linear(X, q, s, "nv").shape == (4, 4)  # and the context is intact

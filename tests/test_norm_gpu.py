@@ -116,7 +116,9 @@ def test_forward_to_codes(torch, qg, M, D, fmt, dtype):
     X = on_gpu(torch, rows(M, D, 7 + D), dtype)
     g, b = params(torch, D, dtype)
     scale = torch.full((1,), 0.03, device="cuda") if fmt == "nv" and M % 2 else None
-    q, s, mean, rstd = qg.layer_norm_fp4(X, g, b, EPS, fmt, scale=scale)
+    q, s, mean, rstd = qg.layer_norm_fp4(X, g, b, EPS, fmt, scale=scale, stats=True)
+    q2, s2, none, none2 = qg.layer_norm_fp4(X, g, b, EPS, fmt, scale=scale)
+    assert torch.equal(q, q2) and torch.equal(s, s2) and none is None and none2 is None
     _, mean2, rstd2 = qg.layer_norm(X, g, b, EPS)
     # same statistics as the plain norm up to the order of the sums
     assert np.allclose(as_np(mean), as_np(mean2), rtol=1e-5, atol=1e-6) and np.allclose(as_np(rstd), as_np(rstd2), rtol=1e-5)
