@@ -213,10 +213,52 @@ __device__ __forceinline__ void cut_piece(uint64_t (&v)[4], int k, int D) {
         v[j] = two(a >= 0 && a < D ? f.x : 0.f, a + 1 >= 0 && a + 1 < D ? f.y : 0.f);
     }
 }
+// What is left of a piece, as a mask on its words in memory; at most the first
+// and the last piece of a row are cut, so a thread keeps one mask for each.
 template <class T>
-__device__ __forceinline__ void load_piece(const T* p, int k, int D, uint64_t (&v)[4]) {
-    load_pairs<T>(p, v);
-    if (piece_cut(k, D)) cut_piece(v, k, D);
+struct PieceMask {
+    uint32_t w[2 * sizeof(T)];
+};
+template <class T>
+__device__ __forceinline__ PieceMask<T> piece_mask(int k, int D) {
+    PieceMask<T> m;
+    auto in = [&](int j) { return k + j >= 0 && k + j < D; };
+#pragma unroll
+    for (int i = 0; i < 2 * static_cast<int>(sizeof(T)); ++i) {
+        if constexpr (sizeof(T) == 4)
+            m.w[i] = in(i) ? 0xffffffffu : 0u;
+        else
+            m.w[i] = (in(2 * i) ? 0xffffu : 0u) | (in(2 * i + 1) ? 0xffff0000u : 0u);
+    }
+    return m;
+}
+template <class T>
+__device__ __forceinline__ void load_piece(const T* p, uint64_t (&v)[4], const PieceMask<T>& a, bool use_a,
+                                           const PieceMask<T>& b, bool use_b) {
+    constexpr int W = 2 * static_cast<int>(sizeof(T));
+    uint32_t w[W];
+#pragma unroll
+    for (int i = 0; i < W; i += 4) {
+        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = q.x; w[i + 1] = q.y; w[i + 2] = q.z; w[i + 3] = q.w;
+    }
+    if (use_a) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] &= a.w[i];
+    }
+    if (use_b) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] &= b.w[i];
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+            v[j] = two(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+        } else {
+            const float2 f = unpack2<T>(w[j]);
+            v[j] = two(f.x, f.y);
+        }
+    }
 }
 // To memory: whole where p is the start of a 16-byte piece, else one by one.
 template <class T>

@@ -21,7 +21,7 @@ constexpr int kQuantThreads = 256;
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kQuantThreads)
-    k_fp4_quantize(int64_t M, int64_t rows, int64_t K, int log_tx, const T* __restrict__ X, int64_t ldx, bool aligned,
+    k_fp4_quantize(int64_t M, int64_t rows, int64_t K, int log_tx, const T* __restrict__ X, int64_t ldx,
                    const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
     constexpr int B = fp4_block(FMT);
     __shared__ float factors[128];
@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kQuantThreads)
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             if (some && row + u * step < M) {
-                load_words<T, B>(x, n, aligned, w[u]);
+                load_words<T, B>(x, n, true, w[u]);
             } else {
 #pragma unroll
                 for (int i = 0; i < W; ++i) w[u][i] = 0;  // also a block behind K
@@ -79,6 +79,43 @@ __global__ void __launch_bounds__(kQuantThreads)
             const uint32_t r = static_cast<uint32_t>(here) & 127u;
             if ((threadIdx.x & 3) == 0)
                 *reinterpret_cast<uint32_t*>(s0 + (here >> 7) * tiles * 512 + (r & 31u) * 16 + (r >> 5) * 4) = word;
+        }
+    }
+}
+
+// Rows whose addresses are not 16-byte aligned: one value a lane, neighbours in
+// neighbouring lanes, so that a warp still reads whole lines (a block a thread,
+// read value by value, took 7 us for 777 x 1333 fp32).  A warp takes 32 / B
+// blocks a step; a block's maximum is found with shuffles over its lanes, each
+// lane makes one code, and three more shuffles put eight of them into a word.
+template <int FMT, class T>
+__global__ void __launch_bounds__(kQuantThreads)
+    k_fp4_quantize_lanes(int64_t M, int64_t rows, int64_t K, const T* __restrict__ X, int64_t ldx,
+                         const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
+    constexpr int B = fp4_block(FMT);
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    const TensorScale ts = tensor_scale(FMT == kNv ? tscale : nullptr);
+    const int lane = threadIdx.x & 31;
+    const int64_t tiles = fp4_col_tiles(FMT, K), ld = fp4_codes_ld(K);
+    const int64_t steps = tiles * (4 * B / 32);  // of 32 values, up to whole scale words
+    const int64_t warps = static_cast<int64_t>(gridDim.x) * (kQuantThreads / 32);
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (kQuantThreads / 32) + (threadIdx.x >> 5);
+    for (int64_t row = blockIdx.y; row < rows; row += gridDim.y) {
+        const T* const x = X + row * ldx;
+        for (int64_t s = first; s < steps; s += warps) {
+            const int64_t k = s * 32 + lane;
+            const float v = row < M && k < K ? to_f32<T>(x[k]) : 0.f;
+            uint32_t m = __float_as_uint(v) & 0x7fffffffu;
+#pragma unroll
+            for (int o = B / 2; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const BlockScale b = block_scale<FMT>(m, ts);
+            const float y[8] = {__fmul_rn(v, b.r), 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+            uint32_t w = (e2m1x8(y) & 0xfu) << (4 * (lane & 7));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) w |= __shfl_xor_sync(0xffffffffu, w, o);
+            if ((lane & 7) == 0 && row < M && k < 2 * ld) *reinterpret_cast<uint32_t*>(Xq + row * ld + k / 2) = w;
+            if (lane % B == 0) Xs[fp4_scale_offset(row, k / B, tiles)] = static_cast<uint8_t>(b.byte);
         }
     }
 }
@@ -329,7 +366,7 @@ constexpr int kDequantThreads = 256;
 template <int FMT, class T>
 __global__ void __launch_bounds__(kDequantThreads)
     k_fp4_dequantize(int64_t M, int64_t K, int log_tx, const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
-                     const float* __restrict__ tscale, T* __restrict__ Y, int64_t ldy, bool aligned, bool sectors) {
+                     const float* __restrict__ tscale, T* __restrict__ Y, int64_t ldy, bool sectors) {
     constexpr int B = fp4_block(FMT);
     pdl_wait_prior_grid();
     pdl_launch_dependents();
@@ -361,7 +398,30 @@ __global__ void __launch_bounds__(kDequantThreads)
         if (sectors && n == 16)
             store_sectors(y, x);
         else
-            store_some<T, 16>(y, n, aligned, x);
+            store_some<T, 16>(y, n, true, x);
+    }
+}
+
+// The same into rows that are not 16-byte aligned: one value a lane.
+template <int FMT, class T>
+__global__ void __launch_bounds__(kDequantThreads)
+    k_fp4_dequantize_lanes(int64_t M, int64_t K, const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
+                           const float* __restrict__ tscale, T* __restrict__ Y, int64_t ldy) {
+    constexpr int B = fp4_block(FMT);
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    const float ts = FMT == kNv && tscale ? *tscale : 1.f;
+    const int64_t tiles = fp4_col_tiles(FMT, K), ld = fp4_codes_ld(K);
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kDequantThreads;
+    for (int64_t row = blockIdx.y; row < M; row += gridDim.y) {
+        for (int64_t k = static_cast<int64_t>(blockIdx.x) * kDequantThreads + threadIdx.x; k < K; k += step) {
+            const uint32_t code = Xq[row * ld + k / 2] >> (4 * (k & 1)) & 0xfu;
+            const float d = __fmul_rn(scale_value<FMT>(Xs[fp4_scale_offset(row, k / B, tiles)]), ts);
+            // e2m1: exponent code >> 1, one bit behind the point (0 and 0.5 below exponent 1)
+            const uint32_t c = code & 7u;
+            const float v = static_cast<float>(c > 1 ? (2u + (c & 1u)) << (c >> 1) : 2u * c) * 0.25f;
+            Y[row * ldy + k] = from_f32<T>(__fmul_rn(code & 8u ? -v : v, d));
+        }
     }
 }
 
@@ -389,6 +449,15 @@ static Walk walk(int64_t rows, int64_t per_row, int threads) {
     return w;
 }
 
+// Cut of a kernel with one value a thread: grid.y over rows, grid.x along them,
+// 16 CTAs an SM.
+static dim3 row_grid(int64_t rows, int64_t cols, int threads) {
+    const int64_t gx = (cols + threads - 1) / threads;
+    int64_t gy = 16 * num_sms(current_device()) / gx + 1;
+    if (gy > rows) gy = rows;
+    return dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy < 65535 ? gy : 65535));
+}
+
 int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                      uint8_t* Xq, uint8_t* Xs, bool zero_pad, cudaStream_t s) {
     const int64_t rows = zero_pad ? (M + 127) / 128 * 128 : M;
@@ -398,9 +467,14 @@ int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, in
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const bool al = rows_aligned(X, ldx, sizeof(T), M);
+        if (!al) {
+            auto* f = fmt == kNv ? k_fp4_quantize_lanes<kNv, T> : k_fp4_quantize_lanes<kMx, T>;
+            return launch_serialized(f, row_grid(rows, per_row * fp4_block(fmt), kQuantThreads), kQuantThreads, 0, 1, s,
+                                     M, rows, K, static_cast<const T*>(X), ldx, ts, Xq, Xs);
+        }
         auto* f = fmt == kNv ? k_fp4_quantize<kNv, T> : k_fp4_quantize<kMx, T>;
         return launch_serialized(f, w.grid, kQuantThreads, 0, 1, s, M, rows, K, w.log_tx, static_cast<const T*>(X), ldx,
-                                 al, ts, Xq, Xs);
+                                 ts, Xq, Xs);
     });
 }
 
@@ -446,8 +520,12 @@ static dim3 amax_grid(int64_t M, int64_t K, size_t elem) {
 }
 
 #define QG_FP4_BUDGETS(T, NAME)                                                                              \
-    QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize<nv," NAME ">", reinterpret_cast<const void*>(k_fp4_quantize<kNv, T>), \
+    QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize_lanes<nv," NAME ">", reinterpret_cast<const void*>(k_fp4_quantize_lanes<kNv, T>), \
                            kQuantThreads, 0, 0, 1, 4);                                                       \
+    QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize_lanes<mx," NAME ">", reinterpret_cast<const void*>(k_fp4_quantize_lanes<kMx, T>), \
+                           kQuantThreads, 0, 0, 1, 4);                                                       \
+    QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize<nv," NAME ">", reinterpret_cast<const void*>(k_fp4_quantize<kNv, T>), \
+                           kQuantThreads, 0, 0, 1, 2);                                                       \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize<mx," NAME ">", reinterpret_cast<const void*>(k_fp4_quantize<kMx, T>), \
                            kQuantThreads, 0, 0, 1, 4);                                                       \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_quantize_both<nv," NAME ">",                                               \
@@ -458,6 +536,10 @@ static dim3 amax_grid(int64_t M, int64_t K, size_t elem) {
                            (BothSmem<kMx, T>::BYTES), 0, 1, 2);                                              \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_amax<" NAME ">", reinterpret_cast<const void*>(k_fp4_amax<T>), kAmaxThreads, \
                            0, 0, 1, 2);                                                                      \
+    QG_BLOCK_KERNEL_BUDGET("k_fp4_dequantize_lanes<nv," NAME ">", reinterpret_cast<const void*>(k_fp4_dequantize_lanes<kNv, T>), \
+                           kDequantThreads, 0, 0, 1, 4);                                                       \
+    QG_BLOCK_KERNEL_BUDGET("k_fp4_dequantize_lanes<mx," NAME ">", reinterpret_cast<const void*>(k_fp4_dequantize_lanes<kMx, T>), \
+                           kDequantThreads, 0, 0, 1, 4);                                                       \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_dequantize<nv," NAME ">",                                                  \
                            reinterpret_cast<const void*>(k_fp4_dequantize<kNv, T>), kDequantThreads, 0, 0, 1, 4); \
     QG_BLOCK_KERNEL_BUDGET("k_fp4_dequantize<mx," NAME ">",                                                  \
@@ -568,10 +650,15 @@ int fp4_dequantize(int fmt, int dtype, int64_t M, int64_t K, const uint8_t* Xq, 
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         auto* f = fmt == kNv ? k_fp4_dequantize<kNv, T> : k_fp4_dequantize<kMx, T>;
+        if (!rows_aligned(Y, ldy, sizeof(T), M)) {
+            auto* g = fmt == kNv ? k_fp4_dequantize_lanes<kNv, T> : k_fp4_dequantize_lanes<kMx, T>;
+            return launch_serialized(g, row_grid(M, K, kDequantThreads), kDequantThreads, 0, 1,
+                                     static_cast<cudaStream_t>(stream), M, K, Xq, Xs, tscale, static_cast<T*>(Y), ldy);
+        }
         const bool sectors = (reinterpret_cast<uintptr_t>(Y) & 31u) == 0 &&
                              (M <= 1 || static_cast<size_t>(ldy) * sizeof(T) % 32 == 0);
         return launch_serialized(f, w.grid, kDequantThreads, 0, 1, static_cast<cudaStream_t>(stream), M, K, w.log_tx, Xq,
-                                 Xs, tscale, static_cast<T*>(Y), ldy, rows_aligned(Y, ldy, sizeof(T), M), sectors);
+                                 Xs, tscale, static_cast<T*>(Y), ldy, sectors);
     });
 }
 

@@ -186,6 +186,11 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
                          ? static_cast<int>((reinterpret_cast<uintptr_t>(X + row * p.ldx) & 15) / sizeof(T))
                          : 0;
     auto first = [&](int i) { return (i * TPR + t) * 8 - lead; };  // column of step i
+    // what the row leaves of its first piece and of its last
+    const int last_piece = (D - 1 + lead) / 8, last_step = last_piece / TPR;
+    const PieceMask<T> head = piece_mask<T>(t == 0 ? -lead : 0, D < 8 ? 8 : D);
+    const PieceMask<T> tail = piece_mask<T>(t == last_piece % TPR ? last_piece * 8 - lead : 0,
+                                            t == last_piece % TPR ? D : 8);
     uint64_t hg[4 * VPT], hb[4 * VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
@@ -214,7 +219,10 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
             uint64_t u[4] = {0, 0, 0, 0};
             if (k < D) {
                 if constexpr (PIECES) {
-                    load_piece<T>(x + k, k, D, u);
+                    if constexpr (EDGES || FMT >= 0)
+                        load_piece<T>(x + k, u, head, i == 0, tail, i == last_step);
+                    else
+                        load_pairs<T>(x + k, u);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -403,7 +411,7 @@ static int norm_by_size(const NormParams& p, int dev, cudaStream_t s) {
         if (D <= 8192) return launch_norm<T, 1024, 1, FMT, VEC>(p, s);
     } else if (D <= kMaxRingFwd) {
         const int64_t same = same_place_rows(p.ldx, sizeof(T));
-        const bool edges = !p.x_vec || p.D * sizeof(T) % 16 != 0;
+        const bool edges = !p.x_vec || (FMT < 0 ? p.D % 8 : p.D * static_cast<int64_t>(sizeof(T)) % 16) != 0;
         // y is stored in pieces where its rows start at the same places as those of x
         NormParams q = p;
         q.y_vec = FMT >= 0 || (reinterpret_cast<uintptr_t>(p.X) % 16 == reinterpret_cast<uintptr_t>(p.Y) % 16 &&

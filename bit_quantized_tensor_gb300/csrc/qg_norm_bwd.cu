@@ -146,9 +146,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // column of value j of step i, and whether the thread has none left
     auto column = [&](int i, int j) { return VEC ? (i * TPR + t) * 8 - lead + j : (8 * i + j) * TPR + t; };
     auto step_done = [&](int i) { return VEC ? column(i, 0) >= D : 8 * i * TPR >= D; };
+    // what the row leaves of its first piece and of its last
+    const int last_piece = (D - 1 + lead) / 8, last_step = last_piece / TPR;
+    const PieceMask<T> head = piece_mask<T>(t == 0 ? -lead : 0, D < 8 ? 8 : D);
+    const PieceMask<T> tail = piece_mask<T>(t == last_piece % TPR ? last_piece * 8 - lead : 0,
+                                            t == last_piece % TPR ? D : 8);
     auto values = [&](const T* x, int i, uint64_t(&v)[4]) {
         if constexpr (VEC && EDGES) {
-            load_piece<T>(x + column(i, 0), column(i, 0), D, v);
+            load_piece<T>(x + column(i, 0), v, head, i == 0, tail, i == last_step);
         } else if constexpr (VEC) {
             load_pairs<T>(x + column(i, 0), v);
         } else {
