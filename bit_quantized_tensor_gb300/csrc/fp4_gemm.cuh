@@ -39,17 +39,27 @@ __device__ __forceinline__ uint32_t elect_lane() {
     return e;
 }
 
+// Shared-memory descriptors, of which only the low word (start address >> 4)
+// differs: built as a 32-bit sum, since a 64-bit one costs dependent uniform
+// instructions in front of every issue.  kRowsHi: rows of 128 bytes, 128-byte
+// swizzle, 1024 bytes between groups of 8 rows; kScalesHi: a scale tile, 32 rows
+// of 16 bytes, no swizzle, 128 bytes between groups of 8 rows; version 1.
+constexpr uint32_t kRowsHi = (1024u >> 4) | (1u << 14) | (2u << 29), kScalesHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t rows_lo(uint32_t smem_addr) { return ((smem_addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t scales_lo(uint32_t smem_addr) { return (smem_addr & 0x3FFFFu) >> 4; }
+
 #define QG_FP4_MMA(GROUP, KIND)                                                                              \
-    asm volatile("{\n.reg .pred p, q;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"                       \
-                 "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%4], [%5], p;\n}" ::"r"( \
+    asm volatile("{\n.reg .pred p, q;\n.reg .b64 da, db;\nsetp.ne.b32 p, %6, 0;\nsetp.ne.b32 q, %7, 0;\n"   \
+                 "mov.b64 da, {%1, %8};\nmov.b64 db, {%2, %8};\n"                                            \
+                 "@q tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], da, db, %3, [%4], [%5], p;\n}" ::"r"( \
                      d_tmem),                                                                                \
-                 "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected)       \
+                 "r"(alo), "r"(blo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected), "r"(kRowsHi) \
                  : "memory")
 
 // PAIR: M = 256 across the two CTAs of a cluster, issued by the leader.
 template <int FMT, bool PAIR>
-__device__ __forceinline__ void fp4_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t elected) {
+__device__ __forceinline__ void fp4_mma(uint32_t d_tmem, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t sfa,
+                                        uint32_t sfb, uint32_t accumulate, uint32_t elected) {
     if constexpr (FMT == kNv && !PAIR)
         QG_FP4_MMA("1", "mxf4nvf4.block_scale.block16");
     else if constexpr (FMT == kNv)
@@ -63,18 +73,17 @@ __device__ __forceinline__ void fp4_mma(uint32_t d_tmem, uint64_t adesc, uint64_
 // One 512-byte scale tile from shared memory into four columns of tensor
 // memory, repeated in each quarter of the lanes (PAIR: in both CTAs, each from
 // its own shared memory).
+#define QG_FP4_COPY(GROUP)                                                                                 \
+    asm volatile("{\n.reg .pred q;\n.reg .b64 d;\nsetp.ne.b32 q, %2, 0;\nmov.b64 d, {%1, %3};\n"           \
+                 "@q tcgen05.cp.cta_group::" GROUP ".32x128b.warpx4 [%0], d;\n}" ::"r"(tmem),               \
+                 "r"(lo), "r"(elected), "r"(kScalesHi)                                                     \
+                 : "memory")
 template <bool PAIR>
-__device__ __forceinline__ void fp4_copy_scales(uint32_t tmem, uint64_t desc, uint32_t elected) {
+__device__ __forceinline__ void fp4_copy_scales(uint32_t tmem, uint32_t lo, uint32_t elected) {
     if constexpr (PAIR)
-        asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(
-                         tmem),
-                     "l"(desc), "r"(elected)
-                     : "memory");
+        QG_FP4_COPY("2");
     else
-        asm volatile("{\n.reg .pred q;\nsetp.ne.b32 q, %2, 0;\n@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(
-                         tmem),
-                     "l"(desc), "r"(elected)
-                     : "memory");
+        QG_FP4_COPY("1");
 }
 
 // tma_load_2d and tma_load_2d_pair of an elected lane.
@@ -95,13 +104,6 @@ __device__ __forceinline__ void fp4_load_pair(uint32_t dst, const void* tmap, in
         "[%1, {%2, %3}], [%4];\n}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(cluster_bar), "r"(elected)
         : "memory");
-}
-
-// Shared-memory descriptor of a scale tile: 32 rows of 16 bytes, no swizzle,
-// 128 bytes between groups of 8 rows, descriptor version 1.
-__device__ __forceinline__ uint64_t fp4_scale_desc(uint32_t smem_addr) {
-    return static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 32) |
-           (static_cast<uint64_t>(1u) << 46);
 }
 
 // ------------------------------------------------ one CTA per tile
@@ -218,7 +220,8 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     float* const join = reinterpret_cast<float*>(smem + STAGES * Cfg::STAGE_BYTES + Cfg::BARRIER_BYTES);
-    auto a_smem = [&](int s) { return smem_u32(smem + s * Cfg::STAGE_BYTES); };
+    const uint32_t ring0 = smem_u32(smem);
+    auto a_smem = [&](int s) { return ring0 + static_cast<uint32_t>(s) * Cfg::STAGE_BYTES; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int splits = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);  // the cluster
@@ -309,21 +312,22 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
             }
             tc_fence_after();
             const int steps = min(4, (p.K - kb * kFp4Bk + 63) / 64);  // none behind K: its scales may be stale
-            const uint32_t a = a_smem(ps.slot()), b = a + Cfg::A_BYTES;
-            const uint32_t sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
+            const uint32_t at = a_smem(ps.slot());
+            const uint32_t a = rows_lo(at), b = a + Cfg::A_BYTES / 16;
+            const uint32_t sa = scales_lo(at) + (Cfg::A_BYTES + Cfg::B_BYTES) / 16, sb = sa + Cfg::S_BYTES / 16;
             const int atoms = FMT == kNv ? steps : (steps + 1) / 2;
 #pragma unroll
             for (int j = 0; j < Cfg::ATOMS; ++j) {
                 if (j >= atoms) break;
-                fp4_copy_scales<false>(tmem + Cfg::SFA_COL + 4 * j, fp4_scale_desc(sa + 512 * j), elected);
-                fp4_copy_scales<false>(tmem + Cfg::SFB_COL + 4 * j, fp4_scale_desc(sb + 512 * j), elected);
+                fp4_copy_scales<false>(tmem + Cfg::SFA_COL + 4 * j, sa + 32 * j, elected);
+                fp4_copy_scales<false>(tmem + Cfg::SFB_COL + 4 * j, sb + 32 * j, elected);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (j >= steps) break;
                 const uint32_t col = FMT == kNv ? 4u * j : 4u * (j >> 1);
                 const uint32_t id = FMT == kNv ? 0u : 2u * (j & 1);
-                fp4_mma<FMT, false>(tmem, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
+                fp4_mma<FMT, false>(tmem, a + 2u * j, b + 2u * j,
                                     fp4_idesc<FMT>(128, NT, id), tmem + Cfg::SFA_COL + col,
                                     tmem + Cfg::SFB_COL + col, (kb > kb0 || j > 0) ? 1u : 0u, elected);
             }

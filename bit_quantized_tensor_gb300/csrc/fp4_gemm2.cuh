@@ -105,7 +105,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 4);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     uint8_t* const out_smem = smem + STAGES * Cfg::STAGE_BYTES + Cfg::BARRIER_BYTES;
-    auto stage_smem = [&](int s) { return smem_u32(smem + s * Cfg::STAGE_BYTES); };
+    const uint32_t ring0 = smem_u32(smem);
+    auto stage_smem = [&](int s) { return ring0 + static_cast<uint32_t>(s) * Cfg::STAGE_BYTES; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_ctarank();
@@ -194,6 +195,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             // ------------------------------------------------ MMA issuer (leader)
             const uint32_t elected = elect_lane();
             Ring<STAGES> ps;
+            const int last_steps = (p.K - (num_kb - 1) * kFp4Bk + 63) / 64;  // of 64, in a row's last block
             int n = 0;  // tiles begun
             bool ok = true;
             for (int t = pair; ok && t < ntiles; t += npairs, ++n) {
@@ -210,26 +212,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t a = stage_smem(ps.slot()), b = a + Cfg::A_BYTES;
-                    const uint32_t sa = b + Cfg::B_BYTES, sb = sa + Cfg::S_BYTES;
-                    const int steps = min(4, (p.K - kb * kFp4Bk + 63) / 64);  // none behind K
-                    const int atoms = FMT == kNv ? steps : (steps + 1) / 2;
-#pragma unroll
-                    for (int j = 0; j < ATOMS; ++j) {
-                        if (j >= atoms) break;
-                        fp4_copy_scales<true>(tmem + Cfg::SFA_COL + 4 * j, fp4_scale_desc(sa + 512 * j), elected);
-                        fp4_copy_scales<true>(tmem + Cfg::SFB_COL + 8 * j, fp4_scale_desc(sb + 512 * j), elected);
-                        fp4_copy_scales<true>(tmem + Cfg::SFB_COL + 8 * j + 4,
-                                              fp4_scale_desc(sb + Cfg::S_BYTES + 512 * j), elected);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (j >= steps) break;
+                    const uint32_t at = stage_smem(ps.slot());
+                    const uint32_t a = rows_lo(at), b = a + Cfg::A_BYTES / 16;
+                    const uint32_t sa = scales_lo(at) + (Cfg::A_BYTES + Cfg::B_BYTES) / 16, sb = sa + Cfg::S_BYTES / 16;
+                    auto scales = [&](int j) {
+                        fp4_copy_scales<true>(tmem + Cfg::SFA_COL + 4 * j, sa + 32 * j, elected);
+                        fp4_copy_scales<true>(tmem + Cfg::SFB_COL + 8 * j, sb + 32 * j, elected);
+                        fp4_copy_scales<true>(tmem + Cfg::SFB_COL + 8 * j + 4, sb + Cfg::S_BYTES / 16 + 32 * j, elected);
+                    };
+                    auto mma = [&](int j) {
                         const uint32_t atom = FMT == kNv ? j : j >> 1;
                         const uint32_t id = FMT == kNv ? 0u : 2u * (j & 1);
-                        fp4_mma<FMT, true>(d, smem_desc_sw128(a + 32u * j), smem_desc_sw128(b + 32u * j),
-                                           fp4_idesc<FMT>(256, 256, id), tmem + Cfg::SFA_COL + 4 * atom,
-                                           tmem + Cfg::SFB_COL + 8 * atom, (kb > 0 || j > 0) ? 1u : 0u, elected);
+                        fp4_mma<FMT, true>(d, a + 2u * j, b + 2u * j, fp4_idesc<FMT>(256, 256, id),
+                                           tmem + Cfg::SFA_COL + 4 * atom, tmem + Cfg::SFB_COL + 8 * atom,
+                                           (kb > 0 || j > 0) ? 1u : 0u, elected);
+                    };
+                    if (kb + 1 < num_kb || last_steps == 4) {
+#pragma unroll
+                        for (int j = 0; j < ATOMS; ++j) scales(j);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) mma(j);
+                    } else {  // nothing behind K: its scales may be stale
+#pragma unroll
+                        for (int j = 0; j < ATOMS; ++j)
+                            if (j * (4 / ATOMS) < last_steps) scales(j);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (j < last_steps) mma(j);
                     }
                     if (elected) tc_commit_pair(empty_bar(ps.slot()), 0x3);
                     __syncwarp();
