@@ -196,9 +196,25 @@ __global__ void __launch_bounds__(kBothThreads)
     // place of (row, block) in this tile's scale tiles
     auto scale_at = [](int r, int b) { return (b >> 2) * 512 + (r & 31) * 16 + (r >> 5) * 4 + (b & 3); };
 
-    // the tile, zero outside X, and the blocks along its rows; a thread's blocks are
-    // loaded (U at a time) before the first is quantized
+    // the tile, zero outside X, and the blocks along its rows.  Aligned rows are
+    // loaded a block a thread (U at a time, before the first is quantized);
+    // others into the tile first, one value a lane and 16 rows of a warp in flight
     constexpr int ITERS = kTile * NB / kBothThreads, U = 32 / W < ITERS ? 32 / W : ITERS;
+    if (!aligned) {
+        T* const values = reinterpret_cast<T*>(tile);
+        constexpr int PER_WARP = kTile / (kBothThreads / 32), LANE_PITCH = PITCH * 4 / static_cast<int>(sizeof(T));
+        const int lane = threadIdx.x & 31, first = (threadIdx.x >> 5) * PER_WARP;
+#pragma unroll 1
+        for (int c = lane; c < kTile; c += 32) {
+            T v[PER_WARP];
+#pragma unroll
+            for (int j = 0; j < PER_WARP; ++j)
+                v[j] = m0 + first + j < M && k0 + c < K ? X[(m0 + first + j) * ldx + k0 + c] : from_f32<T>(0.f);
+#pragma unroll
+            for (int j = 0; j < PER_WARP; ++j) values[(first + j) * LANE_PITCH + c] = v[j];
+        }
+        __syncthreads();
+    }
 #pragma unroll 1
     for (int i0 = 0; i0 < ITERS; i0 += U) {
         uint32_t w[U][W];
@@ -206,8 +222,11 @@ __global__ void __launch_bounds__(kBothThreads)
         for (int u = 0; u < U; ++u) {
             const int i = (i0 + u) * kBothThreads + threadIdx.x, m = i / NB, b = i % NB;
             const int64_t k = k0 + b * B;
-            if (m0 + m < M && k < K) {
-                load_words<T, B>(X + (m0 + m) * ldx + k, static_cast<int>(min(K - k, int64_t(B))), aligned, w[u]);
+            if (!aligned) {
+#pragma unroll
+                for (int j = 0; j < W; ++j) w[u][j] = tile[m * PITCH + b * W + j];
+            } else if (m0 + m < M && k < K) {
+                load_words<T, B>(X + (m0 + m) * ldx + k, static_cast<int>(min(K - k, int64_t(B))), true, w[u]);
             } else {
 #pragma unroll
                 for (int j = 0; j < W; ++j) w[u][j] = 0;
@@ -217,8 +236,10 @@ __global__ void __launch_bounds__(kBothThreads)
         for (int u = 0; u < U; ++u) {
             const int i = (i0 + u) * kBothThreads + threadIdx.x, m = i / NB, b = i % NB;
             const int64_t k = k0 + b * B;
+            if (aligned) {
 #pragma unroll
-            for (int j = 0; j < W; ++j) tile[m * PITCH + b * W + j] = w[u][j];
+                for (int j = 0; j < W; ++j) tile[m * PITCH + b * W + j] = w[u][j];
+            }
             if (Xq) {
                 uint32_t codes[B / 8];
                 rscales[scale_at(m, b)] = static_cast<uint8_t>(quantize_words<FMT, T>(w[u], ts, factors, codes));
