@@ -62,6 +62,7 @@ int sum_partials_run(const float* partial, int64_t parts, int64_t n, float* out,
 // row i from the ring, and only then wait.  At the end each CTA adds up its
 // groups, in order, and leaves one row of partial sums.
 constexpr int kBwdThreads = 512;
+__host__ __device__ constexpr int bwd_sums(int tpr, int vpt) { return 8 * vpt * (tpr + 4); }  // places of a group's sums
 constexpr int kSiteNormSums = 402;
 
 // Sums of two values over a warp with one value's shuffles: the halves of the
@@ -106,7 +107,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     k_layer_norm_backward(const NormBwdParams p, int slots, const Ctl ctl) {
     constexpr int GROUPS = kBwdThreads / TPR, WARPS = TPR / 32;
     constexpr int E = 8 * VPT;
-    constexpr int COLS = TPR * E;
     extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ __align__(8) uint64_t bars[GROUPS][kRingMax];
     __shared__ __align__(8) uint64_t sum_bars[GROUPS];
@@ -324,24 +324,34 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         while (global_timer_ns() - t0 < 1000000) {
         }
     }
-    // every group's sums over the idle ring, then one row of partials
-    float* sums = reinterpret_cast<float*>(ring_smem);  // [GROUPS][2][COLS]
+    // every group's sums over the idle ring, then one row of partials.  Value e of
+    // thread t lies at e (TPR + 4) + t, where neighbouring threads write and
+    // neighbouring columns are read without meeting in a bank (column by column,
+    // eight lanes met in one, and the end of a CTA took 2 to 3 us)
+    float* sums = reinterpret_cast<float*>(ring_smem);  // [GROUPS][2][SUMS]
+    constexpr int SUMS = bwd_sums(TPR, VPT);
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-        const int k = column(e / 8, e % 8);
-        if (k < 0 || k >= D) continue;
         const float2 fg = both(dg[e / 2]), fb = both(db[e / 2]);
-        sums[2 * group * COLS + k] = e & 1 ? fg.y : fg.x;
-        sums[(2 * group + 1) * COLS + k] = e & 1 ? fb.y : fb.x;
+        sums[2 * group * SUMS + e * (TPR + 4) + t] = e & 1 ? fg.y : fg.x;
+        sums[(2 * group + 1) * SUMS + e * (TPR + 4) + t] = e & 1 ? fb.y : fb.x;
     }
     __syncthreads();
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.D;
+    const T* const first_row = X + static_cast<int64_t>(blockIdx.x) * GROUPS * p.ldx;
     for (int k = threadIdx.x; k < D; k += kBwdThreads) {
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            a += sums[2 * g * COLS + k];
-            b += sums[(2 * g + 1) * COLS + k];
+            // the thread and value that held column k in this group
+            int e = k / TPR, u = k % TPR;
+            if constexpr (VEC) {
+                const int l = k + (EDGES ? static_cast<int>((reinterpret_cast<uintptr_t>(first_row + g * p.ldx) & 15) / sizeof(T)) : 0);
+                u = l / 8 % TPR;
+                e = l / 8 / TPR * 8 + l % 8;
+            }
+            a += sums[2 * g * SUMS + e * (TPR + 4) + u];
+            b += sums[(2 * g + 1) * SUMS + e * (TPR + 4) + u];
         }
         out[k] = a;
         out[p.D + k] = b;
@@ -420,7 +430,7 @@ static int64_t bwd_smem(int tpr, int vpt, int64_t D, size_t elem, bool vec, int*
     const int64_t slot = 2 * row_slot_bytes(D * static_cast<int64_t>(elem));
     *slots = ring_slots(slot, groups, 3, 200 * 1024);  // two rows are in use at a time
     const int64_t ring = slot * *slots * groups + (vec ? 0 : (D + 7) / 8 * 32);
-    const int64_t sums = int64_t(groups) * 2 * tpr * vpt * 8 * 4;
+    const int64_t sums = int64_t(groups) * 2 * bwd_sums(tpr, vpt) * 4;
     return ring > sums ? ring : sums;
 }
 
