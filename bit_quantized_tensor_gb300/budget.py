@@ -2,6 +2,7 @@
 
     python -m bit_quantized_tensor_gb300.budget            # host only
     python -m bit_quantized_tensor_gb300.budget --measure  # + registers and residency (needs a GPU)
+    python -m bit_quantized_tensor_gb300.budget --table block  # the microscaled 4-bit operators and layer norm
 
 One row per kernel instance: threads, dynamic shared memory, tensor-memory
 columns, cluster size and the CTAs per SM the design counts on; with
@@ -56,8 +57,9 @@ def format_table(rows: list) -> str:
 def main() -> None:
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--measure", action="store_true", help="add registers and residency (needs a GPU)")
+    ap.add_argument("--table", choices=("gemm", "block"), default="gemm", help="which of the two tables")
     args = ap.parse_args()
-    rows = qg.kernel_budgets(measure=args.measure)
+    rows = qg.kernel_budgets(measure=args.measure, table=args.table)
     print(format_table(rows))
     bad = [(r["kernel"], accounting_errors(r)) for r in rows if accounting_errors(r)]
     for name, errs in bad:

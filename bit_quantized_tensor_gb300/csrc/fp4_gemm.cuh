@@ -121,7 +121,9 @@ __device__ __forceinline__ void fp4_load_pair(uint32_t dst, const void* tmap, in
 //              the ring themselves, which spares a small batch a kernel
 // With few tokens nothing but latency counts: the ring takes less than half an
 // SM's shared memory, so that a call's CTAs can set up and fetch their weights
-// while those of the call before it finish.
+// while those of the call before it finish.  16 tokens of 4096 f16 values by
+// 4096 rows of mx weights: 6.0 us a call in a chain, quantization included (9.0 MB,
+// mostly weights that the L2 holds: 1.5 TB/s); 777 x 1001 x 2304: 10 us.
 constexpr int kFp4Threads = 192;
 constexpr int kFp4Bk = 256;  // K of a stage: one 128-byte swizzled row of codes
 

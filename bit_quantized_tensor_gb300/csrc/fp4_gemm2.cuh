@@ -11,6 +11,14 @@
 // The epilogue drains the shared columns of a tile first and then lets the
 // MMAs of the next tile go, which write the other accumulator.  That costs the
 // tensor cores the time to drain 48 columns a tile instead of 256.
+//
+// Bound by the issuing warp: 4096 x 8192 x 8192 takes 86 us (6.4 PFLOP/s) with
+// blocks of 16 and 77 us (7.2) with blocks of 32, whose scales are half as many
+// copies; the MMAs alone would take 62 us, without the epilogue it is 2 to 3 us
+// less, and filling the ring costs about 3.  Slower were: 64-bit descriptor
+// arithmetic (95 us), a warp of its own for the scale copies with two sets of
+// scales in tensor memory (114), copies between the MMAs of a block (125), a
+// first look at the next block's barrier while one is issued (91).
 #pragma once
 #include "fp4_gemm.cuh"
 #include "tc_gemm.cuh"

@@ -55,14 +55,6 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 //
 // A group of TPR threads (a warp, or the CTA) has a ring of its own.
 
-template <int TPR>
-__device__ __forceinline__ void group_sync() {
-    if constexpr (TPR == 32)
-        __syncwarp();
-    else
-        __syncthreads();
-}
-
 struct RowRing {
     uint32_t bar0;      // mbarriers, one a slot
     uint8_t* slots;     // this group's slots
