@@ -9,42 +9,52 @@ namespace qg {
 
 // ------------------------------------------------------- sums of partials
 //
-// out[j] = sum over i of partial[i][j], in a fixed order: 32 slices of the
-// parts in parallel, each thread with its few loads in flight together, then
-// the slices pairwise.  Latency is all there is (152 x 1030: 7.6 us from launch
-// to end with 8 slices, whose threads waited for five rounds of loads, 6.4 us so).
-constexpr int kSumCols = 32, kSumSlices = 32;
+// out[j] = sum over i of partial[i][j], in a fixed order: SLICES slices of the
+// parts in parallel, each thread with up to eight loads in flight, then the
+// slices pairwise.  Few columns leave latency alone to count, and take 32 slices
+// (152 x 1030: 5.8 us; 7.6 with 8, whose threads wait for three rounds of loads);
+// with more than an SM has CTAs for, the instructions of a slice's end count, and
+// 8 slices do (152 x 16384, 10 MB: 6.6 us from launch to end, 9.8 with 32).
+constexpr int kSumCols = 32;
 
-__global__ void __launch_bounds__(kSumCols* kSumSlices)
+template <int SLICES>
+__global__ void __launch_bounds__(kSumCols* SLICES)
     k_sum_partials(const float* __restrict__ partial, int64_t parts, int64_t n, float* __restrict__ out0,
                    int64_t n0, float* __restrict__ out1) {
-    __shared__ float acc[kSumSlices][kSumCols + 1];
+    __shared__ float acc[SLICES][kSumCols + 1];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int c = threadIdx.x % kSumCols, s = threadIdx.x / kSumCols;
-    const int64_t j = static_cast<int64_t>(blockIdx.x) * kSumCols + c;
+    const int64_t col0 = static_cast<int64_t>(blockIdx.x) * kSumCols, step = SLICES * n;
+    const float* q = partial + s * n + col0 + c;
+    int left = col0 + c < n ? (static_cast<int>(parts) - s + SLICES - 1) / SLICES : 0;  // rows of this slice
     float a = 0.f;
-    for (int64_t i = s; i < parts; i += 8 * kSumSlices) {
+    for (; left > 0; left -= 8) {
         float v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            v[u] = j < n && i + u * kSumSlices < parts ? partial[(i + u * kSumSlices) * n + j] : 0.f;
+        for (int u = 0; u < 8; ++u, q += step) v[u] = u < left ? *q : 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) a += v[u];
     }
     acc[s][c] = a;
     __syncthreads();
-    // warp c, lane s: the slices of a column in the lanes of a warp
-    a = warp_sum(acc[threadIdx.x % 32][threadIdx.x / 32]);
-    const int64_t k = static_cast<int64_t>(blockIdx.x) * kSumCols + threadIdx.x / 32;
-    if (threadIdx.x % 32 == 0 && k < n) (k < n0 ? out0[k] : out1[k - n0]) = a;
+    // the slices of a column in neighbouring lanes
+    constexpr int PER_WARP = 32 / SLICES;
+    const int lane = threadIdx.x % 32, k = threadIdx.x / 32 * PER_WARP + lane / SLICES;
+    a = acc[lane % SLICES][k];
+#pragma unroll
+    for (int o = SLICES / 2; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+    if (lane % SLICES == 0 && col0 + k < n) (col0 + k < n0 ? out0[col0 + k] : out1[col0 + k - n0]) = a;
 }
 
 static int sum_partials2(const float* partial, int64_t parts, int64_t n, float* out0, int64_t n0, float* out1,
                          cudaStream_t s) {
     if (n == 0) return QG_OK;
-    return launch_serialized(k_sum_partials, dim3(static_cast<unsigned>((n + kSumCols - 1) / kSumCols)),
-                             kSumCols * kSumSlices, 0, 1, s, partial, parts, n, out0, n0, out1);
+    const int64_t ctas = (n + kSumCols - 1) / kSumCols;
+    const dim3 grid(static_cast<unsigned>(ctas));
+    if (ctas <= num_sms(current_device()))
+        return launch_serialized(k_sum_partials<32>, grid, kSumCols * 32, 0, 1, s, partial, parts, n, out0, n0, out1);
+    return launch_serialized(k_sum_partials<8>, grid, kSumCols * 8, 0, 1, s, partial, parts, n, out0, n0, out1);
 }
 
 int sum_partials_run(const float* partial, int64_t parts, int64_t n, float* out, cudaStream_t s) {
@@ -61,7 +71,7 @@ int sum_partials_run(const float* partial, int64_t parts, int64_t n, float* out,
 // the warps leave their part of row i + 1, arrive at a barrier, finish dx of
 // row i from the ring, and only then wait.  At the end each CTA adds up its
 // groups, in order, and leaves one row of partial sums.  8192 x 8192 bf16: 81 us,
-// 86 with the sums of the partial rows (4.7 TB/s), bound by the latency of a row's
+// 82.5 with the sums of the partial rows (4.9 TB/s), bound by the latency of a row's
 // arithmetic with four warps a scheduler; both of a row's sums exchanged at once
 // with its neighbour's, two rows a barrier, read the ring more often (113 us).
 // Rows that start inside a piece cost masks on top: 16411 x 515 f16 24 us,
@@ -543,8 +553,9 @@ QG_NORM_BWD(__half, "f16", 32, 3, true, false);
 QG_NORM_BWD(__half, "f16", 32, 3, true, true);
 QG_NORM_BWD(__nv_bfloat16, "bf16", 32, 3, true, false);
 QG_NORM_BWD(__nv_bfloat16, "bf16", 32, 3, true, true);
-QG_BLOCK_KERNEL_BUDGET("k_sum_partials", reinterpret_cast<const void*>(k_sum_partials), kSumCols* kSumSlices, 0, 0,
+QG_BLOCK_KERNEL_BUDGET("k_sum_partials<32>", reinterpret_cast<const void*>(k_sum_partials<32>), kSumCols * 32, 0, 0,
                        1, 1);
+QG_BLOCK_KERNEL_BUDGET("k_sum_partials<8>", reinterpret_cast<const void*>(k_sum_partials<8>), kSumCols * 8, 0, 0, 1, 4);
 
 }  // namespace qg
 
