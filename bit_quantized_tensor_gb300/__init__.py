@@ -496,7 +496,7 @@ _HOST_ENTRIES = ("qg_workspace_size", "fp4_tensor_scale", "fp4_quantize", "fp4_d
                  "fp4_linear_backward", "layer_norm", "layer_norm_fp4", "layer_norm_backward")
 
 
-def _host():
+def _ordinary():
     """csrc/qg_host.cpp: the ordinary call of each function below, in C++.  Its functions
     return None for any other call, which then goes through ctypes."""
     global _host_module
@@ -654,7 +654,7 @@ def _weights(gamma, beta, D, xdtype, device):
 def fp4_tensor_scale(X, out=None, ws=None, stream=None):
     """The "nv" tensor scale of X: max(|x|) / 2688 over its finite values, one fp32 on the device."""
     if out is None and ws is None and stream is None:
-        scale = _host().fp4_tensor_scale(X)
+        scale = _ordinary().fp4_tensor_scale(X)
         if scale is not None:
             return scale
     torch = _torch()
@@ -674,7 +674,7 @@ def fp4_tensor_scale(X, out=None, ws=None, stream=None):
 def fp4_quantize(X, fmt: str = "nv", scale=None, out=None, stream=None):
     """X (M x K) -> (codes, scales), blocks along its rows; scale: the "nv" tensor scale (None = 1)."""
     if out is None and stream is None:
-        both = _host().fp4_quantize(X, fmt, scale)
+        both = _ordinary().fp4_quantize(X, fmt, scale)
         if both is not None:
             return both
     _torch()
@@ -718,7 +718,7 @@ def fp4_quantize_both(X, fmt: str = "nv", scale=None, out=None, stream=None):
 def fp4_dequantize(Xq, Xs, K: int, fmt: str = "nv", scale=None, dtype=None, Y=None, stream=None):
     """The values (M x K) of a packed operand, in `dtype` (default: that of Y, or float32)."""
     if Y is None and stream is None:
-        values = _host().fp4_dequantize(Xq, Xs, K, fmt, scale, dtype)
+        values = _ordinary().fp4_dequantize(Xq, Xs, K, fmt, scale, dtype)
         if values is not None:
             return values
     torch = _torch()
@@ -740,7 +740,7 @@ def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None
              Y=None, stream=None):
     """Y = A . B^T + bias of packed A (M x K) and B (N x K), in `dtype` (default: that of Y, or bfloat16)."""
     if Y is None and stream is None:
-        product = _host().fp4_gemm(Aq, As, Bq, Bs, K, fmt, a_scale, b_scale, bias, dtype)
+        product = _ordinary().fp4_gemm(Aq, As, Bq, Bs, K, fmt, a_scale, b_scale, bias, dtype)
         if product is not None:
             return product
     torch = _torch()
@@ -767,7 +767,7 @@ def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None
 def fp4_linear(X, Wq, Ws, fmt: str = "nv", x_scale=None, w_scale=None, bias=None, Y=None, ws=None, stream=None):
     """Y = Q(X) . W^T + bias with packed weights W (N x K); X (M x K) is quantized in the call, Y has its type."""
     if Y is None and ws is None and stream is None:
-        product = _host().fp4_linear(X, Wq, Ws, fmt, x_scale, w_scale, bias)
+        product = _ordinary().fp4_linear(X, Wq, Ws, fmt, x_scale, w_scale, bias)
         if product is not None:
             return product
     torch = _torch()
@@ -802,7 +802,7 @@ def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale
     column sums of dY) is fp32.  A gradient that is not needed is None.
     """
     if need_dx and need_dw and need_db and out is None and ws is None and stream is None:
-        grads = _host().fp4_linear_backward(dY, X, Wtq, Wts, fmt, dy_scale, x_scale, w_scale)
+        grads = _ordinary().fp4_linear_backward(dY, X, Wtq, Wts, fmt, dy_scale, x_scale, w_scale)
         if grads is not None:
             return grads
     torch = _torch()
@@ -851,7 +851,7 @@ def _stats(stats, M, device):
 def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, Y=None, stats=None, stream=None):
     """(Y, mean, rstd) of the rows of X (M x D); gamma and beta in X's type or fp32 (None = 1, 0)."""
     if Y is None and stats is None and stream is None:
-        result = _host().layer_norm(X, gamma, beta, eps)
+        result = _ordinary().layer_norm(X, gamma, beta, eps)
         if result is not None:
             return result
     torch = _torch()
@@ -878,7 +878,7 @@ def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv",
     mean and rstd are None unless stats is True (new ones) or gives the two tensors.
     """
     if out is None and stream is None and (stats is None or stats is True):
-        result = _host().layer_norm_fp4(X, gamma, beta, eps, fmt, scale, stats is True)
+        result = _ordinary().layer_norm_fp4(X, gamma, beta, eps, fmt, scale, stats is True)
         if result is not None:
             return result
     _torch()
@@ -905,7 +905,7 @@ def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv",
 def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None):
     """(dX, dgamma, dbeta) of layer_norm, with the mean and rstd it returned; dgamma and dbeta are fp32."""
     if out is None and ws is None and stream is None:
-        grads = _host().layer_norm_backward(dY, X, gamma, mean, rstd)
+        grads = _ordinary().layer_norm_backward(dY, X, gamma, mean, rstd)
         if grads is not None:
             return grads
     torch = _torch()
