@@ -487,7 +487,7 @@ def w4a4_gemm_prepacked(Xq, Xscale, packed, N: int, K: int, XU=None, Vt=None, bi
 # ---------------------------------------------------------------- microscaled 4-bit, layer norm
 #
 # A small call takes a few microseconds on the device, so the host side counts:
-# the ordinary call goes through _host(); for the others each operand is looked
+# the ordinary call goes through _ordinary(); for the others each operand is looked
 # at once, and the current stream comes as a raw handle (the stream object that
 # torch.cuda.current_stream() builds costs 3 us).
 

@@ -20,6 +20,7 @@
 //            memory (lane r % 32, column r / 32, byte c), so a tile moves from
 //            global memory to the tensor core untouched.
 #pragma once
+#include <atomic>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -417,6 +418,26 @@ int launch_serialized(F* kernel, dim3 grid, int threads, size_t smem, int cluste
         cfg.numAttrs = 2;
     }
     return map_cuda(cudaLaunchKernelEx(&cfg, kernel, args...));
+}
+
+// Lifts the kernel's limit of dynamic shared memory to all that a CTA can have, once per
+// device; each kernel is called with a type of its own as TAG, which keeps its flags.
+// The limit of a call's own size would not do: another thread's launch, with less, could
+// lower it again between the two calls.
+template <class TAG, class F>
+int raise_smem(F* kernel) {
+    static std::atomic<bool> done[64] = {};
+    const int dev = current_device();
+    if (dev < 0 || dev >= 64) return QG_ERR_CUDA;
+    if (done[dev].load(std::memory_order_acquire)) return QG_OK;
+    cudaFuncAttributes a;
+    cudaError_t e = cudaFuncGetAttributes(&a, kernel);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 232448 - static_cast<int>(a.sharedSizeBytes));
+    if (e != cudaSuccess) return map_cuda(e);
+    done[dev].store(true, std::memory_order_release);
+    return QG_OK;
 }
 
 // Calls f with a value of the C++ type of `dtype`.

@@ -138,7 +138,7 @@ static int budget_measure(const std::vector<qg::KernelBudget>& table, int index,
     if (e != cudaSuccess) return qg::map_cuda(e);
     *regs_per_thread = fa.numRegs;
     *static_smem_bytes = static_cast<int>(fa.sharedSizeBytes);
-    if (b.smem_bytes > 0) {
+    if (b.smem_bytes > fa.maxDynamicSharedSizeBytes) {  // raised if need be, never lowered under a launch
         e = cudaFuncSetAttribute(b.func, cudaFuncAttributeMaxDynamicSharedMemorySize, b.smem_bytes);
         if (e != cudaSuccess) return qg::map_cuda(e);
     }

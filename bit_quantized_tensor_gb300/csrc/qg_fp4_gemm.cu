@@ -3,7 +3,6 @@
 // the activations, the weights and the bias).  Kernels: fp4_gemm.cuh
 // (one CTA a tile) and fp4_gemm2.cuh (CTA pairs).
 #include <atomic>
-#include <mutex>
 
 #include "fp4_gemm2.cuh"
 
@@ -14,22 +13,6 @@ struct Fp4Operand {
     int64_t rows;
     const float* ts;
 };
-
-// Lifts the kernel's dynamic shared-memory limit, once per device;
-// each kernel is called with a type of its own as TAG, which keeps its flags.
-template <class TAG, class F>
-static int raise_smem(F* kernel, int bytes) {
-    static std::mutex mu;
-    static bool done[64] = {};
-    const int dev = current_device();
-    if (dev < 0 || dev >= 64) return QG_ERR_CUDA;
-    std::lock_guard<std::mutex> g(mu);
-    if (done[dev]) return QG_OK;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return map_cuda(e);
-    done[dev] = true;
-    return QG_OK;
-}
 
 static int codes_map(CUtensorMap* map, const Fp4Operand& o, int64_t K, int box_rows) {
     return make_tmap_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, o.codes, fp4_codes_ld(K), o.rows, fp4_codes_ld(K), 128,
@@ -55,7 +38,7 @@ static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params&
         tx = tw;
         tsx = tsw;
     }
-    if (!rc) rc = raise_smem<Flags>(fp4_gemm_kernel<Cfg, QUANT>, Cfg::SMEM_JOIN_BYTES);
+    if (!rc) rc = raise_smem<Flags>(fp4_gemm_kernel<Cfg, QUANT>);
     if (rc) return rc;
     const int64_t gy = (p.N + 127) / 128, gz = (p.M + Cfg::NT - 1) / Cfg::NT;
     if (gy > 65535 || gz > 65535) return QG_ERR_UNSUPPORTED;
@@ -72,7 +55,7 @@ static int launch_fp4_pair(const Fp4Operand& x, const Fp4Operand& w, const Fp4Pa
     if (!rc) rc = codes_map(&tx, x, p.K, 128);
     if (!rc) rc = scales_map(&tsw, w, Cfg::FMT, p.K, Cfg::ATOMS);
     if (!rc) rc = scales_map(&tsx, x, Cfg::FMT, p.K, Cfg::ATOMS);
-    if (!rc) rc = raise_smem<Cfg>(fp4_gemm2_kernel<Cfg>, Cfg::SMEM_BYTES);
+    if (!rc) rc = raise_smem<Cfg>(fp4_gemm2_kernel<Cfg>);
     if (rc) return rc;
     const int64_t tiles = (int64_t(p.M) + 255) / 256 * ((int64_t(p.N) + 255) / 256);
     if (tiles > INT32_MAX) return QG_ERR_UNSUPPORTED;

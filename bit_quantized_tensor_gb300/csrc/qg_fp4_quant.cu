@@ -558,10 +558,9 @@ static int launch_both(int64_t gx, int64_t gy, int64_t M, int64_t K, const void*
                        uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* partial, cudaStream_t s) {
     constexpr int SMEM = BothSmem<FMT, T>::BYTES;
     auto* f = k_fp4_quantize_both<FMT, T>;
-    if constexpr (SMEM > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        if (e != cudaSuccess) return map_cuda(e);
-    }
+    struct Flags {};
+    const int rc = raise_smem<Flags>(f);
+    if (rc) return rc;
     return launch_serialized(f, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kBothThreads, SMEM, 1, s, M,
                              K, static_cast<const T*>(X), ldx, rows_aligned(X, ldx, sizeof(T), M), ts, Xq, Xs, Tq, Ts,
                              partial);

@@ -384,10 +384,9 @@ static int launch_norm_rows(const NormParams& p, int64_t same, int dev, cudaStre
     const int slots = norm_slots(slot, TPR);
     const int64_t smem = slot * slots * GROUPS;
     auto* f = k_layer_norm_rows<T, TPR, FMT, EDGES>;
-    if (smem > 48 * 1024 - 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return map_cuda(e);
-    }
+    struct Flags {};
+    const int rc = raise_smem<Flags>(f);
+    if (rc) return rc;
     const int64_t ctas = norm_ctas(p.M, GROUPS, int64_t(CTAS) * num_sms(dev), same);
     return launch_serialized(f, dim3(static_cast<unsigned>(ctas)), THREADS, static_cast<size_t>(smem), 1, s, p, slots,
                              ctl);

@@ -460,10 +460,9 @@ static int launch_norm_bwd(const NormBwdParams& p, int64_t same, int dev, int64_
     int slots = 0;
     const int64_t smem = bwd_smem(TPR, VPT, p.D, sizeof(T), VEC, &slots);
     auto* f = k_layer_norm_backward<T, TPR, VPT, VEC, EDGES>;
-    if (smem > 44 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-        if (e != cudaSuccess) return map_cuda(e);
-    }
+    struct Flags {};
+    const int rc = raise_smem<Flags>(f);
+    if (rc) return rc;
     return launch_serialized(f, dim3(static_cast<unsigned>(ctas)), kBwdThreads, static_cast<size_t>(smem), 1, s, p,
                              slots, ctl);
 }

@@ -246,3 +246,14 @@ def test_refusals(torch, qg):
         qg.layer_norm_backward(X, X, g, stats[:3], stats)
     with pytest.raises(qg.QgError, match="QG_ERR_WORKSPACE"):
         qg.layer_norm_backward(X, X, g, stats, stats, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+def test_after_measuring_the_table(torch, qg):
+    """Measuring the kernels' residency leaves them launchable with more shared memory
+    than the table's entry (which is that of the longest row, not of the fullest ring)."""
+    qg.kernel_budgets(measure=True, table="block")
+    for D in (1000, 1333, 2048, 4100):
+        X = on_gpu(torch, rows(200, D, D), "float32")
+        g, b = params(torch, D, "float32")
+        check_forward(qg.layer_norm(X, g, b, EPS), X, g, b, "float32")
+        qg.layer_norm_backward(X, X, g, *qg.layer_norm(X, g, b, EPS)[1:])
