@@ -14,11 +14,11 @@ namespace qg {
 // of the four blocks of a scale tile's row go out as one word through two
 // shuffles.  2^log_tx threads lie along a row (at least 4), the others of the
 // CTA on further rows; a thread walks down the rows with the same column, so
-// that addresses only advance.  Bound by memory (2 or 4 bytes in, 0.56 or 0.53
-// out per value) once the instructions are few: with one block a thread and the
-// divisions written out it took 34 us for 4096 x 8192 bf16, with the factors of
-// the 128 scale bytes in a table and 128 bytes a thread in flight 22 us (86 MB,
-// 3.9 TB/s), of which the arithmetic on 33.6 million values is the larger part.
+// that addresses only advance.  Memory (2 or 4 bytes in, 0.56 or 0.53 out per
+// value) would allow 13 us for 4096 x 8192 bf16; from cold caches it takes 20.9 us
+// (86 MB, 4.1 TB/s), for the instructions a value: maxima are found on packed
+// words, the factors of the 128 scale bytes lie in a table, and divisions are left
+// to the few scales next to a rounding boundary.
 constexpr int kQuantThreads = 256;
 
 template <int FMT, class T>
@@ -332,7 +332,7 @@ __global__ void __launch_bounds__(kBothThreads)
 // 2688 = 6 * 448, so the largest value of the tensor lands on the largest
 // code times the largest block scale.  Each CTA leaves its maximum in the
 // workspace and one more warp joins them (a maximum does not depend on the
-// order); bound by reading X once (8192 x 4096 bf16: 17 us, 4.0 TB/s).
+// order); bound by reading X once (8192 x 4096 bf16: 15.6 us, 4.3 TB/s).
 constexpr int kAmaxThreads = 512;
 constexpr int kAmaxMaxCtas = 1024;
 
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(32) k_fp4_scale_join(const uint32_t* __restric
 // One thread takes 16 values a step and walks down the rows, as above; its two
 // 16-byte stores are one of 32 bytes where rows are aligned to that.  Bound by
 // memory (0.56 or 0.53 bytes in, 2 or 4 out per value): 4096 x 8192 to bf16 in
-// 19.6 us (4.4 TB/s).
+// 16.8 us (5.1 TB/s).
 constexpr int kDequantThreads = 256;
 
 template <int FMT, class T>
@@ -509,18 +509,22 @@ static bool rows_aligned(const void* p, int64_t ld, size_t elem, int64_t rows) {
 }
 
 // Cut of a kernel whose threads walk down the rows: 2^log_tx threads along a
-// row, grid.y over the row, and in grid.x enough CTAs for eight an SM.
+// row, grid.y over the row, and in grid.x CTAs for `per_sm` an SM: whole rounds of
+// those that are resident at once, and never one more.  The quantizer's four are
+// so busy that two rounds do (4096 x 8192 bf16: 20.9 us; 22.0 with two CTAs above
+// them, 22.2 with a round and a half); the way back, whose rounds are of loads and
+// stores alone, gains from more (eight 19.3 us, twelve 17.4, sixteen 16.8).
 struct Walk {
     int log_tx;
     dim3 grid;
 };
-static Walk walk(int64_t rows, int64_t per_row, int threads) {
+static Walk walk(int64_t rows, int64_t per_row, int threads, int per_sm) {
     Walk w;
     w.log_tx = 2;
     while (w.log_tx < 8 && (int64_t(1) << w.log_tx) < per_row) ++w.log_tx;
     const int64_t ty = threads >> w.log_tx;
     const int64_t gy = (per_row + (int64_t(1) << w.log_tx) - 1) >> w.log_tx;
-    const int64_t most = 8 * num_sms(current_device()) / gy + 1;
+    const int64_t share = int64_t(per_sm) * num_sms(current_device()) / gy, most = share > 1 ? share : 1;
     const int64_t gx = (rows + ty - 1) / ty;
     w.grid = dim3(static_cast<unsigned>(gx < most ? gx : most), static_cast<unsigned>(gy));
     return w;
@@ -538,7 +542,7 @@ int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, in
     const int64_t rows = zero_pad ? (M + 127) / 128 * 128 : M;
     const int64_t per_row = 4 * fp4_col_tiles(fmt, K);
     if (rows == 0 || per_row == 0) return QG_OK;
-    const Walk w = walk(rows, per_row, kQuantThreads);
+    const Walk w = walk(rows, per_row, kQuantThreads, 8);
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         const bool al = rows_aligned(X, ldx, sizeof(T), M);
@@ -583,12 +587,14 @@ int fp4_quantize_both_run(int fmt, int dtype, int64_t M, int64_t K, const void* 
     return sum_partials_run(partial, gy, K, colsum, s);
 }
 
-// CTAs along a row and over the rows: about two an SM, each thread with 4 loads.
+// CTAs along a row and over the rows: the two an SM that are resident at once (8192 x
+// 4096 bf16: 15.6 us; 16.7 with 512 CTAs on 152 SMs), each thread with 4 loads.
 static dim3 amax_grid(int64_t M, int64_t K, size_t elem) {
     const int64_t pieces = (K * static_cast<int64_t>(elem) + 15) / 16;
     int64_t x = (pieces + 4 * kAmaxThreads - 1) / (4 * kAmaxThreads);
-    x = x < 1 ? 1 : x > kAmaxMaxCtas / 2 ? kAmaxMaxCtas / 2 : x;
-    int64_t y = kAmaxMaxCtas / 2 / x;
+    const int64_t two = 2 * num_sms(current_device()), most = two < kAmaxMaxCtas ? two : kAmaxMaxCtas;
+    x = x < 1 ? 1 : x > most ? most : x;
+    int64_t y = most / x;
     y = M < 1 ? 1 : y > M ? M : y;
     return dim3(static_cast<unsigned>(x), static_cast<unsigned>(y));
 }
@@ -720,7 +726,7 @@ int fp4_dequantize(int fmt, int dtype, int64_t M, int64_t K, const uint8_t* Xq, 
     if (!Xq || !Xs) return QG_ERR_INVALID_ARG;
     if (!aligned16(Xq) || !aligned16(Xs)) return QG_ERR_MISALIGNED;
     if (current_device() < 0) return QG_ERR_CUDA;
-    const Walk w = walk(M, (K + 15) / 16, kDequantThreads);
+    const Walk w = walk(M, (K + 15) / 16, kDequantThreads, 16);
     return by_dtype(dtype, [&](auto t) {
         using T = decltype(t);
         auto* f = fmt == kNv ? k_fp4_dequantize<kNv, T> : k_fp4_dequantize<kMx, T>;
