@@ -45,13 +45,20 @@ struct NormParams {
     float *mean, *rstd;
 };
 
-// Rows whose scale words behind the last row are zeroed (up to whole tiles).
+// Zeroes the scale words behind the last row, up to the whole tile of 128 rows:
+// word i of a tile belongs to row i / 4 + 32 (i % 4).  (Row by row, with a division
+// a word, a single row of 4096 waited 3 us for its one CTA to get through them.)
 template <int FMT>
 __device__ __forceinline__ void zero_scale_rows(int64_t M, int64_t D, uint8_t* Xs) {
-    const int64_t tiles = fp4_col_tiles(FMT, D), pad = (M + 127) / 128 * 128 - M;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < pad * tiles;
-         i += static_cast<int64_t>(gridDim.x) * blockDim.x)
-        *reinterpret_cast<uint32_t*>(Xs + fp4_scale_offset(M + i / tiles, 4 * (i % tiles), tiles)) = 0;
+    const int used = static_cast<int>(M & 127);  // rows of the last tile
+    if (used == 0) return;
+    const int64_t tiles = fp4_col_tiles(FMT, D);
+    uint32_t* const last = reinterpret_cast<uint32_t*>(Xs + (M >> 7) * tiles * 512);
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < tiles * 128;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int word = static_cast<int>(i & 127);
+        if ((word >> 2) + ((word & 3) << 5) >= used) last[i] = 0;
+    }
 }
 
 // TPR threads hold a row, VPT times 8 values each; VEC: 8 consecutive values a
@@ -67,8 +74,10 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
     pdl_launch_dependents();
     const int64_t row = static_cast<int64_t>(blockIdx.x) * (THREADS / TPR) + threadIdx.x / TPR;
     const int t = threadIdx.x % TPR;
-    if constexpr (FMT >= 0) zero_scale_rows<FMT>(p.M, p.D, p.Xs);
-    if (row >= p.M) return;  // whole warps: TPR >= 32
+    if (row >= p.M) {  // whole warps: TPR >= 32
+        if constexpr (FMT >= 0) zero_scale_rows<FMT>(p.M, p.D, p.Xs);
+        return;
+    }
     const T* x = static_cast<const T*>(p.X) + row * p.ldx;
     const int D = static_cast<int>(p.D);
     float v[E];
@@ -91,6 +100,25 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) sum += v[e];
+    // gamma and beta of 8 columns: on their way with the row where a thread has no
+    // more (a few rows are all latency), else when they are used
+    auto weights = [&](int i, float(&g)[8], float(&b)[8]) {
+        if constexpr (VEC) {
+            const int k = (i * TPR + t) * 8;
+            weights8<T>(p.gamma, p.w_f32, p.w_vec, k, D - k, 1.f, g);
+            weights8<T>(p.beta, p.w_f32, p.w_vec, k, D - k, 0.f, b);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int k = (8 * i + j) * TPR + t;
+                g[j] = k < D && p.gamma ? weight_at<T>(p.gamma, p.w_f32, k) : 1.f;
+                b[j] = k < D && p.beta ? weight_at<T>(p.beta, p.w_f32, k) : 0.f;
+            }
+        }
+    };
+    float g[8], b[8];
+    if constexpr (VPT == 1) weights(0, g, b);
+    if constexpr (FMT >= 0) zero_scale_rows<FMT>(p.M, p.D, p.Xs);
     const float mean = __fdiv_rn(row_sum<TPR>(sum, red[0]), static_cast<float>(D));
     auto index = [&](int e) { return VEC ? ((e >> 3) * TPR + t) * 8 + (e & 7) : e * TPR + t; };
     float var = 0.f;
@@ -111,9 +139,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
         if constexpr (VEC) {
             const int k = (i * TPR + t) * 8;
             if (i > 0 && (i * TPR + (t & ~31)) * 8 >= (D + 127) / 128 * 128) continue;  // the warp is past the row
-            float g[8], b[8], y[8];
-            weights8<T>(p.gamma, p.w_f32, p.w_vec, k, D - k, 1.f, g);
-            weights8<T>(p.beta, p.w_f32, p.w_vec, k, D - k, 0.f, b);
+            float y[8];
+            if constexpr (VPT > 1) weights(i, g, b);
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 y[j] = k + j < D ? fmaf((v[8 * i + j] - mean) * rstd, g[j], b[j]) : 0.f;
@@ -122,13 +149,12 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
             else if (k < D)
                 store_some<T, 8>(static_cast<T*>(p.Y) + row * p.ldy + k, D - k, p.y_vec, y);
         } else {
+            if constexpr (VPT > 1) weights(i, g, b);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const int k = (8 * i + j) * TPR + t;
-                if (k >= D) continue;
-                const float g = p.gamma ? weight_at<T>(p.gamma, p.w_f32, k) : 1.f;
-                const float b = p.beta ? weight_at<T>(p.beta, p.w_f32, k) : 0.f;
-                static_cast<T*>(p.Y)[row * p.ldy + k] = from_f32<T>(fmaf((v[8 * i + j] - mean) * rstd, g, b));
+                if (k < D)
+                    static_cast<T*>(p.Y)[row * p.ldy + k] = from_f32<T>(fmaf((v[8 * i + j] - mean) * rstd, g[j], b[j]));
             }
         }
     }
