@@ -265,10 +265,18 @@ __device__ __forceinline__ void store_piece(T* row, int k, int D, bool whole, co
         }
     }
 }
-// gamma or beta of a piece, 0 outside [0, D), `none` without one.
+// gamma or beta of a piece, 0 outside [0, D), `none` without one; vec: w is 16-byte
+// aligned (then whole pieces from a multiple of 8 on come in one or two loads).
 template <class T>
-__device__ __forceinline__ void weight_piece(const void* w, bool f32, int k, int D, float none, uint64_t (&g)[4]) {
+__device__ __forceinline__ void weight_piece(const void* w, bool f32, bool vec, int k, int D, float none,
+                                             uint64_t (&g)[4]) {
     float f[8];
+    if (vec && (k & 7) == 0 && !piece_cut(k, D)) {
+        weights8<T>(w, f32, true, k, 8, none, f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) g[j] = two(f[2 * j], f[2 * j + 1]);
+        return;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         f[j] = k + j < 0 || k + j >= D ? 0.f : w ? weight_at<T>(w, f32, k + j) : none;

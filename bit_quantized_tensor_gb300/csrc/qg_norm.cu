@@ -10,15 +10,17 @@ namespace qg {
 // Eight consecutive normalised values of a row per lane to codes: the lanes of
 // a block find its maximum with shuffles, each lane stores its word of codes,
 // and the first lane of every four blocks their scale word.  All lanes of the
-// warp take part; positions behind D hold 0.
+// warp take part; positions behind D hold 0.  factors: fill_factors' table, or none
+// (a division a block, where rows are too few to pay for the table).
 template <int FMT>
 __device__ __forceinline__ void quantize_lane8(const float (&y)[8], int64_t k, int64_t D, int64_t row,
-                                               const TensorScale& ts, uint8_t* Xq, uint8_t* Xs) {
+                                               const TensorScale& ts, const float* factors, uint8_t* Xq,
+                                               uint8_t* Xs) {
     constexpr int LANES = fp4_block(FMT) / 8;
     uint32_t m = absmax_bits<8>(y);
 #pragma unroll
     for (int o = 1; o < LANES; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const BlockScale s = block_scale<FMT>(m, ts);
+    const BlockScale s = factors ? block_scale<FMT>(m, ts, factors) : block_scale<FMT>(m, ts);
     const int64_t ld = fp4_codes_ld(D), tiles = fp4_col_tiles(FMT, D);
     if (k < 2 * ld) *reinterpret_cast<uint32_t*>(Xq + row * ld + k / 2) = scaled_codes8(y, s.r);
     const int blk = (threadIdx.x & 31) / LANES;
@@ -145,7 +147,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) k_layer_norm(const Norm
             for (int j = 0; j < 8; ++j)
                 y[j] = k + j < D ? fmaf((v[8 * i + j] - mean) * rstd, g[j], b[j]) : 0.f;
             if constexpr (FMT >= 0)
-                quantize_lane8<FMT>(y, k, p.D, row, ts, p.Xq, p.Xs);
+                quantize_lane8<FMT>(y, k, p.D, row, ts, nullptr, p.Xq, p.Xs);
             else if (k < D)
                 store_some<T, 8>(static_cast<T*>(p.Y) + row * p.ldy + k, D - k, p.y_vec, y);
         } else {
@@ -184,6 +186,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
     __shared__ __align__(8) uint64_t bars[GROUPS][kRingMax];
     __shared__ float red[2][32];
     __shared__ int abort_flag;
+    __shared__ float factors[FMT == kNv ? 128 : 1];
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
     const int D = static_cast<int>(p.D);
     RowRing ring;
@@ -205,8 +208,9 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
     int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group;
     for (int s = 0; s < slots; ++s)
         if (row + s * step < p.M) row_fetch<TPR, EDGES>(ring, s, X + (row + s * step) * p.ldx, row + s * step, p.M);
-    __syncthreads();
     const TensorScale ts = tensor_scale(FMT == kNv ? p.ts : nullptr);
+    if constexpr (FMT == kNv) fill_factors(factors, ts.ts);
+    __syncthreads();
     const float inv_d = __frcp_rn(static_cast<float>(D));
     // values before column 0 in a row's first piece
     const int lead = FMT < 0 && EDGES
@@ -222,8 +226,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         uint64_t g[4], b[4];
-        weight_piece<T>(p.gamma, p.w_f32, first(i), D, 1.f, g);
-        weight_piece<T>(p.beta, p.w_f32, first(i), D, 0.f, b);
+        weight_piece<T>(p.gamma, p.w_f32, p.w_vec, first(i), D, 1.f, g);
+        weight_piece<T>(p.beta, p.w_f32, p.w_vec, first(i), D, 0.f, b);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             hg[4 * i + j] = g[j];
@@ -311,7 +315,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
                     f[2 * j] = h.x;
                     f[2 * j + 1] = h.y;
                 }
-                quantize_lane8<FMT>(f, k, p.D, row, ts, p.Xq, p.Xs);
+                quantize_lane8<FMT>(f, k, p.D, row, ts, factors, p.Xq, p.Xs);
             } else {
                 store_piece<T>(static_cast<T*>(p.Y) + row * p.ldy, k, D, !EDGES || p.y_vec, y);
             }
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(kLongThreads) k_layer_norm_long(const NormPara
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = j < n ? fmaf((u[j] - mean) * rstd, g[j], b[j]) : 0.f;
         if constexpr (FMT >= 0)
-            quantize_lane8<FMT>(y, k, D, row, ts, p.Xq, p.Xs);
+            quantize_lane8<FMT>(y, k, D, row, ts, nullptr, p.Xq, p.Xs);
         else if (n > 0)
             store_some<T, 8>(static_cast<T*>(p.Y) + row * p.ldy + k, n, p.y_vec, y);
     }

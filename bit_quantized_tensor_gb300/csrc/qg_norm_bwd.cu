@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             uint64_t g[4];
-            weight_piece<T>(p.gamma, p.w_f32, column(i, 0), D, 1.f, g);
+            weight_piece<T>(p.gamma, p.w_f32, p.w_vec, column(i, 0), D, 1.f, g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) hg[4 * i + j] = g[j];
         }
