@@ -14,11 +14,11 @@
 //
 // Bound by the issuing warp: 4096 x 8192 x 8192 takes 86 us (6.4 PFLOP/s) with
 // blocks of 16 and 77 us (7.2) with blocks of 32, whose scales are half as many
-// copies; the MMAs alone would take 62 us, without the epilogue it is 2 to 3 us
-// less, and filling the ring costs about 3.  Slower were: 64-bit descriptor
-// arithmetic (95 us), a warp of its own for the scale copies with two sets of
-// scales in tensor memory (114), copies between the MMAs of a block (125), a
-// first look at the next block's barrier while one is issued (91).
+// copies.  With descriptors as 64-bit sums it took 95 us (84 without its epilogue,
+// 76 without its loads, 62 with the MMAs alone); a stage unrolled around those 91.
+// A first look at the next block's barrier while one is issued costs 5 us.  A warp
+// of its own for the scale copies, with two sets of scales in tensor memory, took
+// a quantizing call from 120 to 143 us, copies between the MMAs of a block to 154.
 #pragma once
 #include "fp4_gemm.cuh"
 #include "tc_gemm.cuh"
