@@ -307,7 +307,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = fma_two(mul_two(v[4 * i + j], r2), hg[4 * i + j], hb[4 * i + j]);
             if constexpr (FMT >= 0) {
-                // 0 behind the row: c, gamma and beta are 0 there
+                // 0 behind the row: c, gamma and beta are 0 there, but 1 / std may be NaN
+                if (piece_cut(k, D)) cut_piece(y, k, D);
                 float f[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
