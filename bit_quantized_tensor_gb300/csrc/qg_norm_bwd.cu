@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     extern __shared__ __align__(16) uint8_t ring_smem[];
     __shared__ __align__(8) uint64_t bars[GROUPS][kRingMax];
     __shared__ __align__(8) uint64_t sum_bars[GROUPS];
-    __shared__ float red[2][GROUPS][2][16];  // a row's sums, per warp: d, d c
+    __shared__ float red[2][GROUPS][2][16];  // a row's sums, per warp: d, d xh
     __shared__ int abort_flag;
     const int t = threadIdx.x % TPR, group = threadIdx.x / TPR, lane = threadIdx.x & 31;
     const int D = static_cast<int>(p.D);
@@ -212,7 +212,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 
     // part 1 of row r in slot s: dgamma, dbeta and the warp's part of the row's sums,
     // by halves of the warp (outside the row dy is 0, and with it every term);
-    // with c = x - mean: dgamma += (dy rstd) c
+    // the sums are those of d and d xh: of the size of the gradient, however large or
+    // small the row is (d (x - mean) and rstd^2 may not be fp32 numbers)
     auto part1 = [&](int64_t r, int s, uint32_t phase, float mean, float rstd) {
         // a wait that runs out is recorded, ends the fetching, and lets the
         // remaining rows through with whatever their slots hold
@@ -231,22 +232,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             gammas(i, g);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const uint64_t c = add_two(u[j], minus), d = mul_two(y[j], g[j]);
-                dg[4 * i + j] = fma_two(mul_two(y[j], r2), c, dg[4 * i + j]);
+                const uint64_t xh = mul_two(add_two(u[j], minus), r2), d = mul_two(y[j], g[j]);
+                dg[4 * i + j] = fma_two(y[j], xh, dg[4 * i + j]);
                 db[4 * i + j] = add_two(db[4 * i + j], y[j]);
                 a1 = add_two(a1, d);
-                a2 = fma_two(d, c, a2);
+                a2 = fma_two(d, xh, a2);
             }
         }
         const float2 f1 = both(a1), f2 = both(a2);
         return warp_sums_by_half(f1.x + f1.y, f2.x + f2.y);
     };
-    // part 2: dx = d rstd - (sum(d) / D) rstd - c (sum(d c) / D) rstd^3
+    // part 2: dx = (d - sum(d) / D - (x - mean) (sum(d xh) / D rstd)) rstd
     auto part2 = [&](int64_t r, int s, float mean, float rstd, float2 sum) {
         const uint8_t* slot = ring.slots + static_cast<int64_t>(s) * ring.slot_bytes;
         const T* x = reinterpret_cast<const T*>(slot + place(X, p.ldx, r));
         const T* dy = reinterpret_cast<const T*>(slot + ring.slot_bytes / 2 + place(dY, p.lddy, r));
-        const float k0 = -(sum.x * inv_d) * rstd, k1 = -((sum.y * rstd) * inv_d) * rstd * rstd;
+        const float k0 = -(sum.x * inv_d), k1 = -(sum.y * inv_d) * rstd;
         const uint64_t b0 = two(k0, k0), b1 = two(k1, k1), r2 = two(rstd, rstd), minus = two(-mean, -mean);
         T* o = static_cast<T*>(p.dX) + r * p.lddx;
 #pragma unroll
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             gammas(i, g);
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                y[j] = fma_two(add_two(u[j], minus), b1, fma_two(mul_two(y[j], g[j]), r2, b0));
+                y[j] = mul_two(fma_two(add_two(u[j], minus), b1, fma_two(y[j], g[j], b0)), r2);
             if constexpr (VEC && EDGES) {
                 store_piece<T>(o, column(i, 0), D, true, y);
             } else if constexpr (VEC) {
