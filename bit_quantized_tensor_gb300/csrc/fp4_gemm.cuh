@@ -1,7 +1,7 @@
 // Product of two microscaled 4-bit operands on the block-scaled tensor cores:
 //   Y[m][n] = alpha * sum_k (a[m][k] sa[m][k / B]) (b[n][k] sb[n][k / B]) + bias[n]
 // with a, b e2m1 codes and sa, sb block scales (fp4_common.cuh), alpha the
-// product of the tensor scales.  tcgen05.mma multiplies the codes, applies both
+// product of the tensor scales (fp4_alpha).  tcgen05.mma multiplies the codes, applies both
 // block scales and accumulates in fp32 in tensor memory; each K step of 64
 // needs the scales of its rows in tensor memory too, which tcgen05.cp brings
 // there from shared memory in the layout that the packed scales already have.
@@ -171,8 +171,21 @@ constexpr int kSiteFp4Acc = 303;
 constexpr int kSiteFp4Quant = 304;
 constexpr int kSiteFp4Join = 305;
 
-__device__ __forceinline__ float fp4_alpha(const Fp4Params& p) {
-    return (p.ts_a ? *p.ts_a : 1.f) * (p.ts_b ? *p.ts_b : 1.f);
+// The sums are multiplied by `first`, which is 1 where the product of the tensor
+// scales is a normal fp32 number (alpha, `second`).  Where it is not, the result may
+// still be one: a product below the normal range takes the larger scale first, one
+// above it the smaller.
+struct Fp4Alpha {
+    float first, second;
+};
+__device__ __forceinline__ Fp4Alpha fp4_alpha(const Fp4Params& p) {
+    const float a = p.ts_a ? *p.ts_a : 1.f, b = p.ts_b ? *p.ts_b : 1.f, ab = a * b;
+    if (ab >= 0x1p-126f && ab <= 0x1.fffffep+127f) return {1.f, ab};
+    return ab < 1.f ? Fp4Alpha{fmaxf(a, b), fminf(a, b)} : Fp4Alpha{fminf(a, b), fmaxf(a, b)};
+}
+// alpha acc + bias, rounded once where alpha is normal.
+__device__ __forceinline__ float fp4_scaled(float acc, const Fp4Alpha& alpha, float bias) {
+    return fmaf(acc * alpha.first, alpha.second, bias);
 }
 
 __device__ __forceinline__ float typed_at(const void* v, int dtype, int64_t i) {
@@ -385,7 +398,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     tc_fence_after();
     pdl_launch_dependents();
     const bool good = __syncthreads_and(ok && !*abort_flag);
-    const float alpha = fp4_alpha(p);
+    const Fp4Alpha alpha = fp4_alpha(p);
     const bool empty = kb1 == kb0;
     const int n = n0 + warp * 32 + lane;
     const float bias = warp < 4 && p.bias && n < p.N ? typed_at(p.bias, p.dtype, n) : 0.f;
@@ -402,7 +415,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 for (int i = 0; i < 16; ++i) {
                     const float acc = empty ? 0.f : __uint_as_float(r[i]);
                     if (n < p.N && c + i < cols)
-                        typed_store(p.Y, p.dtype, (m0 + c + i) * p.ldy + n, fmaf(acc, alpha, bias));
+                        typed_store(p.Y, p.dtype, (m0 + c + i) * p.ldy + n, fp4_scaled(acc, alpha, bias));
                 }
             }
         }
@@ -441,7 +454,7 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
                 for (int c = split * per; c < c1; ++c) {
                     float acc = 0.f;
                     for (int s = 0; s < splits; ++s) acc += join[(s * per + c - split * per) * 128 + threadIdx.x];
-                    typed_store(p.Y, p.dtype, (m0 + c) * p.ldy + n, fmaf(acc, alpha, bias));
+                    typed_store(p.Y, p.dtype, (m0 + c) * p.ldy + n, fp4_scaled(acc, alpha, bias));
                 }
         }
         cluster_sync();  // nobody leaves while its sums may still be on their way

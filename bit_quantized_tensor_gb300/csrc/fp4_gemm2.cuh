@@ -264,7 +264,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
     } else {
         // ---------------------------------------------------- epilogue (both CTAs)
         const int quad = warp & 3, half = (warp - 2) >> 2;
-        const float alpha = fp4_alpha(p);
+        const Fp4Alpha alpha = fp4_alpha(p);
         const uint32_t next = mapa_shared(next_bar, 0);
         uint8_t* const buf = out_smem + (warp - 2) * 2048;
         const bool sectors = (reinterpret_cast<uintptr_t>(p.Y) & 31) == 0 &&
@@ -275,7 +275,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             const T* bias = static_cast<const T*>(p.bias);
             float f[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha;
+            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha.first * alpha.second;
             if (bias) {
                 if (col + 16 <= p.N) {
 #pragma unroll
