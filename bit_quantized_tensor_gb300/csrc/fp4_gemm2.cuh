@@ -274,16 +274,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             using T = typename std::remove_pointer<decltype(Y)>::type;
             const T* bias = static_cast<const T*>(p.bias);
             float f[16];
+            if (!bias) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha.first * alpha.second;
-            if (bias) {
-                if (col + 16 <= p.N) {
+                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(r[j]) * alpha.first * alpha.second;
+            } else if (col + 16 <= p.N) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] += to_f32<T>(__ldg(bias + col + j));
-                } else {
+                for (int j = 0; j < 16; ++j)
+                    f[j] = fp4_scaled(__uint_as_float(r[j]), alpha, to_f32<T>(__ldg(bias + col + j)));
+            } else {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f[j] += to_f32<T>(__ldg(bias + min(col + j, p.N - 1)));
-                }
+                for (int j = 0; j < 16; ++j)
+                    f[j] = fp4_scaled(__uint_as_float(r[j]), alpha, to_f32<T>(__ldg(bias + min(col + j, p.N - 1))));
             }
             if (sectors && col + 16 <= p.N) {
                 if (row0 + lane < p.M) store_sectors(Y + (row0 + lane) * p.ldy + col, f);

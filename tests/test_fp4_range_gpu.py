@@ -37,3 +37,27 @@ def test_products_of_extreme_tensor_scales(torch, qg, ta, tb, big, tokens, split
     for y in outs:
         err = np.abs(as_np(y) - want)
         assert np.all(err <= bound), (float(np.nanmax(err / bound)), np.argwhere(~(err <= bound))[:4])
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_one_rounding_behind_the_sum(torch, qg, fmt):
+    """With sums that are exact in fp32 every cut gives the same bits: alpha sum + bias is rounded once."""
+    M, N, K = 16, 320, 256
+    rng = np.random.default_rng(90)
+    a, b = (rng.choice(np.concatenate((ref.GRID, -ref.GRID)), size=(n, K)).astype(np.float32) for n in (M, N))
+    a[:, ::16], b[:, ::16] = 6, 6  # every block's scale is a power of two
+    scales = dict(a_scale=one(torch, 0.337), b_scale=one(torch, 1.0)) if fmt == "nv" else {}
+    pa, pb = packed(torch, a, fmt), packed(torch, b, fmt)
+    bias = on_gpu(torch, activations(1, N, 91)[0])
+    outs = []
+    try:
+        for tokens, splits in CUTS:
+            assert qg.lib().qg_set_fp4_path(tokens, splits) == qg.QG_OK
+            outs.append(qg.fp4_gemm(*pa, *pb, K, fmt, bias=bias, dtype=torch.float32, **scales))
+    finally:
+        qg.lib().qg_set_fp4_path(0, 0)
+    alpha = np.float32(0.337) if fmt == "nv" else np.float32(1)
+    exact = (ref.quantized(a, fmt) @ ref.quantized(b, fmt).T).astype(np.longdouble) * np.longdouble(alpha)
+    want = (exact + as_np(bias).astype(np.longdouble)).astype(np.float32)
+    for y, cut in zip(outs, CUTS):
+        assert np.array_equal(y.cpu().numpy(), want), cut
