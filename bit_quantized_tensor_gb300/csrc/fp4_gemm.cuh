@@ -202,6 +202,18 @@ __device__ __forceinline__ void typed_store(void* v, int dtype, int64_t i, float
         static_cast<float*>(v)[i] = x;
 }
 
+// CTAs of the cluster, and its index along x; 1 and the block's own without one.
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_index() {
+    uint32_t r;
+    asm("mov.u32 %0, %%clusterid.x;" : "=r"(r));
+    return r;
+}
+
 // The two halves of cluster_sync.
 __device__ __forceinline__ void cluster_arrive() {
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -239,9 +251,11 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
     auto a_smem = [&](int s) { return ring0 + static_cast<uint32_t>(s) * Cfg::STAGE_BYTES; };
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int splits = static_cast<int>(gridDim.x), split = static_cast<int>(blockIdx.x);  // the cluster
-    const int n0 = static_cast<int>(blockIdx.y) * 128;
-    const int m0 = static_cast<int>(blockIdx.z) * NT;
+    // a cluster takes a tile; clusters along x take the rows of weights, of which there may
+    // be more tiles than a grid's y or z counts
+    const int splits = static_cast<int>(cluster_size()), split = static_cast<int>(cluster_ctarank());
+    const int n0 = static_cast<int>(cluster_index()) * 128;
+    const int m0 = static_cast<int>(blockIdx.y) * NT;
     const int num_kb = (p.K + kFp4Bk - 1) / kFp4Bk;
     const int kb0 = static_cast<int>(static_cast<int64_t>(num_kb) * split / splits);
     const int kb1 = static_cast<int>(static_cast<int64_t>(num_kb) * (split + 1) / splits);

@@ -25,6 +25,8 @@ static int scales_map(CUtensorMap* map, const Fp4Operand& o, int fmt, int64_t K,
                         512, 128, atoms, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
+constexpr int64_t kMaxGridY = 65535;
+
 template <class Cfg, class QUANT>
 static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, int splits, cudaStream_t s) {
     struct Flags {};  // the kernel's own shared-memory flag below
@@ -40,12 +42,11 @@ static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params&
     }
     if (!rc) rc = raise_smem<Flags>(fp4_gemm_kernel<Cfg, QUANT>);
     if (rc) return rc;
-    const int64_t gy = (p.N + 127) / 128, gz = (p.M + Cfg::NT - 1) / Cfg::NT;
-    if (gy > 65535 || gz > 65535) return QG_ERR_UNSUPPORTED;
+    const int64_t gx = (int64_t(p.N) + 127) / 128 * splits, gy = (int64_t(p.M) + Cfg::NT - 1) / Cfg::NT;
+    if (gy > kMaxGridY) return QG_ERR_UNSUPPORTED;  // not by plan_fp4
     return launch_serialized(fp4_gemm_kernel<Cfg, QUANT>,
-                             dim3(static_cast<unsigned>(splits), static_cast<unsigned>(gy), static_cast<unsigned>(gz)),
-                             kFp4Threads, splits > 1 ? Cfg::SMEM_JOIN_BYTES : Cfg::SMEM_BYTES, splits, s, tw, tx, tsw,
-                             tsx, p);
+                             dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kFp4Threads,
+                             splits > 1 ? Cfg::SMEM_JOIN_BYTES : Cfg::SMEM_BYTES, splits, s, tw, tx, tsw, tsx, p);
 }
 
 template <class Cfg>
@@ -115,6 +116,8 @@ static Fp4Plan plan_fp4(int64_t M, int64_t N, int64_t K, bool sectors, int sms) 
     const bool chosen = f.nt != 0;
     if (!chosen) f.nt = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
     if (!f.splits) f.splits = choose_splits((N + 127) / 128 * ((M + f.nt - 1) / f.nt), kb, f.nt, sms);
+    // a grid's y counts the single CTAs' tiles of tokens; pairs walk over any number
+    if (f.nt == 128 && (M + 127) / 128 > kMaxGridY) f.nt = 256;
     if (!chosen && f.nt == 128 && pair_time(M, N, kb, sectors, sms) < single_time(M, N, kb, f.splits, sms)) f.nt = 256;
     if (f.nt == 256 || f.splits > kb) f.splits = 1;
     return f;

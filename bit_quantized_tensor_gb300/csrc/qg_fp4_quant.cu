@@ -190,7 +190,10 @@ __global__ void __launch_bounds__(kBothThreads)
     float* const factors = sums + NB * kTile;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    const int64_t m0 = static_cast<int64_t>(blockIdx.y) * kTile, k0 = static_cast<int64_t>(blockIdx.x) * kTile;
+    // a grid's y would not count all tiles of rows
+    const uint32_t tiles_k = static_cast<uint32_t>((K + kTile - 1) / kTile), tile_m = blockIdx.x / tiles_k;
+    const int64_t m0 = static_cast<int64_t>(tile_m) * kTile;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.x - tile_m * tiles_k) * kTile;
     const TensorScale ts = tensor_scale(FMT == kNv ? tscale : nullptr);
     if constexpr (FMT == kNv) {
         fill_factors(factors, ts.ts);
@@ -322,7 +325,7 @@ __global__ void __launch_bounds__(kBothThreads)
         float sum = sums[threadIdx.x];
 #pragma unroll
         for (int b = 1; b < NB; ++b) sum += sums[b * kTile + threadIdx.x];
-        partial[blockIdx.y * K + k0 + threadIdx.x] = sum;
+        partial[tile_m * K + k0 + threadIdx.x] = sum;
     }
 }
 
@@ -558,33 +561,33 @@ int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, in
 }
 
 template <int FMT, class T>
-static int launch_both(int64_t gx, int64_t gy, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
+static int launch_both(int64_t tiles, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                        uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* partial, cudaStream_t s) {
     constexpr int SMEM = BothSmem<FMT, T>::BYTES;
     auto* f = k_fp4_quantize_both<FMT, T>;
     struct Flags {};
     const int rc = raise_smem<Flags>(f);
     if (rc) return rc;
-    return launch_serialized(f, dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kBothThreads, SMEM, 1, s, M,
-                             K, static_cast<const T*>(X), ldx, rows_aligned(X, ldx, sizeof(T), M), ts, Xq, Xs, Tq, Ts,
+    return launch_serialized(f, dim3(static_cast<unsigned>(tiles)), kBothThreads, SMEM, 1, s, M, K,
+                             static_cast<const T*>(X), ldx, rows_aligned(X, ldx, sizeof(T), M), ts, Xq, Xs, Tq, Ts,
                              partial);
 }
 
 int fp4_quantize_both_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                           uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* colsum, float* partial,
                           cudaStream_t s) {
-    const int64_t gx = (K + kTile - 1) / kTile, gy = (M + kTile - 1) / kTile;
-    if (gy > 65535 || gx > INT32_MAX) return QG_ERR_UNSUPPORTED;
+    const int64_t tiles_m = (M + kTile - 1) / kTile, tiles = tiles_m * ((K + kTile - 1) / kTile);
+    if (tiles > INT32_MAX) return QG_ERR_UNSUPPORTED;  // 35 T values
     int rc = QG_OK;
-    if (gx && gy)
+    if (tiles)
         rc = by_dtype(dtype, [&](auto t) {
             using T = decltype(t);
             float* const part = colsum ? partial : nullptr;
-            return fmt == kNv ? launch_both<kNv, T>(gx, gy, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s)
-                              : launch_both<kMx, T>(gx, gy, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s);
+            return fmt == kNv ? launch_both<kNv, T>(tiles, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s)
+                              : launch_both<kMx, T>(tiles, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s);
         });
     if (rc || !colsum) return rc;
-    return sum_partials_run(partial, gy, K, colsum, s);
+    return sum_partials_run(partial, tiles_m, K, colsum, s);
 }
 
 // CTAs along a row and over the rows: the two an SM that are resident at once (8192 x

@@ -1,5 +1,5 @@
 """Microscaled 4-bit products at the ends of their range: tensor scales whose product
-leaves fp32's normal range."""
+leaves fp32's normal range, and as many rows as the calls take."""
 import numpy as np
 import pytest
 
@@ -61,3 +61,61 @@ def test_one_rounding_behind_the_sum(torch, qg, fmt):
     want = (exact + as_np(bias).astype(np.longdouble)).astype(np.float32)
     for y, cut in zip(outs, CUTS):
         assert np.array_equal(y.cpu().numpy(), want), cut
+
+
+# ------------------------------------------------------------- as many rows as the calls take
+
+ROWS = 65536 * 128 + 1  # one more tile of 128 rows than a grid's y or z counts
+
+
+def test_products_of_very_many_rows(torch, qg):
+    K, few = 32, 8
+    a, w = activations(few, K, 95), activations(128, K, 96)
+    pick = torch.arange(ROWS, device="cuda") * 7 % 128
+    wq, ws = packed(torch, w, "mx")
+    many_q = wq[pick]
+    # scales of many rows: the bytes of w's rows in their new places (one block a row)
+    byte = torch.from_numpy(ref.codes_and_bytes(w, "mx")[1][:, 0].copy()).cuda()[pick]
+    tiles = -(-ROWS // 128)
+    at = torch.arange(ROWS, device="cuda")
+    many_s = torch.zeros((tiles, 1, 512), dtype=torch.uint8, device="cuda")
+    many_s.view(-1)[at // 128 * 512 + at % 32 * 16 + at % 128 // 32 * 4] = byte
+    aq, as_ = packed(torch, a, "mx")
+    small = qg.fp4_gemm(aq, as_, wq, ws, K, "mx", dtype=torch.float32)
+    y = qg.fp4_gemm(aq, as_, many_q, many_s, K, "mx", dtype=torch.float32)       # as weights
+    assert torch.equal(y, small[:, pick])
+    del y
+    y = qg.fp4_gemm(many_q, many_s, aq, as_, K, "mx", dtype=torch.float32)       # as tokens
+    assert torch.equal(y, small.t()[pick])
+
+
+@pytest.mark.parametrize("fmt", ["nv", "mx"])
+def test_both_directions_of_very_many_rows(torch, qg, fmt):
+    K = 16
+    X = torch.randn((ROWS, K), device="cuda", generator=torch.Generator("cuda").manual_seed(97)).to(torch.bfloat16)
+    q, s, tq, ts = qg.fp4_quantize_both(X, fmt)
+    for got, want in zip((q, s, tq, ts), qg.fp4_quantize(X, fmt) + qg.fp4_quantize(X.t().contiguous(), fmt)):
+        assert torch.equal(got, want)
+
+
+def test_gradients_of_very_many_rows(torch, qg):
+    """dX row by row, dW and db over all of them."""
+    N, K = 16, 32
+    g = torch.Generator("cuda").manual_seed(98)
+    dY = (torch.randint(-3, 4, (ROWS, N), device="cuda", generator=g)).to(torch.bfloat16)
+    X = (torch.randint(-1, 2, (ROWS, K), device="cuda", generator=g)).to(torch.bfloat16)
+    wt = activations(K, N, 99)
+    dx, dw, db = qg.fp4_linear_backward(dY, X, *packed(torch, wt, "mx"), "mx")
+    q, s = qg.fp4_quantize(dY, "mx")
+    v = qg.fp4_dequantize(q, s, N, "mx").double()
+    want = v @ torch.from_numpy(ref.quantized(wt, "mx").T.copy()).cuda()
+    size = v.abs() @ torch.from_numpy(np.abs(ref.quantized(wt, "mx")).T.copy()).cuda()
+    assert bool(((dx.double() - want).abs() <= 9 * 2.0 ** -22 * size + 1.01 * 2.0 ** -8 * want.abs() + 2.0 ** -133).all())
+    del v, want, size
+    # whole numbers: 128 rows' sums are exact in fp32, and so are their sums up to 2^24
+    assert torch.equal(db.double(), dY.double().sum(0))
+    vt = qg.fp4_dequantize(*qg.fp4_quantize(dY.t().contiguous(), "mx"), ROWS, "mx").double()
+    xt = qg.fp4_dequantize(*qg.fp4_quantize(X.t().contiguous(), "mx"), ROWS, "mx").double()
+    size = (vt.abs() @ xt.abs().t())
+    bound = (ROWS / 64 + 8) * 2.0 ** -22 * size + 1.01 * 2.0 ** -8 * (vt @ xt.t()).abs() + 2.0 ** -133
+    assert bool(((dw.double() - vt @ xt.t()).abs() <= bound).all())
