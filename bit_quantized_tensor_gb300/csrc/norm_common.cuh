@@ -328,6 +328,7 @@ inline int64_t norm_ctas(int64_t M, int64_t groups, int64_t most, int64_t same) 
 // Argument checks of the norm's calls (qg_norm.cu).
 int check_rows(int dtype, int64_t M, int64_t D, const void* X, int64_t ldx);
 int check_weight(const void* w, int dtype);
+int check_f32(const float* v);
 int check_norm(int dtype, int wdtype, int64_t M, int64_t D, float eps);
 
 constexpr int kLongThreads = 1024;  // CTAs of the kernels for rows too long to hold

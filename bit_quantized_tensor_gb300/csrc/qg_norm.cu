@@ -473,6 +473,8 @@ int check_weight(const void* w, int dtype) {
     return reinterpret_cast<uintptr_t>(w) % dtype_bytes(dtype) ? QG_ERR_MISALIGNED : QG_OK;
 }
 
+int check_f32(const float* v) { return check_weight(v, QG_F32); }
+
 int check_norm(int dtype, int wdtype, int64_t M, int64_t D, float eps) {
     if (!dtype_ok(dtype) || (wdtype != dtype && wdtype != QG_F32)) return QG_ERR_UNSUPPORTED;
     if (M < 0 || D < 1 || M > INT32_MAX || D > INT32_MAX) return QG_ERR_INVALID_ARG;
@@ -487,6 +489,8 @@ static int norm_call(int fmt, int dtype, int64_t M, int64_t D, const void* X, in
     if (!rc) rc = check_rows(dtype, M, D, X, ldx);
     if (!rc) rc = check_weight(gamma, wdtype);
     if (!rc) rc = check_weight(beta, wdtype);
+    if (!rc) rc = check_f32(mean);
+    if (!rc) rc = check_f32(rstd);
     if (rc) return rc;
     if (M == 0) return QG_OK;
     const int dev = current_device();

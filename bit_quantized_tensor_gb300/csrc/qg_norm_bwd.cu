@@ -572,6 +572,8 @@ int layer_norm_backward(int dtype, int64_t M, int64_t D, const void* dY, int64_t
     if (!rc) rc = check_rows(dtype, M, D, dY, lddy);
     if (!rc) rc = check_rows(dtype, M, D, dX, lddx);
     if (!rc) rc = check_weight(gamma, wdtype);
+    for (const float* v : {mean, rstd, static_cast<const float*>(dgamma), static_cast<const float*>(dbeta)})
+        if (!rc) rc = check_f32(v);
     if (rc) return rc;
     if (!dgamma || !dbeta || (M > 0 && (!mean || !rstd))) return QG_ERR_INVALID_ARG;
     if (!ws || ws_bytes < norm_backward_workspace(D)) return QG_ERR_WORKSPACE;
