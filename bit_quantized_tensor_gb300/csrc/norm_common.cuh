@@ -2,6 +2,7 @@
 #pragma once
 #include "fp4_common.cuh"
 #include "qg_ptx.cuh"
+#include "row_pieces.h"
 
 namespace qg {
 
@@ -66,76 +67,58 @@ struct RowRing {
 // to the end of its last 32 bytes.
 __host__ __device__ inline int64_t row_slot_bytes(int64_t row_bytes) { return (row_bytes + 15 + 31) / 32 * 32; }
 
-// The 16-byte pieces that a bulk copy fetches for a row: all that it touches,
-// but of the matrix's first row none that begins before it, and of its last
-// row none that ends behind it (memory there need not be the caller's).
-struct RowPieces {
-    uintptr_t start, end, base;  // the row; the piece it starts in
-    uintptr_t a;                 // first piece fetched
-    uint32_t bytes;              // of pieces fetched
-};
-__device__ __forceinline__ RowPieces row_pieces(const void* row, int64_t row_bytes, bool first, bool last) {
-    RowPieces q;
-    q.start = reinterpret_cast<uintptr_t>(row);
-    q.end = q.start + row_bytes;
-    q.base = q.start & ~uintptr_t(15);
-    q.a = first ? (q.start + 15) & ~uintptr_t(15) : q.base;
-    const uintptr_t b = last ? q.end & ~uintptr_t(15) : (q.end + 15) & ~uintptr_t(15);
-    q.bytes = b > q.a ? static_cast<uint32_t>(b - q.a) : 0u;
-    return q;
-}
-// The rest of a first or last row, two bytes a thread (elements are 2 or 4
-// bytes, at addresses that are multiples of 2).
+// The rest of a row at an end of the matrix, two bytes a thread (elements are 2 or 4
+// bytes, at addresses that are multiples of 2).  Later bulk copies into the slot
+// have to come behind these stores.
 __device__ __forceinline__ void row_edges(const RowPieces& q, uint8_t* dst, int t) {
     if (t >= 32) return;
-    const uintptr_t head_end = q.bytes ? q.a : q.end;
-    const uintptr_t h = q.start + 2 * t;
-    if (h < head_end) *reinterpret_cast<uint16_t*>(dst + (h - q.base)) = *reinterpret_cast<const uint16_t*>(h);
-    const uintptr_t e = q.a + q.bytes + 2 * t;
-    if (q.bytes && e < q.end) *reinterpret_cast<uint16_t*>(dst + (e - q.base)) = *reinterpret_cast<const uint16_t*>(e);
+    const uintptr_t h = q.start + 2 * t, e = q.tail() + 2 * t;
+    if (h < q.head_end()) *reinterpret_cast<uint16_t*>(dst + (h - q.base)) = *reinterpret_cast<const uint16_t*>(h);
+    if (e < q.end) *reinterpret_cast<uint16_t*>(dst + (e - q.base)) = *reinterpret_cast<const uint16_t*>(e);
+    fence_proxy_async_smem();
 }
 
 __device__ __forceinline__ void row_copy(const RowPieces& q, uint8_t* dst, uint32_t bar) {
     if (q.bytes) bulk_copy_g2s(smem_u32(dst + (q.a - q.base)), reinterpret_cast<const void*>(q.a), q.bytes, bar);
 }
 
-// Starts the copy of row i of M into slot s.  All threads of the group call it,
-// after all of them have read the slot's previous row and synchronized; what
-// row_edges copies is visible after the group's next synchronization.
+// Starts the copy of row i of the matrix m into slot s.  All threads of the group
+// call it, after all of them have read the slot's previous row and synchronized;
+// what row_edges copies is visible after the group's next synchronization.
 // EDGES: rows may start or end inside a piece.
 template <int TPR, bool EDGES>
-__device__ __forceinline__ void row_fetch(const RowRing& r, int s, const void* row, int64_t i, int64_t M) {
+__device__ __forceinline__ void row_fetch(const RowRing& r, int s, const void* row, int64_t i, const RowBounds& m) {
     const int t = threadIdx.x % TPR;
-    const bool first = i == 0, last = i == M - 1;
-    const bool alone = EDGES && (first || last);
-    if (t && !alone) return;
+    const bool at_end = EDGES && m.at_end(i);
+    if (t && !at_end) return;
     uint8_t* dst = r.slots + static_cast<int64_t>(s) * r.slot_bytes;
-    const RowPieces q = row_pieces(row, r.row_bytes, first, last);
+    const RowPieces q = row_pieces(reinterpret_cast<uintptr_t>(row), r.row_bytes, m, at_end);
     const uint32_t bar = r.bar0 + 8 * s;
     if (t == 0) {
         mbar_arrive_expect_tx(bar, q.bytes);
         row_copy(q, dst, bar);
     }
-    if (alone) row_edges(q, dst, t);
+    if (at_end) row_edges(q, dst, t);
 }
 
 // The same for two rows of one length that share a slot: x, then y half a slot on.
 template <int TPR>
 __device__ __forceinline__ void row_fetch2(const RowRing& r, int s, const void* x, const void* y, int64_t i,
-                                           int64_t M) {
+                                           const RowBounds& mx, const RowBounds& my) {
     const int t = threadIdx.x % TPR;
-    const bool first = i == 0, last = i == M - 1;
-    if (t && !first && !last) return;
+    const bool at_end = mx.at_end(i) || my.at_end(i);
+    if (t && !at_end) return;
     uint8_t* dx = r.slots + static_cast<int64_t>(s) * r.slot_bytes;
     uint8_t* dy = dx + r.slot_bytes / 2;
-    const RowPieces p = row_pieces(x, r.row_bytes, first, last), q = row_pieces(y, r.row_bytes, first, last);
+    const RowPieces p = row_pieces(reinterpret_cast<uintptr_t>(x), r.row_bytes, mx, at_end);
+    const RowPieces q = row_pieces(reinterpret_cast<uintptr_t>(y), r.row_bytes, my, at_end);
     const uint32_t bar = r.bar0 + 8 * s;
     if (t == 0) {
         mbar_arrive_expect_tx(bar, p.bytes + q.bytes);
         row_copy(p, dx, bar);
         row_copy(q, dy, bar);
     }
-    if (first || last) {
+    if (at_end) {
         row_edges(p, dx, t);
         row_edges(q, dy, t);
     }

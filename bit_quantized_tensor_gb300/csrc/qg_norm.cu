@@ -37,6 +37,7 @@ struct NormParams {
     int64_t M, D;
     const void* X;
     int64_t ldx;
+    RowBounds xb;
     const void *gamma, *beta;
     bool w_f32, x_vec, w_vec, y_vec;
     float eps;
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
     const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
     int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group;
     for (int s = 0; s < slots; ++s)
-        if (row + s * step < p.M) row_fetch<TPR, EDGES>(ring, s, X + (row + s * step) * p.ldx, row + s * step, p.M);
+        if (row + s * step < p.M) row_fetch<TPR, EDGES>(ring, s, X + (row + s * step) * p.ldx, row + s * step, p.xb);
     const TensorScale ts = tensor_scale(FMT == kNv ? p.ts : nullptr);
     if constexpr (FMT == kNv) fill_factors(factors, ts.ts);
     __syncthreads();
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
         // all threads have read the slot
         if constexpr (TPR == 32) __syncwarp();
         if (row + slots * step < p.M && !*static_cast<volatile int*>(&abort_flag))
-            row_fetch<TPR, EDGES>(ring, s, X + (row + slots * step) * p.ldx, row + slots * step, p.M);
+            row_fetch<TPR, EDGES>(ring, s, X + (row + slots * step) * p.ldx, row + slots * step, p.xb);
         if (++s == slots) {
             s = 0;
             phase ^= 1u;
@@ -497,6 +498,8 @@ static int norm_call(int fmt, int dtype, int64_t M, int64_t D, const void* X, in
     if (dev < 0) return QG_ERR_CUDA;
     NormParams p = {};
     p.M = M; p.D = D; p.X = X; p.ldx = ldx; p.gamma = gamma; p.beta = beta; p.eps = eps;
+    const int64_t elem = static_cast<int64_t>(dtype_bytes(dtype));
+    p.xb = row_bounds(X, M, ldx * elem, D * elem);
     p.w_f32 = wdtype == QG_F32;
     p.x_vec = vec_ok(X, ldx, dtype_bytes(dtype), M);
     p.w_vec = aligned16(gamma) && aligned16(beta);

@@ -103,6 +103,7 @@ struct NormBwdParams {
     int64_t M, D;
     const void *dY, *X;
     int64_t lddy, ldx;
+    RowBounds dyb, xb;
     const void* gamma;
     bool w_f32, x_vec, dy_vec, w_vec, dx_vec;
     const float *mean, *rstd;
@@ -150,7 +151,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group;
     for (int s = 0; s < slots; ++s) {
         const int64_t r = row + s * step;
-        if (r < p.M) row_fetch2<TPR>(ring, s, X + r * p.ldx, dY + r * p.lddy, r, p.M);
+        if (r < p.M) row_fetch2<TPR>(ring, s, X + r * p.ldx, dY + r * p.lddy, r, p.xb, p.dyb);
     }
     float* const sg = reinterpret_cast<float*>(ring_smem + static_cast<int64_t>(GROUPS) * slots * ring.slot_bytes);
     if constexpr (!VEC) stage_weights<T>(sg, p.gamma, p.w_f32, D, 1.f);
@@ -316,9 +317,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int64_t ahead = row + (slots - 2) * step;
         if (n > 1 && ahead < p.M && !*static_cast<volatile int*>(&abort_flag)) {
             const int free_slot = s >= 2 ? s - 2 : s + slots - 2;
-            row_fetch2<TPR>(ring, free_slot, X + ahead * p.ldx, dY + ahead * p.lddy, ahead, p.M);
+            row_fetch2<TPR>(ring, free_slot, X + ahead * p.ldx, dY + ahead * p.lddy, ahead, p.xb, p.dyb);
         }
-        if (n > 1 && ahead == p.M - 1) {  // what threads copied of the last row, once
+        if (n > 1 && ahead < p.M && (p.xb.at_end(ahead) || p.dyb.at_end(ahead))) {  // what threads copied of the last rows
             if constexpr (TPR > 32)
                 asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
             else
@@ -582,6 +583,9 @@ int layer_norm_backward(int dtype, int64_t M, int64_t D, const void* dY, int64_t
     if (dev < 0) return QG_ERR_CUDA;
     NormBwdParams p = {};
     p.M = M; p.D = D; p.dY = dY; p.X = X; p.lddy = lddy; p.ldx = ldx; p.gamma = gamma;
+    const int64_t elem = static_cast<int64_t>(dtype_bytes(dtype));
+    p.xb = row_bounds(X, M, ldx * elem, D * elem);
+    p.dyb = row_bounds(dY, M, lddy * elem, D * elem);
     p.w_f32 = wdtype == QG_F32;
     p.x_vec = vec_ok(X, ldx, dtype_bytes(dtype), M);
     p.dy_vec = vec_ok(dY, lddy, dtype_bytes(dtype), M);

@@ -24,3 +24,65 @@ def test_misaligned_statistics_are_refused(L):
     for bad in range(4):
         v = [P + 2 if i == bad else P for i in range(4)]
         assert L.layer_norm_backward(1, 4, 64, P, 64, P, 64, None, 1, v[0], v[1], P, 64, v[2], v[3], P, BIG, None) == 3
+
+
+# ------------------------------------------------------------- what the norm's bulk copies fetch
+
+ROW_PIECES = r"""
+#include <cstdio>
+#include <initializer_list>
+#include "row_pieces.h"
+using namespace qg;
+// Every matrix of short rows at every place: what is fetched for a row lies in the
+// matrix, in whole pieces, and with what is copied by hand it is the row.
+int main() {
+    long n = 0;
+    for (int elem : {2, 4})
+        for (int off = 0; off < 32; off += elem)
+            for (int D = 1; D <= 40; ++D)
+                for (int gap : {0, 1, 2, 3, 7, 8, 11})
+                    for (int M : {1, 2, 3, 7, 8, 9, 17, 40}) {
+                        const uintptr_t start = 4096 + off, rb = D * elem, ld = (D + gap) * elem;
+                        const uintptr_t stop = start + (M - 1) * ld + rb;
+                        const RowBounds m = row_bounds(reinterpret_cast<const void*>(start), M, ld, rb);
+                        for (int i = 0; i < M; ++i, ++n) {
+                            const uintptr_t r = start + i * ld;
+                            const RowPieces q = row_pieces(r, rb, m, m.at_end(i));
+                            const uintptr_t b = q.a + q.bytes;
+                            bool ok = q.start == r && q.end == r + rb && q.base <= r && r - q.base < 16;
+                            ok = ok && (!q.bytes || (q.a % 16 == 0 && q.bytes % 16 == 0 && q.a >= start && b <= stop));
+                            ok = ok && (!q.bytes || q.a >= q.base);  // inside the slot, whose end is 31 bytes on
+                            ok = ok && (!q.bytes || b <= ((q.end + 15) & ~uintptr_t(15)));
+                            // [start, head_end), [a, b), [tail, end) follow one another without a gap
+                            ok = ok && q.head_end() <= q.end && q.tail() <= q.end + 15;
+                            if (q.bytes)
+                                ok = ok && q.a <= (q.start > q.head_end() ? q.start : q.head_end()) && q.tail() == b;
+                            else
+                                ok = ok && q.head_end() == q.end && q.tail() == q.end;
+                            // 32 lanes of 2 bytes copy each by hand; only rows at an end have any
+                            const uintptr_t head = q.head_end() > q.start ? q.head_end() - q.start : 0;
+                            const uintptr_t tail = q.end > q.tail() ? q.end - q.tail() : 0;
+                            ok = ok && head <= 64 && tail <= 64 && (m.at_end(i) || (!head && !tail && q.bytes));
+                            if (!ok) {
+                                std::printf("elem %d offset %d D %d gap %d M %d row %d\n", elem, off, D, gap, M, i);
+                                return 1;
+                            }
+                        }
+                    }
+    std::printf("%ld rows\n", n);
+    return 0;
+}
+"""
+
+
+def test_bulk_copies_stay_inside_the_matrix(tmp_path):
+    import shutil
+    import subprocess
+
+    from bit_quantized_tensor_gb300 import _build
+    src, exe = tmp_path / "row_pieces.cpp", tmp_path / "row_pieces"
+    src.write_text(ROW_PIECES)
+    subprocess.run([shutil.which("g++") or "c++", "-std=c++17", "-O1", "-Wall", "-Werror", "-I", _build.CSRC, str(src),
+                    "-o", str(exe)], check=True)
+    run = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert run.returncode == 0, run.stdout
