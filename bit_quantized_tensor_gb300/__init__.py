@@ -490,6 +490,10 @@ def w4a4_gemm_prepacked(Xq, Xscale, packed, N: int, K: int, XU=None, Vt=None, bi
 # the ordinary call goes through _ordinary(); for the others each operand is looked
 # at once, and the current stream comes as a raw handle (the stream object that
 # torch.cuda.current_stream() builds costs 3 us).
+#
+# A call with stream= is the same call with that stream as the current one: what it
+# allocates (outputs, workspaces) comes from that stream's pool, whose blocks nothing
+# on another stream may still use.
 
 _host_module = None
 _HOST_ENTRIES = ("qg_workspace_size", "fp4_tensor_scale", "fp4_quantize", "fp4_dequantize", "fp4_gemm", "fp4_linear",
@@ -535,10 +539,8 @@ def _fmt_id(fmt):
     raise ValueError(f"fmt must be 'nv' or 'mx', got {fmt!r}")
 
 
-def _raw_stream(stream, device):
-    if stream is None:
-        return _torch_module._C._cuda_getCurrentRawStream(device.index)
-    return stream.cuda_stream
+def _raw_stream(device):
+    return _torch_module._C._cuda_getCurrentRawStream(device.index)
 
 
 def _on(t, name, device):
@@ -622,14 +624,12 @@ def _vector(t, name, n, dtype, device):
     return t.data_ptr()
 
 
-def _scratch(ws, need, device, stream):
-    """Address and size of the caller's workspace, or of a new one that stays alive for `stream`."""
+def _scratch(ws, need, device):
+    """Address and size of the caller's workspace, or of a new one of the current stream."""
     if ws is None:
         if need == 0:
             return None, None, 0
         ws = _torch_module.empty(need, dtype=_torch_module.uint8, device=device)
-        if stream is not None:
-            ws.record_stream(stream)
     else:
         _on(ws, "ws", device)
         need = ws.numel() * ws.element_size()
@@ -653,7 +653,10 @@ def _weights(gamma, beta, D, xdtype, device):
 
 def fp4_tensor_scale(X, out=None, ws=None, stream=None):
     """The "nv" tensor scale of X: max(|x|) / 2688 over its finite values, one fp32 on the device."""
-    if out is None and ws is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return fp4_tensor_scale(X, out, ws)
+    if out is None and ws is None:
         scale = _ordinary().fp4_tensor_scale(X)
         if scale is not None:
             return scale
@@ -664,16 +667,19 @@ def fp4_tensor_scale(X, out=None, ws=None, stream=None):
     if out is None:
         out = torch.empty(1, dtype=torch.float32, device=dev)
     ptr = _one_f32(out, "out", "nv", dev)
-    ws, wsp, wsb = _scratch(ws, 4096, dev, stream)
+    ws, wsp, wsb = _scratch(ws, 4096, dev)
     M, K = X.shape
     _check("fp4_tensor_scale", lib().fp4_tensor_scale(dt, M, K, X.data_ptr(), ld, ptr, wsp, wsb,
-                                                      _raw_stream(stream, dev)))
+                                                      _raw_stream(dev)))
     return out
 
 
 def fp4_quantize(X, fmt: str = "nv", scale=None, out=None, stream=None):
     """X (M x K) -> (codes, scales), blocks along its rows; scale: the "nv" tensor scale (None = 1)."""
-    if out is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return fp4_quantize(X, fmt, scale, out)
+    if out is None:
         both = _ordinary().fp4_quantize(X, fmt, scale)
         if both is not None:
             return both
@@ -691,12 +697,15 @@ def fp4_quantize(X, fmt: str = "nv", scale=None, out=None, stream=None):
             raise ValueError(f"out must have {M} rows")
     _check("fp4_quantize", lib().fp4_quantize(
         f, dt, M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, dev), Xq.data_ptr(), Xs.data_ptr(),
-        _raw_stream(stream, dev)))
+        _raw_stream(dev)))
     return Xq, Xs
 
 
 def fp4_quantize_both(X, fmt: str = "nv", scale=None, out=None, stream=None):
     """X (M x K) -> (codes, scales) of X and (codes, scales) of its transpose, reading X once."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return fp4_quantize_both(X, fmt, scale, out)
     _torch()
     f = _fmt_id(fmt)
     ld = _matrix(X, "X")
@@ -711,13 +720,16 @@ def fp4_quantize_both(X, fmt: str = "nv", scale=None, out=None, stream=None):
     Xq, Xs, Tq, Ts = out
     _check("fp4_quantize_both", lib().fp4_quantize_both(
         f, dt, M, K, X.data_ptr(), ld, _one_f32(scale, "scale", fmt, dev), Xq.data_ptr(), Xs.data_ptr(),
-        Tq.data_ptr(), Ts.data_ptr(), _raw_stream(stream, dev)))
+        Tq.data_ptr(), Ts.data_ptr(), _raw_stream(dev)))
     return Xq, Xs, Tq, Ts
 
 
 def fp4_dequantize(Xq, Xs, K: int, fmt: str = "nv", scale=None, dtype=None, Y=None, stream=None):
     """The values (M x K) of a packed operand, in `dtype` (default: that of Y, or float32)."""
-    if Y is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return fp4_dequantize(Xq, Xs, K, fmt, scale, dtype, Y)
+    if Y is None:
         values = _ordinary().fp4_dequantize(Xq, Xs, K, fmt, scale, dtype)
         if values is not None:
             return values
@@ -732,14 +744,17 @@ def fp4_dequantize(Xq, Xs, K: int, fmt: str = "nv", scale=None, dtype=None, Y=No
         ld = _matrix(Y, "Y", dev, dtype, M, K)
     _check("fp4_dequantize", lib().fp4_dequantize(
         f, _dtype_id(Y.dtype, "Y"), M, K, Xq.data_ptr(), Xs.data_ptr(), _one_f32(scale, "scale", fmt, dev),
-        Y.data_ptr(), ld, _raw_stream(stream, dev)))
+        Y.data_ptr(), ld, _raw_stream(dev)))
     return Y
 
 
 def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None, bias=None, dtype=None,
              Y=None, stream=None):
     """Y = A . B^T + bias of packed A (M x K) and B (N x K), in `dtype` (default: that of Y, or bfloat16)."""
-    if Y is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return fp4_gemm(Aq, As, Bq, Bs, K, fmt, a_scale, b_scale, bias, dtype, Y)
+    if Y is None:
         product = _ordinary().fp4_gemm(Aq, As, Bq, Bs, K, fmt, a_scale, b_scale, bias, dtype)
         if product is not None:
             return product
@@ -760,13 +775,16 @@ def fp4_gemm(Aq, As, Bq, Bs, K: int, fmt: str = "nv", a_scale=None, b_scale=None
     _check("fp4_gemm", lib().fp4_gemm(
         f, dt, M, N, K, Aq.data_ptr(), As.data_ptr(), _one_f32(a_scale, "a_scale", fmt, dev), Bq.data_ptr(),
         Bs.data_ptr(), _one_f32(b_scale, "b_scale", fmt, dev), _vector(bias, "bias", N, dtype, dev), Y.data_ptr(),
-        ld, _raw_stream(stream, dev)))
+        ld, _raw_stream(dev)))
     return Y
 
 
 def fp4_linear(X, Wq, Ws, fmt: str = "nv", x_scale=None, w_scale=None, bias=None, Y=None, ws=None, stream=None):
     """Y = Q(X) . W^T + bias with packed weights W (N x K); X (M x K) is quantized in the call, Y has its type."""
-    if Y is None and ws is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return fp4_linear(X, Wq, Ws, fmt, x_scale, w_scale, bias, Y, ws)
+    if Y is None and ws is None:
         product = _ordinary().fp4_linear(X, Wq, Ws, fmt, x_scale, w_scale, bias)
         if product is not None:
             return product
@@ -784,11 +802,11 @@ def fp4_linear(X, Wq, Ws, fmt: str = "nv", x_scale=None, w_scale=None, bias=None
     else:
         ldy = _matrix(Y, "Y", dev, dtype, M, N)
     L = lib()
-    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K), dev, stream)
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR, M, N, K), dev)
     _check("fp4_linear", L.fp4_linear(
         f, dt, M, N, K, X.data_ptr(), ldx, _one_f32(x_scale, "x_scale", fmt, dev), Wq.data_ptr(), Ws.data_ptr(),
         _one_f32(w_scale, "w_scale", fmt, dev), _vector(bias, "bias", N, dtype, dev), Y.data_ptr(), ldy,
-        wsp, wsb, _raw_stream(stream, dev)))
+        wsp, wsb, _raw_stream(dev)))
     return Y
 
 
@@ -801,7 +819,10 @@ def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale
     results of fp4_quantize_both(W)).  dX and dW have the type of dY, db (the
     column sums of dY) is fp32.  A gradient that is not needed is None.
     """
-    if need_dx and need_dw and need_db and out is None and ws is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return fp4_linear_backward(dY, X, Wtq, Wts, fmt, dy_scale, x_scale, w_scale, need_dx, need_dw, need_db, out, ws)
+    if need_dx and need_dw and need_db and out is None and ws is None:
         grads = _ordinary().fp4_linear_backward(dY, X, Wtq, Wts, fmt, dy_scale, x_scale, w_scale)
         if grads is not None:
             return grads
@@ -826,13 +847,13 @@ def fp4_linear_backward(dY, X, Wtq, Wts, fmt: str = "nv", dy_scale=None, x_scale
     if dX is None and dW is None and db is None:
         return out
     L = lib()
-    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K), dev, stream)
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_FP4_LINEAR_BACKWARD, M, N, K), dev)
     _check("fp4_linear_backward", L.fp4_linear_backward(
         f, dt, M, N, K, dY.data_ptr(), lddy, _one_f32(dy_scale, "dy_scale", fmt, dev), X.data_ptr(), ldx,
         _one_f32(x_scale, "x_scale", fmt, dev), Wtq.data_ptr(), Wts.data_ptr(),
         _one_f32(w_scale, "w_scale", fmt, dev), None if dX is None else dX.data_ptr(), lddx,
         None if dW is None else dW.data_ptr(), lddw, _vector(db, "db", N, torch.float32, dev),
-        wsp, wsb, _raw_stream(stream, dev)))
+        wsp, wsb, _raw_stream(dev)))
     return out
 
 
@@ -850,7 +871,10 @@ def _stats(stats, M, device):
 
 def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, Y=None, stats=None, stream=None):
     """(Y, mean, rstd) of the rows of X (M x D); gamma and beta in X's type or fp32 (None = 1, 0)."""
-    if Y is None and stats is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return layer_norm(X, gamma, beta, eps, Y, stats)
+    if Y is None and stats is None:
         result = _ordinary().layer_norm(X, gamma, beta, eps)
         if result is not None:
             return result
@@ -867,7 +891,7 @@ def layer_norm(X, gamma=None, beta=None, eps: float = 1e-5, Y=None, stats=None, 
         ldy = _matrix(Y, "Y", dev, dtype, M, D)
     mean, rstd = _stats(stats, M, dev)
     _check("layer_norm", lib().layer_norm(dt, M, D, X.data_ptr(), ldx, g, b, wd, eps, Y.data_ptr(), ldy,
-                                          mean.data_ptr(), rstd.data_ptr(), _raw_stream(stream, dev)))
+                                          mean.data_ptr(), rstd.data_ptr(), _raw_stream(dev)))
     return Y, mean, rstd
 
 
@@ -877,7 +901,10 @@ def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv",
 
     mean and rstd are None unless stats is True (new ones) or gives the two tensors.
     """
-    if out is None and stream is None and (stats is None or stats is True):
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return layer_norm_fp4(X, gamma, beta, eps, fmt, scale, out, stats)
+    if out is None and (stats is None or stats is True):
         result = _ordinary().layer_norm_fp4(X, gamma, beta, eps, fmt, scale, stats is True)
         if result is not None:
             return result
@@ -898,13 +925,16 @@ def layer_norm_fp4(X, gamma=None, beta=None, eps: float = 1e-5, fmt: str = "nv",
     _check("layer_norm_fp4", lib().layer_norm_fp4(
         f, dt, M, D, X.data_ptr(), ldx, g, b, wd, eps, _one_f32(scale, "scale", fmt, dev), Xq.data_ptr(),
         Xs.data_ptr(), None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(),
-        _raw_stream(stream, dev)))
+        _raw_stream(dev)))
     return Xq, Xs, mean, rstd
 
 
 def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None):
     """(dX, dgamma, dbeta) of layer_norm, with the mean and rstd it returned; dgamma and dbeta are fp32."""
-    if out is None and ws is None and stream is None:
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return layer_norm_backward(dY, X, gamma, mean, rstd, out, ws)
+    if out is None and ws is None:
         grads = _ordinary().layer_norm_backward(dY, X, gamma, mean, rstd)
         if grads is not None:
             return grads
@@ -923,9 +953,9 @@ def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None
         dX, dgamma, dbeta = out
         lddx = _matrix(dX, "dX", dev, dtype, M, D)
     L = lib()
-    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D), dev, stream)
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_LAYER_NORM_BACKWARD, 1, 1, D), dev)
     _check("layer_norm_backward", L.layer_norm_backward(
         dt, M, D, dY.data_ptr(), lddy, X.data_ptr(), ldx, g, wd, _vector(mean, "mean", M, f32, dev),
         _vector(rstd, "rstd", M, f32, dev), dX.data_ptr(), lddx, _vector(dgamma, "dgamma", D, f32, dev),
-        _vector(dbeta, "dbeta", D, f32, dev), wsp, wsb, _raw_stream(stream, dev)))
+        _vector(dbeta, "dbeta", D, f32, dev), wsp, wsb, _raw_stream(dev)))
     return dX, dgamma, dbeta

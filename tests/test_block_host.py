@@ -86,3 +86,143 @@ def test_bulk_copies_stay_inside_the_matrix(tmp_path):
                     "-o", str(exe)], check=True)
     run = subprocess.run([str(exe)], capture_output=True, text=True)
     assert run.returncode == 0, run.stdout
+
+
+# ------------------------------------------------------------- streams and devices
+#
+# The calls on stand-ins for torch and for the library: which stream an allocation is
+# made on and a kernel is launched on, and that nothing is launched when refused.
+
+class Stream:
+    def __init__(self, handle, index=0):
+        self.cuda_stream, self.device = handle, Device(index)
+
+
+class Device:
+    def __init__(self, index):
+        self.index = index
+
+    def __eq__(self, other):
+        return self.index == other.index
+
+    def __str__(self):
+        return f"cuda:{self.index}"
+
+
+class Tensor:
+    is_cuda = True
+
+    def __init__(self, shape, dtype, index=0):
+        self.shape, self.dtype, self.device = tuple(shape), dtype, Device(index)
+
+    def stride(self):
+        return tuple(self.numel() // max(1, self._upto(i + 1)) for i in range(len(self.shape)))
+
+    def _upto(self, n):
+        k = 1
+        for s in self.shape[:n]:
+            k *= s
+        return k
+
+    def numel(self):
+        return self._upto(len(self.shape))
+
+    def element_size(self):
+        return 4
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+
+class Torch:
+    """What the host side uses of torch, with a current stream and a log of allocations."""
+
+    def __init__(self):
+        import torch
+        self.uint8, self.float32, self.bfloat16, self.float16 = torch.uint8, torch.float32, torch.bfloat16, torch.float16
+        self.Tensor, self.current, self.allocated_on = Tensor, Stream(1), []
+        self.cuda, self._C = self, self
+
+    def empty(self, shape, dtype, device):
+        self.allocated_on.append(self.current.cuda_stream)
+        return Tensor(shape if isinstance(shape, tuple) else (shape,), dtype, device.index)
+
+    def current_device(self):
+        return self.current.device.index
+
+    def _cuda_getCurrentRawStream(self, index):
+        return self.current.cuda_stream
+
+    def stream(self, s):
+        import contextlib
+
+        @contextlib.contextmanager
+        def swap():
+            before, self.current = self.current, s
+            yield
+            self.current = before
+        return swap()
+
+
+class Library:
+    def __init__(self):
+        self.launched = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            if name == "qg_workspace_size":
+                return 4096
+            self.launched.append((name, args[-1]))
+            return 0
+        return call
+
+
+class Nothing:
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
+@pytest.fixture
+def stand_ins(monkeypatch):
+    torch, lib = Torch(), Library()
+    monkeypatch.setattr(qg, "_torch_module", torch)
+    monkeypatch.setattr(qg, "lib", lambda: lib)
+    monkeypatch.setattr(qg, "_ordinary", Nothing)
+    monkeypatch.setattr(qg, "_dtype_ids", None)
+    return torch, lib
+
+
+def calls(torch, index=0):
+    """Every call, 64 tokens of 64 values by 64 outputs, operands on cuda:index."""
+    x = Tensor((64, 64), torch.bfloat16, index)
+    q, s = Tensor((64, 32), torch.uint8, index), Tensor((1, 1, 512), torch.uint8, index)
+    v = Tensor((64,), torch.float32, index)
+    return {
+        "fp4_tensor_scale": lambda **kw: qg.fp4_tensor_scale(x, **kw),
+        "fp4_quantize": lambda **kw: qg.fp4_quantize(x, **kw),
+        "fp4_quantize_both": lambda **kw: qg.fp4_quantize_both(x, **kw),
+        "fp4_dequantize": lambda **kw: qg.fp4_dequantize(q, s, 64, **kw),
+        "fp4_gemm": lambda **kw: qg.fp4_gemm(q, s, q, s, 64, **kw),
+        "fp4_linear": lambda **kw: qg.fp4_linear(x, q, s, **kw),
+        "fp4_linear_backward": lambda **kw: qg.fp4_linear_backward(x, x, q, s, **kw),
+        "layer_norm": lambda **kw: qg.layer_norm(x, **kw),
+        "layer_norm_fp4": lambda **kw: qg.layer_norm_fp4(x, stats=True, **kw),
+        "layer_norm_backward": lambda **kw: qg.layer_norm_backward(x, x, None, v, v, **kw),
+    }
+
+
+CALLS = list(calls(Torch()))
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_what_a_call_allocates_belongs_to_its_stream(stand_ins, name):
+    torch, lib = stand_ins
+    calls(torch)[name]()
+    assert lib.launched == [(name, 1)] and set(torch.allocated_on) == {1}
+    lib.launched.clear(), torch.allocated_on.clear()
+    calls(torch)[name](stream=Stream(2))
+    assert lib.launched == [(name, 2)] and set(torch.allocated_on) == {2}
+    assert torch.current.cuda_stream == 1
