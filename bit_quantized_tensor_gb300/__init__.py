@@ -546,7 +546,10 @@ def _raw_stream(device):
 def _on(t, name, device):
     if not isinstance(t, _torch_module.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if device is not None and t.device != device:
+    if device is None:  # the first operand: the library launches on the current device
+        if t.device.index != _torch_module.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_torch_module.cuda.current_device()}")
+    elif t.device != device:
         raise ValueError(f"{name} is on {t.device}, other operands on {device}")
 
 

@@ -226,3 +226,16 @@ def test_what_a_call_allocates_belongs_to_its_stream(stand_ins, name):
     calls(torch)[name](stream=Stream(2))
     assert lib.launched == [(name, 2)] and set(torch.allocated_on) == {2}
     assert torch.current.cuda_stream == 1
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_operands_on_another_device_are_refused(stand_ins, name):
+    """A launch goes to the current device, which cannot be relied on to reach another's memory."""
+    torch, lib = stand_ins
+    with pytest.raises(ValueError, match="is on cuda:1, the current device is cuda:0"):
+        calls(torch, index=1)[name]()
+    with pytest.raises(ValueError, match="is on cuda:0, the current device is cuda:1"):
+        calls(torch)[name](stream=Stream(2, index=1))
+    assert not lib.launched
+    calls(torch, index=1)[name](stream=Stream(2, index=1))  # which makes cuda:1 the current one
+    assert lib.launched == [(name, 2)]
