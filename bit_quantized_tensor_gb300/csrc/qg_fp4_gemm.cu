@@ -30,6 +30,9 @@ constexpr int64_t kMaxGridY = 65535;
 template <class Cfg, class QUANT>
 static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, int splits, cudaStream_t s) {
     struct Flags {};  // the kernel's own shared-memory flag below
+    // a tile of fewer than 128 tokens holds all of them (plan_fp4 sees to it): another one
+    // would begin inside 128 scale rows, at a column of tensor memory that is none of theirs
+    if (Cfg::NT < 128 && p.M > Cfg::NT) return QG_ERR_UNSUPPORTED;
     CUtensorMap tw, tx, tsw, tsx;
     int rc = codes_map(&tw, w, p.K, 128);
     if (!rc) rc = scales_map(&tsw, w, Cfg::FMT, p.K, Cfg::ATOMS);
