@@ -500,9 +500,17 @@ _HOST_ENTRIES = ("qg_workspace_size", "fp4_tensor_scale", "fp4_quantize", "fp4_d
                  "fp4_linear_backward", "layer_norm", "layer_norm_fp4", "layer_norm_backward")
 
 
+class _NotBuilt:
+    """Stands for the module where there is none: no call is ordinary."""
+
+    def __getattr__(self, name):
+        return lambda *args: None
+
+
 def _ordinary():
     """csrc/qg_host.cpp: the ordinary call of each function below, in C++.  Its functions
-    return None for any other call, which then goes through ctypes."""
+    return None for any other call, which then goes through ctypes, as all do where the
+    module was not built or is another torch's."""
     global _host_module
     if _host_module is None:
         _torch()
@@ -510,8 +518,11 @@ def _ordinary():
         try:
             from . import _qg_host
         except ImportError as e:
-            raise RuntimeError("_qg_host.so is missing or does not load: build it with `python -c \"import "
-                               "__graft_entry__ as g; g.build()\"`") from e
+            import warnings
+            warnings.warn(f"_qg_host.so is missing or does not load ({e}): small calls take longer.  Build it with "
+                          f"`python -c \"import __graft_entry__ as g; g.build()\"`", RuntimeWarning, stacklevel=3)
+            _host_module = _NotBuilt()
+            return _host_module
         _qg_host.bind([ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _HOST_ENTRIES])
         _host_module = _qg_host
     return _host_module

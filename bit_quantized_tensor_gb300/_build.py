@@ -6,15 +6,19 @@ repository root, then nvcc links them into
 statically (the library has no run-time dependency on libcudart or
 libcuda; the driver's tensor-map encoder is fetched through the runtime's
 entry-point query).  Beside it g++ builds ``_qg_host.so``, the torch-facing
-host side of the small calls.  A build is skipped when both are newer than
-every source and header.
+host side of the small calls, where a torch with CUDA is installed; the library
+needs neither.  Each of the two is built only when it is older than its sources
+and headers, and the second also when torch or Python has changed.
 """
 from __future__ import annotations
 
 import glob
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -25,6 +29,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqgemm.so")
 HOST_SRC = os.path.join(CSRC, "qg_host.cpp")
 HOST = os.path.join(PKG, "_qg_host.so")
+HOST_FOR = os.path.join(BUILD_DIR, "_qg_host.for")  # what HOST was built against
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -45,17 +50,47 @@ def sources() -> list[str]:
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps() -> list[str]:
-    return (sources() + [HOST_SRC] + glob.glob(os.path.join(CSRC, "*.cuh"))
-            + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h"))
-            + [os.path.abspath(__file__)])
+def _newer(out: str, deps: list[str]) -> bool:
+    return os.path.exists(out) and all(os.path.getmtime(d) <= os.path.getmtime(out) for d in deps)
+
+
+def _headers() -> list[str]:
+    return glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + _headers())
+
+
+def _installed() -> str:
+    """The torch and Python that the extension is built against; empty without torch."""
+    if importlib.util.find_spec("torch") is None:
+        return ""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "unknown"
+    return f"torch {torch}, Python {sys.version_info.major}.{sys.version_info.minor}"
+
+
+def host_up_to_date() -> bool:
+    """True also where there is nothing to build it against."""
+    now = _installed()
+    if not now:
+        return True
+    try:
+        with open(HOST_FOR) as f:
+            built = f.read()
+    except OSError:
+        built = ""
+    return built in (now, now + NO_CUDA) and (built != now or _newer(HOST, [HOST_SRC] + _headers()))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(HOST):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(HOST))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return library_up_to_date() and host_up_to_date()
+
+
+NO_CUDA = ", without CUDA"
 
 
 def build_host() -> None:
@@ -63,6 +98,11 @@ def build_host() -> None:
     import sysconfig
 
     import torch
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    if torch.version.cuda is None:
+        with open(HOST_FOR, "w") as f:
+            f.write(_installed() + NO_CUDA)
+        return
     tdir = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = HOST + f".tmp{os.getpid()}"
@@ -75,11 +115,24 @@ def build_host() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {HOST_SRC}:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, HOST)
+    with open(HOST_FOR, "w") as f:
+        f.write(_installed())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and up_to_date():
-        return LIB
+    """Builds what is out of date; a failure of the extension is raised once the library is there."""
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        host = None
+        if _installed() and (force or not host_up_to_date()):
+            host = ex.submit(build_host)
+        if force or not library_up_to_date():
+            build_library(verbose)
+        if host is not None:
+            host.result()
+    return LIB
+
+
+def build_library(verbose: bool = False) -> None:
     os.makedirs(BUILD_DIR, exist_ok=True)
     cc = nvcc()
 
@@ -96,19 +149,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         return obj
 
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        host = ex.submit(build_host)
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
         objs = list(ex.map(compile_one, srcs))
-        host.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
