@@ -7,8 +7,9 @@
 //       448, tensor scale ts (fp32);
 //   mx: blocks of 32, e8m0 block scale  s = 2^(floor(log2 amax) - 2), no
 //       tensor scale (1).
-// With d = fl(s ts) and r = fl(1 / d), the code of x is fl(x r) rounded to
-// e2m1, ties to even, saturated at +-6; a block whose scale is 0 gets codes 0.
+// With d = fl(s ts) and r = fl(1 / d), at most the largest fp32 number, the code of x
+// is fl(x r) rounded to e2m1, ties to even, saturated at +-6; a block whose scale is 0
+// gets codes 0.
 // A block that holds an infinity or a NaN gets the format's NaN scale.
 //
 // Packed layout of a rows x K operand:
@@ -209,7 +210,8 @@ __device__ __forceinline__ uint32_t nv_scale_byte(uint32_t amax_bits, float six_
     return __nv_cvt_float_to_fp8(q, __NV_SATFINITE, __NV_E4M3);
 }
 
-// What a kernel needs of the tensor scale.
+// What a kernel needs of the tensor scale.  inv_six is 0 where 1 / six is no normal
+// number (ts below 2^-130 or above 2^123): then every block takes the division.
 struct TensorScale {
     float ts, six, inv_six;
 };
@@ -218,12 +220,14 @@ __device__ __forceinline__ TensorScale tensor_scale(const float* ts) {
     t.ts = ts ? *ts : 1.f;
     t.six = __fmul_rn(6.f, t.ts);
     t.inv_six = __frcp_rn(t.six);
+    if (!(t.inv_six >= 0x1p-126f && t.inv_six <= 0x1.fffffep+127f)) t.inv_six = 0.f;
     return t;
 }
 
-// r of every e4m3 byte (128 of them).
+// r of every e4m3 byte (128 of them); at most the largest number, since 0 times an
+// infinity would not be 0.
 __device__ __forceinline__ float nv_factor(uint32_t byte, float ts) {
-    return byte && byte < 127 ? __frcp_rn(__fmul_rn(e4m3_value(byte), ts)) : 0.f;
+    return byte && byte < 127 ? fminf(__frcp_rn(__fmul_rn(e4m3_value(byte), ts)), 0x1.fffffep+127f) : 0.f;
 }
 
 template <int FMT>

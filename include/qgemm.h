@@ -440,10 +440,11 @@ int w4a4_gemm_prepacked(int64_t M, int64_t N, int64_t K,
  *              device memory (NULL = 1).
  *   QG_FP4_MX  blocks of 32; block scale s = 2^(floor(log2 amax) - 2), as an
  *              e8m0 byte (exponent + 127, at least 0); no tensor scale.
- * With d = fl(s ts) and r = fl(1 / d) (fl: rounded to fp32), the code of x is
- * fl(x r) rounded to e2m1, ties to even, saturated at +-6.  A block whose
- * scale rounds to 0 has codes 0.  A block with an infinity or a NaN gets the
- * NaN scale (0x7f, 0xff): its values, and sums over them, are NaN.
+ * With d = fl(s ts) and r = fl(1 / d) (fl: rounded to fp32), r at most the
+ * largest fp32 number, the code of x is fl(x r) rounded to e2m1, ties to even,
+ * saturated at +-6.  A block whose scale rounds to 0 has codes 0.  A block with
+ * an infinity or a NaN gets the NaN scale (0x7f, 0xff): its values, and sums
+ * over them, are NaN.
  *
  * Packed operand of a rows x K matrix, K >= 1:
  *   codes   rows x qg_fp4_codes_ld(K) bytes (K up to whole 16 bytes), the even

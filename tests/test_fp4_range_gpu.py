@@ -1,5 +1,5 @@
 """Microscaled 4-bit products at the ends of their range: tensor scales whose product
-leaves fp32's normal range, and as many rows as the calls take."""
+leaves fp32's normal range, tensor scales at its ends, and as many rows as the calls take."""
 import numpy as np
 import pytest
 
@@ -61,6 +61,43 @@ def test_one_rounding_behind_the_sum(torch, qg, fmt):
     want = (exact + as_np(bias).astype(np.longdouble)).astype(np.float32)
     for y, cut in zip(outs, CUTS):
         assert np.array_equal(y.cpu().numpy(), want), cut
+
+
+# ------------------------------------------------------------- tensor scales at the ends of fp32
+
+def plain_nv(X, ts):
+    """Codes and scale bytes by the formula, each step rounded to 32 bits; r = fl(1 / d), at most the largest fp32."""
+    f = np.float32
+    x = X.reshape(X.shape[0], -1, 16)
+    with np.errstate(all="ignore"):
+        q = (np.abs(x).max(axis=2) / (f(6) * f(ts))).astype(f)
+        byte = ref._nearest_even(q.astype(np.float64), ref.E4M3)
+        d = (ref.E4M3[byte].astype(f) * f(ts)).astype(f)
+        r = np.where(byte > 0, np.minimum(f(1) / d, np.finfo(f).max), f(0)).astype(f)
+        y = (x * r[:, :, None]).astype(f)
+    code = ref._nearest_even(np.abs(y).astype(np.float64), ref.GRID) | np.where(np.signbit(y), 8, 0)
+    return code.reshape(X.shape).astype(np.uint8), byte.astype(np.uint8)
+
+
+@pytest.mark.parametrize("ts", [2.0 ** -149, 1.3 * 2.0 ** -140, 1.3 * 2.0 ** -131, 1.7 * 2.0 ** -127, 1.9 * 2.0 ** -119, 1.7 * 2.0 ** 110,
+                                1.3 * 2.0 ** 124, 1.9 * 2.0 ** 125, 3e38])
+def test_tensor_scales_at_the_ends_of_fp32(torch, qg, ts):
+    ts = float(np.float32(ts))
+    rng = np.random.default_rng(101)
+    for K in (256, 250):  # 250: rows that are not 16-byte aligned
+        X = np.zeros((40, 256), dtype=np.float32)
+        size = np.minimum(np.exp(rng.uniform(-6, 9, (40, 1))) * ts, 1e38)
+        X[:, :K] = np.clip(rng.standard_normal((40, K)) * size, -3e38, 3e38).astype(np.float32)
+        X[:, :K][rng.random((40, K)) < 0.2] = 0
+        code, byte = plain_nv(X, ts)
+        q_ref, s_ref = ref.pack(code, byte)
+        x = on_gpu(torch, X[:, :K])
+        for got in (qg.fp4_quantize(x, "nv", scale=one(torch, ts)), qg.fp4_quantize_both(x, "nv", scale=one(torch, ts))[:2]):
+            assert np.array_equal(as_np(got[1]), s_ref)
+            assert np.array_equal(as_np(got[0]), q_ref)
+        # what was 0 stands for 0
+        v = as_np(qg.fp4_dequantize(*qg.fp4_quantize(x, "nv", scale=one(torch, ts)), K, "nv", scale=one(torch, ts)))
+        assert not v[X[:, :K] == 0].any()
 
 
 # ------------------------------------------------------------- as many rows as the calls take
