@@ -393,6 +393,8 @@ __device__ __forceinline__ void load_words(const T* p, int n, bool aligned, uint
 
 // ------------------------------------------------------- host
 
+constexpr int64_t kMaxGridY = 65535;  // of a grid's y and z
+
 inline size_t dtype_bytes(int dtype) { return dtype == QG_F32 ? 4 : 2; }
 inline bool dtype_ok(int dtype) { return dtype == QG_F16 || dtype == QG_BF16 || dtype == QG_F32; }
 inline bool fmt_ok(int fmt) { return fmt == kNv || fmt == kMx; }

@@ -101,24 +101,28 @@ __device__ __forceinline__ void row_fetch(const RowRing& r, int s, const void* r
     if (at_end) row_edges(q, dst, t);
 }
 
-// The same for two rows of one length that share a slot: x, then y half a slot on.
+// The same for two rows of one length that share a slot: x, then y half a slot on;
+// at_end: either row is at an end of its matrix.
 template <int TPR>
-__device__ __forceinline__ void row_fetch2(const RowRing& r, int s, const void* x, const void* y, int64_t i,
+__device__ __forceinline__ void row_fetch2(const RowRing& r, int s, const void* x, const void* y, bool at_end,
                                            const RowBounds& mx, const RowBounds& my) {
     const int t = threadIdx.x % TPR;
-    const bool at_end = mx.at_end(i) || my.at_end(i);
-    if (t && !at_end) return;
     uint8_t* dx = r.slots + static_cast<int64_t>(s) * r.slot_bytes;
     uint8_t* dy = dx + r.slot_bytes / 2;
-    const RowPieces p = row_pieces(reinterpret_cast<uintptr_t>(x), r.row_bytes, mx, at_end);
-    const RowPieces q = row_pieces(reinterpret_cast<uintptr_t>(y), r.row_bytes, my, at_end);
     const uint32_t bar = r.bar0 + 8 * s;
-    if (t == 0) {
-        mbar_arrive_expect_tx(bar, p.bytes + q.bytes);
-        row_copy(p, dx, bar);
-        row_copy(q, dy, bar);
-    }
-    if (at_end) {
+    auto copy = [&](const RowPieces& p, const RowPieces& q) {
+        if (t == 0) {
+            mbar_arrive_expect_tx(bar, p.bytes + q.bytes);
+            row_copy(p, dx, bar);
+            row_copy(q, dy, bar);
+        }
+    };
+    const uintptr_t ax = reinterpret_cast<uintptr_t>(x), ay = reinterpret_cast<uintptr_t>(y);
+    if (!at_end) {
+        if (t == 0) copy(row_pieces(ax, r.row_bytes, mx, false), row_pieces(ay, r.row_bytes, my, false));
+    } else {
+        const RowPieces p = row_pieces(ax, r.row_bytes, mx, true), q = row_pieces(ay, r.row_bytes, my, true);
+        copy(p, q);
         row_edges(p, dx, t);
         row_edges(q, dy, t);
     }

@@ -25,10 +25,8 @@ static int scales_map(CUtensorMap* map, const Fp4Operand& o, int fmt, int64_t K,
                         512, 128, atoms, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
-constexpr int64_t kMaxGridY = 65535;
-
 template <class Cfg, class QUANT>
-static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params& p, int splits, cudaStream_t s) {
+static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, Fp4Params p, int splits, cudaStream_t s) {
     struct Flags {};  // the kernel's own shared-memory flag below
     // a tile of fewer than 128 tokens holds all of them (plan_fp4 sees to it): another one
     // would begin inside 128 scale rows, at a column of tensor memory that is none of theirs
@@ -47,6 +45,7 @@ static int launch_fp4(const Fp4Operand& x, const Fp4Operand& w, const Fp4Params&
     if (rc) return rc;
     const int64_t gx = (int64_t(p.N) + 127) / 128 * splits, gy = (int64_t(p.M) + Cfg::NT - 1) / Cfg::NT;
     if (gy > kMaxGridY) return QG_ERR_UNSUPPORTED;  // not by plan_fp4
+    while ((1 << p.log_splits) < splits) ++p.log_splits;
     return launch_serialized(fp4_gemm_kernel<Cfg, QUANT>,
                              dim3(static_cast<unsigned>(gx), static_cast<unsigned>(gy)), kFp4Threads,
                              splits > 1 ? Cfg::SMEM_JOIN_BYTES : Cfg::SMEM_BYTES, splits, s, tw, tx, tsw, tsx, p);

@@ -190,10 +190,10 @@ __global__ void __launch_bounds__(kBothThreads)
     float* const factors = sums + NB * kTile;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    // a grid's y would not count all tiles of rows
-    const uint32_t tiles_k = static_cast<uint32_t>((K + kTile - 1) / kTile), tile_m = blockIdx.x / tiles_k;
-    const int64_t m0 = static_cast<int64_t>(tile_m) * kTile;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x - tile_m * tiles_k) * kTile;
+    // tiles of rows along y, and along z where y does not count them all
+    const int64_t tile_m = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y, m0 = tile_m * kTile;
+    const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTile;
+    if (m0 >= M) return;
     const TensorScale ts = tensor_scale(FMT == kNv ? tscale : nullptr);
     if constexpr (FMT == kNv) {
         fill_factors(factors, ts.ts);
@@ -561,31 +561,33 @@ int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, in
 }
 
 template <int FMT, class T>
-static int launch_both(int64_t tiles, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
+static int launch_both(dim3 grid, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                        uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* partial, cudaStream_t s) {
     constexpr int SMEM = BothSmem<FMT, T>::BYTES;
     auto* f = k_fp4_quantize_both<FMT, T>;
     struct Flags {};
     const int rc = raise_smem<Flags>(f);
     if (rc) return rc;
-    return launch_serialized(f, dim3(static_cast<unsigned>(tiles)), kBothThreads, SMEM, 1, s, M, K,
-                             static_cast<const T*>(X), ldx, rows_aligned(X, ldx, sizeof(T), M), ts, Xq, Xs, Tq, Ts,
-                             partial);
+    return launch_serialized(f, grid, kBothThreads, SMEM, 1, s, M, K, static_cast<const T*>(X), ldx,
+                             rows_aligned(X, ldx, sizeof(T), M), ts, Xq, Xs, Tq, Ts, partial);
 }
 
 int fp4_quantize_both_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                           uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* colsum, float* partial,
                           cudaStream_t s) {
-    const int64_t tiles_m = (M + kTile - 1) / kTile, tiles = tiles_m * ((K + kTile - 1) / kTile);
-    if (tiles > INT32_MAX) return QG_ERR_UNSUPPORTED;  // 35 T values
+    const int64_t tiles_k = (K + kTile - 1) / kTile, tiles_m = (M + kTile - 1) / kTile;
+    const int64_t gy = tiles_m < kMaxGridY ? tiles_m : kMaxGridY;
     int rc = QG_OK;
-    if (tiles)
+    if (tiles_k && tiles_m) {
+        const dim3 grid(static_cast<unsigned>(tiles_k), static_cast<unsigned>(gy),
+                        static_cast<unsigned>((tiles_m + gy - 1) / gy));
         rc = by_dtype(dtype, [&](auto t) {
             using T = decltype(t);
             float* const part = colsum ? partial : nullptr;
-            return fmt == kNv ? launch_both<kNv, T>(tiles, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s)
-                              : launch_both<kMx, T>(tiles, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s);
+            return fmt == kNv ? launch_both<kNv, T>(grid, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s)
+                              : launch_both<kMx, T>(grid, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s);
         });
+    }
     if (rc || !colsum) return rc;
     return sum_partials_run(partial, tiles_m, K, colsum, s);
 }

@@ -298,7 +298,24 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
             if (p.mean) p.mean[row] = mean;
             if (p.rstd) p.rstd[row] = rstd;
         }
-        const uint64_t r2 = two(rstd, rstd);
+        uint64_t r2 = two(rstd, rstd);
+        if constexpr (FMT >= 0) {
+            // codes are 0 behind the row: x - mean, gamma and beta are 0 there, but 1 / std may be NaN
+            // or infinite; then it is the row's own values that become NaN (tested once a row:
+            // a cut of every piece costs 2 us in 39 at 8192 x 4096)
+            if (!(rstd < INFINITY)) {
+                r2 = two(1.f, 1.f);
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    uint64_t c[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) c[j] = two(NAN, NAN);
+                    cut_piece(c, first(i), D);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[4 * i + j] = c[j];
+                }
+            }
+        }
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int k = first(i);
@@ -308,8 +325,6 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
 #pragma unroll
             for (int j = 0; j < 4; ++j) y[j] = fma_two(mul_two(v[4 * i + j], r2), hg[4 * i + j], hb[4 * i + j]);
             if constexpr (FMT >= 0) {
-                // 0 behind the row: c, gamma and beta are 0 there, but 1 / std may be NaN
-                if (piece_cut(k, D)) cut_piece(y, k, D);
                 float f[8];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {

@@ -3,6 +3,8 @@
 //   dx = rstd (d - sum(d) / D - xh sum(d xh) / D)
 //   dgamma = sum over rows of dy xh,  dbeta = sum over rows of dy
 // Sums are fp32.  Bound by memory: x and dy are read and dx written once.
+#include <algorithm>
+
 #include "norm_common.cuh"
 
 namespace qg {
@@ -149,9 +151,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const T* dY = static_cast<const T*>(p.dY);
     const int64_t step = static_cast<int64_t>(gridDim.x) * GROUPS;
     int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + group;
+    // whole rows of whole pieces leave nothing to copy by hand; xb's ends are dyb's too
+    auto at_end = [&](int64_t r) { return (!VEC || EDGES) && p.xb.at_end(r); };
     for (int s = 0; s < slots; ++s) {
         const int64_t r = row + s * step;
-        if (r < p.M) row_fetch2<TPR>(ring, s, X + r * p.ldx, dY + r * p.lddy, r, p.xb, p.dyb);
+        if (r < p.M) row_fetch2<TPR>(ring, s, X + r * p.ldx, dY + r * p.lddy, at_end(r), p.xb, p.dyb);
     }
     float* const sg = reinterpret_cast<float*>(ring_smem + static_cast<int64_t>(GROUPS) * slots * ring.slot_bytes);
     if constexpr (!VEC) stage_weights<T>(sg, p.gamma, p.w_f32, D, 1.f);
@@ -317,9 +321,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int64_t ahead = row + (slots - 2) * step;
         if (n > 1 && ahead < p.M && !*static_cast<volatile int*>(&abort_flag)) {
             const int free_slot = s >= 2 ? s - 2 : s + slots - 2;
-            row_fetch2<TPR>(ring, free_slot, X + ahead * p.ldx, dY + ahead * p.lddy, ahead, p.xb, p.dyb);
+            row_fetch2<TPR>(ring, free_slot, X + ahead * p.ldx, dY + ahead * p.lddy, at_end(ahead), p.xb, p.dyb);
         }
-        if (n > 1 && ahead < p.M && (p.xb.at_end(ahead) || p.dyb.at_end(ahead))) {  // what threads copied of the last rows
+        if (n > 1 && ahead < p.M && at_end(ahead)) {  // what threads copied of the last rows
             if constexpr (TPR > 32)
                 asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
             else
@@ -586,6 +590,8 @@ int layer_norm_backward(int dtype, int64_t M, int64_t D, const void* dY, int64_t
     const int64_t elem = static_cast<int64_t>(dtype_bytes(dtype));
     p.xb = row_bounds(X, M, ldx * elem, D * elem);
     p.dyb = row_bounds(dY, M, lddy * elem, D * elem);
+    p.xb.near = std::max(p.xb.near, p.dyb.near);
+    p.xb.far = M - p.xb.near;
     p.w_f32 = wdtype == QG_F32;
     p.x_vec = vec_ok(X, ldx, dtype_bytes(dtype), M);
     p.dy_vec = vec_ok(dY, lddy, dtype_bytes(dtype), M);

@@ -17,16 +17,16 @@ namespace qg {
 // less than a piece behind it can start ahead of lo.
 struct RowBounds {
     uintptr_t lo, hi;
-    int64_t rows, near;
-    QG_HOST_DEVICE bool at_end(int64_t i) const { return i < near || i >= rows - near; }
+    int64_t near, far;  // rows from 0 to near, and from far on
+    QG_HOST_DEVICE bool at_end(int64_t i) const { return i < near || i >= far; }
 };
 inline RowBounds row_bounds(const void* matrix, int64_t rows, int64_t ld_bytes, int64_t row_bytes) {
     const uintptr_t start = reinterpret_cast<uintptr_t>(matrix);
     RowBounds b;
     b.lo = (start + 15) & ~uintptr_t(15);
     b.hi = (start + (rows > 0 ? static_cast<uintptr_t>((rows - 1) * ld_bytes + row_bytes) : 0)) & ~uintptr_t(15);
-    b.rows = rows;
     b.near = ld_bytes > 0 && ld_bytes < 16 ? (15 + ld_bytes) / ld_bytes : 1;
+    b.far = rows - b.near;
     return b;
 }
 
