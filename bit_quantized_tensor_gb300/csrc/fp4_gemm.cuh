@@ -309,12 +309,18 @@ __global__ void __launch_bounds__(kFp4Threads, 1)
         // Weights that were complete before the previous kernel began may
         // be fetched while that kernel (which makes the tokens' codes) runs.
         const int ahead = min(kb1 - kb0, STAGES);
-        if (!p.weights_ready) pdl_wait_prior_grid();
+        if (!p.weights_ready) {
+            pdl_wait_prior_grid();
+            fence_proxy_async_global();
+        }
         for (int i = 0; i < ahead; ++i) {
             arm(i);
             load_w(kb0 + i, i);
         }
-        if (p.weights_ready) pdl_wait_prior_grid();
+        if (p.weights_ready) {
+            pdl_wait_prior_grid();
+            fence_proxy_async_global();
+        }
         for (int i = 0; i < ahead; ++i) load_x(kb0 + i, i);
         Ring<STAGES> ps;
         for (int i = 0; i < ahead; ++i) ps.next();

@@ -152,6 +152,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer (both CTAs)
+        fence_proxy_async_global();
         const uint32_t elected = elect_lane();
         Ring<STAGES> ps;
         uint32_t armed = 0, armed_phase = 0;

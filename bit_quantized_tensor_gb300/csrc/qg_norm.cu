@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), norm_min_ctas(TPR))
     if (threadIdx.x == 0) abort_flag = 0;
     __syncthreads();
     pdl_wait_prior_grid();
+    fence_proxy_async_global();
     pdl_launch_dependents();
     if constexpr (FMT >= 0) zero_scale_rows<FMT>(p.M, p.D, p.Xs);
     const T* X = static_cast<const T*>(p.X);

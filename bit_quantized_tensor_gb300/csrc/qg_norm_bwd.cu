@@ -146,6 +146,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (threadIdx.x == 0) abort_flag = 0;
     __syncthreads();
     pdl_wait_prior_grid();
+    fence_proxy_async_global();
     pdl_launch_dependents();
     const T* X = static_cast<const T*>(p.X);
     const T* dY = static_cast<const T*>(p.dY);
