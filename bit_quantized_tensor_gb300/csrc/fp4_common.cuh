@@ -403,6 +403,8 @@ inline bool fmt_ok(int fmt) { return fmt == kNv || fmt == kMx; }
 // while the one before it on the stream drains.  Every kernel launched this
 // way begins with pdl_wait_prior_grid() before it reads or writes memory that
 // an earlier call may use, and lets its own successor start only after that.
+// Inputs may thus be written while it already runs: its parameters are not
+// `const ... __restrict__` and nothing is read with __ldg, which promise the opposite.
 template <class F, class... Args>
 int launch_serialized(F* kernel, dim3 grid, int threads, size_t smem, int cluster, cudaStream_t stream,
                       Args... args) {

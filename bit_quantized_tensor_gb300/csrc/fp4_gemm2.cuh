@@ -283,11 +283,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                 for (int j = 0; j < 16; ++j) f[j] *= alpha.second;
             } else if (col + 16 <= p.N) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = fmaf(f[j], alpha.second, to_f32<T>(__ldg(bias + col + j)));
+                for (int j = 0; j < 16; ++j) f[j] = fmaf(f[j], alpha.second, to_f32<T>(bias[col + j]));
             } else {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
-                    f[j] = fmaf(f[j], alpha.second, to_f32<T>(__ldg(bias + min(col + j, p.N - 1))));
+                    f[j] = fmaf(f[j], alpha.second, to_f32<T>(bias[min(col + j, p.N - 1)]));
             }
             if (sectors && col + 16 <= p.N) {
                 if (row0 + lane < p.M) store_sectors(Y + (row0 + lane) * p.ldy + col, f);

@@ -23,8 +23,8 @@ constexpr int kQuantThreads = 256;
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kQuantThreads)
-    k_fp4_quantize(int64_t M, int64_t rows, int64_t K, int log_tx, const T* __restrict__ X, int64_t ldx,
-                   const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
+    k_fp4_quantize(int64_t M, int64_t rows, int64_t K, int log_tx, const T* X, int64_t ldx,
+                   const float* tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
     constexpr int B = fp4_block(FMT);
     __shared__ float factors[128];
     pdl_wait_prior_grid();
@@ -94,8 +94,8 @@ __global__ void __launch_bounds__(kQuantThreads)
 // this way 3.1 us.
 template <int FMT, class T>
 __global__ void __launch_bounds__(kQuantThreads)
-    k_fp4_quantize_lanes(int64_t M, int64_t rows, int64_t K, const T* __restrict__ X, int64_t ldx,
-                         const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
+    k_fp4_quantize_lanes(int64_t M, int64_t rows, int64_t K, const T* X, int64_t ldx,
+                         const float* tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs) {
     constexpr int B = fp4_block(FMT), COLS = 8 * B, LOADS = COLS / 32;
     __shared__ float staged[kQuantThreads][B + 1];
     pdl_wait_prior_grid();
@@ -176,8 +176,8 @@ struct BothSmem {
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kBothThreads)
-    k_fp4_quantize_both(int64_t M, int64_t K, const T* __restrict__ X, int64_t ldx, bool aligned,
-                        const float* __restrict__ tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs,
+    k_fp4_quantize_both(int64_t M, int64_t K, const T* X, int64_t ldx, bool aligned,
+                        const float* tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs,
                         uint8_t* __restrict__ Tq, uint8_t* __restrict__ Ts, float* __restrict__ partial) {
     using S = BothSmem<FMT, T>;
     constexpr int B = S::B, NB = S::NB, PITCH = S::PITCH, W = B * static_cast<int>(sizeof(T)) / 4;
@@ -346,7 +346,7 @@ __device__ __forceinline__ uint32_t finite_abs_bits(float v) {
 
 template <class T>
 __global__ void __launch_bounds__(kAmaxThreads)
-    k_fp4_amax(int64_t M, int64_t K, const T* __restrict__ X, int64_t ldx, bool aligned,
+    k_fp4_amax(int64_t M, int64_t K, const T* X, int64_t ldx, bool aligned,
                uint32_t* __restrict__ part) {
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     pdl_wait_prior_grid();
@@ -399,7 +399,7 @@ __global__ void __launch_bounds__(kAmaxThreads)
     }
 }
 
-__global__ void __launch_bounds__(32) k_fp4_scale_join(const uint32_t* __restrict__ part, int parts,
+__global__ void __launch_bounds__(32) k_fp4_scale_join(const uint32_t* part, int parts,
                                                        float* __restrict__ scale) {
     pdl_wait_prior_grid();
     pdl_launch_dependents();
@@ -420,8 +420,8 @@ constexpr int kDequantThreads = 256;
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kDequantThreads)
-    k_fp4_dequantize(int64_t M, int64_t K, int log_tx, const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
-                     const float* __restrict__ tscale, T* __restrict__ Y, int64_t ldy, bool sectors) {
+    k_fp4_dequantize(int64_t M, int64_t K, int log_tx, const uint8_t* Xq, const uint8_t* Xs,
+                     const float* tscale, T* __restrict__ Y, int64_t ldy, bool sectors) {
     constexpr int B = fp4_block(FMT);
     pdl_wait_prior_grid();
     pdl_launch_dependents();
@@ -464,8 +464,8 @@ __global__ void __launch_bounds__(kDequantThreads)
 // into fp32, against 2.7 us.)
 template <int FMT, class T>
 __global__ void __launch_bounds__(kDequantThreads)
-    k_fp4_dequantize_lanes(int64_t M, int64_t K, const uint8_t* __restrict__ Xq, const uint8_t* __restrict__ Xs,
-                           const float* __restrict__ tscale, T* __restrict__ Y, int64_t ldy) {
+    k_fp4_dequantize_lanes(int64_t M, int64_t K, const uint8_t* Xq, const uint8_t* Xs,
+                           const float* tscale, T* __restrict__ Y, int64_t ldy) {
     constexpr int B = fp4_block(FMT);
     __shared__ float staged[kDequantThreads][17];
     pdl_wait_prior_grid();

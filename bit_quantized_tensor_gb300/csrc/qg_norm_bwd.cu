@@ -21,7 +21,7 @@ constexpr int kSumCols = 32;
 
 template <int SLICES>
 __global__ void __launch_bounds__(kSumCols* SLICES)
-    k_sum_partials(const float* __restrict__ partial, int64_t parts, int64_t n, float* __restrict__ out0,
+    k_sum_partials(const float* partial, int64_t parts, int64_t n, float* __restrict__ out0,
                    int64_t n0, float* __restrict__ out1) {
     __shared__ float acc[SLICES][kSumCols + 1];
     pdl_wait_prior_grid();
