@@ -444,7 +444,11 @@ __global__ void __launch_bounds__(kColThreads) k_layer_norm_columns(const NormBw
 // ------------------------------------------------------- host side
 
 constexpr int64_t kMaxHeldBwd = 8192;  // longest row that k_layer_norm_backward takes
-constexpr int kMaxPartials = 512;      // rows of partial sums, at most
+
+// Rows of partial sums, at most: one a CTA of k_layer_norm_backward, of which a GB300's
+// 152 SMs take one each, or of k_layer_norm_columns, of which eight an SM share 33
+// blocks of columns and more.
+static int max_partials(int64_t D) { return D <= kMaxHeldBwd ? 160 : 40; }
 
 // Dynamic shared memory of a launch: the rings, or the sums that follow them.
 static int64_t bwd_smem(int tpr, int vpt, int64_t D, size_t elem, bool vec, int* slots) {
@@ -461,7 +465,7 @@ static int launch_norm_bwd(const NormBwdParams& p, int64_t same, int dev, int64_
     constexpr int GROUPS = kBwdThreads / TPR;
     const Ctl ctl = host_ctl(dev);
     if (!ctl.status) return QG_ERR_CUDA;
-    const int most = num_sms(dev) < kMaxPartials ? num_sms(dev) : kMaxPartials;
+    const int most = std::min(num_sms(dev), max_partials(p.D));
     const int64_t ctas = norm_ctas(p.M, GROUPS, most, same);
     *parts = ctas;
     int slots = 0;
@@ -515,7 +519,7 @@ static int norm_backward(const NormBwdParams& p, float* dgamma, float* dbeta, in
             if (rc) return rc;
             const int64_t cols = (p.D + kColThreads - 1) / kColThreads;
             int64_t want = 8 * num_sms(dev) / cols + 1;  // about 8 CTAs an SM
-            if (want > kMaxPartials) want = kMaxPartials;
+            if (want > max_partials(p.D)) want = max_partials(p.D);
             const int64_t per = (p.M + want - 1) / want;
             parts = (p.M + per - 1) / per;
             rc = launch_serialized(k_layer_norm_columns<T>,
@@ -528,7 +532,7 @@ static int norm_backward(const NormBwdParams& p, float* dgamma, float* dbeta, in
 }
 
 size_t norm_backward_workspace(int64_t D) {
-    return static_cast<size_t>(kMaxPartials) * 2 * static_cast<size_t>(D) * sizeof(float);
+    return static_cast<size_t>(max_partials(D)) * 2 * static_cast<size_t>(D) * sizeof(float);
 }
 
 static int bwd_smem_most(int tpr, int vpt, size_t elem, bool vec) {

@@ -239,3 +239,11 @@ def test_operands_on_another_device_are_refused(stand_ins, name):
     assert not lib.launched
     calls(torch, index=1)[name](stream=Stream(2, index=1))  # which makes cuda:1 the current one
     assert lib.launched == [(name, 2)]
+
+
+# ------------------------------------------------------------- workspaces
+
+def test_workspace_of_the_norms_gradient(L):
+    """The rows of partial sums that a launch can leave: one an SM, fewer for long rows."""
+    for D, parts in ((1, 160), (8192, 160), (8193, 40), (16384, 40)):
+        assert L.qg_workspace_size(qg.QG_OP_LAYER_NORM_BACKWARD, 1, 1, D) == parts * 2 * D * 4
