@@ -176,7 +176,7 @@ struct BothSmem {
 
 template <int FMT, class T>
 __global__ void __launch_bounds__(kBothThreads)
-    k_fp4_quantize_both(int64_t M, int64_t K, const T* X, int64_t ldx, bool aligned,
+    k_fp4_quantize_both(uint32_t first_tile, int64_t M, int64_t K, const T* X, int64_t ldx, bool aligned,
                         const float* tscale, uint8_t* __restrict__ Xq, uint8_t* __restrict__ Xs,
                         uint8_t* __restrict__ Tq, uint8_t* __restrict__ Ts, float* __restrict__ partial) {
     using S = BothSmem<FMT, T>;
@@ -190,10 +190,8 @@ __global__ void __launch_bounds__(kBothThreads)
     float* const factors = sums + NB * kTile;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
-    // tiles of rows along y, and along z where y does not count them all
-    const int64_t tile_m = static_cast<int64_t>(blockIdx.z) * gridDim.y + blockIdx.y, m0 = tile_m * kTile;
-    const int64_t k0 = static_cast<int64_t>(blockIdx.x) * kTile;
-    if (m0 >= M) return;
+    const uint32_t tile_m = first_tile + blockIdx.y;
+    const int64_t m0 = static_cast<int64_t>(tile_m) * kTile, k0 = static_cast<int64_t>(blockIdx.x) * kTile;
     const TensorScale ts = tensor_scale(FMT == kNv ? tscale : nullptr);
     if constexpr (FMT == kNv) {
         fill_factors(factors, ts.ts);
@@ -561,14 +559,14 @@ int fp4_quantize_run(int fmt, int dtype, int64_t M, int64_t K, const void* X, in
 }
 
 template <int FMT, class T>
-static int launch_both(dim3 grid, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
+static int launch_both(dim3 grid, uint32_t first_tile, int64_t M, int64_t K, const void* X, int64_t ldx, const float* ts,
                        uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* partial, cudaStream_t s) {
     constexpr int SMEM = BothSmem<FMT, T>::BYTES;
     auto* f = k_fp4_quantize_both<FMT, T>;
     struct Flags {};
     const int rc = raise_smem<Flags>(f);
     if (rc) return rc;
-    return launch_serialized(f, grid, kBothThreads, SMEM, 1, s, M, K, static_cast<const T*>(X), ldx,
+    return launch_serialized(f, grid, kBothThreads, SMEM, 1, s, first_tile, M, K, static_cast<const T*>(X), ldx,
                              rows_aligned(X, ldx, sizeof(T), M), ts, Xq, Xs, Tq, Ts, partial);
 }
 
@@ -576,16 +574,17 @@ int fp4_quantize_both_run(int fmt, int dtype, int64_t M, int64_t K, const void* 
                           uint8_t* Xq, uint8_t* Xs, uint8_t* Tq, uint8_t* Ts, float* colsum, float* partial,
                           cudaStream_t s) {
     const int64_t tiles_k = (K + kTile - 1) / kTile, tiles_m = (M + kTile - 1) / kTile;
-    const int64_t gy = tiles_m < kMaxGridY ? tiles_m : kMaxGridY;
     int rc = QG_OK;
-    if (tiles_k && tiles_m) {
-        const dim3 grid(static_cast<unsigned>(tiles_k), static_cast<unsigned>(gy),
-                        static_cast<unsigned>((tiles_m + gy - 1) / gy));
+    // as many tiles of rows a launch as a grid's y counts
+    for (int64_t first = 0; !rc && tiles_k && first < tiles_m; first += kMaxGridY) {
+        const int64_t gy = tiles_m - first < kMaxGridY ? tiles_m - first : kMaxGridY;
+        const dim3 grid(static_cast<unsigned>(tiles_k), static_cast<unsigned>(gy));
+        const uint32_t at = static_cast<uint32_t>(first);
         rc = by_dtype(dtype, [&](auto t) {
             using T = decltype(t);
             float* const part = colsum ? partial : nullptr;
-            return fmt == kNv ? launch_both<kNv, T>(grid, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s)
-                              : launch_both<kMx, T>(grid, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s);
+            return fmt == kNv ? launch_both<kNv, T>(grid, at, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s)
+                              : launch_both<kMx, T>(grid, at, M, K, X, ldx, ts, Xq, Xs, Tq, Ts, part, s);
         });
     }
     if (rc || !colsum) return rc;
