@@ -16,9 +16,11 @@ namespace qg {
 // CTA on further rows; a thread walks down the rows with the same column, so
 // that addresses only advance.  Memory (2 or 4 bytes in, 0.56 or 0.53 out per
 // value) would allow 13 us for 4096 x 8192 bf16; from cold caches it takes 20.9 us
-// (86 MB, 4.1 TB/s), for the instructions a value: maxima are found on packed
-// words, the factors of the 128 scale bytes lie in a table, and divisions are left
-// to the few scales next to a rounding boundary.
+// (86 MB, 4.1 TB/s): a thread loads, waits and computes in turn, waits for loads are
+// the largest stall, and 44 % of an SM's warps do not cover them (DRAM 43 % busy).
+// Few instructions a value still count: maxima are found on packed words, the
+// factors of the 128 scale bytes lie in a table, and divisions are left to the few
+// scales next to a rounding boundary.
 constexpr int kQuantThreads = 256;
 
 template <int FMT, class T>
@@ -157,8 +159,9 @@ __global__ void __launch_bounds__(kQuantThreads)
 // at a time.  Codes of X^T and all scales are put together in shared memory
 // and leave in 16-byte pieces.  The tile also gives the column sums (the bias
 // gradient).  Memory (2 or 4 bytes in, 1.12 or 1.06 out per value) would allow
-// 15.7 us for 8192 x 4096 bf16; it takes 27 us, since each value is quantized twice
-// and the tile crosses shared memory once each way.
+// 15.7 us for 8192 x 4096 bf16; it takes 27 to 29 us (mx 25): each value is quantized
+// twice, the tile crosses shared memory once each way, and a CTA loads, waits and
+// computes in turn.
 constexpr int kBothThreads = 256;
 constexpr int kTile = 128;
 

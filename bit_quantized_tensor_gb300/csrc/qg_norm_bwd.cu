@@ -72,12 +72,12 @@ int sum_partials_run(const float* partial, int64_t parts, int64_t n, float* out,
 // exchange of a row's two sums between its warps does not show, it is split:
 // the warps leave their part of row i + 1, arrive at a barrier, finish dx of
 // row i from the ring, and only then wait.  At the end each CTA adds up its
-// groups, in order, and leaves one row of partial sums.  8192 x 8192 bf16: 81 us,
-// 82.5 with the sums of the partial rows (4.9 TB/s), bound by the latency of a row's
+// groups, in order, and leaves one row of partial sums.  8192 x 8192 bf16: 76 us with
+// the sums of the partial rows (5.3 TB/s), bound by the latency of a row's
 // arithmetic with four warps a scheduler; both of a row's sums exchanged at once
 // with its neighbour's, two rows a barrier, read the ring more often (113 us).
-// Rows that start inside a piece cost masks on top: 16411 x 515 f16 24 us,
-// 16411 x 512 15 us.
+// Rows that start inside a piece cost masks on top: from L2, sums included,
+// 16411 x 515 f16 24 us, 16411 x 512 14 us.
 constexpr int kBwdThreads = 512;
 __host__ __device__ constexpr int bwd_sums(int tpr, int vpt) { return 8 * vpt * (tpr + 4); }  // places of a group's sums
 constexpr int kSiteNormSums = 402;
@@ -480,7 +480,8 @@ static int launch_norm_bwd(const NormBwdParams& p, int64_t same, int dev, int64_
 
 // Threads a row: a warp while its lanes can hold the row's sums (up to 24
 // columns each; fp32 rows 16, for their slots), above that as few as hold them
-// in 16 columns each.
+// in 16 columns each.  Measured against the next count, 2^26 bf16 values, us: rows of
+// 512 69 (194 with 128 threads), 768 66 (132), 2048 78 (122 with 256), 4096 83 (111).
 template <class T, bool VEC, bool EDGES>
 static int norm_bwd_by_size(const NormBwdParams& p, int64_t same, int dev, int64_t* parts, cudaStream_t s) {
     const int64_t D = p.D + (VEC && EDGES ? 8 : 0);  // its place in the first piece
