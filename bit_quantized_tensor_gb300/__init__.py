@@ -28,6 +28,18 @@ tensor scale; "mx": blocks of 32 with power-of-two scales) and layer norm:
   layer_norm(X, gamma, beta)      y, mean, rstd
   layer_norm_fp4(X, gamma, beta)  the same, y quantized to a packed operand
   layer_norm_backward(...)        dX, dgamma, dbeta
+
+8-bit integers with a scale for each row (token or output channel), and the
+attention of a layer whose cache is held in 8 bits:
+  s8_quantize(X)                  X -> (codes, scales)
+  s8_gemm(Aq, As, Bq, Bs, K)      A . B^T (+ bias) of such operands
+  s8_linear(X, Wq, Ws)            Q(X) . W^T (+ bias), X quantized in the call
+  qk_norm_rope(Q, K, ...)         RMS norm of every head and rotation by position
+  qk_norm_rope_backward(...)      its gradients
+  kv8_cache(pages, heads, ...)    an empty paged cache: codes and scales of K and V
+  kv8_append(K, V, cache, ...)    new tokens into the cache
+  kv8_gather(cache, ...)          tokens of the cache as values
+  kv8_attention(Q, cache, ...)    attention of the new tokens over the cache
 """
 from __future__ import annotations
 
@@ -49,7 +61,8 @@ STATUS_NAMES = {0: "QG_OK", 1: "QG_ERR_INVALID_ARG", 2: "QG_ERR_UNSUPPORTED",
 QG_ROW_MAJOR, QG_COL_MAJOR = 0, 1
 (QG_OP_S8, QG_OP_S4, QG_OP_F16, QG_OP_W4A16, QG_OP_W4A4, QG_OP_S8_HOST, QG_OP_W4A4_PREPACKED,
  QG_OP_W4A4_WEIGHTS, QG_OP_FP4_LINEAR, QG_OP_FP4_LINEAR_BACKWARD, QG_OP_LAYER_NORM_BACKWARD,
- QG_OP_FP4_TENSOR_SCALE) = range(12)
+ QG_OP_FP4_TENSOR_SCALE, QG_OP_S8_LINEAR, QG_OP_QK_NORM_ROPE_BACKWARD, QG_OP_KV8_ATTENTION) = range(15)
+QG_ROPE_HALF, QG_ROPE_PAIRS = 0, 1
 QG_FP4_NV, QG_FP4_MX = 0, 1
 QG_F16, QG_BF16, QG_F32 = 0, 1, 2
 
@@ -129,6 +142,20 @@ SIGNATURES = {
                               _p]),
     "layer_norm_backward": (_int, [_int, _i64, _i64, _p, _i64, _p, _i64, _p, _int, _p, _p, _p, _i64, _p,
                                    _p, _p, _sz, _p]),
+    "qg_s8_codes_ld": (_i64, [_i64]),
+    "s8_quantize": (_int, [_int, _i64, _i64, _p, _i64, _p, _p, _p]),
+    "s8_gemm": (_int, [_int, _i64, _i64, _i64, _p, _p, _p, _p, _p, _p, _i64, _p, _sz, _p]),
+    "s8_linear": (_int, [_int, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _i64, _p, _sz, _p]),
+    "qk_norm_rope": (_int, [_int, _int, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _int, _p, _p, _i64,
+                            _f32, _p, _i64, _p, _i64, _p, _p, _p]),
+    "qk_norm_rope_backward": (_int, [_int, _int, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
+                                     _p, _p, _int, _p, _p, _i64, _p, _p, _p, _i64, _p, _i64, _p, _p, _p, _sz, _p]),
+    "kv8_append": (_int, [_int, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _p, _i64, _i64, _p, _i64, _p,
+                          _p, _p]),
+    "kv8_gather": (_int, [_int, _i64, _i64, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _p, _i64, _p, _p, _p, _i64, _p,
+                          _i64, _p]),
+    "kv8_attention": (_int, [_int, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p, _p, _p, _p, _i64, _i64, _p, _i64, _p,
+                             _p, _f32, _int, _p, _i64, _p, _sz, _p]),
 }
 
 _lib = None
@@ -497,7 +524,8 @@ def w4a4_gemm_prepacked(Xq, Xscale, packed, N: int, K: int, XU=None, Vt=None, bi
 
 _host_module = None
 _HOST_ENTRIES = ("qg_workspace_size", "fp4_tensor_scale", "fp4_quantize", "fp4_dequantize", "fp4_gemm", "fp4_linear",
-                 "fp4_linear_backward", "layer_norm", "layer_norm_fp4", "layer_norm_backward")
+                 "fp4_linear_backward", "layer_norm", "layer_norm_fp4", "layer_norm_backward", "s8_quantize", "s8_gemm",
+                 "s8_linear", "qk_norm_rope", "qk_norm_rope_backward", "kv8_append", "kv8_gather", "kv8_attention")
 
 
 class _NotBuilt:
@@ -973,3 +1001,354 @@ def layer_norm_backward(dY, X, gamma, mean, rstd, out=None, ws=None, stream=None
         _vector(rstd, "rstd", M, f32, dev), dX.data_ptr(), lddx, _vector(dgamma, "dgamma", D, f32, dev),
         _vector(dbeta, "dbeta", D, f32, dev), wsp, wsb, _raw_stream(dev)))
     return dX, dgamma, dbeta
+
+
+# ---------------------------------------------------------------- 8-bit integers with a scale for each row
+
+def _s8_operand(codes, scales, name, K, device=None):
+    """Checks an operand of 8-bit codes; returns its number of rows."""
+    torch = _torch_module
+    _on(codes, name, device)
+    _on(scales, name, codes.device)
+    if codes.dtype is not torch.int8 or scales.dtype is not torch.float32:
+        raise TypeError(f"{name}: codes must be int8 and scales float32")
+    shape = codes.shape
+    ld = (K + 15) // 16 * 16
+    if len(shape) != 2 or shape[1] != ld or not codes.is_contiguous():
+        raise ValueError(f"{name}: codes must be contiguous, rows x {ld} bytes for K = {K}")
+    if scales.numel() != shape[0] or not scales.is_contiguous():
+        raise ValueError(f"{name}: {shape[0]} contiguous scales are needed")
+    return shape[0]
+
+
+def s8_quantize(X, out=None, stream=None):
+    """X (M x K) -> (codes, scales): 8-bit integers and an fp32 scale for each row."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return s8_quantize(X, out)
+    if out is None:
+        both = _ordinary().s8_quantize(X)
+        if both is not None:
+            return both
+    torch = _torch()
+    ld = _matrix(X, "X")
+    dev = X.device
+    dt = _dtype_id(X.dtype, "X")
+    M, K = X.shape
+    if out is None:
+        out = (torch.empty((M, (K + 15) // 16 * 16), dtype=torch.int8, device=dev),
+               torch.empty(M, dtype=torch.float32, device=dev))
+    Q, S = out
+    if _s8_operand(Q, S, "out", K, dev) != M:
+        raise ValueError(f"out must have {M} rows")
+    _check("s8_quantize", lib().s8_quantize(dt, M, K, X.data_ptr(), ld, Q.data_ptr(), S.data_ptr(), _raw_stream(dev)))
+    return Q, S
+
+
+def s8_gemm(Aq, As, Bq, Bs, K: int, bias=None, dtype=None, Y=None, ws=None, stream=None):
+    """Y = A . B^T + bias of operands A (M x K) and B (N x K), in `dtype` (default: that of Y, or bfloat16)."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return s8_gemm(Aq, As, Bq, Bs, K, bias, dtype, Y, ws)
+    if Y is None and ws is None:
+        product = _ordinary().s8_gemm(Aq, As, Bq, Bs, K, bias, dtype)
+        if product is not None:
+            return product
+    torch = _torch()
+    M = _s8_operand(Aq, As, "A", K)
+    dev = Aq.device
+    N = _s8_operand(Bq, Bs, "B", K, dev)
+    if Y is None:
+        dtype = dtype or torch.bfloat16
+        dt = _dtype_id(dtype, "Y")
+        Y = torch.empty((M, N), dtype=dtype, device=dev)
+        ld = N
+    else:
+        ld = _matrix(Y, "Y", dev, dtype, M, N)
+        dtype = Y.dtype
+        dt = _dtype_id(dtype, "Y")
+    L = lib()
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_S8_LINEAR, M, N, K), dev)
+    _check("s8_gemm", L.s8_gemm(
+        dt, M, N, K, Aq.data_ptr(), As.data_ptr(), Bq.data_ptr(), Bs.data_ptr(), _vector(bias, "bias", N, dtype, dev),
+        Y.data_ptr(), ld, wsp, wsb, _raw_stream(dev)))
+    return Y
+
+
+def s8_linear(X, Wq, Ws, bias=None, Y=None, ws=None, stream=None):
+    """Y = Q(X) . W^T + bias with the operand W (N x K); X (M x K) is quantized in the call, Y has its type."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return s8_linear(X, Wq, Ws, bias, Y, ws)
+    if Y is None and ws is None:
+        product = _ordinary().s8_linear(X, Wq, Ws, bias)
+        if product is not None:
+            return product
+    torch = _torch()
+    ldx = _matrix(X, "X")
+    dev = X.device
+    dtype = X.dtype
+    dt = _dtype_id(dtype, "X")
+    M, K = X.shape
+    N = _s8_operand(Wq, Ws, "W", K, dev)
+    if Y is None:
+        Y = torch.empty((M, N), dtype=dtype, device=dev)
+        ldy = N
+    else:
+        ldy = _matrix(Y, "Y", dev, dtype, M, N)
+    L = lib()
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_S8_LINEAR, M, N, K), dev)
+    _check("s8_linear", L.s8_linear(
+        dt, M, N, K, X.data_ptr(), ldx, Wq.data_ptr(), Ws.data_ptr(), _vector(bias, "bias", N, dtype, dev),
+        Y.data_ptr(), ldy, wsp, wsb, _raw_stream(dev)))
+    return Y
+
+
+# ---------------------------------------------------------------- norm of queries and keys with rotation
+
+def _heads(t, name, device=None, dtype=None, shape=None):
+    """Checks a tokens x heads x D tensor, heads one after another; returns its rows' distance."""
+    _on(t, name, device)
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be tokens x heads x D")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {' x '.join(map(str, shape))}, got {' x '.join(map(str, t.shape))}")
+    T, H, D = t.shape
+    ld, head, unit = t.stride()
+    if t.numel() and ((unit != 1 and D > 1) or (head != D and H > 1)):
+        raise ValueError(f"the heads of {name} must lie one after another, with a contiguous last dimension")
+    if T <= 1:
+        return H * D
+    if ld < H * D:
+        raise ValueError(f"the rows of {name} overlap")
+    return ld
+
+
+def _rope_style(style):
+    if style == "half":
+        return QG_ROPE_HALF
+    if style == "pairs":
+        return QG_ROPE_PAIRS
+    raise ValueError(f"style must be 'half' or 'pairs', got {style!r}")
+
+
+def _rope_common(Q, K, gq, gk, positions, table, names):
+    """What both calls check: (T, Hq, Hk, D, R, ldq, ldk, gain addresses and type, positions, table)."""
+    torch = _torch()
+    ldq = _heads(Q, names[0])
+    dev, dtype = Q.device, Q.dtype
+    T, Hq, D = Q.shape
+    Hk, ldk = 0, 0
+    if K is not None:
+        _on(K, names[1], dev)
+        Hk = K.shape[1] if K.dim() == 3 else 0
+        ldk = _heads(K, names[1], dev, dtype, (T, Hk, D))
+    gains = [g for g in (gq, gk) if g is not None]
+    wdtype = gains[0].dtype if gains else dtype
+    if wdtype is not dtype and wdtype is not torch.float32:
+        raise TypeError(f"gains must be {dtype} or float32, got {wdtype}")
+    R, rows, tab = 0, 0, None
+    if table is not None:
+        _on(table, "table", dev)
+        if table.dtype is not torch.float32 or table.dim() != 2 or not table.is_contiguous():
+            raise TypeError("table must be a contiguous float32 matrix: positions x R")
+        rows, R = table.shape
+        tab = table.data_ptr()
+    return (T, Hq, Hk, D, R, ldq, ldk, _vector(gq, "gq", D, wdtype, dev), _vector(gk, "gk", D, wdtype, dev),
+            _dtype_id(wdtype, "gq"), _vector(positions, "positions", T, torch.int32, dev), tab, rows)
+
+
+def qk_norm_rope(Q, K, gq=None, gk=None, positions=None, table=None, eps: float = 1e-6, style: str = "half", out=None,
+                 stats=None, stream=None):
+    """(Yq, Yk, rq, rk): RMS norm of every head of Q (T x Hq x D) and K (T x Hk x D or None), times gq, gk (D values
+    in their type or fp32, None = 1), and the rotation of the first R values of a head by the token's position.
+
+    table (positions x R, fp32): cos of the R / 2 pairs, then sin; None leaves the rotation out.  positions (T, int32):
+    each token's row of the table, None = 0, 1, ...  style "half": pairs (i, R / 2 + i); "pairs": (2 i, 2 i + 1).
+    rq (T x Hq) and rk: 1 / rms, fp32, for the backward call.  Q and K may be views of a packed product's rows, and
+    the outputs in `out` may be Q and K themselves.
+    """
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return qk_norm_rope(Q, K, gq, gk, positions, table, eps, style, out, stats)
+    if out is None and stats is None:
+        result = _ordinary().qk_norm_rope(Q, K, gq, gk, positions, table, eps, style)
+        if result is not None:
+            return result
+    torch = _torch()
+    st = _rope_style(style)
+    T, Hq, Hk, D, R, ldq, ldk, g1, g2, wd, pos, tab, rows = _rope_common(Q, K, gq, gk, positions, table, ("Q", "K"))
+    dev, dtype = Q.device, Q.dtype
+    dt = _dtype_id(dtype, "Q")
+    if out is None:
+        out = (torch.empty((T, Hq, D), dtype=dtype, device=dev),
+               None if K is None else torch.empty((T, Hk, D), dtype=dtype, device=dev))
+    Yq, Yk = out
+    ldyq = _heads(Yq, "Yq", dev, dtype, (T, Hq, D))
+    ldyk = 0 if K is None else _heads(Yk, "Yk", dev, dtype, (T, Hk, D))
+    if stats is None:
+        stats = (torch.empty((T, Hq), dtype=torch.float32, device=dev),
+                 None if K is None else torch.empty((T, Hk), dtype=torch.float32, device=dev))
+    rq, rk = stats
+    _check("qk_norm_rope", lib().qk_norm_rope(
+        dt, st, T, Hq, Hk, D, R, Q.data_ptr(), ldq, None if K is None else K.data_ptr(), ldk, g1, g2, wd, pos, tab, rows,
+        eps, Yq.data_ptr(), ldyq, None if K is None else Yk.data_ptr(), ldyk,
+        _vector(rq, "rq", T * Hq, torch.float32, dev),
+        None if K is None else _vector(rk, "rk", T * Hk, torch.float32, dev), _raw_stream(dev)))
+    return Yq, None if K is None else Yk, rq, rk
+
+
+def qk_norm_rope_backward(dYq, dYk, Q, K, gq, gk, positions, table, rq, rk, style: str = "half", out=None, ws=None,
+                          stream=None):
+    """(dQ, dK, dgq, dgk) of qk_norm_rope, with the Q and K it read and the rq and rk it returned; the gains'
+    gradients are fp32.  out: (dQ, dK, dgq, dgk), of which dQ and dK may be views of a packed gradient's rows."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return qk_norm_rope_backward(dYq, dYk, Q, K, gq, gk, positions, table, rq, rk, style, out, ws)
+    if out is None and ws is None:
+        grads = _ordinary().qk_norm_rope_backward(dYq, dYk, Q, K, gq, gk, positions, table, rq, rk, style)
+        if grads is not None:
+            return grads
+    torch = _torch()
+    st = _rope_style(style)
+    T, Hq, Hk, D, R, ldq, ldk, g1, g2, wd, pos, tab, rows = _rope_common(Q, K, gq, gk, positions, table, ("Q", "K"))
+    dev, dtype, f32 = Q.device, Q.dtype, torch.float32
+    dt = _dtype_id(dtype, "Q")
+    lddyq = _heads(dYq, "dYq", dev, dtype, (T, Hq, D))
+    lddyk = 0 if K is None else _heads(dYk, "dYk", dev, dtype, (T, Hk, D))
+    if out is None:
+        out = (torch.empty((T, Hq, D), dtype=dtype, device=dev),
+               None if K is None else torch.empty((T, Hk, D), dtype=dtype, device=dev),
+               torch.empty(D, dtype=f32, device=dev), None if K is None else torch.empty(D, dtype=f32, device=dev))
+    dQ, dK, dgq, dgk = out
+    lddq = _heads(dQ, "dQ", dev, dtype, (T, Hq, D))
+    lddk = 0 if K is None else _heads(dK, "dK", dev, dtype, (T, Hk, D))
+    L = lib()
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_QK_NORM_ROPE_BACKWARD, 1, 1, D), dev)
+    none = K is None
+    _check("qk_norm_rope_backward", L.qk_norm_rope_backward(
+        dt, st, T, Hq, Hk, D, R, dYq.data_ptr(), lddyq, None if none else dYk.data_ptr(), lddyk, Q.data_ptr(), ldq,
+        None if none else K.data_ptr(), ldk, g1, g2, wd, pos, tab, rows, _vector(rq, "rq", T * Hq, f32, dev),
+        None if none else _vector(rk, "rk", T * Hk, f32, dev), dQ.data_ptr(), lddq, None if none else dK.data_ptr(), lddk,
+        _vector(dgq, "dgq", D, f32, dev), None if none else _vector(dgk, "dgk", D, f32, dev), wsp, wsb, _raw_stream(dev)))
+    return dQ, None if none else dK, dgq, None if none else dgk
+
+
+# ---------------------------------------------------------------- paged cache in 8 bits
+
+def kv8_cache(pages: int, heads: int, page: int = 64, D: int = 128, device="cuda"):
+    """An empty cache (kq, vq, ks, vs): codes pages x heads x page x D (int8), scales pages x heads (fp32), for K and V."""
+    torch = _torch()
+    kq, vq = (torch.zeros((pages, heads, page, D), dtype=torch.int8, device=device) for _ in range(2))
+    ks, vs = (torch.zeros((pages, heads), dtype=torch.float32, device=device) for _ in range(2))
+    return kq, vq, ks, vs
+
+
+def _kv8(cache, table, starts, lengths, device):
+    """Checks a cache and its batch; returns (B, heads, D, addresses and sizes as the C calls take them)."""
+    torch = _torch_module
+    kq, vq, ks, vs = cache
+    for name, t, dtype in (("kq", kq, torch.int8), ("vq", vq, torch.int8), ("ks", ks, torch.float32),
+                           ("vs", vs, torch.float32), ("table", table, torch.int32), ("starts", starts, torch.int32),
+                           ("lengths", lengths, torch.int32)):
+        _on(t, name, device)
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    if kq.dim() != 4 or vq.shape != kq.shape:
+        raise ValueError("kq and vq must be pages x heads x page x D")
+    pages, heads, page, D = kq.shape
+    if tuple(ks.shape) != (pages, heads) or tuple(vs.shape) != (pages, heads):
+        raise ValueError(f"ks and vs must be {pages} x {heads}")
+    if table.dim() != 2 or lengths.dim() != 1 or starts.dim() != 1:
+        raise ValueError("table must be 2-D, starts and lengths 1-D")
+    B, cols = table.shape
+    if lengths.shape[0] != B or starts.shape[0] != B + 1:
+        raise ValueError(f"{B} sequences need {B} lengths and {B + 1} starts")
+    return B, heads, D, (kq.data_ptr(), vq.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, page, table.data_ptr(), cols,
+                         starts.data_ptr(), lengths.data_ptr())
+
+
+def kv8_append(K, V, cache, table, starts, lengths, stream=None):
+    """Writes new tokens K, V (rows x heads x D) into the cache: row starts[b] + i is token
+    lengths[b] - (starts[b + 1] - starts[b]) + i of sequence b, in page table[b][token // page]."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return kv8_append(K, V, cache, table, starts, lengths)
+    if _ordinary().kv8_append(K, V, cache, table, starts, lengths) is not None:
+        return
+    _torch()
+    ldk = _heads(K, "K")
+    dev = K.device
+    dt = _dtype_id(K.dtype, "K")
+    B, heads, D, args = _kv8(cache, table, starts, lengths, dev)
+    rows = K.shape[0]
+    if tuple(K.shape[1:]) != (heads, D):
+        raise ValueError(f"K must be rows x {heads} x {D}")
+    ldv = _heads(V, "V", dev, K.dtype, K.shape)
+    _check("kv8_append", lib().kv8_append(dt, B, rows, heads, D, K.data_ptr(), ldk, V.data_ptr(), ldv, *args,
+                                          _raw_stream(dev)))
+
+
+def kv8_gather(cache, table, starts, lengths, rows: int, dtype=None, out=None, stream=None):
+    """(K, V), rows x heads x D in `dtype` (default: that of out, or bfloat16): rows starts[b] .. starts[b + 1] are the
+    last tokens of sequence b, as values.  Rows of no sequence are not written."""
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return kv8_gather(cache, table, starts, lengths, rows, dtype, out)
+    if out is None:
+        both = _ordinary().kv8_gather(cache, table, starts, lengths, rows, dtype)
+        if both is not None:
+            return both
+    torch = _torch()
+    _on(cache[0], "kq", None)
+    dev = cache[0].device
+    B, heads, D, args = _kv8(cache, table, starts, lengths, dev)
+    if out is None:
+        out = tuple(torch.empty((rows, heads, D), dtype=dtype or torch.bfloat16, device=dev) for _ in range(2))
+    K, V = out
+    ldk = _heads(K, "K", dev, dtype, (rows, heads, D))
+    ldv = _heads(V, "V", dev, K.dtype, (rows, heads, D))
+    _check("kv8_gather", lib().kv8_gather(_dtype_id(K.dtype, "K"), B, rows, heads, D, *args, K.data_ptr(), ldk,
+                                          V.data_ptr(), ldv, _raw_stream(dev)))
+    return K, V
+
+
+def kv8_attention(Q, cache, table, starts, lengths, scale=None, causal: bool = True, O=None, ws=None, stream=None):
+    """softmax(scale Q K^T) V of Q (rows x query heads x D, float16 or bfloat16) over the cache, in Q's type.
+
+    Rows starts[b] .. starts[b + 1] are the last tokens of sequence b; causal: each sees the tokens up to its own, else
+    all lengths[b].  Query head h reads head h // (query heads // heads).  scale: default 1 / sqrt(D).  Rows of no
+    sequence are not written.
+    """
+    if stream is not None:
+        with _torch().cuda.stream(stream):
+            return kv8_attention(Q, cache, table, starts, lengths, scale, causal, O, ws)
+    if scale is None:
+        scale = Q.shape[-1] ** -0.5
+    if O is None and ws is None:
+        result = _ordinary().kv8_attention(Q, cache, table, starts, lengths, scale, causal)
+        if result is not None:
+            return result
+    torch = _torch()
+    ldq = _heads(Q, "Q")
+    dev = Q.device
+    if Q.dtype is not torch.float16 and Q.dtype is not torch.bfloat16:
+        raise TypeError(f"Q must be float16 or bfloat16, got {Q.dtype}")
+    dt = _dtype_id(Q.dtype, "Q")
+    B, heads, D, args = _kv8(cache, table, starts, lengths, dev)
+    rows, q_heads, d = Q.shape
+    if d != D or q_heads % heads:
+        raise ValueError(f"Q must be rows x a multiple of {heads} heads x {D}")
+    if O is None:
+        O = torch.empty((rows, q_heads, D), dtype=Q.dtype, device=dev)
+    ldo = _heads(O, "O", dev, Q.dtype, Q.shape)
+    L = lib()
+    ws, wsp, wsb = _scratch(ws, L.qg_workspace_size(QG_OP_KV8_ATTENTION, rows, q_heads, D), dev)
+    _check("kv8_attention", L.kv8_attention(
+        dt, B, rows, q_heads, heads, D, Q.data_ptr(), ldq, *args, scale, int(bool(causal)), O.data_ptr(), ldo, wsp, wsb,
+        _raw_stream(dev)))
+    return O

@@ -199,6 +199,9 @@ size_t qg_workspace_size(int op, int64_t M, int64_t N, int64_t K) {
         case QG_OP_FP4_LINEAR_BACKWARD: return qg::fp4_linear_backward_workspace(M, N, K);
         case QG_OP_LAYER_NORM_BACKWARD: return qg::norm_backward_workspace(K);
         case QG_OP_FP4_TENSOR_SCALE: return 4096;  // one maximum per CTA, at most 1024
+        case QG_OP_S8_LINEAR: return qg::s8_linear_workspace(M, N, K);
+        case QG_OP_QK_NORM_ROPE_BACKWARD: return qg::rope_backward_workspace(K);
+        case QG_OP_KV8_ATTENTION: return qg::kv8_attention_workspace(M, N, K);
         default:
             return 0;
     }

@@ -85,7 +85,7 @@ static std::atomic<int> g_l2_mode{0};
 template <class Cfg>
 static int launch_tc(const void* A, int64_t lda_bytes, const void* B, int64_t ldb_bytes, int64_t M,
                      int64_t N, int64_t K, void* C, int64_t ldc, int chunk_kb, const __half* bias,
-                     const Ctl& ctl, cudaStream_t stream) {
+                     const Ctl& ctl, cudaStream_t stream, const S8Scales& s8 = {}) {
     constexpr bool f16 = Cfg::KIND == MmaKind::F16;
     CUtensorMap ta, tb;
     int rc = make_tmap_kmajor(&ta, f16, A, K, M, lda_bytes, Cfg::BK, Cfg::BM);
@@ -119,6 +119,7 @@ static int launch_tc(const void* A, int64_t lda_bytes, const void* B, int64_t ld
     p.bias = bias;
     p.ctl = ctl;
     p.l2_mode = g_l2_mode.load();
+    p.s8 = s8;
     const int64_t tiles = ((M + Cfg::BM - 1) / Cfg::BM) * ((N + Cfg::BN - 1) / Cfg::BN);
     const int grid = static_cast<int>(tiles < num_sms(dev) ? tiles : num_sms(dev));
     cudaEvent_t ev0 = static_cast<cudaEvent_t>(g_prof_before.load());
@@ -134,7 +135,7 @@ static int launch_tc(const void* A, int64_t lda_bytes, const void* B, int64_t ld
 template <class Cfg>
 static int launch_tc2(const void* A, int64_t lda_bytes, const void* B, int64_t ldb_bytes, int64_t M,
                       int64_t N, int64_t K, void* C, int64_t ldc, int chunk_kb, const __half* bias,
-                      const Ctl& ctl, cudaStream_t stream) {
+                      const Ctl& ctl, cudaStream_t stream, const S8Scales& s8 = {}) {
     constexpr bool f16 = Cfg::KIND == MmaKind::F16;
     CUtensorMap ta, tb;
     int rc = make_tmap_kmajor(&ta, f16, A, K, M, lda_bytes, Cfg::BK, Cfg::BM);
@@ -166,6 +167,7 @@ static int launch_tc2(const void* A, int64_t lda_bytes, const void* B, int64_t l
     p.bias = bias;
     p.ctl = ctl;
     p.l2_mode = g_l2_mode.load();
+    p.s8 = s8;
     const int64_t tiles = ((M + 2 * Cfg::BM - 1) / (2 * Cfg::BM)) * ((N + Cfg::BN - 1) / Cfg::BN);
     const int64_t max_pairs = num_sms(dev) / 2;
     const int grid = 2 * static_cast<int>(tiles < max_pairs ? tiles : max_pairs);
@@ -195,12 +197,12 @@ static bool use_pairs(int64_t M, int64_t N) {
 template <MmaKind KIND, Epi EPI>
 static int launch_gemm(const void* A, int64_t lda_bytes, const void* B, int64_t ldb_bytes, int64_t M,
                        int64_t N, int64_t K, void* C, int64_t ldc, int chunk_kb, const __half* bias,
-                       const Ctl& ctl, cudaStream_t stream) {
+                       const Ctl& ctl, cudaStream_t stream, const S8Scales& s8 = {}) {
     if (use_pairs(M, N))
         return launch_tc2<Tc2Cfg<KIND, EPI>>(A, lda_bytes, B, ldb_bytes, M, N, K, C, ldc, chunk_kb,
-                                            bias, ctl, stream);
+                                            bias, ctl, stream, s8);
     return launch_tc<TcGemmCfg<KIND, EPI>>(A, lda_bytes, B, ldb_bytes, M, N, K, C, ldc, chunk_kb,
-                                          bias, ctl, stream);
+                                          bias, ctl, stream, s8);
 }
 
 // qgemm_s4 route (qg_set_s4_path): 0 = the in-kernel nibble conversion where
@@ -456,6 +458,12 @@ int run_gemm_s8_converted(const __half* A16, const __half* B16, int64_t M, int64
                                                ctl, stream);
 }
 
+int run_gemm_s8_scaled(const __half* A16, const __half* B16, int64_t M, int64_t N, int64_t K, int64_t ld, void* Y,
+                       int64_t ldy, const S8Scales& e, const Ctl& ctl, cudaStream_t stream) {
+    return launch_gemm<MmaKind::F16, Epi::S8>(A16, ld * 2, B16, ld * 2, M, N, K, Y, ldy, g_s8_chunk_kb.load(), nullptr,
+                                              ctl, stream, e);
+}
+
 // Resource budgets of the instances launched above.
 #define QG_TC_BUDGET(CFG, NAME, CLUSTER)                                                      \
     QG_KERNEL_BUDGET(NAME, reinterpret_cast<const void*>(CFG), CFG##_Cfg::THREADS,              \
@@ -478,6 +486,12 @@ QG_TC_BUDGET(TcF16, "tc_gemm_kernel<F16,F16>", 1);
 QG_TC_BUDGET(Tc2S8, "tc_gemm2_kernel<F16,S32>", 2);
 QG_TC_BUDGET(Tc2S4, "tc_gemm2_kernel<F8F6F4,S32>", 2);
 QG_TC_BUDGET(Tc2F16, "tc_gemm2_kernel<F16,F16>", 2);
+using TcS8Scaled_Cfg = TcGemmCfg<MmaKind::F16, Epi::S8>;
+using Tc2S8Scaled_Cfg = Tc2Cfg<MmaKind::F16, Epi::S8>;
+QG_BLOCK_KERNEL_BUDGET("tc_gemm_kernel<F16,S8>", reinterpret_cast<const void*>(tc_gemm_kernel<TcS8Scaled_Cfg>),
+                       TcS8Scaled_Cfg::THREADS, TcS8Scaled_Cfg::SMEM_BYTES, TcS8Scaled_Cfg::TMEM_COLS, 1, 1);
+QG_BLOCK_KERNEL_BUDGET("tc_gemm2_kernel<F16,S8>", reinterpret_cast<const void*>(tc_gemm2_kernel<Tc2S8Scaled_Cfg>),
+                       Tc2S8Scaled_Cfg::THREADS, Tc2S8Scaled_Cfg::SMEM_BYTES, Tc2S8Scaled_Cfg::TMEM_COLS, 2, 1);
 #undef QG_TC_BUDGET
 QG_KERNEL_BUDGET("tc_gemm2_s4raw_kernel", reinterpret_cast<const void*>(tc_gemm2_s4raw_kernel), S4RawCfg::THREADS,
                  S4RawCfg::SMEM_BYTES, S4RawCfg::TMEM_COLS, 2, 1);

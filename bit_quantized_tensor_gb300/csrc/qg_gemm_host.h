@@ -44,6 +44,20 @@ int s8_to_f16_rows(const int8_t* src, int64_t rows, int64_t lds, __half* dst, in
 int run_gemm_s8_converted(const __half* A16, const __half* B16, int64_t M, int64_t N, int64_t K, int32_t* C,
                           int64_t ldc, const Ctl& ctl, cudaStream_t stream);
 
+// What turns the sums of 8-bit codes into values: a scale for each row and each
+// column, and an optional bias (`dtype`, the type of the result) for each column.
+struct S8Scales {
+    const float* sa = nullptr;
+    const float* sb = nullptr;
+    const void* bias = nullptr;
+    int dtype = 0;
+};
+
+// The sums of run_gemm_s8_converted over the first K of `ld` values a row (the rest
+// does not count), scaled: Y (M x N of e.dtype) = sum * sa * sb + bias.
+int run_gemm_s8_scaled(const __half* A16, const __half* B16, int64_t M, int64_t N, int64_t K, int64_t ld, void* Y,
+                       int64_t ldy, const S8Scales& e, const Ctl& ctl, cudaStream_t stream);
+
 // Grid size for the elementwise grid-stride kernels (256 threads per block).
 int conv_grid(int dev, int64_t work_items);
 

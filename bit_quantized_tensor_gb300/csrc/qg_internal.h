@@ -85,6 +85,13 @@ size_t fp4_linear_workspace(int64_t M, int64_t K);
 size_t fp4_linear_backward_workspace(int64_t M, int64_t N, int64_t K);
 size_t norm_backward_workspace(int64_t D);
 
+// Workspace bytes of the scaled 8-bit products.
+size_t s8_linear_workspace(int64_t M, int64_t N, int64_t K);
+
+// Workspace bytes of qk_norm_rope_backward and of kv8_attention.
+size_t rope_backward_workspace(int64_t D);
+size_t kv8_attention_workspace(int64_t rows, int64_t q_heads, int64_t D);
+
 // Workspace bytes of qgemm_s8_host (qg_hostio.cu).
 size_t s8_host_workspace(int64_t M, int64_t N, int64_t K);
 

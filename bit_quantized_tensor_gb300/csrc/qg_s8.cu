@@ -1,0 +1,487 @@
+// Products of 8-bit integers with a scale for each token and output channel:
+//   Y[m][n] = sa[m] sb[n] sum_k qa[m][k] qb[n][k] + bias[n]
+// and the quantizer that makes such operands (s8_common.cuh).  The integer sums
+// are exact (K < 131072) and rounded once to fp32.
+#include <cuda.h>
+#include <cuda_fp16.h>
+
+#include "qg_gemm_host.h"
+#include "s8_common.cuh"
+
+namespace qg {
+
+// ------------------------------------------------------------ quantizer
+
+// One row a group of TPR threads, up to 32 values a thread in registers; LONG: any
+// length, read twice.  OUT: int8_t (packed operand) or __half (the codes as fp16
+// numbers, the tensor cores' operand).  Bound by the bytes it reads and writes.
+constexpr int kQuantChunks = 4;
+
+template <class OUT>
+__device__ __forceinline__ void store_codes(OUT* dst, const float (&x)[8], float r) {
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = s8_code(x[i], r);
+    if constexpr (sizeof(OUT) == 1) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
+    } else {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(q[i]);
+        store_vec<OUT, 8>(dst, f);
+    }
+}
+
+template <class T, class OUT, int TPR, bool LONG>
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
+    k_s8_quantize(int M, int K, const void* X, int64_t ldx, bool aligned, OUT* Q, int ldq, float* S) {
+    constexpr int GROUPS = TPR < 128 ? 128 / TPR : 1;
+    __shared__ uint32_t red[32];
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    const int t = threadIdx.x % TPR;
+    const int64_t row = static_cast<int64_t>(blockIdx.x) * GROUPS + threadIdx.x / TPR;
+    if (TPR <= 32 && row >= M) return;  // whole groups; wider groups have a row each
+    const T* x = static_cast<const T*>(X) + row * ldx;
+    OUT* q = Q + row * ldq;
+    uint32_t amax = 0;
+    float v[kQuantChunks][8];
+    if constexpr (LONG) {
+        for (int k = 8 * t; k < K; k += 8 * TPR) {
+            load_some<T, 8>(x + k, K - k, aligned, v[0]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[0][i]));
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < kQuantChunks; ++c) {
+            const int k = 8 * (t + c * TPR);
+            if (k < K) load_some<T, 8>(x + k, K - k, aligned, v[c]);
+        }
+#pragma unroll
+        for (int c = 0; c < kQuantChunks; ++c) {
+            if (8 * (t + c * TPR) < K) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[c][i]));
+            }
+        }
+    }
+    amax = warp_max_u32(amax);
+    if constexpr (TPR > 32) {
+        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
+        __syncthreads();
+        amax = warp_max_u32((threadIdx.x & 31) < TPR / 32 ? red[threadIdx.x & 31] : 0u);
+    }
+    const float s = s8_scale(amax, kRowScaleFloor), r = s8_inverse(s);
+    if (t == 0) S[row] = s;
+    if constexpr (LONG) {
+        for (int k = 8 * t; k < ldq; k += 8 * TPR) {
+            load_some<T, 8>(x + k, K - k, aligned, v[0]);
+            store_codes(q + k, v[0], r);
+        }
+    } else {
+#pragma unroll
+        for (int c = 0; c < kQuantChunks; ++c) {
+            const int k = 8 * (t + c * TPR);
+            if (k >= ldq) break;
+            if (k >= K) {  // the row's padding: one piece of 8 at most
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[c][i] = 0.f;
+            }
+            store_codes(q + k, v[c], r);
+        }
+    }
+}
+
+template <class T, class OUT>
+static int launch_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, OUT* Q, float* S, cudaStream_t s) {
+    const bool aligned = aligned16(X) && (M == 1 || ldx * sizeof(T) % 16 == 0);
+    const int m = static_cast<int>(M), k = static_cast<int>(K), ldq = static_cast<int>(s8_codes_ld(K));
+    const unsigned rows = static_cast<unsigned>(M);
+    if (ldq <= 32 * 8 * kQuantChunks)
+        return launch_serialized(k_s8_quantize<T, OUT, 32, false>, dim3((rows + 3) / 4), 128, 0, 1, s, m, k, X, ldx,
+                                 aligned, Q, ldq, S);
+    if (ldq <= 128 * 8 * kQuantChunks)
+        return launch_serialized(k_s8_quantize<T, OUT, 128, false>, dim3(rows), 128, 0, 1, s, m, k, X, ldx, aligned, Q,
+                                 ldq, S);
+    if (ldq <= 512 * 8 * kQuantChunks)
+        return launch_serialized(k_s8_quantize<T, OUT, 512, false>, dim3(rows), 512, 0, 1, s, m, k, X, ldx, aligned, Q,
+                                 ldq, S);
+    return launch_serialized(k_s8_quantize<T, OUT, 512, true>, dim3(rows), 512, 0, 1, s, m, k, X, ldx, aligned, Q, ldq,
+                             S);
+}
+
+// ------------------------------------------------------------ few tokens
+
+// Up to 16 tokens: the weights' rows are the rows of the MMA and the tokens its
+// columns.  A CTA takes 16 weight rows, its 16 warps every 16th block of 64 values
+// along K; a thread's bytes of a row (16 at a time) are the values of four MMA steps,
+// since a sum does not depend on the order of k.  Sums of a few blocks are exact in
+// fp32; they are added up in 32-bit integers, over the warps as well.  The tokens
+// are quantized by every CTA for itself into shared memory (QUANT), which costs less
+// than a kernel ahead of this one.
+constexpr int kGemvWarps = 16, kGemvThreads = 32 * kGemvWarps;
+constexpr int kGemvBatch = 4;            // blocks of 64 values in flight a thread
+constexpr int kGemvTokens = 16;
+constexpr size_t kGemvSmem = 110 * 1024;  // two CTAs an SM
+
+__host__ __device__ inline int64_t gemv_token_stride(int64_t K) { return (K + 63) / 64 * 64 + 16; }
+static bool gemv_fits(int64_t M, int64_t K) {
+    return M <= kGemvTokens && static_cast<size_t>(M * gemv_token_stride(K)) <= kGemvSmem;
+}
+
+struct GemvParams {
+    int M, N, K, ldq;
+    const void* X;        // QUANT: values, else int8 codes (rows of ldq)
+    int64_t ldx;
+    bool x_aligned;
+    const float* sa;      // scales of given codes
+    const int8_t* W;
+    const float* sb;
+    const void* bias;
+    void* Y;
+    int64_t ldy;
+};
+
+// The first n bytes of 16, the others 0.
+__device__ __forceinline__ uint4 first_bytes(uint4 w, int n) {
+    auto keep = [&](uint32_t v, int at) {
+        const int have = n - at;
+        return have >= 4 ? v : have <= 0 ? 0u : v & ((1u << (8 * have)) - 1u);
+    };
+    return make_uint4(keep(w.x, 0), keep(w.y, 4), keep(w.z, 8), keep(w.w, 12));
+}
+
+template <class T, int MB, bool QUANT>
+__global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p) {
+    extern __shared__ __align__(16) uint8_t codes[];
+    __shared__ uint32_t red_max[kGemvTokens][kGemvWarps];
+    __shared__ float token_scale[kGemvTokens];
+    __shared__ int sums[kGemvWarps][MB * 4][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int n0 = blockIdx.x * 16;
+    const int blocks = (p.ldq + 63) / 64;
+    const int stride = static_cast<int>(gemv_token_stride(p.ldq));
+    const bool has0 = n0 + g < p.N, has1 = n0 + g + 8 < p.N;
+    const int8_t* const w0 = p.W + static_cast<int64_t>(n0 + g) * p.ldq + 16 * t;
+    const int8_t* const w1 = w0 + 8 * static_cast<int64_t>(p.ldq);
+
+    // The weights may still be written by the kernel ahead, so they are read after the
+    // wait; a prefetch only moves lines to the L2, where that kernel's stores go too.
+    for (int b = warp; b < blocks; b += kGemvWarps) {
+        const int k = 64 * b + 16 * t;
+        if (k < p.ldq) {
+            if (has0) asm volatile("prefetch.global.L2 [%0];" ::"l"(w0 + 64 * b));
+            if (has1) asm volatile("prefetch.global.L2 [%0];" ::"l"(w1 + 64 * b));
+        }
+    }
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+
+    uint4 a[kGemvBatch][2];
+    auto load = [&](int b0) {
+#pragma unroll
+        for (int j = 0; j < kGemvBatch; ++j) {
+            const int b = b0 + j * kGemvWarps;
+            const bool in = b < blocks && 64 * b + 16 * t < p.ldq;
+            a[j][0] = a[j][1] = make_uint4(0, 0, 0, 0);
+            if (in && has0) a[j][0] = *reinterpret_cast<const uint4*>(w0 + 64 * static_cast<int64_t>(b));
+            if (in && has1) a[j][1] = *reinterpret_cast<const uint4*>(w1 + 64 * static_cast<int64_t>(b));
+        }
+    };
+    load(warp);
+
+    if constexpr (QUANT) {
+        for (int m = 0; m < p.M; ++m) {
+            const T* x = static_cast<const T*>(p.X) + m * p.ldx;
+            uint32_t amax = 0;
+            for (int k = 8 * threadIdx.x; k < p.K; k += 8 * kGemvThreads) {
+                float v[8];
+                load_some<T, 8>(x + k, p.K - k, p.x_aligned, v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[i]));
+            }
+            amax = warp_max_u32(amax);
+            if (lane == 0) red_max[m][warp] = amax;
+        }
+        __syncthreads();
+        for (int m = 0; m < p.M; ++m) {
+            const T* x = static_cast<const T*>(p.X) + m * p.ldx;
+            const uint32_t amax = warp_max_u32(red_max[m][lane & (kGemvWarps - 1)]);
+            const float s = s8_scale(amax, kRowScaleFloor), r = s8_inverse(s);
+            if (threadIdx.x == 0) token_scale[m] = s;
+            for (int k = 8 * threadIdx.x; k < 64 * blocks; k += 8 * kGemvThreads) {
+                float v[8];
+                load_some<T, 8>(x + k, p.K - k, p.x_aligned, v);
+                store_codes(reinterpret_cast<int8_t*>(codes) + m * stride + k, v, r);
+            }
+        }
+    } else {
+        for (int m = 0; m < p.M; ++m) {
+            const int8_t* x = static_cast<const int8_t*>(p.X) + static_cast<int64_t>(m) * p.ldq;
+            for (int k = 16 * threadIdx.x; k < 64 * blocks; k += 16 * kGemvThreads) {
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (k < p.ldq) w = *reinterpret_cast<const uint4*>(x + k);
+                if (k + 16 > p.K) w = first_bytes(w, p.K - k);  // what lies behind K does not count
+                *reinterpret_cast<uint4*>(codes + m * stride + k) = w;
+            }
+        }
+        if (threadIdx.x < p.M) token_scale[threadIdx.x] = p.sa[threadIdx.x];
+    }
+    __syncthreads();
+
+    int total[MB][4];
+#pragma unroll
+    for (int i = 0; i < MB * 4; ++i) total[i / 4][i % 4] = 0;
+    for (int b0 = warp; b0 < blocks; b0 += kGemvBatch * kGemvWarps) {
+        if (b0 != warp) load(b0);
+        float acc[MB][4];
+#pragma unroll
+        for (int i = 0; i < MB * 4; ++i) acc[i / 4][i % 4] = 0.f;
+#pragma unroll
+        for (int j = 0; j < kGemvBatch; ++j) {
+            const int b = b0 + j * kGemvWarps;
+            if (b >= blocks) break;
+            uint4 x[MB];
+#pragma unroll
+            for (int i = 0; i < MB; ++i)
+                x[i] = g + 8 * i < p.M ? *reinterpret_cast<const uint4*>(codes + (g + 8 * i) * stride + 64 * b + 16 * t)
+                                       : make_uint4(0, 0, 0, 0);
+            const uint32_t r0[4] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w};
+            const uint32_t r1[4] = {a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t a0, a1, a2, a3;
+                s8_to_f16(r0[c], a0, a2);
+                s8_to_f16(r1[c], a1, a3);
+#pragma unroll
+                for (int i = 0; i < MB; ++i) {
+                    const uint32_t xw = c == 0 ? x[i].x : c == 1 ? x[i].y : c == 2 ? x[i].z : x[i].w;
+                    uint32_t b0h, b1h;
+                    s8_to_f16(xw, b0h, b1h);
+                    mma_f16(acc[i], a0, a1, a2, a3, b0h, b1h);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MB * 4; ++i) total[i / 4][i % 4] += __float2int_rn(acc[i / 4][i % 4]);
+    }
+#pragma unroll
+    for (int i = 0; i < MB * 4; ++i) sums[warp][i][lane] = total[i / 4][i % 4];
+    __syncthreads();
+    // accumulator element (tile i, value v) of lane 4 g + t: weight row g + 8 (v / 2), token 8 i + 2 t + v % 2
+    if (threadIdx.x < 128 * MB) {
+        const int e = threadIdx.x >> 5, row = g + 8 * ((e & 3) >> 1), m = 8 * (e >> 2) + 2 * t + (e & 1);
+        int sum = 0;
+#pragma unroll
+        for (int w = 0; w < kGemvWarps; ++w) sum += sums[w][e][lane];
+        const int n = n0 + row;
+        if (m < p.M && n < p.N) {
+            const float b = p.bias ? to_f32<T>(static_cast<const T*>(p.bias)[n]) : 0.f;
+            static_cast<T*>(p.Y)[m * p.ldy + n] =
+                from_f32<T>(fmaf(static_cast<float>(sum) * token_scale[m], p.sb[n], b));
+        }
+    }
+}
+
+template <class T, bool QUANT>
+static int launch_gemv(const GemvParams& p, cudaStream_t s) {
+    const size_t smem = static_cast<size_t>(p.M * gemv_token_stride(p.ldq));
+    const dim3 grid(static_cast<unsigned>((p.N + 15) / 16));
+    struct Few;
+    struct More;
+    if (p.M <= 8) {
+        const int rc = raise_smem<Few>(k_s8_gemv<T, 1, QUANT>);
+        return rc ? rc : launch_serialized(k_s8_gemv<T, 1, QUANT>, grid, kGemvThreads, smem, 1, s, p);
+    }
+    const int rc = raise_smem<More>(k_s8_gemv<T, 2, QUANT>);
+    return rc ? rc : launch_serialized(k_s8_gemv<T, 2, QUANT>, grid, kGemvThreads, smem, 1, s, p);
+}
+
+// ------------------------------------------------------------ workspaces and calls
+
+static size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+// fp16 forms of both operands, and the tokens' scales.
+struct S8Workspace {
+    size_t a, b, sa, total;
+};
+static S8Workspace s8_workspace(int64_t M, int64_t N, int64_t K) {
+    const size_t ld = static_cast<size_t>(s8_codes_ld(K));
+    S8Workspace w;
+    w.a = 0;
+    w.b = up256(2 * ld * static_cast<size_t>(M));
+    w.sa = w.b + up256(2 * ld * static_cast<size_t>(N));
+    w.total = w.sa + up256(4 * static_cast<size_t>(M));
+    return w;
+}
+size_t s8_linear_workspace(int64_t M, int64_t N, int64_t K) {
+    return gemv_fits(M, K) ? 0 : s8_workspace(M, N, K).total;
+}
+
+constexpr int64_t kMaxRows = int64_t(1) << 27, kMaxK = 131072;
+
+static int check_s8(int dtype, int64_t M, int64_t N, int64_t K) {
+    if (!dtype_ok(dtype)) return QG_ERR_UNSUPPORTED;
+    if (M < 0 || N < 0 || K < 0 || M > kMaxRows || N > kMaxRows || K >= kMaxK) return QG_ERR_INVALID_ARG;
+    return QG_OK;
+}
+
+static int check_out(int dtype, int64_t N, const float* sb, const void* bias, const void* Y, int64_t ldy, int64_t M) {
+    if (!Y || (M > 1 && ldy < N)) return QG_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(Y) % dtype_bytes(dtype) || reinterpret_cast<uintptr_t>(bias) % dtype_bytes(dtype) ||
+        reinterpret_cast<uintptr_t>(sb) % 4)
+        return QG_ERR_MISALIGNED;
+    return QG_OK;
+}
+
+static int check_workspace(const void* ws, size_t bytes, size_t want) {
+    if (want == 0) return QG_OK;
+    if (!ws || bytes < want) return QG_ERR_WORKSPACE;
+    return reinterpret_cast<uintptr_t>(ws) % 256 ? QG_ERR_MISALIGNED : QG_OK;
+}
+
+__global__ void __launch_bounds__(256) k_s8_only_bias(int64_t M, int64_t N, const void* bias, void* Y, int64_t ldy,
+                                                      int dtype) {
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    for (int64_t i = blockIdx.x * 256 + threadIdx.x; i < M * N; i += gridDim.x * int64_t(256)) {
+        const int64_t m = i / N, n = i % N;
+        if (dtype == QG_F32)
+            static_cast<float*>(Y)[m * ldy + n] = bias ? static_cast<const float*>(bias)[n] : 0.f;
+        else  // 16-bit types: 0 has the same bits in both
+            static_cast<uint16_t*>(Y)[m * ldy + n] = bias ? static_cast<const uint16_t*>(bias)[n] : uint16_t(0);
+    }
+}
+
+static int only_bias(int dtype, int64_t M, int64_t N, const void* bias, void* Y, int64_t ldy, cudaStream_t s) {
+    return launch_serialized(k_s8_only_bias, dim3(static_cast<unsigned>(conv_grid(current_device(), M * N))), 256, 0, 1,
+                             s, M, N, bias, Y, ldy, dtype);
+}
+
+// Sums of fp16 operands, scaled: the exact chunked GEMM of qgemm_s8 with another epilogue.
+static int tensor_product(int dtype, int64_t M, int64_t N, int64_t K, const __half* A, const float* sa, const __half* B,
+                          const float* sb, const void* bias, void* Y, int64_t ldy, const Ctl& ctl, cudaStream_t s) {
+    S8Scales e;
+    e.sa = sa;
+    e.sb = sb;
+    e.bias = bias;
+    e.dtype = dtype;
+    return run_gemm_s8_scaled(A, B, M, N, K, s8_codes_ld(K), Y, ldy, e, ctl, s);
+}
+
+#define QG_S8_QUANT(T, NAME, OUT, ONAME, TPR, LONG)                                                  \
+    QG_BLOCK_KERNEL_BUDGET("k_s8_quantize<" NAME "," ONAME "," #TPR "," #LONG ">",                   \
+                           (reinterpret_cast<const void*>(k_s8_quantize<T, OUT, TPR, LONG>)),        \
+                           TPR < 128 ? 128 : TPR, 0, 0, 1, 1)
+#define QG_S8_QUANT_SIZES(T, NAME, OUT, ONAME)  \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 32, false);  \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 128, false); \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 512, false); \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 512, true)
+#define QG_S8_GEMV(T, NAME, MB, QUANT)                                                            \
+    QG_BLOCK_KERNEL_BUDGET("k_s8_gemv<" NAME "," #MB "," #QUANT ">",                              \
+                           (reinterpret_cast<const void*>(k_s8_gemv<T, MB, QUANT>)), kGemvThreads, \
+                           static_cast<int>(kGemvSmem) - MB * 8192 - 2048, 0, 1, 2)
+#define QG_S8_BUDGETS(T, NAME)                    \
+    QG_S8_QUANT_SIZES(T, NAME, int8_t, "s8");     \
+    QG_S8_QUANT_SIZES(T, NAME, __half, "codes");  \
+    QG_S8_GEMV(T, NAME, 1, true);                 \
+    QG_S8_GEMV(T, NAME, 2, true);                 \
+    QG_S8_GEMV(T, NAME, 1, false);                \
+    QG_S8_GEMV(T, NAME, 2, false)
+QG_S8_BUDGETS(__half, "f16");
+QG_S8_BUDGETS(__nv_bfloat16, "bf16");
+QG_S8_BUDGETS(float, "f32");
+
+}  // namespace qg
+
+using namespace qg;
+
+extern "C" {
+
+int64_t qg_s8_codes_ld(int64_t K) { return K > 0 ? s8_codes_ld(K) : 0; }
+
+int s8_quantize(int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, int8_t* Q, float* S, void* stream) {
+    const NvtxRange nvtx_range("s8_quantize");
+    int rc = check_s8(dtype, M, 0, K);
+    if (rc) return rc;
+    if (M == 0 || K == 0) return QG_OK;
+    if (!X || !Q || !S || (M > 1 && ldx < K)) return QG_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(X) % dtype_bytes(dtype) || !aligned16(Q) || reinterpret_cast<uintptr_t>(S) % 4)
+        return QG_ERR_MISALIGNED;
+    if (current_device() < 0) return QG_ERR_CUDA;
+    return by_dtype(dtype, [&](auto t) {
+        return launch_quantize<decltype(t), int8_t>(M, K, X, ldx, Q, S, static_cast<cudaStream_t>(stream));
+    });
+}
+
+int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const float* As, const int8_t* Bq,
+            const float* Bs, const void* bias, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    const NvtxRange nvtx_range("s8_gemm");
+    int rc = check_s8(dtype, M, N, K);
+    if (rc) return rc;
+    if (M == 0 || N == 0) return QG_OK;
+    if (K > 0 && (!Aq || !As || !Bq || !Bs)) return QG_ERR_INVALID_ARG;
+    rc = check_out(dtype, N, Bs, bias, Y, ldy, M);
+    if (rc) return rc;
+    if (!aligned16(Aq) || !aligned16(Bq) || reinterpret_cast<uintptr_t>(As) % 4) return QG_ERR_MISALIGNED;
+    if (K > 0) rc = check_workspace(ws, ws_bytes, s8_linear_workspace(M, N, K));
+    if (rc) return rc;
+    const int dev = current_device();
+    if (dev < 0) return QG_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) return only_bias(dtype, M, N, bias, Y, ldy, s);
+    const int64_t ld = s8_codes_ld(K);
+    if (gemv_fits(M, K)) {
+        GemvParams p = {};
+        p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K); p.ldq = static_cast<int>(ld);
+        p.X = Aq; p.sa = As; p.W = Bq; p.sb = Bs; p.bias = bias; p.Y = Y; p.ldy = ldy;
+        return by_dtype(dtype, [&](auto t) { return launch_gemv<decltype(t), false>(p, s); });
+    }
+    const Ctl ctl = host_ctl(dev);
+    if (!ctl.status) return QG_ERR_CUDA;
+    const S8Workspace w = s8_workspace(M, N, K);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    __half *a = reinterpret_cast<__half*>(base + w.a), *b = reinterpret_cast<__half*>(base + w.b);
+    rc = s8_to_f16_rows(Aq, M, ld, a, ld, dev, s);
+    if (!rc) rc = s8_to_f16_rows(Bq, N, ld, b, ld, dev, s);
+    return rc ? rc : tensor_product(dtype, M, N, K, a, As, b, Bs, bias, Y, ldy, ctl, s);
+}
+
+int s8_linear(int dtype, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx, const int8_t* Wq,
+              const float* Ws, const void* bias, void* Y, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+    const NvtxRange nvtx_range("s8_linear");
+    int rc = check_s8(dtype, M, N, K);
+    if (rc) return rc;
+    if (M == 0 || N == 0) return QG_OK;
+    if (K > 0 && (!X || !Wq || !Ws || (M > 1 && ldx < K))) return QG_ERR_INVALID_ARG;
+    rc = check_out(dtype, N, Ws, bias, Y, ldy, M);
+    if (rc) return rc;
+    if (!aligned16(Wq) || reinterpret_cast<uintptr_t>(X) % dtype_bytes(dtype)) return QG_ERR_MISALIGNED;
+    if (K > 0) rc = check_workspace(ws, ws_bytes, s8_linear_workspace(M, N, K));
+    if (rc) return rc;
+    const int dev = current_device();
+    if (dev < 0) return QG_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (K == 0) return only_bias(dtype, M, N, bias, Y, ldy, s);
+    const int64_t ld = s8_codes_ld(K);
+    if (gemv_fits(M, K)) {
+        GemvParams p = {};
+        p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K); p.ldq = static_cast<int>(ld);
+        p.X = X; p.ldx = ldx; p.x_aligned = aligned16(X) && (M == 1 || ldx * dtype_bytes(dtype) % 16 == 0);
+        p.W = Wq; p.sb = Ws; p.bias = bias; p.Y = Y; p.ldy = ldy;
+        return by_dtype(dtype, [&](auto t) { return launch_gemv<decltype(t), true>(p, s); });
+    }
+    const Ctl ctl = host_ctl(dev);
+    if (!ctl.status) return QG_ERR_CUDA;
+    const S8Workspace w = s8_workspace(M, N, K);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    __half *a = reinterpret_cast<__half*>(base + w.a), *b = reinterpret_cast<__half*>(base + w.b);
+    float* sa = reinterpret_cast<float*>(base + w.sa);
+    rc = by_dtype(dtype, [&](auto t) { return launch_quantize<decltype(t), __half>(M, K, X, ldx, a, sa, s); });
+    if (!rc) rc = s8_to_f16_rows(Wq, N, ld, b, ld, dev, s);
+    return rc ? rc : tensor_product(dtype, M, N, K, a, sa, b, Ws, bias, Y, ldy, ctl, s);
+}
+
+}  // extern "C"

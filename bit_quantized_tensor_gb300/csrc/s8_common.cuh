@@ -1,0 +1,62 @@
+// 8-bit integer operands with a scale for each row: the row of a matrix of
+// activations is a token, that of a weight matrix an output channel.
+//   s = max(fl(amax / 127), 2^-100),  r = fl(1 / s),  q = clamp(rint(fl(x r)), -127, 127)
+// A row that holds an infinity or a NaN has the scale NaN and codes 0.
+// Codes: rows x s8_codes_ld(K) bytes (K up to whole 16 bytes), 0 behind K.
+#pragma once
+#include <cuda_fp16.h>
+
+#include "fp4_common.cuh"
+#include "qg_ptx.cuh"
+
+namespace qg {
+
+constexpr float kRowScaleFloor = 0x1p-100f;
+
+__host__ __device__ inline int64_t s8_codes_ld(int64_t K) { return (K + 15) / 16 * 16; }
+
+// |x| as bits: unsigned numbers that order like the magnitudes, infinity and NaN above all.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ bool bits_finite(uint32_t amax_bits) { return amax_bits < 0x7f800000u; }
+
+// Scale of values whose largest magnitude is `amax_bits`, at least `least`.
+__device__ __forceinline__ float s8_scale(uint32_t amax_bits, float least) {
+    return bits_finite(amax_bits) ? fmaxf(__fdiv_rn(__uint_as_float(amax_bits), 127.f), least)
+                                  : __uint_as_float(0x7fc00000u);
+}
+// r; 0 for a scale that is NaN, so that every code is 0 (x r is NaN for a NaN, code 0 as well).
+__device__ __forceinline__ float s8_inverse(float scale) { return scale == scale ? __fdiv_rn(1.f, scale) : 0.f; }
+__device__ __forceinline__ int s8_code(float x, float r) {
+    return max(-127, min(127, __float2int_rn(__fmul_rn(x, r))));
+}
+
+// Four codes in a word, the first in the low byte.
+__device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// The four codes of a word as fp16 pairs, exact: the byte XOR 0x80 (offset binary)
+// under the exponent of 1024 is 1024 + q + 128, and 1152 less is q.
+__device__ __forceinline__ void s8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const __half2 c1152 = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    w ^= 0x80808080u;
+    const uint32_t l = __byte_perm(w, 0x64646464u, 0x4140), h = __byte_perm(w, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&l), c1152);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&h), c1152);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+}
+
+__device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
+// D += A . B of 16 x 16 by 16 x 8 fp16 values.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+}  // namespace qg

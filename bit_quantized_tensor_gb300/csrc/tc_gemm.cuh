@@ -23,15 +23,19 @@
 //             stay within 2^24 in magnitude (so every partial sum is an exactly
 //             representable integer); each chunk is converted to int32 and
 //             added in registers; the int32 tile is stored at the end.
+//   Epi::S8   the same sums, stored as sum * sa[row] * sb[column] + bias[column]
+//             in fp16, bf16 or fp32.
 #pragma once
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "qg_gemm_host.h"
 #include "qg_ptx.cuh"
 
 namespace qg {
 
-enum class Epi { F16, S32 };
+enum class Epi { F16, S32, S8 };
 
 // Call-site tags recorded with QG_ERR_TIMEOUT.
 enum WaitSite : int {
@@ -94,6 +98,7 @@ struct TcGemmParams {
     const __half* bias;  // optional per-column bias (F16 epilogue), may be null
     Ctl ctl;
     int l2_mode;    // L2 policy of the operand loads and output stores (qg_set_l2_policy)
+    S8Scales s8;    // Epi::S8
 };
 
 // L2 policies of one GEMM launch.  Mode 0: every TMA load evict-normal.
@@ -222,6 +227,67 @@ __device__ __forceinline__ void store_row_s32(int32_t* dst, int col0, int N_tota
                     if (col0 + c + h + i < N_total) dst[c + h + i] = v[c + h + i];
             }
         }
+    }
+}
+
+// N columns (a multiple of 16) of a row of integer sums, scaled, in the output's type.
+template <class T, int N>
+__device__ __forceinline__ void store_row_s8(T* dst, int col0, int N_total, const int32_t* v, float sa,
+                                             const S8Scales& e) {
+    constexpr int PER = 32 / static_cast<int>(sizeof(T));  // values of a 32-byte sector
+    const T* bias = static_cast<const T*>(e.bias);
+    auto widen = [](T x) {
+        if constexpr (sizeof(T) == 4)
+            return x;
+        else
+            return static_cast<float>(x);
+    };
+#pragma unroll
+    for (int c = 0; c < N; c += PER) {
+        if (col0 + c >= N_total) return;
+        float f[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int col = col0 + c + i;
+            f[i] = 0.f;
+            if (col < N_total)
+                f[i] = fmaf(static_cast<float>(v[c + i]) * sa, e.sb[col], bias ? widen(bias[col]) : 0.f);
+        }
+        if (col0 + c + PER <= N_total && (reinterpret_cast<uintptr_t>(dst + c) & 31u) == 0) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if constexpr (sizeof(T) == 4) {
+                    w[i] = __float_as_uint(f[i]);
+                } else {
+                    const T a = static_cast<T>(f[2 * i]), b = static_cast<T>(f[2 * i + 1]);
+                    w[i] = *reinterpret_cast<const uint16_t*>(&a) |
+                           static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&b)) << 16;
+                }
+            }
+            st_global_32(dst + c, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), false);
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                if (col0 + c + i < N_total) dst[c + i] = static_cast<T>(f[i]);
+        }
+    }
+}
+
+// A row of sums of either integer epilogue.
+template <Epi EPI, int N>
+__device__ __forceinline__ void store_row_sums(const TcGemmParams& p, int row, int col0, const int32_t* v) {
+    const int64_t at = static_cast<int64_t>(row) * p.ldc + col0;
+    if constexpr (EPI == Epi::S32) {
+        store_row_s32<N>(static_cast<int32_t*>(p.C) + at, col0, p.N, v, p.l2_mode == 2);
+    } else {
+        const float sa = p.s8.sa[row];
+        if (p.s8.dtype == QG_F16)
+            store_row_s8<__half, N>(static_cast<__half*>(p.C) + at, col0, p.N, v, sa, p.s8);
+        else if (p.s8.dtype == QG_BF16)
+            store_row_s8<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(p.C) + at, col0, p.N, v, sa, p.s8);
+        else
+            store_row_s8<float, N>(static_cast<float*>(p.C) + at, col0, p.N, v, sa, p.s8);
     }
 }
 
@@ -366,7 +432,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
             tile_coords(t, num_m, num_n, mb, nb);
             const int row = mb * Cfg::BM + quad * 32 + lane;
             const int col0 = nb * Cfg::BN + colhalf * 128;
-            if constexpr (Cfg::EPI == Epi::S32) {
+            if constexpr (Cfg::EPI != Epi::F16) {
                 int32_t sum[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) sum[i] = 0;
@@ -395,10 +461,7 @@ __global__ void __launch_bounds__(Cfg::THREADS, 1)
                     as.next();
                 }
                 if (!ok) break;
-                if (row < p.M)
-                    store_row_s32<128>(static_cast<int32_t*>(p.C) + static_cast<int64_t>(row) * p.ldc +
-                                           col0,
-                                       col0, p.N, sum, p.l2_mode == 2);
+                if (row < p.M) store_row_sums<Cfg::EPI, 128>(p, row, col0, sum);
             } else {
                 bool got = bounded_wait(accf_bar(as.slot()), as.parity(), abort_flag, p.ctl,
                                         kSiteEpiAccFull);

@@ -224,7 +224,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
             tile_coords(t, num_m, num_n, mb, nb, kGroupMPairs);
             const int row = mb * 2 * Cfg::BM + static_cast<int>(rank) * Cfg::BM + quad * 32 + lane;
             const int col0 = nb * Cfg::BN + colhalf * 128;
-            if constexpr (Cfg::EPI == Epi::S32) {
+            if constexpr (Cfg::EPI != Epi::F16) {
                 int32_t sum[128];
 #pragma unroll
                 for (int i = 0; i < 128; ++i) sum[i] = 0;
@@ -255,10 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Cfg::THREADS, 1)
                     as.next();
                 }
                 if (!ok) break;
-                if (row < p.M)
-                    store_row_s32<128>(static_cast<int32_t*>(p.C) + static_cast<int64_t>(row) * p.ldc +
-                                           col0,
-                                       col0, p.N, sum, p.l2_mode == 2);
+                if (row < p.M) store_row_sums<Cfg::EPI, 128>(p, row, col0, sum);
             } else {
                 bool got = bounded_wait(accf_bar(as.slot()), as.parity(), abort_flag, p.ctl,
                                         kSitePairEpiAcc);

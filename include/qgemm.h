@@ -70,7 +70,10 @@ typedef enum {
     QG_OP_FP4_LINEAR = 8,           /* workspace of fp4_linear (either format) */
     QG_OP_FP4_LINEAR_BACKWARD = 9,  /* workspace of fp4_linear_backward (either format) */
     QG_OP_LAYER_NORM_BACKWARD = 10, /* workspace of layer_norm_backward (K = row length; M, N unused: pass 1) */
-    QG_OP_FP4_TENSOR_SCALE = 11     /* workspace of fp4_tensor_scale (sizes unused: pass 1) */
+    QG_OP_FP4_TENSOR_SCALE = 11,    /* workspace of fp4_tensor_scale (sizes unused: pass 1) */
+    QG_OP_S8_LINEAR = 12,           /* workspace of s8_linear and s8_gemm */
+    QG_OP_QK_NORM_ROPE_BACKWARD = 13, /* workspace of qk_norm_rope_backward (K = head size; M, N unused: pass 1) */
+    QG_OP_KV8_ATTENTION = 14        /* workspace of kv8_attention (M = rows of q, N = query heads, K = head size) */
 } qg_op;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -554,6 +557,124 @@ int layer_norm_backward(int dtype, int64_t M, int64_t D, const void *dY, int64_t
                         const void *X, int64_t ldx, const void *gamma, int wdtype,
                         const float *mean, const float *rstd, void *dX, int64_t lddx,
                         float *dgamma, float *dbeta, void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit integer operands with a scale for each row, and the linear layer on
+ * them.  A row is a token (activations) or an output channel (weights):
+ *   s = max(fl(amax / 127), 2^-100),  r = fl(1 / s),
+ *   q = clamp(rint(fl(x r)), -127, 127)      (fl: rounded to fp32)
+ * A row with an infinity or a NaN has the scale NaN and codes 0.
+ * Operand of a rows x K matrix: rows x qg_s8_codes_ld(K) bytes (K up to whole
+ * 16 bytes; s8_quantize writes 0 behind K, the products ignore what is there)
+ * and `rows` fp32 scales.
+ * Matrices of floating type, sizes of 0, streams, graphs and overlap: as for the
+ * microscaled operators above.  M, N at most 2^27, K below 131072. */
+
+/* Bytes of a row of K codes; 0 for K <= 0. */
+int64_t qg_s8_codes_ld(int64_t K);
+
+/* X (M x K) to codes Q and scales S (M). */
+int s8_quantize(int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, int8_t* Q, float* S,
+                void* stream);
+
+/* Y (M x N, `dtype`) = As[m] Bs[n] sum_k Aq[m][k] Bq[n][k] + bias[n]: the integer
+ * sum is exact, then rounded to fp32, multiplied by As and in one fused step by Bs
+ * with the bias added, and rounded to `dtype`.  bias: N values of `dtype` or NULL.
+ *  ws: qg_workspace_size(QG_OP_S8_LINEAR, M, N, K) bytes, 256-byte aligned; 0 bytes
+ *      (ws may be NULL) for a few tokens. */
+int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const float* As,
+            const int8_t* Bq, const float* Bs, const void* bias, void* Y, int64_t ldy, void* ws,
+            size_t ws_bytes, void* stream);
+
+/* Y = Q(X) . W^T + bias: s8_quantize of X (M x K, `dtype`) and s8_gemm with the
+ * operand (Wq, Ws) of the weights (N x K) in one call.  Workspace as s8_gemm. */
+int s8_linear(int dtype, int64_t M, int64_t N, int64_t K, const void* X, int64_t ldx,
+              const int8_t* Wq, const float* Ws, const void* bias, void* Y, int64_t ldy, void* ws,
+              size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Norm of queries and keys for each head, with the rotation by position.
+ *   rstd = 1 / sqrt(sum(x^2) / D + eps),  z = x rstd g
+ *   y_a = z_a cos - z_b sin,  y_b = z_b cos + z_a sin   for the R / 2 pairs (a, b)
+ *   y = z for the other D - R values
+ * Pair i is (i, R / 2 + i) (QG_ROPE_HALF) or (2 i, 2 i + 1) (QG_ROPE_PAIRS).  Its
+ * cos is table[pos][i] and its sin table[pos][R / 2 + i]; table: table_rows x R fp32,
+ * contiguous, pos = positions[t] (positions NULL: t).  A position outside the table
+ * makes the rotated values of its token NaN.
+ *  Q, K, Yq, Yk : T rows of Hq (Hk) heads of D values, heads one after another, rows
+ *                 ld apart: a view of a packed product's rows is one.  Hk may be 0.
+ *  gq, gk       : D values of wdtype (that of Q, or QG_F32), NULL = 1
+ *  rq, rk       : T x Hq (T x Hk) fp32, contiguous, or NULL
+ *  D <= 1024, R even, 0 <= R <= D.  Yq may be Q and Yk K (in place). */
+typedef enum { QG_ROPE_HALF = 0, QG_ROPE_PAIRS = 1 } qg_rope_style;
+int qk_norm_rope(int dtype, int style, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R,
+                 const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* gq,
+                 const void* gk, int wdtype, const int32_t* positions, const float* table,
+                 int64_t table_rows, float eps, void* Yq, int64_t ldyq, void* Yk, int64_t ldyk,
+                 float* rq, float* rk, void* stream);
+
+/* Its gradients, with rq and rk as it wrote them and Q, K as it read them:
+ *   dz = the rotation by the negative angle of dy, xh = x rstd, e = dz g
+ *   dx = rstd (e - xh sum(e xh) / D)          (type of Q; dQ may be dYq, dK dYk)
+ *   dg = sum over tokens and heads of dz xh   (D fp32 each; 0 for T = 0)
+ *  ws: qg_workspace_size(QG_OP_QK_NORM_ROPE_BACKWARD, 1, 1, D) bytes. */
+int qk_norm_rope_backward(int dtype, int style, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
+                          int64_t R, const void* dYq, int64_t lddyq, const void* dYk,
+                          int64_t lddyk, const void* Q, int64_t ldq, const void* K, int64_t ldk,
+                          const void* gq, const void* gk, int wdtype, const int32_t* positions,
+                          const float* table, int64_t table_rows, const float* rq,
+                          const float* rk, void* dQ, int64_t lddq, void* dK, int64_t lddk,
+                          float* dgq, float* dgk, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged cache of keys and values in 8-bit codes.
+ *  kq, vq  : pages x heads x page x D codes, contiguous, 16-byte aligned
+ *  ks, vs  : pages x heads fp32 scales
+ *  table   : B x table_cols page numbers; token j of sequence b is token j % page of
+ *            page table[b][j / page]
+ *  starts  : B + 1 row numbers; sequence b has rows starts[b] .. starts[b + 1] of the
+ *            tensors with one row a token
+ *  lengths : B; tokens of the sequence, of which its rows are the last ones
+ * page: 16, 32, 64 or 128; D: 64, 128 or 256; heads at most 1024.
+ * A page's scale is s = max(fl(amax / 127), 2^-64) over its tokens for one head, its
+ * codes clamp(rint(fl(x fl(1 / s))), -127, 127); NaN, and codes 0, once a value is not
+ * finite.  starts, lengths and table are device memory that is read when the work
+ * runs.  What they say wrongly does no harm: rows that are not within [0, rows) or run
+ * backwards are skipped, rows of tokens ahead of a sequence's first too (append) or
+ * read as NaN (gather), and a page number outside [0, pages) or a token behind the
+ * table's last column is not written and reads as NaN.  Rows of no sequence (behind
+ * starts[B]) are neither read nor written. */
+
+/* New tokens into the cache: rows of K and V (heads x D values of `dtype`, rows ldk,
+ * ldv apart).  lengths counts the new tokens.  A page with older tokens of the
+ * sequence takes the larger of its scale and its new values' scale; if that grew, the
+ * older codes become rint(fl(q fl(old / new))).  A page whose first token is written
+ * starts afresh.  A page that is written belongs to one sequence of the call. */
+int kv8_append(int dtype, int64_t B, int64_t rows, int64_t heads, int64_t D, const void* K,
+               int64_t ldk, const void* V, int64_t ldv, int8_t* kq, int8_t* vq, float* ks,
+               float* vs, int64_t pages, int64_t page, const int32_t* table, int64_t table_cols,
+               const int32_t* starts, const int32_t* lengths, void* stream);
+
+/* The last starts[b + 1] - starts[b] tokens of every sequence as values, fl(q s)
+ * rounded to `dtype`. */
+int kv8_gather(int dtype, int64_t B, int64_t rows, int64_t heads, int64_t D, const int8_t* kq,
+               const int8_t* vq, const float* ks, const float* vs, int64_t pages, int64_t page,
+               const int32_t* table, int64_t table_cols, const int32_t* starts,
+               const int32_t* lengths, void* K, int64_t ldk, void* V, int64_t ldv, void* stream);
+
+/* O = softmax(scale Q K^T) V over the cache, `dtype` QG_F16 or QG_BF16, statistics and
+ * sums in fp32, the weights rounded to fp16 for the product with V's codes.
+ *  Q, O : rows of q_heads heads of D values, rows ldq, ldo apart; q_heads is a multiple
+ *         of heads, query head h reads head h / (q_heads / heads) of the cache
+ *  causal : row i of a sequence with n rows sees its tokens up to lengths - n + i, else
+ *         all of them.  A row that sees no token is 0; rows of a sequence that is longer
+ *         than its table are NaN.
+ *  ws: qg_workspace_size(QG_OP_KV8_ATTENTION, rows, q_heads, D) bytes, 256-byte aligned */
+int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads, int64_t heads, int64_t D,
+                  const void* Q, int64_t ldq, const int8_t* kq, const int8_t* vq, const float* ks,
+                  const float* vs, int64_t pages, int64_t page, const int32_t* table,
+                  int64_t table_cols, const int32_t* starts, const int32_t* lengths, float scale,
+                  int causal, void* O, int64_t ldo, void* ws, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
