@@ -6,11 +6,13 @@ namespace qg {
 
 // ------------------------------------------------------------ append
 //
-// A CTA takes a page that new tokens go to, for one head and K or V: the largest
+// A warp takes a page that new tokens go to, for one head and K or V: the largest
 // magnitude of the page's new values, the page's new scale, its older codes rounded to
 // that scale if it grew, and the new codes.  Only the first page of a sequence's new
-// tokens can hold older ones; a page is started afresh with its token 0.
-constexpr int kAppendThreads = 128;
+// tokens can hold older ones; a page is started afresh with its token 0.  The warps of a
+// CTA share the page, which takes three dependent loads to find.
+constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / 32;
+constexpr int kAppendHeld = 4;  // pieces of 8 values that a lane keeps between the two passes
 
 struct AppendParams {
     Kv8Cache c;
@@ -23,7 +25,6 @@ struct AppendParams {
 template <class T>
 __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParams p) {
     __shared__ int64_t mem[kAppendThreads / 32 + 2];
-    __shared__ uint32_t red[kAppendThreads / 32];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const Kv8Cache& c = p.c;
@@ -50,34 +51,49 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
     const int number = kv8_page(c, at.b, static_cast<int>(which));
     if (number < 0) return;
     const int kept = static_cast<int>(lo - start), count = static_cast<int>(hi - lo);
-    const int head = blockIdx.y;
-    const bool value = blockIdx.z == 1;
+    const int lane = threadIdx.x & 31;
+    const int log_d8 = 31 - __clz(c.D) - 3, pieces = count << log_d8;  // D is 64, 128 or 256
+
+    const int job = blockIdx.y * kAppendWarps + (threadIdx.x >> 5);
+    if (job >= 2 * c.heads) return;
+    const int head = job >> 1;
+    const bool value = job & 1;
     const bool aligned = value ? p.v_aligned : p.k_aligned;
     const int64_t ld = value ? p.ldv : p.ldk;
     const T* x = static_cast<const T*>(value ? p.V : p.K) + (s.row0 + (lo - s.first)) * ld + head * c.D;
     const int64_t unit = static_cast<int64_t>(number) * c.heads + head;
-    int8_t* codes = (value ? p.c.vq : p.c.kq) + unit * page * c.D;
-    float* scale = (value ? p.c.vs : p.c.ks) + unit;
+    int8_t* codes = (value ? c.vq : c.kq) + unit * page * c.D;
+    float* scale = (value ? c.vs : c.ks) + unit;
+    const float old = kept ? *scale : 0.f;
+    auto piece = [&](int i, float (&v)[8]) {
+        load_some<T, 8>(x + (i >> log_d8) * ld + 8 * (i & ((1 << log_d8) - 1)), 8, aligned, v);
+    };
 
-    const int per = c.D / 8, pieces = count * per;  // D is 64, 128 or 256
+    float held[kAppendHeld][8];
     uint32_t amax = 0;
-    for (int i = threadIdx.x; i < pieces; i += kAppendThreads) {
-        float v[8];
-        load_some<T, 8>(x + i / per * ld + i % per * 8, 8, aligned, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) amax = max(amax, abs_bits(v[k]));
+    for (int k = 0; k < kAppendHeld; ++k)
+        if (lane + 32 * k < pieces) piece(lane + 32 * k, held[k]);
+#pragma unroll
+    for (int k = 0; k < kAppendHeld; ++k)
+        if (lane + 32 * k < pieces) {
+#pragma unroll
+            for (int m = 0; m < 8; ++m) amax = max(amax, abs_bits(held[k][m]));
+        }
+#pragma unroll 4
+    for (int i = lane + 32 * kAppendHeld; i < pieces; i += 32) {
+        float v[8];
+        piece(i, v);
+#pragma unroll
+        for (int m = 0; m < 8; ++m) amax = max(amax, abs_bits(v[m]));
     }
     amax = warp_max_u32(amax);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
-    const float old = kept ? *scale : 0.f;
-    __syncthreads();
-    amax = warp_max_u32(red[threadIdx.x & (kAppendThreads / 32 - 1)]);
     float now = s8_scale(amax, kPageScaleFloor);
     if (kept && (old > now || old != old)) now = old;
     const float r = s8_inverse(now);
     if (kept && old != now) {  // also where one of them is NaN: 0 then
         const float ratio = __fdiv_rn(old, now);
-        for (int i = threadIdx.x; i < kept * c.D / 16; i += kAppendThreads) {
+        for (int i = lane; i < kept * c.D / 16; i += 32) {
             uint4 w = reinterpret_cast<uint4*>(codes)[i];
             uint32_t* q = reinterpret_cast<uint32_t*>(&w);
 #pragma unroll
@@ -92,15 +108,22 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
         }
     }
     int8_t* to = codes + kept * c.D;
-    for (int i = threadIdx.x; i < pieces; i += kAppendThreads) {
-        float v[8];
-        load_some<T, 8>(x + i / per * ld + i % per * 8, 8, aligned, v);
+    auto store = [&](int i, const float (&v)[8]) {
         int q[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[k] = s8_code(v[k], r);
         *reinterpret_cast<uint2*>(to + i * 8) = make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
+    };
+#pragma unroll
+    for (int k = 0; k < kAppendHeld; ++k)
+        if (lane + 32 * k < pieces) store(lane + 32 * k, held[k]);
+#pragma unroll 4
+    for (int i = lane + 32 * kAppendHeld; i < pieces; i += 32) {
+        float v[8];
+        piece(i, v);
+        store(i, v);
     }
-    if (threadIdx.x == 0) *scale = now;
+    if (lane == 0) *scale = now;
 }
 
 // ------------------------------------------------------------ gather
@@ -113,40 +136,53 @@ struct GatherParams {
     bool k_aligned, v_aligned;
 };
 
-constexpr int kGatherThreads = 256;
+// A CTA takes kGatherRows rows one after another, a warp a row at a time: its token's codes
+// of all heads, 16 a lane.  The CTA finds its first row's sequence, a warp goes on from there.
+constexpr int kGatherThreads = 256, kGatherWarps = kGatherThreads / 32;
+constexpr int kGatherRows = 16;
 
-// A CTA takes a row: its token's codes of all heads, 16 a thread.
 template <class T>
 __global__ void __launch_bounds__(kGatherThreads) k_kv8_gather(const GatherParams p) {
     __shared__ int64_t mem[kGatherThreads / 32 + 2];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const Kv8Cache& c = p.c;
-    // rows are found among the sequences that have any
-    const Kv8Place at = kv8_find<kGatherThreads>(p.bt.B, blockIdx.x, 0, mem,
+    // rows are counted among the sequences that have any
+    const Kv8Place at = kv8_find<kGatherThreads>(p.bt.B, static_cast<int64_t>(blockIdx.x) * kGatherRows, 0, mem,
                                                  [&](int b) -> int64_t { return kv8_seq(p.bt, c, b).n; });
     if (at.b >= p.bt.B) return;
-    const Kv8Seq s = kv8_seq(p.bt, c, at.b);
-    const int64_t row = s.row0 + at.at, pos = s.first + at.at;
-    const int number = pos < 0 || pos >= s.len ? -1 : kv8_page(c, at.b, static_cast<int>(pos >> c.page_log2));
-    const int page = 1 << c.page_log2, offset = static_cast<int>(pos & (page - 1));
-    const int per = c.D / 16, pieces = c.heads * per;
-    for (int i = threadIdx.x; i < 2 * pieces; i += kGatherThreads) {
-        const bool value = i >= pieces;
-        const int k = value ? i - pieces : i, head = k / per, d = k % per * 16;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        float scale = __uint_as_float(0x7fc00000u);
-        if (number >= 0) {
-            const int64_t unit = static_cast<int64_t>(number) * c.heads + head;
-            w = *reinterpret_cast<const uint4*>((value ? c.vq : c.kq) + (unit * page + offset) * c.D + d);
-            scale = (value ? c.vs : c.ks)[unit];
+    const int lane = threadIdx.x & 31;
+    const int per = c.D / 16, pieces = c.heads * per, page = 1 << c.page_log2;
+    int b = at.b;
+    int64_t i = at.at + (threadIdx.x >> 5);  // place in sequence b
+    Kv8Seq s = kv8_seq(p.bt, c, b);
+    for (int k = threadIdx.x >> 5; k < kGatherRows; k += kGatherWarps, i += kGatherWarps) {
+        while (i >= s.n) {
+            i -= s.n;
+            if (++b >= p.bt.B) return;
+            s = kv8_seq(p.bt, c, b);
         }
-        float f[16];
-        const uint32_t q[4] = {w.x, w.y, w.z, w.w};
+        const int64_t row = s.row0 + i, pos = s.first + i;
+        const int number = pos < 0 || pos >= s.len ? -1 : kv8_page(c, b, static_cast<int>(pos >> c.page_log2));
+        const int offset = static_cast<int>(pos & (page - 1));
+#pragma unroll 2
+        for (int j = lane; j < 2 * pieces; j += 32) {
+            const bool value = j >= pieces;
+            const int at_piece = value ? j - pieces : j, head = at_piece / per, d = at_piece % per * 16;
+            uint4 w = make_uint4(0, 0, 0, 0);
+            float scale = __uint_as_float(0x7fc00000u);
+            if (number >= 0) {
+                const int64_t unit = static_cast<int64_t>(number) * c.heads + head;
+                w = *reinterpret_cast<const uint4*>((value ? c.vq : c.kq) + (unit * page + offset) * c.D + d);
+                scale = (value ? c.vs : c.ks)[unit];
+            }
+            float f[16];
+            const uint32_t q[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int m = 0; m < 16; ++m) f[m] = static_cast<float>(static_cast<int8_t>(q[m / 4] >> (8 * (m % 4)))) * scale;
-        T* to = static_cast<T*>(value ? p.V : p.K) + row * (value ? p.ldv : p.ldk) + head * c.D + d;
-        store_some<T, 16>(to, 16, value ? p.v_aligned : p.k_aligned, f);
+            for (int m = 0; m < 16; ++m) f[m] = static_cast<float>(static_cast<int8_t>(q[m / 4] >> (8 * (m % 4)))) * scale;
+            T* to = static_cast<T*>(value ? p.V : p.K) + row * (value ? p.ldv : p.ldk) + head * c.D + d;
+            store_some<T, 16>(to, 16, value ? p.v_aligned : p.k_aligned, f);
+        }
     }
 }
 
@@ -224,7 +260,9 @@ int kv8_append(int dtype, int64_t B, int64_t rows, int64_t heads, int64_t D, con
     const int64_t bound = rows / page + 2 * B, units = rows < bound ? rows : bound;
     return by_dtype(dtype, [&](auto t) {
         return launch_serialized(k_kv8_append<decltype(t)>,
-                                 dim3(static_cast<unsigned>(units), static_cast<unsigned>(heads), 2), kAppendThreads, 0,
+                                 dim3(static_cast<unsigned>(units),
+                                      static_cast<unsigned>((2 * heads + kAppendWarps - 1) / kAppendWarps)),
+                                 kAppendThreads, 0,
                                  1, static_cast<cudaStream_t>(stream), p);
     });
 }
@@ -249,7 +287,8 @@ int kv8_gather(int dtype, int64_t B, int64_t rows, int64_t heads, int64_t D, con
     p.k_aligned = rows_aligned(dtype, K, ldk);
     p.v_aligned = rows_aligned(dtype, V, ldv);
     return by_dtype(dtype, [&](auto t) {
-        return launch_serialized(k_kv8_gather<decltype(t)>, dim3(static_cast<unsigned>(rows)), kGatherThreads, 0, 1,
+        return launch_serialized(k_kv8_gather<decltype(t)>, dim3(static_cast<unsigned>((rows + kGatherRows - 1) / kGatherRows)),
+                                 kGatherThreads, 0, 1,
                                  static_cast<cudaStream_t>(stream), p);
     });
 }

@@ -424,45 +424,113 @@ __global__ void __launch_bounds__(kAttnThreads) k_kv8_attention(const AttnParams
 }
 
 // Joins the parts of a unit that CTA borders cut: CTA k takes the unit that border k
-// (the start of piece k) cuts, if no earlier border cuts it too.
+// (the start of piece k) cuts, if no earlier border cuts it too.  Only rows that exist are
+// joined; the parts are spread over the threads, since a long sequence alone has 50 of them
+// a unit and each is a load from the L2 away.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 64;  // parts whose weights are held at a time
+
 template <class T, int D>
-__global__ void __launch_bounds__(kAttnThreads) k_kv8_attention_join(const AttnParams p) {
+__global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnParams p) {
     using Cfg = AttnCfg<D>;
-    __shared__ int64_t mem[kAttnWarps + 2];
+    constexpr int LANES = D / 2;                      // threads across a row, two values each
+    constexpr int SLICES = kJoinThreads / LANES;      // parts, or rows, at a time
+    __shared__ int64_t mem[kJoinThreads / 32 + 2];
+    __shared__ float weight[kJoinParts][kAttnRows];
+    __shared__ float top[kAttnRows], total[kAttnRows];
+    __shared__ float2 sums[SLICES][LANES];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int k = blockIdx.x + 1;
     const Kv8Place at =
-        kv8_find<kAttnThreads>(p.bt.B, k, p.ctas, mem, [&](int b) { return attn_seq(p, b).work(p.c.heads); });
+        kv8_find<kJoinThreads>(p.bt.B, k, p.ctas, mem, [&](int b) { return attn_seq(p, b).work(p.c.heads); });
     const AttnUnit u = attn_unit(p, at);
     if (u.b >= p.bt.B || u.tile == 0) return;
     const AttnSeq a = attn_seq(p, u.b);
     const int64_t wk = at.total * k / p.ctas, u0 = wk - u.tile, u1 = u0 + a.tiles;
     auto border = [&](int i) { return at.total * i / p.ctas; };
     if (border(k - 1) > u0) return;
-    // parts: the piece that starts the unit (an earlier one may be empty), then those that go on
-    for (int i = threadIdx.x; i < kAttnRows * D; i += kAttnThreads) {
-        const int r = i / D, d = i % D;
-        auto part = [&](int cta) {
-            return p.part + (static_cast<int64_t>(cta) * 2 + (border(cta) <= u0 ? 1 : 0)) * kAttnRows * Cfg::STRIDE +
-                   r * Cfg::STRIDE;
-        };
+    // parts of pieces k - 1 .. last; a piece without tiles (fewer tiles than pieces) has none
+    int last = static_cast<int>((u1 * p.ctas - 1) / at.total);
+    while (last > k && border(last) >= u1) --last;
+    while (last + 1 < p.ctas && border(last + 1) < u1) ++last;
+    const bool dense = at.total >= p.ctas;
+    auto part = [&](int cta) {
+        return p.part + (static_cast<int64_t>(cta) * 2 + (cta < k ? 1 : 0)) * kAttnRows * Cfg::STRIDE;
+    };
+    const int rows = min(kAttnRows, a.rows - u.row_tile * kAttnRows), count = last - k + 2;
+    // a row's largest M over its parts: 16 threads a row
+    {
+        const int r = threadIdx.x / 16, j0 = threadIdx.x % 16;
         float m = neg_inf();
-        for (int cta = k - 1; cta < p.ctas && border(cta) < u1; ++cta)
-            if (border(cta + 1) > border(cta)) m = fmaxf(m, part(cta)[D]);
-        float sum = 0.f, total = 0.f;
-        for (int cta = k - 1; cta < p.ctas && border(cta) < u1; ++cta) {
-            if (border(cta + 1) == border(cta)) continue;
-            const float* f = part(cta);
-            const float e = f[D] == neg_inf() ? 0.f : exp2_fast(f[D] - m);
-            sum = fmaf(f[d], e, sum);
-            total = fmaf(f[D + 1], e, total);
+        for (int j = j0; j < count; j += 16)
+            if (dense || border(k + j) > border(k - 1 + j)) m = fmaxf(m, part(k - 1 + j)[r * Cfg::STRIDE + D]);
+#pragma unroll
+        for (int o = 8; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (j0 == 0) {
+            top[r] = m;
+            total[r] = 0.f;
         }
-        const int rr = u.row_tile * kAttnRows + r;
-        if (rr < a.rows) {
-            const float v = a.s.cut ? __uint_as_float(0x7fc00000u) : total == 0.f ? 0.f : sum / total;
-            static_cast<T*>(p.O)[(a.s.row0 + rr / p.group) * p.ldo + (u.head * p.group + rr % p.group) * D + d] =
-                from_f32<T>(v);
+    }
+    const int slice = threadIdx.x / LANES, lane = threadIdx.x % LANES;
+    // rows and slices of parts share the CTA's slices: one row at a time, or all slices a row
+    float2 o[kAttnRows];
+#pragma unroll
+    for (int r = 0; r < kAttnRows; ++r) o[r] = make_float2(0.f, 0.f);
+    for (int j0 = 0; j0 < count; j0 += kJoinParts) {
+        const int n = min(kJoinParts, count - j0);
+        __syncthreads();
+        // thread (r, i): weights of parts i, i + 16, ... of row r, and their denominators
+        const int r = threadIdx.x / 16, i0 = threadIdx.x % 16;
+        float den = 0.f;
+        for (int i = i0; i < n; i += 16) {
+            const int j = j0 + i;
+            float e = 0.f;
+            if (dense || border(k + j) > border(k - 1 + j)) {
+                const float* f = part(k - 1 + j) + r * Cfg::STRIDE;
+                e = f[D] == neg_inf() ? 0.f : exp2_fast(f[D] - top[r]);
+                den = fmaf(f[D + 1], e, den);
+            }
+            weight[i][r] = e;
+        }
+#pragma unroll
+        for (int o2 = 8; o2 > 0; o2 /= 2) den += __shfl_xor_sync(0xffffffffu, den, o2);
+        if (i0 == 0) total[r] += den;
+        __syncthreads();
+        for (int i = slice; i < n; i += SLICES) {
+            if (!dense && border(k + j0 + i) == border(k - 1 + j0 + i)) continue;
+            const float* f = part(k - 1 + j0 + i) + 2 * lane;
+            float2 v[kAttnRows];  // all rows' loads ahead of their use
+#pragma unroll
+            for (int q = 0; q < kAttnRows; ++q)
+                if (q < rows) v[q] = *reinterpret_cast<const float2*>(f + q * Cfg::STRIDE);
+#pragma unroll
+            for (int q = 0; q < kAttnRows; ++q)
+                if (q < rows) {
+                    o[q].x = fmaf(v[q].x, weight[i][q], o[q].x);
+                    o[q].y = fmaf(v[q].y, weight[i][q], o[q].y);
+                }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kAttnRows; ++q) {
+        if (q >= rows) break;
+        __syncthreads();
+        sums[slice][lane] = o[q];
+        __syncthreads();
+        if (slice == 0) {
+            float2 v = sums[0][lane];
+#pragma unroll
+            for (int i = 1; i < SLICES; ++i) {
+                v.x += sums[i][lane].x;
+                v.y += sums[i][lane].y;
+            }
+            const int rr = u.row_tile * kAttnRows + q;
+            const float t = total[q], nan = __uint_as_float(0x7fc00000u);
+            T* out = static_cast<T*>(p.O) + (a.s.row0 + rr / p.group) * p.ldo +
+                     (u.head * p.group + rr % p.group) * D + 2 * lane;
+            out[0] = from_f32<T>(a.s.cut ? nan : t == 0.f ? 0.f : v.x / t);
+            out[1] = from_f32<T>(a.s.cut ? nan : t == 0.f ? 0.f : v.y / t);
         }
     }
 }
@@ -484,7 +552,7 @@ static int launch_attention(AttnParams p, int dev, cudaStream_t s) {
     rc = launch_serialized(k_kv8_attention<T, D>, dim3(static_cast<unsigned>(p.ctas)), kAttnThreads, AttnCfg<D>::SMEM, 1,
                            s, p);
     if (rc || p.ctas == 1) return rc;
-    return launch_serialized(k_kv8_attention_join<T, D>, dim3(static_cast<unsigned>(p.ctas - 1)), kAttnThreads, 0, 1, s,
+    return launch_serialized(k_kv8_attention_join<T, D>, dim3(static_cast<unsigned>(p.ctas - 1)), kJoinThreads, 0, 1, s,
                              p);
 }
 
@@ -499,7 +567,7 @@ static int attention_by_size(const AttnParams& p, int dev, cudaStream_t s) {
     QG_BLOCK_KERNEL_BUDGET("k_kv8_attention<" NAME "," #D ">", (reinterpret_cast<const void*>(k_kv8_attention<T, D>)), \
                            kAttnThreads, AttnCfg<D>::SMEM, 0, 1, PER);                                            \
     QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_join<" NAME "," #D ">",                                               \
-                           (reinterpret_cast<const void*>(k_kv8_attention_join<T, D>)), kAttnThreads, 0, 0, 1, 1)
+                           (reinterpret_cast<const void*>(k_kv8_attention_join<T, D>)), kJoinThreads, 0, 0, 1, 1)
 QG_ATTN_BUDGETS(__half, "f16", 64, 3);
 QG_ATTN_BUDGETS(__half, "f16", 128, 3);
 QG_ATTN_BUDGETS(__half, "f16", 256, 1);

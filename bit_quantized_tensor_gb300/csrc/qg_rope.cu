@@ -17,8 +17,7 @@
 namespace qg {
 
 constexpr int kRopeThreads = 128, kRopeWarps = kRopeThreads / 32;
-constexpr int kRopeUnroll = 4;       // heads in flight a group of lanes, forward
-constexpr int kRopeUnrollBwd = 2;    // backward
+constexpr int kRopeUnroll = 2;       // heads in flight a group of lanes
 constexpr int64_t kRopeMaxD = 1024;
 constexpr int kRopeMaxParts = 1024;  // rows of partial sums of either gain
 
@@ -37,7 +36,7 @@ struct RopeParams {
     int blocks[2];       // CTAs of either job, Q's first
     int tokens, D, R;
     int lanes, rotating, group;  // lanes that hold a head, that rotate; power of two
-    int splits, heads_per;       // a token's heads in `splits` parts of heads_per (warps)
+    int heads_per, splits[2];    // a warp takes heads_per heads of a token: parts of either job's
     bool gain_f32;
     const int32_t* positions;
     const float* table;
@@ -99,10 +98,23 @@ struct RopeLane {
     __device__ __forceinline__ static bool aligned(const void* q) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0; }
     // its gains, piece a then piece b
     __device__ __forceinline__ void gains(const RopeParams& p, const void* gain, float (&g)[2 * E]) const {
+        float ga[E], gb[E];
 #pragma unroll
-        for (int i = 0; i < 2 * E; ++i) {
-            const int at = i < E ? a + i : b + i - E;
-            g[i] = !on || !gain ? 1.f : weight_at<T>(gain, p.gain_f32, at);
+        for (int i = 0; i < E; ++i) ga[i] = gb[i] = 1.f;
+        if (on && gain) {
+            const bool vec = aligned(gain);
+            if (p.gain_f32) {
+                load_some<float, E>(static_cast<const float*>(gain) + a, E, vec, ga);
+                load_some<float, E>(static_cast<const float*>(gain) + b, E, vec, gb);
+            } else {
+                load_some<T, E>(static_cast<const T*>(gain) + a, E, vec, ga);
+                load_some<T, E>(static_cast<const T*>(gain) + b, E, vec, gb);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            g[i] = ga[i];
+            g[E + i] = gb[i];
         }
     }
 };
@@ -112,6 +124,27 @@ template <bool PAIRS, int E>
 __device__ __forceinline__ constexpr int first_of(int i) { return PAIRS ? 2 * i : i; }
 template <bool PAIRS, int E>
 __device__ __forceinline__ constexpr int second_of(int i) { return PAIRS ? 2 * i + 1 : E + i; }
+
+// The first and the second values of a lane's pairs, two pairs a register pair.
+template <bool PAIRS, int E>
+__device__ __forceinline__ void split_pairs(const float (&v)[2 * E], uint64_t (&a)[E / 2], uint64_t (&b)[E / 2]) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        a[i] = two(v[first_of<PAIRS, E>(2 * i)], v[first_of<PAIRS, E>(2 * i + 1)]);
+        b[i] = two(v[second_of<PAIRS, E>(2 * i)], v[second_of<PAIRS, E>(2 * i + 1)]);
+    }
+}
+template <bool PAIRS, int E>
+__device__ __forceinline__ void join_pairs(const uint64_t (&a)[E / 2], const uint64_t (&b)[E / 2], float (&v)[2 * E]) {
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        const float2 x = both(a[i]), y = both(b[i]);
+        v[first_of<PAIRS, E>(2 * i)] = x.x;
+        v[first_of<PAIRS, E>(2 * i + 1)] = x.y;
+        v[second_of<PAIRS, E>(2 * i)] = y.x;
+        v[second_of<PAIRS, E>(2 * i + 1)] = y.y;
+    }
+}
 
 template <class T>
 __device__ __forceinline__ void widen(uint4 w, float* f) {
@@ -140,6 +173,10 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
     return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
+// A warp takes heads_per heads of a token, U steps of as many as its lanes hold at most;
+// their loads go out ahead of those of the gains and the table.  The hardware deals the
+// CTAs out, which evens out what a loop over tokens left uneven (43 -> 30 us at 8192 tokens
+// of 40 heads).
 template <class T, bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeParams p) {
     constexpr int E = RopeLane<T>::E, U = kRopeUnroll;
@@ -147,67 +184,77 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeParams 
     pdl_launch_dependents();
     const bool second = static_cast<int>(blockIdx.x) >= p.blocks[0];
     const RopeJob& j = p.job[second];
-    const int block = blockIdx.x - (second ? p.blocks[0] : 0), blocks = p.blocks[second];
+    const int splits = p.splits[second];
+    const int64_t item = static_cast<int64_t>(blockIdx.x - (second ? p.blocks[0] : 0)) * kRopeWarps + (threadIdx.x >> 5);
+    if (item >= static_cast<int64_t>(p.tokens) * splits) return;
+    const int token = static_cast<int>(item / splits), h0 = static_cast<int>(item % splits) * p.heads_per;
+    const int h1 = min(j.heads, h0 + p.heads_per);
     RopeLane<T> lane;
     lane.template init<PAIRS>(p);
-    float g[2 * E];
-    lane.gains(p, j.gain, g);
-    const int step = 32 / p.group;
-    const float inv_d = 1.f / static_cast<float>(p.D);
-    const int64_t items = static_cast<int64_t>(p.tokens) * p.splits;
-    for (int64_t item = block * kRopeWarps + (threadIdx.x >> 5); item < items; item += blocks * kRopeWarps) {
-        const int token = static_cast<int>(item / p.splits), part = static_cast<int>(item % p.splits);
-        const int h0 = part * p.heads_per, h1 = min(j.heads, h0 + p.heads_per);
-        if (h0 >= h1) continue;
-        float c[E], s[E];
+    const int step = 32 / p.group, h = h0 + lane.sub;
+    const T* x = static_cast<const T*>(j.X) + token * j.ldx;
+    T* y = static_cast<T*>(j.Y) + token * j.ldy;
+    uint4 wa[U], wb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
+        if (lane.on && h + u * step < h1) {
+            const T* at = x + (h + u * step) * p.D;
+            wa[u] = *reinterpret_cast<const uint4*>(at + lane.a);
+            wb[u] = *reinterpret_cast<const uint4*>(at + lane.b);
+        }
+    }
+    // y_a = x_a (g_a cos) - x_b (g_b sin), y_b = x_b (g_b cos) + x_a (g_a sin), both times rstd
+    uint64_t ac[E / 2], bs[E / 2], bc[E / 2], as[E / 2];
+    {
+        float c[E], s[E], g[2 * E];
         lane.angles(p, p.R ? table_row(p, token) : nullptr, c, s);
-        const T* x = static_cast<const T*>(j.X) + token * j.ldx;
-        T* y = static_cast<T*>(j.Y) + token * j.ldy;
-        for (int h = h0 + lane.sub; h - lane.sub < h1; h += U * step) {
-            uint4 wa[U], wb[U];
+        lane.gains(p, j.gain, g);
+        uint64_t ga[E / 2], gb[E / 2];
+        split_pairs<PAIRS, E>(g, ga, gb);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                wa[u] = wb[u] = make_uint4(0, 0, 0, 0);
-                if (lane.on && h + u * step < h1) {
-                    const T* at = x + (h + u * step) * p.D;
-                    wa[u] = *reinterpret_cast<const uint4*>(at + lane.a);
-                    wb[u] = *reinterpret_cast<const uint4*>(at + lane.b);
-                }
-            }
+        for (int i = 0; i < E / 2; ++i) {
+            const uint64_t cc = two(c[2 * i], c[2 * i + 1]), ss = two(s[2 * i], s[2 * i + 1]);
+            ac[i] = mul_two(ga[i], cc);
+            bc[i] = mul_two(gb[i], cc);
+            as[i] = mul_two(ga[i], ss);
+            bs[i] = mul_two(gb[i], two(-s[2 * i], -s[2 * i + 1]));
+        }
+    }
+    const float inv_d = 1.f / static_cast<float>(p.D);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (h - lane.sub + u * step >= h1) break;  // the same for the whole warp
-                float v[2 * E];
-                widen<T>(wa[u], v);
-                widen<T>(wb[u], v + E);
-                float sum = 0.f;
+    for (int u = 0; u < U; ++u) {
+        if (h0 + u * step >= h1) break;  // the same for the whole warp
+        float v[2 * E];
+        widen<T>(wa[u], v);
+        widen<T>(wb[u], v + E);
+        uint64_t a[E / 2], b[E / 2], sq = two(0.f, 0.f);
+        split_pairs<PAIRS, E>(v, a, b);
 #pragma unroll
-                for (int i = 0; i < 2 * E; ++i) sum = fmaf(v[i], v[i], sum);
-                sum = group_sum(sum, p.group);
-                const float rstd = __fdiv_rn(1.f, __fsqrt_rn(fmaf(sum, inv_d, p.eps)));
-                float o[2 * E];
+        for (int i = 0; i < E / 2; ++i) sq = fma_two(b[i], b[i], fma_two(a[i], a[i], sq));
+        const float2 half = both(sq);
+        const float rstd = rsqrtf(fmaf(group_sum(half.x + half.y, p.group), inv_d, p.eps));
+        const uint64_t r2 = two(rstd, rstd);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int ia = first_of<PAIRS, E>(i), ib = second_of<PAIRS, E>(i);
-                    const float za = v[ia] * rstd * g[ia], zb = v[ib] * rstd * g[ib];
-                    o[ia] = fmaf(za, c[i], -(zb * s[i]));
-                    o[ib] = fmaf(zb, c[i], za * s[i]);
-                }
-                const int head = h + u * step;
-                if (lane.on && head < h1) {
-                    T* at = y + head * p.D;
-                    *reinterpret_cast<uint4*>(at + lane.a) = narrow<T>(o);
-                    *reinterpret_cast<uint4*>(at + lane.b) = narrow<T>(o + E);
-                    if (j.rstd && lane.l == 0) j.rstd[static_cast<int64_t>(token) * j.heads + head] = rstd;
-                }
-            }
+        for (int i = 0; i < E / 2; ++i) {
+            const uint64_t za = mul_two(a[i], r2), zb = mul_two(b[i], r2);
+            a[i] = fma_two(za, ac[i], mul_two(zb, bs[i]));
+            b[i] = fma_two(zb, bc[i], mul_two(za, as[i]));
+        }
+        join_pairs<PAIRS, E>(a, b, v);
+        const int head = h + u * step;
+        if (lane.on && head < h1) {
+            T* at = y + head * p.D;
+            *reinterpret_cast<uint4*>(at + lane.a) = narrow<T>(v);
+            *reinterpret_cast<uint4*>(at + lane.b) = narrow<T>(v + E);
+            if (j.rstd && lane.l == 0) j.rstd[static_cast<int64_t>(token) * j.heads + head] = rstd;
         }
     }
 }
 
 template <class T, bool PAIRS>
-__global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope_backward(const RopeParams p) {
-    constexpr int E = RopeLane<T>::E, U = kRopeUnrollBwd;
+__global__ void __launch_bounds__(kRopeThreads, 4) k_qk_norm_rope_backward(const RopeParams p) {
+    constexpr int E = RopeLane<T>::E, U = kRopeUnroll;
     __shared__ float sums[kRopeWarps][32][2 * E + 1];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
@@ -216,76 +263,92 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope_backward(const Ro
     const int block = blockIdx.x - (second ? p.blocks[0] : 0), blocks = p.blocks[second];
     RopeLane<T> lane;
     lane.template init<PAIRS>(p);
-    float g[2 * E], dg[2 * E];
-    lane.gains(p, j.gain, g);
+    uint64_t ga[E / 2], gb[E / 2], dga[E / 2], dgb[E / 2];
+    {
+        float g[2 * E];
+        lane.gains(p, j.gain, g);
+        split_pairs<PAIRS, E>(g, ga, gb);
+    }
 #pragma unroll
-    for (int i = 0; i < 2 * E; ++i) dg[i] = 0.f;
+    for (int i = 0; i < E / 2; ++i) dga[i] = dgb[i] = two(0.f, 0.f);
     const int step = 32 / p.group;
     const float inv_d = 1.f / static_cast<float>(p.D);
-    const int64_t items = static_cast<int64_t>(p.tokens) * p.splits;
+    const int splits = p.splits[second];
+    const int64_t items = static_cast<int64_t>(p.tokens) * splits;
     for (int64_t item = block * kRopeWarps + (threadIdx.x >> 5); item < items; item += blocks * kRopeWarps) {
-        const int token = static_cast<int>(item / p.splits), part = static_cast<int>(item % p.splits);
+        const int token = static_cast<int>(item / splits), part = static_cast<int>(item % splits);
         const int h0 = part * p.heads_per, h1 = min(j.heads, h0 + p.heads_per);
-        if (h0 >= h1) continue;
-        float c[E], s[E];
-        lane.angles(p, p.R ? table_row(p, token) : nullptr, c, s);
         const T* x = static_cast<const T*>(j.X) + token * j.ldx;
         const T* dy = static_cast<const T*>(j.dY) + token * j.lddy;
         T* dx = static_cast<T*>(j.Y) + token * j.ldy;
         const float* rs = j.rstd + static_cast<int64_t>(token) * j.heads;
-        for (int h = h0 + lane.sub; h - lane.sub < h1; h += U * step) {
-            uint4 xa[U], xb[U], ya[U], yb[U];
-            float r[U];
+        const int h = h0 + lane.sub;
+        uint4 xa[U], xb[U], ya[U], yb[U];
+        float r[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                xa[u] = xb[u] = ya[u] = yb[u] = make_uint4(0, 0, 0, 0);
-                r[u] = 0.f;
-                const int head = h + u * step;
-                if (lane.on && head < h1) {
-                    xa[u] = *reinterpret_cast<const uint4*>(x + head * p.D + lane.a);
-                    xb[u] = *reinterpret_cast<const uint4*>(x + head * p.D + lane.b);
-                    ya[u] = *reinterpret_cast<const uint4*>(dy + head * p.D + lane.a);
-                    yb[u] = *reinterpret_cast<const uint4*>(dy + head * p.D + lane.b);
-                    r[u] = rs[head];
-                }
+        for (int u = 0; u < U; ++u) {
+            xa[u] = xb[u] = ya[u] = yb[u] = make_uint4(0, 0, 0, 0);
+            r[u] = 0.f;
+            const int head = h + u * step;
+            if (lane.on && head < h1) {
+                xa[u] = *reinterpret_cast<const uint4*>(x + head * p.D + lane.a);
+                xb[u] = *reinterpret_cast<const uint4*>(x + head * p.D + lane.b);
+                ya[u] = *reinterpret_cast<const uint4*>(dy + head * p.D + lane.a);
+                yb[u] = *reinterpret_cast<const uint4*>(dy + head * p.D + lane.b);
+                r[u] = rs[head];
             }
+        }
+        float c[E], s[E];
+        lane.angles(p, p.R ? table_row(p, token) : nullptr, c, s);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (h - lane.sub + u * step >= h1) break;
-                float xh[2 * E], d[2 * E];
-                widen<T>(xa[u], xh);
-                widen<T>(xb[u], xh + E);
-                widen<T>(ya[u], d);
-                widen<T>(yb[u], d + E);
-                float dot = 0.f;
+        for (int u = 0; u < U; ++u) {
+            if (h0 + u * step >= h1) break;
+            // values of heads or lanes that are not there are 0, and so is what they add
+            float v[2 * E], d[2 * E];
+            widen<T>(xa[u], v);
+            widen<T>(xb[u], v + E);
+            widen<T>(ya[u], d);
+            widen<T>(yb[u], d + E);
+            uint64_t ha[E / 2], hb[E / 2], da[E / 2], db[E / 2], dot2 = two(0.f, 0.f);
+            split_pairs<PAIRS, E>(v, ha, hb);
+            split_pairs<PAIRS, E>(d, da, db);
+            const uint64_t r2 = two(r[u], r[u]);
 #pragma unroll
-                for (int i = 0; i < E; ++i) {
-                    const int ia = first_of<PAIRS, E>(i), ib = second_of<PAIRS, E>(i);
-                    const float da = fmaf(d[ia], c[i], d[ib] * s[i]), db = fmaf(d[ib], c[i], -(d[ia] * s[i]));
-                    xh[ia] *= r[u];
-                    xh[ib] *= r[u];
-                    if (lane.on && h + u * step < h1) {
-                        dg[ia] = fmaf(da, xh[ia], dg[ia]);
-                        dg[ib] = fmaf(db, xh[ib], dg[ib]);
-                    }
-                    d[ia] = da * g[ia];
-                    d[ib] = db * g[ib];
-                    dot = fmaf(d[ia], xh[ia], fmaf(d[ib], xh[ib], dot));
+            for (int i = 0; i < E / 2; ++i) {
+                const uint64_t cc = two(c[2 * i], c[2 * i + 1]), ss = two(s[2 * i], s[2 * i + 1]);
+                const uint64_t ns = two(-s[2 * i], -s[2 * i + 1]);
+                const uint64_t za = fma_two(da[i], cc, mul_two(db[i], ss)), zb = fma_two(db[i], cc, mul_two(da[i], ns));
+                ha[i] = mul_two(ha[i], r2);
+                hb[i] = mul_two(hb[i], r2);
+                dga[i] = fma_two(za, ha[i], dga[i]);
+                dgb[i] = fma_two(zb, hb[i], dgb[i]);
+                da[i] = mul_two(za, ga[i]);
+                db[i] = mul_two(zb, gb[i]);
+                dot2 = fma_two(db[i], hb[i], fma_two(da[i], ha[i], dot2));
+            }
+            const float2 half = both(dot2);
+            const float dot = -group_sum(half.x + half.y, p.group) * inv_d;
+            const int head = h + u * step;
+            if (lane.on && head < h1) {
+                const uint64_t dot_two = two(dot, dot);
+#pragma unroll
+                for (int i = 0; i < E / 2; ++i) {
+                    da[i] = mul_two(r2, fma_two(ha[i], dot_two, da[i]));
+                    db[i] = mul_two(r2, fma_two(hb[i], dot_two, db[i]));
                 }
-                dot = group_sum(dot, p.group) * inv_d;
-                const int head = h + u * step;
-                if (lane.on && head < h1) {
-#pragma unroll
-                    for (int i = 0; i < 2 * E; ++i) d[i] = r[u] * fmaf(-xh[i], dot, d[i]);
-                    *reinterpret_cast<uint4*>(dx + head * p.D + lane.a) = narrow<T>(d);
-                    *reinterpret_cast<uint4*>(dx + head * p.D + lane.b) = narrow<T>(d + E);
-                }
+                join_pairs<PAIRS, E>(da, db, d);
+                *reinterpret_cast<uint4*>(dx + head * p.D + lane.a) = narrow<T>(d);
+                *reinterpret_cast<uint4*>(dx + head * p.D + lane.b) = narrow<T>(d + E);
             }
         }
     }
     // the CTA's sums, in the order of warps and heads
+    {
+        float dg[2 * E];
+        join_pairs<PAIRS, E>(dga, dgb, dg);
 #pragma unroll
-    for (int i = 0; i < 2 * E; ++i) sums[threadIdx.x >> 5][threadIdx.x & 31][i] = dg[i];
+        for (int i = 0; i < 2 * E; ++i) sums[threadIdx.x >> 5][threadIdx.x & 31][i] = dg[i];
+    }
     __syncthreads();
     float* out = p.partial + (static_cast<int64_t>(second ? kRopeMaxParts : 0) + block) * p.D;
     for (int i = threadIdx.x; i < p.lanes * 2 * E; i += kRopeThreads) {
@@ -355,7 +418,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope_any(const RopePar
         sum = warp_sum(sum);
         const float mean = sum / static_cast<float>(p.D);
         if constexpr (!BACKWARD) {
-            rstd = __fdiv_rn(1.f, __fsqrt_rn(mean + p.eps));
+            rstd = rsqrtf(mean + p.eps);
             if (j.rstd && lane == 0) j.rstd[item] = rstd;
         }
         for (int i = lane; i < slots; i += 32) {
@@ -398,8 +461,10 @@ __global__ void __launch_bounds__(1024) k_rope_gains(const float* partial, int p
     const int parts = second ? parts_k : parts_q;
     const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
     float v = 0.f;
-    if (col < D)
+    if (col < D) {
+#pragma unroll 8
         for (int i = slice; i < parts; i += 32) v += src[static_cast<int64_t>(i) * D + col];
+    }
     red[slice][threadIdx.x & 31] = v;
     __syncthreads();
     if (slice == 0 && col < D) {
@@ -428,8 +493,8 @@ static int launch_rope(RopeParams p, int dev, cudaStream_t s, int* parts) {
     const bool pieces = p.D * elem % 16 == 0 && (p.D - p.R) % (2 * E) == 0 && p.R % (2 * E) == 0 && p.D / (2 * E) <= 32 &&
                         pieces_fit(p.job[0], elem, BACKWARD) && pieces_fit(p.job[1], elem, BACKWARD);
     const int64_t most = BACKWARD ? kRopeMaxParts : int64_t(1) << 20;
-    // CTAs of a job: enough for its items, at most its share of `full`
-    const int64_t full = static_cast<int64_t>(num_sms(dev)) * (BACKWARD ? 6 : 8);
+    // CTAs of a job that walks over its items: enough for them, at most its share of `full`
+    const int64_t full = static_cast<int64_t>(num_sms(dev)) * (BACKWARD ? 4 : 8);
     auto share = [&](int i, int64_t items) -> int {
         if (!p.job[i].heads) return 0;
         const int64_t want = (items + kRopeWarps - 1) / kRopeWarps;
@@ -443,14 +508,16 @@ static int launch_rope(RopeParams p, int dev, cudaStream_t s, int* parts) {
         p.group = 1;
         while (p.group < p.lanes) p.group *= 2;
         const int step = 32 / p.group;
-        const int chunks = ((p.job[0].heads > p.job[1].heads ? p.job[0].heads : p.job[1].heads) + step - 1) / step;
-        // with few tokens a token's heads are spread over warps
-        const int64_t warps = full * kRopeWarps;
-        int64_t splits = warps / p.tokens;
-        splits = splits < 1 ? 1 : splits > chunks ? chunks : splits;
-        p.heads_per = static_cast<int>((chunks + splits - 1) / splits) * step;
-        p.splits = (chunks * step + p.heads_per - 1) / p.heads_per;
-        for (int i = 0; i < 2; ++i) parts[i] = p.blocks[i] = share(i, static_cast<int64_t>(p.tokens) * p.splits);
+        // heads of a token that a warp takes: as many as it has in flight, fewer where that
+        // would leave SMs without warps
+        p.heads_per = kRopeUnroll * step;
+        while (p.heads_per > step && static_cast<int64_t>(p.tokens) * heads / p.heads_per < 4 * kRopeWarps * num_sms(dev))
+            p.heads_per /= 2;
+        for (int i = 0; i < 2; ++i) {
+            p.splits[i] = (p.job[i].heads + p.heads_per - 1) / p.heads_per;
+            const int64_t items = static_cast<int64_t>(p.tokens) * p.splits[i];
+            parts[i] = p.blocks[i] = BACKWARD ? share(i, items) : static_cast<int>((items + kRopeWarps - 1) / kRopeWarps);
+        }
         const dim3 grid(static_cast<unsigned>(p.blocks[0] + p.blocks[1]));
         if constexpr (BACKWARD)
             return launch_serialized(k_qk_norm_rope_backward<T, PAIRS>, grid, kRopeThreads, 0, 1, s, p);
