@@ -59,6 +59,21 @@ int make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
     return r == CUDA_SUCCESS ? QG_OK : record_cuda_error(-static_cast<int>(r));
 }
 
+int make_tmap_3d_bytes(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t blocks, int box_inner,
+                       int box_rows, CUtensorMapSwizzle swizzle) {
+    EncodeTiledFn fn = encode_tiled();
+    if (!fn) return QG_ERR_CUDA;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                                static_cast<cuuint64_t>(blocks)};
+    const cuuint64_t strides[2] = {dims[0], dims[0] * dims[1]};
+    const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_rows), 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? QG_OK : record_cuda_error(-static_cast<int>(r));
+}
+
 int make_tmap_kmajor(CUtensorMap* map, bool fp16, const void* base, int64_t k_elems, int64_t rows,
                      int64_t row_stride_bytes, int box_k, int box_rows) {
     return make_tmap_2d(map, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8,

@@ -13,6 +13,11 @@ int make_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
                  int64_t outer, int64_t row_stride_bytes, int box_inner, int box_outer,
                  CUtensorMapSwizzle swizzle);
 
+// The same for `blocks` contiguous blocks of `rows` rows of `inner` bytes, with a
+// box of box_rows rows of a block.
+int make_tmap_3d_bytes(CUtensorMap* map, const void* base, int64_t inner, int64_t rows, int64_t blocks, int box_inner,
+                       int box_rows, CUtensorMapSwizzle swizzle);
+
 // Kernel choice set by qg_set_gemm_path: 0 by shape, 1 one CTA per tile,
 // 2 CTA pairs.
 int gemm_path();

@@ -194,7 +194,7 @@ int check_kv8(const Kv8Args& a) {
     if (a.page != 16 && a.page != 32 && a.page != 64 && a.page != 128) return QG_ERR_UNSUPPORTED;
     if (a.D != 64 && a.D != 128 && a.D != 256) return QG_ERR_UNSUPPORTED;
     if (a.heads > 1024 || a.B > (1 << 20) || a.rows > (1 << 27) || a.pages > (int64_t(1) << 30) ||
-        a.table_cols * a.page > (int64_t(1) << 30))
+        a.table_cols * a.page > (int64_t(1) << 30) || a.pages * a.heads > INT32_MAX)
         return QG_ERR_INVALID_ARG;
     if (a.B == 0 || a.rows == 0) return QG_OK;
     if (!a.kq || !a.vq || !a.ks || !a.vs || !a.table || !a.starts || !a.lengths || a.pages < 1 || a.table_cols < 1)

@@ -10,34 +10,47 @@
 // second product, is at most 2^8 whatever the pages' scales are.  Sums, M and the
 // denominator are fp32.  Queries go in as fp16 times a power of two of their row, which
 // is exact for bf16 too but for values 2^-28 of the row's largest.
+#include <cuda.h>
+
 #include "kv8_common.cuh"
 #include "kv8_host.h"
+#include "qg_gemm_host.h"
 
 namespace qg {
 
-// One warp takes 16 tokens a step, for 16 rows: the heads that share a key head, times a
-// sequence's query rows.  All (sequence, key head, 16 rows) units' tiles of 64 tokens lie
-// on one axis that the CTAs cut into equal pieces, wherever the units' borders are, so a
-// batch of any lengths loads all SMs alike; a unit that several CTAs have parts of is
-// joined by a second kernel from their fp32 sums.
+// One warp takes 32 tokens a step, for 8 or 16 rows (NB = 1, 2): the heads that share a key
+// head, times a sequence's query rows.  Tokens are the rows of the products' results and
+// query rows their 8 columns (S^T = K Q^T, O^T = V^T P^T), so that 4 or 8 heads a key head
+// waste little; the weights change sides in registers (movmatrix).  All (sequence, key
+// head, rows) units' tiles of 128 tokens lie on one axis that the CTAs cut into equal
+// pieces, wherever the units' borders are, so a batch of any lengths loads all SMs alike;
+// a unit that several CTAs have parts of is joined by a second kernel from their fp32 sums.
+//
+// The cache's bytes are what this cannot do without, and turning them into fp16 is most of
+// what it executes, so the rest is kept small: each warp has a ring of its own that TMA
+// fills (a box for 16 or 32 tokens, swizzled so that no lanes meet in a bank), and no
+// barrier but the end of a unit; the running maximum is looked at once for 32 tokens and
+// the sums are rescaled only when it has grown by 2^8.
 constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
-constexpr int kAttnRows = 16;
-constexpr int kAttnTile = 16 * kAttnWarps;
-constexpr int kAttnStages = 4;
+constexpr int kAttnStep = 32;                       // tokens of a warp's step
+constexpr int kAttnTile = kAttnStep * kAttnWarps;
+constexpr int kAttnStages = 2;
 constexpr float kLazy = 8.f;  // log2 of how far M may lag behind
+constexpr int kSiteAttnK = 411, kSiteAttnV = 412;
 
 struct AttnParams {
     Kv8Cache c;
     Kv8Batch bt;
     const void* Q;
     int64_t ldq;
-    bool q_bf16, causal;
+    bool causal, q_vec;  // q_vec: heads start at multiples of 8 bytes
     int group;          // query heads a key head
     float scale_log2;   // scale * log2(e)
     void* O;
     int64_t ldo;
-    float* part;        // 2 partial sums a CTA: kAttnRows x (D + 2)
+    float* part;        // 2 partial sums a CTA: rows x (D + 2)
     int ctas;
+    Ctl ctl;
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -47,15 +60,28 @@ __device__ __forceinline__ float exp2_fast(float x) {
 }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// Box of 16 or 32 tokens of a page and head, 128 bytes (or D) of each.  Issued by a whole
+// warp under an elected lane's predicate, which keeps its operands in uniform registers.
+__device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, int d, int token, int unit, uint32_t bar,
+                                         uint32_t elected) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.b32 q, %6, 0;\n"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(token), "r"(unit), "r"(bar), "r"(elected)
+        : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// An 8 x 8 matrix of 16-bit values, two a lane (row lane / 4), transposed.
+__device__ __forceinline__ uint32_t transposed(uint32_t v) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+    return d;
+}
 
 // Units and tiles of a sequence.
 struct AttnSeq {
@@ -63,11 +89,12 @@ struct AttnSeq {
     int rows, row_tiles, tiles;
     __device__ __forceinline__ int64_t work(int heads) const { return static_cast<int64_t>(heads) * row_tiles * tiles; }
 };
+template <int NB>
 __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
     AttnSeq a;
     a.s = kv8_seq(p.bt, p.c, b);
     a.rows = a.s.n * p.group;
-    a.row_tiles = (a.rows + kAttnRows - 1) / kAttnRows;
+    a.row_tiles = (a.rows + 8 * NB - 1) / (8 * NB);
     a.tiles = max(1, (a.s.len + kAttnTile - 1) / kAttnTile);
     return a;
 }
@@ -77,10 +104,11 @@ struct AttnUnit {
     int b, head, row_tile;
     int64_t tile;
 };
+template <int NB>
 __device__ __forceinline__ AttnUnit attn_unit(const AttnParams& p, const Kv8Place& at) {
     AttnUnit u = {at.b, 0, 0, 0};
     if (at.b >= p.bt.B) return u;
-    const AttnSeq a = attn_seq(p, at.b);
+    const AttnSeq a = attn_seq<NB>(p, at.b);
     const int64_t per_head = static_cast<int64_t>(a.row_tiles) * a.tiles;
     u.head = static_cast<int>(at.at / per_head);
     const int64_t rest = at.at - u.head * per_head;
@@ -89,29 +117,30 @@ __device__ __forceinline__ AttnUnit attn_unit(const AttnParams& p, const Kv8Plac
     return u;
 }
 
-// Place of 16-byte piece `chunk` of token `t` of a warp's 16 in its stage: rows of D bytes,
-// pieces exchanged so that neither K's reads (two tokens by four pieces) nor V's (four even
-// tokens by two pieces, or by four halves) meet in a bank.
-template <int D>
-__device__ __forceinline__ int kv_place(int t, int chunk) {
-    if constexpr (D == 64) {
-        const int half = (t ^ (t >> 2)) & 1;
-        return (t >> 1) * 128 + half * 64 + ((chunk ^ (t & 2)) << 4);
-    } else {
-        return t * D + ((chunk ^ (t & 6) ^ ((t & 1) << 2)) << 4);
-    }
+// The token of a box's 8 (or the second 8) that is column n of a product, so that the
+// lanes that read together, two tokens by four 16-byte pieces of K and four tokens by two
+// pieces (D = 64: four half pieces) of V, lie in different banks under TMA's swizzle.
+__device__ __forceinline__ constexpr int token_of(int n) {
+    return (((n >> 2) & 1) * 4 + ((n >> 1) & 1) * 3) ^ ((n & 1) * 5);
 }
 
-template <int D>
+template <int D, int NB_>
 struct AttnCfg {
-    static constexpr int CHUNKS = D / 16;               // 16-byte pieces of a token
-    static constexpr int KV_BYTES = 16 * D;             // a warp's tokens of K, or V
-    static constexpr int STAGE_BYTES = 2 * KV_BYTES + 16;  // and the two scales
-    static constexpr int WARP_BYTES = kAttnStages * STAGE_BYTES;
+    static constexpr int NB = NB_, ROWS = 8 * NB;
+    static constexpr int W = D < 128 ? D : 128;         // bytes of a box's row
+    static constexpr int BOXES = D / W;                 // boxes across a head
+    static constexpr int HALF_BYTES = 16 * W;           // 16 tokens of a box
+    static constexpr int KV_BYTES = 2 * BOXES * HALF_BYTES;  // K, or V, of a step
+    static constexpr int WARP_BYTES = 2 * kAttnStages * KV_BYTES;
     static constexpr int STRIDE = D + 2;                // floats of a row of partial sums: O, M, denominator
-    static constexpr int SMEM = kAttnWarps * WARP_BYTES > kAttnWarps * kAttnRows * STRIDE * 4
-                                    ? kAttnWarps * WARP_BYTES
-                                    : kAttnWarps * kAttnRows * STRIDE * 4;
+    static constexpr int PART = ROWS * STRIDE;
+    static constexpr int SMEM = kAttnWarps * WARP_BYTES + 1024;
+    static constexpr int PER_SM = D == 64 ? 4 : D == 128 ? 3 : 1;
+    static_assert(kAttnWarps * PART * 4 <= SMEM - 1024, "partial sums reuse the rings");
+    // address in a box of 16-byte piece `chunk` of token t
+    __device__ __forceinline__ static int place(int t, int chunk) {
+        return t * W + ((chunk ^ (W == 128 ? t & 7 : (t >> 1) & 3)) << 4);
+    }
 };
 
 // 2^14 .. 2^15 over a row's largest magnitude (as bits), a power of two, and 1 over it.
@@ -124,292 +153,411 @@ __device__ __forceinline__ RowPower row_power(uint32_t amax_bits) {
     return {__uint_as_float(static_cast<uint32_t>(e) << 23), __uint_as_float(static_cast<uint32_t>(254 - e) << 23)};
 }
 
-template <class T, int D>
-__global__ void __launch_bounds__(kAttnThreads) k_kv8_attention(const AttnParams p) {
-    using Cfg = AttnCfg<D>;
-    constexpr int KS = D / 16;   // MMA steps of q . k
-    constexpr int NT = D / 8;    // 8-column tiles of O
-    extern __shared__ __align__(16) uint8_t smem[];
+// Two values of a row of the result: 0 for a row that sees nothing, NaN for a sequence
+// that is longer than its table.
+template <class T>
+__device__ __forceinline__ void store_out(const AttnParams& p, const AttnSeq& a, int head, int row, int d, int D,
+                                          float2 sum, float total) {
+    const float nan = __uint_as_float(0x7fc00000u);
+    T* out = static_cast<T*>(p.O) + (a.s.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D + d;
+    out[0] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.x / total);
+    out[1] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.y / total);
+}
+
+template <class T, int D, int NB>
+__global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
+    k_kv8_attention(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const AttnParams p) {
+    using Cfg = AttnCfg<D, NB>;
+    constexpr int KS = D / 16;          // MMA steps of k . q
+    constexpr int DT = D / 16;          // 16-value tiles of O^T
+    constexpr int PER = Cfg::W / 8;     // values of a token that a lane holds of a box of V
+    constexpr int ROWS = Cfg::ROWS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                     ~static_cast<uintptr_t>(1023));
     __shared__ int64_t mem[kAttnWarps + 2];
+    __shared__ __align__(8) uint64_t bars[kAttnWarps][2 * kAttnStages];
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    uint8_t* const ring = smem + warp * Cfg::WARP_BYTES;
+    const uint32_t ring_u32 = smem_u32(ring), bar0 = smem_u32(&bars[warp][0]);
+    const uint32_t elected = elect_lane();
+    auto k_bar = [&](int s) { return bar0 + 16u * s; };
+    auto v_bar = [&](int s) { return bar0 + 16u * s + 8u; };
+    if (elected) {
+        for (int s = 0; s < kAttnStages; ++s) {
+            mbar_init(k_bar(s), 1);
+            mbar_init(v_bar(s), 1);
+        }
+        fence_mbar_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    __syncwarp();
     pdl_wait_prior_grid();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    fence_proxy_async_global();  // the cache may have been written just before, with ordinary stores
     const Kv8Place at = kv8_find<kAttnThreads>(p.bt.B, blockIdx.x, p.ctas, mem,
-                                               [&](int b) { return attn_seq(p, b).work(p.c.heads); });
+                                               [&](int b) { return attn_seq<NB>(p, b).work(p.c.heads); });
     int64_t w0 = at.total * blockIdx.x / p.ctas;
     const int64_t w1 = at.total * (blockIdx.x + 1) / p.ctas;
-    AttnUnit u = attn_unit(p, at);
-    uint8_t* const ring = smem + warp * Cfg::WARP_BYTES;
-    const uint32_t ring_u32 = smem_u32(ring);
+    AttnUnit u = attn_unit<NB>(p, at);
     const int page_log2 = p.c.page_log2;
-    const int64_t page_bytes = static_cast<int64_t>(p.c.heads) * D << page_log2;
+    const bool wide = page_log2 > 4;  // a step's tokens lie in one page: boxes of 32
+    uint32_t filled = 0;  // steps whose copies this warp has issued: their stage and phase
+    bool ok = true;
 
     while (w0 < w1 && u.b < p.bt.B) {
-        const AttnSeq a = attn_seq(p, u.b);
+        const AttnSeq a = attn_seq<NB>(p, u.b);
         if (a.rows == 0) {  // a sequence without rows has no place on the axis
             u = {u.b + 1, 0, 0, 0};
             continue;
         }
         const int64_t end = min(static_cast<int64_t>(a.tiles), u.tile + (w1 - w0));
-        // the two rows of this thread, g and g + 8 of the unit's 16
-        int row[2], sees[2];
-        const T* q[2];
+        // tokens that a row of the sequence sees
+        auto seen_by = [&](int row) {
+            const int64_t n = p.causal ? a.s.first + row / p.group + 1 : a.s.len;
+            return row >= a.rows || n < 0 ? 0 : n < a.s.len ? static_cast<int>(n) : a.s.len;
+        };
+        const int row0 = u.row_tile * ROWS;
+        const int most = seen_by(min(a.rows, row0 + ROWS) - 1), least = seen_by(row0);
+        // this lane's columns of the products: rows 8 n + 2 c + m of the unit
+        int sees[NB][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            row[i] = u.row_tile * kAttnRows + g + 8 * i;
-            const int token = row[i] / p.group;
-            sees[i] = 0;
-            q[i] = nullptr;
-            if (row[i] < a.rows) {
-                const int64_t upto = p.causal ? a.s.first + token + 1 : a.s.len;
-                sees[i] = upto < 0 ? 0 : upto < a.s.len ? static_cast<int>(upto) : a.s.len;
-                q[i] = static_cast<const T*>(p.Q) + (a.s.row0 + token) * p.ldq +
-                       (u.head * p.group + row[i] % p.group) * D;
-            }
-        }
-        // what any row of the unit sees, the same in all threads
-        const int last_row = min(a.rows, (u.row_tile + 1) * kAttnRows) - 1;
-        const int64_t most64 = p.causal ? a.s.first + last_row / p.group + 1 : a.s.len;
-        const int most = most64 < 0 ? 0 : most64 < a.s.len ? static_cast<int>(most64) : a.s.len;
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) sees[n][m] = seen_by(row0 + 8 * n + 2 * c + m);
 
-        // this warp's 16 tokens of tiles u.tile .. end that anyone sees
-        const int t0 = static_cast<int>(u.tile) * kAttnTile + 16 * warp;
+        // this warp's steps of 32 tokens of tiles u.tile .. end that anyone sees
+        const int t0 = static_cast<int>(u.tile) * kAttnTile + kAttnStep * warp;
         const int t1 = min(most, static_cast<int>(end) * kAttnTile);
         const int steps = t1 > t0 ? (t1 - t0 + kAttnTile - 1) / kAttnTile : 0;
-        int page_of = -1;  // of step (base + lane)
-        int page_base = 0;
-        auto fetch_pages = [&](int base) {
-            page_base = base;
-            const int step = base + lane;
-            page_of = step < steps ? kv8_page(p.c, u.b, (t0 + step * kAttnTile) >> page_log2) : -1;
+        // pages of 16 steps' halves, one a lane, and what their scales come to: of this batch of
+        // steps and of the next
+        struct Half {
+            int unit;          // page * heads + head, -1: no page
+            float sk, lsv, isv;
         };
-        auto issue = [&](int step) {
-            if (step < steps) {
-                if (step >= page_base + 32) fetch_pages(step);
-                const int number = __shfl_sync(0xffffffffu, page_of, step - page_base);
-                const uint32_t st = ring_u32 + (step % kAttnStages) * Cfg::STAGE_BYTES;
-                const int offset = (t0 + step * kAttnTile) & ((1 << page_log2) - 1);
-                const int64_t from = (number < 0 ? 0 : number) * page_bytes +
-                                     ((static_cast<int64_t>(u.head) << page_log2) + offset) * D;
-#pragma unroll
-                for (int i = lane; i < 16 * Cfg::CHUNKS; i += 32) {
-                    const int t = i / Cfg::CHUNKS, chunk = i % Cfg::CHUNKS;
-                    cp_async16(st + kv_place<D>(t, chunk), p.c.kq + from + t * D + 16 * chunk);
-                    cp_async16(st + Cfg::KV_BYTES + kv_place<D>(t, chunk), p.c.vq + from + t * D + 16 * chunk);
+        auto fetch = [&](int batch) {
+            const int token = t0 + (batch * 16 + (lane >> 1)) * kAttnTile + 16 * (lane & 1);
+            Half h = {-1, __uint_as_float(0x7fc00000u), 0.f, 0.f};
+            if (token < t1) {
+                const int page = kv8_page(p.c, u.b, token >> page_log2);
+                float sv = h.sk;
+                if (page >= 0) {
+                    h.unit = page * p.c.heads + u.head;
+                    h.sk = p.c.ks[h.unit];
+                    sv = p.c.vs[h.unit];
                 }
-                if (number >= 0) {
-                    const int64_t unit = static_cast<int64_t>(number) * p.c.heads + u.head;
-                    if (lane < 2) cp_async4(st + 2 * Cfg::KV_BYTES + 4 * lane, (lane ? p.c.vs : p.c.ks) + unit);
-                } else if (lane < 2) {
-                    reinterpret_cast<uint32_t*>(ring + (step % kAttnStages) * Cfg::STAGE_BYTES + 2 * Cfg::KV_BYTES)[lane] =
-                        0x7fc00000u;
-                }
+                h.lsv = __log2f(sv);
+                h.isv = __fdividef(1.f, sv);
             }
-            cp_async_commit();
+            return h;
         };
-        fetch_pages(0);
+        Half now = fetch(0), next = now;
+        if (steps > 16) next = fetch(1);
+        // copies of K, or V, of a step; `unit` is that of its batch.  Steps are counted over all
+        // units that the warp works on: stage and phase of a step
+        const uint32_t base = filled;
+        auto stage = [&](int step) { return static_cast<int>((base + step) % kAttnStages); };
+        auto phase = [&](int step) { return ((base + step) / kAttnStages) & 1u; };
+        auto load = [&](int step, int unit, bool value) {
+            const int j = 2 * (step & 15), s = stage(step), token = t0 + step * kAttnTile, mask = (1 << page_log2) - 1;
+            const int u0 = max(__shfl_sync(0xffffffffu, unit, j), 0);
+            const uint32_t bar = value ? v_bar(s) : k_bar(s);
+            const uint32_t dst = ring_u32 + (2 * s + (value ? 1 : 0)) * Cfg::KV_BYTES;
+            const CUtensorMap* map = value ? &tmV : &tmK;
+            const bool both_in = wide || token + 16 < t1;
+            if (elected) mbar_arrive_expect_tx(bar, both_in ? Cfg::KV_BYTES : Cfg::KV_BYTES / 2);
+            __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kAttnStages - 1; ++i) issue(i);
-
-        // queries: lane c holds, for MMA step k, the four values that its 32-bit word of a
-        // token's codes has in that step
-        uint32_t qf[KS][4];
-        float row_factor[2];
-        {
-            uint32_t bits[2] = {0u, 0u};
+            for (int i = 0; i < Cfg::BOXES; ++i)
+                load_box(dst + 2 * i * Cfg::HALF_BYTES, map, i * Cfg::W, token & mask, u0, bar, elected);
+            if (!wide && both_in) {
+                const int u1 = max(__shfl_sync(0xffffffffu, unit, j + 1), 0);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const int d = (k / 4) * 64 + c * 16 + (k % 4) * 4;
-#pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        if (q[i]) bits[i] = max(bits[i], abs_bits(to_f32<T>(q[i][d + m])));
-                }
-                bits[i] = max(bits[i], __shfl_xor_sync(0xffffffffu, bits[i], 1));
-                bits[i] = max(bits[i], __shfl_xor_sync(0xffffffffu, bits[i], 2));
-                const RowPower power = row_power(bits[i]);
-                row_factor[i] = power.down * p.scale_log2;
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const int d = (k / 4) * 64 + c * 16 + (k % 4) * 4;
-                    float f[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) f[m] = q[i] ? to_f32<T>(q[i][d + m]) * power.up : 0.f;
-                    qf[k][i] = pack2<__half>(f[0], f[1]);
-                    qf[k][i + 2] = pack2<__half>(f[2], f[3]);
-                }
+                for (int i = 0; i < Cfg::BOXES; ++i)
+                    load_box(dst + (2 * i + 1) * Cfg::HALF_BYTES, map, i * Cfg::W, (token + 16) & mask, u1, bar, elected);
             }
+        };
+        const int ready = ok ? steps : 0;
+        for (int i = 0; i < kAttnStages && i < ready; ++i) {
+            load(i, now.unit, false);
+            load(i, now.unit, true);
         }
 
-        float o[NT][4], M[2] = {neg_inf(), neg_inf()}, den[2] = {0.f, 0.f};
+        // queries: for MMA step k lane c of row g holds the four values that its 32-bit word of a
+        // token's codes has in that step
+        uint32_t qf[NB][KS][2];
+        float factor[NB][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < NB; ++n) {
+            const int row = row0 + 8 * n + g;
+            const T* q = static_cast<const T*>(p.Q) + (a.s.row0 + row / p.group) * p.ldq +
+                         (u.head * p.group + row % p.group) * D + c * 16;
+            uint32_t bits = 0;
+            uint2 raw[KS];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+            for (int k = 0; k < KS; ++k) {
+                raw[k] = make_uint2(0u, 0u);
+                const T* at_k = q + (k / 4) * 64 + (k % 4) * 4;
+                if (row < a.rows) {
+                    if (p.q_vec) {
+                        raw[k] = *reinterpret_cast<const uint2*>(at_k);
+                    } else {
+                        const uint16_t* h = reinterpret_cast<const uint16_t*>(at_k);
+                        raw[k] = make_uint2(h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const float2 x = unpack2<T>(raw[k].x), y = unpack2<T>(raw[k].y);
+                bits = max(max(max(bits, abs_bits(x.x)), max(abs_bits(x.y), abs_bits(y.x))), abs_bits(y.y));
+            }
+            bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+            bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
+            const RowPower power = row_power(bits);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const float2 x = unpack2<T>(raw[k].x), y = unpack2<T>(raw[k].y);
+                qf[n][k][0] = pack2<__half>(x.x * power.up, x.y * power.up);
+                qf[n][k][1] = pack2<__half>(y.x * power.up, y.y * power.up);
+            }
+            const float down = power.down * p.scale_log2;
+            factor[n][0] = __shfl_sync(0xffffffffu, down, 8 * c);
+            factor[n][1] = __shfl_sync(0xffffffffu, down, 8 * c + 4);
+        }
 
-        for (int step = 0; step < steps; ++step) {
-            cp_async_wait<kAttnStages - 2>();
-            __syncwarp();
-            issue(step + kAttnStages - 1);
-            const uint8_t* st = ring + (step % kAttnStages) * Cfg::STAGE_BYTES;
-            const float sk = reinterpret_cast<const float*>(st + 2 * Cfg::KV_BYTES)[0];
-            const float sv = reinterpret_cast<const float*>(st + 2 * Cfg::KV_BYTES)[1];
-            // scores of 16 rows by 2 x 8 tokens
-            float x[2][4];
+        float o[DT][NB][4], M[NB][2], den[NB][2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+        for (int n = 0; n < NB; ++n) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[n][i] = 0.f;
-#pragma unroll
-                for (int k = 0; k < KS; k += 4) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(st + kv_place<D>(8 * n + g, (k / 4) * 4 + c));
-                    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        uint32_t b0, b1;
-                        s8_to_f16(word[m], b0, b1);
-                        mma_f16(x[n], qf[k + m][0], qf[k + m][1], qf[k + m][2], qf[k + m][3], b0, b1);
-                    }
-                }
-            }
-            const int tok = t0 + step * kAttnTile + 2 * c;  // of x[0][0]; x[n][i] is 8 n + i % 2 on
-            const float lsv = __log2f(sv), isv = __fdividef(1.f, sv);
-            float top[2] = {neg_inf(), neg_inf()};
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float f = row_factor[i] * sk;
-#pragma unroll
-                for (int n = 0; n < 2; ++n)
-#pragma unroll
-                    for (int m = 0; m < 2; ++m) {
-                        float& v = x[n][2 * i + m];
-                        v = tok + 8 * n + m < sees[i] ? fmaf(v, f, lsv) : neg_inf();
-                        top[i] = fmaxf(top[i], v);
-                    }
-                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 1));
-                top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], 2));
-            }
-            const bool moves = top[0] > M[0] + kLazy || top[1] > M[1] + kLazy || (M[0] == neg_inf() && top[0] > M[0]) ||
-                               (M[1] == neg_inf() && top[1] > M[1]);
-            if (__any_sync(0xffffffffu, moves)) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float m = fmaxf(M[i], top[i]);
-                    const float f = M[i] == neg_inf() ? 0.f : exp2_fast(M[i] - m);
-                    M[i] = m;
-                    den[i] *= f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        o[n][2 * i] *= f;
-                        o[n][2 * i + 1] *= f;
-                    }
-                }
-            }
-            uint32_t pf[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float m = M[i] == neg_inf() ? 0.f : M[i];
-                float sum = 0.f;
-#pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    const float e0 = exp2_fast(x[n][2 * i] - m), e1 = exp2_fast(x[n][2 * i + 1] - m);
-                    sum += e0 + e1;
-                    pf[2 * n + i] = pack2<__half>(e0, e1);
-                }
-                if (!(sum == 0.f)) den[i] = fmaf(sum, isv, den[i]);  // not 0 times a NaN of tokens that it does not see
-            }
-            // O += w . V: column g of tile n is value g D / 8 + n of a head; lane c's tokens are 2 c,
-            // 2 c + 1, 2 c + 8 and 2 c + 9, whose bytes are brought together
-            constexpr int PER = D / 8;  // values of a lane a token
-            const uint8_t* sv8 = st + Cfg::KV_BYTES;
-            uint32_t vw[4][PER / 4];
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-                const int token = 2 * c + (t & 1) + 8 * (t >> 1);
-                if constexpr (D == 64) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(sv8 + kv_place<D>(token, g >> 1) + 8 * (g & 1));
-                    vw[t][0] = w.x;
-                    vw[t][1] = w.y;
-                } else {
-#pragma unroll
-                    for (int k = 0; k < PER / 16; ++k) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(sv8 + kv_place<D>(token, (PER / 16) * g + k));
-                        vw[t][4 * k] = w.x;
-                        vw[t][4 * k + 1] = w.y;
-                        vw[t][4 * k + 2] = w.z;
-                        vw[t][4 * k + 3] = w.w;
-                    }
-                }
+            for (int m = 0; m < 2; ++m) {
+                M[n][m] = neg_inf();
+                den[n][m] = 0.f;
             }
 #pragma unroll
-            for (int k = 0; k < PER / 4; ++k) {
-                // bytes of token pairs side by side, then as fp16 pairs
-                uint32_t b[4][2];
+            for (int d = 0; d < DT; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[d][n][i] = 0.f;
+        }
+
+        for (int step = 0; step < ready; ++step) {
+            if ((step & 15) == 0 && step) {
+                now = next;
+                if (step + 16 < ready) next = fetch(step / 16 + 1);
+            }
+            const int s = stage(step);
+            if (!__all_sync(0xffffffffu, bounded_wait(k_bar(s), phase(step), nullptr, p.ctl, kSiteAttnK))) {
+                ok = false;
+                break;
+            }
+            // scores of 2 x 16 tokens (rows token_of(g) and 8 more of each 16) by the unit's rows
+            const uint8_t* st = ring + 2 * s * Cfg::KV_BYTES;
+            float x[2][NB][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[h][n][i] = 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; k += 4) {
+                const int chunk = (k / 4) * 4 + c;  // of the head's 16-byte pieces
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t lo = __byte_perm(vw[2 * h][k], vw[2 * h + 1][k], 0x5140);
-                    const uint32_t hi = __byte_perm(vw[2 * h][k], vw[2 * h + 1][k], 0x7362);
-                    s8_to_f16(lo, b[0][h], b[1][h]);
-                    s8_to_f16(hi, b[2][h], b[3][h]);
+                    const uint8_t* box = st + (2 * (chunk / (Cfg::W / 16)) + h) * Cfg::HALF_BYTES;
+                    const uint4 lo = *reinterpret_cast<const uint4*>(box + Cfg::place(token_of(g), chunk % (Cfg::W / 16)));
+                    const uint4 hi = *reinterpret_cast<const uint4*>(box + Cfg::place(8 + token_of(g), chunk % (Cfg::W / 16)));
+                    const uint32_t lw[4] = {lo.x, lo.y, lo.z, lo.w}, hw[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        uint32_t a0, a1, a2, a3;
+                        s8_to_f16(lw[m], a0, a2);
+                        s8_to_f16(hw[m], a1, a3);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+                            mma_f16(x[h][n], a0, a1, a2, a3, qf[n][k + m][0], qf[n][k + m][1]);
+                    }
                 }
-#pragma unroll
-                for (int m = 0; m < 4; ++m) mma_f16(o[4 * k + m], pf[0], pf[1], pf[2], pf[3], b[m][0], b[m][1]);
             }
-        }
-        cp_async_wait<0>();
+            __syncwarp();
+            const int ahead = (step + kAttnStages) >> 4 == step >> 4 ? now.unit : next.unit;
+            if (step + kAttnStages < ready) load(step + kAttnStages, ahead, false);
+
+            const int j = 2 * (step & 15);
+            float lsv[2], isv[2], top[NB][2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            den[i] += __shfl_xor_sync(0xffffffffu, den[i], 1);
-            den[i] += __shfl_xor_sync(0xffffffffu, den[i], 2);
-        }
-        __syncthreads();  // the rings are free: partial sums of the warps go there
-        float* mine = reinterpret_cast<float*>(smem) + warp * kAttnRows * Cfg::STRIDE;
+            for (int h = 0; h < 2; ++h) {
+                const float sk = __shfl_sync(0xffffffffu, now.sk, j + h);
+                lsv[h] = __shfl_sync(0xffffffffu, now.lsv, j + h);
+                isv[h] = __shfl_sync(0xffffffffu, now.isv, j + h);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            float* r = mine + (g + 8 * i) * Cfg::STRIDE;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                // columns 2 c and 2 c + 1 of tile n: lanes' values (2 c) D / 8 + n
-                r[(2 * c) * (D / 8) + n] = o[n][2 * i];
-                r[(2 * c + 1) * (D / 8) + n] = o[n][2 * i + 1];
+                for (int n = 0; n < NB; ++n) {
+                    const float f0 = factor[n][0] * sk, f1 = factor[n][1] * sk;
+                    x[h][n][0] = fmaf(x[h][n][0], f0, lsv[h]);
+                    x[h][n][1] = fmaf(x[h][n][1], f1, lsv[h]);
+                    x[h][n][2] = fmaf(x[h][n][2], f0, lsv[h]);
+                    x[h][n][3] = fmaf(x[h][n][3], f1, lsv[h]);
+                }
             }
-            if (c == 0) {
-                r[D] = M[i];
-                r[D + 1] = den[i];
+            const int tok = t0 + step * kAttnTile;
+            if (tok + kAttnStep > least) {  // a step at the end of what some row sees
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (tok + 16 * h + token_of(g) + 8 * (i >> 1) >= sees[n][i & 1]) x[h][n][i] = neg_inf();
+            }
+            bool moves = false;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    float v = fmaxf(fmaxf(x[0][n][m], x[0][n][m + 2]), fmaxf(x[1][n][m], x[1][n][m + 2]));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    top[n][m] = v;
+                    moves |= v > M[n][m] + kLazy;  // M is -inf at first
+                }
+            if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const float v = fmaxf(M[n][m], top[n][m]);
+                        const float f = M[n][m] == neg_inf() ? 0.f : exp2_fast(M[n][m] - v);
+                        M[n][m] = v;
+                        den[n][m] *= f;
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) {
+                            o[d][n][m] *= f;
+                            o[d][n][m + 2] *= f;
+                        }
+                    }
+            }
+            // weights, in fp16 and from the products' rows to their columns
+            uint32_t pf[2][NB][2];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                const float m0 = M[n][0] == neg_inf() ? 0.f : M[n][0], m1 = M[n][1] == neg_inf() ? 0.f : M[n][1];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float e0 = exp2_fast(x[h][n][0] - m0), e1 = exp2_fast(x[h][n][1] - m1);
+                    const float e2 = exp2_fast(x[h][n][2] - m0), e3 = exp2_fast(x[h][n][3] - m1);
+                    // not 0 times a NaN of tokens that are not seen
+                    if (!(e0 + e2 == 0.f)) den[n][0] = fmaf(e0 + e2, isv[h], den[n][0]);
+                    if (!(e1 + e3 == 0.f)) den[n][1] = fmaf(e1 + e3, isv[h], den[n][1]);
+                    pf[h][n][0] = transposed(pack2<__half>(e0, e1));
+                    pf[h][n][1] = transposed(pack2<__half>(e2, e3));
+                }
+            }
+            if (!__all_sync(0xffffffffu, bounded_wait(v_bar(s), phase(step), nullptr, p.ctl, kSiteAttnV))) {
+                ok = false;
+                break;
+            }
+            // O^T += V^T w: row g of a box's tiles are values g PER .. of its row, two a tile; lane c's
+            // tokens are those of columns 2 c, 2 c + 1 of either 8, whose bytes are brought together
+            st += Cfg::KV_BYTES;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < Cfg::BOXES; ++i) {
+                    const uint8_t* box = st + (2 * i + h) * Cfg::HALF_BYTES;
+                    uint32_t vw[4][PER / 4];
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int token = 8 * (t >> 1) + token_of(2 * c + (t & 1));
+                        if constexpr (PER == 8) {
+                            const uint2 w = *reinterpret_cast<const uint2*>(box + Cfg::place(token, g >> 1) + 8 * (g & 1));
+                            vw[t][0] = w.x;
+                            vw[t][1] = w.y;
+                        } else {
+                            const uint4 w = *reinterpret_cast<const uint4*>(box + Cfg::place(token, g));
+                            vw[t][0] = w.x;
+                            vw[t][1] = w.y;
+                            vw[t][2] = w.z;
+                            vw[t][3] = w.w;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < PER / 4; ++k) {
+                        // bytes of token pairs side by side, then as fp16 pairs
+                        uint32_t b[4][2];
+#pragma unroll
+                        for (int r = 0; r < 2; ++r) {
+                            const uint32_t lo = __byte_perm(vw[2 * r][k], vw[2 * r + 1][k], 0x5140);
+                            const uint32_t hi = __byte_perm(vw[2 * r][k], vw[2 * r + 1][k], 0x7362);
+                            s8_to_f16(lo, b[0][r], b[1][r]);
+                            s8_to_f16(hi, b[2][r], b[3][r]);
+                        }
+                        const int tile = (i * PER + 4 * k) / 2;
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            mma_f16(o[tile][n], b[0][0], b[1][0], b[0][1], b[1][1], pf[h][n][0], pf[h][n][1]);
+                            mma_f16(o[tile + 1][n], b[2][0], b[3][0], b[2][1], b[3][1], pf[h][n][0], pf[h][n][1]);
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+            if (step + kAttnStages < ready) load(step + kAttnStages, ahead, true);
+        }
+        filled += static_cast<uint32_t>(ready);
+
+        // the warps' sums go where the rings were, and become the unit's or a part's
+        __syncthreads();
+        float* mine = reinterpret_cast<float*>(smem) + warp * Cfg::PART;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                float v = den[n][m];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                v += __shfl_xor_sync(0xffffffffu, v, 16);
+                float* r = mine + (8 * n + 2 * c + m) * Cfg::STRIDE;
+#pragma unroll
+                for (int d = 0; d < DT; ++d)
+                    *reinterpret_cast<float2*>(r + (2 * d / PER) * Cfg::W + g * PER + 2 * d % PER) =
+                        make_float2(o[d][n][m], o[d][n][m + 2]);
+                if (g == 0) *reinterpret_cast<float2*>(r + D) = make_float2(M[n][m], v);
             }
         }
         __syncthreads();
         const bool whole = u.tile == 0 && end == a.tiles;
-        float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (u.tile == 0 ? 1 : 0)) * kAttnRows * Cfg::STRIDE;
-        for (int i = threadIdx.x; i < kAttnRows * D; i += kAttnThreads) {
-            const int r = i / D, d = i % D;
+        const int rows = min(ROWS, a.rows - row0);
+        float* part = p.part + (static_cast<int64_t>(blockIdx.x) * 2 + (u.tile == 0 ? 1 : 0)) * Cfg::PART;
+        for (int i = threadIdx.x; i < rows * (D / 2); i += kAttnThreads) {
+            const int r = i / (D / 2), d = 2 * (i % (D / 2));
             const float* from = reinterpret_cast<const float*>(smem) + r * Cfg::STRIDE;
-            float m = neg_inf(), sum = 0.f, total = 0.f;
-#pragma unroll
-            for (int w = 0; w < kAttnWarps; ++w) m = fmaxf(m, from[w * kAttnRows * Cfg::STRIDE + D]);
+            float2 md[kAttnWarps];
+            float m = neg_inf(), total = 0.f;
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float* f = from + w * kAttnRows * Cfg::STRIDE;
-                const float e = f[D] == neg_inf() ? 0.f : exp2_fast(f[D] - m);
-                sum = fmaf(f[d], e, sum);
-                total = fmaf(f[D + 1], e, total);
+                md[w] = *reinterpret_cast<const float2*>(from + w * Cfg::PART + D);
+                m = fmaxf(m, md[w].x);
+            }
+            float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kAttnWarps; ++w) {
+                const float e = md[w].x == neg_inf() ? 0.f : exp2_fast(md[w].x - m);
+                const float2 v = *reinterpret_cast<const float2*>(from + w * Cfg::PART + d);
+                sum.x = fmaf(v.x, e, sum.x);
+                sum.y = fmaf(v.y, e, sum.y);
+                total = fmaf(md[w].y, e, total);
             }
             if (whole) {
-                const int rr = u.row_tile * kAttnRows + r;
-                if (rr < a.rows) {
-                    const float v = a.s.cut ? __uint_as_float(0x7fc00000u) : total == 0.f ? 0.f : sum / total;
-                    static_cast<T*>(p.O)[(a.s.row0 + rr / p.group) * p.ldo + (u.head * p.group + rr % p.group) * D + d] =
-                        from_f32<T>(v);
-                }
+                store_out<T>(p, a, u.head, row0 + r, d, D, sum, total);
             } else {
-                part[r * Cfg::STRIDE + d] = sum;
-                if (d == 0) {
-                    part[r * Cfg::STRIDE + D] = m;
-                    part[r * Cfg::STRIDE + D + 1] = total;
-                }
+                *reinterpret_cast<float2*>(part + r * Cfg::STRIDE + d) = sum;
+                if (d == 0) *reinterpret_cast<float2*>(part + r * Cfg::STRIDE + D) = make_float2(m, total);
             }
         }
-        __syncthreads();  // the rings may be filled again
+        fence_proxy_async_smem();  // the rings, read and written here, are filled by TMA again
+        __syncthreads();
         w0 += end - u.tile;
         u.tile = 0;
         if (end == a.tiles && ++u.row_tile == a.row_tiles) {
@@ -418,6 +566,12 @@ __global__ void __launch_bounds__(kAttnThreads) k_kv8_attention(const AttnParams
                 u.head = 0;
                 ++u.b;
             }
+        }
+    }
+    if (!ok && elected) {
+        // copies may still be in flight: give them a fixed time to land
+        const uint64_t start = global_timer_ns();
+        while (global_timer_ns() - start < 1000000) {
         }
     }
     pdl_launch_dependents();
@@ -430,23 +584,24 @@ __global__ void __launch_bounds__(kAttnThreads) k_kv8_attention(const AttnParams
 constexpr int kJoinThreads = 256;
 constexpr int kJoinParts = 64;  // parts whose weights are held at a time
 
-template <class T, int D>
+template <class T, int D, int NB>
 __global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnParams p) {
-    using Cfg = AttnCfg<D>;
+    using Cfg = AttnCfg<D, NB>;
+    constexpr int ROWS = Cfg::ROWS;
     constexpr int LANES = D / 2;                      // threads across a row, two values each
     constexpr int SLICES = kJoinThreads / LANES;      // parts, or rows, at a time
     __shared__ int64_t mem[kJoinThreads / 32 + 2];
-    __shared__ float weight[kJoinParts][kAttnRows];
-    __shared__ float top[kAttnRows], total[kAttnRows];
+    __shared__ float weight[kJoinParts][ROWS];
+    __shared__ float top[ROWS], total[ROWS];
     __shared__ float2 sums[SLICES][LANES];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const int k = blockIdx.x + 1;
     const Kv8Place at =
-        kv8_find<kJoinThreads>(p.bt.B, k, p.ctas, mem, [&](int b) { return attn_seq(p, b).work(p.c.heads); });
-    const AttnUnit u = attn_unit(p, at);
+        kv8_find<kJoinThreads>(p.bt.B, k, p.ctas, mem, [&](int b) { return attn_seq<NB>(p, b).work(p.c.heads); });
+    const AttnUnit u = attn_unit<NB>(p, at);
     if (u.b >= p.bt.B || u.tile == 0) return;
-    const AttnSeq a = attn_seq(p, u.b);
+    const AttnSeq a = attn_seq<NB>(p, u.b);
     const int64_t wk = at.total * k / p.ctas, u0 = wk - u.tile, u1 = u0 + a.tiles;
     auto border = [&](int i) { return at.total * i / p.ctas; };
     if (border(k - 1) > u0) return;
@@ -456,34 +611,34 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnP
     while (last + 1 < p.ctas && border(last + 1) < u1) ++last;
     const bool dense = at.total >= p.ctas;
     auto part = [&](int cta) {
-        return p.part + (static_cast<int64_t>(cta) * 2 + (cta < k ? 1 : 0)) * kAttnRows * Cfg::STRIDE;
+        return p.part + (static_cast<int64_t>(cta) * 2 + (cta < k ? 1 : 0)) * Cfg::PART;
     };
-    const int rows = min(kAttnRows, a.rows - u.row_tile * kAttnRows), count = last - k + 2;
-    // a row's largest M over its parts: 16 threads a row
+    const int rows = min(ROWS, a.rows - u.row_tile * ROWS), count = last - k + 2;
+    // a row's largest M over its parts: 16 threads a row, those of the rows that exist
     {
         const int r = threadIdx.x / 16, j0 = threadIdx.x % 16;
         float m = neg_inf();
-        for (int j = j0; j < count; j += 16)
+        for (int j = j0; j < count && r < rows; j += 16)
             if (dense || border(k + j) > border(k - 1 + j)) m = fmaxf(m, part(k - 1 + j)[r * Cfg::STRIDE + D]);
 #pragma unroll
         for (int o = 8; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (j0 == 0) {
+        if (j0 == 0 && r < ROWS) {
             top[r] = m;
             total[r] = 0.f;
         }
     }
     const int slice = threadIdx.x / LANES, lane = threadIdx.x % LANES;
     // rows and slices of parts share the CTA's slices: one row at a time, or all slices a row
-    float2 o[kAttnRows];
+    float2 o[ROWS];
 #pragma unroll
-    for (int r = 0; r < kAttnRows; ++r) o[r] = make_float2(0.f, 0.f);
+    for (int r = 0; r < ROWS; ++r) o[r] = make_float2(0.f, 0.f);
     for (int j0 = 0; j0 < count; j0 += kJoinParts) {
         const int n = min(kJoinParts, count - j0);
         __syncthreads();
         // thread (r, i): weights of parts i, i + 16, ... of row r, and their denominators
         const int r = threadIdx.x / 16, i0 = threadIdx.x % 16;
         float den = 0.f;
-        for (int i = i0; i < n; i += 16) {
+        for (int i = i0; i < n && r < rows; i += 16) {
             const int j = j0 + i;
             float e = 0.f;
             if (dense || border(k + j) > border(k - 1 + j)) {
@@ -495,17 +650,17 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnP
         }
 #pragma unroll
         for (int o2 = 8; o2 > 0; o2 /= 2) den += __shfl_xor_sync(0xffffffffu, den, o2);
-        if (i0 == 0) total[r] += den;
+        if (i0 == 0 && r < ROWS) total[r] += den;
         __syncthreads();
         for (int i = slice; i < n; i += SLICES) {
             if (!dense && border(k + j0 + i) == border(k - 1 + j0 + i)) continue;
             const float* f = part(k - 1 + j0 + i) + 2 * lane;
-            float2 v[kAttnRows];  // all rows' loads ahead of their use
+            float2 v[ROWS];  // all rows' loads ahead of their use
 #pragma unroll
-            for (int q = 0; q < kAttnRows; ++q)
+            for (int q = 0; q < ROWS; ++q)
                 if (q < rows) v[q] = *reinterpret_cast<const float2*>(f + q * Cfg::STRIDE);
 #pragma unroll
-            for (int q = 0; q < kAttnRows; ++q)
+            for (int q = 0; q < ROWS; ++q)
                 if (q < rows) {
                     o[q].x = fmaf(v[q].x, weight[i][q], o[q].x);
                     o[q].y = fmaf(v[q].y, weight[i][q], o[q].y);
@@ -513,7 +668,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnP
         }
     }
 #pragma unroll
-    for (int q = 0; q < kAttnRows; ++q) {
+    for (int q = 0; q < ROWS; ++q) {
         if (q >= rows) break;
         __syncthreads();
         sums[slice][lane] = o[q];
@@ -525,55 +680,72 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnP
                 v.x += sums[i][lane].x;
                 v.y += sums[i][lane].y;
             }
-            const int rr = u.row_tile * kAttnRows + q;
-            const float t = total[q], nan = __uint_as_float(0x7fc00000u);
-            T* out = static_cast<T*>(p.O) + (a.s.row0 + rr / p.group) * p.ldo +
-                     (u.head * p.group + rr % p.group) * D + 2 * lane;
-            out[0] = from_f32<T>(a.s.cut ? nan : t == 0.f ? 0.f : v.x / t);
-            out[1] = from_f32<T>(a.s.cut ? nan : t == 0.f ? 0.f : v.y / t);
+            store_out<T>(p, a, u.head, u.row_tile * ROWS + q, 2 * lane, D, v, total[q]);
         }
     }
 }
 
-constexpr int kAttnCtas = 152 * 3;  // the most pieces (three CTAs an SM)
+constexpr int kAttnCtas = 152 * 4;  // the most pieces (four CTAs an SM)
 
 size_t kv8_attention_workspace(int64_t, int64_t, int64_t D) {
-    return static_cast<size_t>(kAttnCtas) * 2 * kAttnRows * static_cast<size_t>(D + 2) * sizeof(float);
+    return static_cast<size_t>(kAttnCtas) * 2 * 16 * static_cast<size_t>(D + 2) * sizeof(float);
 }
 
-template <class T, int D>
+// The cache's codes as pages * heads blocks of `page` rows of D bytes, boxes of 16 or 32 rows.
+template <int D>
+static int code_map(CUtensorMap* map, const int8_t* codes, const Kv8Cache& c) {
+    constexpr int W = D < 128 ? D : 128;
+    return make_tmap_3d_bytes(map, codes, D, 1 << c.page_log2, static_cast<int64_t>(c.pages) * c.heads, W,
+                              c.page_log2 > 4 ? 32 : 16, W == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B);
+}
+
+template <class T, int D, int NB>
 static int launch_attention(AttnParams p, int dev, cudaStream_t s) {
     struct Tag;
-    int rc = raise_smem<Tag>(k_kv8_attention<T, D>);
+    int rc = raise_smem<Tag>(k_kv8_attention<T, D, NB>);
     if (rc) return rc;
-    const int per_sm = D == 256 ? 1 : 3;
-    p.ctas = num_sms(dev) * per_sm;
+    CUtensorMap k, v;
+    rc = code_map<D>(&k, p.c.kq, p.c);
+    if (!rc) rc = code_map<D>(&v, p.c.vq, p.c);
+    if (rc) return rc;
+    p.ctas = num_sms(dev) * AttnCfg<D, NB>::PER_SM;
     if (p.ctas > kAttnCtas) p.ctas = kAttnCtas;
-    rc = launch_serialized(k_kv8_attention<T, D>, dim3(static_cast<unsigned>(p.ctas)), kAttnThreads, AttnCfg<D>::SMEM, 1,
-                           s, p);
+    rc = launch_serialized(k_kv8_attention<T, D, NB>, dim3(static_cast<unsigned>(p.ctas)), kAttnThreads,
+                           AttnCfg<D, NB>::SMEM, 1, s, k, v, p);
     if (rc || p.ctas == 1) return rc;
-    return launch_serialized(k_kv8_attention_join<T, D>, dim3(static_cast<unsigned>(p.ctas - 1)), kJoinThreads, 0, 1, s,
-                             p);
+    return launch_serialized(k_kv8_attention_join<T, D, NB>, dim3(static_cast<unsigned>(p.ctas - 1)), kJoinThreads, 0, 1,
+                             s, p);
+}
+
+// 8 rows a unit where that is all that a sequence has of a key head on average.
+template <class T, int D>
+static int attention_by_rows(const AttnParams& p, int dev, cudaStream_t s) {
+    const int64_t rows = (static_cast<int64_t>(p.bt.rows) + p.bt.B - 1) / p.bt.B * p.group;
+    return rows <= 8 ? launch_attention<T, D, 1>(p, dev, s) : launch_attention<T, D, 2>(p, dev, s);
 }
 
 template <class T>
 static int attention_by_size(const AttnParams& p, int dev, cudaStream_t s) {
-    if (p.c.D == 64) return launch_attention<T, 64>(p, dev, s);
-    if (p.c.D == 128) return launch_attention<T, 128>(p, dev, s);
-    return launch_attention<T, 256>(p, dev, s);
+    if (p.c.D == 64) return attention_by_rows<T, 64>(p, dev, s);
+    if (p.c.D == 128) return attention_by_rows<T, 128>(p, dev, s);
+    return attention_by_rows<T, 256>(p, dev, s);
 }
 
-#define QG_ATTN_BUDGETS(T, NAME, D, PER)                                                                          \
-    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention<" NAME "," #D ">", (reinterpret_cast<const void*>(k_kv8_attention<T, D>)), \
-                           kAttnThreads, AttnCfg<D>::SMEM, 0, 1, PER);                                            \
-    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_join<" NAME "," #D ">",                                               \
-                           (reinterpret_cast<const void*>(k_kv8_attention_join<T, D>)), kJoinThreads, 0, 0, 1, 1)
-QG_ATTN_BUDGETS(__half, "f16", 64, 3);
-QG_ATTN_BUDGETS(__half, "f16", 128, 3);
-QG_ATTN_BUDGETS(__half, "f16", 256, 1);
-QG_ATTN_BUDGETS(__nv_bfloat16, "bf16", 64, 3);
-QG_ATTN_BUDGETS(__nv_bfloat16, "bf16", 128, 3);
-QG_ATTN_BUDGETS(__nv_bfloat16, "bf16", 256, 1);
+#define QG_ATTN_BUDGETS_NB(T, NAME, D, NB)                                                                           \
+    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention<" NAME "," #D "," #NB ">",                                               \
+                           (reinterpret_cast<const void*>(k_kv8_attention<T, D, NB>)), kAttnThreads,                 \
+                           (AttnCfg<D, NB>::SMEM), 0, 1, (AttnCfg<D, NB>::PER_SM));                                  \
+    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_join<" NAME "," #D "," #NB ">",                                          \
+                           (reinterpret_cast<const void*>(k_kv8_attention_join<T, D, NB>)), kJoinThreads, 0, 0, 1, 1)
+#define QG_ATTN_BUDGETS(T, NAME, D)    \
+    QG_ATTN_BUDGETS_NB(T, NAME, D, 1); \
+    QG_ATTN_BUDGETS_NB(T, NAME, D, 2)
+QG_ATTN_BUDGETS(__half, "f16", 64);
+QG_ATTN_BUDGETS(__half, "f16", 128);
+QG_ATTN_BUDGETS(__half, "f16", 256);
+QG_ATTN_BUDGETS(__nv_bfloat16, "bf16", 64);
+QG_ATTN_BUDGETS(__nv_bfloat16, "bf16", 128);
+QG_ATTN_BUDGETS(__nv_bfloat16, "bf16", 256);
 
 }  // namespace qg
 
@@ -605,9 +777,12 @@ extern "C" int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads
     kv8_params(a, &p.c, &p.bt);
     p.Q = Q; p.ldq = ldq; p.O = O; p.ldo = ldo;
     p.causal = causal != 0;
+    p.q_vec = reinterpret_cast<uintptr_t>(Q) % 8 == 0 && ldq % 4 == 0;
     p.group = static_cast<int>(q_heads / heads);
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.part = static_cast<float*>(ws);
+    p.ctl = host_ctl(dev);
+    if (!p.ctl.status) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return dtype == QG_F16 ? attention_by_size<__half>(p, dev, s) : attention_by_size<__nv_bfloat16>(p, dev, s);
 }
