@@ -1,0 +1,52 @@
+// Pieces that both kernels of the attention over the 8-bit cache use.
+#pragma once
+#include "kv8_common.cuh"
+
+namespace qg {
+
+constexpr float kLazy = 8.f;  // log2 of how far a row's running maximum may lag behind
+
+struct AttnParams {
+    Kv8Cache c;
+    Kv8Batch bt;
+    const void* Q;
+    int64_t ldq;
+    bool causal;
+    int q_align;        // 16 or 8 where all heads of Q start at such addresses, else 2
+    int group;          // query heads a key head
+    float scale_log2;   // scale * log2(e)
+    void* O;
+    int64_t ldo;
+    float* part;        // 2 partial sums a CTA: rows x (D + 2)
+    int ctas;
+    Ctl ctl;
+};
+
+// The kernel for many rows (qg_kv8_rows.cu), and whether it takes a problem.
+bool attention_takes_rows(const AttnParams& p);
+int attention_rows(int dtype, const AttnParams& p, cudaStream_t s);
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
+
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
+    return e;
+}
+
+// 2^14 .. 2^15 over a row's largest magnitude (as bits), a power of two, and 1 over it.
+struct RowPower {
+    float up, down;
+};
+__device__ __forceinline__ RowPower row_power(uint32_t amax_bits) {
+    int e = 268 - static_cast<int>(amax_bits >> 23);
+    e = min(e, 253);
+    return {__uint_as_float(static_cast<uint32_t>(e) << 23), __uint_as_float(static_cast<uint32_t>(254 - e) << 23)};
+}
+
+}  // namespace qg

@@ -12,7 +12,7 @@
 // is exact for bf16 too but for values 2^-28 of the row's largest.
 #include <cuda.h>
 
-#include "kv8_common.cuh"
+#include "kv8_attn.cuh"
 #include "kv8_host.h"
 #include "qg_gemm_host.h"
 
@@ -35,30 +35,7 @@ constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnStep = 32;                       // tokens of a warp's step
 constexpr int kAttnTile = kAttnStep * kAttnWarps;
 constexpr int kAttnStages = 2;
-constexpr float kLazy = 8.f;  // log2 of how far M may lag behind
 constexpr int kSiteAttnK = 411, kSiteAttnV = 412;
-
-struct AttnParams {
-    Kv8Cache c;
-    Kv8Batch bt;
-    const void* Q;
-    int64_t ldq;
-    bool causal, q_vec;  // q_vec: heads start at multiples of 8 bytes
-    int group;          // query heads a key head
-    float scale_log2;   // scale * log2(e)
-    void* O;
-    int64_t ldo;
-    float* part;        // 2 partial sums a CTA: rows x (D + 2)
-    int ctas;
-    Ctl ctl;
-};
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 
 // Box of 16 or 32 tokens of a page and head, 128 bytes (or D) of each.  Issued by a whole
 // warp under an elected lane's predicate, which keeps its operands in uniform registers.
@@ -70,11 +47,6 @@ __device__ __forceinline__ void load_box(uint32_t dst, const CUtensorMap* map, i
         "[%5];\n}" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(d), "r"(token), "r"(unit), "r"(bar), "r"(elected)
         : "memory");
-}
-__device__ __forceinline__ uint32_t elect_lane() {
-    uint32_t e;
-    asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(e));
-    return e;
 }
 // An 8 x 8 matrix of 16-bit values, two a lane (row lane / 4), transposed.
 __device__ __forceinline__ uint32_t transposed(uint32_t v) {
@@ -142,16 +114,6 @@ struct AttnCfg {
         return t * W + ((chunk ^ (W == 128 ? t & 7 : (t >> 1) & 3)) << 4);
     }
 };
-
-// 2^14 .. 2^15 over a row's largest magnitude (as bits), a power of two, and 1 over it.
-struct RowPower {
-    float up, down;
-};
-__device__ __forceinline__ RowPower row_power(uint32_t amax_bits) {
-    int e = 268 - static_cast<int>(amax_bits >> 23);
-    e = min(e, 253);
-    return {__uint_as_float(static_cast<uint32_t>(e) << 23), __uint_as_float(static_cast<uint32_t>(254 - e) << 23)};
-}
 
 // Two values of a row of the result: 0 for a row that sees nothing, NaN for a sequence
 // that is longer than its table.
@@ -300,7 +262,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
                 raw[k] = make_uint2(0u, 0u);
                 const T* at_k = q + (k / 4) * 64 + (k % 4) * 4;
                 if (row < a.rows) {
-                    if (p.q_vec) {
+                    if (p.q_align >= 8) {
                         raw[k] = *reinterpret_cast<const uint2*>(at_k);
                     } else {
                         const uint16_t* h = reinterpret_cast<const uint16_t*>(at_k);
@@ -777,12 +739,14 @@ extern "C" int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads
     kv8_params(a, &p.c, &p.bt);
     p.Q = Q; p.ldq = ldq; p.O = O; p.ldo = ldo;
     p.causal = causal != 0;
-    p.q_vec = reinterpret_cast<uintptr_t>(Q) % 8 == 0 && ldq % 4 == 0;
+    const uintptr_t places = reinterpret_cast<uintptr_t>(Q) | static_cast<uintptr_t>(2 * ldq);
+    p.q_align = places % 16 == 0 ? 16 : places % 8 == 0 ? 8 : 2;
     p.group = static_cast<int>(q_heads / heads);
     p.scale_log2 = scale * 1.44269504088896340736f;
     p.part = static_cast<float*>(ws);
     p.ctl = host_ctl(dev);
     if (!p.ctl.status) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (attention_takes_rows(p)) return attention_rows(dtype, p, s);
     return dtype == QG_F16 ? attention_by_size<__half>(p, dev, s) : attention_by_size<__nv_bfloat16>(p, dev, s);
 }
