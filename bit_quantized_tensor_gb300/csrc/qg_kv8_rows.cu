@@ -19,6 +19,7 @@
 #include <cuda.h>
 
 #include "kv8_attn.cuh"
+#include "norm_common.cuh"
 #include "qg_gemm_host.h"
 
 namespace qg {
@@ -78,6 +79,12 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[
         : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // Units of a sequence: key heads times pairs of row tiles.
 __device__ __forceinline__ int64_t rows_units(const AttnParams& p, int b) {
@@ -224,27 +231,37 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             tc_fence_after();
             const int left = sees - step * TILE;  // of the step's tokens
             const bool whole = __all_sync(0xffffffffu, left >= TILE);
+            // loops over 32 tokens are not unrolled: the roles' code has to stay in the instruction cache
             float top = neg_inf();
+            if (whole) {
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t x[32];
+                    tmem_ld_32x32b_x32(s_at + 32 * ch, x);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t x[32];
-                tmem_ld_32x32b_x32(s_at + 32 * ch, x);
-                tmem_wait_ld();
+                    for (int h = 0; h < 2; ++h) {
+                        float m0 = __uint_as_float(x[16 * h]), m1 = __uint_as_float(x[16 * h + 1]);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float c = factor * __shfl_sync(0xffffffffu, now.sk, 2 * ch + h);
-                    const float l = __shfl_sync(0xffffffffu, now.lsv, 2 * ch + h);
-                    float m = neg_inf();
-                    if (whole) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) m = fmaxf(m, __uint_as_float(x[16 * h + i]));
-                        top = fmaxf(top, fmaf(m, c, l));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (32 * ch + 16 * h + i < left) m = fmaxf(m, fmaf(__uint_as_float(x[16 * h + i]), c, l));
-                        top = fmaxf(top, m);
+                        for (int i = 2; i < 14; i += 4) {
+                            m0 = max3(m0, __uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + i + 1]));
+                            m1 = max3(m1, __uint_as_float(x[16 * h + i + 2]), __uint_as_float(x[16 * h + i + 3]));
+                        }
+                        m0 = max3(m0, __uint_as_float(x[16 * h + 14]), __uint_as_float(x[16 * h + 15]));
+                        const float c = factor * __shfl_sync(0xffffffffu, now.sk, 2 * ch + h);
+                        top = fmaxf(top, fmaf(fmaxf(m0, m1), c, __shfl_sync(0xffffffffu, now.lsv, 2 * ch + h)));
                     }
+                }
+            } else {
+#pragma unroll 1
+                for (int b = 0; b < 8; ++b) {
+                    uint32_t x[16];
+                    tmem_ld_32x32b_x16(s_at + 16 * b, x);
+                    tmem_wait_ld();
+                    const float c = factor * __shfl_sync(0xffffffffu, now.sk, b), l = __shfl_sync(0xffffffffu, now.lsv, b);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (16 * b + i < left) top = fmaxf(top, fmaf(__uint_as_float(x[i]), c, l));
                 }
             }
             // O is at rest: this step's scores were issued behind the last step's product with V
@@ -266,35 +283,42 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                 }
             }
             const float base = M == neg_inf() ? 0.f : M;
+            auto weights = [&](auto all) {
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    uint32_t x[32], w[16];
+                    tmem_ld_32x32b_x32(s_at + 32 * ch, x);
+                    tmem_wait_ld();
 #pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-                uint32_t x[32], w[16];
-                tmem_ld_32x32b_x32(s_at + 32 * ch, x);
-                tmem_wait_ld();
+                    for (int h = 0; h < 2; ++h) {
+                        const float c = factor * __shfl_sync(0xffffffffu, now.sk, 2 * ch + h);
+                        const float l = __shfl_sync(0xffffffffu, now.lsv, 2 * ch + h) - base;
+                        const float isv = __shfl_sync(0xffffffffu, now.isv, 2 * ch + h);
+                        const uint64_t cc = two(c, c), ll = two(l, l);
+                        uint64_t sum = two(0.f, 0.f);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float c = factor * __shfl_sync(0xffffffffu, now.sk, 2 * ch + h);
-                    const float l = __shfl_sync(0xffffffffu, now.lsv, 2 * ch + h) - base;
-                    const float isv = __shfl_sync(0xffffffffu, now.isv, 2 * ch + h);
-                    float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        float e0 = fmaf(__uint_as_float(x[16 * h + i]), c, l);
-                        float e1 = fmaf(__uint_as_float(x[16 * h + i + 1]), c, l);
-                        if (!whole) {
-                            if (32 * ch + 16 * h + i >= left) e0 = neg_inf();
-                            if (32 * ch + 16 * h + i + 1 >= left) e1 = neg_inf();
+                        for (int i = 0; i < 8; ++i) {
+                            const int k = 16 * h + 2 * i;
+                            float2 e = both(fma_two(two(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cc, ll));
+                            if constexpr (!decltype(all)::value) {
+                                if (32 * ch + k >= left) e.x = neg_inf();
+                                if (32 * ch + k + 1 >= left) e.y = neg_inf();
+                            }
+                            e.x = exp2_fast(e.x);
+                            e.y = exp2_fast(e.y);
+                            sum = add_two(sum, two(e.x, e.y));
+                            w[8 * h + i] = pack2<__half>(e.x, e.y);
                         }
-                        e0 = exp2_fast(e0);
-                        e1 = exp2_fast(e1);
-                        sum0 += e0;
-                        sum1 += e1;
-                        w[8 * h + i / 2] = pack2<__half>(e0, e1);
+                        const float2 s2 = both(sum);
+                        if (!(s2.x + s2.y == 0.f)) den = fmaf(s2.x + s2.y, isv, den);  // not 0 times a NaN not seen
                     }
-                    if (!(sum0 + sum1 == 0.f)) den = fmaf(sum0 + sum1, isv, den);  // not 0 times a NaN not seen
+                    tmem_st_x16(s_at + 16 * ch, w);  // over scores that have been read
                 }
-                tmem_st_x16(s_at + 16 * ch, w);  // over scores that have been read
-            }
+            };
+            if (whole)
+                weights(std::true_type{});
+            else
+                weights(std::false_type{});
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
