@@ -9,13 +9,17 @@
 // sequence and key head, against its tokens 128 at a time:
 //   warps 0-3   softmax of tile 0, thread = row (its lane of tensor memory)
 //   warps 4-7   softmax of tile 1
-//   warps 8-11  codes of K and V from the cache through registers to fp16 in shared memory
+//   warps 8-11  codes of K and V to fp16 in shared memory
 //   warp 12     MMA issuer, owner of the tensor memory
 // S (128 x 128 fp32) of either tile lies in tensor memory, its weights (fp16) over its first half,
 // from where they are the A operand of the product with V; O (128 x D fp32) beside it.  One
 // tile's products run while the other's weights are made.  Both K and V lie in shared memory as
 // tokens by 64 values (128-byte swizzle), which is K's K-major and V's MN-major form, so they are
 // converted alike.  A row's sums are rescaled, in tensor memory, only when its maximum grows by 2^8.
+//
+// The chain scores -> weights -> product of a tile is what a step takes, so a softmax thread keeps
+// half of its 128 scores between the maximum and the weights and has the next ones on their way
+// while it works.
 #include <cuda.h>
 
 #include "kv8_attn.cuh"
@@ -24,10 +28,11 @@
 
 namespace qg {
 
-constexpr int kRowsThreads = 13 * 32;
+constexpr int kRowsSoftmaxWarps = 8, kRowsCodeWarps = 4, kRowsMmaWarp = 12;
+constexpr int kRowsThreads = 32 * (kRowsMmaWarp + 1);
 constexpr int kRowsTile = 128;   // rows of a tile, tokens of a step
 constexpr int kSiteRowsK = 421, kSiteRowsV = 422, kSiteRowsS = 423, kSiteRowsP = 424, kSiteRowsPv = 425,
-              kSiteRowsFree = 426, kSiteRowsQ = 427, kSiteRowsDrain = 428;
+              kSiteRowsFree = 426, kSiteRowsQ = 427, kSiteRowsDrain = 428, kSiteRowsRaw = 429;
 
 template <int D>
 struct RowsCfg {
@@ -35,9 +40,11 @@ struct RowsCfg {
     static constexpr int TILE_BYTES = 128 * 2 * D;         // 128 rows of fp16
     static constexpr int STAGES = 2;                       // of K and of V
     static constexpr int RING = 2 * TILE_BYTES;            // after the two tiles of Q
-    static constexpr int BARS = RING + 2 * STAGES * TILE_BYTES;
+    static constexpr int RAW = RING + 2 * STAGES * TILE_BYTES;
+    static constexpr int RAW_SLOTS = 2, RAW_BYTES = 32 * D;   // a warp's 32 tokens of K or V on their way
+    static constexpr int BARS = RAW + kRowsCodeWarps * RAW_SLOTS * RAW_BYTES;
     // at least half an SM's, so that no two CTAs meet on one (each takes all tensor memory)
-    static constexpr int SMEM = BARS + 256 + 1024 > 117760 ? BARS + 256 + 1024 : 117760;
+    static constexpr int SMEM = BARS + 512 + 1024 > 117760 ? BARS + 512 + 1024 : 117760;
     static constexpr uint32_t O_COL = 256;                 // S of tile t at 128 t, O at 256 + D t
     static constexpr uint32_t IDESC_S = make_idesc(0, 0, 128, 128);
     static constexpr uint32_t IDESC_O = make_idesc(0, 0, 128, D) | (1u << 16);  // B is MN-major
@@ -100,6 +107,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                      ~static_cast<uintptr_t>(1023));
     __shared__ int64_t mem[kRowsThreads / 32 + 2];
+    // a step's 8 blocks' sk and log2 sv, and the next step's, for each softmax warp
+    __shared__ float2 scales[kRowsSoftmaxWarps][2][8];
     uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + Cfg::BARS);
     const uint32_t bar0 = smem_u32(bars), smem0 = smem_u32(smem);
     auto k_full = [&](int s) { return bar0 + 8u * s; };
@@ -116,23 +125,25 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(k_full(i), 4);
+            mbar_init(k_full(i), kRowsCodeWarps);
             mbar_init(k_free(i), 1);
-            mbar_init(v_full(i), 4);
+            mbar_init(v_full(i), kRowsCodeWarps);
             mbar_init(v_free(i), 1);
             mbar_init(s_full(i), 1);
             mbar_init(p_full(i), 4);
             mbar_init(pv_done(i), 1);
         }
-        mbar_init(q_full, 8);
+        mbar_init(q_full, kRowsSoftmaxWarps);
         mbar_init(drain, 1);
+        for (int i = 0; i < kRowsCodeWarps * Cfg::RAW_SLOTS; ++i) mbar_init(bar0 + 144u + 8u * i, 1);
         *abort_flag = 0;
         fence_mbar_init();
     }
     pdl_wait_prior_grid();
+    fence_proxy_async_global();  // the cache may have been written just before, with ordinary stores
     const Kv8Place at = kv8_find<kRowsThreads>(p.bt.B, blockIdx.x, 0, mem, [&](int b) { return rows_units(p, b); });
     if (at.b >= p.bt.B) return;  // more CTAs than units; no tensor memory is held yet
-    if (warp == 12) tmem_alloc(smem_u32(tmem_holder), 512);
+    if (warp == kRowsMmaWarp) tmem_alloc(smem_u32(tmem_holder), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -167,9 +178,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     };
     const float nan = __uint_as_float(0x7fc00000u);
 
-    if (warp < 8) {
+    if (warp < kRowsSoftmaxWarps) {
         // ------------------------------------------------ queries, softmax, result of a row
-        const int t = warp >> 2, r = threadIdx.x & (TILE - 1), row = row0 + t * TILE + r;
+        const int t = warp >> 2, r = (warp & 3) * 32 + lane, row = row0 + t * TILE + r;
         const uint32_t quad = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t s_at = quad + 128u * t, o_at = quad + Cfg::O_COL + D * t;
         float factor = 0.f;
@@ -178,7 +189,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             const T* q = static_cast<const T*>(p.Q) + (seq.row0 + row / p.group) * p.ldq +
                          (head * p.group + row % p.group) * D;
             uint32_t bits = 0;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < D / 8; ++i) {
                 float f[8];
                 load_some<T, 8>(q + 8 * i, in ? 8 : 0, p.q_align == 16, f);
@@ -190,7 +201,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             const float up = p.scale_log2 < 0.f ? -power.up : power.up;
             factor = power.down * fabsf(p.scale_log2);
             uint8_t* const to = smem + t * Cfg::TILE_BYTES + r * 128;
-#pragma unroll 4
+#pragma unroll 8
             for (int i = 0; i < D / 8; ++i) {
                 float f[8];
                 load_some<T, 8>(q + 8 * i, in ? 8 : 0, p.q_align == 16, f);
@@ -205,65 +216,82 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             if (lane == 0) mbar_arrive(q_full);
         }
         const int sees = seen_by(row), mine = steps[t];
-        // scales of a step's 8 blocks, one a lane, read a step ahead
-        struct Scales {
-            float sk, lsv, isv;
+        // scales of a step's 8 blocks, one a lane: the page three steps ahead, its scales two, what
+        // they come to one, so that no load is waited for
+        auto page_of = [&](int step) {
+            const int block = 8 * step + lane, col = (16 * block) >> page_log2;
+            return lane < 8 && step < mine && 16 * block < tokens && col < p.c.table_cols
+                       ? p.c.table[static_cast<int64_t>(at.b) * p.c.table_cols + col]
+                       : -1;
         };
-        auto fetch = [&](int step) {
-            Scales v = {nan, nan, nan};
-            const int unit = lane < 8 && step < mine ? unit_of(8 * step + lane) : -1;
-            if (unit >= 0) {
-                const float sv = p.c.vs[unit];
-                v = {p.c.ks[unit], __log2f(sv), __fdividef(1.f, sv)};
-            }
-            return v;
+        auto scales_of = [&](int page) {
+            const int unit = page * heads + head;
+            return page >= 0 && page < p.c.pages ? make_float2(p.c.ks[unit], p.c.vs[unit]) : make_float2(nan, nan);
         };
-        Scales next = fetch(0);
+        auto keep = [&](int step, float2 v) {
+            if (lane < 8) scales[warp][step & 1][lane] = make_float2(v.x, __log2f(v.y));
+            __syncwarp();
+        };
+        keep(0, scales_of(page_of(0)));
+        float2 raw = scales_of(page_of(1));
+        int page = page_of(2);
         float M = neg_inf(), den = 0.f;
         bool ok = true;
         for (int step = 0; step < mine; ++step) {
-            const Scales now = next;
-            next = fetch(step + 1);
+            keep(step + 1, raw);
+            raw = scales_of(page);
+            page = page_of(step + 3);
+            const float2* const sc = scales[warp][step & 1];
+            const int left = sees - step * TILE;  // of the step's tokens
+            const bool whole = __all_sync(0xffffffffu, left >= TILE);
             if (!__all_sync(0xffffffffu, bounded_wait(s_full(t), step & 1, abort_flag, p.ctl, kSiteRowsS))) {
                 ok = false;
                 break;
             }
             tc_fence_after();
-            const int left = sees - step * TILE;  // of the step's tokens
-            const bool whole = __all_sync(0xffffffffu, left >= TILE);
-            // loops over 32 tokens are not unrolled: the roles' code has to stay in the instruction cache
+            // scores 32 at a time; the last two quarters first, and again for their weights
+            uint32_t xa[32], xb[32];
             float top = neg_inf();
-            if (whole) {
-#pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t x[32];
-                    tmem_ld_32x32b_x32(s_at + 32 * ch, x);
-                    tmem_wait_ld();
+            auto maximum = [&](auto all, const uint32_t(&v)[32], int ch) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float m0 = __uint_as_float(x[16 * h]), m1 = __uint_as_float(x[16 * h + 1]);
+                for (int h = 0; h < 2; ++h) {
+                    const int b = 2 * ch + h, o = 16 * h;
+                    const float2 sl = sc[b];
+                    const float c = factor * sl.x;
+                    if constexpr (decltype(all)::value) {
+                        float m[4];
 #pragma unroll
-                        for (int i = 2; i < 14; i += 4) {
-                            m0 = max3(m0, __uint_as_float(x[16 * h + i]), __uint_as_float(x[16 * h + i + 1]));
-                            m1 = max3(m1, __uint_as_float(x[16 * h + i + 2]), __uint_as_float(x[16 * h + i + 3]));
-                        }
-                        m0 = max3(m0, __uint_as_float(x[16 * h + 14]), __uint_as_float(x[16 * h + 15]));
-                        const float c = factor * __shfl_sync(0xffffffffu, now.sk, 2 * ch + h);
-                        top = fmaxf(top, fmaf(fmaxf(m0, m1), c, __shfl_sync(0xffffffffu, now.lsv, 2 * ch + h)));
+                        for (int i = 0; i < 4; ++i)
+                            m[i] = max3(__uint_as_float(v[o + 3 * i]), __uint_as_float(v[o + 3 * i + 1]),
+                                        __uint_as_float(v[o + 3 * i + 2]));
+                        const float m4 = max3(__uint_as_float(v[o + 12]), __uint_as_float(v[o + 13]),
+                                              __uint_as_float(v[o + 14]));
+                        m[0] = max3(m[0], m[1], __uint_as_float(v[o + 15]));
+                        m[2] = max3(m[2], m[3], m4);
+                        top = fmaxf(top, fmaf(fmaxf(m[0], m[2]), c, sl.y));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (16 * b + i < left) top = fmaxf(top, fmaf(__uint_as_float(v[o + i]), c, sl.y));
                     }
                 }
-            } else {
-#pragma unroll 1
-                for (int b = 0; b < 8; ++b) {
-                    uint32_t x[16];
-                    tmem_ld_32x32b_x16(s_at + 16 * b, x);
-                    tmem_wait_ld();
-                    const float c = factor * __shfl_sync(0xffffffffu, now.sk, b), l = __shfl_sync(0xffffffffu, now.lsv, b);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (16 * b + i < left) top = fmaxf(top, fmaf(__uint_as_float(x[i]), c, l));
-                }
-            }
+            };
+            auto maxima = [&](auto all) {
+                tmem_ld_32x32b_x32(s_at + 64, xa);
+                tmem_ld_32x32b_x32(s_at + 96, xb);
+                tmem_wait_ld();
+                maximum(all, xa, 2);
+                tmem_ld_32x32b_x32(s_at, xa);
+                maximum(all, xb, 3);
+                tmem_ld_32x32b_x32(s_at + 32, xb);
+                tmem_wait_ld();
+                maximum(all, xa, 0);
+                maximum(all, xb, 1);
+            };
+            if (whole)
+                maxima(std::true_type{});
+            else
+                maxima(std::false_type{});
             // O is at rest: this step's scores were issued behind the last step's product with V
             if (__any_sync(0xffffffffu, top > M + kLazy)) {
                 const float m = fmaxf(M, top);
@@ -273,52 +301,57 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                 if (step) {
 #pragma unroll 1
                     for (int d = 0; d < D; d += 16) {
-                        uint32_t x[16];
-                        tmem_ld_32x32b_x16(o_at + d, x);
+                        uint32_t y[16];
+                        tmem_ld_32x32b_x16(o_at + d, y);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                        tmem_st_x16(o_at + d, x);
+                        for (int i = 0; i < 16; ++i) y[i] = __float_as_uint(__uint_as_float(y[i]) * f);
+                        tmem_st_x16(o_at + d, y);
                     }
                 }
             }
             const float base = M == neg_inf() ? 0.f : M;
-            auto weights = [&](auto all) {
-#pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    uint32_t x[32], w[16];
-                    tmem_ld_32x32b_x32(s_at + 32 * ch, x);
-                    tmem_wait_ld();
+            auto weights = [&](auto all, const uint32_t(&x)[32], int ch) {
+                uint32_t w[16];
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float c = factor * __shfl_sync(0xffffffffu, now.sk, 2 * ch + h);
-                        const float l = __shfl_sync(0xffffffffu, now.lsv, 2 * ch + h) - base;
-                        const float isv = __shfl_sync(0xffffffffu, now.isv, 2 * ch + h);
-                        const uint64_t cc = two(c, c), ll = two(l, l);
-                        uint64_t sum = two(0.f, 0.f);
+                for (int h = 0; h < 2; ++h) {
+                    const int b = 2 * ch + h;
+                    const float2 sl = sc[b];
+                    const float c = factor * sl.x, l = sl.y - base, isv = exp2_fast(-sl.y);  // 1 / sv
+                    const uint64_t cc = two(c, c), ll = two(l, l);
+                    uint64_t sum = two(0.f, 0.f);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int k = 16 * h + 2 * i;
-                            float2 e = both(fma_two(two(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cc, ll));
-                            if constexpr (!decltype(all)::value) {
-                                if (32 * ch + k >= left) e.x = neg_inf();
-                                if (32 * ch + k + 1 >= left) e.y = neg_inf();
-                            }
-                            e.x = exp2_fast(e.x);
-                            e.y = exp2_fast(e.y);
-                            sum = add_two(sum, two(e.x, e.y));
-                            w[8 * h + i] = pack2<__half>(e.x, e.y);
+                    for (int i = 0; i < 8; ++i) {
+                        const int k = 16 * h + 2 * i;
+                        float2 e = both(fma_two(two(__uint_as_float(x[k]), __uint_as_float(x[k + 1])), cc, ll));
+                        if constexpr (!decltype(all)::value) {
+                            if (32 * ch + k >= left) e.x = neg_inf();
+                            if (32 * ch + k + 1 >= left) e.y = neg_inf();
                         }
-                        const float2 s2 = both(sum);
-                        if (!(s2.x + s2.y == 0.f)) den = fmaf(s2.x + s2.y, isv, den);  // not 0 times a NaN not seen
+                        e.x = exp2_fast(e.x);
+                        e.y = exp2_fast(e.y);
+                        sum = add_two(sum, two(e.x, e.y));
+                        w[8 * h + i] = pack2<__half>(e.x, e.y);
                     }
-                    tmem_st_x16(s_at + 16 * ch, w);  // over scores that have been read
+                    const float2 s2 = both(sum);
+                    if (!(s2.x + s2.y == 0.f)) den = fmaf(s2.x + s2.y, isv, den);  // not 0 times a NaN not seen
                 }
+                tmem_st_x16(s_at + 16 * ch, w);  // over scores that have been read
+            };
+            auto all_weights = [&](auto all) {
+                weights(all, xa, 0);
+                tmem_ld_32x32b_x32(s_at + 64, xa);
+                weights(all, xb, 1);
+                tmem_wait_ld();
+                tmem_ld_32x32b_x32(s_at + 96, xb);
+                weights(all, xa, 2);
+                tmem_wait_ld();
+                weights(all, xb, 3);
             };
             if (whole)
-                weights(std::true_type{});
+                all_weights(std::true_type{});
             else
-                weights(std::false_type{});
+                all_weights(std::false_type{});
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -333,15 +366,15 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             const float scale = den == 0.f ? 0.f : 1.f / den;
 #pragma unroll 1
             for (int d = 0; d < D; d += 16) {
-                uint32_t x[16];
+                uint32_t y[16];
                 float f[16];
                 if (mine) {
-                    tmem_ld_32x32b_x16(o_at + d, x);
+                    tmem_ld_32x32b_x16(o_at + d, y);
                     tmem_wait_ld();
                 }
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
-                    f[i] = seq.cut ? nan : !mine || den == 0.f ? 0.f : __uint_as_float(x[i]) * scale;
+                    f[i] = seq.cut ? nan : !mine || den == 0.f ? 0.f : __uint_as_float(y[i]) * scale;
                 if (row < all_rows) {
                     if (sectors)
                         store_sectors<T>(out + d, f);
@@ -351,37 +384,73 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             }
         }
         tc_fence_before();
-    } else if (warp < 12) {
+    } else if (warp < kRowsMmaWarp) {
         // ------------------------------------------------ codes to fp16
-        constexpr int CH = D / 16, PASS = 128 / CH;  // 16-byte pieces of a token; tokens a pass
-        const int tid = threadIdx.x - 256, chunk = tid % CH, tok0 = tid / CH;
-        int unit = lane < 8 ? unit_of(lane) : -1, unit_next = -1;
-        uint4 raw[CH];
-        // pieces of K or V of a step into registers; zeros where there is no token
-        auto load = [&](int step, int units, const int8_t* codes) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int tok = tok0 + i * PASS;
-                const int at_unit = __shfl_sync(0xffffffffu, units, tok >> 4);
-                raw[i] = make_uint4(0, 0, 0, 0);
-                if (at_unit >= 0) {
-                    const int offset = (step * TILE + tok) & ((1 << page_log2) - 1);
-                    raw[i] = *reinterpret_cast<const uint4*>(
-                        codes + ((static_cast<int64_t>(at_unit) << page_log2) + offset) * D + 16 * chunk);
-                }
-            }
+        // A warp takes 32 of a step's 128 tokens, of K and then of V.  Their bytes, 16 tokens in one
+        // piece, come by bulk copies a step ahead into a ring of the warp's own; a pass ends in a
+        // proxy fence, so it has to be a long one (16 tokens a pass: 1450 cycles each).
+        constexpr int CH = D / 16, PASS = 32 / CH, N = 32 / PASS;  // 16-byte pieces of a token; tokens a pass; passes
+        constexpr int SLOTS = Cfg::RAW_SLOTS;
+        const uint32_t elected = elect_lane();
+        const int chunk = lane % CH, tok0 = lane / CH, w = warp - kRowsSoftmaxWarps;
+        const uint8_t* const raw = smem + Cfg::RAW + w * SLOTS * Cfg::RAW_BYTES;
+        const uint32_t raw_u32 = smem_u32(raw);
+        auto raw_full = [&](int slot) { return bar0 + 144u + 8u * (w * SLOTS + slot); };
+        // page * heads + head of the warp's two blocks of 16 steps, one a lane
+        auto fetch = [&](int step) {
+            step += lane >> 1;
+            return step < most ? unit_of(8 * step + 2 * w + (lane & 1)) : -1;
         };
-        auto store = [&](uint32_t stage_at) {
-            uint8_t* const to = smem + stage_at + (chunk >> 2) * 16384;
-            const int odd = (chunk >> 2) & 1;  // the second columns' lanes store their halves in turn, not to meet in a bank
+        int now = fetch(0), next = fetch(16);
+        // K (slot 0) or V (slot 1) of a step; only blocks that hold tokens
+        auto copy = [&](int step, int units, int slot) {
+            if (step >= most) return;
+            const int u0 = __shfl_sync(0xffffffffu, units, 2 * (step & 15));
+            const int u1 = __shfl_sync(0xffffffffu, units, 2 * (step & 15) + 1);
+            const uint32_t bytes = (u0 >= 0 ? Cfg::RAW_BYTES / 2 : 0) + (u1 >= 0 ? Cfg::RAW_BYTES / 2 : 0);
+            if (elected) {
+                const int8_t* codes = slot ? p.c.vq : p.c.kq;
+                const int token = step * TILE + 32 * w, mask = (1 << page_log2) - 1;
+                mbar_arrive_expect_tx(raw_full(slot), bytes);
+                const uint32_t to = raw_u32 + slot * Cfg::RAW_BYTES;
+                if (u0 >= 0)
+                    bulk_copy_g2s(to, codes + ((static_cast<int64_t>(u0) << page_log2) + (token & mask)) * D,
+                                  Cfg::RAW_BYTES / 2, raw_full(slot));
+                if (u1 >= 0)
+                    bulk_copy_g2s(to + Cfg::RAW_BYTES / 2,
+                                  codes + ((static_cast<int64_t>(u1) << page_log2) + ((token + 16) & mask)) * D,
+                                  Cfg::RAW_BYTES / 2, raw_full(slot));
+            }
+            __syncwarp();
+        };
+        auto convert = [&](int step, int slot, int ahead) {
+            const int s = step & 1;
+            const bool in0 = __shfl_sync(0xffffffffu, now, 2 * (step & 15)) >= 0;
+            const bool in1 = __shfl_sync(0xffffffffu, now, 2 * (step & 15) + 1) >= 0;
+            if (!__all_sync(0xffffffffu, bounded_wait(raw_full(slot), step & 1, abort_flag, p.ctl, kSiteRowsRaw)))
+                return false;
+            uint4 from[N];
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-                const int tok = tok0 + i * PASS, c0 = 2 * (chunk & 3);
+            for (int j = 0; j < N; ++j) {
+                from[j] = *reinterpret_cast<const uint4*>(raw + slot * Cfg::RAW_BYTES + (tok0 + j * PASS) * D + 16 * chunk);
+                if (!(j < N / 2 ? in0 : in1)) from[j] = make_uint4(0, 0, 0, 0);  // zeros where there is no token
+            }
+            __syncwarp();  // all have read the slot
+            copy(step + 1, ahead, slot);
+            if (!__all_sync(0xffffffffu, bounded_wait(slot ? v_free(s) : k_free(s), ((step >> 1) & 1) ^ 1, abort_flag, p.ctl,
+                                                      kSiteRowsFree)))
+                return false;
+            uint8_t* const to = smem + Cfg::RING + (2 * slot + s) * Cfg::TILE_BYTES + (chunk >> 2) * 16384 + w * 4096;
+            const int odd = (chunk >> 2) & 1;  // the second columns' lanes store their halves in turn, not to meet in a bank
+            const int c0 = 2 * (chunk & 3);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const int tok = tok0 + j * PASS;
                 uint32_t h[8];
-                s8_to_f16(raw[i].x, h[0], h[1]);
-                s8_to_f16(raw[i].y, h[2], h[3]);
-                s8_to_f16(raw[i].z, h[4], h[5]);
-                s8_to_f16(raw[i].w, h[6], h[7]);
+                s8_to_f16(from[j].x, h[0], h[1]);
+                s8_to_f16(from[j].y, h[2], h[3]);
+                s8_to_f16(from[j].z, h[4], h[5]);
+                s8_to_f16(from[j].w, h[6], h[7]);
                 const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
                 uint8_t* const at_row = to + tok * 128;
                 *reinterpret_cast<uint4*>(at_row + (((c0 + odd) ^ (tok & 7)) << 4)) = odd ? b : a;
@@ -389,21 +458,25 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             }
             fence_proxy_async_smem();
             __syncwarp();
+            if (elected) mbar_arrive(slot ? v_full(s) : k_full(s));
+            return true;
         };
-        if (most) load(0, unit, p.c.kq);
-        for (int step = 0; step < most; ++step) {
-            const int s = step & 1;
-            const uint32_t parity = ((step >> 1) & 1) ^ 1;
-            if (lane < 8) unit_next = unit_of(8 * (step + 1) + lane);
-            if (!__all_sync(0xffffffffu, bounded_wait(k_free(s), parity, abort_flag, p.ctl, kSiteRowsFree))) break;
-            store(Cfg::RING + s * Cfg::TILE_BYTES);
-            if (lane == 0) mbar_arrive(k_full(s));
-            load(step, unit, p.c.vq);
-            if (!__all_sync(0xffffffffu, bounded_wait(v_free(s), parity, abort_flag, p.ctl, kSiteRowsFree))) break;
-            store(Cfg::RING + (2 + s) * Cfg::TILE_BYTES);
-            if (lane == 0) mbar_arrive(v_full(s));
-            unit = unit_next;
-            if (step + 1 < most) load(step + 1, unit, p.c.kq);
+        copy(0, now, 0);
+        copy(0, now, 1);
+        bool ok = true;
+        for (int step = 0; ok && step < most; ++step) {
+            const int ahead = (step & 15) == 15 ? next : now;  // units of step + 1
+            ok = convert(step, 0, ahead) && convert(step, 1, ahead);
+            if ((step & 15) == 15) {
+                now = next;
+                next = fetch(step + 17);
+            }
+        }
+        if (!ok && elected) {
+            // copies may still be in flight: give them a fixed time to land
+            const uint64_t start = global_timer_ns();
+            while (global_timer_ns() - start < 1000000) {
+            }
         }
     } else {
         // ------------------------------------------------ MMA issuer
@@ -469,7 +542,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         tc_fence_before();
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kRowsMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
