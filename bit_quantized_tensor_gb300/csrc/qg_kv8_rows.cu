@@ -93,10 +93,65 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// Units of a sequence: key heads times pairs of row tiles.
-__device__ __forceinline__ int64_t rows_units(const AttnParams& p, int b) {
+// Units of a sequence: key heads times pairs of row tiles, of which those of the last rows see
+// most.  How many take at least `steps` steps of 128 tokens:
+__device__ __forceinline__ int64_t rows_units(const AttnParams& p, int b, int steps) {
     const Kv8Seq s = kv8_seq(p.bt, p.c, b);
-    return static_cast<int64_t>(p.c.heads) * ((static_cast<int64_t>(s.n) * p.group + 2 * kRowsTile - 1) / (2 * kRowsTile));
+    const int64_t rows = static_cast<int64_t>(s.n) * p.group, pairs = (rows + 2 * kRowsTile - 1) / (2 * kRowsTile);
+    int64_t from = 0;  // first pair of tiles
+    if (steps > 0) {
+        const int64_t tokens = static_cast<int64_t>(steps - 1) * kRowsTile;  // to see more than these
+        if (s.len <= tokens) return 0;
+        if (p.causal) {
+            const int64_t row = (tokens - s.first) * p.group;  // the first row that does
+            if (row >= rows) return 0;
+            from = row > 0 ? row / (2 * kRowsTile) : 0;
+        }
+    }
+    return p.c.heads * (pairs - from);
+}
+__device__ __forceinline__ int64_t rows_sum(int64_t v, int64_t* mem) {
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) v += __shfl_xor_sync(0xffffffffu, v, o);
+    __syncthreads();  // `mem` may still be read
+    if ((threadIdx.x & 31) == 0) mem[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kRowsThreads / 32; ++w) v += mem[w];
+    return v;
+}
+// The u-th longest unit: its sequence, which of those of its length, and its steps; b = B
+// without one.  Long units first leaves the SMs done together: 4 prompts of 1392 to 2048 tokens
+// over 3058 to 8192 take 251 steps where their own order took 285 (245: all alike).
+struct RowsPlace {
+    int b, steps;
+    int64_t at;
+};
+__device__ __forceinline__ RowsPlace rows_find(const AttnParams& p, int64_t u, int64_t* mem) {
+    auto at_least = [&](int steps) {
+        int64_t mine = 0;
+        for (int b = threadIdx.x; b < p.bt.B; b += kRowsThreads) mine += rows_units(p, b, steps);
+        return rows_sum(mine, mem);
+    };
+    if (at_least(0) <= u) return {p.bt.B, 0, 0};
+    // the most steps that more than u units take at least
+    int lo = 0, hi = static_cast<int>(((static_cast<int64_t>(p.c.table_cols) << p.c.page_log2) + kRowsTile - 1) / kRowsTile) + 1;
+    int64_t longer = 0;  // units of more steps than `lo`
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        const int64_t n = at_least(mid);
+        if (n > u) {
+            lo = mid;
+        } else {
+            hi = mid;
+            longer = n;
+        }
+    }
+    const Kv8Place at = kv8_find<kRowsThreads>(p.bt.B, u - longer, 0, mem, [&](int b) {
+        return rows_units(p, b, lo) - rows_units(p, b, lo + 1);
+    });
+    return {at.b, lo, at.at};
 }
 
 template <class T, int D>
@@ -141,7 +196,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     }
     pdl_wait_prior_grid();
     fence_proxy_async_global();  // the cache may have been written just before, with ordinary stores
-    const Kv8Place at = kv8_find<kRowsThreads>(p.bt.B, blockIdx.x, 0, mem, [&](int b) { return rows_units(p, b); });
+    const RowsPlace at = rows_find(p, blockIdx.x, mem);
     if (at.b >= p.bt.B) return;  // more CTAs than units; no tensor memory is held yet
     if (warp == kRowsMmaWarp) tmem_alloc(smem_u32(tmem_holder), 512);
     tc_fence_before();
@@ -151,11 +206,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     pdl_launch_dependents();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
 
-    // the unit: the last rows, which see most, come first
+    // the unit: among its sequence's of this length, which are consecutive pairs of tiles
     const Kv8Seq seq = kv8_seq(p.bt, p.c, at.b);
     const int heads = p.c.heads, all_rows = seq.n * p.group;
     const int head = static_cast<int>(at.at % heads);
-    const int row0 = ((all_rows + 2 * TILE - 1) / (2 * TILE) - 1 - static_cast<int>(at.at / heads)) * 2 * TILE;
+    const int pairs = (all_rows + 2 * TILE - 1) / (2 * TILE);
+    const int longer = static_cast<int>(rows_units(p, at.b, at.steps + 1) / heads);
+    const int row0 = (pairs - 1 - longer - static_cast<int>(at.at / heads)) * 2 * TILE;
     auto seen_by = [&](int row) {
         const int64_t n = p.causal ? seq.first + row / p.group + 1 : seq.len;
         return row >= all_rows || n < 0 ? 0 : n < seq.len ? static_cast<int>(n) : seq.len;
