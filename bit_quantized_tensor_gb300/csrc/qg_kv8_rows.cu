@@ -25,6 +25,7 @@
 #include "kv8_attn.cuh"
 #include "norm_common.cuh"
 #include "qg_gemm_host.h"
+#include "tc_issue.cuh"
 
 namespace qg {
 
@@ -52,21 +53,6 @@ struct RowsCfg {
     static_assert(2 * SMEM > 233472, "one CTA an SM");
 };
 
-// Shared-memory descriptors: 128-byte swizzle, 1024 bytes between groups of 8 rows; the low word
-// has the address and, MN-major, the distance of the next 64 columns.
-constexpr uint32_t kTileHi = (1024u >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ uint32_t tile_lo(uint32_t addr, uint32_t next) {
-    return ((addr & 0x3FFFFu) >> 4) | ((next >> 4) << 16);
-}
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t elected) {
-    asm volatile(
-        "{\n.reg .pred p, q;\n.reg .b64 da, db;\nsetp.ne.b32 p, %4, 0;\nsetp.ne.b32 q, %5, 0;\n"
-        "mov.b64 da, {%1, %6};\nmov.b64 db, {%2, %6};\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d),
-        "r"(alo), "r"(blo), "r"(idesc), "r"(accumulate), "r"(elected), "r"(kTileHi)
-        : "memory");
-}
 // A from tensor memory.
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t blo, uint32_t idesc, uint32_t accumulate,
                                        uint32_t elected) {

@@ -7,6 +7,7 @@
 
 #include "qg_gemm_host.h"
 #include "s8_common.cuh"
+#include "s8_gemm.cuh"
 
 namespace qg {
 
@@ -298,11 +299,35 @@ static int launch_gemv(const GemvParams& p, cudaStream_t s) {
     return rc ? rc : launch_serialized(k_s8_gemv<T, 2, QUANT>, grid, kGemvThreads, smem, 1, s, p);
 }
 
+// ------------------------------------------------------------ which kernel
+
+// Up to here the weights are turned into fp16 on the SM; with more tokens that is done once, in
+// memory, for the tiles of CTA pairs.
+constexpr int64_t kS8SomeTokens = 1024;
+
+// A tile holds all tokens up to 128.  Its accumulators hold 1024 values of K each, so there is a
+// most that a CTA can take.
+static int some_tile(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
+static int64_t some_most_k(int64_t M) { return int64_t(512) / some_tile(M) * 1024 - kS8Bk; }
+static bool takes_some(int64_t M, int64_t K) { return M <= kS8SomeTokens && K <= 8 * some_most_k(M); }
+
+// CTAs of a cluster that share K: more while SMs are left without work and each keeps at least 256
+// values of it, and as many as its accumulators ask for.
+static int some_splits(int64_t M, int64_t N, int64_t K, int dev) {
+    const int tile = some_tile(M);
+    const int64_t tiles = (N + 127) / 128 * ((M + tile - 1) / tile);
+    int splits = 1;
+    while (splits < 8 && 2 * splits * tiles <= num_sms(dev) && K >= 512 * splits) splits *= 2;
+    while (K > splits * some_most_k(M)) splits *= 2;
+    return splits;
+}
+
 // ------------------------------------------------------------ workspaces and calls
 
 static size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// fp16 forms of both operands, and the tokens' scales.
+// fp16 forms of the tokens and, where they are turned into fp16 in memory, of the weights; the
+// tokens' scales.
 struct S8Workspace {
     size_t a, b, sa, total;
 };
@@ -311,7 +336,7 @@ static S8Workspace s8_workspace(int64_t M, int64_t N, int64_t K) {
     S8Workspace w;
     w.a = 0;
     w.b = up256(2 * ld * static_cast<size_t>(M));
-    w.sa = w.b + up256(2 * ld * static_cast<size_t>(N));
+    w.sa = w.b + (takes_some(M, K) ? 0 : up256(2 * ld * static_cast<size_t>(N)));
     w.total = w.sa + up256(4 * static_cast<size_t>(M));
     return w;
 }
@@ -369,6 +394,44 @@ static int tensor_product(int dtype, int64_t M, int64_t N, int64_t K, const __ha
     e.dtype = dtype;
     return run_gemm_s8_scaled(A, B, M, N, K, s8_codes_ld(K), Y, ldy, e, ctl, s);
 }
+
+// ------------------------------------------------------------ some tokens
+
+template <int NT>
+static int launch_some(const int8_t* W, const __half* X, const S8Params& p, int splits, cudaStream_t s) {
+    using Cfg = S8Cfg<NT>;
+    struct Tag;
+    int rc = raise_smem<Tag>(s8_gemm_kernel<Cfg>);
+    if (rc) return rc;
+    const int64_t ld = s8_codes_ld(p.K);
+    CUtensorMap tw, tx;
+    rc = make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K, p.N, ld, kS8Bk, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (!rc) rc = make_tmap_kmajor(&tx, true, X, p.K, p.M, 2 * ld, kS8Bk, NT);
+    if (rc) return rc;
+    return launch_serialized(s8_gemm_kernel<Cfg>,
+                             dim3(static_cast<unsigned>((p.N + 127) / 128 * splits), static_cast<unsigned>((p.M + NT - 1) / NT)),
+                             kS8Threads, Cfg::SMEM, splits, s, tw, tx, p);
+}
+
+static int some_product(int dtype, int dev, int64_t M, int64_t N, int64_t K, const __half* A, const float* sa,
+                        const int8_t* W, const float* sb, const void* bias, void* Y, int64_t ldy, const Ctl& ctl,
+                        cudaStream_t s) {
+    S8Params p = {};
+    p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K);
+    const int splits = some_splits(M, N, K, dev), tile = some_tile(M);
+    while ((1 << p.log_splits) < splits) ++p.log_splits;
+    p.sa = sa; p.sb = sb; p.bias = bias; p.Y = Y; p.ldy = ldy; p.dtype = dtype; p.ctl = ctl;
+    if (tile == 32) return launch_some<32>(W, A, p, splits, s);
+    if (tile == 64) return launch_some<64>(W, A, p, splits, s);
+    return launch_some<128>(W, A, p, splits, s);
+}
+
+#define QG_S8_SOME(NT)                                                                                              \
+    QG_BLOCK_KERNEL_BUDGET("s8_gemm_kernel<" #NT ">", (reinterpret_cast<const void*>(s8_gemm_kernel<S8Cfg<NT>>)),   \
+                           kS8Threads, S8Cfg<NT>::SMEM, 512, 8, 1)
+QG_S8_SOME(32);
+QG_S8_SOME(64);
+QG_S8_SOME(128);
 
 #define QG_S8_QUANT(T, NAME, OUT, ONAME, TPR, LONG)                                                  \
     QG_BLOCK_KERNEL_BUDGET("k_s8_quantize<" NAME "," ONAME "," #TPR "," #LONG ">",                   \
@@ -445,6 +508,7 @@ int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const 
     uint8_t* base = static_cast<uint8_t*>(ws);
     __half *a = reinterpret_cast<__half*>(base + w.a), *b = reinterpret_cast<__half*>(base + w.b);
     rc = s8_to_f16_rows(Aq, M, ld, a, ld, dev, s);
+    if (!rc && takes_some(M, K)) return some_product(dtype, dev, M, N, K, a, As, Bq, Bs, bias, Y, ldy, ctl, s);
     if (!rc) rc = s8_to_f16_rows(Bq, N, ld, b, ld, dev, s);
     return rc ? rc : tensor_product(dtype, M, N, K, a, As, b, Bs, bias, Y, ldy, ctl, s);
 }
@@ -480,6 +544,7 @@ int s8_linear(int dtype, int64_t M, int64_t N, int64_t K, const void* X, int64_t
     __half *a = reinterpret_cast<__half*>(base + w.a), *b = reinterpret_cast<__half*>(base + w.b);
     float* sa = reinterpret_cast<float*>(base + w.sa);
     rc = by_dtype(dtype, [&](auto t) { return launch_quantize<decltype(t), __half>(M, K, X, ldx, a, sa, s); });
+    if (!rc && takes_some(M, K)) return some_product(dtype, dev, M, N, K, a, sa, Wq, Ws, bias, Y, ldy, ctl, s);
     if (!rc) rc = s8_to_f16_rows(Wq, N, ld, b, ld, dev, s);
     return rc ? rc : tensor_product(dtype, M, N, K, a, sa, b, Ws, bias, Y, ldy, ctl, s);
 }

@@ -20,7 +20,8 @@ def test_sizes(L):
     assert [L.qg_s8_codes_ld(k) for k in (-3, 0, 1, 16, 17, 4096)] == [0, 0, 16, 16, 32, 4096]
     ws = L.qg_workspace_size
     assert ws(qg.QG_OP_S8_LINEAR, 1, 4096, 4096) == 0  # quantized inside the product
-    assert ws(qg.QG_OP_S8_LINEAR, 100, 50, 33) >= 150 * 48 * 2
+    assert ws(qg.QG_OP_S8_LINEAR, 100, 50, 33) >= 100 * 48 * 2 + 100 * 4      # the tokens as fp16
+    assert ws(qg.QG_OP_S8_LINEAR, 5000, 50, 33) >= 5050 * 48 * 2 + 5000 * 4   # and the weights
     assert ws(qg.QG_OP_QK_NORM_ROPE_BACKWARD, 1, 1, 128) > 0
     assert ws(qg.QG_OP_KV8_ATTENTION, 4, 8, 128) > 0
 
