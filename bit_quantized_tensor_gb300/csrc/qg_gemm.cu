@@ -475,7 +475,8 @@ int run_gemm_s8_converted(const __half* A16, const __half* B16, int64_t M, int64
 
 int run_gemm_s8_scaled(const __half* A16, const __half* B16, int64_t M, int64_t N, int64_t K, int64_t ld, void* Y,
                        int64_t ldy, const S8Scales& e, const Ctl& ctl, cudaStream_t stream) {
-    return launch_gemm<MmaKind::F16, Epi::S8>(A16, ld * 2, B16, ld * 2, M, N, K, Y, ldy, g_s8_chunk_kb.load(), nullptr,
+    // the weights are the product's rows, the tokens its columns
+    return launch_gemm<MmaKind::F16, Epi::S8>(B16, ld * 2, A16, ld * 2, N, M, K, Y, ldy, g_s8_chunk_kb.load(), nullptr,
                                               ctl, stream, e);
 }
 

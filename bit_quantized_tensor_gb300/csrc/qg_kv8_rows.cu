@@ -533,19 +533,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         };
         // scores of tile t of a step: S = Q K^T
         auto scores = [&](int t, int step) {
-            const uint32_t q = smem0 + t * Cfg::TILE_BYTES, k = smem0 + Cfg::RING + (step & 1) * Cfg::TILE_BYTES;
+            // descriptors as sums of 32-bit words: anything else is done in vector registers and moved
+            const uint32_t q = tile_lo(smem0, 16) + t * (Cfg::TILE_BYTES / 16);
+            const uint32_t k = tile_lo(smem0 + Cfg::RING, 16) + (step & 1) * (Cfg::TILE_BYTES / 16);
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                const uint32_t at_k = (i >> 2) * 16384u + (i & 3) * 32u;
-                mma_ss(tmem + 128u * t, tile_lo(q + at_k, 16), tile_lo(k + at_k, 16), Cfg::IDESC_S, i > 0, elected);
+                const uint32_t at_k = (i >> 2) * 1024u + (i & 3) * 2u;
+                mma_ss(tmem + 128u * t, q + at_k, k + at_k, Cfg::IDESC_S, i > 0, elected);
             }
             commit(s_full(t));
         };
         auto values = [&](int t, int step) {
-            const uint32_t v = smem0 + Cfg::RING + (2 + (step & 1)) * Cfg::TILE_BYTES;
+            const uint32_t v = tile_lo(smem0 + Cfg::RING + 2 * Cfg::TILE_BYTES, 16384) + (step & 1) * (Cfg::TILE_BYTES / 16);
 #pragma unroll
             for (int i = 0; i < TILE / 16; ++i)
-                mma_ts(tmem + Cfg::O_COL + D * t, tmem + 128u * t + 8u * i, tile_lo(v + 2048u * i, 16384), Cfg::IDESC_O,
+                mma_ts(tmem + Cfg::O_COL + D * t, tmem + 128u * t + 8u * i, v + 128u * i, Cfg::IDESC_O,
                        step > 0 || i > 0, elected);
             commit(pv_done(t));
         };

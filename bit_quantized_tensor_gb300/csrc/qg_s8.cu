@@ -13,11 +13,10 @@ namespace qg {
 
 // ------------------------------------------------------------ quantizer
 
-// One row a group of TPR threads, up to 32 values a thread in registers; LONG: any
-// length, read twice.  OUT: int8_t (packed operand) or __half (the codes as fp16
-// numbers, the tensor cores' operand).  Bound by the bytes it reads and writes.
-constexpr int kQuantChunks = 4;
-
+// One row a group of TPR threads, CHUNKS pieces of 8 values a thread in registers; LONG: any
+// length, read twice.  OUT: int8_t (packed operand) or __half (the codes as fp16 numbers, the
+// tensor cores' operand).  Bound by the bytes it reads and writes, so few threads hold a row and
+// many rows are under way.
 template <class OUT>
 __device__ __forceinline__ void store_codes(OUT* dst, const float (&x)[8], float r) {
     int q[8];
@@ -33,10 +32,12 @@ __device__ __forceinline__ void store_codes(OUT* dst, const float (&x)[8], float
     }
 }
 
-template <class T, class OUT, int TPR, bool LONG>
+template <class T, class OUT, int TPR, int CHUNKS>  // CHUNKS 0: LONG
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     k_s8_quantize(int M, int K, const void* X, int64_t ldx, bool aligned, OUT* Q, int ldq, float* S) {
     constexpr int GROUPS = TPR < 128 ? 128 / TPR : 1;
+    constexpr bool LONG = CHUNKS == 0;
+    constexpr int C = LONG ? 1 : CHUNKS;
     __shared__ uint32_t red[32];
     pdl_wait_prior_grid();
     pdl_launch_dependents();
@@ -46,7 +47,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     const T* x = static_cast<const T*>(X) + row * ldx;
     OUT* q = Q + row * ldq;
     uint32_t amax = 0;
-    float v[kQuantChunks][8];
+    float v[C][8];
     if constexpr (LONG) {
         for (int k = 8 * t; k < K; k += 8 * TPR) {
             load_some<T, 8>(x + k, K - k, aligned, v[0]);
@@ -55,12 +56,12 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < kQuantChunks; ++c) {
+        for (int c = 0; c < C; ++c) {
             const int k = 8 * (t + c * TPR);
             if (k < K) load_some<T, 8>(x + k, K - k, aligned, v[c]);
         }
 #pragma unroll
-        for (int c = 0; c < kQuantChunks; ++c) {
+        for (int c = 0; c < C; ++c) {
             if (8 * (t + c * TPR) < K) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[c][i]));
@@ -82,7 +83,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
         }
     } else {
 #pragma unroll
-        for (int c = 0; c < kQuantChunks; ++c) {
+        for (int c = 0; c < C; ++c) {
             const int k = 8 * (t + c * TPR);
             if (k >= ldq) break;
             if (k >= K) {  // the row's padding: one piece of 8 at most
@@ -99,17 +100,14 @@ static int launch_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, OUT
     const bool aligned = aligned16(X) && (M == 1 || ldx * sizeof(T) % 16 == 0);
     const int m = static_cast<int>(M), k = static_cast<int>(K), ldq = static_cast<int>(s8_codes_ld(K));
     const unsigned rows = static_cast<unsigned>(M);
-    if (ldq <= 32 * 8 * kQuantChunks)
-        return launch_serialized(k_s8_quantize<T, OUT, 32, false>, dim3((rows + 3) / 4), 128, 0, 1, s, m, k, X, ldx,
-                                 aligned, Q, ldq, S);
-    if (ldq <= 128 * 8 * kQuantChunks)
-        return launch_serialized(k_s8_quantize<T, OUT, 128, false>, dim3(rows), 128, 0, 1, s, m, k, X, ldx, aligned, Q,
-                                 ldq, S);
-    if (ldq <= 512 * 8 * kQuantChunks)
-        return launch_serialized(k_s8_quantize<T, OUT, 512, false>, dim3(rows), 512, 0, 1, s, m, k, X, ldx, aligned, Q,
-                                 ldq, S);
-    return launch_serialized(k_s8_quantize<T, OUT, 512, true>, dim3(rows), 512, 0, 1, s, m, k, X, ldx, aligned, Q, ldq,
-                             S);
+    auto launch = [&](auto kernel, unsigned grid, int threads) {
+        return launch_serialized(kernel, dim3(grid), threads, 0, 1, s, m, k, X, ldx, aligned, Q, ldq, S);
+    };
+    if (ldq <= 32 * 8 * 4) return launch(k_s8_quantize<T, OUT, 32, 4>, (rows + 3) / 4, 128);
+    if (ldq <= 128 * 8 * 4) return launch(k_s8_quantize<T, OUT, 128, 4>, rows, 128);
+    if (ldq <= 128 * 8 * 8) return launch(k_s8_quantize<T, OUT, 128, 8>, rows, 128);
+    if (ldq <= 512 * 8 * 4) return launch(k_s8_quantize<T, OUT, 512, 4>, rows, 512);
+    return launch(k_s8_quantize<T, OUT, 512, 0>, rows, 512);
 }
 
 // ------------------------------------------------------------ few tokens
@@ -305,21 +303,38 @@ static int launch_gemv(const GemvParams& p, cudaStream_t s) {
 // memory, for the tiles of CTA pairs.
 constexpr int64_t kS8SomeTokens = 1024;
 
-// A tile holds all tokens up to 128.  Its accumulators hold 1024 values of K each, so there is a
-// most that a CTA can take.
-static int some_tile(int64_t M) { return M <= 32 ? 32 : M <= 64 ? 64 : 128; }
-static int64_t some_most_k(int64_t M) { return int64_t(512) / some_tile(M) * 1024 - kS8Bk; }
-static bool takes_some(int64_t M, int64_t K) { return M <= kS8SomeTokens && K <= 8 * some_most_k(M); }
+// Tokens a tile (32, 64, 128) and CTAs of a cluster that share K.
+struct SomeForm {
+    int tile, splits;
+};
 
-// CTAs of a cluster that share K: more while SMs are left without work and each keeps at least 256
-// values of it, and as many as its accumulators ask for.
-static int some_splits(int64_t M, int64_t N, int64_t K, int dev) {
-    const int tile = some_tile(M);
-    const int64_t tiles = (N + 127) / 128 * ((M + tile - 1) / tile);
-    int splits = 1;
-    while (splits < 8 && 2 * splits * tiles <= num_sms(dev) && K >= 512 * splits) splits *= 2;
-    while (K > splits * some_most_k(M)) splits *= 2;
-    return splits;
+// A CTA's accumulators hold 1024 values of K each.
+static bool some_holds(const SomeForm& f, int64_t K) {
+    const int64_t stages = (K + kS8Bk - 1) / kS8Bk;
+    return (stages + f.splits - 1) / f.splits <= 512 / f.tile * kS8Exact;
+}
+static bool takes_some(int64_t M, int64_t K) { return M <= kS8SomeTokens && some_holds(SomeForm{32, 8}, K); }
+
+// The form with the least estimated time, in cycles of an SM, as measured: a CTA's start, its
+// stages (bound by turning codes into fp16, with 128 tokens by the MMA as much), its epilogue and
+// the exchange of sums; whole rounds of CTAs.
+static SomeForm some_form(int64_t M, int64_t N, int64_t K, int sms) {
+    SomeForm best = {32, 8};
+    int64_t least = INT64_MAX;
+    for (int tile = 32; tile <= 128; tile *= 2) {
+        if (tile > 32 && tile >= 2 * M) break;
+        const int64_t tiles = (N + 127) / 128 * ((M + tile - 1) / tile);
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            const SomeForm f = {tile, splits};
+            if (!some_holds(f, K) || (splits > 1 && K < 256 * splits)) continue;
+            const int64_t stages = ((K + kS8Bk - 1) / kS8Bk + splits - 1) / splits;
+            const int64_t cta = 4500 + stages * (tile == 128 ? 620 : 520) + 1200 + 20 * tile +
+                                (splits > 1 ? 2500 + 32 * tile : 0);
+            const int64_t time = (tiles * splits + sms - 1) / sms * cta;
+            if (time < least) least = time, best = f;
+        }
+    }
+    return best;
 }
 
 // ------------------------------------------------------------ workspaces and calls
@@ -406,7 +421,7 @@ static int launch_some(const int8_t* W, const __half* X, const S8Params& p, int 
     const int64_t ld = s8_codes_ld(p.K);
     CUtensorMap tw, tx;
     rc = make_tmap_2d(&tw, CU_TENSOR_MAP_DATA_TYPE_UINT8, W, p.K, p.N, ld, kS8Bk, 128, CU_TENSOR_MAP_SWIZZLE_NONE);
-    if (!rc) rc = make_tmap_kmajor(&tx, true, X, p.K, p.M, 2 * ld, kS8Bk, NT);
+    if (!rc) rc = make_tmap_kmajor(&tx, true, X, p.K, p.M, 2 * ld, 64, NT);
     if (rc) return rc;
     return launch_serialized(s8_gemm_kernel<Cfg>,
                              dim3(static_cast<unsigned>((p.N + 127) / 128 * splits), static_cast<unsigned>((p.M + NT - 1) / NT)),
@@ -418,12 +433,12 @@ static int some_product(int dtype, int dev, int64_t M, int64_t N, int64_t K, con
                         cudaStream_t s) {
     S8Params p = {};
     p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K);
-    const int splits = some_splits(M, N, K, dev), tile = some_tile(M);
-    while ((1 << p.log_splits) < splits) ++p.log_splits;
+    const SomeForm f = some_form(M, N, K, num_sms(dev));
+    while ((1 << p.log_splits) < f.splits) ++p.log_splits;
     p.sa = sa; p.sb = sb; p.bias = bias; p.Y = Y; p.ldy = ldy; p.dtype = dtype; p.ctl = ctl;
-    if (tile == 32) return launch_some<32>(W, A, p, splits, s);
-    if (tile == 64) return launch_some<64>(W, A, p, splits, s);
-    return launch_some<128>(W, A, p, splits, s);
+    if (f.tile == 32) return launch_some<32>(W, A, p, f.splits, s);
+    if (f.tile == 64) return launch_some<64>(W, A, p, f.splits, s);
+    return launch_some<128>(W, A, p, f.splits, s);
 }
 
 #define QG_S8_SOME(NT)                                                                                              \
@@ -433,15 +448,16 @@ QG_S8_SOME(32);
 QG_S8_SOME(64);
 QG_S8_SOME(128);
 
-#define QG_S8_QUANT(T, NAME, OUT, ONAME, TPR, LONG)                                                  \
-    QG_BLOCK_KERNEL_BUDGET("k_s8_quantize<" NAME "," ONAME "," #TPR "," #LONG ">",                   \
-                           (reinterpret_cast<const void*>(k_s8_quantize<T, OUT, TPR, LONG>)),        \
+#define QG_S8_QUANT(T, NAME, OUT, ONAME, TPR, CHUNKS)                                                \
+    QG_BLOCK_KERNEL_BUDGET("k_s8_quantize<" NAME "," ONAME "," #TPR "," #CHUNKS ">",                 \
+                           (reinterpret_cast<const void*>(k_s8_quantize<T, OUT, TPR, CHUNKS>)),      \
                            TPR < 128 ? 128 : TPR, 0, 0, 1, 1)
 #define QG_S8_QUANT_SIZES(T, NAME, OUT, ONAME)  \
-    QG_S8_QUANT(T, NAME, OUT, ONAME, 32, false);  \
-    QG_S8_QUANT(T, NAME, OUT, ONAME, 128, false); \
-    QG_S8_QUANT(T, NAME, OUT, ONAME, 512, false); \
-    QG_S8_QUANT(T, NAME, OUT, ONAME, 512, true)
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 32, 4);    \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 128, 4);   \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 128, 8);   \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 512, 4);   \
+    QG_S8_QUANT(T, NAME, OUT, ONAME, 512, 0)
 #define QG_S8_GEMV(T, NAME, MB, QUANT)                                                            \
     QG_BLOCK_KERNEL_BUDGET("k_s8_gemv<" NAME "," #MB "," #QUANT ">",                              \
                            (reinterpret_cast<const void*>(k_s8_gemv<T, MB, QUANT>)), kGemvThreads, \

@@ -2,11 +2,12 @@
 // up to the SM and become fp16 in shared memory.
 //
 // The 128 rows of the MMA are weight rows and its NT columns tokens.  A cluster of S CTAs splits
-// K.  Per stage of 64 values of K
-//   warp 16     TMA producer: 128 x 64 codes, NT x 64 fp16 codes of the tokens
-//   warps 0-15  four groups, a group every fourth stage: codes to fp16 in the MMA's layout (a pass
-//               is bound by its latency, fence and barrier included, so four are under way)
+// K.  Per stage of 128 values of K
+//   warp 16     TMA producer: 128 x 128 codes, NT x 128 fp16 codes of the tokens
+//   warps 0-15  two groups, a group every second stage: codes to fp16 in the MMA's layout (a pass is
+//               bound by its latency, fence and barrier included, so two are under way)
 //   warp 17     MMA issuer, owner of the tensor memory
+// (Stages of 64 values, with boxes of 64-byte rows, took 1300 cycles each where the MMA takes 256.)
 // Every 1024 values of K have an accumulator of their own, whose fp32 sums are whole numbers of
 // at most 2^24; they are added up as 32-bit integers, over the accumulators and over the cluster
 // (each CTA sends a token's sums to the CTA that owns the token).  Lanes are weight rows in the
@@ -18,9 +19,9 @@
 
 namespace qg {
 
-constexpr int kS8CodeWarps = 16, kS8Groups = 4, kS8GroupWarps = kS8CodeWarps / kS8Groups;
+constexpr int kS8CodeWarps = 16, kS8Groups = 2, kS8GroupWarps = kS8CodeWarps / kS8Groups;
 constexpr int kS8Threads = 32 * (kS8CodeWarps + 2);
-constexpr int kS8Bk = 64;             // K of a stage: 128 bytes of fp16
+constexpr int kS8Bk = 128;              // K of a stage: 128 bytes of codes, two 128-byte columns of fp16
 constexpr int kS8Exact = 1024 / kS8Bk;  // stages of an accumulator
 
 template <int NT_>
@@ -28,19 +29,19 @@ struct S8Cfg {
     static constexpr int NT = NT_;
     static constexpr int RAW_BYTES = 128 * kS8Bk;              // weights' codes of a stage
     static constexpr int X_BYTES = NT * kS8Bk * 2;
-    static constexpr int STAGES = 4;
-    static constexpr int W_BYTES = 128 * kS8Bk * 2, SLOTS = kS8Groups;  // fp16 weights
+    static constexpr int STAGES = NT == 128 ? 3 : 4;
+    static constexpr int W_BYTES = 128 * kS8Bk * 2, SLOTS = NT == 128 ? 2 : 3;  // fp16 weights
+    static_assert(SLOTS < STAGES, "a slot's last use is told by its stage's barrier");
     static constexpr int W_AT = STAGES * (RAW_BYTES + X_BYTES);
-    static constexpr int JOIN_AT = W_AT + SLOTS * W_BYTES;     // sums from the cluster
-    static constexpr int JOIN_BYTES = NT * 128 * 4;
-    static constexpr int BARS_AT = JOIN_AT + JOIN_BYTES;
+    static constexpr int BARS_AT = W_AT + SLOTS * W_BYTES;
+    static constexpr int SUM_BYTES = NT * 128 * 4;             // after the loop: sums to send, then sums received
     static constexpr int SMEM = BARS_AT + 256 + 1024;
     static constexpr int ACCS = 512 / NT;                      // accumulators that fit
     static constexpr uint32_t IDESC = make_idesc(0, 0, 128, NT);
     static_assert(NT % 32 == 0 && NT <= 128, "MMA columns; lanes and columns of the epilogue's warps");
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(2 * SMEM > 233472, "one CTA an SM keeps all tensor memory free");
-    static_assert(NT * 128 * 4 <= W_AT, "the sums to send lie over the ring");
+    static_assert(2 * SUM_BYTES <= BARS_AT, "the sums lie over the rings");
 };
 
 struct S8Params {
@@ -57,6 +58,11 @@ struct S8Params {
 constexpr int kSiteS8Empty = 321, kSiteS8Full = 322, kSiteS8Ready = 323, kSiteS8Free = 324, kSiteS8Acc = 325,
               kSiteS8Join = 326, kSiteS8Raw = 327;
 
+// Barrier of the cluster without memory ordering: the copies carry their own completion.
+__device__ __forceinline__ void cluster_meet() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+
 template <class Cfg>
 __global__ void __launch_bounds__(kS8Threads, 1)
     s8_gemm_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX, const S8Params p) {
@@ -69,9 +75,8 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     auto full_bar = [&](int s) { return bar0 + 8u * s; };               // codes and tokens of a stage landed
     auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };    // ... and are done with
     auto ready_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };  // fp16 weights of a stage
-    auto free_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + SLOTS + b); };
-    const uint32_t acc_bar = bar0 + 8u * (2 * STAGES + 2 * SLOTS), join_bar = acc_bar + 8u;
-    uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 2 * SLOTS + 2);
+    const uint32_t acc_bar = bar0 + 8u * (2 * STAGES + SLOTS), join_bar = acc_bar + 8u;
+    uint32_t* const tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + SLOTS + 2);
     volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
     // a stage's codes, then all stages' tokens (swizzle atoms of 1 KB)
     auto raw_at = [&](int s) { return s * Cfg::RAW_BYTES; };
@@ -90,10 +95,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
         }
-        for (int b = 0; b < SLOTS; ++b) {
-            mbar_init(ready_bar(b), kS8GroupWarps);
-            mbar_init(free_bar(b), 1);
-        }
+        for (int b = 0; b < SLOTS; ++b) mbar_init(ready_bar(b), kS8GroupWarps);
         mbar_init(acc_bar, 1);
         mbar_init(join_bar, 1);
         *abort_flag = 0;
@@ -109,7 +111,6 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     tc_fence_after();
     // not before the tensor memory is held: the next kernel may take its own and then wait for this one
     pdl_launch_dependents();
-    if (splits > 1) cluster_arrive();  // this CTA runs: its shared memory may be written (awaited below)
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_holder, 0);
 
     bool ok = true;
@@ -123,7 +124,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
             if (elected) mbar_arrive_expect_tx(full_bar(ps.slot()), Cfg::RAW_BYTES + Cfg::X_BYTES);
             __syncwarp();
             fp4_load(smem0 + raw_at(ps.slot()), &tmW, kb * kS8Bk, n0, full_bar(ps.slot()), elected);
-            fp4_load(smem0 + x_at(ps.slot()), &tmX, kb * kS8Bk, m0, full_bar(ps.slot()), elected);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                fp4_load(smem0 + x_at(ps.slot()) + h * (Cfg::X_BYTES / 2), &tmX, kb * kS8Bk + 64 * h, m0,
+                         full_bar(ps.slot()), elected);
             ps.next();
         }
     } else if (warp == kS8CodeWarps + 1) {
@@ -138,16 +142,15 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 break;
             }
             tc_fence_after();
-            const uint32_t w = smem0 + Cfg::W_AT + bs.slot() * Cfg::W_BYTES, x = smem0 + x_at(ps.slot());
+            // descriptors as sums of 32-bit words: anything else is done in vector registers and moved
+            const uint32_t w = tile_lo(smem0 + Cfg::W_AT, 16) + bs.slot() * (Cfg::W_BYTES / 16);
+            const uint32_t x = tile_lo(smem0 + x_at(0), 16) + ps.slot() * (Cfg::X_BYTES / 16);
             const uint32_t d = tmem + static_cast<uint32_t>(i / kS8Exact * NT);
 #pragma unroll
             for (int k = 0; k < kS8Bk / 16; ++k)
-                mma_ss(d, tile_lo(w + 32u * k, 16), tile_lo(x + 32u * k, 16), Cfg::IDESC, i % kS8Exact > 0 || k > 0,
-                       elected);
-            if (elected) {
-                tc_commit(empty_bar(ps.slot()));
-                tc_commit(free_bar(bs.slot()));
-            }
+                mma_ss(d, w + (k >> 2) * (Cfg::W_BYTES / 32) + 2u * (k & 3), x + (k >> 2) * (Cfg::X_BYTES / 32) + 2u * (k & 3),
+                       Cfg::IDESC, i % kS8Exact > 0 || k > 0, elected);
+            if (elected) tc_commit(empty_bar(ps.slot()));  // the stage, and the slot of its weights
             __syncwarp();
             ps.next();
             bs.next();
@@ -157,7 +160,9 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     } else {
         // ------------------------------------------------ codes to fp16
         const int group = warp / kS8GroupWarps, t = threadIdx.x & (32 * kS8GroupWarps - 1);
-        const int chunk = t & 3, row = t >> 2;  // 16-byte pieces of a row's 64 codes; rows 32 apart
+        // 16-byte pieces of a row's 128 codes, rows 32 apart; the lanes of the second column of fp16
+        // store their halves in turn, not to meet in a bank
+        const int chunk = t & 7, row = t >> 3, odd = chunk >> 2, c0 = 2 * (chunk & 3);
         for (int i = group; i < count; i += kS8Groups) {
             const int s = i % STAGES, b = i % SLOTS;
             if (!warp_wait(full_bar(s), (i / STAGES) & 1, abort_flag, p.ctl, kSiteS8Raw)) break;
@@ -165,7 +170,11 @@ __global__ void __launch_bounds__(kS8Threads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
                 w[j] = *reinterpret_cast<const uint4*>(smem + raw_at(s) + (row + 32 * j) * kS8Bk + 16 * chunk);
-            if (!warp_wait(free_bar(b), ((i / SLOTS) & 1) ^ 1u, abort_flag, p.ctl, kSiteS8Free)) break;
+            // the MMA is done with the slot's last stage; that stage's barrier cannot be a round further,
+            // since it would take this stage's MMA to get there
+            if (i >= SLOTS && !warp_wait(empty_bar((i - SLOTS) % STAGES), ((i - SLOTS) / STAGES) & 1, abort_flag, p.ctl,
+                                         kSiteS8Free))
+                break;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int r = row + 32 * j;
@@ -174,9 +183,10 @@ __global__ void __launch_bounds__(kS8Threads, 1)
                 s8_to_f16(w[j].y, h[2], h[3]);
                 s8_to_f16(w[j].z, h[4], h[5]);
                 s8_to_f16(w[j].w, h[6], h[7]);
-                uint8_t* const at = smem + Cfg::W_AT + b * Cfg::W_BYTES + r * 128;
-                *reinterpret_cast<uint4*>(at + (((2 * chunk) ^ (r & 7)) << 4)) = make_uint4(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint4*>(at + (((2 * chunk + 1) ^ (r & 7)) << 4)) = make_uint4(h[4], h[5], h[6], h[7]);
+                const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
+                uint8_t* const at = smem + Cfg::W_AT + b * Cfg::W_BYTES + odd * (Cfg::W_BYTES / 2) + r * 128;
+                *reinterpret_cast<uint4*>(at + (((c0 + odd) ^ (r & 7)) << 4)) = odd ? hi : lo;
+                *reinterpret_cast<uint4*>(at + (((c0 + 1 - odd) ^ (r & 7)) << 4)) = odd ? lo : hi;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -209,23 +219,40 @@ __global__ void __launch_bounds__(kS8Threads, 1)
     };
     const bool mine = warp < kS8CodeWarps;
     const float sb = mine && n < p.N ? p.sb[n] : 0.f, bias = mine && p.bias && n < p.N ? typed_at(p.bias, p.dtype, n) : 0.f;
+    // 16 tokens' results of a lane's row; the scales are read ahead of the stores
+    auto store = [&](int c, int c1, const int (&v)[16]) {
+        float f[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = c + i < c1 ? p.sa[m0 + c + i] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = fmaf(static_cast<float>(v[i]) * f[i], sb, bias);
+        if (n >= p.N) return;
+        auto all = [&](auto* y) {
+            using Y = std::remove_pointer_t<decltype(y)>;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if (c + i < c1) y[(m0 + c + i) * p.ldy + n] = from_f32<Y>(f[i]);
+        };
+        if (p.dtype == QG_F16)
+            all(static_cast<__half*>(p.Y));
+        else if (p.dtype == QG_BF16)
+            all(static_cast<__nv_bfloat16*>(p.Y));
+        else
+            all(static_cast<float*>(p.Y));
+    };
     if (splits == 1) {
         if (mine && good) {
             for (int c = 16 * (warp >> 2); c < cols; c += 64) {
                 int v[16];
                 sums_of(c, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if (n < p.N && c + i < cols)
-                        typed_store(p.Y, p.dtype, (m0 + c + i) * p.ldy + n,
-                                    fmaf(static_cast<float>(v[i]) * p.sa[m0 + c + i], sb, bias));
+                store(c, cols, v);
             }
         }
         tc_fence_before();
         __syncthreads();
     } else {
         int* const sums = reinterpret_cast<int*>(smem);
-        const int* const join = reinterpret_cast<const int*>(smem + Cfg::JOIN_AT);
+        const int* const join = reinterpret_cast<const int*>(smem + Cfg::SUM_BYTES);
         if (mine) {
             for (int c = 16 * (warp >> 2); c < cols; c += 64) {
                 int v[16];
@@ -238,26 +265,32 @@ __global__ void __launch_bounds__(kS8Threads, 1)
         }
         tc_fence_before();
         __syncthreads();
-        cluster_wait();  // every CTA of the cluster runs and has armed its barrier
+        cluster_meet();  // every CTA of the cluster is past its loop: its rings may be written
         if (threadIdx.x < splits) {
             const int owner = threadIdx.x, count_of = min(cols - owner * per, per);
             if (count_of > 0)
-                bulk_copy_s2s_cluster(mapa_shared(smem0 + Cfg::JOIN_AT + 512u * (split * per), owner),
+                bulk_copy_s2s_cluster(mapa_shared(smem0 + Cfg::SUM_BYTES + 512u * (split * per), owner),
                                       smem0 + 512u * (owner * per), 512u * count_of, mapa_shared(join_bar, owner));
         }
         __syncwarp();
         const int c1 = min(cols, (split + 1) * per);
         if (mine && split * per < cols) {
             const bool joined = warp_wait(join_bar, 0u, nullptr, p.ctl, kSiteS8Join);
-            if (good && joined && n < p.N)
-                for (int c = split * per + (warp >> 2); c < c1; c += 4) {
-                    int v = 0;
-                    for (int s = 0; s < splits; ++s) v += join[(s * per + c - split * per) * 128 + quad * 32 + lane];
-                    typed_store(p.Y, p.dtype, (m0 + c) * p.ldy + n,
-                                fmaf(static_cast<float>(v) * p.sa[m0 + c], sb, bias));
+            if (good && joined)
+                for (int c = split * per + 16 * (warp >> 2); c < c1; c += 64) {
+                    int v[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) v[i] = 0;
+                    for (int s = 0; s < splits; ++s) {
+                        const int* from = join + (s * per + c - split * per) * 128 + quad * 32 + lane;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + i < c1) v[i] += from[i * 128];
+                    }
+                    store(c, c1, v);
                 }
         }
-        cluster_sync();  // nobody leaves while its sums may still be on their way
+        cluster_meet();  // nobody leaves while its sums may still be on their way
     }
     if (warp == kS8CodeWarps + 1) {
         __syncwarp();

@@ -23,8 +23,10 @@
 //             stay within 2^24 in magnitude (so every partial sum is an exactly
 //             representable integer); each chunk is converted to int32 and
 //             added in registers; the int32 tile is stored at the end.
-//   Epi::S8   the same sums, stored as sum * sa[row] * sb[column] + bias[column]
-//             in fp16, bf16 or fp32.
+//   Epi::S8   the same sums, scaled and stored transposed, in fp16, bf16 or fp32:
+//             Y[column][row] = sum * sa[column] * sb[row] + bias[row].  A is the
+//             weights there: the lanes of a warp hold neighbouring outputs of a
+//             token, so every store fills sectors whatever the row length is.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -230,64 +232,34 @@ __device__ __forceinline__ void store_row_s32(int32_t* dst, int col0, int N_tota
     }
 }
 
-// N columns (a multiple of 16) of a row of integer sums, scaled, in the output's type.
+// N columns of a row of integer sums, scaled, to column `row` of the output.  The kernel is
+// launched behind its inputs, so the scales may be read as constants (ahead of the stores).
 template <class T, int N>
-__device__ __forceinline__ void store_row_s8(T* dst, int col0, int N_total, const int32_t* v, float sa,
-                                             const S8Scales& e) {
-    constexpr int PER = 32 / static_cast<int>(sizeof(T));  // values of a 32-byte sector
-    const T* bias = static_cast<const T*>(e.bias);
-    auto widen = [](T x) {
-        if constexpr (sizeof(T) == 4)
-            return x;
-        else
-            return static_cast<float>(x);
-    };
+__device__ __forceinline__ void store_row_s8(T* y, int64_t ldy, int col0, int cols, const int32_t* v, const S8Scales& e,
+                                             int row) {
+    const float sb = __ldg(e.sb + row);
+    float bias = 0.f;
+    if (e.bias) bias = static_cast<float>(static_cast<const T*>(e.bias)[row]);
+    T* at = y + static_cast<int64_t>(col0) * ldy + row;
 #pragma unroll
-    for (int c = 0; c < N; c += PER) {
-        if (col0 + c >= N_total) return;
-        float f[PER];
-#pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int col = col0 + c + i;
-            f[i] = 0.f;
-            if (col < N_total)
-                f[i] = fmaf(static_cast<float>(v[c + i]) * sa, e.sb[col], bias ? widen(bias[col]) : 0.f);
-        }
-        if (col0 + c + PER <= N_total && (reinterpret_cast<uintptr_t>(dst + c) & 31u) == 0) {
-            uint32_t w[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                if constexpr (sizeof(T) == 4) {
-                    w[i] = __float_as_uint(f[i]);
-                } else {
-                    const T a = static_cast<T>(f[2 * i]), b = static_cast<T>(f[2 * i + 1]);
-                    w[i] = *reinterpret_cast<const uint16_t*>(&a) |
-                           static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(&b)) << 16;
-                }
-            }
-            st_global_32(dst + c, make_uint4(w[0], w[1], w[2], w[3]), make_uint4(w[4], w[5], w[6], w[7]), false);
-        } else {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                if (col0 + c + i < N_total) dst[c + i] = static_cast<T>(f[i]);
-        }
+    for (int c = 0; c < N; ++c) {
+        if (col0 + c < cols) *at = static_cast<T>(fmaf(static_cast<float>(v[c]) * __ldg(e.sa + col0 + c), sb, bias));
+        at += ldy;
     }
 }
 
 // A row of sums of either integer epilogue.
 template <Epi EPI, int N>
 __device__ __forceinline__ void store_row_sums(const TcGemmParams& p, int row, int col0, const int32_t* v) {
-    const int64_t at = static_cast<int64_t>(row) * p.ldc + col0;
     if constexpr (EPI == Epi::S32) {
-        store_row_s32<N>(static_cast<int32_t*>(p.C) + at, col0, p.N, v, p.l2_mode == 2);
+        store_row_s32<N>(static_cast<int32_t*>(p.C) + static_cast<int64_t>(row) * p.ldc + col0, col0, p.N, v,
+                         p.l2_mode == 2);
+    } else if (p.s8.dtype == QG_F16) {
+        store_row_s8<__half, N>(static_cast<__half*>(p.C), p.ldc, col0, p.N, v, p.s8, row);
+    } else if (p.s8.dtype == QG_BF16) {
+        store_row_s8<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(p.C), p.ldc, col0, p.N, v, p.s8, row);
     } else {
-        const float sa = p.s8.sa[row];
-        if (p.s8.dtype == QG_F16)
-            store_row_s8<__half, N>(static_cast<__half*>(p.C) + at, col0, p.N, v, sa, p.s8);
-        else if (p.s8.dtype == QG_BF16)
-            store_row_s8<__nv_bfloat16, N>(static_cast<__nv_bfloat16*>(p.C) + at, col0, p.N, v, sa, p.s8);
-        else
-            store_row_s8<float, N>(static_cast<float*>(p.C) + at, col0, p.N, v, sa, p.s8);
+        store_row_s8<float, N>(static_cast<float*>(p.C), p.ldc, col0, p.N, v, p.s8, row);
     }
 }
 
