@@ -31,6 +31,13 @@ __device__ __forceinline__ float exp2_fast(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Below this sum of a block's weights its part of the denominator is summed without log2 sv.
+// Weights lost to underflow next to a larger sum are 2^-26 of it at most.
+constexpr float kLowWeight = 0x1p-100f;
+// Denominators are kept times 2^20.  With a page's scale from 2^-64 to 2^121 their terms are then
+// between 2^-101 and 2^92; as M moves they are multiplied by 2^(d / 2) twice, since 2^d alone may
+// be below fp32's range where the result is not.
+constexpr float kDenPower = 20.f;
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 
 __device__ __forceinline__ uint32_t elect_lane() {

@@ -7,7 +7,8 @@
 // stay outside: sk is a factor of the product's result, and sv goes into the exponent,
 //   w_j = 2^(x_j + log2 sv_j - M),   O = sum w_j vq_j / sum (w_j / sv_j),
 // with M a running upper bound of x_j + log2 sv_j, so that w_j, rounded to fp16 for the
-// second product, is at most 2^8 whatever the pages' scales are.  Sums, M and the
+// second product, is at most 2^8 whatever the pages' scales are.  (Where that leaves w_j
+// hardly anything, its term of the denominator is 2^(x_j - M).)  Sums, M and the
 // denominator are fp32.  Queries go in as fp16 times a power of two of their row, which
 // is exact for bf16 too but for values 2^-28 of the row's largest.
 #include <cuda.h>
@@ -122,8 +123,8 @@ __device__ __forceinline__ void store_out(const AttnParams& p, const AttnSeq& a,
                                           float2 sum, float total) {
     const float nan = __uint_as_float(0x7fc00000u);
     T* out = static_cast<T*>(p.O) + (a.s.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D + d;
-    out[0] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.x / total);
-    out[1] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.y / total);
+    out[0] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.x * (0x1p20f / total));
+    out[1] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.y * (0x1p20f / total));
 }
 
 template <class T, int D, int NB>
@@ -210,7 +211,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
                     sv = p.c.vs[h.unit];
                 }
                 h.lsv = __log2f(sv);
-                h.isv = __fdividef(1.f, sv);
+                h.isv = exp2_fast(kDenPower - h.lsv);
             }
             return h;
         };
@@ -390,9 +391,9 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         const float v = fmaxf(M[n][m], top[n][m]);
-                        const float f = M[n][m] == neg_inf() ? 0.f : exp2_fast(M[n][m] - v);
+                        const float half = M[n][m] == neg_inf() ? 0.f : exp2_fast(0.5f * (M[n][m] - v)), f = half * half;
                         M[n][m] = v;
-                        den[n][m] *= f;
+                        den[n][m] = den[n][m] * half * half;
 #pragma unroll
                         for (int d = 0; d < DT; ++d) {
                             o[d][n][m] *= f;
@@ -402,6 +403,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
             }
             // weights, in fp16 and from the products' rows to their columns
             uint32_t pf[2][NB][2];
+            bool low = false;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
                 const float m0 = M[n][0] == neg_inf() ? 0.f : M[n][0], m1 = M[n][1] == neg_inf() ? 0.f : M[n][1];
@@ -409,12 +411,31 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
                 for (int h = 0; h < 2; ++h) {
                     const float e0 = exp2_fast(x[h][n][0] - m0), e1 = exp2_fast(x[h][n][1] - m1);
                     const float e2 = exp2_fast(x[h][n][2] - m0), e3 = exp2_fast(x[h][n][3] - m1);
-                    // not 0 times a NaN of tokens that are not seen
-                    if (!(e0 + e2 == 0.f)) den[n][0] = fmaf(e0 + e2, isv[h], den[n][0]);
-                    if (!(e1 + e3 == 0.f)) den[n][1] = fmaf(e1 + e3, isv[h], den[n][1]);
+                    const float s0 = e0 + e2, s1 = e1 + e3;
+                    // not the low ones, nor 0 times a NaN of tokens that are not seen
+                    if (!(s0 < kLowWeight)) den[n][0] = fmaf(s0, isv[h], den[n][0]);
+                    if (!(s1 < kLowWeight)) den[n][1] = fmaf(s1, isv[h], den[n][1]);
+                    low |= s0 < kLowWeight || s1 < kLowWeight;
                     pf[h][n][0] = transposed(pack2<__half>(e0, e1));
                     pf[h][n][1] = transposed(pack2<__half>(e2, e3));
                 }
+            }
+            if (__any_sync(0xffffffffu, low)) {
+                // tokens of small scales next to large ones: 2^(x - M), whose size they keep in the denominator
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        const float base = M[n][m] == neg_inf() ? 0.f : M[n][m];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float x0 = x[h][n][m], x2 = x[h][n][m + 2];
+                            const bool less = exp2_fast(x0 - base) + exp2_fast(x2 - base) < kLowWeight;
+                            if (less && x0 > neg_inf()) den[n][m] += exp2_fast(x0 - base + (kDenPower - lsv[h]));
+                            if (less && x2 > neg_inf()) den[n][m] += exp2_fast(x2 - base + (kDenPower - lsv[h]));
+                        }
+                    }
+                __syncwarp();
             }
             if (!__all_sync(0xffffffffu, bounded_wait(v_bar(s), phase(step), nullptr, p.ctl, kSiteAttnV))) {
                 ok = false;
@@ -505,11 +526,11 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
             float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < kAttnWarps; ++w) {
-                const float e = md[w].x == neg_inf() ? 0.f : exp2_fast(md[w].x - m);
+                const float half = md[w].x == neg_inf() ? 0.f : exp2_fast(0.5f * (md[w].x - m)), e = half * half;
                 const float2 v = *reinterpret_cast<const float2*>(from + w * Cfg::PART + d);
                 sum.x = fmaf(v.x, e, sum.x);
                 sum.y = fmaf(v.y, e, sum.y);
-                total = fmaf(md[w].y, e, total);
+                total = fmaf(md[w].y * half, half, total);
             }
             if (whole) {
                 store_out<T>(p, a, u.head, row0 + r, d, D, sum, total);
@@ -605,8 +626,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnP
             float e = 0.f;
             if (dense || border(k + j) > border(k - 1 + j)) {
                 const float* f = part(k - 1 + j) + r * Cfg::STRIDE;
-                e = f[D] == neg_inf() ? 0.f : exp2_fast(f[D] - top[r]);
-                den = fmaf(f[D + 1], e, den);
+                const float half = f[D] == neg_inf() ? 0.f : exp2_fast(0.5f * (f[D] - top[r]));
+                e = half * half;
+                den = fmaf(f[D + 1] * half, half, den);
             }
             weight[i][r] = e;
         }

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             tc_fence_after();
             // scores 32 at a time; the last two quarters first, and again for their weights
             uint32_t xa[32], xb[32];
-            float top = neg_inf();
+            float top = neg_inf(), least = -neg_inf();  // the greatest of the step, the least of its blocks' greatest
             auto maximum = [&](auto all, const uint32_t(&v)[32], int ch) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
@@ -311,7 +311,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                                               __uint_as_float(v[o + 14]));
                         m[0] = max3(m[0], m[1], __uint_as_float(v[o + 15]));
                         m[2] = max3(m[2], m[3], m4);
-                        top = fmaxf(top, fmaf(fmaxf(m[0], m[2]), c, sl.y));
+                        const float t = fmaf(fmaxf(m[0], m[2]), c, sl.y);
+                        top = fmaxf(top, t);
+                        least = fminf(least, t);
                     } else {
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -319,15 +321,23 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                     }
                 }
             };
+            // no use of a load's registers moves ahead of its wait
+            auto landed = [&](uint32_t(&v)[32]) {
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(v[i]));
+            };
             auto maxima = [&](auto all) {
                 tmem_ld_32x32b_x32(s_at + 64, xa);
                 tmem_ld_32x32b_x32(s_at + 96, xb);
-                tmem_wait_ld();
+                landed(xa);
+                landed(xb);
                 maximum(all, xa, 2);
                 tmem_ld_32x32b_x32(s_at, xa);
                 maximum(all, xb, 3);
                 tmem_ld_32x32b_x32(s_at + 32, xb);
-                tmem_wait_ld();
+                landed(xa);
+                landed(xb);
                 maximum(all, xa, 0);
                 maximum(all, xb, 1);
             };
@@ -338,9 +348,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             // O is at rest: this step's scores were issued behind the last step's product with V
             if (__any_sync(0xffffffffu, top > M + kLazy)) {
                 const float m = fmaxf(M, top);
-                const float f = M == neg_inf() ? 0.f : exp2_fast(M - m);
+                const float half = M == neg_inf() ? 0.f : exp2_fast(0.5f * (M - m)), f = half * half;
                 M = m;
-                den *= f;
+                den = den * half * half;
                 if (step) {
 #pragma unroll 1
                     for (int d = 0; d < D; d += 16) {
@@ -360,7 +370,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                 for (int h = 0; h < 2; ++h) {
                     const int b = 2 * ch + h;
                     const float2 sl = sc[b];
-                    const float c = factor * sl.x, l = sl.y - base, isv = exp2_fast(-sl.y);  // 1 / sv
+                    const float c = factor * sl.x, l = sl.y - base, isv = exp2_fast(kDenPower - sl.y);
                     const uint64_t cc = two(c, c), ll = two(l, l);
                     uint64_t sum = two(0.f, 0.f);
 #pragma unroll
@@ -377,7 +387,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                         w[8 * h + i] = pack2<__half>(e.x, e.y);
                     }
                     const float2 s2 = both(sum);
-                    if (!(s2.x + s2.y == 0.f)) den = fmaf(s2.x + s2.y, isv, den);  // not 0 times a NaN not seen
+                    const float s = s2.x + s2.y;
+                    if constexpr (decltype(all)::value) {
+                        den = fmaf(s, isv, den);
+                    } else {
+                        // not the low ones, nor 0 times a NaN of tokens not seen
+                        const bool low = s < kLowWeight;
+                        if (!low) den = fmaf(s, isv, den);
+                        if (__any_sync(0xffffffffu, low && 16 * b < left)) {
+                            float d = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                if (16 * b + i < left) d += exp2_fast(fmaf(__uint_as_float(x[16 * h + i]), c, kDenPower - base));
+                            if (low) den += d;
+                        }
+                    }
                 }
                 tmem_st_x16(s_at + 16 * ch, w);  // over scores that have been read
             };
@@ -385,13 +409,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                 weights(all, xa, 0);
                 tmem_ld_32x32b_x32(s_at + 64, xa);
                 weights(all, xb, 1);
-                tmem_wait_ld();
+                landed(xa);
                 tmem_ld_32x32b_x32(s_at + 96, xb);
                 weights(all, xa, 2);
-                tmem_wait_ld();
+                landed(xb);
                 weights(all, xb, 3);
             };
-            if (whole)
+            if (whole && !__any_sync(0xffffffffu, least < M - 99.f))
                 all_weights(std::true_type{});
             else
                 all_weights(std::false_type{});
@@ -406,7 +430,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         if (ok) {
             T* out = static_cast<T*>(p.O) + (seq.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D;
             const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-            const float scale = den == 0.f ? 0.f : 1.f / den;
+            const float scale = den == 0.f ? 0.f : 0x1p20f / den;
 #pragma unroll 1
             for (int d = 0; d < D; d += 16) {
                 uint32_t y[16];

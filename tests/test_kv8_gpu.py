@@ -274,6 +274,22 @@ def test_attention_over_pages_of_very_different_scales(torch, qg, dtype):
     check_attention(torch, O, Q, cache, table, news, lengths, D ** -0.5, True, dtype)
 
 
+@pytest.mark.parametrize("small,large", [(-60, 60), (-64, 80), (-40, 115)])
+@pytest.mark.parametrize("news", [1, 80])
+def test_attention_counts_tokens_of_small_scales_next_to_large_ones(torch, qg, news, small, large):
+    """Most of a row's weight on pages whose V scale is 2^small, some on pages of 2^large."""
+    heads, D, page, length = 2, 64, 16, 180
+    cache, table = filled(torch, [length], heads, D, page, 7)
+    used = table[0, :-(-length // page)].long()
+    for j, p in enumerate(used):
+        cache[3][p] = 2.0 ** (large if j % 5 == 2 else small)
+    gen = torch.Generator(device="cuda").manual_seed(news)
+    for sharp in (0.1, 1.0, 4.0):
+        Q = (sharp * torch.randn(news, heads * 4, D, generator=gen, device="cuda")).bfloat16()
+        O = qg.kv8_attention(Q, cache, table, int32(torch, [0, news]), int32(torch, [length]))
+        check_attention(torch, O, Q, cache, table, [news], [length], D ** -0.5, True, "bfloat16")
+
+
 def test_attention_with_large_and_small_queries(torch, qg):
     """bf16 queries far outside fp16's range, with keys to match, and sharp weights."""
     news, lengths, heads, D = [2, 20], [100, 150], 1, 128
