@@ -109,10 +109,7 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
     }
     int8_t* to = codes + kept * c.D;
     auto store = [&](int i, const float (&v)[8]) {
-        int q[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = s8_code(v[k], r);
-        *reinterpret_cast<uint2*>(to + i * 8) = make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
+        *reinterpret_cast<uint2*>(to + i * 8) = make_uint2(s8_pack(v, r), s8_pack(v + 4, r));
     };
 #pragma unroll
     for (int k = 0; k < kAppendHeld; ++k)

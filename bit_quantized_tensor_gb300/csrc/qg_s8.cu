@@ -19,15 +19,12 @@ namespace qg {
 // many rows are under way.
 template <class OUT>
 __device__ __forceinline__ void store_codes(OUT* dst, const float (&x)[8], float r) {
-    int q[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = s8_code(x[i], r);
     if constexpr (sizeof(OUT) == 1) {
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_s8(q[0], q[1], q[2], q[3]), pack_s8(q[4], q[5], q[6], q[7]));
+        *reinterpret_cast<uint2*>(dst) = make_uint2(s8_pack(x, r), s8_pack(x + 4, r));
     } else {
         float f[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = static_cast<float>(q[i]);
+        for (int i = 0; i < 8; ++i) f[i] = s8_number(x[i], r);
         store_vec<OUT, 8>(dst, f);
     }
 }
@@ -112,21 +109,23 @@ static int launch_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, OUT
 
 // ------------------------------------------------------------ few tokens
 
-// Up to 16 tokens: the weights' rows are the rows of the MMA and the tokens its
+// Up to 8 tokens: the weights' rows are the rows of the MMA and the tokens its
 // columns.  A CTA takes 16 weight rows, its 16 warps every 16th block of 64 values
 // along K; a thread's bytes of a row (16 at a time) are the values of four MMA steps,
 // since a sum does not depend on the order of k.  Sums of a few blocks are exact in
-// fp32; they are added up in 32-bit integers, over the warps as well.  The tokens
+// fp32; they are added up in 32-bit integers, over the warps as well.  One or two tokens
 // are quantized by every CTA for itself into shared memory (QUANT), which costs less
-// than a kernel ahead of this one.
+// than a kernel ahead of this one but about 1 us a token; more come as codes, straight into
+// registers.
 constexpr int kGemvWarps = 16, kGemvThreads = 32 * kGemvWarps;
 constexpr int kGemvBatch = 4;            // blocks of 64 values in flight a thread
-constexpr int kGemvTokens = 16;
-constexpr size_t kGemvSmem = 110 * 1024;  // two CTAs an SM
+constexpr int kGemvTokens = 8, kGemvQuantTokens = 2;
+constexpr size_t kGemvSmem = 100 * 1024;  // two CTAs an SM
 
 __host__ __device__ inline int64_t gemv_token_stride(int64_t K) { return (K + 63) / 64 * 64 + 16; }
-static bool gemv_fits(int64_t M, int64_t K) {
-    return M <= kGemvTokens && static_cast<size_t>(M * gemv_token_stride(K)) <= kGemvSmem;
+// Are M tokens quantized inside the product's kernel?  Their codes have to fit its shared memory.
+static bool gemv_quantizes(int64_t M, int64_t K) {
+    return M <= kGemvQuantTokens && static_cast<size_t>(M * gemv_token_stride(K)) <= kGemvSmem;
 }
 
 struct GemvParams {
@@ -151,12 +150,12 @@ __device__ __forceinline__ uint4 first_bytes(uint4 w, int n) {
     return make_uint4(keep(w.x, 0), keep(w.y, 4), keep(w.z, 8), keep(w.w, 12));
 }
 
-template <class T, int MB, bool QUANT>
+template <class T, bool QUANT>
 __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p) {
     extern __shared__ __align__(16) uint8_t codes[];
-    __shared__ uint32_t red_max[kGemvTokens][kGemvWarps];
+    __shared__ uint32_t red_max[kGemvQuantTokens][kGemvWarps];
     __shared__ float token_scale[kGemvTokens];
-    __shared__ int sums[kGemvWarps][MB * 4][32];
+    __shared__ int sums[kGemvWarps][4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = blockIdx.x * 16;
     const int blocks = (p.ldq + 63) / 64;
@@ -177,15 +176,23 @@ __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p)
     pdl_wait_prior_grid();
     pdl_launch_dependents();
 
-    uint4 a[kGemvBatch][2];
+    uint4 a[kGemvBatch][2], xc[QUANT ? 1 : kGemvBatch];
     auto load = [&](int b0) {
 #pragma unroll
         for (int j = 0; j < kGemvBatch; ++j) {
-            const int b = b0 + j * kGemvWarps;
-            const bool in = b < blocks && 64 * b + 16 * t < p.ldq;
+            const int b = b0 + j * kGemvWarps, k = 64 * b + 16 * t;
+            const bool in = b < blocks && k < p.ldq;
             a[j][0] = a[j][1] = make_uint4(0, 0, 0, 0);
             if (in && has0) a[j][0] = *reinterpret_cast<const uint4*>(w0 + 64 * static_cast<int64_t>(b));
             if (in && has1) a[j][1] = *reinterpret_cast<const uint4*>(w1 + 64 * static_cast<int64_t>(b));
+            if constexpr (!QUANT) {
+                xc[j] = make_uint4(0, 0, 0, 0);
+                if (in && g < p.M) {
+                    xc[j] = *reinterpret_cast<const uint4*>(static_cast<const int8_t*>(p.X) +
+                                                            static_cast<int64_t>(g) * p.ldq + k);
+                    if (k + 16 > p.K) xc[j] = first_bytes(xc[j], p.K - k);  // what lies behind K does not count
+                }
+            }
         }
     };
     load(warp);
@@ -215,62 +222,45 @@ __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p)
                 store_codes(reinterpret_cast<int8_t*>(codes) + m * stride + k, v, r);
             }
         }
+        __syncthreads();
     } else {
-        for (int m = 0; m < p.M; ++m) {
-            const int8_t* x = static_cast<const int8_t*>(p.X) + static_cast<int64_t>(m) * p.ldq;
-            for (int k = 16 * threadIdx.x; k < 64 * blocks; k += 16 * kGemvThreads) {
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (k < p.ldq) w = *reinterpret_cast<const uint4*>(x + k);
-                if (k + 16 > p.K) w = first_bytes(w, p.K - k);  // what lies behind K does not count
-                *reinterpret_cast<uint4*>(codes + m * stride + k) = w;
-            }
-        }
         if (threadIdx.x < p.M) token_scale[threadIdx.x] = p.sa[threadIdx.x];
     }
-    __syncthreads();
 
-    int total[MB][4];
-#pragma unroll
-    for (int i = 0; i < MB * 4; ++i) total[i / 4][i % 4] = 0;
+    int total[4] = {0, 0, 0, 0};
     for (int b0 = warp; b0 < blocks; b0 += kGemvBatch * kGemvWarps) {
         if (b0 != warp) load(b0);
-        float acc[MB][4];
-#pragma unroll
-        for (int i = 0; i < MB * 4; ++i) acc[i / 4][i % 4] = 0.f;
+        float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < kGemvBatch; ++j) {
             const int b = b0 + j * kGemvWarps;
             if (b >= blocks) break;
-            uint4 x[MB];
-#pragma unroll
-            for (int i = 0; i < MB; ++i)
-                x[i] = g + 8 * i < p.M ? *reinterpret_cast<const uint4*>(codes + (g + 8 * i) * stride + 64 * b + 16 * t)
-                                       : make_uint4(0, 0, 0, 0);
+            uint4 x;
+            if constexpr (QUANT)
+                x = g < p.M ? *reinterpret_cast<const uint4*>(codes + g * stride + 64 * b + 16 * t) : make_uint4(0, 0, 0, 0);
+            else
+                x = xc[j];
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
             const uint32_t r0[4] = {a[j][0].x, a[j][0].y, a[j][0].z, a[j][0].w};
             const uint32_t r1[4] = {a[j][1].x, a[j][1].y, a[j][1].z, a[j][1].w};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                uint32_t a0, a1, a2, a3;
+                uint32_t a0, a1, a2, a3, b0h, b1h;
                 s8_to_f16(r0[c], a0, a2);
                 s8_to_f16(r1[c], a1, a3);
-#pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    const uint32_t xw = c == 0 ? x[i].x : c == 1 ? x[i].y : c == 2 ? x[i].z : x[i].w;
-                    uint32_t b0h, b1h;
-                    s8_to_f16(xw, b0h, b1h);
-                    mma_f16(acc[i], a0, a1, a2, a3, b0h, b1h);
-                }
+                s8_to_f16(xw[c], b0h, b1h);
+                mma_f16(acc, a0, a1, a2, a3, b0h, b1h);
             }
         }
 #pragma unroll
-        for (int i = 0; i < MB * 4; ++i) total[i / 4][i % 4] += __float2int_rn(acc[i / 4][i % 4]);
+        for (int i = 0; i < 4; ++i) total[i] += __float2int_rn(acc[i]);
     }
 #pragma unroll
-    for (int i = 0; i < MB * 4; ++i) sums[warp][i][lane] = total[i / 4][i % 4];
+    for (int i = 0; i < 4; ++i) sums[warp][i][lane] = total[i];
     __syncthreads();
-    // accumulator element (tile i, value v) of lane 4 g + t: weight row g + 8 (v / 2), token 8 i + 2 t + v % 2
-    if (threadIdx.x < 128 * MB) {
-        const int e = threadIdx.x >> 5, row = g + 8 * ((e & 3) >> 1), m = 8 * (e >> 2) + 2 * t + (e & 1);
+    // accumulator element e of lane 4 g + t: weight row g + 8 (e / 2), token 2 t + e % 2
+    if (threadIdx.x < 128) {
+        const int e = threadIdx.x >> 5, row = g + 8 * (e >> 1), m = 2 * t + (e & 1);
         int sum = 0;
 #pragma unroll
         for (int w = 0; w < kGemvWarps; ++w) sum += sums[w][e][lane];
@@ -285,23 +275,21 @@ __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p)
 
 template <class T, bool QUANT>
 static int launch_gemv(const GemvParams& p, cudaStream_t s) {
-    const size_t smem = static_cast<size_t>(p.M * gemv_token_stride(p.ldq));
     const dim3 grid(static_cast<unsigned>((p.N + 15) / 16));
-    struct Few;
-    struct More;
-    if (p.M <= 8) {
-        const int rc = raise_smem<Few>(k_s8_gemv<T, 1, QUANT>);
-        return rc ? rc : launch_serialized(k_s8_gemv<T, 1, QUANT>, grid, kGemvThreads, smem, 1, s, p);
+    if constexpr (QUANT) {
+        struct Tag;
+        const int rc = raise_smem<Tag>(k_s8_gemv<T, true>);
+        if (rc) return rc;
+        return launch_serialized(k_s8_gemv<T, true>, grid, kGemvThreads,
+                                 static_cast<size_t>(p.M * gemv_token_stride(p.ldq)), 1, s, p);
+    } else {
+        return launch_serialized(k_s8_gemv<T, false>, grid, kGemvThreads, 0, 1, s, p);
     }
-    const int rc = raise_smem<More>(k_s8_gemv<T, 2, QUANT>);
-    return rc ? rc : launch_serialized(k_s8_gemv<T, 2, QUANT>, grid, kGemvThreads, smem, 1, s, p);
 }
 
 // ------------------------------------------------------------ which kernel
 
-// Up to here the weights are turned into fp16 on the SM; with more tokens that is done once, in
-// memory, for the tiles of CTA pairs.
-constexpr int64_t kS8SomeTokens = 1024;
+static bool takes_gemv(int64_t M) { return M <= kGemvTokens; }
 
 // Tokens a tile (32, 64, 128) and CTAs of a cluster that share K.
 struct SomeForm {
@@ -313,12 +301,13 @@ static bool some_holds(const SomeForm& f, int64_t K) {
     const int64_t stages = (K + kS8Bk - 1) / kS8Bk;
     return (stages + f.splits - 1) / f.splits <= 512 / f.tile * kS8Exact;
 }
-static bool takes_some(int64_t M, int64_t K) { return M <= kS8SomeTokens && some_holds(SomeForm{32, 8}, K); }
 
 // The form with the least estimated time, in cycles of an SM, as measured: a CTA's start, its
-// stages (bound by turning codes into fp16, with 128 tokens by the MMA as much), its epilogue and
-// the exchange of sums; whole rounds of CTAs.
-static SomeForm some_form(int64_t M, int64_t N, int64_t K, int sms) {
+// stages (the bytes that they bring from the L2, and turning codes into fp16), its epilogue and
+// the exchange of sums; whole rounds of CTAs, of which clusters of 8 leave SMs out.  Estimates
+// were within 10% of 4 to 250 us at 36 problems; the best form of each was chosen, or one at most
+// 8% slower.
+static SomeForm some_form(int64_t M, int64_t N, int64_t K, int64_t* cycles) {
     SomeForm best = {32, 8};
     int64_t least = INT64_MAX;
     for (int tile = 32; tile <= 128; tile *= 2) {
@@ -328,35 +317,47 @@ static SomeForm some_form(int64_t M, int64_t N, int64_t K, int sms) {
             const SomeForm f = {tile, splits};
             if (!some_holds(f, K) || (splits > 1 && K < 256 * splits)) continue;
             const int64_t stages = ((K + kS8Bk - 1) / kS8Bk + splits - 1) / splits;
-            const int64_t cta = 4500 + stages * (tile == 128 ? 620 : 520) + 1200 + 20 * tile +
-                                (splits > 1 ? 2500 + 32 * tile : 0);
+            const int64_t cta = 5700 + 20 * tile + stages * (500 + 6 * tile) + (splits > 1 ? 2500 + 32 * tile : 0);
+            const int64_t sms = splits == 8 ? 104 : 148;
             const int64_t time = (tiles * splits + sms - 1) / sms * cta;
             if (time < least) least = time, best = f;
         }
     }
+    *cycles = least;
     return best;
+}
+
+// Does that kernel take the problem, or the one on CTA pairs, behind a pass that writes the
+// weights as fp16?  The latter's estimate: that pass at 6.2 TB/s (3.3 kB a cycle) and rounds of
+// 256 x 256 tiles, 630 cycles a step of 64 values of K.
+static bool takes_some(int64_t M, int64_t N, int64_t K) {
+    if (M > 4096 || !some_holds(SomeForm{32, 8}, K)) return false;
+    int64_t cycles = 0;
+    some_form(M, N, K, &cycles);
+    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
+    return cycles <= 5700 + 3 * N * K / 3300 + (tiles + 75) / 76 * ((K + 63) / 64 * 630 + 7600);
 }
 
 // ------------------------------------------------------------ workspaces and calls
 
 static size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// fp16 forms of the tokens and, where they are turned into fp16 in memory, of the weights; the
-// tokens' scales.
+// The tokens' codes (a few tokens: 8 bits, more: fp16) and scales and, where they are turned
+// into fp16 in memory, the weights.
 struct S8Workspace {
     size_t a, b, sa, total;
 };
 static S8Workspace s8_workspace(int64_t M, int64_t N, int64_t K) {
-    const size_t ld = static_cast<size_t>(s8_codes_ld(K));
+    const size_t ld = static_cast<size_t>(s8_codes_ld(K)), m = static_cast<size_t>(M);
     S8Workspace w;
     w.a = 0;
-    w.b = up256(2 * ld * static_cast<size_t>(M));
-    w.sa = w.b + (takes_some(M, K) ? 0 : up256(2 * ld * static_cast<size_t>(N)));
-    w.total = w.sa + up256(4 * static_cast<size_t>(M));
+    w.b = up256((takes_gemv(M) ? 1 : 2) * ld * m);
+    w.sa = w.b + (takes_gemv(M) || takes_some(M, N, K) ? 0 : up256(2 * ld * static_cast<size_t>(N)));
+    w.total = w.sa + up256(4 * m);
     return w;
 }
 size_t s8_linear_workspace(int64_t M, int64_t N, int64_t K) {
-    return gemv_fits(M, K) ? 0 : s8_workspace(M, N, K).total;
+    return gemv_quantizes(M, K) ? 0 : s8_workspace(M, N, K).total;
 }
 
 constexpr int64_t kMaxRows = int64_t(1) << 27, kMaxK = 131072;
@@ -428,12 +429,13 @@ static int launch_some(const int8_t* W, const __half* X, const S8Params& p, int 
                              kS8Threads, Cfg::SMEM, splits, s, tw, tx, p);
 }
 
-static int some_product(int dtype, int dev, int64_t M, int64_t N, int64_t K, const __half* A, const float* sa,
+static int some_product(int dtype, int64_t M, int64_t N, int64_t K, const __half* A, const float* sa,
                         const int8_t* W, const float* sb, const void* bias, void* Y, int64_t ldy, const Ctl& ctl,
                         cudaStream_t s) {
     S8Params p = {};
     p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K);
-    const SomeForm f = some_form(M, N, K, num_sms(dev));
+    int64_t cycles = 0;
+    const SomeForm f = some_form(M, N, K, &cycles);
     while ((1 << p.log_splits) < f.splits) ++p.log_splits;
     p.sa = sa; p.sb = sb; p.bias = bias; p.Y = Y; p.ldy = ldy; p.dtype = dtype; p.ctl = ctl;
     if (f.tile == 32) return launch_some<32>(W, A, p, f.splits, s);
@@ -458,17 +460,15 @@ QG_S8_SOME(128);
     QG_S8_QUANT(T, NAME, OUT, ONAME, 128, 8);   \
     QG_S8_QUANT(T, NAME, OUT, ONAME, 512, 4);   \
     QG_S8_QUANT(T, NAME, OUT, ONAME, 512, 0)
-#define QG_S8_GEMV(T, NAME, MB, QUANT)                                                            \
-    QG_BLOCK_KERNEL_BUDGET("k_s8_gemv<" NAME "," #MB "," #QUANT ">",                              \
-                           (reinterpret_cast<const void*>(k_s8_gemv<T, MB, QUANT>)), kGemvThreads, \
-                           static_cast<int>(kGemvSmem) - MB * 8192 - 2048, 0, 1, 2)
+#define QG_S8_GEMV(T, NAME, QUANT)                                                                \
+    QG_BLOCK_KERNEL_BUDGET("k_s8_gemv<" NAME "," #QUANT ">"       ,                              \
+                           (reinterpret_cast<const void*>(k_s8_gemv<T, QUANT>)), kGemvThreads,     \
+                           QUANT ? static_cast<int>(kGemvSmem) : 0, 0, 1, 2)
 #define QG_S8_BUDGETS(T, NAME)                    \
     QG_S8_QUANT_SIZES(T, NAME, int8_t, "s8");     \
     QG_S8_QUANT_SIZES(T, NAME, __half, "codes");  \
-    QG_S8_GEMV(T, NAME, 1, true);                 \
-    QG_S8_GEMV(T, NAME, 2, true);                 \
-    QG_S8_GEMV(T, NAME, 1, false);                \
-    QG_S8_GEMV(T, NAME, 2, false)
+    QG_S8_GEMV(T, NAME, true);                    \
+    QG_S8_GEMV(T, NAME, false)
 QG_S8_BUDGETS(__half, "f16");
 QG_S8_BUDGETS(__nv_bfloat16, "bf16");
 QG_S8_BUDGETS(float, "f32");
@@ -505,14 +505,14 @@ int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const 
     rc = check_out(dtype, N, Bs, bias, Y, ldy, M);
     if (rc) return rc;
     if (!aligned16(Aq) || !aligned16(Bq) || reinterpret_cast<uintptr_t>(As) % 4) return QG_ERR_MISALIGNED;
-    if (K > 0) rc = check_workspace(ws, ws_bytes, s8_linear_workspace(M, N, K));
+    if (K > 0 && !takes_gemv(M)) rc = check_workspace(ws, ws_bytes, s8_linear_workspace(M, N, K));
     if (rc) return rc;
     const int dev = current_device();
     if (dev < 0) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return only_bias(dtype, M, N, bias, Y, ldy, s);
     const int64_t ld = s8_codes_ld(K);
-    if (gemv_fits(M, K)) {
+    if (takes_gemv(M)) {
         GemvParams p = {};
         p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K); p.ldq = static_cast<int>(ld);
         p.X = Aq; p.sa = As; p.W = Bq; p.sb = Bs; p.bias = bias; p.Y = Y; p.ldy = ldy;
@@ -524,7 +524,7 @@ int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const 
     uint8_t* base = static_cast<uint8_t*>(ws);
     __half *a = reinterpret_cast<__half*>(base + w.a), *b = reinterpret_cast<__half*>(base + w.b);
     rc = s8_to_f16_rows(Aq, M, ld, a, ld, dev, s);
-    if (!rc && takes_some(M, K)) return some_product(dtype, dev, M, N, K, a, As, Bq, Bs, bias, Y, ldy, ctl, s);
+    if (!rc && takes_some(M, N, K)) return some_product(dtype, M, N, K, a, As, Bq, Bs, bias, Y, ldy, ctl, s);
     if (!rc) rc = s8_to_f16_rows(Bq, N, ld, b, ld, dev, s);
     return rc ? rc : tensor_product(dtype, M, N, K, a, As, b, Bs, bias, Y, ldy, ctl, s);
 }
@@ -546,21 +546,31 @@ int s8_linear(int dtype, int64_t M, int64_t N, int64_t K, const void* X, int64_t
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (K == 0) return only_bias(dtype, M, N, bias, Y, ldy, s);
     const int64_t ld = s8_codes_ld(K);
-    if (gemv_fits(M, K)) {
+    const S8Workspace w = s8_workspace(M, N, K);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    if (takes_gemv(M)) {
         GemvParams p = {};
         p.M = static_cast<int>(M); p.N = static_cast<int>(N); p.K = static_cast<int>(K); p.ldq = static_cast<int>(ld);
-        p.X = X; p.ldx = ldx; p.x_aligned = aligned16(X) && (M == 1 || ldx * dtype_bytes(dtype) % 16 == 0);
         p.W = Wq; p.sb = Ws; p.bias = bias; p.Y = Y; p.ldy = ldy;
-        return by_dtype(dtype, [&](auto t) { return launch_gemv<decltype(t), true>(p, s); });
+        if (gemv_quantizes(M, K)) {
+            p.X = X; p.ldx = ldx; p.x_aligned = aligned16(X) && (M == 1 || ldx * dtype_bytes(dtype) % 16 == 0);
+            return by_dtype(dtype, [&](auto t) { return launch_gemv<decltype(t), true>(p, s); });
+        }
+        float* sa = reinterpret_cast<float*>(base + w.sa);
+        p.X = base + w.a;
+        p.sa = sa;
+        return by_dtype(dtype, [&](auto t) {
+            using T = decltype(t);
+            const int rc = launch_quantize<T, int8_t>(M, K, X, ldx, reinterpret_cast<int8_t*>(base + w.a), sa, s);
+            return rc ? rc : launch_gemv<T, false>(p, s);
+        });
     }
     const Ctl ctl = host_ctl(dev);
     if (!ctl.status) return QG_ERR_CUDA;
-    const S8Workspace w = s8_workspace(M, N, K);
-    uint8_t* base = static_cast<uint8_t*>(ws);
     __half *a = reinterpret_cast<__half*>(base + w.a), *b = reinterpret_cast<__half*>(base + w.b);
     float* sa = reinterpret_cast<float*>(base + w.sa);
     rc = by_dtype(dtype, [&](auto t) { return launch_quantize<decltype(t), __half>(M, K, X, ldx, a, sa, s); });
-    if (!rc && takes_some(M, K)) return some_product(dtype, dev, M, N, K, a, sa, Wq, Ws, bias, Y, ldy, ctl, s);
+    if (!rc && takes_some(M, N, K)) return some_product(dtype, M, N, K, a, sa, Wq, Ws, bias, Y, ldy, ctl, s);
     if (!rc) rc = s8_to_f16_rows(Wq, N, ld, b, ld, dev, s);
     return rc ? rc : tensor_product(dtype, M, N, K, a, sa, b, Ws, bias, Y, ldy, ctl, s);
 }

@@ -26,11 +26,23 @@ __device__ __forceinline__ float s8_scale(uint32_t amax_bits, float least) {
 }
 // r; 0 for a scale that is NaN, so that every code is 0 (x r is NaN for a NaN, code 0 as well).
 __device__ __forceinline__ float s8_inverse(float scale) { return scale == scale ? __fdiv_rn(1.f, scale) : 0.f; }
-__device__ __forceinline__ int s8_code(float x, float r) {
-    return max(-127, min(127, __float2int_rn(__fmul_rn(x, r))));
+// fl(x r) rounded to a whole number, ties to even, by adding 1.5 * 2^23: the sum's unit is 1, its
+// low byte the code (conversions to integers run at an eighth of this rate).  No clamp is needed:
+// |x| <= 127 s (1 + 2^-24), so |fl(x r)| < 127.5.  Not for r = 0, where x may be infinite or NaN.
+__device__ __forceinline__ float s8_shifted(float x, float r) { return __fadd_rn(__fmul_rn(x, r), 12582912.f); }
+// Codes in a word, the first in the low byte; 0 for r = 0.
+__device__ __forceinline__ uint32_t s8_pack(const float* x, float r) {
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = __float_as_uint(s8_shifted(x[i], r));
+    return r == 0.f ? 0u : __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+}
+// The code as a number.
+__device__ __forceinline__ float s8_number(float x, float r) {
+    return r == 0.f ? 0.f : __fadd_rn(s8_shifted(x, r), -12582912.f);
 }
 
-// Four codes in a word, the first in the low byte.
+// Four whole numbers' low bytes in a word, the first in the low byte.
 __device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
