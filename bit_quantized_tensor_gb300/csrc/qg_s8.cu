@@ -44,28 +44,22 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     const T* x = static_cast<const T*>(X) + row * ldx;
     OUT* q = Q + row * ldq;
     uint32_t amax = 0;
-    float v[C][8];
+    S8Piece<T> v[C];
     if constexpr (LONG) {
         for (int k = 8 * t; k < K; k += 8 * TPR) {
-            load_some<T, 8>(x + k, K - k, aligned, v[0]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[0][i]));
+            v[0].load(x + k, K - k, aligned);
+            amax = v[0].largest(amax);
         }
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int k = 8 * (t + c * TPR);
-            if (k < K) load_some<T, 8>(x + k, K - k, aligned, v[c]);
+            v[c].load(x + k, K - k, aligned);  // zeros behind K
         }
 #pragma unroll
-        for (int c = 0; c < C; ++c) {
-            if (8 * (t + c * TPR) < K) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[c][i]));
-            }
-        }
+        for (int c = 0; c < C; ++c) amax = v[c].largest(amax);
     }
-    amax = warp_max_u32(amax);
+    amax = warp_max_u32(S8Piece<T>::bits(amax));
     if constexpr (TPR > 32) {
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = amax;
         __syncthreads();
@@ -73,21 +67,20 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR)
     }
     const float s = s8_scale(amax, kRowScaleFloor), r = s8_inverse(s);
     if (t == 0) S[row] = s;
+    float f[8];
     if constexpr (LONG) {
         for (int k = 8 * t; k < ldq; k += 8 * TPR) {
-            load_some<T, 8>(x + k, K - k, aligned, v[0]);
-            store_codes(q + k, v[0], r);
+            v[0].load(x + k, K - k, aligned);
+            v[0].values(f);
+            store_codes(q + k, f, r);
         }
     } else {
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int k = 8 * (t + c * TPR);
             if (k >= ldq) break;
-            if (k >= K) {  // the row's padding: one piece of 8 at most
-#pragma unroll
-                for (int i = 0; i < 8; ++i) v[c][i] = 0.f;
-            }
-            store_codes(q + k, v[c], r);
+            v[c].values(f);
+            store_codes(q + k, f, r);
         }
     }
 }

@@ -59,6 +59,62 @@ __device__ __forceinline__ void s8_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi
     hi = *reinterpret_cast<const uint32_t*>(&b);
 }
 
+// Eight values of a row as they lie in memory, 0 from the n-th on.
+template <class T>
+struct S8Piece {
+    static constexpr int WORDS = 2 * static_cast<int>(sizeof(T));
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T* p, int n, bool aligned) {
+        if (aligned && n >= 8) {
+#pragma unroll
+            for (int i = 0; i < WORDS / 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = i < n ? __float_as_uint(p[i]) : 0u;
+        } else {
+            const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = (2 * i < n ? h[2 * i] : 0u) | (2 * i + 1 < n ? static_cast<uint32_t>(h[2 * i + 1]) << 16 : 0u);
+        }
+    }
+    __device__ __forceinline__ void values(float (&x)[8]) const {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(T) == 4) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 f = unpack2<T>(w[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        }
+    }
+    // The running maximum of the magnitudes' bits, of 16-bit types in either half of the word
+    // (half the work of doing it behind the conversion), and its fp32 bits.
+    __device__ __forceinline__ uint32_t largest(uint32_t m) const {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+            if constexpr (sizeof(T) == 4)
+                m = max(m, w[i] & 0x7fffffffu);
+            else
+                m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+        }
+        return m;
+    }
+    __device__ __forceinline__ static uint32_t bits(uint32_t m) {
+        if constexpr (sizeof(T) == 4) {
+            return m;
+        } else {
+            const float2 f = unpack2<T>(m);
+            return max(abs_bits(f.x), abs_bits(f.y));
+        }
+    }
+};
+
 __device__ __forceinline__ uint32_t warp_max_u32(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
 
 // D += A . B of 16 x 16 by 16 x 8 fp16 values.
