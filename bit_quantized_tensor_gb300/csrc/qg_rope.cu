@@ -35,8 +35,10 @@ struct RopeParams {
     RopeJob job[2];
     int blocks[2];       // CTAs of either job, Q's first
     int tokens, D, R;
-    int lanes, rotating, group;  // lanes that hold a head, that rotate; power of two
-    int heads_per, splits[2];    // a warp takes heads_per heads of a token: parts of either job's
+    int lanes, rotating;             // lanes that hold a head, that rotate
+    int group, group_log, step;      // lanes set aside for a head, a power of two; heads a warp
+    int heads_per, splits[2];        // a warp takes heads_per heads of a token: parts of either job's
+    uint64_t split_inv[2];           // floor(2^64 / splits) + 1, by which an item's token is found
     bool gain_f32;
     const int32_t* positions;
     const float* table;
@@ -58,6 +60,14 @@ __device__ __forceinline__ const float* table_row(const RopeParams& p, int token
     return pos >= 0 && pos < p.table_rows ? p.table + static_cast<int64_t>(pos) * p.R : nullptr;
 }
 
+// Token of an item, the part of its heads in `part`.  Exact for items below 2^64 / splits.
+__device__ __forceinline__ int token_of(const RopeParams& p, bool second, int64_t item, int& part) {
+    const int splits = p.splits[second];
+    const int token = static_cast<int>(splits == 1 ? item : __umul64hi(item, p.split_inv[second]));
+    part = static_cast<int>(item) - token * splits;
+    return token;
+}
+
 // What a lane holds of every head.
 template <class T>
 struct RopeLane {
@@ -68,8 +78,8 @@ struct RopeLane {
     template <bool PAIRS>
     __device__ __forceinline__ void init(const RopeParams& p) {
         const int lane = threadIdx.x & 31;
-        sub = lane / p.group;
-        l = lane % p.group;
+        sub = lane >> p.group_log;
+        l = lane & (p.group - 1);
         on = l < p.lanes;
         turns = l < p.rotating;
         a = PAIRS || !turns ? 2 * E * l : E * l;
@@ -178,20 +188,21 @@ __device__ __forceinline__ uint4 narrow(const float* f) {
 // CTAs out, which evens out what a loop over tokens left uneven (43 -> 30 us at 8192 tokens
 // of 40 heads).
 template <class T, bool PAIRS>
-__global__ void __launch_bounds__(kRopeThreads) k_qk_norm_rope(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 7) k_qk_norm_rope(const RopeParams p) {
     constexpr int E = RopeLane<T>::E, U = kRopeUnroll;
     pdl_wait_prior_grid();
     pdl_launch_dependents();
     const bool second = static_cast<int>(blockIdx.x) >= p.blocks[0];
     const RopeJob& j = p.job[second];
-    const int splits = p.splits[second];
     const int64_t item = static_cast<int64_t>(blockIdx.x - (second ? p.blocks[0] : 0)) * kRopeWarps + (threadIdx.x >> 5);
-    if (item >= static_cast<int64_t>(p.tokens) * splits) return;
-    const int token = static_cast<int>(item / splits), h0 = static_cast<int>(item % splits) * p.heads_per;
+    if (item >= static_cast<int64_t>(p.tokens) * p.splits[second]) return;
+    int h0;
+    const int token = token_of(p, second, item, h0);
+    h0 *= p.heads_per;
     const int h1 = min(j.heads, h0 + p.heads_per);
     RopeLane<T> lane;
     lane.template init<PAIRS>(p);
-    const int step = 32 / p.group, h = h0 + lane.sub;
+    const int step = p.step, h = h0 + lane.sub;
     const T* x = static_cast<const T*>(j.X) + token * j.ldx;
     T* y = static_cast<T*>(j.Y) + token * j.ldy;
     uint4 wa[U], wb[U];
@@ -271,13 +282,12 @@ __global__ void __launch_bounds__(kRopeThreads, 4) k_qk_norm_rope_backward(const
     }
 #pragma unroll
     for (int i = 0; i < E / 2; ++i) dga[i] = dgb[i] = two(0.f, 0.f);
-    const int step = 32 / p.group;
+    const int step = p.step;
     const float inv_d = 1.f / static_cast<float>(p.D);
-    const int splits = p.splits[second];
-    const int64_t items = static_cast<int64_t>(p.tokens) * splits;
+    const int64_t items = static_cast<int64_t>(p.tokens) * p.splits[second];
     for (int64_t item = block * kRopeWarps + (threadIdx.x >> 5); item < items; item += blocks * kRopeWarps) {
-        const int token = static_cast<int>(item / splits), part = static_cast<int>(item % splits);
-        const int h0 = part * p.heads_per, h1 = min(j.heads, h0 + p.heads_per);
+        int part;
+        const int token = token_of(p, second, item, part), h0 = part * p.heads_per, h1 = min(j.heads, h0 + p.heads_per);
         const T* x = static_cast<const T*>(j.X) + token * j.ldx;
         const T* dy = static_cast<const T*>(j.dY) + token * j.lddy;
         T* dx = static_cast<T*>(j.Y) + token * j.ldy;
@@ -506,8 +516,8 @@ static int launch_rope(RopeParams p, int dev, cudaStream_t s, int* parts) {
         p.lanes = p.D / (2 * E);
         p.rotating = p.R / (2 * E);
         p.group = 1;
-        while (p.group < p.lanes) p.group *= 2;
-        const int step = 32 / p.group;
+        while (p.group < p.lanes) p.group *= 2, ++p.group_log;
+        const int step = p.step = 32 / p.group;
         // heads of a token that a warp takes: as many as it has in flight, fewer where that
         // would leave SMs without warps
         p.heads_per = kRopeUnroll * step;
@@ -515,6 +525,7 @@ static int launch_rope(RopeParams p, int dev, cudaStream_t s, int* parts) {
             p.heads_per /= 2;
         for (int i = 0; i < 2; ++i) {
             p.splits[i] = (p.job[i].heads + p.heads_per - 1) / p.heads_per;
+            p.split_inv[i] = p.splits[i] > 1 ? ~0ull / p.splits[i] + 1 : 0;
             const int64_t items = static_cast<int64_t>(p.tokens) * p.splits[i];
             parts[i] = p.blocks[i] = BACKWARD ? share(i, items) : static_cast<int>((items + kRopeWarps - 1) / kRopeWarps);
         }
