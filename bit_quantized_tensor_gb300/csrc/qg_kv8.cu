@@ -65,28 +65,25 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
     int8_t* codes = (value ? c.vq : c.kq) + unit * page * c.D;
     float* scale = (value ? c.vs : c.ks) + unit;
     const float old = kept ? *scale : 0.f;
-    auto piece = [&](int i, float (&v)[8]) {
-        load_some<T, 8>(x + (i >> log_d8) * ld + 8 * (i & ((1 << log_d8) - 1)), 8, aligned, v);
+    auto piece = [&](int i, S8Piece<T>& v) {
+        v.load(x + (i >> log_d8) * ld + 8 * (i & ((1 << log_d8) - 1)), 8, aligned);
     };
 
-    float held[kAppendHeld][8];
+    S8Piece<T> held[kAppendHeld];
     uint32_t amax = 0;
 #pragma unroll
     for (int k = 0; k < kAppendHeld; ++k)
         if (lane + 32 * k < pieces) piece(lane + 32 * k, held[k]);
 #pragma unroll
     for (int k = 0; k < kAppendHeld; ++k)
-        if (lane + 32 * k < pieces) {
-#pragma unroll
-            for (int m = 0; m < 8; ++m) amax = max(amax, abs_bits(held[k][m]));
-        }
+        if (lane + 32 * k < pieces) amax = held[k].largest(amax);
 #pragma unroll 4
     for (int i = lane + 32 * kAppendHeld; i < pieces; i += 32) {
-        float v[8];
+        S8Piece<T> v;
         piece(i, v);
-#pragma unroll
-        for (int m = 0; m < 8; ++m) amax = max(amax, abs_bits(v[m]));
+        amax = v.largest(amax);
     }
+    amax = S8Piece<T>::bits(amax);
     amax = warp_max_u32(amax);
     float now = s8_scale(amax, kPageScaleFloor);
     if (kept && (old > now || old != old)) now = old;
@@ -108,15 +105,17 @@ __global__ void __launch_bounds__(kAppendThreads) k_kv8_append(const AppendParam
         }
     }
     int8_t* to = codes + kept * c.D;
-    auto store = [&](int i, const float (&v)[8]) {
-        *reinterpret_cast<uint2*>(to + i * 8) = make_uint2(s8_pack(v, r), s8_pack(v + 4, r));
+    auto store = [&](int i, const S8Piece<T>& v) {
+        float f[8];
+        v.values(f);
+        *reinterpret_cast<uint2*>(to + i * 8) = make_uint2(s8_pack(f, r), s8_pack(f + 4, r));
     };
 #pragma unroll
     for (int k = 0; k < kAppendHeld; ++k)
         if (lane + 32 * k < pieces) store(lane + 32 * k, held[k]);
 #pragma unroll 4
     for (int i = lane + 32 * kAppendHeld; i < pieces; i += 32) {
-        float v[8];
+        S8Piece<T> v;
         piece(i, v);
         store(i, v);
     }
