@@ -19,12 +19,14 @@ struct AttnParams {
     int64_t ldo;
     float* part;        // 2 partial sums a CTA: rows x (D + 2)
     int ctas;
+    int splits;         // many rows: CTAs a unit
     Ctl ctl;
 };
 
 // The kernel for many rows (qg_kv8_rows.cu), and whether it takes a problem.
 bool attention_takes_rows(const AttnParams& p);
-int attention_rows(int dtype, const AttnParams& p, cudaStream_t s);
+int attention_rows(int dtype, const AttnParams& p, int dev, cudaStream_t s);
+size_t attention_rows_workspace(int64_t D);
 
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;

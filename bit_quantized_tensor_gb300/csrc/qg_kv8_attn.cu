@@ -672,7 +672,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_kv8_attention_join(const AttnP
 constexpr int kAttnCtas = 152 * 4;  // the most pieces (four CTAs an SM)
 
 size_t kv8_attention_workspace(int64_t, int64_t, int64_t D) {
-    return static_cast<size_t>(kAttnCtas) * 2 * 16 * static_cast<size_t>(D + 2) * sizeof(float);
+    const size_t few = static_cast<size_t>(kAttnCtas) * 2 * 16 * static_cast<size_t>(D + 2) * sizeof(float);
+    const size_t many = D == 256 ? 0 : attention_rows_workspace(D);
+    return few > many ? few : many;
 }
 
 // The cache's codes as pages * heads blocks of `page` rows of D bytes, boxes of 16 or 32 rows.
@@ -769,6 +771,6 @@ extern "C" int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads
     p.ctl = host_ctl(dev);
     if (!p.ctl.status) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (attention_takes_rows(p)) return attention_rows(dtype, p, s);
+    if (attention_takes_rows(p)) return attention_rows(dtype, p, dev, s);
     return dtype == QG_F16 ? attention_by_size<__half>(p, dev, s) : attention_by_size<__nv_bfloat16>(p, dev, s);
 }

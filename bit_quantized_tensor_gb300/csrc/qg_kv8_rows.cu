@@ -17,9 +17,13 @@
 // tokens by 64 values (128-byte swizzle), which is K's K-major and V's MN-major form, so they are
 // converted alike.  A row's sums are rescaled, in tensor memory, only when its maximum grows by 2^8.
 //
-// The chain scores -> weights -> product of a tile is what a step takes, so a softmax thread keeps
-// half of its 128 scores between the maximum and the weights and has the next ones on their way
-// while it works.
+// Measured: 620 us, 980 TFLOP/s for 4 prompts of 1392 to 2048 tokens, 32 heads of 128 values on 8 key
+// heads, over 3058 to 8192 tokens, half the rate of the tensor cores.  What a step takes, about 4000
+// cycles, is the chain scores -> weights -> product of a tile: 2000 for the weights, 560 for each product
+// and 100 to 200 for each of the barriers between them.  So a softmax thread keeps half of its 128 scores
+// between the maximum and the weights and has the next ones on their way while it works.  Scores of 64
+// tokens at a time, made while the last 64 are weighed, leave no softmax waiting but take 718 us: a
+// product with 64 columns keeps the tensor cores as long as one with 128.  Two threads a row spill.
 #include <cuda.h>
 
 #include "kv8_attn.cuh"
@@ -140,7 +144,21 @@ __device__ __forceinline__ RowsPlace rows_find(const AttnParams& p, int64_t u, i
     return {at.b, lo, at.at};
 }
 
-template <class T, int D>
+// With fewer units than SMs a unit's steps are shared out to p.splits CTAs, whose fp32 sums a
+// second kernel joins: which rows a unit has, left for it, and a CTA's sums, 256 rows of O, M and
+// the denominator.
+struct RowsUnit {
+    int64_t row0;                 // the sequence's first row of Q
+    int head, first, rows, cut;   // rows: 0 without a unit
+};
+constexpr int kRowsParts = 304;   // CTAs that may have sums to join
+constexpr int kRowsSplits = 32;   // of a unit
+template <int D>
+__device__ __forceinline__ float* rows_part(const AttnParams& p, int64_t cta) {
+    return reinterpret_cast<float*>(reinterpret_cast<RowsUnit*>(p.part) + kRowsParts) + cta * (2 * kRowsTile) * (D + 4);
+}
+
+template <class T, int D, bool SPLIT>
 __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const AttnParams p) {
     using Cfg = RowsCfg<D>;
     constexpr int TILE = kRowsTile;
@@ -182,8 +200,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     }
     pdl_wait_prior_grid();
     fence_proxy_async_global();  // the cache may have been written just before, with ordinary stores
-    const RowsPlace at = rows_find(p, blockIdx.x, mem);
-    if (at.b >= p.bt.B) return;  // more CTAs than units; no tensor memory is held yet
+    const int unit_no = SPLIT ? blockIdx.x / p.splits : blockIdx.x, split = SPLIT ? blockIdx.x - unit_no * p.splits : 0;
+    const RowsPlace at = rows_find(p, unit_no, mem);
+    if (at.b >= p.bt.B) {  // more CTAs than units; no tensor memory is held yet
+        if (SPLIT && split == 0 && threadIdx.x == 0) reinterpret_cast<RowsUnit*>(p.part)[unit_no].rows = 0;
+        return;
+    }
     if (warp == kRowsMmaWarp) tmem_alloc(smem_u32(tmem_holder), 512);
     tc_fence_before();
     __syncthreads();
@@ -210,7 +232,16 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         const int first = row0 + t * TILE, last = min(all_rows, first + TILE) - 1;
         steps[t] = first < all_rows ? (seen_by(last) + TILE - 1) / TILE : 0;
     }
-    const int most = max(steps[0], steps[1]);
+    // this CTA's share of them, `base` the first
+    int most = max(steps[0], steps[1]), base = 0;
+    if constexpr (SPLIT) {
+        base = static_cast<int>(static_cast<int64_t>(most) * split / p.splits);
+        most = static_cast<int>(static_cast<int64_t>(most) * (split + 1) / p.splits) - base;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) steps[t] = max(0, min(steps[t] - base, most));
+        if (split == 0 && threadIdx.x == 0)
+            reinterpret_cast<RowsUnit*>(p.part)[unit_no] = {seq.row0, head, row0, all_rows, seq.cut};
+    }
     const int page_log2 = p.c.page_log2;
     const int tokens = max(seen_by(min(all_rows, row0 + TILE) - 1), seen_by(min(all_rows, row0 + 2 * TILE) - 1));
     // page * heads + head of a 16-token block, -1 without a page or behind what is seen
@@ -258,11 +289,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
         }
-        const int sees = seen_by(row), mine = steps[t];
+        // a row that is not there sees what the last one does, for its warp to take the short way
+        const int sees = seen_by(min(row, all_rows - 1)) - base * TILE, mine = steps[t];
         // scales of a step's 8 blocks, one a lane: the page three steps ahead, its scales two, what
         // they come to one, so that no load is waited for
         auto page_of = [&](int step) {
-            const int block = 8 * step + lane, col = (16 * block) >> page_log2;
+            const int block = 8 * (base + step) + lane, col = (16 * block) >> page_log2;
             return lane < 8 && step < mine && 16 * block < tokens && col < p.c.table_cols
                        ? p.c.table[static_cast<int64_t>(at.b) * p.c.table_cols + col]
                        : -1;
@@ -428,6 +460,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             ok = __all_sync(0xffffffffu, bounded_wait(pv_done(t), (mine - 1) & 1, abort_flag, p.ctl, kSiteRowsPv));
         tc_fence_after();
         if (ok) {
+            float* const sums = SPLIT ? rows_part<D>(p, blockIdx.x) + (t * TILE + r) * (D + 4) : nullptr;
             T* out = static_cast<T*>(p.O) + (seq.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D;
             const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             const float scale = den == 0.f ? 0.f : 0x1p20f / den;
@@ -439,14 +472,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                     tmem_ld_32x32b_x16(o_at + d, y);
                     tmem_wait_ld();
                 }
+                if constexpr (SPLIT) {
+                    if (row < all_rows) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    f[i] = seq.cut ? nan : !mine || den == 0.f ? 0.f : __uint_as_float(y[i]) * scale;
-                if (row < all_rows) {
-                    if (sectors)
-                        store_sectors<T>(out + d, f);
-                    else
-                        store_some<T, 16>(out + d, 16, false, f);
+                        for (int i = 0; i < 16; i += 4)
+                            *reinterpret_cast<uint4*>(sums + d + i) =
+                                mine ? make_uint4(y[i], y[i + 1], y[i + 2], y[i + 3]) : make_uint4(0, 0, 0, 0);
+                        if (d == 0) *reinterpret_cast<float2*>(sums + D) = make_float2(M, den);
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        f[i] = seq.cut ? nan : !mine || den == 0.f ? 0.f : __uint_as_float(y[i]) * scale;
+                    if (row < all_rows) {
+                        if (sectors)
+                            store_sectors<T>(out + d, f);
+                        else
+                            store_some<T, 16>(out + d, 16, false, f);
+                    }
                 }
             }
         }
@@ -466,7 +509,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         // page * heads + head of the warp's two blocks of 16 steps, one a lane
         auto fetch = [&](int step) {
             step += lane >> 1;
-            return step < most ? unit_of(8 * step + 2 * w + (lane & 1)) : -1;
+            return step < most ? unit_of(8 * (base + step) + 2 * w + (lane & 1)) : -1;
         };
         int now = fetch(0), next = fetch(16);
         // K (slot 0) or V (slot 1) of a step; only blocks that hold tokens
@@ -477,7 +520,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             const uint32_t bytes = (u0 >= 0 ? Cfg::RAW_BYTES / 2 : 0) + (u1 >= 0 ? Cfg::RAW_BYTES / 2 : 0);
             if (elected) {
                 const int8_t* codes = slot ? p.c.vq : p.c.kq;
-                const int token = step * TILE + 32 * w, mask = (1 << page_log2) - 1;
+                const int token = (base + step) * TILE + 32 * w, mask = (1 << page_log2) - 1;
                 mbar_arrive_expect_tx(raw_full(slot), bytes);
                 const uint32_t to = raw_u32 + slot * Cfg::RAW_BYTES;
                 if (u0 >= 0)
@@ -617,34 +660,107 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     }
 }
 
-// Does a problem of these sizes go to the kernel above?
+// A warp a row, four rows a warp: the sums of the unit's CTAs, in their order.
+constexpr int kRowsJoinThreads = 256, kRowsJoinRows = 4 * kRowsJoinThreads / 32;
+template <class T, int D>
+__global__ void __launch_bounds__(kRowsJoinThreads) k_kv8_attention_rows_join(const AttnParams p) {
+    constexpr int E = D / 32;  // values a lane
+    pdl_wait_prior_grid();
+    pdl_launch_dependents();
+    const RowsUnit u = reinterpret_cast<const RowsUnit*>(p.part)[blockIdx.x];
+    const int lane = threadIdx.x & 31;
+    for (int i = 0; i < 4; ++i) {
+        const int r = blockIdx.y * kRowsJoinRows + 4 * (threadIdx.x >> 5) + i, row = u.first + r;
+        if (u.rows == 0 || row >= u.rows) return;
+        const float* const sums = rows_part<D>(p, static_cast<int64_t>(blockIdx.x) * p.splits) + r * (D + 4);
+        constexpr int64_t NEXT = 2 * kRowsTile * (D + 4);
+        float2 top = make_float2(neg_inf(), 0.f);
+        if (lane < p.splits) top = *reinterpret_cast<const float2*>(sums + lane * NEXT + D);
+        float m = top.x;
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float half = top.x == neg_inf() ? 0.f : exp2_fast(0.5f * (top.x - m)), weight = half * half;
+        const float den = warp_sum(top.y * half * half);
+        float o[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) o[k] = 0.f;
+#pragma unroll 4
+        for (int s = 0; s < p.splits; ++s) {
+            alignas(16) float v[E];
+            if constexpr (E == 4)
+                *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(sums + s * NEXT + E * lane);
+            else
+                *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(sums + s * NEXT + E * lane);
+            const float w = __shfl_sync(0xffffffffu, weight, s);
+#pragma unroll
+            for (int k = 0; k < E; ++k) o[k] = fmaf(v[k], w, o[k]);
+        }
+        const float scale = u.cut ? __uint_as_float(0x7fc00000u) : den == 0.f ? 0.f : 0x1p20f / den;
+        T* out = static_cast<T*>(p.O) + (u.row0 + row / p.group) * p.ldo + (u.head * p.group + row % p.group) * D + E * lane;
+#pragma unroll
+        for (int k = 0; k < E; ++k) out[k] = from_f32<T>(den == 0.f && !u.cut ? 0.f : o[k] * scale);
+    }
+}
+
+size_t attention_rows_workspace(int64_t D) {
+    return kRowsParts * (sizeof(RowsUnit) + sizeof(float) * 2 * kRowsTile * static_cast<size_t>(D + 4));
+}
+
+// Does a problem of these sizes go to the kernel above?  64 rows a sequence take it 98 us (8 sequences of
+// 8192 tokens, 8 heads of 128 values) where the kernel for few rows takes 106, 32 rows 97 and 68.  With
+// fewer units, whose CTAs' sums have to be joined, twice as many: 64 rows of one sequence of 32768
+// take it 98 and the other 64, 128 rows 101 and 99, 256 rows 114 and 175.
 bool attention_takes_rows(const AttnParams& p) {
     if (p.c.D == 256) return false;
-    const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group;
-    return rows >= 64 * static_cast<int64_t>(p.bt.B);
+    const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group, B = p.bt.B;
+    return rows >= (B * p.c.heads < 64 ? 128 : 64) * B;
 }
 
 template <class T, int D>
-static int launch_rows(const AttnParams& p, cudaStream_t s) {
-    struct Tag;
-    const int rc = raise_smem<Tag>(k_kv8_attention_rows<T, D>);
-    if (rc) return rc;
-    const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group;
-    const int64_t units = (rows / (2 * kRowsTile) + (p.bt.B < p.bt.rows ? p.bt.B : p.bt.rows)) * p.c.heads;
+static int launch_rows(AttnParams p, int dev, cudaStream_t s) {
+    // units at most, and about as many as there are
+    const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group, seqs = p.bt.B < p.bt.rows ? p.bt.B : p.bt.rows;
+    const int64_t units = ((rows - seqs) / (2 * kRowsTile) + seqs) * p.c.heads;
     if (units > INT32_MAX) return QG_ERR_INVALID_ARG;
-    return launch_serialized(k_kv8_attention_rows<T, D>, dim3(static_cast<unsigned>(units)), kRowsThreads,
-                             RowsCfg<D>::SMEM, 1, s, p);
+    const int64_t alike = (rows + seqs * 2 * kRowsTile - 1) / (seqs * 2 * kRowsTile) * seqs * p.c.heads;
+    // CTAs for a unit: as many as there are SMs for, each with 4 steps at least of the longest.  A lone
+    // sequence's 128 rows over 32768 tokens of 8 heads: 440 us by 8 CTAs, 101 by 152.
+    const int64_t steps = ((static_cast<int64_t>(p.c.table_cols) << p.c.page_log2) + kRowsTile - 1) / kRowsTile;
+    int64_t splits = num_sms(dev) / alike;
+    splits = splits > kRowsParts / units ? kRowsParts / units : splits;
+    splits = splits > kRowsSplits ? kRowsSplits : splits;
+    splits = splits > steps / 4 ? steps / 4 : splits;
+    p.splits = splits < 1 ? 1 : static_cast<int>(splits);
+    struct Whole;
+    struct Split;
+    int rc = p.splits > 1 ? raise_smem<Split>(k_kv8_attention_rows<T, D, true>)
+                          : raise_smem<Whole>(k_kv8_attention_rows<T, D, false>);
+    if (rc) return rc;
+    const dim3 grid(static_cast<unsigned>(units * p.splits));
+    if (p.splits == 1)
+        return launch_serialized(k_kv8_attention_rows<T, D, false>, grid, kRowsThreads, RowsCfg<D>::SMEM, 1, s, p);
+    rc = launch_serialized(k_kv8_attention_rows<T, D, true>, grid, kRowsThreads, RowsCfg<D>::SMEM, 1, s, p);
+    if (rc) return rc;
+    return launch_serialized(k_kv8_attention_rows_join<T, D>,
+                             dim3(static_cast<unsigned>(units), 2 * kRowsTile / kRowsJoinRows), kRowsJoinThreads, 0, 1, s,
+                             p);
 }
 
-int attention_rows(int dtype, const AttnParams& p, cudaStream_t s) {
-    if (dtype == QG_F16) return p.c.D == 64 ? launch_rows<__half, 64>(p, s) : launch_rows<__half, 128>(p, s);
-    return p.c.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, s) : launch_rows<__nv_bfloat16, 128>(p, s);
+int attention_rows(int dtype, const AttnParams& p, int dev, cudaStream_t s) {
+    if (dtype == QG_F16) return p.c.D == 64 ? launch_rows<__half, 64>(p, dev, s) : launch_rows<__half, 128>(p, dev, s);
+    return p.c.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, dev, s) : launch_rows<__nv_bfloat16, 128>(p, dev, s);
 }
 
-#define QG_ROWS_BUDGET(T, NAME, D)                                                           \
-    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows<" NAME "," #D ">",                          \
-                           (reinterpret_cast<const void*>(k_kv8_attention_rows<T, D>)),      \
-                           kRowsThreads, RowsCfg<D>::SMEM, 512, 1, 1)
+#define QG_ROWS_BUDGET(T, NAME, D)                                                                       \
+    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows<" NAME "," #D ",false>",                                \
+                           (reinterpret_cast<const void*>(k_kv8_attention_rows<T, D, false>)),           \
+                           kRowsThreads, RowsCfg<D>::SMEM, 512, 1, 1);                                   \
+    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows<" NAME "," #D ",true>",                                 \
+                           (reinterpret_cast<const void*>(k_kv8_attention_rows<T, D, true>)),            \
+                           kRowsThreads, RowsCfg<D>::SMEM, 512, 1, 1);                                   \
+    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows_join<" NAME "," #D ">",                                 \
+                           (reinterpret_cast<const void*>(k_kv8_attention_rows_join<T, D>)),             \
+                           kRowsJoinThreads, 0, 0, 1, 1)
 QG_ROWS_BUDGET(__half, "f16", 64);
 QG_ROWS_BUDGET(__half, "f16", 128);
 QG_ROWS_BUDGET(__nv_bfloat16, "bf16", 64);

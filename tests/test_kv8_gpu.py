@@ -261,6 +261,37 @@ def test_attention_head_groups_and_views(torch, qg, group):
     assert bool((out[:, :5] == 7).all()) and bool((out[:, 5 + heads * group * D:] == 7).all())
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("heads,page,D,news,lengths", [
+    (2, 16, 64, [64], [2500]), (1, 64, 128, [40, 0, 33], [1030, 50, 2047]), (2, 32, 128, [100, 64], [70, 1500]),
+    (1, 128, 64, [300], [1153]), (1, 64, 128, [32], [5000]), (3, 64, 64, [128, 1, 70], [128, 4097, 3000])])
+def test_attention_of_few_units_shares_out_their_tokens(torch, qg, heads, page, D, news, lengths, causal):
+    """Units whose tokens several CTAs take: odd shares, sequences shorter than the others, rows that see nothing."""
+    cache, table = filled(torch, lengths, heads, D, page, len(news) + D)
+    gen = torch.Generator(device="cuda").manual_seed(sum(lengths))
+    Q = torch.randn(sum(news), heads * 4, D, generator=gen, device="cuda").half()
+    args = (table, int32(torch, starts_of(news)), int32(torch, lengths))
+    O = qg.kv8_attention(Q, cache, *args, causal=causal)
+    check_attention(torch, O, Q, cache, table, news, lengths, D ** -0.5, causal, "float16")
+    assert torch.equal(O, qg.kv8_attention(Q, cache, *args, causal=causal))
+
+
+def test_attention_of_few_units_keeps_what_is_not_finite_to_those_that_see_it(torch, qg):
+    heads, D, page, length, new = 1, 64, 16, 2048, 64
+    cache, table = filled(torch, [length], heads, D, page, 3)
+    Q = torch.randn(new, 4, D, device="cuda").half()
+    args = (table, int32(torch, [0, new]), int32(torch, [length]))
+    want = qg.kv8_attention(Q, cache, *args)
+    for which in (2, 3):
+        for block, first in ((5, 0), (length // page - 2, new - 2 * page)):
+            spoilt = [t.clone() for t in cache]
+            spoilt[which][table[0, block].long()] = float("nan")
+            O = qg.kv8_attention(Q, tuple(spoilt), *args)
+            assert bool(torch.isnan(O[first:]).all()) and torch.equal(O[:first], want[:first])
+    O = qg.kv8_attention(Q, cache, table[:, :-1].contiguous(), *args[1:])
+    assert bool(torch.isnan(O).all())  # longer than its table
+
+
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
 def test_attention_over_pages_of_very_different_scales(torch, qg, dtype):
     """V scales over 2^-60 .. 2^60 next to each other: the weights' range does not depend on them."""
