@@ -10,7 +10,9 @@ namespace qg {
 // magnitude of the page's new values, the page's new scale, its older codes rounded to
 // that scale if it grew, and the new codes.  Only the first page of a sequence's new
 // tokens can hold older ones; a page is started afresh with its token 0.  The warps of a
-// CTA share the page, which takes three dependent loads to find.
+// CTA share the page, which takes three dependent loads to find.  Measured, with the read of the same
+// pages behind it: one token each for 64 sequences (8 heads of 128 values) 10 us, 1333 tokens of 7
+// sequences 10 us; latency of two kernels of four or five dependent loads each.
 constexpr int kAppendThreads = 256, kAppendWarps = kAppendThreads / 32;
 constexpr int kAppendHeld = 4;  // pieces of 8 values that a lane keeps between the two passes
 

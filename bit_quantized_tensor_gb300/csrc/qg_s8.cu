@@ -15,8 +15,9 @@ namespace qg {
 
 // One row a group of TPR threads, CHUNKS pieces of 8 values a thread in registers; LONG: any
 // length, read twice.  OUT: int8_t (packed operand) or __half (the codes as fp16 numbers, the
-// tensor cores' operand).  Bound by the bytes it reads and writes, so few threads hold a row and
-// many rows are under way.
+// tensor cores' operand).  Bound by the bytes it reads and writes, so few threads hold a row, as it
+// lies in memory, and many rows are under way.  Measured: 4096 x 8192 bf16 15.0 us, 6.7 TB/s; 777 x
+// 2304 f16 2.5 us; rows read twice 4.3 TB/s of what they have to move.
 template <class OUT>
 __device__ __forceinline__ void store_codes(OUT* dst, const float (&x)[8], float r) {
     if constexpr (sizeof(OUT) == 1) {
@@ -106,19 +107,25 @@ static int launch_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, OUT
 // columns.  A CTA takes 16 weight rows, its 16 warps every 16th block of 64 values
 // along K; a thread's bytes of a row (16 at a time) are the values of four MMA steps,
 // since a sum does not depend on the order of k.  Sums of a few blocks are exact in
-// fp32; they are added up in 32-bit integers, over the warps as well.  One or two tokens
-// are quantized by every CTA for itself into shared memory (QUANT), which costs less
-// than a kernel ahead of this one but about 1 us a token; more come as codes, straight into
-// registers.
+// fp32; they are added up in 32-bit integers, over the warps as well.  A lone token
+// is quantized by every CTA for itself into shared memory (QUANT), which costs less
+// than a kernel ahead of this one; more come as codes, straight into registers (2 tokens
+// inside 6.5 us, with that kernel 6.3).
+//
+// Measured, linear of 4096 x 4096 in a chain of calls: 1 token 5.6 us (3.0 TB/s of weights),
+// 4 and 8 with the quantizer's kernel 6.4 and 6.7, by the next kernel 9.8; 16 tokens by
+// that 9.9 (by this one, with two columns of tokens, 11); 8192 x 8192 17.0 us for 1 token (3.9 TB/s), 8 tokens 20.3.
+// Latency: a CTA's weights are one or two rounds of loads, and none of them goes out before the
+// kernel ahead has ended.
 constexpr int kGemvWarps = 16, kGemvThreads = 32 * kGemvWarps;
 constexpr int kGemvBatch = 4;            // blocks of 64 values in flight a thread
-constexpr int kGemvTokens = 8, kGemvQuantTokens = 2;
+constexpr int kGemvTokens = 8;
 constexpr size_t kGemvSmem = 100 * 1024;  // two CTAs an SM
 
-__host__ __device__ inline int64_t gemv_token_stride(int64_t K) { return (K + 63) / 64 * 64 + 16; }
-// Are M tokens quantized inside the product's kernel?  Their codes have to fit its shared memory.
+__host__ __device__ inline int64_t gemv_token_bytes(int64_t K) { return (K + 63) / 64 * 64 + 16; }
+// Is a lone token quantized inside the product's kernel?  Its codes have to fit the shared memory.
 static bool gemv_quantizes(int64_t M, int64_t K) {
-    return M <= kGemvQuantTokens && static_cast<size_t>(M * gemv_token_stride(K)) <= kGemvSmem;
+    return M == 1 && static_cast<size_t>(gemv_token_bytes(K)) <= kGemvSmem;
 }
 
 struct GemvParams {
@@ -146,13 +153,12 @@ __device__ __forceinline__ uint4 first_bytes(uint4 w, int n) {
 template <class T, bool QUANT>
 __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p) {
     extern __shared__ __align__(16) uint8_t codes[];
-    __shared__ uint32_t red_max[kGemvQuantTokens][kGemvWarps];
+    __shared__ uint32_t red_max[kGemvWarps];
     __shared__ float token_scale[kGemvTokens];
     __shared__ int sums[kGemvWarps][4][32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int n0 = blockIdx.x * 16;
     const int blocks = (p.ldq + 63) / 64;
-    const int stride = static_cast<int>(gemv_token_stride(p.ldq));
     const bool has0 = n0 + g < p.N, has1 = n0 + g + 8 < p.N;
     const int8_t* const w0 = p.W + static_cast<int64_t>(n0 + g) * p.ldq + 16 * t;
     const int8_t* const w1 = w0 + 8 * static_cast<int64_t>(p.ldq);
@@ -191,29 +197,37 @@ __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p)
     load(warp);
 
     if constexpr (QUANT) {
-        for (int m = 0; m < p.M; ++m) {
-            const T* x = static_cast<const T*>(p.X) + m * p.ldx;
-            uint32_t amax = 0;
-            for (int k = 8 * threadIdx.x; k < p.K; k += 8 * kGemvThreads) {
-                float v[8];
-                load_some<T, 8>(x + k, p.K - k, p.x_aligned, v);
+        const T* x = static_cast<const T*>(p.X);
+        auto at = [&](int i) { return 8 * (static_cast<int>(threadIdx.x) + i * kGemvThreads); };
+        const int pieces = (64 * blocks + 8 * kGemvThreads - 1) / (8 * kGemvThreads);
+        constexpr int HELD = sizeof(T) == 4 ? 1 : 2;  // pieces that a thread keeps
+        S8Piece<T> held[HELD], v;
+        uint32_t amax = 0;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) amax = max(amax, abs_bits(v[i]));
-            }
-            amax = warp_max_u32(amax);
-            if (lane == 0) red_max[m][warp] = amax;
+        for (int i = 0; i < HELD; ++i) held[i].load(x + at(i), p.K - at(i), p.x_aligned);
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) amax = held[i].largest(amax);
+        for (int i = HELD; i < pieces; ++i) {
+            v.load(x + at(i), p.K - at(i), p.x_aligned);
+            amax = v.largest(amax);
         }
+        amax = warp_max_u32(S8Piece<T>::bits(amax));
+        if (lane == 0) red_max[warp] = amax;
         __syncthreads();
-        for (int m = 0; m < p.M; ++m) {
-            const T* x = static_cast<const T*>(p.X) + m * p.ldx;
-            const uint32_t amax = warp_max_u32(red_max[m][lane & (kGemvWarps - 1)]);
-            const float s = s8_scale(amax, kRowScaleFloor), r = s8_inverse(s);
-            if (threadIdx.x == 0) token_scale[m] = s;
-            for (int k = 8 * threadIdx.x; k < 64 * blocks; k += 8 * kGemvThreads) {
-                float v[8];
-                load_some<T, 8>(x + k, p.K - k, p.x_aligned, v);
-                store_codes(reinterpret_cast<int8_t*>(codes) + m * stride + k, v, r);
-            }
+        amax = warp_max_u32(red_max[lane & (kGemvWarps - 1)]);
+        const float s = s8_scale(amax, kRowScaleFloor), r = s8_inverse(s);
+        if (threadIdx.x == 0) token_scale[0] = s;
+        auto store = [&](int i, const S8Piece<T>& w) {
+            if (at(i) >= 64 * blocks) return;
+            float f[8];
+            w.values(f);
+            store_codes(reinterpret_cast<int8_t*>(codes) + at(i), f, r);
+        };
+#pragma unroll
+        for (int i = 0; i < HELD; ++i) store(i, held[i]);
+        for (int i = HELD; i < pieces; ++i) {
+            v.load(x + at(i), p.K - at(i), p.x_aligned);
+            store(i, v);
         }
         __syncthreads();
     } else {
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p)
             if (b >= blocks) break;
             uint4 x;
             if constexpr (QUANT)
-                x = g < p.M ? *reinterpret_cast<const uint4*>(codes + g * stride + 64 * b + 16 * t) : make_uint4(0, 0, 0, 0);
+                x = g == 0 ? *reinterpret_cast<const uint4*>(codes + 64 * b + 16 * t) : make_uint4(0, 0, 0, 0);
             else
                 x = xc[j];
             const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
@@ -274,7 +288,7 @@ static int launch_gemv(const GemvParams& p, cudaStream_t s) {
         const int rc = raise_smem<Tag>(k_s8_gemv<T, true>);
         if (rc) return rc;
         return launch_serialized(k_s8_gemv<T, true>, grid, kGemvThreads,
-                                 static_cast<size_t>(p.M * gemv_token_stride(p.ldq)), 1, s, p);
+                                 static_cast<size_t>(gemv_token_bytes(p.ldq)), 1, s, p);
     } else {
         return launch_serialized(k_s8_gemv<T, false>, grid, kGemvThreads, 0, 1, s, p);
     }
@@ -322,7 +336,11 @@ static SomeForm some_form(int64_t M, int64_t N, int64_t K, int64_t* cycles) {
 
 // Does that kernel take the problem, or the one on CTA pairs, behind a pass that writes the
 // weights as fp16?  The latter's estimate: that pass at 6.2 TB/s (3.3 kB a cycle) and rounds of
-// 256 x 256 tiles, 630 cycles a step of 64 values of K.
+// 256 x 256 tiles, 630 cycles a step of 64 values of K.  Measured, linear of 4096 x 4096, this kernel and
+// pairs: 128 tokens 16.3 and 33.6 us, 512 27.8 and 35.7, 777 49.5 and 36.6, 2048 98 and 60; of 1024 x 8192: 777
+// tokens 33 and 53, 2048 62 and 60; of 8192 x 8192: 256 tokens 57.5 and 80.6, 512 113 and 83.  The choice was within 3% of the
+// better one at 45 sizes.  4096 x 8192 x 8192 by pairs 344 us, 1.6 PFLOP/s, of which the product takes 289 (1.9),
+// the weights' pass 28 and the quantizer 19.
 static bool takes_some(int64_t M, int64_t N, int64_t K) {
     if (M > 4096 || !some_holds(SomeForm{32, 8}, K)) return false;
     int64_t cycles = 0;
