@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kGemvThreads, 2) k_s8_gemv(const GemvParams p)
         if (m < p.M && n < p.N) {
             const float b = p.bias ? to_f32<T>(static_cast<const T*>(p.bias)[n]) : 0.f;
             static_cast<T*>(p.Y)[m * p.ldy + n] =
-                from_f32<T>(fmaf(static_cast<float>(sum) * token_scale[m], p.sb[n], b));
+                from_f32<T>(s8_scaled(sum, token_scale[m], p.sb[n], b));
         }
     }
 }

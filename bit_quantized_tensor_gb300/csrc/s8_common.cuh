@@ -42,6 +42,13 @@ __device__ __forceinline__ float s8_number(float x, float r) {
     return r == 0.f ? 0.f : __fadd_rn(s8_shifted(x, r), -12582912.f);
 }
 
+// sum sa sb + bias, the smaller scale first: fl(sum) times the larger one alone can be infinite where the
+// result is not.  Scales that are NaN stay.
+__device__ __forceinline__ float s8_scaled(int sum, float sa, float sb, float bias) {
+    const bool less = sa < sb;
+    return fmaf(static_cast<float>(sum) * (less ? sa : sb), less ? sb : sa, bias);
+}
+
 // Four whole numbers' low bytes in a word, the first in the low byte.
 __device__ __forceinline__ uint32_t pack_s8(int a, int b, int c, int d) {
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);

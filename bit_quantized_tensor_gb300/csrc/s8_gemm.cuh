@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kS8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) f[i] = c + i < c1 ? p.sa[m0 + c + i] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) f[i] = fmaf(static_cast<float>(v[i]) * f[i], sb, bias);
+        for (int i = 0; i < 16; ++i) f[i] = s8_scaled(v[i], f[i], sb, bias);
         if (n >= p.N) return;
         auto all = [&](auto* y) {
             using Y = std::remove_pointer_t<decltype(y)>;

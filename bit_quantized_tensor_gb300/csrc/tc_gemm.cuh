@@ -34,6 +34,7 @@
 
 #include "qg_gemm_host.h"
 #include "qg_ptx.cuh"
+#include "s8_common.cuh"
 
 namespace qg {
 
@@ -232,18 +233,25 @@ __device__ __forceinline__ void store_row_s32(int32_t* dst, int col0, int N_tota
     }
 }
 
-// N columns of a row of integer sums, scaled, to column `row` of the output.  The kernel is
-// launched behind its inputs, so the scales may be read as constants (ahead of the stores).
+// A scale, which nothing writes while the kernel runs: such a load may go ahead of the stores around it,
+// but, being volatile, not ahead of the wait for the kernel that wrote it.
+__device__ __forceinline__ float load_scale(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
+// N columns of a row of integer sums, scaled, to column `row` of the output.
 template <class T, int N>
 __device__ __forceinline__ void store_row_s8(T* y, int64_t ldy, int col0, int cols, const int32_t* v, const S8Scales& e,
                                              int row) {
-    const float sb = __ldg(e.sb + row);
+    const float sb = load_scale(e.sb + row);
     float bias = 0.f;
     if (e.bias) bias = static_cast<float>(static_cast<const T*>(e.bias)[row]);
     T* at = y + static_cast<int64_t>(col0) * ldy + row;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
-        if (col0 + c < cols) *at = static_cast<T>(fmaf(static_cast<float>(v[c]) * __ldg(e.sa + col0 + c), sb, bias));
+        if (col0 + c < cols) *at = static_cast<T>(s8_scaled(v[c], load_scale(e.sa + col0 + c), sb, bias));
         at += ldy;
     }
 }

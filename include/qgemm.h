@@ -578,8 +578,8 @@ int s8_quantize(int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, int
                 void* stream);
 
 /* Y (M x N, `dtype`) = As[m] Bs[n] sum_k Aq[m][k] Bq[n][k] + bias[n]: the integer
- * sum is exact, then rounded to fp32, multiplied by As and in one fused step by Bs
- * with the bias added, and rounded to `dtype`.  bias: N values of `dtype` or NULL.
+ * sum is exact, then rounded to fp32, multiplied by the smaller of As[m] and Bs[n] and
+ * in one fused step by the other with the bias added, and rounded to `dtype`.  bias: N values of `dtype` or NULL.
  *  ws: qg_workspace_size(QG_OP_S8_LINEAR, M, N, K) bytes, 256-byte aligned; 0 bytes
  *      (ws may be NULL) for one token, K up to 102336. */
 int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const float* As,
@@ -605,7 +605,8 @@ int s8_linear(int dtype, int64_t M, int64_t N, int64_t K, const void* X, int64_t
  *                 ld apart: a view of a packed product's rows is one.  Hk may be 0.
  *  gq, gk       : D values of wdtype (that of Q, or QG_F32), NULL = 1
  *  rq, rk       : T x Hq (T x Hk) fp32, contiguous, or NULL
- *  D <= 1024, R even, 0 <= R <= D.  Yq may be Q and Yk K (in place). */
+ *  D <= 1024, R even, 0 <= R <= D.  Yq may be Q and Yk K (in place).  sum(x^2) is an
+ *  fp32 sum: infinite, and z 0, from magnitudes of about 2^64 / sqrt(D) on. */
 typedef enum { QG_ROPE_HALF = 0, QG_ROPE_PAIRS = 1 } qg_rope_style;
 int qk_norm_rope(int dtype, int style, int64_t T, int64_t Hq, int64_t Hk, int64_t D, int64_t R,
                  const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* gq,
@@ -669,6 +670,7 @@ int kv8_gather(int dtype, int64_t B, int64_t rows, int64_t heads, int64_t D, con
  *  causal : row i of a sequence with n rows sees its tokens up to lengths - n + i, else
  *         all of them.  A row that sees no token is 0; rows of a sequence that is longer
  *         than its table are NaN.
+ *  Scales are what kv8_append writes: 2^-64 to 2^121, or NaN.  O and Q do not overlap.
  *  ws: qg_workspace_size(QG_OP_KV8_ATTENTION, rows, q_heads, D) bytes, 256-byte aligned */
 int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads, int64_t heads, int64_t D,
                   const void* Q, int64_t ldq, const int8_t* kq, const int8_t* vq, const float* ks,

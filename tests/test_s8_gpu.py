@@ -117,6 +117,18 @@ def test_sums_are_exact_at_their_largest(torch, qg):
         assert torch.equal(Y, want.float().expand(M, N))
 
 
+def test_scales_whose_product_with_the_sum_alone_leaves_fp32(torch, qg):
+    """Tokens near fp32's largest against weights near its smallest scales, in every kernel, and the other way round."""
+    for M, N, K in ((1, 40, 512), (5, 40, 512), (60, 40, 512), (1500, 2100, 512)):
+        for x, w in ((118, -90), (-90, 118)):
+            X, W = (on_gpu(torch, values(r, K, r), "float32") * 2.0 ** f for r, f in ((M, x), (N, w)))
+            Wq, Ws = qg.s8_quantize(W)
+            (qa, sa), (qb, sb) = ref.s8_quantize(as_np(X)), ref.s8_quantize(as_np(W))
+            Y = qg.s8_linear(X, Wq, Ws)
+            assert bool(torch.isfinite(Y).all())
+            check_product(Y, qa, sa, qb, sb, None, "float32")
+
+
 def test_what_lies_behind_k_does_not_count(torch, qg):
     for M in (2, 40):
         X, W = on_gpu(torch, values(M, 100, 1), "bfloat16"), on_gpu(torch, values(50, 100, 2), "float32")
