@@ -1239,10 +1239,11 @@ def qk_norm_rope_backward(dYq, dYk, Q, K, gq, gk, positions, table, rq, rk, styl
 # ---------------------------------------------------------------- paged cache in 8 bits
 
 def kv8_cache(pages: int, heads: int, page: int = 64, D: int = 128, device="cuda"):
-    """An empty cache (kq, vq, ks, vs): codes pages x heads x page x D (int8), scales pages x heads (fp32), for K and V."""
+    """An empty cache (kq, vq, ks, vs): codes pages x heads x page x D (int8), scales pages x heads (fp32), for K and V.
+    Its tokens are zeros under the smallest scale."""
     torch = _torch()
     kq, vq = (torch.zeros((pages, heads, page, D), dtype=torch.int8, device=device) for _ in range(2))
-    ks, vs = (torch.zeros((pages, heads), dtype=torch.float32, device=device) for _ in range(2))
+    ks, vs = (torch.full((pages, heads), 2.0 ** -64, dtype=torch.float32, device=device) for _ in range(2))
     return kq, vq, ks, vs
 
 
@@ -1341,7 +1342,7 @@ def kv8_attention(Q, cache, table, starts, lengths, scale=None, causal: bool = T
     dt = _dtype_id(Q.dtype, "Q")
     B, heads, D, args = _kv8(cache, table, starts, lengths, dev)
     rows, q_heads, d = Q.shape
-    if d != D or q_heads % heads:
+    if d != D or heads < 1 or q_heads % heads:
         raise ValueError(f"Q must be rows x a multiple of {heads} heads x {D}")
     if O is None:
         O = torch.empty((rows, q_heads, D), dtype=Q.dtype, device=dev)

@@ -20,11 +20,12 @@ struct AttnParams {
     float* part;        // 2 partial sums a CTA: rows x (D + 2)
     int ctas;
     int splits;         // many rows: CTAs a unit
+    int from;           // sequences of so many rows and more go to the kernel for many rows
     Ctl ctl;
 };
 
 // The kernel for many rows (qg_kv8_rows.cu), and whether it takes a problem.
-bool attention_takes_rows(const AttnParams& p);
+int attention_rows_from(const AttnParams& p);
 int attention_rows(int dtype, const AttnParams& p, int dev, cudaStream_t s);
 size_t attention_rows_workspace(int64_t D);
 
@@ -40,6 +41,8 @@ constexpr float kLowWeight = 0x1p-100f;
 // between 2^-101 and 2^92; as M moves they are multiplied by 2^(d / 2) twice, since 2^d alone may
 // be below fp32's range where the result is not.
 constexpr float kDenPower = 20.f;
+// log2 of a page's scale; zeros of a page that nothing was written to count like the smallest.
+__device__ __forceinline__ float page_log2_of(float s) { return s <= kPageScaleFloor ? -64.f : __log2f(s); }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xff800000u); }
 
 __device__ __forceinline__ uint32_t elect_lane() {

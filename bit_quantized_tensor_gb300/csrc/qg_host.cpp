@@ -513,6 +513,7 @@ inline Cache cache(PyObject* o, PyObject* table, PyObject* starts, PyObject* len
     Cache c;
     c.pages = kq.size(0), c.heads = kq.size(1), c.page = kq.size(2), c.D = kq.size(3);
     c.B = t.size(0), c.cols = t.size(1);
+    need(c.heads > 0);
     auto scales = [&](PyObject* s) {
         const at::Tensor& v = tensor(s);
         need(v.device() == dev && v.scalar_type() == at::kFloat && v.dim() == 2 && v.size(0) == c.pages &&

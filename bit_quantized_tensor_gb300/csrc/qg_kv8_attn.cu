@@ -71,6 +71,7 @@ __device__ __forceinline__ AttnSeq attn_seq(const AttnParams& p, int b) {
     AttnSeq a;
     a.s = kv8_seq(p.bt, p.c, b);
     a.rows = a.s.n * p.group;
+    if (a.rows >= p.from) a.rows = 0;  // the other kernel's
     a.row_tiles = (a.rows + 8 * NB - 1) / (8 * NB);
     a.tiles = max(1, (a.s.len + kAttnTile - 1) / kAttnTile);
     return a;
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
                     h.sk = p.c.ks[h.unit];
                     sv = p.c.vs[h.unit];
                 }
-                h.lsv = __log2f(sv);
+                h.lsv = page_log2_of(sv);
                 h.isv = exp2_fast(kDenPower - h.lsv);
             }
             return h;
@@ -775,6 +776,10 @@ extern "C" int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads
     p.ctl = host_ctl(dev);
     if (!p.ctl.status) return QG_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (attention_takes_rows(p)) return attention_rows(dtype, p, dev, s);
+    p.from = attention_rows_from(p);
+    if (p.from <= p.bt.rows * static_cast<int64_t>(p.group)) {
+        rc = attention_rows(dtype, p, dev, s);
+        if (rc || p.from == 1) return rc;
+    }
     return dtype == QG_F16 ? attention_by_size<__half>(p, dev, s) : attention_by_size<__nv_bfloat16>(p, dev, s);
 }

@@ -85,9 +85,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // Units of a sequence: key heads times pairs of row tiles, of which those of the last rows see
 // most.  How many take at least `steps` steps of 128 tokens:
+template <bool SOME>  // only those of sequences that come here
 __device__ __forceinline__ int64_t rows_units(const AttnParams& p, int b, int steps) {
     const Kv8Seq s = kv8_seq(p.bt, p.c, b);
     const int64_t rows = static_cast<int64_t>(s.n) * p.group, pairs = (rows + 2 * kRowsTile - 1) / (2 * kRowsTile);
+    if (SOME && rows < p.from) return 0;
     int64_t from = 0;  // first pair of tiles
     if (steps > 0) {
         const int64_t tokens = static_cast<int64_t>(steps - 1) * kRowsTile;  // to see more than these
@@ -118,10 +120,11 @@ struct RowsPlace {
     int b, steps;
     int64_t at;
 };
+template <bool SOME>
 __device__ __forceinline__ RowsPlace rows_find(const AttnParams& p, int64_t u, int64_t* mem) {
     auto at_least = [&](int steps) {
         int64_t mine = 0;
-        for (int b = threadIdx.x; b < p.bt.B; b += kRowsThreads) mine += rows_units(p, b, steps);
+        for (int b = threadIdx.x; b < p.bt.B; b += kRowsThreads) mine += rows_units<SOME>(p, b, steps);
         return rows_sum(mine, mem);
     };
     if (at_least(0) <= u) return {p.bt.B, 0, 0};
@@ -139,11 +142,12 @@ __device__ __forceinline__ RowsPlace rows_find(const AttnParams& p, int64_t u, i
         }
     }
     const Kv8Place at = kv8_find<kRowsThreads>(p.bt.B, u - longer, 0, mem, [&](int b) {
-        return rows_units(p, b, lo) - rows_units(p, b, lo + 1);
+        return rows_units<SOME>(p, b, lo) - rows_units<SOME>(p, b, lo + 1);
     });
     return {at.b, lo, at.at};
 }
 
+// SPLIT: the form that looks at p.splits and p.from (their registers cost the other one 4%).
 // With fewer units than SMs a unit's steps are shared out to p.splits CTAs, whose fp32 sums a
 // second kernel joins: which rows a unit has, left for it, and a CTA's sums, 256 rows of O, M and
 // the denominator.
@@ -201,9 +205,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     pdl_wait_prior_grid();
     fence_proxy_async_global();  // the cache may have been written just before, with ordinary stores
     const int unit_no = SPLIT ? blockIdx.x / p.splits : blockIdx.x, split = SPLIT ? blockIdx.x - unit_no * p.splits : 0;
-    const RowsPlace at = rows_find(p, unit_no, mem);
+    const RowsPlace at = rows_find<SPLIT>(p, unit_no, mem);
     if (at.b >= p.bt.B) {  // more CTAs than units; no tensor memory is held yet
-        if (SPLIT && split == 0 && threadIdx.x == 0) reinterpret_cast<RowsUnit*>(p.part)[unit_no].rows = 0;
+        if (SPLIT && p.splits > 1 && split == 0 && threadIdx.x == 0) reinterpret_cast<RowsUnit*>(p.part)[unit_no].rows = 0;
         return;
     }
     if (warp == kRowsMmaWarp) tmem_alloc(smem_u32(tmem_holder), 512);
@@ -219,7 +223,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     const int heads = p.c.heads, all_rows = seq.n * p.group;
     const int head = static_cast<int>(at.at % heads);
     const int pairs = (all_rows + 2 * TILE - 1) / (2 * TILE);
-    const int longer = static_cast<int>(rows_units(p, at.b, at.steps + 1) / heads);
+    const int longer = static_cast<int>(rows_units<false>(p, at.b, at.steps + 1) / heads);
     const int row0 = (pairs - 1 - longer - static_cast<int>(at.at / heads)) * 2 * TILE;
     auto seen_by = [&](int row) {
         const int64_t n = p.causal ? seq.first + row / p.group + 1 : seq.len;
@@ -239,7 +243,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         most = static_cast<int>(static_cast<int64_t>(most) * (split + 1) / p.splits) - base;
 #pragma unroll
         for (int t = 0; t < 2; ++t) steps[t] = max(0, min(steps[t] - base, most));
-        if (split == 0 && threadIdx.x == 0)
+        if (p.splits > 1 && split == 0 && threadIdx.x == 0)
             reinterpret_cast<RowsUnit*>(p.part)[unit_no] = {seq.row0, head, row0, all_rows, seq.cut};
     }
     const int page_log2 = p.c.page_log2;
@@ -304,7 +308,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             return page >= 0 && page < p.c.pages ? make_float2(p.c.ks[unit], p.c.vs[unit]) : make_float2(nan, nan);
         };
         auto keep = [&](int step, float2 v) {
-            if (lane < 8) scales[warp][step & 1][lane] = make_float2(v.x, __log2f(v.y));
+            if (lane < 8) scales[warp][step & 1][lane] = make_float2(v.x, page_log2_of(v.y));
             __syncwarp();
         };
         keep(0, scales_of(page_of(0)));
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             ok = __all_sync(0xffffffffu, bounded_wait(pv_done(t), (mine - 1) & 1, abort_flag, p.ctl, kSiteRowsPv));
         tc_fence_after();
         if (ok) {
-            float* const sums = SPLIT ? rows_part<D>(p, blockIdx.x) + (t * TILE + r) * (D + 4) : nullptr;
+            float* const sums = SPLIT && p.splits > 1 ? rows_part<D>(p, blockIdx.x) + (t * TILE + r) * (D + 4) : nullptr;
             T* out = static_cast<T*>(p.O) + (seq.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D;
             const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             const float scale = den == 0.f ? 0.f : 0x1p20f / den;
@@ -472,7 +476,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                     tmem_ld_32x32b_x16(o_at + d, y);
                     tmem_wait_ld();
                 }
-                if constexpr (SPLIT) {
+                if (SPLIT && p.splits > 1) {
                     if (row < all_rows) {
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
@@ -706,20 +710,27 @@ size_t attention_rows_workspace(int64_t D) {
     return kRowsParts * (sizeof(RowsUnit) + sizeof(float) * 2 * kRowsTile * static_cast<size_t>(D + 4));
 }
 
-// Does a problem of these sizes go to the kernel above?  64 rows a sequence take it 98 us (8 sequences of
-// 8192 tokens, 8 heads of 128 values) where the kernel for few rows takes 106, 32 rows 97 and 68.  With
-// fewer units, whose CTAs' sums have to be joined, twice as many: 64 rows of one sequence of 32768
-// take it 98 and the other 64, 128 rows 101 and 99, 256 rows 114 and 175.
-bool attention_takes_rows(const AttnParams& p) {
-    if (p.c.D == 256) return false;
+// How many rows a sequence has to have for the kernel above; 1: all sequences go to it, INT32_MAX:
+// none.  64 rows a sequence take it 98 us (8 sequences of 8192 tokens, 8 heads of 128 values) where
+// the kernel for few rows takes 106, 32 rows 97 and 68.  With fewer units, whose CTAs' sums have to be
+// joined, twice as many: 64 rows of one sequence of 32768 take it 98 and the other 64, 128 rows 101
+// and 99, 256 rows 114 and 175.  A batch of fewer rows a sequence may still hold a prompt (512 tokens
+// next to 63 single ones over 8192 tokens: 492 us by the kernel for few rows alone, 350 by both), which the host cannot
+// see: both kernels run once what is over one token a sequence makes four units, and cost batches
+// that are all alike 5 us.
+int attention_rows_from(const AttnParams& p) {
+    if (p.c.D == 256) return INT32_MAX;
     const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group, B = p.bt.B;
-    return rows >= (B * p.c.heads < 64 ? 128 : 64) * B;
+    const int from = B * p.c.heads < 64 ? 128 : 64;
+    if (rows >= B * from) return 1;
+    return B > 1 && (p.bt.rows - B) * p.group >= 8 * kRowsTile ? from : INT32_MAX;
 }
 
 template <class T, int D>
 static int launch_rows(AttnParams p, int dev, cudaStream_t s) {
     // units at most, and about as many as there are
-    const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group, seqs = p.bt.B < p.bt.rows ? p.bt.B : p.bt.rows;
+    const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group, holds = p.from > 1 ? rows / p.from : p.bt.rows;
+    const int64_t seqs = p.bt.B < holds ? p.bt.B : holds;
     const int64_t units = ((rows - seqs) / (2 * kRowsTile) + seqs) * p.c.heads;
     if (units > INT32_MAX) return QG_ERR_INVALID_ARG;
     const int64_t alike = (rows + seqs * 2 * kRowsTile - 1) / (seqs * 2 * kRowsTile) * seqs * p.c.heads;
@@ -733,14 +744,15 @@ static int launch_rows(AttnParams p, int dev, cudaStream_t s) {
     p.splits = splits < 1 ? 1 : static_cast<int>(splits);
     struct Whole;
     struct Split;
-    int rc = p.splits > 1 ? raise_smem<Split>(k_kv8_attention_rows<T, D, true>)
-                          : raise_smem<Whole>(k_kv8_attention_rows<T, D, false>);
+    const bool split = p.splits > 1 || p.from > 1;
+    int rc = split ? raise_smem<Split>(k_kv8_attention_rows<T, D, true>)
+                   : raise_smem<Whole>(k_kv8_attention_rows<T, D, false>);
     if (rc) return rc;
     const dim3 grid(static_cast<unsigned>(units * p.splits));
-    if (p.splits == 1)
+    if (!split)
         return launch_serialized(k_kv8_attention_rows<T, D, false>, grid, kRowsThreads, RowsCfg<D>::SMEM, 1, s, p);
     rc = launch_serialized(k_kv8_attention_rows<T, D, true>, grid, kRowsThreads, RowsCfg<D>::SMEM, 1, s, p);
-    if (rc) return rc;
+    if (rc || p.splits == 1) return rc;
     return launch_serialized(k_kv8_attention_rows_join<T, D>,
                              dim3(static_cast<unsigned>(units), 2 * kRowsTile / kRowsJoinRows), kRowsJoinThreads, 0, 1, s,
                              p);

@@ -276,6 +276,20 @@ def test_attention_of_few_units_shares_out_their_tokens(torch, qg, heads, page, 
     assert torch.equal(O, qg.kv8_attention(Q, cache, *args, causal=causal))
 
 
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+@pytest.mark.parametrize("heads,D,group,causal", [(2, 64, 4, True), (1, 128, 8, True), (2, 128, 1, False), (1, 64, 20, True)])
+def test_prompts_next_to_single_tokens(torch, qg, heads, D, group, causal, dtype):
+    """Sequences for either kernel in one batch, with some at the border between them and some without rows."""
+    news = [1, 300, 0, 16, 15, 1, 33, 128, 2, 0, 127, 1]
+    lengths = [700, 300, 50, 16, 1030, 1, 33, 2000, 5, 0, 1500, 0]
+    cache, table = filled(torch, lengths, heads, D, 32, 11)
+    gen = torch.Generator(device="cuda").manual_seed(group)
+    Q = torch.randn(sum(news), heads * group, D, generator=gen, device="cuda").to(getattr(torch, dtype))
+    args = (table, int32(torch, starts_of(news)), int32(torch, lengths))
+    O = qg.kv8_attention(Q, cache, *args, causal=causal)
+    check_attention(torch, O, Q, cache, table, news, lengths, D ** -0.5, causal, dtype)
+
+
 def test_attention_of_few_units_keeps_what_is_not_finite_to_those_that_see_it(torch, qg):
     heads, D, page, length, new = 1, 64, 16, 2048, 64
     cache, table = filled(torch, [length], heads, D, page, 3)
@@ -319,6 +333,22 @@ def test_attention_counts_tokens_of_small_scales_next_to_large_ones(torch, qg, n
         Q = (sharp * torch.randn(news, heads * 4, D, generator=gen, device="cuda")).bfloat16()
         O = qg.kv8_attention(Q, cache, table, int32(torch, [0, news]), int32(torch, [length]))
         check_attention(torch, O, Q, cache, table, [news], [length], D ** -0.5, True, "bfloat16")
+
+
+@pytest.mark.parametrize("new", [1, 64])
+def test_tokens_that_nothing_was_written_to_are_zeros(torch, qg, new):
+    heads, D, page, length = 1, 64, 16, 200
+    cache = qg.kv8_cache(20, heads, page, D)
+    table = torch.randperm(20, device="cuda")[:13].view(1, 13).int()
+    kv = torch.randn(60, heads, D, device="cuda").half()
+    qg.kv8_append(kv, kv, cache, table, int32(torch, [0, 60]), int32(torch, [100]))
+    Q = torch.randn(new, 4, D, device="cuda").half()
+    args = (table, int32(torch, [0, new]), int32(torch, [length]))
+    O = qg.kv8_attention(Q, cache, *args)
+    check_attention(torch, O, Q, cache, table, [new], [length], D ** -0.5, True, "float16")
+    for s in cache[2:]:  # and so under scales of 0
+        s[s == 2.0 ** -64] = 0
+    assert torch.equal(qg.kv8_attention(Q, cache, *args), O)
 
 
 def test_attention_with_large_and_small_queries(torch, qg):
