@@ -8,7 +8,10 @@ w4a4_quant (M x K activations with rank-32 projection) or w4a4_gemm
 (M x N x K, rank 32, bias); of the microscaled 4-bit operators fp4_quant
 (M x K bf16), fp4_both (both directions), fp4_gemm, fp4_linear and fp4_backward
 (M x N x K); norm, norm_fp4 and norm_backward (M x K).  --fmt picks the 4-bit
-format, --dtype the type of values (bf16, f16, f32).  Sizes default to 2048 each.  Prints one line
+format, --dtype the type of values (bf16, f16, f32).  Of the attention layer's operators s8_quant
+(M x K), s8_linear (M x N x K); rope and rope_backward (M tokens), kv8_append, kv8_gather and
+kv8_attention (M new tokens for each of --batch sequences of --length) with --heads key heads of
+--head values, --group query heads each and pages of --page.  Sizes default to 2048 each.  Prints one line
 with the call's device time from CUDA events (a number taken under a
 profiler is not a benchmark figure).
 """
@@ -58,15 +61,58 @@ def _block_case(qg, torch, a, dev):
     return lambda: qg.fp4_linear_backward(dY, X, Wtq, Wts, fmt, dy_scale=scale(dY), x_scale=xs, w_scale=ws)
 
 
+def _layer_case(qg, torch, a, dev):
+    """The call of an operator of the attention layer, as a function."""
+    M, N, K, D = a.m, a.n, a.k, a.head
+    dtype = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[a.dtype]
+    g = torch.Generator(device=dev).manual_seed(1009)
+
+    def normal(*shape):
+        return torch.randn(*shape, generator=g, device=dev).to(dtype)
+
+    if a.op.startswith("s8"):
+        X = normal(M, K)
+        if a.op == "s8_quant":
+            return lambda: qg.s8_quantize(X)
+        Wq, Ws = qg.s8_quantize(normal(N, K))
+        return lambda: qg.s8_linear(X, Wq, Ws)
+    if a.op.startswith("rope"):
+        Q, Kh = normal(M, a.heads * a.group, D), normal(M, a.heads, D)
+        gq, gk, table = normal(D), normal(D), torch.rand(M, D, generator=g, device=dev)
+        dQ, dK = normal(*Q.shape), normal(*Kh.shape)
+        _, _, rq, rk = qg.qk_norm_rope(Q, Kh, gq, gk, None, table)
+        if a.op == "rope":
+            return lambda: qg.qk_norm_rope(Q, Kh, gq, gk, None, table)
+        return lambda: qg.qk_norm_rope_backward(dQ, dK, Q, Kh, gq, gk, None, table, rq, rk)
+    per = -(-a.length // a.page)
+    cache = qg.kv8_cache(a.batch * per, a.heads, a.page, D)
+    for codes, scales in zip(cache[:2], cache[2:]):
+        codes.random_(-127, 128, generator=g)
+        scales.fill_(0.02)
+    table = torch.randperm(a.batch * per, generator=g, device=dev).int().view(a.batch, per)
+    starts = torch.arange(0, M * a.batch + 1, M, dtype=torch.int32, device=dev)
+    lengths = torch.full((a.batch,), a.length, dtype=torch.int32, device=dev)
+    if a.op == "kv8_attention":
+        Q = normal(M * a.batch, a.heads * a.group, D)
+        return lambda: qg.kv8_attention(Q, cache, table, starts, lengths)
+    Kh, V = normal(M * a.batch, a.heads, D), normal(M * a.batch, a.heads, D)
+    if a.op == "kv8_append":
+        return lambda: qg.kv8_append(Kh, V, cache, table, starts, lengths)
+    return lambda: qg.kv8_gather(cache, table, starts, lengths, M * a.batch, dtype=dtype)
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawTextHelpFormatter)
     ap.add_argument("op", choices=["s8", "s4", "f16", "w4a16", "w4a4_quant", "w4a4_gemm", "fp4_quant", "fp4_both", "fp4_gemm",
-                                  "fp4_linear", "fp4_backward", "norm", "norm_fp4", "norm_backward"])
+                                  "fp4_linear", "fp4_backward", "norm", "norm_fp4", "norm_backward", "s8_quant",
+                                  "s8_linear", "rope", "rope_backward", "kv8_append", "kv8_gather", "kv8_attention"])
     ap.add_argument("--m", type=int, default=2048)
     ap.add_argument("--n", type=int, default=2048)
     ap.add_argument("--k", type=int, default=2048)
     ap.add_argument("--fmt", choices=["nv", "mx"], default="nv")
     ap.add_argument("--dtype", choices=["bf16", "f16", "f32"], default="bf16")
+    for name, size in (("heads", 8), ("group", 4), ("head", 128), ("batch", 4), ("length", 4096), ("page", 64)):
+        ap.add_argument("--" + name, type=int, default=size)
     a = ap.parse_args(argv)
 
     import torch
@@ -101,6 +147,8 @@ def main(argv=None):
         X = t(inputs.f32_normal(M, K, 1004))
         Ut = t(inputs.f16_normal(K, 32, 3004, sigma=0.02).T)
         run = lambda: qg.w4a4_quantize(X, Ut)  # noqa: E731
+    elif a.op.startswith(("s8_", "rope", "kv8")):
+        run = _layer_case(qg, torch, a, dev)
     elif a.op.startswith(("fp4", "norm")):
         run = _block_case(qg, torch, a, dev)
     else:
