@@ -448,6 +448,30 @@ def test_streams_graphs_and_their_workspaces(torch, qg):
     check_attention(torch, outs[1], Qs[1], cache, table, news, [n + 8 for n in lengths], 128 ** -0.5, True, "float16")
 
 
+@pytest.mark.parametrize("group,news,lengths,later,grown", [
+    (4, [64], [1500], [64], [1999]), (4, [60, 40], [1100, 90], [1, 70], [1999, 1500]),
+    (8, [300, 1, 1, 0, 16], [400, 1300, 2, 9, 16], [1, 3, 0, 200, 90], [1, 1999, 7, 900, 1000])])
+def test_a_graph_serves_other_rows_and_lengths(torch, qg, group, news, lengths, later, grown):
+    """Shared units and batches for both kernels, captured; then other rows, lengths and rows of no sequence."""
+    heads, D, page = 2, 128, 16
+    cache, table = filled(torch, [1999] * len(news), heads, D, page, 21)
+    gen = torch.Generator(device="cuda").manual_seed(group)
+    Q = torch.randn(sum(news), heads * group, D, generator=gen, device="cuda").half()
+    starts, length = int32(torch, starts_of(news)), int32(torch, lengths)
+    graph = torch.cuda.CUDAGraph()
+    qg.kv8_attention(Q, cache, table, starts, length)
+    with torch.cuda.graph(graph):
+        O = qg.kv8_attention(Q, cache, table, starts, length)
+    for n, m in ((news, lengths), (later, grown), (news, lengths)):
+        starts.copy_(int32(torch, starts_of(n)))
+        length.copy_(int32(torch, m))
+        O.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_attention(torch, O, Q, cache, table, n, m, D ** -0.5, True, "float16")
+        assert bool((O[sum(n):] == 7).all())
+
+
 def test_a_layer_run_as_it_is_used(torch, qg):
     """Product, norm and rotation, append, attention, product: a prompt, then tokens one at a time, eagerly and as a graph.
 

@@ -191,6 +191,24 @@ def test_positions_outside_the_table_and_not_finite(torch, qg):
             assert bool(torch.isnan(y[t, 1]).all()) == (t == 3)
 
 
+@pytest.mark.parametrize("D,Hq,Hk", [(16, 3, 1), (24, 1, 2)])
+def test_many_tokens(torch, qg, D, Hq, Hk):
+    """Far more items than CTAs: the first, some middle and the last tokens are those of a short call."""
+    T = 700001
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    Q, K = (torch.randn(T, h, D, generator=gen, device="cuda").half() for h in (Hq, Hk))
+    table = torch.rand(T, 8, generator=gen, device="cuda")
+    got = qg.qk_norm_rope(Q, K, None, None, None, table, EPS)
+    grads = qg.qk_norm_rope_backward(Q, K, Q, K, None, None, None, table, got[2], got[3])
+    for i in (0, T // 2, T - 50):
+        pos = torch.arange(i, i + 50, dtype=torch.int32, device="cuda")
+        q, k = Q[i:i + 50].contiguous(), K[i:i + 50].contiguous()
+        want = qg.qk_norm_rope(q, k, None, None, pos, table, EPS)
+        assert all(torch.equal(a[i:i + 50], b) for a, b in zip(got, want))
+        dq, dk, _, _ = qg.qk_norm_rope_backward(q, k, q, k, None, None, pos, table, want[2], want[3])
+        assert torch.equal(grads[0][i:i + 50], dq) and torch.equal(grads[1][i:i + 50], dk)
+
+
 def test_empty_and_graph(torch, qg):
     Q, K, gq, gk, pos, table = case(torch, 6, 2, 2, 64, 64, "bfloat16")
     yq, yk, rq, rk = qg.qk_norm_rope(Q[:0], K[:0], gq, gk, pos[:0], table, EPS)

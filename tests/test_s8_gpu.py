@@ -117,6 +117,22 @@ def test_sums_are_exact_at_their_largest(torch, qg):
         assert torch.equal(Y, want.float().expand(M, N))
 
 
+@pytest.mark.parametrize("M,N,K", [(4200003, 24, 32), (1, 4200003, 32), (3, 4200003, 32), (40, 1100003, 32), (70001, 40, 16)])
+def test_many_tokens_and_channels(torch, qg, M, N, K):
+    """Grids and offsets far from small: the first, some middle and the last rows and columns."""
+    gen = torch.Generator(device="cuda").manual_seed(M % 1000)
+    X, W = (torch.randn(r, K, generator=gen, device="cuda").half() for r in (M, N))
+    Wq, Ws = qg.s8_quantize(W)
+    Xq, Xs = qg.s8_quantize(X)
+    Y = qg.s8_linear(X, Wq, Ws)
+    rows, cols = (torch.cat([torch.arange(n, device="cuda")[i:i + 40] for i in (0, n // 2, max(0, n - 40))]).unique() for n in (M, N))
+    for t, q, scale, at in ((X, Xq, Xs, rows), (W, Wq, Ws, cols)):
+        want, s = ref.s8_quantize(as_np(t[at]))
+        assert np.array_equal(as_np(q[at]), want) and np.array_equal(as_np(scale[at]).astype(np.float32), s)
+    qa, sa, qb, sb = (as_np(t) for t in (Xq[rows], Xs[rows], Wq[cols], Ws[cols]))
+    check_product(Y[rows][:, cols], qa, sa.astype(np.float32), qb, sb.astype(np.float32), None, "float16")
+
+
 def test_scales_whose_product_with_the_sum_alone_leaves_fp32(torch, qg):
     """Tokens near fp32's largest against weights near its smallest scales, in every kernel, and the other way round."""
     for M, N, K in ((1, 40, 512), (5, 40, 512), (60, 40, 512), (1500, 2100, 512)):
