@@ -363,6 +363,34 @@ def test_attention_with_large_and_small_queries(torch, qg):
         check_attention(torch, O, Q, cache, table, news, lengths, scale, True, "bfloat16")
 
 
+@pytest.mark.parametrize("new", [3, 80])
+@pytest.mark.parametrize("scale", [0.0, -0.2, 1e-30])
+def test_scales_of_any_sign(torch, qg, new, scale):
+    cache, table = filled(torch, [300], 2, 128, 32, 13)
+    gen = torch.Generator(device="cuda").manual_seed(new)
+    Q = torch.randn(new, 8, 128, generator=gen, device="cuda").half()
+    O = qg.kv8_attention(Q, cache, table, int32(torch, [0, new]), int32(torch, [300]), scale)
+    check_attention(torch, O, Q, cache, table, [new], [300], scale, True, "float16")
+
+
+@pytest.mark.parametrize("new", [3, 80])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float16"])
+def test_queries_that_are_not_finite_spoil_their_own_results(torch, qg, new, dtype):
+    cache, table = filled(torch, [400], 2, 64, 16, 17)
+    gen = torch.Generator(device="cuda").manual_seed(new)
+    good = torch.randn(new, 8, 64, generator=gen, device="cuda").to(getattr(torch, dtype))
+    bad, places = good.clone(), [(0, 2, float("inf")), (1, 7, float("nan")), (new - 1, 0, -float("inf"))]
+    for row, head, value in places:
+        good[row, head] = 0
+        bad[row, head, 5] = value
+    args = (cache, table, int32(torch, [0, new]), int32(torch, [400]))
+    O, want = qg.kv8_attention(bad, *args), qg.kv8_attention(good, *args)
+    for row, head, _ in places:
+        assert bool(torch.isnan(O[row, head]).all())
+        O[row, head] = want[row, head]
+    check_attention(torch, O, good, cache, table, [new], [400], 64 ** -0.5, True, dtype)
+
+
 def test_attention_keeps_what_is_not_finite_to_those_that_see_it(torch, qg):
     """A page that holds a NaN, or a bad key, reaches the rows that see one of its tokens and no others."""
     D, page = 64, 16

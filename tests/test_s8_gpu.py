@@ -82,7 +82,7 @@ def test_quantize_marks_rows_that_are_not_finite(torch, qg):
 
 SIZES = [(1, 1, 1), (1, 16, 16), (1, 17, 63), (1, 333, 4096), (3, 40, 65), (8, 100, 1000), (9, 64, 2049), (16, 129, 512),
          (17, 64, 64), (16, 48, 20000), (33, 1001, 2304), (128, 256, 1040), (130, 300, 777), (257, 515, 1100),
-         (300, 260, 4097), (512, 512, 512)]
+         (300, 260, 4097), (512, 512, 512), (4100, 261, 1100)]
 
 
 @pytest.mark.parametrize("dtype", ["bfloat16", "float16", "float32"])
