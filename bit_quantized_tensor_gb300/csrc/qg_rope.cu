@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(kRopeThreads, 7) k_qk_norm_rope(const RopePara
 }
 
 // The gains' gradients stay in registers while a warp walks over its items, so the grid is what
-// fits at once.  Measured: 8192 tokens of 40 heads of 128 bf16 values 49.5 us with the sum over the CTAs, 5.2 TB/s (77% of a
-// copy); bound by latency with 16 warps an SM of 128 registers (four heads in flight spill: 74 us).
+// fits at once.  Measured: 8192 tokens of 40 heads of 128 bf16 values 49.5 us with the sum over
+// the CTAs, 5.2 TB/s (77% of a copy); bound by latency with 16 warps an SM of 128 registers (four
+// heads in flight spill: 74 us).
 template <class T, bool PAIRS>
 __global__ void __launch_bounds__(kRopeThreads, 4) k_qk_norm_rope_backward(const RopeParams p) {
     constexpr int E = RopeLane<T>::E, U = kRopeUnroll;

@@ -114,7 +114,7 @@ static int launch_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, OUT
 //
 // Measured, linear of 4096 x 4096 in a chain of calls: 1 token 5.6 us (3.0 TB/s of weights),
 // 4 and 8 with the quantizer's kernel 6.4 and 6.7, by the next kernel 9.8; 16 tokens by
-// that 9.9 (by this one, with two columns of tokens, 11); 8192 x 8192 17.0 us for 1 token (3.9 TB/s), 8 tokens 20.3.
+// that 9.9; 8192 x 8192 17.0 us for 1 token (3.9 TB/s), 8 tokens 20.3.
 // Latency: a CTA's weights are one or two rounds of loads, and none of them goes out before the
 // kernel ahead has ended.
 constexpr int kGemvWarps = 16, kGemvThreads = 32 * kGemvWarps;
@@ -337,9 +337,9 @@ static SomeForm some_form(int64_t M, int64_t N, int64_t K, int64_t* cycles) {
 // Does that kernel take the problem, or the one on CTA pairs, behind a pass that writes the
 // weights as fp16?  The latter's estimate: that pass at 6.2 TB/s (3.3 kB a cycle) and rounds of
 // 256 x 256 tiles, 630 cycles a step of 64 values of K.  Measured, linear of 4096 x 4096, this kernel and
-// pairs: 128 tokens 16.3 and 33.6 us, 512 27.8 and 35.7, 777 49.5 and 36.6, 2048 98 and 60; of 1024 x 8192: 777
-// tokens 33 and 53, 2048 62 and 60; of 8192 x 8192: 256 tokens 57.5 and 80.6, 512 113 and 83.  The choice was within 3% of the
-// better one at 45 sizes.  4096 x 8192 x 8192 by pairs 344 us, 1.6 PFLOP/s, of which the product takes 289 (1.9),
+// pairs: 128 tokens 16.3 and 33.6 us, 512 27.8 and 35.7, 777 49.5 and 36.6, 2048 98 and 60; of
+// 1024 x 8192: 777 tokens 33 and 53, 2048 62 and 60; of 8192 x 8192: 256 tokens 57.5 and 80.6, 512 113
+// and 83.  The choice was within 3% of the better one at 45 sizes.  4096 x 8192 x 8192 by pairs 344 us, 1.6 PFLOP/s, of which the product takes 289 (1.9),
 // the weights' pass 28 and the quantizer 19.
 static bool takes_some(int64_t M, int64_t N, int64_t K) {
     if (M > 4096 || !some_holds(SomeForm{32, 8}, K)) return false;
