@@ -716,8 +716,8 @@ size_t attention_rows_workspace(int64_t D) {
 // joined, twice as many: 64 rows of one sequence of 32768 take it 98 and the other 64, 128 rows 101
 // and 99, 256 rows 114 and 175.  A batch of fewer rows a sequence may still hold a prompt (512 tokens
 // next to 63 single ones over 8192 tokens: 492 us by the kernel for few rows alone, 350 by both),
-// which the host cannot see: both kernels run once what is over one token a sequence makes four units, and cost batches
-// that are all alike 5 us.
+// which the host cannot see: both kernels run once what is over one token a sequence makes four
+// units, and cost a batch of equals 5 us.
 int attention_rows_from(const AttnParams& p) {
     if (p.c.D == 256) return INT32_MAX;
     const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group, B = p.bt.B;
