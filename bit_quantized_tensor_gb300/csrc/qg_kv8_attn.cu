@@ -121,15 +121,17 @@ struct AttnCfg {
     }
 };
 
-// Two values of a row of the result: 0 for a row that sees nothing, NaN for a sequence
-// that is longer than its table.
+// Two values of a row of the result: 0 for a row that sees nothing, NaN for a sequence that is
+// longer than its table and for a row whose scores are all -inf (a query with an infinity; its
+// softmax is 0 / 0).  With any finite score the total is not 0.
 template <class T>
 __device__ __forceinline__ void store_out(const AttnParams& p, const AttnSeq& a, int head, int row, int d, int D,
                                           float2 sum, float total) {
-    const float nan = __uint_as_float(0x7fc00000u);
+    const bool sees = a.s.len > 0 && (!p.causal || a.s.first + row / p.group >= 0);
+    const float none = a.s.cut || sees ? __uint_as_float(0x7fc00000u) : 0.f;
     T* out = static_cast<T*>(p.O) + (a.s.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D + d;
-    out[0] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.x * (0x1p20f / total));
-    out[1] = from_f32<T>(a.s.cut ? nan : total == 0.f ? 0.f : sum.y * (0x1p20f / total));
+    out[0] = from_f32<T>(a.s.cut || total == 0.f ? none : sum.x * (0x1p20f / total));
+    out[1] = from_f32<T>(a.s.cut || total == 0.f ? none : sum.y * (0x1p20f / total));
 }
 
 template <class T, int D, int NB>

@@ -151,9 +151,10 @@ __device__ __forceinline__ RowsPlace rows_find(const AttnParams& p, int64_t u, i
 // With fewer units than SMs a unit's steps are shared out to p.splits CTAs, whose fp32 sums a
 // second kernel joins: which rows a unit has, left for it, and a CTA's sums, 256 rows of O, M and
 // the denominator.
-struct RowsUnit {
+struct alignas(16) RowsUnit {
     int64_t row0;                 // the sequence's first row of Q
     int head, first, rows, cut;   // rows: 0 without a unit
+    int blind;                    // the sequence's first so many rows see no token
 };
 constexpr int kRowsParts = 304;   // CTAs that may have sums to join
 constexpr int kRowsSplits = 32;   // of a unit
@@ -243,8 +244,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         most = static_cast<int>(static_cast<int64_t>(most) * (split + 1) / p.splits) - base;
 #pragma unroll
         for (int t = 0; t < 2; ++t) steps[t] = max(0, min(steps[t] - base, most));
-        if (p.splits > 1 && split == 0 && threadIdx.x == 0)
-            reinterpret_cast<RowsUnit*>(p.part)[unit_no] = {seq.row0, head, row0, all_rows, seq.cut};
+        if (p.splits > 1 && split == 0 && threadIdx.x == 0) {
+            const int64_t ahead = p.causal && seq.first < 0 ? -seq.first * p.group : 0;
+            const int blind = seq.len == 0 || ahead > all_rows ? all_rows : static_cast<int>(ahead);
+            reinterpret_cast<RowsUnit*>(p.part)[unit_no] = {seq.row0, head, row0, all_rows, seq.cut, blind};
+        }
     }
     const int page_log2 = p.c.page_log2;
     const int tokens = max(seen_by(min(all_rows, row0 + TILE) - 1), seen_by(min(all_rows, row0 + 2 * TILE) - 1));
@@ -467,7 +471,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             float* const sums = SPLIT && p.splits > 1 ? rows_part<D>(p, blockIdx.x) + (t * TILE + r) * (D + 4) : nullptr;
             T* out = static_cast<T*>(p.O) + (seq.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D;
             const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-            const float scale = den == 0.f ? 0.f : 0x1p20f / den;
+            const float scale = 0x1p20f / den;
+            // a row that sees nothing is 0; without a sum, its scores are all -inf and their softmax 0 / 0
+            const float none = seq.cut || seen_by(row) > 0 ? nan : 0.f;
 #pragma unroll 1
             for (int d = 0; d < D; d += 16) {
                 uint32_t y[16];
@@ -487,7 +493,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        f[i] = seq.cut ? nan : !mine || den == 0.f ? 0.f : __uint_as_float(y[i]) * scale;
+                        f[i] = seq.cut || den == 0.f ? none : __uint_as_float(y[i]) * scale;
                     if (row < all_rows) {
                         if (sectors)
                             store_sectors<T>(out + d, f);
@@ -699,10 +705,10 @@ __global__ void __launch_bounds__(kRowsJoinThreads) k_kv8_attention_rows_join(co
 #pragma unroll
             for (int k = 0; k < E; ++k) o[k] = fmaf(v[k], w, o[k]);
         }
-        const float scale = u.cut ? __uint_as_float(0x7fc00000u) : den == 0.f ? 0.f : 0x1p20f / den;
+        const float scale = 0x1p20f / den, none = u.cut || row >= u.blind ? __uint_as_float(0x7fc00000u) : 0.f;
         T* out = static_cast<T*>(p.O) + (u.row0 + row / p.group) * p.ldo + (u.head * p.group + row % p.group) * D + E * lane;
 #pragma unroll
-        for (int k = 0; k < E; ++k) out[k] = from_f32<T>(den == 0.f && !u.cut ? 0.f : o[k] * scale);
+        for (int k = 0; k < E; ++k) out[k] = from_f32<T>(u.cut || den == 0.f ? none : o[k] * scale);
     }
 }
 

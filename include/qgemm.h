@@ -669,7 +669,7 @@ int kv8_gather(int dtype, int64_t B, int64_t rows, int64_t heads, int64_t D, con
  *         of heads, query head h reads head h / (q_heads / heads) of the cache
  *  causal : row i of a sequence with n rows sees its tokens up to lengths - n + i, else
  *         all of them.  A row that sees no token is 0; rows of a sequence that is longer
- *         than its table are NaN.
+ *         than its table, and rows whose scores are all -inf, are NaN.
  *  Scales are what kv8_append writes: 2^-64 to 2^121, or NaN.  O and Q do not overlap.
  *  ws: qg_workspace_size(QG_OP_KV8_ATTENTION, rows, q_heads, D) bytes, 256-byte aligned */
 int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads, int64_t heads, int64_t D,
