@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             const float scale = 0x1p20f / den;
             // a row that sees nothing is 0; without a sum, its scores are all -inf and their softmax 0 / 0
-            const float none = seq.cut || seen_by(row) > 0 ? nan : 0.f;
+            const float none = seq.cut || sees > 0 ? nan : 0.f;  // (of a whole unit: base is 0)
 #pragma unroll 1
             for (int d = 0; d < D; d += 16) {
                 uint32_t y[16];
