@@ -5,10 +5,10 @@
 //
 // The codes go to the tensor cores as exact fp16 numbers, so a page's scales have to
 // stay outside: sk is a factor of the product's result, and sv goes into the exponent,
-//   w_j = 2^(x_j + log2 sv_j - M),   O = sum w_j vq_j / sum (w_j / sv_j),
-// with M a running upper bound of x_j + log2 sv_j, so that w_j, rounded to fp16 for the
-// second product, is at most 2^8 whatever the pages' scales are.  (Where that leaves w_j
-// hardly anything, its term of the denominator is 2^(x_j - M).)  Sums, M and the
+//   w_j = 2^(x_j + log2 sv_j - M + 9),   O = sum w_j vq_j / sum (w_j / sv_j),
+// with M + 6 a running upper bound of x_j + log2 sv_j, so that w_j, rounded to fp16 for the
+// second product, is at most 2^15 whatever the pages' scales are.  (Where that leaves w_j
+// hardly anything, its term of the denominator is 2^(x_j - M + 9).)  Sums, M and the
 // denominator are fp32.  Queries go in as fp16 times a power of two of their row, which
 // is exact for bf16 too but for values 2^-28 of the row's largest.
 #include <cuda.h>
@@ -31,7 +31,7 @@ namespace qg {
 // what it executes, so the rest is kept small: each warp has a ring of its own that TMA
 // fills (a box for 16 or 32 tokens, swizzled so that no lanes meet in a bank), and no
 // barrier but the end of a unit; the running maximum is looked at once for 32 tokens and
-// the sums are rescaled only when it has grown by 2^8.
+// the sums are rescaled only when it has grown by 2^6.
 //
 // Measured, 32 heads of 128 values on 8 key heads: one token each for 64 sequences of up to 8192
 // 118 us, 5.6 TB/s (83% of a copy); one token over 131071 62 us, 4.3 TB/s, where the join, which a
@@ -128,7 +128,7 @@ template <class T>
 __device__ __forceinline__ void store_out(const AttnParams& p, const AttnSeq& a, int head, int row, int d, int D,
                                           float2 sum, float total) {
     T* out = static_cast<T*>(p.O) + (a.s.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D + d;
-    float f = 0x1p20f / total;
+    float f = kDenUnit / total;
     if (total == 0.f) {  // (a branch: as a choice it cost the kernel's loop 1 to 3%)
         const bool sees = a.s.len > 0 && (!p.causal || a.s.first + row / p.group >= 0);
         sum.x = sum.y = 0.f;
@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
             bool low = false;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                const float m0 = M[n][0] == neg_inf() ? 0.f : M[n][0], m1 = M[n][1] == neg_inf() ? 0.f : M[n][1];
+                const float m0 = weight_base(M[n][0]), m1 = weight_base(M[n][1]);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const float e0 = exp2_fast(x[h][n][0] - m0), e1 = exp2_fast(x[h][n][1] - m1);
@@ -433,12 +433,12 @@ __global__ void __launch_bounds__(kAttnThreads, AttnCfg<D, NB>::PER_SM)
                 }
             }
             if (__any_sync(0xffffffffu, low)) {
-                // tokens of small scales next to large ones: 2^(x - M), whose size they keep in the denominator
+                // tokens of small scales next to large ones: 2^x, whose size they keep in the denominator
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
-                        const float base = M[n][m] == neg_inf() ? 0.f : M[n][m];
+                        const float base = weight_base(M[n][m]);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float x0 = x[h][n][m], x2 = x[h][n][m + 2];

@@ -1,7 +1,7 @@
 // Attention over the paged 8-bit cache (kv8_common.cuh): many query rows a sequence, on tcgen05.
 //
 // The mathematics is that of the kernel for few rows: codes as exact fp16 operands, a page's
-// scales outside the products, weights 2^(x + log2 sv - M) in fp16.  With
+// scales outside the products, weights 2^(x + log2 sv - M + 9) in fp16.  With
 //   t_j = raw_j c_b + l_b,   c_b = factor sk_b,  l_b = log2 sv_b      (b: j's 16 tokens)
 // a weight is one fused multiply-add and one 2^x, like a softmax without scales.
 //
@@ -15,7 +15,7 @@
 // from where they are the A operand of the product with V; O (128 x D fp32) beside it.  One
 // tile's products run while the other's weights are made.  Both K and V lie in shared memory as
 // tokens by 64 values (128-byte swizzle), which is K's K-major and V's MN-major form, so they are
-// converted alike.  A row's sums are rescaled, in tensor memory, only when its maximum grows by 2^8.
+// converted alike.  A row's sums are rescaled, in tensor memory, only when its maximum grows by 2^6.
 //
 // Measured: 620 us, 980 TFLOP/s for 4 prompts of 1392 to 2048 tokens, 32 heads of 128 values on 8 key
 // heads, over 3058 to 8192 tokens, half the rate of the tensor cores.  What a step takes, about 4000
@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                     }
                 }
             }
-            const float base = M == neg_inf() ? 0.f : M;
+            const float base = weight_base(M);
             auto weights = [&](auto all, const uint32_t(&x)[32], int ch) {
                 uint32_t w[16];
 #pragma unroll
@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                 landed(xb);
                 weights(all, xb, 3);
             };
-            if (whole && !__any_sync(0xffffffffu, least < M - 99.f))
+            if (whole && !__any_sync(0xffffffffu, least < base - 99.f))
                 all_weights(std::true_type{});
             else
                 all_weights(std::false_type{});
@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             float* const sums = SPLIT && p.splits > 1 ? rows_part<D>(p, blockIdx.x) + (t * TILE + r) * (D + 4) : nullptr;
             T* out = static_cast<T*>(p.O) + (seq.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D;
             const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
-            const float scale = 0x1p20f / den;
+            const float scale = kDenUnit / den;
             // a row that sees nothing is 0; without a sum, its scores are all -inf and their softmax 0 / 0
             const float none = seq.cut || sees > 0 ? nan : 0.f;  // (of a whole unit: base is 0)
 #pragma unroll 1
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kRowsJoinThreads) k_kv8_attention_rows_join(co
 #pragma unroll
             for (int k = 0; k < E; ++k) o[k] = fmaf(v[k], w, o[k]);
         }
-        const float scale = 0x1p20f / den, none = u.cut || row >= u.blind ? __uint_as_float(0x7fc00000u) : 0.f;
+        const float scale = kDenUnit / den, none = u.cut || row >= u.blind ? __uint_as_float(0x7fc00000u) : 0.f;
         T* out = static_cast<T*>(p.O) + (u.row0 + row / p.group) * p.ldo + (u.head * p.group + row % p.group) * D + E * lane;
 #pragma unroll
         for (int k = 0; k < E; ++k) out[k] = from_f32<T>(u.cut || den == 0.f ? none : o[k] * scale);

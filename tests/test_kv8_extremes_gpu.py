@@ -1,9 +1,12 @@
-"""Attention over the 8-bit cache at the ends of its range: scores that are -inf throughout."""
+"""Attention over the 8-bit cache at the ends of its range: scores that are -inf throughout, weights far
+below the largest.  Bounds as in test_kv8_gpu.py where none is derived here."""
 import math
 
 import pytest
 
+from tests.test_fp4_gpu import HALF_UNIT
 from tests.test_kv8_gpu import check_attention, filled, int32, starts_of
+from tests.test_s8_gpu import TINY
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +68,46 @@ def test_scores_that_are_all_minus_infinity(torch, qg, news, lengths, D, causal)
                     O[row + i, h] = want[row + i, h]
             row += n
         check_attention(torch, O, good, cache, table, news, lengths, scale, causal, "float16")
+
+
+@pytest.mark.parametrize("page,D", [(16, 64), (64, 128), (32, 256)])
+@pytest.mark.parametrize("B,new,length", [(1, 1, 131072), (1, 40, 131072), (700, 1, 8192), (40, 40, 8192)])
+@pytest.mark.parametrize("below", [17.0, 18.0, 22.0])
+def test_many_small_weights_next_to_large_ones(torch, qg, below, B, new, length, page, D):
+    """Four tokens that hold nearly all of the weight but whose values are 0, as a sink's are, before thousands whose
+    weights are e^-below of theirs each: the result is what the thousands make.  (B sequences on the same pages.)
+
+    A weight is rounded to fp16 in units in which the largest is at least 2^9: by half of 2^-10 of itself, or by half
+    of 2^-24 below the normal range, which is 2^-34 of the largest.  The rest of the bound is that of check_attention.
+    """
+    heads, group = 1, 4
+    cache, table = filled(torch, [length], heads, D, page, 23, spread=0.0)
+    kq, vq, ks, vs = cache
+    kq[..., 0] = 0
+    vq.copy_(vq.int().abs().clamp(60, 127).to(torch.int8))
+    for at in (3, 35, 67, 99):
+        sink = int(table[0, at // page]), 0, at % page
+        kq[sink] = 0
+        vq[sink] = 0
+        kq[sink][0] = 100
+    gen = torch.Generator(device="cuda").manual_seed(new)
+    # scores of the others are normal with 0.1 (codes have a mean square of about 73^2), the sinks' are `below`
+    Q = (0.1 / (73 * 0.01 * D ** 0.5) * torch.randn(B * new, heads * group, D, generator=gen, device="cuda")).half()
+    Q[..., 0] = below / (100 * 0.01)
+    starts, lengths = int32(torch, starts_of([new] * B)), int32(torch, [length] * B)
+    O = qg.kv8_attention(Q, cache, table.expand(B, -1).contiguous(), starts, lengths, 1.0).double()
+    k8, v8 = (c[table[0].long(), 0].double().reshape(-1, D)[:length] for c in (kq, vq))
+    sk, sv = (s[table[0].long(), 0].double().repeat_interleave(page)[:length, None] for s in (ks, vs))
+    last = torch.arange(length - new, length, device="cuda").repeat(B)
+    hide = torch.arange(length, device="cuda")[None, :] > last[:, None]
+    for h in range(group):
+        q = Q[:, h].double()
+        x = (q @ (k8 * sk).t()).masked_fill(hide, -math.inf)
+        w = torch.softmax(x, 1)
+        want = w @ (v8 * sv)
+        e = D * 2.0 ** -23 * (q.abs() @ (k8.abs() * sk).t()).amax(1) + 10 * 2.0 ** -24 * (x.amax(1) + 8) + 2.0 ** -21
+        joined = (length / 16 + 64) * 2.0 ** -23
+        bulk, low = w @ (v8.abs() * sv), 2.0 ** -34 * w.amax(1, keepdim=True) * (v8.abs() * sv).sum(0)
+        bound = bulk * (1.01 * 2.0 ** -11 + 2 * e[:, None] + joined) + low + 1.01 * HALF_UNIT["float16"] * want.abs() + TINY["float16"]
+        err = (O[:, h] - want).abs()
+        assert bool((err <= bound).all()), (h, float((err / bound).max()), float((err / want).max()))
