@@ -650,7 +650,7 @@ int qk_norm_rope_backward(int dtype, int style, int64_t T, int64_t Hq, int64_t H
     const NvtxRange nvtx_range("qk_norm_rope_backward");
     int rc = check_rope(dtype, wdtype, style, T, Hq, Hk, D, R, positions, table, table_rows, gq, gk);
     if (rc) return rc;
-    if (Hq + Hk == 0) return QG_OK;
+    if (Hq + Hk == 0 && !dgq && !dgk) return QG_OK;
     if ((Hq && !dgq) || (Hk && !dgk)) return QG_ERR_INVALID_ARG;
     rc = check_f32(dgq);
     if (!rc) rc = check_f32(dgk);
@@ -675,14 +675,14 @@ int qk_norm_rope_backward(int dtype, int style, int64_t T, int64_t Hq, int64_t H
     p.job[0] = {Q, dYq, gq, dQ, const_cast<float*>(rq), dgq, ldq, lddyq, lddq, static_cast<int>(Hq)};
     p.job[1] = {K, dYk, gk, dK, const_cast<float*>(rk), dgk, ldk, lddyk, lddk, static_cast<int>(Hk)};
     p.partial = static_cast<float*>(ws);
-    int parts[2] = {0, 0};
-    if (T > 0) {
+    int parts[2] = {0, 0};  // none without tokens or heads: the gains' gradients are 0
+    if (T > 0 && Hq + Hk > 0) {
         rc = rope_by_type<true>(dtype, style, p, dev, s, parts);
         if (rc) return rc;
     }
     return launch_serialized(k_rope_gains, dim3(static_cast<unsigned>((D + 31) / 32), 2), 1024, 0, 1, s,
                              static_cast<const float*>(p.partial), parts[0], parts[1], static_cast<int>(D),
-                             Hq ? dgq : nullptr, Hk ? dgk : nullptr);
+                             dgq, dgk);
 }
 
 }  // extern "C"

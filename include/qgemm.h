@@ -617,7 +617,8 @@ int qk_norm_rope(int dtype, int style, int64_t T, int64_t Hq, int64_t Hk, int64_
 /* Its gradients, with rq and rk as it wrote them and Q, K as it read them:
  *   dz = the rotation by the negative angle of dy, xh = x rstd, e = dz g
  *   dx = rstd (e - xh sum(e xh) / D)          (type of Q; dQ may be dYq, dK dYk)
- *   dg = sum over tokens and heads of dz xh   (D fp32 each; 0 for T = 0)
+ *   dg = sum over tokens and heads of dz xh   (D fp32 each; 0 without tokens or heads,
+ *                                              where one may also be NULL for no heads)
  *  ws: qg_workspace_size(QG_OP_QK_NORM_ROPE_BACKWARD, 1, 1, D) bytes. */
 int qk_norm_rope_backward(int dtype, int style, int64_t T, int64_t Hq, int64_t Hk, int64_t D,
                           int64_t R, const void* dYq, int64_t lddyq, const void* dYk,
