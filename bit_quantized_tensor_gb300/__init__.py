@@ -1041,6 +1041,8 @@ def s8_quantize(X, out=None, stream=None):
     Q, S = out
     if _s8_operand(Q, S, "out", K, dev) != M:
         raise ValueError(f"out must have {M} rows")
+    if K == 0:  # no codes to write, and the library writes nothing: the scale of a row of zeros
+        S.fill_(2.0 ** -100)
     _check("s8_quantize", lib().s8_quantize(dt, M, K, X.data_ptr(), ld, Q.data_ptr(), S.data_ptr(), _raw_stream(dev)))
     return Q, S
 

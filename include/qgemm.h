@@ -573,7 +573,8 @@ int layer_norm_backward(int dtype, int64_t M, int64_t D, const void *dY, int64_t
 /* Bytes of a row of K codes; 0 for K <= 0. */
 int64_t qg_s8_codes_ld(int64_t K);
 
-/* X (M x K) to codes Q and scales S (M). */
+/* X (M x K) to codes Q and scales S (M).  K = 0: nothing is written (the products read
+ * no scales then). */
 int s8_quantize(int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, int8_t* Q, float* S,
                 void* stream);
 
