@@ -42,10 +42,10 @@ __device__ __forceinline__ float s8_number(float x, float r) {
     return r == 0.f ? 0.f : __fadd_rn(s8_shifted(x, r), -12582912.f);
 }
 
-// sum sa sb + bias, the smaller scale first: fl(sum) times the larger one alone can be infinite where the
-// result is not.  Scales that are NaN stay.
+// sum sa sb + bias, the scale of the smaller magnitude first: fl(sum) times the larger one alone can
+// be infinite where the result is not.  Scales that are NaN stay.
 __device__ __forceinline__ float s8_scaled(int sum, float sa, float sb, float bias) {
-    const bool less = sa < sb;
+    const bool less = fabsf(sa) < fabsf(sb);
     return fmaf(static_cast<float>(sum) * (less ? sa : sb), less ? sb : sa, bias);
 }
 

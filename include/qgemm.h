@@ -579,8 +579,9 @@ int s8_quantize(int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, int
                 void* stream);
 
 /* Y (M x N, `dtype`) = As[m] Bs[n] sum_k Aq[m][k] Bq[n][k] + bias[n]: the integer
- * sum is exact, then rounded to fp32, multiplied by the smaller of As[m] and Bs[n] and
- * in one fused step by the other with the bias added, and rounded to `dtype`.  bias: N values of `dtype` or NULL.
+ * sum is exact, then rounded to fp32, multiplied by that of As[m] and Bs[n] which has the
+ * smaller magnitude (either may have any sign) and in one fused step by the other with the
+ * bias added, and rounded to `dtype`.  bias: N values of `dtype` or NULL.
  *  ws: qg_workspace_size(QG_OP_S8_LINEAR, M, N, K) bytes, 256-byte aligned; 0 bytes
  *      (ws may be NULL) for one token, K up to 102336. */
 int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const float* As,
