@@ -314,19 +314,22 @@ static bool some_holds(const SomeForm& f, int64_t K) {
 // the exchange of sums; whole rounds of CTAs, of which clusters of 8 leave SMs out.  Estimates
 // were within 10% of 4 to 250 us at 36 problems; the best form of each was chosen, or one at most
 // 8% slower.
+static int64_t some_cycles(const SomeForm& f, int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = (N + 127) / 128 * ((M + f.tile - 1) / f.tile);
+    const int64_t stages = ((K + kS8Bk - 1) / kS8Bk + f.splits - 1) / f.splits;
+    const int64_t cta = 5700 + 20 * f.tile + stages * (500 + 6 * f.tile) + (f.splits > 1 ? 2500 + 32 * f.tile : 0);
+    const int64_t sms = f.splits == 8 ? 104 : 148;
+    return (tiles * f.splits + sms - 1) / sms * cta;
+}
 static SomeForm some_form(int64_t M, int64_t N, int64_t K, int64_t* cycles) {
     SomeForm best = {32, 8};
     int64_t least = INT64_MAX;
     for (int tile = 32; tile <= 128; tile *= 2) {
         if (tile > 32 && tile >= 2 * M) break;
-        const int64_t tiles = (N + 127) / 128 * ((M + tile - 1) / tile);
         for (int splits = 1; splits <= 8; splits *= 2) {
             const SomeForm f = {tile, splits};
             if (!some_holds(f, K) || (splits > 1 && K < 256 * splits)) continue;
-            const int64_t stages = ((K + kS8Bk - 1) / kS8Bk + splits - 1) / splits;
-            const int64_t cta = 5700 + 20 * tile + stages * (500 + 6 * tile) + (splits > 1 ? 2500 + 32 * tile : 0);
-            const int64_t sms = splits == 8 ? 104 : 148;
-            const int64_t time = (tiles * splits + sms - 1) / sms * cta;
+            const int64_t time = some_cycles(f, M, N, K);
             if (time < least) least = time, best = f;
         }
     }
@@ -341,19 +344,39 @@ static SomeForm some_form(int64_t M, int64_t N, int64_t K, int64_t* cycles) {
 // 1024 x 8192: 777 tokens 33 and 53, 2048 62 and 60; of 8192 x 8192: 256 tokens 57.5 and 80.6, 512 113
 // and 83.  The choice was within 3% of the better one at 45 sizes.  4096 x 8192 x 8192 by pairs 344 us, 1.6 PFLOP/s, of which the product takes 289 (1.9),
 // the weights' pass 28 and the quantizer 19.
+static int64_t pairs_cycles(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
+    return 5700 + 3 * N * K / 3300 + (tiles + 75) / 76 * ((K + 63) / 64 * 630 + 7600);
+}
 static bool takes_some(int64_t M, int64_t N, int64_t K) {
     if (M > 4096 || !some_holds(SomeForm{32, 8}, K)) return false;
     int64_t cycles = 0;
     some_form(M, N, K, &cycles);
-    const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
-    return cycles <= 5700 + 3 * N * K / 3300 + (tiles + 75) / 76 * ((K + 63) / 64 * 630 + 7600);
+    return cycles <= pairs_cycles(M, N, K);
+}
+
+// May a product of up to M tokens be one on pairs?  Whole rounds of CTAs let the choice go back and forth
+// as M grows, but a workspace for M tokens has to do for fewer, so it has the weights' place from
+// the first such M on, or a little earlier.  In each 256 tokens the pairs' estimate is one number, and the
+// other kernel's grows with M as long as it chooses among the same tiles (up to 32 tokens, up to 64, above).
+static bool may_take_pairs(int64_t M, int64_t N, int64_t K) {
+    if (M > 4096 || !some_holds(SomeForm{32, 8}, K)) return true;
+    int64_t most = 0;  // of the other kernel, up to `end` tokens
+    for (int64_t end = 32;; end = end < 64 ? 64 : end < 256 ? 256 : end + 256) {
+        const int64_t m = M < end ? M : end;
+        int64_t cycles = 0;
+        some_form(m, N, K, &cycles);
+        most = cycles > most ? cycles : most;
+        if (most > pairs_cycles(m, N, K)) return true;
+        if (end >= M) return false;
+    }
 }
 
 // ------------------------------------------------------------ workspaces and calls
 
 static size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
-// The tokens' codes (a few tokens: 8 bits, more: fp16) and scales and, where they are turned
+// The tokens' codes (a few tokens: 8 bits, more: fp16) and scales and, where they may be turned
 // into fp16 in memory, the weights.
 struct S8Workspace {
     size_t a, b, sa, total;
@@ -363,7 +386,7 @@ static S8Workspace s8_workspace(int64_t M, int64_t N, int64_t K) {
     S8Workspace w;
     w.a = 0;
     w.b = up256((takes_gemv(M) ? 1 : 2) * ld * m);
-    w.sa = w.b + (takes_gemv(M) || takes_some(M, N, K) ? 0 : up256(2 * ld * static_cast<size_t>(N)));
+    w.sa = w.b + (takes_gemv(M) || !may_take_pairs(M, N, K) ? 0 : up256(2 * ld * static_cast<size_t>(N)));
     w.total = w.sa + up256(4 * m);
     return w;
 }

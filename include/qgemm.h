@@ -583,7 +583,8 @@ int s8_quantize(int dtype, int64_t M, int64_t K, const void* X, int64_t ldx, int
  * smaller magnitude (either may have any sign) and in one fused step by the other with the
  * bias added, and rounded to `dtype`.  bias: N values of `dtype` or NULL.
  *  ws: qg_workspace_size(QG_OP_S8_LINEAR, M, N, K) bytes, 256-byte aligned; 0 bytes
- *      (ws may be NULL) for one token, K up to 102336. */
+ *      (ws may be NULL) for one token, K up to 102336.  That of M tokens is large enough
+ *      for fewer with the same N and K. */
 int s8_gemm(int dtype, int64_t M, int64_t N, int64_t K, const int8_t* Aq, const float* As,
             const int8_t* Bq, const float* Bs, const void* bias, void* Y, int64_t ldy, void* ws,
             size_t ws_bytes, void* stream);

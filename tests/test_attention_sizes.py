@@ -1,0 +1,17 @@
+"""CPU checks of the attention layer's operators: workspace sizes."""
+import pytest
+
+import bit_quantized_tensor_gb300 as qg
+
+
+@pytest.fixture(scope="module")
+def L():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    return qg.lib()
+
+
+@pytest.mark.parametrize("N,K", [(4096, 4096), (11008, 4096), (1001, 2304), (8192, 8192), (17, 20000), (4096, 130000), (64, 1)])
+def test_a_workspace_for_many_tokens_serves_fewer(L, N, K):
+    sizes = [L.qg_workspace_size(qg.QG_OP_S8_LINEAR, m, N, K) for m in list(range(1, 4400)) + [5000, 8192, 1 << 20]]
+    assert all(a <= b for a, b in zip(sizes, sizes[1:]))
