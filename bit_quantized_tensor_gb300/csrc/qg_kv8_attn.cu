@@ -715,7 +715,9 @@ static int launch_attention(AttnParams p, int dev, cudaStream_t s) {
                              s, p);
 }
 
-// 8 rows a unit where that is all that a sequence has of a key head on average.
+// 8 rows a unit where that is all that a sequence has of a key head on average, else 16.  Next to prompts
+// that go to the other kernel the rest may have fewer: 1024 tokens next to 63 single ones of 4 heads a key
+// head would take 272 us with 8 (282), but 64 sequences of 8 tokens each 392 (248).
 template <class T, int D>
 static int attention_by_rows(const AttnParams& p, int dev, cudaStream_t s) {
     const int64_t rows = (static_cast<int64_t>(p.bt.rows) + p.bt.B - 1) / p.bt.B * p.group;

@@ -147,10 +147,12 @@ __device__ __forceinline__ RowsPlace rows_find(const AttnParams& p, int64_t u, i
     return {at.b, lo, at.at};
 }
 
-// SPLIT: the form that looks at p.splits and p.from (their registers cost the other one 4%).
-// With fewer units than SMs a unit's steps are shared out to p.splits CTAs, whose fp32 sums a
-// second kernel joins: which rows a unit has, left for it, and a CTA's sums, 256 rows of O, M and
-// the denominator.
+// The forms of the kernel: of all sequences, of those of p.from rows and more, and of these with a unit's
+// steps shared out to p.splits CTAs.  (What the second asks ahead of its loop costs the first 4% by
+// the registers it leaves: 573 us of 4 prompts of 2048 tokens became 596.)
+// With fewer units than SMs the last form's CTAs leave fp32 sums that a second kernel joins: which rows
+// a unit has, left for it, and a CTA's sums, 256 rows of O, M and the denominator.
+enum RowsForm { kWhole, kSome, kSplit };
 struct alignas(16) RowsUnit {
     int64_t row0;                 // the sequence's first row of Q
     int head, first, rows, cut;   // rows: 0 without a unit
@@ -163,10 +165,11 @@ __device__ __forceinline__ float* rows_part(const AttnParams& p, int64_t cta) {
     return reinterpret_cast<float*>(reinterpret_cast<RowsUnit*>(p.part) + kRowsParts) + cta * (2 * kRowsTile) * (D + 4);
 }
 
-template <class T, int D, bool SPLIT>
+template <class T, int D, int FORM>
 __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const AttnParams p) {
     using Cfg = RowsCfg<D>;
     constexpr int TILE = kRowsTile;
+    constexpr bool SPLIT = FORM == kSplit;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* const smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                      ~static_cast<uintptr_t>(1023));
@@ -206,9 +209,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
     pdl_wait_prior_grid();
     fence_proxy_async_global();  // the cache may have been written just before, with ordinary stores
     const int unit_no = SPLIT ? blockIdx.x / p.splits : blockIdx.x, split = SPLIT ? blockIdx.x - unit_no * p.splits : 0;
-    const RowsPlace at = rows_find<SPLIT>(p, unit_no, mem);
+    const RowsPlace at = rows_find<FORM != kWhole>(p, unit_no, mem);
     if (at.b >= p.bt.B) {  // more CTAs than units; no tensor memory is held yet
-        if (SPLIT && p.splits > 1 && split == 0 && threadIdx.x == 0) reinterpret_cast<RowsUnit*>(p.part)[unit_no].rows = 0;
+        if (SPLIT && split == 0 && threadIdx.x == 0) reinterpret_cast<RowsUnit*>(p.part)[unit_no].rows = 0;
         return;
     }
     if (warp == kRowsMmaWarp) tmem_alloc(smem_u32(tmem_holder), 512);
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
         most = static_cast<int>(static_cast<int64_t>(most) * (split + 1) / p.splits) - base;
 #pragma unroll
         for (int t = 0; t < 2; ++t) steps[t] = max(0, min(steps[t] - base, most));
-        if (p.splits > 1 && split == 0 && threadIdx.x == 0) {
+        if (split == 0 && threadIdx.x == 0) {
             const int64_t ahead = p.causal && seq.first < 0 ? -seq.first * p.group : 0;
             const int blind = seq.len == 0 || ahead > all_rows ? all_rows : static_cast<int>(ahead);
             reinterpret_cast<RowsUnit*>(p.part)[unit_no] = {seq.row0, head, row0, all_rows, seq.cut, blind};
@@ -468,12 +471,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
             ok = __all_sync(0xffffffffu, bounded_wait(pv_done(t), (mine - 1) & 1, abort_flag, p.ctl, kSiteRowsPv));
         tc_fence_after();
         if (ok) {
-            float* const sums = SPLIT && p.splits > 1 ? rows_part<D>(p, blockIdx.x) + (t * TILE + r) * (D + 4) : nullptr;
+            float* const sums = SPLIT ? rows_part<D>(p, blockIdx.x) + (t * TILE + r) * (D + 4) : nullptr;
             T* out = static_cast<T*>(p.O) + (seq.row0 + row / p.group) * p.ldo + (head * p.group + row % p.group) * D;
             const bool sectors = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
             const float scale = kDenUnit / den;
             // a row that sees nothing is 0; without a sum, its scores are all -inf and their softmax 0 / 0
-            const float none = seq.cut || sees > 0 ? nan : 0.f;  // (of a whole unit: base is 0)
+            const float none = seq.cut || sees > 0 ? nan : 0.f;
 #pragma unroll 1
             for (int d = 0; d < D; d += 16) {
                 uint32_t y[16];
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) k_kv8_attention_rows(const At
                     tmem_ld_32x32b_x16(o_at + d, y);
                     tmem_wait_ld();
                 }
-                if (SPLIT && p.splits > 1) {
+                if constexpr (SPLIT) {
                     if (row < all_rows) {
 #pragma unroll
                         for (int i = 0; i < 16; i += 4)
@@ -716,19 +719,29 @@ size_t attention_rows_workspace(int64_t D) {
     return kRowsParts * (sizeof(RowsUnit) + sizeof(float) * 2 * kRowsTile * static_cast<size_t>(D + 4));
 }
 
+static int64_t table_steps(const AttnParams& p) {
+    return ((static_cast<int64_t>(p.c.table_cols) << p.c.page_log2) + kRowsTile - 1) / kRowsTile;
+}
+
 // How many rows a sequence has to have for the kernel above; 1: all sequences go to it, INT32_MAX:
-// none.  64 rows a sequence take it 98 us (8 sequences of 8192 tokens, 8 heads of 128 values) where
+// none.  64 rows a sequence take it 97 us (8 sequences of 8192 tokens, 8 heads of 128 values) where
 // the kernel for few rows takes 106, 32 rows 97 and 68.  With fewer units, whose CTAs' sums have to be
 // joined, twice as many: 64 rows of one sequence of 32768 take it 98 and the other 64, 128 rows 101
-// and 99, 256 rows 114 and 175.  A batch of fewer rows a sequence may still hold a prompt (512 tokens
-// next to 63 single ones over 8192 tokens: 492 us by the kernel for few rows alone, 350 by both),
-// which the host cannot see: both kernels run once what is over one token a sequence makes four
-// units, and cost a batch of equals 5 us.
+// and 99, 256 rows 114 and 175.
+// A batch may hold prompts next to single tokens, which the host cannot see.  On average few rows a
+// sequence: both kernels run once what is over one token a sequence makes four units (512 tokens
+// next to 63 single ones over 8192 tokens: 492 us by the kernel for few rows alone, 284 by both; 5 us
+// more for a batch of equals).  On average many: all but one sequence may be single tokens, each of
+// which then keeps a CTA a key head busy for all of its steps.  Both run where that could be 16384 steps
+// (108 on each SM, 220 us).  Of 64 sequences of 8 key heads over 8192 tokens 1024 tokens next to 63 single
+// ones take 282 us and 414 by this kernel alone, 4096 596 and 678, but 16 tokens of each sequence 333 and
+// 308.  4096 tokens next to 15 single ones could be 7680 steps and take 520 us by both, 493 by this
+// kernel; with 65536 tokens for each of the 15, 540 and 943.
 int attention_rows_from(const AttnParams& p) {
     if (p.c.D == 256) return INT32_MAX;
     const int64_t rows = static_cast<int64_t>(p.bt.rows) * p.group, B = p.bt.B;
     const int from = B * p.c.heads < 64 ? 128 : 64;
-    if (rows >= B * from) return 1;
+    if (rows >= B * from) return (B - 1) * p.c.heads * table_steps(p) < 16384 ? 1 : from;
     return B > 1 && (p.bt.rows - B) * p.group >= 8 * kRowsTile ? from : INT32_MAX;
 }
 
@@ -742,23 +755,25 @@ static int launch_rows(AttnParams p, int dev, cudaStream_t s) {
     const int64_t alike = (rows + seqs * 2 * kRowsTile - 1) / (seqs * 2 * kRowsTile) * seqs * p.c.heads;
     // CTAs for a unit: as many as there are SMs for, each with 4 steps at least of the longest.  A lone
     // sequence's 128 rows over 32768 tokens of 8 heads: 440 us by 8 CTAs, 101 by 152.
-    const int64_t steps = ((static_cast<int64_t>(p.c.table_cols) << p.c.page_log2) + kRowsTile - 1) / kRowsTile;
+    const int64_t steps = table_steps(p);
     int64_t splits = num_sms(dev) / alike;
     splits = splits > kRowsParts / units ? kRowsParts / units : splits;
     splits = splits > kRowsSplits ? kRowsSplits : splits;
     splits = splits > steps / 4 ? steps / 4 : splits;
     p.splits = splits < 1 ? 1 : static_cast<int>(splits);
     struct Whole;
+    struct Some;
     struct Split;
-    const bool split = p.splits > 1 || p.from > 1;
-    int rc = split ? raise_smem<Split>(k_kv8_attention_rows<T, D, true>)
-                   : raise_smem<Whole>(k_kv8_attention_rows<T, D, false>);
-    if (rc) return rc;
     const dim3 grid(static_cast<unsigned>(units * p.splits));
-    if (!split)
-        return launch_serialized(k_kv8_attention_rows<T, D, false>, grid, kRowsThreads, RowsCfg<D>::SMEM, 1, s, p);
-    rc = launch_serialized(k_kv8_attention_rows<T, D, true>, grid, kRowsThreads, RowsCfg<D>::SMEM, 1, s, p);
-    if (rc || p.splits == 1) return rc;
+    auto launch = [&](auto kernel, int raised) {
+        return raised ? raised : launch_serialized(kernel, grid, kRowsThreads, RowsCfg<D>::SMEM, 1, s, p);
+    };
+    if (p.splits == 1 && p.from == 1)
+        return launch(k_kv8_attention_rows<T, D, kWhole>, raise_smem<Whole>(k_kv8_attention_rows<T, D, kWhole>));
+    if (p.splits == 1)
+        return launch(k_kv8_attention_rows<T, D, kSome>, raise_smem<Some>(k_kv8_attention_rows<T, D, kSome>));
+    const int rc = launch(k_kv8_attention_rows<T, D, kSplit>, raise_smem<Split>(k_kv8_attention_rows<T, D, kSplit>));
+    if (rc) return rc;
     return launch_serialized(k_kv8_attention_rows_join<T, D>,
                              dim3(static_cast<unsigned>(units), 2 * kRowsTile / kRowsJoinRows), kRowsJoinThreads, 0, 1, s,
                              p);
@@ -769,13 +784,14 @@ int attention_rows(int dtype, const AttnParams& p, int dev, cudaStream_t s) {
     return p.c.D == 64 ? launch_rows<__nv_bfloat16, 64>(p, dev, s) : launch_rows<__nv_bfloat16, 128>(p, dev, s);
 }
 
+#define QG_ROWS_FORM_BUDGET(T, NAME, D, FORM, FORM_NAME)                                                 \
+    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows<" NAME "," #D "," FORM_NAME ">",                         \
+                           (reinterpret_cast<const void*>(k_kv8_attention_rows<T, D, FORM>)),            \
+                           kRowsThreads, RowsCfg<D>::SMEM, 512, 1, 1)
 #define QG_ROWS_BUDGET(T, NAME, D)                                                                       \
-    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows<" NAME "," #D ",false>",                                \
-                           (reinterpret_cast<const void*>(k_kv8_attention_rows<T, D, false>)),           \
-                           kRowsThreads, RowsCfg<D>::SMEM, 512, 1, 1);                                   \
-    QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows<" NAME "," #D ",true>",                                 \
-                           (reinterpret_cast<const void*>(k_kv8_attention_rows<T, D, true>)),            \
-                           kRowsThreads, RowsCfg<D>::SMEM, 512, 1, 1);                                   \
+    QG_ROWS_FORM_BUDGET(T, NAME, D, kWhole, "whole");                                                    \
+    QG_ROWS_FORM_BUDGET(T, NAME, D, kSome, "some");                                                      \
+    QG_ROWS_FORM_BUDGET(T, NAME, D, kSplit, "split");                                                    \
     QG_BLOCK_KERNEL_BUDGET("k_kv8_attention_rows_join<" NAME "," #D ">",                                 \
                            (reinterpret_cast<const void*>(k_kv8_attention_rows_join<T, D>)),             \
                            kRowsJoinThreads, 0, 0, 1, 1)

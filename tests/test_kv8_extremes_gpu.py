@@ -111,3 +111,36 @@ def test_many_small_weights_next_to_large_ones(torch, qg, below, B, new, length,
         bound = bulk * (1.01 * 2.0 ** -11 + 2 * e[:, None] + joined) + low + 1.01 * HALF_UNIT["float16"] * want.abs() + TINY["float16"]
         err = (O[:, h] - want).abs()
         assert bool((err <= bound).all()), (h, float((err / bound).max()), float((err / want).max()))
+
+
+def kernels_of(torch, call):
+    """Names of the kernels that a call launches."""
+    from torch.profiler import ProfilerActivity, profile
+    for _ in range(3):  # the first record of a process may be empty
+        with profile(activities=[ProfilerActivity.CUDA]) as prof:
+            call()
+            torch.cuda.synchronize()
+        names = [e.key for e in prof.key_averages()]
+        if any("k_kv8_attention" in n for n in names):
+            return names
+    pytest.skip("no kernels were recorded")
+
+
+@pytest.mark.parametrize("heads,page,D,news,lengths,cols", [
+    (2, 16, 64, [300, 1, 2], [700, 800, 2], 33000), (1, 64, 128, [1, 900, 0, 2], [300, 900, 5, 3000], 12000),
+    (8, 32, 64, [1200, 1, 1, 70, 3], [1300, 500, 1, 90, 2000], 4096)])
+def test_large_prompts_next_to_single_tokens_of_long_sequences(torch, qg, heads, page, D, news, lengths, cols):
+    """On average many rows a sequence, and room in the table for so many tokens that single tokens count: both kernels."""
+    cache, short = filled(torch, lengths, heads, D, page, 29)
+    table = torch.full((len(news), cols), -1, dtype=torch.int32, device="cuda")
+    table[:, :short.shape[1]] = short
+    gen = torch.Generator(device="cuda").manual_seed(heads)
+    Q = torch.randn(sum(news), heads * 4, D, generator=gen, device="cuda").bfloat16()
+    starts, length = int32(torch, starts_of(news)), int32(torch, lengths)
+    O = qg.kv8_attention(Q, cache, table, starts, length)
+    check_attention(torch, O, Q, cache, table, news, lengths, D ** -0.5, True, "bfloat16")
+    names = kernels_of(torch, lambda: qg.kv8_attention(Q, cache, table, starts, length))
+    assert any("k_kv8_attention_rows<" in n for n in names) and any("k_kv8_attention<" in n for n in names)
+    # with little room the kernel for many rows takes them all
+    names = kernels_of(torch, lambda: qg.kv8_attention(Q, cache, short, starts, length))
+    assert any("k_kv8_attention_rows<" in n for n in names) and not any("k_kv8_attention<" in n for n in names)
