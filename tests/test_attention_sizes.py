@@ -1,4 +1,4 @@
-"""CPU checks of the attention layer's operators: workspace sizes."""
+"""CPU checks of the attention layer's operators: workspace sizes, the kernels' table."""
 import pytest
 
 import bit_quantized_tensor_gb300 as qg
@@ -15,3 +15,13 @@ def L():
 def test_a_workspace_for_many_tokens_serves_fewer(L, N, K):
     sizes = [L.qg_workspace_size(qg.QG_OP_S8_LINEAR, m, N, K) for m in list(range(1, 4400)) + [5000, 8192, 1 << 20]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+def test_tensor_core_kernels_are_in_the_table(L):
+    names = [r["kernel"] for r in qg.kernel_budgets(table="block")]
+    for tile in (32, 64, 128):
+        assert f"s8_gemm_kernel<{tile}>" in names
+    for dtype in ("f16", "bf16"):
+        for D in (64, 128):
+            assert all(f"k_kv8_attention_rows<{dtype},{D},{form}>" in names for form in ("whole", "some", "split"))
+            assert f"k_kv8_attention_rows_join<{dtype},{D}>" in names
