@@ -762,8 +762,9 @@ extern "C" int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads
                        const_cast<float*>(vs), table, starts, lengths, B, rows, pages, page, heads, D, table_cols};
     int rc = check_kv8(a);
     if (rc) return rc;
-    if (q_heads < 1 || q_heads % heads || q_heads > 65536 || rows * (q_heads / heads) > INT32_MAX - 128 ||
-        !(scale - scale == 0.f))
+    const float scale_log2 = scale * 1.44269504088896340736f;
+    if (q_heads < 1 || q_heads % heads || q_heads > 65536 || rows * (q_heads / heads) > INT32_MAX - 256 ||
+        !(scale_log2 - scale_log2 == 0.f))
         return QG_ERR_INVALID_ARG;
     if (B == 0 || rows == 0) return QG_OK;
     rc = check_kv8_rows(dtype, Q, ldq, q_heads * D, rows);
@@ -780,7 +781,7 @@ extern "C" int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads
     const uintptr_t places = reinterpret_cast<uintptr_t>(Q) | static_cast<uintptr_t>(2 * ldq);
     p.q_align = places % 16 == 0 ? 16 : places % 8 == 0 ? 8 : 2;
     p.group = static_cast<int>(q_heads / heads);
-    p.scale_log2 = scale * 1.44269504088896340736f;
+    p.scale_log2 = scale_log2;
     p.part = static_cast<float*>(ws);
     p.ctl = host_ctl(dev);
     if (!p.ctl.status) return QG_ERR_CUDA;

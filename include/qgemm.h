@@ -674,6 +674,7 @@ int kv8_gather(int dtype, int64_t B, int64_t rows, int64_t heads, int64_t D, con
  *  causal : row i of a sequence with n rows sees its tokens up to lengths - n + i, else
  *         all of them.  A row that sees no token is 0; rows of a sequence that is longer
  *         than its table, and rows whose scores are all -inf, are NaN.
+ *  scale: finite, also times log2(e) (|scale| up to 2.3e38).
  *  Scales are what kv8_append writes: 2^-64 to 2^121, or NaN.  O and Q do not overlap.
  *  ws: qg_workspace_size(QG_OP_KV8_ATTENTION, rows, q_heads, D) bytes, 256-byte aligned */
 int kv8_attention(int dtype, int64_t B, int64_t rows, int64_t q_heads, int64_t heads, int64_t D,

@@ -1,4 +1,4 @@
-"""CPU checks of the attention layer's operators: workspace sizes, the kernels' table."""
+"""CPU checks of the attention layer's operators: workspace sizes, a refusal, the kernels' table."""
 import pytest
 
 import bit_quantized_tensor_gb300 as qg
@@ -15,6 +15,15 @@ def L():
 def test_a_workspace_for_many_tokens_serves_fewer(L, N, K):
     sizes = [L.qg_workspace_size(qg.QG_OP_S8_LINEAR, m, N, K) for m in list(range(1, 4400)) + [5000, 8192, 1 << 20]]
     assert all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("scale", [3e38, -3e38])
+def test_scales_that_leave_fp32_in_powers_of_two_are_refused(L, scale):
+    p = 0x10000
+    assert L.kv8_attention(1, 2, 4, 4, 2, 64, p, 256, p, p, p, p, 8, 16, p, 4, p, p, scale, 1, p, 256, p, 1 << 40,
+                           None) == 1
+    assert L.kv8_attention(1, 0, 4, 4, 2, 64, p, 256, p, p, p, p, 8, 16, p, 4, p, p, 2e38, 1, p, 256, p, 1 << 40,
+                           None) == 0
 
 
 def test_tensor_core_kernels_are_in_the_table(L):
