@@ -101,6 +101,15 @@ def _layer_case(qg, torch, a, dev):
     return lambda: qg.kv8_gather(cache, table, starts, lengths, M * a.batch, dtype=dtype)
 
 
+def _sizes(a):
+    """The sizes that the case has."""
+    if a.op.startswith("rope"):
+        return f"M={a.m} heads={a.heads} group={a.group} head={a.head}"
+    if a.op.startswith("kv8"):
+        return f"M={a.m} batch={a.batch} length={a.length} heads={a.heads} group={a.group} head={a.head} page={a.page}"
+    return f"M={a.m} N={a.n} K={a.k}"
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawTextHelpFormatter)
     ap.add_argument("op", choices=["s8", "s4", "f16", "w4a16", "w4a4_quant", "w4a4_gemm", "fp4_quant", "fp4_both", "fp4_gemm",
@@ -170,7 +179,7 @@ def main(argv=None):
     e1.record()
     torch.cuda.synchronize()
     assert qg.device_status() == qg.QG_OK
-    print(f"{a.op} M={M} N={N} K={K}: {e0.elapsed_time(e1) * 1e3:.1f} us (one call)")
+    print(f"{a.op} {_sizes(a)}: {e0.elapsed_time(e1) * 1e3:.1f} us (one call)")
 
 
 if __name__ == "__main__":
