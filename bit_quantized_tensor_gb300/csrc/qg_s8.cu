@@ -115,8 +115,8 @@ static int launch_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, OUT
 // Measured, linear of 4096 x 4096 in a chain of calls: 1 token 5.6 us (3.0 TB/s of weights),
 // 4 and 8 with the quantizer's kernel 6.4 and 6.7, by the next kernel 9.8; 16 tokens by
 // that 9.9; 8192 x 8192 17.0 us for 1 token (3.9 TB/s), 8 tokens 20.3.
-// Latency: a CTA's weights are one or two rounds of loads, and none of them goes out before the
-// kernel ahead has ended.
+// Latency: a CTA's weights are one or two rounds of loads, which go out when the kernel ahead has ended;
+// until then lines are only brought to the L2.  With the weights cold 7.1 and 19.2 us for 1 token.
 constexpr int kGemvWarps = 16, kGemvThreads = 32 * kGemvWarps;
 constexpr int kGemvBatch = 4;            // blocks of 64 values in flight a thread
 constexpr int kGemvTokens = 8;
@@ -342,8 +342,8 @@ static SomeForm some_form(int64_t M, int64_t N, int64_t K, int64_t* cycles) {
 // 256 x 256 tiles, 630 cycles a step of 64 values of K.  Measured, linear of 4096 x 4096, this kernel and
 // pairs: 128 tokens 16.3 and 33.6 us, 512 27.8 and 35.7, 777 49.5 and 36.6, 2048 98 and 60; of
 // 1024 x 8192: 777 tokens 33 and 53, 2048 62 and 60; of 8192 x 8192: 256 tokens 57.5 and 80.6, 512 113
-// and 83.  The choice was within 3% of the better one at 45 sizes.  4096 x 8192 x 8192 by pairs 344 us, 1.6 PFLOP/s, of which the product takes 289 (1.9),
-// the weights' pass 28 and the quantizer 19.
+// and 83.  The choice was within 3% of the better one at 45 sizes.  4096 x 8192 x 8192 by pairs 335 to
+// 350 us, 1.6 PFLOP/s, of which the product takes 289 (1.9), the weights' pass 28 and the quantizer 19.
 static int64_t pairs_cycles(int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = (M + 255) / 256 * ((N + 255) / 256);
     return 5700 + 3 * N * K / 3300 + (tiles + 75) / 76 * ((K + 63) / 64 * 630 + 7600);

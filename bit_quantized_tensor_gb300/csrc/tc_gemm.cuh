@@ -233,8 +233,8 @@ __device__ __forceinline__ void store_row_s32(int32_t* dst, int col0, int N_tota
     }
 }
 
-// A scale, which nothing writes while the kernel runs: such a load may go ahead of the stores around it,
-// but, being volatile, not ahead of the wait for the kernel that wrote it.
+// A scale, which nothing writes while the kernel runs (it starts when the kernels ahead of it have ended):
+// such a load may go ahead of the stores around it; volatile, it stays where its tile's results are written.
 __device__ __forceinline__ float load_scale(const float* p) {
     float v;
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));

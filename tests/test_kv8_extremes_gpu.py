@@ -108,7 +108,8 @@ def test_many_small_weights_next_to_large_ones(torch, qg, below, B, new, length,
         e = D * 2.0 ** -23 * (q.abs() @ (k8.abs() * sk).t()).amax(1) + 10 * 2.0 ** -24 * (x.amax(1) + 8) + 2.0 ** -21
         joined = (length / 16 + 64) * 2.0 ** -23
         bulk, low = w @ (v8.abs() * sv), 2.0 ** -34 * w.amax(1, keepdim=True) * (v8.abs() * sv).sum(0)
-        bound = bulk * (1.01 * 2.0 ** -11 + 2 * e[:, None] + joined) + low + 1.01 * HALF_UNIT["float16"] * want.abs() + TINY["float16"]
+        bound = bulk * (1.01 * 2.0 ** -11 + 2 * e[:, None] + joined) + low
+        bound = bound + 1.01 * HALF_UNIT["float16"] * want.abs() + TINY["float16"]
         err = (O[:, h] - want).abs()
         assert bool((err <= bound).all()), (h, float((err / bound).max()), float((err / want).max()))
 
